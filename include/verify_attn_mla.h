@@ -321,6 +321,45 @@ int verify_attn_mla_fp8(const void* q, const void* kv_pool_e4m3, int64_t pool_sl
                         const int32_t* qo_indptr_host, int batch, int num_heads, float sm_scale, int splits, void* out,
                         float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Append of new tokens' rows to the pool the verify calls read, with the
+ * position rotation applied on the way, and the same rotation of the queries.
+ * The pages start from a filled cache and a finished q; this is the step of a
+ * model with latent attention that makes both.  For token t with slot
+ * s = slots[t] and position p = positions[t], (c, d) = row p of the table:
+ *   rot(x): each of the 32 pairs (a, b) of x becomes (a c - b d, a d + b c);
+ *           pairs are (2i, 2i + 1) with neighbour_pairs, else (i, i + 32), and
+ *           pair i uses column i of the cosines and of the sines
+ *   kv_pool[s]        = [ latent[t] | rot(k_rope[t]) ]
+ *   q[t, h, 512:576]  = rot(q_rope[t, h])        (columns 0..511 are left alone)
+ * in fp32, rounded once to bf16 (nearest even), or for an e4m3 pool to the code
+ * of value / kv_scale (nearest even; beyond +-448 the largest code, NaN the NaN
+ * code, which verify_attn_mla_fp8 does not accept).
+ *   latent   [tokens, 512] bf16, latent_stride elements from row to row
+ *   k_rope   [tokens, 64] bf16, k_rope_stride elements from row to row (with
+ *            latent + 512 and the same stride: one [tokens, 576] array)
+ *   q_rope   [tokens, num_heads, 64] bf16, q_rope_stride_t / _h elements from
+ *            token to token / head to head; may be q's own last columns
+ *            (q + 512, strides 576 num_heads and 576), otherwise must not
+ *            overlap q.  num_heads 0: no queries (q_rope, q not read)
+ *   positions [tokens] int32 in [0, table_rows);  slots [tokens] int32
+ *   cos_sin  [table_rows, 64] fp32: 32 cosines, then 32 sines, per position
+ *   kv_pool  [pool_slots, 576] bf16 (kv_scale 0) or e4m3 codes (kv_scale > 0)
+ *   q        [tokens, num_heads, 576] bf16, contiguous
+ *   status_word  optional, two uint32
+ * A token with slot -1 is padding: its row, its q and its position are left
+ * out.  Another slot outside the pool, or a position outside the table, records
+ * VMLA_ERR_INDEX (token index) and that token's row and q are left as they were.
+ * Slots of one call must differ (rows sent to one slot may mix), and the pool
+ * and q overlap no other input.  Bases are
+ * 16-byte aligned and strides multiples of 8 elements (VMLA_ERR_ALIGN).
+ * One launch, no workspace, no host synchronisation; capture-safe (positions
+ * and slots are read when the graph replays). */
+int verify_attn_mla_append(const void* latent, int64_t latent_stride, const void* k_rope, int64_t k_rope_stride,
+                           const void* q_rope, int64_t q_rope_stride_t, int64_t q_rope_stride_h,
+                           const int32_t* positions, const int32_t* slots, const float* cos_sin, int64_t table_rows,
+                           int neighbour_pairs, int64_t tokens, int num_heads, void* kv_pool, int64_t pool_slots,
+                           float kv_scale, void* q, uint32_t* status_word, void* stream);
+
 /* Fixed size of the scratch array behind verify_attn_mla_simt_static (32 MiB). */
 #define VMLA_STATIC_SCRATCH_BYTES (32u << 20)
 

@@ -43,6 +43,7 @@ EXPORTS = (
     "verify_attn_mla_runs_workspace_size", "verify_attn_mla_test_fault", "verify_attn_mla_fp8",
     "verify_attn_mla_simt_static_check", "verify_attn_mla_defrag_append",
     "verify_attn_mla_runs_device_plan_workspace_size", "verify_attn_mla_runs_device_plan",
+    "verify_attn_mla_append",
 )
 
 
@@ -89,6 +90,8 @@ def _load(path: str = LIB_PATH):
         "verify_attn_mla_tree_accept": [vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp],
         "verify_attn_mla_defrag": [vp, i64, vp, vp, vp, i32, vp, i64, vp, vp, vp],
         "verify_attn_mla_defrag_append": [vp, i64, vp, vp, vp, i32, vp, i64, vp, vp, i64, vp, vp],
+        "verify_attn_mla_append": [vp, i64, vp, i64, vp, i64, i64, vp, vp, vp, i64, i32, i64, i32, vp, i64, f32, vp, vp,
+                                   vp],
         "verify_attn_mla_runs": run,
         "verify_attn_mla_runs_workspace_size": [i32, i32, vp, vp, i32, ctypes.POINTER(sz)],
         "verify_attn_mla_test_fault": [i32, i64],
@@ -146,6 +149,33 @@ def _d(t, itemsize: int, name: str) -> Optional[int]:
 
 def _h(t, itemsize: int, name: str) -> Optional[int]:
     return _arg(t, itemsize, name, False)
+
+
+def _rows(t, itemsize: int, name: str, shape) -> int:
+    """Pointer of a device array whose last dimension is contiguous and whose other strides the entry
+    point takes as arguments.  shape: expected sizes (None: any)."""
+    if isinstance(t, np.ndarray) or not t.is_cuda:
+        raise ValueError(f"{name}: device memory expected")
+    _shape(t, name, shape)
+    if t.element_size() != itemsize:
+        raise ValueError(f"{name}: {itemsize}-byte elements expected, got {t.dtype}")
+    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: last dimension not contiguous")
+    return t.data_ptr()
+
+
+def _shape(t, name: str, shape):
+    if len(t.shape) != len(shape) or any(w is not None and int(n) != int(w) for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
+
+
+def _same_device(**tensors):
+    """Every given tensor lies on the current device, where the kernels are launched."""
+    import torch
+    cur = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and getattr(t, "is_cuda", False) and t.device.index != cur:
+            raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{cur}")
 
 
 def _host_i32(a) -> np.ndarray:
@@ -326,6 +356,54 @@ def prepare_verify_attn_mla_defrag_append(*a, **k) -> Prepared:
     """verify_attn_mla_defrag_append with its arguments checked and marshalled once."""
     args, keep = _append_args(*a, **k)
     return Prepared(_lib.verify_attn_mla_defrag_append, "verify_attn_mla_defrag_append", args, keep)
+
+
+def _step(t, dim: int, least: int) -> int:
+    """Stride of a dimension, or `least` where its size makes the stride immaterial."""
+    return int(t.stride(dim)) if int(t.shape[dim]) > 1 else least
+
+
+def _cache_append_args(latent, k_rope, positions, slots, cos_sin, kv_pool, q_rope=None, q=None, kv_scale=0.0,
+                       interleaved=True, status_word=None, stream=None):
+    T = int(latent.shape[0])
+    R = D_QK - D_V
+    fp8 = float(kv_scale) != 0.0
+    if (q_rope is None) != (q is None):
+        raise ValueError("q_rope and q are given together")
+    H = int(q.shape[1]) if q is not None else 0
+    lat = _rows(latent, 2, "latent", (T, D_V))
+    rope = _rows(k_rope, 2, "k_rope", (T, R))
+    qr = _rows(q_rope, 2, "q_rope", (T, H, R)) if q is not None else None
+    if q is not None:
+        _shape(q, "q", (T, H, D_QK))
+    _shape(positions, "positions", (T,))
+    _shape(slots, "slots", (T,))
+    _shape(cos_sin, "cos_sin", (None, R))
+    _shape(kv_pool, "kv_pool", (None, D_QK))
+    if status_word is not None and status_word.numel() < 2:
+        raise ValueError("status_word: two words expected")
+    _same_device(latent=latent, k_rope=k_rope, positions=positions, slots=slots, cos_sin=cos_sin, kv_pool=kv_pool,
+                 q_rope=q_rope, q=q, status_word=status_word)
+    args = (lat, _step(latent, 0, D_V), rope, _step(k_rope, 0, R), qr, _step(q_rope, 0, R) if H else 0,
+            _step(q_rope, 1, R) if H else 0, _d(positions, 4, "positions"), _d(slots, 4, "slots"),
+            _d(cos_sin, 4, "cos_sin"), int(cos_sin.shape[0]), int(bool(interleaved)), T, H,
+            _d(kv_pool, 1 if fp8 else 2, "kv_pool"), int(kv_pool.shape[0]), float(kv_scale), _d(q, 2, "q"),
+            _d(status_word, 4, "status_word"), _stream(stream))
+    return args, (latent, k_rope, positions, slots, cos_sin, kv_pool, q_rope, q, status_word)
+
+
+def verify_attn_mla_append(*a, **k):
+    """Writes new tokens' rows into the pool (bf16, or e4m3 codes with kv_scale > 0), the last 64 columns turned by
+    the tokens' positions, and with q_rope / q the queries' last 64 columns likewise.  latent [T, 512], k_rope
+    [T, 64], q_rope [T, H, 64] may be strided; interleaved: pairs (2i, 2i + 1), else (i, i + 32); slot -1: padding."""
+    args, _ = _cache_append_args(*a, **k)
+    _check(_lib.verify_attn_mla_append(*args), "verify_attn_mla_append")
+
+
+def prepare_verify_attn_mla_append(*a, **k) -> Prepared:
+    """verify_attn_mla_append with its arguments checked and marshalled once."""
+    args, keep = _cache_append_args(*a, **k)
+    return Prepared(_lib.verify_attn_mla_append, "verify_attn_mla_append", args, keep)
 
 
 def verify_attn_mla_runs_workspace_size(qo_indptr_host, kv_indptr_host, num_heads: int, splits: int = 0) -> int:

@@ -709,6 +709,58 @@ int verify_attn_mla_tree_accept(const int32_t* qo_indptr, const int32_t* parent,
                             accept_path, next_token, status_word, stream);
 }
 
+int verify_attn_mla_append(const void* latent, int64_t latent_stride, const void* k_rope, int64_t k_rope_stride,
+                           const void* q_rope, int64_t q_rope_stride_t, int64_t q_rope_stride_h,
+                           const int32_t* positions, const int32_t* slots, const float* cos_sin, int64_t table_rows,
+                           int neighbour_pairs, int64_t tokens, int num_heads, void* kv_pool, int64_t pool_slots,
+                           float kv_scale, void* q, uint32_t* status_word, void* stream) {
+  if (tokens < 0 || tokens > INT32_MAX || num_heads < 0 || num_heads > VMLA_MAX_HEADS || pool_slots < 0 ||
+      pool_slots > INT32_MAX || table_rows < 0 || table_rows > INT32_MAX)
+    return VMLA_ERR_SHAPE;
+  if (kv_scale != 0.f && (!(kv_scale > 0.f) || !(kv_scale < INFINITY))) return VMLA_ERR_SHAPE;
+  if (tokens == 0) return VMLA_OK;
+  if (!latent || !k_rope || !positions || !slots || !cos_sin || !kv_pool) return VMLA_ERR_NULL;
+  if (num_heads > 0 && (!q_rope || !q)) return VMLA_ERR_NULL;
+  if (latent_stride < kDv || k_rope_stride < kDqk - kDv) return VMLA_ERR_SHAPE;
+  if (num_heads > 0 && (q_rope_stride_t < kDqk - kDv || q_rope_stride_h < kDqk - kDv)) return VMLA_ERR_SHAPE;
+  // the largest element offsets stay far inside 64 bits
+  constexpr int64_t kMaxStride = (int64_t)1 << 31;
+  if (latent_stride > kMaxStride || k_rope_stride > kMaxStride ||
+      (num_heads > 0 && (q_rope_stride_t > kMaxStride || q_rope_stride_h > kMaxStride)))
+    return VMLA_ERR_SHAPE;
+  // rows are read in 16-byte granules: bases and strides of 8 elements
+  if (!aligned(latent, 16) || !aligned(k_rope, 16) || !aligned(cos_sin, 16) || !aligned(kv_pool, 16) ||
+      !aligned(positions, 4) || !aligned(slots, 4) || !aligned(status_word, 4) || latent_stride % 8 != 0 ||
+      k_rope_stride % 8 != 0)
+    return VMLA_ERR_ALIGN;
+  if (num_heads > 0 && (!aligned(q_rope, 16) || !aligned(q, 16) || q_rope_stride_t % 8 != 0 || q_rope_stride_h % 8 != 0))
+    return VMLA_ERR_ALIGN;
+  int sms = 0;
+  int rc = current_sm_count(&sms, true);
+  if (rc != VMLA_OK) return rc;
+  AppendArgs a;
+  a.latent = static_cast<const uint16_t*>(latent);
+  a.k_rope = static_cast<const uint16_t*>(k_rope);
+  a.q_rope = static_cast<const uint16_t*>(q_rope);
+  a.latent_stride = latent_stride;
+  a.k_rope_stride = k_rope_stride;
+  a.q_rope_stride_t = q_rope_stride_t;
+  a.q_rope_stride_h = q_rope_stride_h;
+  a.positions = positions;
+  a.slots = slots;
+  a.cos_sin = cos_sin;
+  a.table_rows = table_rows;
+  a.tokens = tokens;
+  a.num_heads = num_heads;
+  a.neighbours = neighbour_pairs != 0;
+  a.pool = kv_pool;
+  a.pool_slots = pool_slots;
+  a.kv_scale = kv_scale;
+  a.q = static_cast<uint16_t*>(q);
+  a.status = status_word;
+  return launch_append(a, stream);
+}
+
 int verify_attn_mla_test_fault(int fault, int64_t wait_cycles) {
   if ((fault != 0 && fault != kFaultNoQReady) || wait_cycles < 0) return VMLA_ERR_SHAPE;
   g_test_fault = fault;

@@ -205,6 +205,28 @@ int launch_tree_accept(const int32_t* qo_indptr, const int32_t* parent, const in
                        const int32_t* root, int batch, int total_q, int32_t* accept_len, int32_t* path,
                        int32_t* next_token, uint32_t* status, void* stream);
 
+// New tokens' rows into the pool, their rotated part turned by position, and the queries'
+// rotated part into q (verify_attn_mla_append).  Strides in elements.
+struct AppendArgs {
+  const uint16_t* latent;   // [tokens, 512], row stride latent_stride
+  const uint16_t* k_rope;   // [tokens, 64], row stride k_rope_stride
+  const uint16_t* q_rope;   // [tokens, num_heads, 64], strides q_rope_stride_t / _h; unused with num_heads 0
+  int64_t latent_stride, k_rope_stride, q_rope_stride_t, q_rope_stride_h;
+  const int32_t* positions;
+  const int32_t* slots;
+  const float* cos_sin;     // [table_rows, 64]: 32 cosines, 32 sines
+  int64_t table_rows;
+  int64_t tokens;
+  int32_t num_heads;        // 0: no queries
+  int32_t neighbours;       // pairs (2i, 2i + 1), else (i, i + 32)
+  void* pool;
+  int64_t pool_slots;
+  float kv_scale;           // 0: bf16 pool; > 0: e4m3 pool
+  uint16_t* q;
+  uint32_t* status;
+};
+int launch_append(const AppendArgs& args, void* stream);
+
 int launch_simt(const PlanParams& plan, const RunArgs& args, void* stream);
 int launch_tc(const PlanParams& plan, const RunArgs& args, void* stream);
 int launch_gather(const RunArgs& args, void* stream);
