@@ -321,6 +321,39 @@ int verify_attn_mla_fp8(const void* q, const void* kv_pool_e4m3, int64_t pool_sl
                         const int32_t* qo_indptr_host, int batch, int num_heads, float sm_scale, int splits, void* out,
                         float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
+/* verify_attn_mla for a batch whose sequences all begin with the same rows (an
+ * instruction text, a document, a tool description): those rows are gathered
+ * once, and their scores and sums are computed once for all sequences' queries
+ * together, 256 (query, head) rows to a tile whatever sequence they belong to;
+ * each sequence's own rows follow as in verify_attn_mla, and a merge joins both
+ * partial softmaxes.  The pages have no counterpart; the result is that of
+ * verify_attn_mla with the shared slots in front of every sequence's own,
+ * up to the rounding of sums taken in another order.
+ *   shared_indices [shared_rows] int32: slots of the shared rows, in front of
+ *                  every sequence; all of them prefix (visible to every query)
+ *   kv_indptr, kv_indices, kv_indptr_host: each sequence's OWN rows only; the
+ *                  last Q_b of them are its draft tokens' rows
+ *   kv_scale       0: kv_pool is bf16 [pool_slots, 576]; > 0: e4m3 codes with
+ *                  one scale, as for verify_attn_mla_fp8
+ *   batch          at most VMLA_MAX_BATCH - 1
+ *   workspace      >= verify_attn_mla_shared_workspace_size() bytes
+ * A sequence's result depends on the shared rows and its own rows alone (no
+ * tile holds rows of two sequences); rows that a sequence reads, hidden drafts
+ * too, hold finite values.
+ * Other arguments, errors and the order of the launches as for verify_attn_mla
+ * (info of VMLA_ERR_INDEX: the row in shared order, then kv_indices' order).
+ * All queries' partial results have to fit 2^31 elements
+ * (total_q x num_heads x pieces x 512), else VMLA_ERR_SHAPE.  shared_rows 0 is
+ * verify_attn_mla itself. */
+int verify_attn_mla_shared_workspace_size(int batch, int num_heads, int64_t shared_rows, const int32_t* qo_indptr_host,
+                                          const int32_t* kv_indptr_host, int splits, size_t* bytes);
+int verify_attn_mla_shared(const void* q, const void* kv_pool, int64_t pool_slots, float kv_scale,
+                           const int32_t* shared_indices, int64_t shared_rows, const int32_t* kv_indptr,
+                           const int32_t* kv_indices, const int32_t* qo_indptr, const uint64_t* draft_mask,
+                           const int32_t* parent, const int32_t* kv_indptr_host, const int32_t* qo_indptr_host,
+                           int batch, int num_heads, float sm_scale, int splits, void* out, float* lse,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
 /* Append of new tokens' rows to the pool the verify calls read, with the
  * position rotation applied on the way, and the same rotation of the queries.
  * The pages start from a filled cache and a finished q; this is the step of a

@@ -43,7 +43,7 @@ EXPORTS = (
     "verify_attn_mla_runs_workspace_size", "verify_attn_mla_test_fault", "verify_attn_mla_fp8",
     "verify_attn_mla_simt_static_check", "verify_attn_mla_defrag_append",
     "verify_attn_mla_runs_device_plan_workspace_size", "verify_attn_mla_runs_device_plan",
-    "verify_attn_mla_append",
+    "verify_attn_mla_append", "verify_attn_mla_shared", "verify_attn_mla_shared_workspace_size",
 )
 
 
@@ -92,6 +92,9 @@ def _load(path: str = LIB_PATH):
         "verify_attn_mla_defrag_append": [vp, i64, vp, vp, vp, i32, vp, i64, vp, vp, i64, vp, vp],
         "verify_attn_mla_append": [vp, i64, vp, i64, vp, i64, i64, vp, vp, vp, i64, i32, i64, i32, vp, i64, f32, vp, vp,
                                    vp],
+        "verify_attn_mla_shared": [vp, vp, i64, f32, vp, i64, vp, vp, vp, vp, vp, vp, vp, i32, i32, f32, i32, vp, vp, vp,
+                                   sz, vp],
+        "verify_attn_mla_shared_workspace_size": [i32, i32, i64, vp, vp, i32, ctypes.POINTER(sz)],
         "verify_attn_mla_runs": run,
         "verify_attn_mla_runs_workspace_size": [i32, i32, vp, vp, i32, ctypes.POINTER(sz)],
         "verify_attn_mla_test_fault": [i32, i64],
@@ -171,10 +174,13 @@ def _shape(t, name: str, shape):
 
 def _same_device(**tensors):
     """Every given tensor lies on the current device, where the kernels are launched."""
+    tensors = {name: t for name, t in tensors.items() if getattr(t, "is_cuda", False)}
+    if not tensors:
+        return  # host memory is refused where the pointers are taken
     import torch
     cur = torch.cuda.current_device()
     for name, t in tensors.items():
-        if t is not None and getattr(t, "is_cuda", False) and t.device.index != cur:
+        if t.device.index != cur:
             raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{cur}")
 
 
@@ -404,6 +410,57 @@ def prepare_verify_attn_mla_append(*a, **k) -> Prepared:
     """verify_attn_mla_append with its arguments checked and marshalled once."""
     args, keep = _cache_append_args(*a, **k)
     return Prepared(_lib.verify_attn_mla_append, "verify_attn_mla_append", args, keep)
+
+
+def verify_attn_mla_shared_workspace_size(shared_rows: int, qo_indptr_host, kv_indptr_host, num_heads: int,
+                                          splits: int = 0) -> int:
+    qo = _host_i32(qo_indptr_host)
+    kv = _host_i32(kv_indptr_host)
+    n = ctypes.c_size_t(0)
+    _check(_lib.verify_attn_mla_shared_workspace_size(len(qo) - 1, num_heads, int(shared_rows), qo.ctypes.data,
+                                                      kv.ctypes.data, splits, ctypes.byref(n)),
+           "verify_attn_mla_shared_workspace_size")
+    return int(n.value)
+
+
+def _shared_args(q, kv_pool, shared_indices, kv_indptr, kv_indices, qo_indptr, kv_indptr_host, qo_indptr_host, out,
+                 lse, workspace, sm_scale, kv_scale=0.0, draft_mask=None, parent=None, splits=0, stream=None):
+    kvh = _host_i32(kv_indptr_host)
+    qoh = _host_i32(qo_indptr_host)
+    if len(kvh) != len(qoh) or len(kvh) < 1:
+        raise ValueError("kv_indptr_host and qo_indptr_host: batch + 1 entries each expected")
+    T, H, N = int(qoh[-1]), int(q.shape[1]), int(kvh[-1])
+    for t, name, shape in ((q, "q", (T, H, D_QK)), (out, "out", (T, H, D_V)), (lse, "lse", (T, H)),
+                           (kv_pool, "kv_pool", (None, D_QK)), (shared_indices, "shared_indices", (None,)),
+                           (kv_indices, "kv_indices", (N,)), (kv_indptr, "kv_indptr", (len(kvh),)),
+                           (qo_indptr, "qo_indptr", (len(kvh),))):
+        _shape(t, name, shape)
+    for t, name in ((draft_mask, "draft_mask"), (parent, "parent")):
+        if t is not None:
+            _shape(t, name, (T,))
+    _same_device(q=q, kv_pool=kv_pool, shared_indices=shared_indices, kv_indptr=kv_indptr, kv_indices=kv_indices,
+                 qo_indptr=qo_indptr, out=out, lse=lse, workspace=workspace, draft_mask=draft_mask, parent=parent)
+    args = (_d(q, 2, "q"), _d(kv_pool, 1 if float(kv_scale) != 0.0 else 2, "kv_pool"), int(kv_pool.shape[0]),
+            float(kv_scale), _d(shared_indices, 4, "shared_indices"), int(shared_indices.shape[0]),
+            _d(kv_indptr, 4, "kv_indptr"), _d(kv_indices, 4, "kv_indices"), _d(qo_indptr, 4, "qo_indptr"),
+            _d(draft_mask, 8, "draft_mask"), _d(parent, 4, "parent"), kvh.ctypes.data, qoh.ctypes.data, len(kvh) - 1,
+            H, float(sm_scale), int(splits), _d(out, 2, "out"), _d(lse, 4, "lse"), _d(workspace, 0, "workspace"),
+            workspace.numel() * workspace.element_size(), _stream(stream))
+    return args, (q, kv_pool, shared_indices, kv_indptr, kv_indices, qo_indptr, kvh, qoh, out, lse, workspace,
+                  draft_mask, parent)
+
+
+def verify_attn_mla_shared(*a, **k):
+    """Verify attention of a batch whose sequences share their first rows (shared_indices); kv_indptr and kv_indices
+    hold each sequence's own rows.  The pool is bf16, or e4m3 codes with kv_scale > 0."""
+    args, _ = _shared_args(*a, **k)
+    _check(_lib.verify_attn_mla_shared(*args), "verify_attn_mla_shared")
+
+
+def prepare_verify_attn_mla_shared(*a, **k) -> Prepared:
+    """verify_attn_mla_shared with its arguments checked and marshalled once."""
+    args, keep = _shared_args(*a, **k)
+    return Prepared(_lib.verify_attn_mla_shared, "verify_attn_mla_shared", args, keep)
 
 
 def verify_attn_mla_runs_workspace_size(qo_indptr_host, kv_indptr_host, num_heads: int, splits: int = 0) -> int:

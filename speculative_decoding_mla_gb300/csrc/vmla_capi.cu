@@ -709,6 +709,119 @@ int verify_attn_mla_tree_accept(const int32_t* qo_indptr, const int32_t* parent,
                             accept_path, next_token, status_word, stream);
 }
 
+namespace {
+// Lengths of a shared-prefix call, beyond those of a plain one.
+int check_shared(int64_t shared_rows, const int32_t* kv_indptr_host, int batch) {
+  if (shared_rows < 0 || batch > VMLA_MAX_BATCH - 1 || shared_rows + kv_indptr_host[batch] > INT32_MAX)
+    return VMLA_ERR_SHAPE;
+  return VMLA_OK;
+}
+}  // namespace
+
+int verify_attn_mla_shared_workspace_size(int batch, int num_heads, int64_t shared_rows, const int32_t* qo_indptr_host,
+                                          const int32_t* kv_indptr_host, int splits, size_t* bytes) {
+  if (!bytes) return VMLA_ERR_NULL;
+  int rc = check_common(kv_indptr_host, qo_indptr_host, batch, num_heads, 0, splits);
+  if (rc != VMLA_OK) return rc;
+  rc = check_shared(shared_rows, kv_indptr_host, batch);
+  if (rc != VMLA_OK) return rc;
+  if (shared_rows == 0 || batch == 0)
+    return verify_attn_mla_workspace_size(batch, num_heads, qo_indptr_host, kv_indptr_host, splits, bytes);
+  int sms = 0, clusters = 0;
+  rc = current_sm_count(&sms, false);
+  if (rc != VMLA_OK) return rc;
+  rc = vmla::tc_max_clusters(&clusters);
+  if (rc != VMLA_OK) return rc;
+  static thread_local PlanParams plan;
+  static thread_local StageMap map;
+  vmla_plan_info info;
+  if (!build_stage_map(batch, shared_rows, kv_indptr_host, &map)) return VMLA_ERR_SHAPE;
+  rc = build_shared_plan(batch, num_heads, shared_rows, qo_indptr_host, kv_indptr_host, map, splits, sms, clusters,
+                         &plan, &info);
+  if (rc != VMLA_OK) return rc;
+  *bytes = info.workspace_bytes;
+  return VMLA_OK;
+}
+
+int verify_attn_mla_shared(const void* q, const void* kv_pool, int64_t pool_slots, float kv_scale,
+                           const int32_t* shared_indices, int64_t shared_rows, const int32_t* kv_indptr,
+                           const int32_t* kv_indices, const int32_t* qo_indptr, const uint64_t* draft_mask,
+                           const int32_t* parent, const int32_t* kv_indptr_host, const int32_t* qo_indptr_host,
+                           int batch, int num_heads, float sm_scale, int splits, void* out, float* lse,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_common(kv_indptr_host, qo_indptr_host, batch, num_heads, pool_slots, splits);
+  if (rc != VMLA_OK) return rc;
+  rc = check_shared(shared_rows, kv_indptr_host, batch);
+  if (rc != VMLA_OK) return rc;
+  if (kv_scale != 0.f && (!(kv_scale > 0.f) || !(kv_scale < INFINITY))) return VMLA_ERR_SHAPE;
+  const int64_t total_q = qo_indptr_host[batch];
+  // nothing shared (or nothing asked): the plain call
+  if (shared_rows == 0 || total_q == 0)
+    return run_verify(VMLA_KERNEL_TC, q, kv_pool, pool_slots, kv_scale, kv_indptr, kv_indices, nullptr, qo_indptr,
+                      draft_mask, parent, kv_indptr_host, qo_indptr_host, batch, num_heads, sm_scale, splits, out, lse,
+                      workspace, workspace_bytes, stream);
+  if (!(sm_scale > 0.f) || !(sm_scale < INFINITY)) return VMLA_ERR_SHAPE;
+  if (!workspace || !q || !kv_pool || !shared_indices || !kv_indptr || !kv_indices || !qo_indptr || !out || !lse)
+    return VMLA_ERR_NULL;
+  if (pool_slots == 0) return VMLA_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(kv_pool, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
+      !aligned(workspace, VMLA_WORKSPACE_ALIGN) || !aligned(draft_mask, 8) || !aligned(parent, 4) ||
+      !aligned(shared_indices, 4) || !aligned(kv_indices, 4))
+    return VMLA_ERR_ALIGN;
+  int sms = 0, clusters = 0;
+  rc = current_sm_count(&sms, true);
+  if (rc != VMLA_OK) return rc;
+  rc = tc_max_clusters(&clusters);
+  if (rc != VMLA_OK) return rc;
+  // As in the plain call the areas that no plan sizes lead the workspace, and the kernels that
+  // fill them are queued before the host builds the plan.
+  static thread_local StageMap map;
+  if (!build_stage_map(batch, shared_rows, kv_indptr_host, &map)) return VMLA_ERR_SHAPE;
+  WorkspaceLayout L = workspace_layout(total_q, 0, map.total);
+  if (workspace_bytes < L.total) return VMLA_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  uint32_t* status = reinterpret_cast<uint32_t*>(ws + L.status_off);
+  if (cudaMemsetAsync(status, 0, 8, (cudaStream_t)stream) != cudaSuccess) return VMLA_ERR_CUDA;
+  RunArgs a;
+  test_fault_settings(&a.test_fault, &a.wait_cycles);
+  a.q = static_cast<const uint16_t*>(q);
+  a.kv = static_cast<const uint16_t*>(kv_pool);
+  a.pool_slots = pool_slots;
+  a.kv_indices = kv_indices;
+  a.masks = draft_mask;
+  a.sm_scale = sm_scale;
+  a.scale_log2 = sm_scale * 1.4426950408889634f;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.out_rows = total_q * num_heads;
+  a.staged = reinterpret_cast<uint16_t*>(ws + L.staged_off);
+  a.total_kv = map.total;
+  a.run_base = nullptr;
+  a.kv_scale = kv_scale;
+  a.status = status;
+  if (!draft_mask && parent) {
+    uint64_t* m = reinterpret_cast<uint64_t*>(ws + L.masks_off);
+    rc = launch_tree_mask(parent, qo_indptr, batch, (int)total_q, m, status, stream);
+    if (rc != VMLA_OK) return rc;
+    a.masks = m;
+  }
+  rc = launch_gather_shared(a, shared_indices, map, stream);
+  if (rc != VMLA_OK) return rc;
+  static thread_local PlanParams plan;
+  vmla_plan_info info;
+  rc = build_shared_plan(batch, num_heads, shared_rows, qo_indptr_host, kv_indptr_host, map, splits, sms, clusters,
+                         &plan, &info);
+  if (rc != VMLA_OK) return rc;
+  if (workspace_bytes < info.workspace_bytes) return VMLA_ERR_WORKSPACE;
+  L = workspace_layout(total_q, plan.partial_rows, map.total);
+  a.part_rows = plan.partial_rows;
+  a.part_o = reinterpret_cast<float*>(ws + L.part_o_off);
+  a.part_lse = reinterpret_cast<float*>(ws + L.part_lse_off);
+  rc = launch_tc(plan, a, stream);
+  if (rc != VMLA_OK) return rc;
+  return launch_merge_shared(plan, a.part_o, a.part_lse, a.out, a.lse, stream);
+}
+
 int verify_attn_mla_append(const void* latent, int64_t latent_stride, const void* k_rope, int64_t k_rope_stride,
                            const void* q_rope, int64_t q_rope_stride_t, int64_t q_rope_stride_h,
                            const int32_t* positions, const int32_t* slots, const float* cos_sin, int64_t table_rows,

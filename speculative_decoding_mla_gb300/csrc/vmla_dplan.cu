@@ -279,7 +279,7 @@ device_plan_kernel(const int32_t* __restrict__ qo, const int32_t* __restrict__ k
       pp->lane_tiles = (int32_t)Lt;
       pp->lane_total = (int32_t)W;
       pp->lane_count = ok ? lane_count : 0;
-      pp->pad = 0;
+      pp->shared = 0;
       status[2] = ok ? (uint32_t)kv[batch] : 0u;
       status[3] = ok ? (uint32_t)qo[batch] : 0u;
       if (!ok) record_shape_error(status, 2u);
@@ -330,7 +330,7 @@ device_plan_kernel(const int32_t* __restrict__ qo, const int32_t* __restrict__ k
     pp->lane_tiles = 0;
     pp->lane_total = 0;
     pp->lane_count = 0;
-    pp->pad = 0;
+    pp->shared = 0;
     status[2] = ok ? (uint32_t)kv[batch] : 0u;  // key rows of the plan (diagnostic)
     status[3] = ok ? (uint32_t)qo[batch] : 0u;  // draft rows the mask kernel expands
     if (!ok) record_shape_error(status, lengths_ok ? 2u : (uint32_t)s_bad);

@@ -144,7 +144,103 @@ gather_rows_fp8_kernel(const uint4* __restrict__ pool, int64_t pool_slots, float
   }
 }
 
+// Gather of a shared-prefix call: the shared rows, then each sequence's own rows, every entry
+// padded with zero rows to a multiple of kStageAlign (StageMap).  A warp takes four staged rows
+// of one entry at a time (kStageAlign is a multiple of four) and has all their loads in flight;
+// an e4m3 row's 36 code granules are the 32 lanes' plus four more, which the lanes 4k .. 4k + 3
+// load for the warp's row k.
+template <bool kFp8>
+__global__ void __launch_bounds__(kGatherWarps * 32)
+gather_shared_kernel(const uint4* __restrict__ pool, int64_t pool_slots, float scale,
+                     const int32_t* __restrict__ shared_indices, const int32_t* __restrict__ kv_indices,
+                     const __grid_constant__ StageMap map, uint4* __restrict__ staged, uint32_t* status) {
+  grid_dependents_launch();
+  constexpr int kSrcU4 = kFp8 ? kDqk / 16 : kRowU4;
+  static_assert(kStageAlign % kRowsPerWarp == 0 && kRowsPerWarp == 4, "a warp's rows belong to one entry");
+  const int lane = threadIdx.x & 31;
+  const int64_t warp0 = (int64_t)blockIdx.x * kGatherWarps + (threadIdx.x >> 5);
+  const int64_t nwarps = (int64_t)gridDim.x * kGatherWarps;
+  for (int64_t j0 = warp0 * kRowsPerWarp; j0 < map.total; j0 += nwarps * kRowsPerWarp) {
+    // the last entry that starts at or before row j0 (one that holds rows: an empty entry shares
+    // its start with the next)
+    int lo = 0, hi = map.entries;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (map.off[mid] <= j0) lo = mid; else hi = mid;
+    }
+    const int r0 = (int)(j0 - map.off[lo]), n = map.len[lo];
+    const int32_t* idx = (lo == 0 ? shared_indices : kv_indices) + map.src[lo];
+    int32_t my = -1;
+    if (lane < kRowsPerWarp && r0 + lane < n) {
+      my = idx[r0 + lane];
+      if (my < 0 || (int64_t)my >= pool_slots) {
+        const int64_t row = (lo == 0 ? 0 : (int64_t)map.len[0] + map.src[lo]) + r0 + lane;
+        record_status(status, VMLA_ERR_INDEX, (uint32_t)row);
+        my = -1;
+      }
+    }
+    uint4 v[kRowsPerWarp][kFp8 ? 1 : 3], x = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < kRowsPerWarp; ++k) {
+      const int32_t slot = __shfl_sync(0xffffffffu, my, k);
+      const bool ok = slot >= 0;
+      const uint4* src = pool + (int64_t)(ok ? slot : 0) * kSrcU4;
+      v[k][0] = ok ? ld_stream(src + lane) : make_uint4(0, 0, 0, 0);
+      if constexpr (!kFp8) {
+        v[k][1] = ok ? ld_stream(src + lane + 32) : make_uint4(0, 0, 0, 0);
+        v[k][2] = (ok && lane < kRowU4 - 64) ? ld_stream(src + lane + 64) : make_uint4(0, 0, 0, 0);
+      }
+    }
+    if constexpr (kFp8) {
+      const int32_t slot = __shfl_sync(0xffffffffu, my, (lane >> 2) & 3);
+      if (lane < 16 && slot >= 0) x = ld_stream(pool + (int64_t)slot * kSrcU4 + 32 + (lane & 3));
+    }
+    auto put_codes = [&](int64_t row, int g, const uint4& c) {
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+      uint32_t o[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        o[2 * k] = e4m3x2_to_bf16x2(w[k] & 0xFFFFu, scale);
+        o[2 * k + 1] = e4m3x2_to_bf16x2(w[k] >> 16, scale);
+      }
+      uint4* dst = staged + row * kRowU4 + 2 * g;
+      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    };
+#pragma unroll
+    for (int k = 0; k < kRowsPerWarp; ++k) {
+      if constexpr (kFp8) {
+        put_codes(j0 + k, lane, v[k][0]);
+      } else {
+        uint4* dst = staged + (j0 + k) * kRowU4;
+        dst[lane] = v[k][0];
+        dst[lane + 32] = v[k][1];
+        if (lane < kRowU4 - 64) dst[lane + 64] = v[k][2];
+      }
+    }
+    if constexpr (kFp8) {
+      if (lane < 16) put_codes(j0 + (lane >> 2), 32 + (lane & 3), x);
+    }
+  }
+}
+
 }  // namespace
+
+int launch_gather_shared(const RunArgs& a, const int32_t* shared_indices, const StageMap& map, void* stream) {
+  if (map.total == 0) return VMLA_OK;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) !=
+                                                cudaSuccess)
+    return VMLA_ERR_CUDA;
+  const int64_t need = (map.total + kGatherWarps * kRowsPerWarp - 1) / (kGatherWarps * kRowsPerWarp);
+  const int64_t cap = (int64_t)sms * 8;
+  const unsigned blocks = (unsigned)(need < cap ? need : cap);
+  const auto kernel = a.kv_scale > 0.f ? gather_shared_kernel<true> : gather_shared_kernel<false>;
+  kernel<<<blocks, kGatherWarps * 32, 0, (cudaStream_t)stream>>>(
+      reinterpret_cast<const uint4*>(a.kv), a.pool_slots, a.kv_scale, shared_indices, a.kv_indices, map,
+      reinterpret_cast<uint4*>(a.staged), a.status);
+  return cudaGetLastError() == cudaSuccess ? VMLA_OK : VMLA_ERR_CUDA;
+}
 
 namespace {
 int launch_gather_impl(const RunArgs& a, const int32_t* total_dev, void* stream) {

@@ -49,7 +49,9 @@ struct PlanParams {
   int32_t lane_tiles;  // L: cost-space length each lane takes
   int32_t lane_total;  // W: cost-space length of all streams
   int32_t lane_count;  // lanes with work (the launch has lane_count x G clusters)
-  int32_t pad;
+  int32_t shared;      // 1: seq[0] stands for rows that every query of the call sees (n_q = all queries, no draft
+                       // keys among its n_kv), seq[b + 1] for the own rows of sequence b; every piece of every
+                       // sequence leaves partials, and a row's result is the merge of both sets
   SeqPlan seq[VMLA_MAX_BATCH];
 };
 
@@ -89,6 +91,13 @@ struct PlanShape {
 int build_plan(int kernel, int batch, int num_heads, const int32_t* qo_indptr_host,
                const int32_t* kv_indptr_host, int splits, int num_sms, int tc_clusters, PlanParams* pp,
                vmla_plan_info* info);
+
+// The plan of a shared-prefix call (tensor-core kernel): batch + 1 entries of pp->seq, see
+// PlanParams::shared.  kv_indptr_host counts own rows only; shared_rows >= 1.
+struct StageMap;
+int build_shared_plan(int batch, int num_heads, int64_t shared_rows, const int32_t* qo_indptr_host,
+                      const int32_t* kv_indptr_host, const StageMap& map, int splits, int num_sms, int tc_clusters,
+                      PlanParams* pp, vmla_plan_info* info);
 
 // Clusters of the tensor-core kernel that are co-resident on the current device.
 int tc_max_clusters(int* out);
@@ -138,6 +147,22 @@ struct RunArgs {
   int32_t test_fault;       // 0; kFaultNoQReady only in the failure test
   uint32_t* status;
 };
+
+// Where a shared-prefix call stages its rows: entry 0 the shared ones, entry b + 1 the own rows
+// of sequence b, each from a multiple of kStageAlign on, the rows between filled with zeros.  So
+// no tile holds rows of two entries, and a sequence's result depends on no other's rows.
+constexpr int kStageAlign = 128;
+struct StageMap {
+  int32_t entries;
+  int32_t total;                     // staged rows, zeros included
+  int32_t off[VMLA_MAX_BATCH + 1];   // first staged row of each entry; off[entries] = total
+  int32_t len[VMLA_MAX_BATCH];       // its rows
+  int32_t src[VMLA_MAX_BATCH];       // its first index in kv_indices (entry 0: in shared_indices)
+};
+// Fills the map (entries = batch + 1 <= VMLA_MAX_BATCH); false when the staged rows pass 2^31.
+bool build_stage_map(int batch, int64_t shared_rows, const int32_t* kv_indptr_host, StageMap* map);
+// Gather of a shared-prefix call into args.staged.
+int launch_gather_shared(const RunArgs& args, const int32_t* shared_indices, const StageMap& map, void* stream);
 
 // One verify call on a caller-provided workspace (argument checks, plan, launches).
 // kv_indices NULL and run_base given: the rows of sequence b are the pool's
@@ -232,6 +257,10 @@ int launch_tc(const PlanParams& plan, const RunArgs& args, void* stream);
 int launch_gather(const RunArgs& args, void* stream);
 int launch_merge(const PlanParams& plan, const float* part_o, const float* part_lse, int lse_is_log2,
                  uint16_t* out, float* lse, void* stream);
+// Merge of a shared-prefix plan: every query row from its pieces over the shared rows and over
+// its sequence's own rows (part_lse in the log2 domain).
+int launch_merge_shared(const PlanParams& plan, const float* part_o, const float* part_lse, uint16_t* out, float* lse,
+                        void* stream);
 int launch_tree_mask(const int32_t* parent, const int32_t* qo_indptr, int batch, int total_q, uint64_t* mask_out,
                      uint32_t* status, void* stream);
 

@@ -161,6 +161,114 @@ __device__ __forceinline__ void merge_row(const PlanParams& plan, int mrow, int 
   if (part == 0 && lane == 0) lse[orow] = (M + log2f(W)) * 0.6931471805599453f;
 }
 
+// Pieces of row r of entry b of a plan (its last piece count in a lane plan depends on the
+// row's stream).
+__device__ __forceinline__ int row_pieces(const PlanParams& plan, const SeqPlan& s, int r) {
+  if (plan.lane_width == 0) return s.n_split;
+  const int64_t T = plan_seq_tiles(s.n_kv);
+  const int g = r / (plan.lane_width * plan.rows_per_unit);
+  return (int)plan_stream_pieces(s.lane_cost + g * (T + kLaneStreamTiles), T, plan.lane_tiles);
+}
+
+// The same merge for query row `row` of a shared-prefix plan: its pieces over the shared rows
+// (entry 0), then those over its sequence's own rows, at most 64 of each; a lane holds the lse
+// of pieces lane + 32 k of the joined list.
+template <int WPR>
+__device__ __forceinline__ void merge_shared_row(const PlanParams& plan, int row, int part,
+                                                 const float* __restrict__ part_o, const float* __restrict__ part_lse,
+                                                 uint16_t* __restrict__ out, float* __restrict__ lse) {
+  constexpr int F = 4 / WPR;
+  constexpr int kBatch = kMergeInFlight / F;
+  const int lane = threadIdx.x & 31;
+  const int H = plan.num_heads;
+  const int t = row / H;
+  // the sequence of query t: the last of entries 1 .. batch - 1 whose queries start at or before t
+  int lo = 1, hi = plan.batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (plan.seq[mid].q_off <= t) lo = mid; else hi = mid;
+  }
+  const SeqPlan& s0 = plan.seq[0];
+  const SeqPlan& s1 = plan.seq[lo];
+  const int r1 = row - s1.q_off * H;
+  const int S0 = row_pieces(plan, s0, row), S = S0 + row_pieces(plan, s1, r1);
+  const int64_t R0 = (int64_t)s0.n_q * H, R1 = (int64_t)s1.n_q * H;
+  const int64_t p0 = s0.part_off + (int64_t)row, p1 = s1.part_off + (int64_t)r1;
+  auto partial_row = [&](int p) { return p < S0 ? p0 + p * R0 : p1 + (p - S0) * R1; };
+  const float4* src = reinterpret_cast<const float4*>(part_o) + part * F * 32 + lane;
+  float4 v[kBatch][F];
+  auto load = [&](int first) {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+        v[b][f] = first + b < S ? __ldg(src + partial_row(first + b) * (kDv / 4) + f * 32)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  load(0);
+  constexpr int kWords = 4;  // 128 pieces
+  float l[kWords], m = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kWords; ++k) {
+    l[k] = lane + 32 * k < S ? part_lse[partial_row(lane + 32 * k)] : -INFINITY;
+    m = fmaxf(m, l[k]);
+  }
+  const float M = warp_max(m);
+  uint2* dst = reinterpret_cast<uint2*>(out + (int64_t)row * kDv) + part * F * 32 + lane;
+  if (M == -INFINITY) {
+#pragma unroll
+    for (int f = 0; f < F; ++f) dst[f * 32] = make_uint2(0u, 0u);
+    if (part == 0 && lane == 0) lse[row] = -INFINITY;
+    return;
+  }
+  float w[kWords], sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < kWords; ++k) {
+    w[k] = exp2f(l[k] - M);
+    sum += w[k];
+  }
+  const float W = warp_sum(sum);
+  const float invW = 1.f / W;
+  float4 acc[F];
+#pragma unroll
+  for (int f = 0; f < F; ++f) acc[f] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int first = 0; first < S; first += kBatch) {
+    if (first > 0) load(first);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int p = first + b;
+      // every lane takes part in the shuffle; a piece without weight is skipped, so whatever its
+      // partial row holds never reaches the sum
+      const float mine = p < 64 ? (p < 32 ? w[0] : w[1]) : (p < 96 ? w[2] : w[3]);
+      const float wp = __shfl_sync(0xffffffffu, mine, p & 31);
+      if (p < S && wp != 0.f) {
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+          acc[f].x = fmaf(wp, v[b][f].x, acc[f].x);
+          acc[f].y = fmaf(wp, v[b][f].y, acc[f].y);
+          acc[f].z = fmaf(wp, v[b][f].z, acc[f].z);
+          acc[f].w = fmaf(wp, v[b][f].w, acc[f].w);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int f = 0; f < F; ++f)
+    dst[f * 32] = make_uint2(pack_bf16x2(acc[f].x * invW, acc[f].y * invW), pack_bf16x2(acc[f].z * invW, acc[f].w * invW));
+  if (part == 0 && lane == 0) lse[row] = (M + log2f(W)) * 0.6931471805599453f;
+}
+
+template <int WPR>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+merge_shared_kernel(const __grid_constant__ PlanParams plan, const float* __restrict__ part_o,
+                    const float* __restrict__ part_lse, uint16_t* __restrict__ out, float* __restrict__ lse) {
+  grid_dependency_wait();  // started under the verify kernel's tail: its partials first
+  constexpr int kRowsPerBlock = kMergeWarps / WPR;
+  const int w = threadIdx.x >> 5;
+  const int row = blockIdx.x * kRowsPerBlock + w / WPR;
+  if (row < plan.merge_rows) merge_shared_row<WPR>(plan, row, w % WPR, part_o, part_lse, out, lse);
+}
+
 // Each block merges kMergeWarps / WPR rows at a time: rows blockIdx.x (rows per block) + i,
 // then a grid's worth further, and so on.
 template <int WPR>
@@ -258,6 +366,27 @@ int launch_merge(const PlanParams& plan, const float* part_o, const float* part_
   else if (wpr == 2) e = cudaLaunchKernelEx(&cfg, merge_kernel<2>, plan, part_o, part_lse, lse_is_log2, out, lse);
   else e = cudaLaunchKernelEx(&cfg, merge_kernel<1>, plan, part_o, part_lse, lse_is_log2, out, lse);
   return e == cudaSuccess ? VMLA_OK : VMLA_ERR_CUDA;
+}
+
+int launch_merge_shared(const PlanParams& plan, const float* part_o, const float* part_lse, uint16_t* out, float* lse,
+                        void* stream) {
+  if (plan.merge_rows == 0) return VMLA_OK;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) !=
+                                                cudaSuccess)
+    return VMLA_ERR_CUDA;
+  // a row has at most max_splits pieces of either entry
+  const int wpr = merge_warps_per_row(plan.merge_rows, 2 * plan.max_splits, sms);
+  const int rows_per_block = kMergeWarps / wpr;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1] = {early_start_attribute()};
+  cfg.gridDim = dim3((unsigned)((plan.merge_rows + rows_per_block - 1) / rows_per_block), 1, 1);
+  cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
+  cfg.stream = (cudaStream_t)stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const auto kernel = wpr == 4 ? merge_shared_kernel<4> : wpr == 2 ? merge_shared_kernel<2> : merge_shared_kernel<1>;
+  return cudaLaunchKernelEx(&cfg, kernel, plan, part_o, part_lse, out, lse) == cudaSuccess ? VMLA_OK : VMLA_ERR_CUDA;
 }
 
 int launch_tree_mask(const int32_t* parent, const int32_t* qo_indptr, int batch, int total_q, uint64_t* mask_out,

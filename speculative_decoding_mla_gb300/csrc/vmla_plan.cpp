@@ -209,8 +209,10 @@ WorkspaceLayout workspace_layout(int64_t total_q, int64_t partial_rows, int64_t 
   return w;
 }
 
-int build_plan(int kernel, int batch, int num_heads, const int32_t* qo, const int32_t* kv, int splits, int num_sms,
-               int tc_clusters, PlanParams* pp, vmla_plan_info* info) {
+// shared: entry 0 holds the shared rows and every query of the call (its counts are not a
+// sequence's), and the partial rows are laid out by the caller.
+static int build_plan_impl(int kernel, int batch, int num_heads, const int32_t* qo, const int32_t* kv, int splits,
+                           int num_sms, int tc_clusters, PlanParams* pp, vmla_plan_info* info, bool shared) {
   if (!qo || !kv || !pp) return VMLA_ERR_NULL;
   if (kernel != VMLA_KERNEL_TC && kernel != VMLA_KERNEL_SIMT) return VMLA_ERR_SHAPE;
   if (batch < 0 || batch > VMLA_MAX_BATCH || num_heads < 1 || num_heads > VMLA_MAX_HEADS) return VMLA_ERR_SHAPE;
@@ -218,7 +220,7 @@ int build_plan(int kernel, int batch, int num_heads, const int32_t* qo, const in
   const bool force_lanes = splits == VMLA_SPLITS_LANES;
   if (force_lanes) splits = 0;  // the uniform plan it falls back on is the planner's own
   if (qo[0] != 0 || kv[0] != 0) return VMLA_ERR_SHAPE;
-  for (int b = 0; b < batch; ++b)
+  for (int b = shared ? 1 : 0; b < batch; ++b)
     if (plan_check_seq((int64_t)qo[b + 1] - qo[b], (int64_t)kv[b + 1] - kv[b]) != VMLA_OK) return VMLA_ERR_SHAPE;
   const PlanShape sh = plan_shape(kernel);
   std::memset(pp, 0, sizeof(PlanParams));
@@ -273,6 +275,62 @@ int build_plan(int kernel, int batch, int num_heads, const int32_t* qo, const in
     info->lane_width = pp->lane_width;
     info->lane_count = pp->lane_count;
   }
+  return VMLA_OK;
+}
+
+int build_plan(int kernel, int batch, int num_heads, const int32_t* qo, const int32_t* kv, int splits, int num_sms,
+               int tc_clusters, PlanParams* pp, vmla_plan_info* info) {
+  return build_plan_impl(kernel, batch, num_heads, qo, kv, splits, num_sms, tc_clusters, pp, info, false);
+}
+
+bool build_stage_map(int batch, int64_t shared_rows, const int32_t* kv, StageMap* map) {
+  int64_t off = 0;
+  map->entries = batch + 1;
+  for (int e = 0; e <= batch; ++e) {
+    const int64_t len = e == 0 ? shared_rows : (int64_t)kv[e] - kv[e - 1];
+    map->off[e] = (int32_t)off;
+    map->len[e] = (int32_t)len;
+    map->src[e] = e == 0 ? 0 : kv[e - 1];
+    off += (len + kStageAlign - 1) / kStageAlign * kStageAlign;
+    if (off > INT32_MAX) return false;
+  }
+  map->off[batch + 1] = map->total = (int32_t)off;
+  return true;
+}
+
+int build_shared_plan(int batch, int num_heads, int64_t shared_rows, const int32_t* qo, const int32_t* kv,
+                      const StageMap& map, int splits, int num_sms, int tc_clusters, PlanParams* pp,
+                      vmla_plan_info* info) {
+  if (!qo || !kv || !pp || !info) return VMLA_ERR_NULL;
+  if (batch < 1 || batch > VMLA_MAX_BATCH - 1 || shared_rows < 1 || qo[0] != 0 || kv[0] != 0) return VMLA_ERR_SHAPE;
+  const int64_t total_q = qo[batch], total_kv = shared_rows + kv[batch];
+  if (total_q > (int64_t)batch * VMLA_MAX_DRAFT || total_kv > INT32_MAX) return VMLA_ERR_SHAPE;
+  // entry 0 with the shared rows and all queries, then each sequence's own rows
+  static thread_local int32_t qo2[VMLA_MAX_BATCH + 1], kv2[VMLA_MAX_BATCH + 1];
+  qo2[0] = kv2[0] = 0;
+  for (int b = 0; b <= batch; ++b) {
+    qo2[b + 1] = (int32_t)total_q + qo[b];
+    kv2[b + 1] = (int32_t)shared_rows + kv[b];
+  }
+  int rc = build_plan_impl(VMLA_KERNEL_TC, batch + 1, num_heads, qo2, kv2, splits, num_sms, tc_clusters, pp, info, true);
+  if (rc != VMLA_OK) return rc;
+  // every piece leaves partials, uncut ones too: a row always has pieces of two entries
+  int64_t part = 0;
+  for (int b = 0; b <= batch; ++b) {
+    SeqPlan& s = pp->seq[b];
+    s.q_off = b == 0 ? 0 : qo[b - 1];
+    s.kv_off = map.off[b];
+    s.part_off = (int32_t)part;
+    s.merge_off = 0;
+    part += (int64_t)s.n_q * num_heads * s.n_split;
+    if (part > INT32_MAX / kDv) return VMLA_ERR_SHAPE;
+  }
+  pp->shared = 1;
+  pp->partial_rows = (int32_t)part;
+  pp->merge_rows = (int32_t)(total_q * num_heads);
+  info->partial_rows = pp->partial_rows;
+  info->merge_rows = pp->merge_rows;
+  info->workspace_bytes = workspace_layout(total_q, part, map.total).total;
   return VMLA_OK;
 }
 

@@ -186,7 +186,20 @@ struct UnitInfo {
   int b, rb, piece, n_pieces, R, prefix, k_lo, k_hi, n_tiles;
 };
 
+// In a shared-prefix plan entry 0's keys are visible to every query (it has no draft keys), and
+// every unit leaves partials.  kShared is a template parameter of the kernel, so that the plain
+// calls' code does not change.
+template <bool kShared>
+__device__ __forceinline__ int unit_prefix(const SeqPlan& s, int b) {
+  return kShared && b == 0 ? s.n_kv : s.n_kv - s.n_q;
+}
+template <bool kShared>
+__device__ __forceinline__ bool whole_rows(const UnitInfo& ui) {
+  return !kShared && ui.n_pieces == 1;
+}
+
 // Unit u of a uniform plan.
+template <bool kShared>
 __device__ __forceinline__ UnitInfo decode_unit(const PlanParams& p, int u) {
   UnitInfo ui;
   ui.b = seq_of_unit(p, u);
@@ -196,7 +209,7 @@ __device__ __forceinline__ UnitInfo decode_unit(const PlanParams& p, int u) {
   ui.piece = local / s.n_rb;
   ui.n_pieces = s.n_split;
   ui.R = s.n_q * p.num_heads;
-  ui.prefix = s.n_kv - s.n_q;
+  ui.prefix = unit_prefix<kShared>(s, ui.b);
   ui.k_lo = ui.piece * s.chunk;
   ui.k_hi = min(s.n_kv, ui.k_lo + s.chunk);
   ui.n_tiles = (ui.k_hi - ui.k_lo + kTileKeys - 1) / kTileKeys;
@@ -237,6 +250,7 @@ __device__ __forceinline__ void lane_streams(const PlanParams& p, int l, int* s_
 
 // Stream s of a lane plan as seen by cluster j of lane l: row block g G + j of
 // the stream's sequence over the tiles of the stream that fall in the lane.
+template <bool kShared>
 __device__ __forceinline__ UnitInfo decode_lane_unit(const PlanParams& p, int s, int l, int j) {
   UnitInfo ui;
   ui.b = seq_of_unit(p, s);
@@ -251,7 +265,7 @@ __device__ __forceinline__ UnitInfo decode_lane_unit(const PlanParams& p, int s,
   ui.piece = (int)(l - A / L);
   ui.n_pieces = (int)plan_stream_pieces(A, T, L);
   ui.R = sp.n_q * p.num_heads;
-  ui.prefix = sp.n_kv - sp.n_q;
+  ui.prefix = unit_prefix<kShared>(sp, ui.b);
   ui.k_lo = (int)(lo * kTileKeys);
   ui.k_hi = min(sp.n_kv, (int)(hi * kTileKeys));
   ui.n_tiles = (int)(hi - lo);
@@ -260,10 +274,11 @@ __device__ __forceinline__ UnitInfo decode_lane_unit(const PlanParams& p, int s,
 
 // The k-th entry of this cluster's work list: an index of the schedule's order
 // (uniform plan) or a stream index (lane plan).
+template <bool kShared>
 __device__ __forceinline__ UnitInfo unit_at(const PlanParams& p, const TcSched& sched, int k) {
-  if (p.lane_width == 0) return decode_unit(p, sched.unit_base + sched.order[k]);
+  if (p.lane_width == 0) return decode_unit<kShared>(p, sched.unit_base + sched.order[k]);
   const int cid = (int)cluster_id_x();
-  return decode_lane_unit(p, k, cid / p.lane_width, cid % p.lane_width);
+  return decode_lane_unit<kShared>(p, k, cid / p.lane_width, cid % p.lane_width);
 }
 
 // Sets the abort flag of every CTA of the cluster.
@@ -344,9 +359,10 @@ __device__ __noinline__ void settle_after_abort() {
   }
 }
 
+template <bool kShared>
 __device__ __forceinline__ int total_tiles(const PlanParams& plan, const TcSched& sched, int u_begin, int u_end) {
   int total = 0;
-  for (int k = u_begin; k < u_end; ++k) total += unit_at(plan, sched, k).n_tiles;
+  for (int k = u_begin; k < u_end; ++k) total += unit_at<kShared>(plan, sched, k).n_tiles;
   return total;
 }
 
@@ -363,6 +379,7 @@ __device__ __forceinline__ int total_tiles(const PlanParams& plan, const TcSched
 // 128) through both K stages: latent chunk c of row half h into stage h, chunk
 // c; the rope chunk into qrope.  The softmax warps move the latent part into
 // tensor memory and release the stages (qfree) before the first K tile loads.
+template <bool kShared>
 __device__ void producer_role(TcSmem& sm, const CUtensorMap* map, const CUtensorMap* vmap, const CUtensorMap* qmap,
                               const PlanParams& plan, const TcSched& sched, const RunArgs& a, int u_begin, int u_end,
                               uint32_t rank) {
@@ -378,7 +395,7 @@ __device__ void producer_role(TcSmem& sm, const CUtensorMap* map, const CUtensor
   grid_dependency_wait();
   if (rank == 0) VTRACE_CLUSTER(28);  // the launch before this one is complete
   for (int ui_idx = u_begin; ui_idx < u_end && ok; ++ui_idx) {
-    const UnitInfo ui = unit_at(plan, sched, ui_idx);
+    const UnitInfo ui = unit_at<kShared>(plan, sched, ui_idx);
     const SeqPlan& sp = plan.seq[ui.b];
     // first row of the sequence in the tensor map: its staged offset, or its pool run
     // (a run outside the pool only reads the out-of-range fill; a check kernel reports it)
@@ -445,13 +462,14 @@ __device__ void producer_role(TcSmem& sm, const CUtensorMap* map, const CUtensor
 // ------------------------------------------------------------------ rank 0: score MMA issuer (warp 1, lane 0)
 // Per tile: 32 M256 N128 K16 MMAs with A = Q latent from TMEM, then 4 with
 // A = Q rope from shared memory; B = the pair's K rows (K-major).
+template <bool kShared>
 __device__ void scorer_mma_role(TcSmem& sm, const PlanParams& plan, const TcSched& sched, const RunArgs& a,
                                 uint32_t tbase, int u_begin, int u_end) {
   constexpr uint32_t idesc = idesc_bf16_f32(kRowsUnit, kTileKeys, 0, 0);
   ScorerSmem& S = sm.u.s;
   int it = 0, uu = 0;
   for (int ui_idx = u_begin; ui_idx < u_end; ++ui_idx, ++uu) {
-    const UnitInfo ui = unit_at(plan, sched, ui_idx);
+    const UnitInfo ui = unit_at<kShared>(plan, sched, ui_idx);
     if (!wait_bar(sm, &sm.c.qfull, uu & 1, a.status, 200)) break;
     tc_fence_after();
     bool ok = true;
@@ -506,6 +524,7 @@ __device__ void scorer_mma_role(TcSmem& sm, const PlanParams& plan, const TcSche
 // all keep the same running reference max m_ref (raised only when a message
 // exceeds it by 2^kTau, which bounds P by 2^kTau and makes rescales rare).
 // The P message is staged in shared memory; the sender thread ships it.
+template <bool kShared>
 __device__ void scorer_softmax_role(TcSmem& sm, const PlanParams& plan, const TcSched& sched, const RunArgs& a,
                                     uint32_t tbase, int u_begin, int u_end, uint32_t rank) {
   constexpr int kPairThreads = 32 * kParts;  // the warps of one TMEM lane quarter (both parts of its rows)
@@ -526,7 +545,7 @@ __device__ void scorer_softmax_role(TcSmem& sm, const PlanParams& plan, const Tc
   // stream is complete (the kernel may start under the gather's tail)
   grid_dependency_wait();
   for (int ui_idx = u_begin; ui_idx < u_end && !stop; ++ui_idx, ++uu) {
-    const UnitInfo ui = unit_at(plan, sched, ui_idx);
+    const UnitInfo ui = unit_at<kShared>(plan, sched, ui_idx);
     const SeqPlan& sp = plan.seq[ui.b];
     const int r = ui.rb * kRowsUnit + (int)(rank & 1) * kRowsCta + row;
     const bool valid = r < ui.R;
@@ -576,7 +595,8 @@ __device__ void scorer_softmax_role(TcSmem& sm, const PlanParams& plan, const Tc
       }
     }
     const int i = valid ? r / H : 0;
-    const uint64_t vis = a.masks ? a.masks[sp.q_off + i] : causal_bits(i);
+    // (entry 0 of a shared plan has more than 64 queries and no draft keys: its word is not used)
+    const uint64_t vis = a.masks ? a.masks[sp.q_off + i] : causal_bits(kShared ? i & 63 : i);
     const int mask_from = min(ui.prefix, ui.k_hi);  // keys below this are visible to every valid row
     float m_ref = -INFINITY, l = 0.f;
     for (int t = 0; t < ui.n_tiles && !stop; ++t, ++it) {
@@ -701,13 +721,14 @@ __device__ void scorer_softmax_role(TcSmem& sm, const PlanParams& plan, const Tc
 // Ships each staged message (and, after a unit's last message, the unit's
 // finals) into the matching mixer CTA's receive slot, then reports when the
 // copy has left the staging buffer.
+template <bool kShared>
 __device__ void scorer_sender_role(TcSmem& sm, const PlanParams& plan, const TcSched& sched, const RunArgs& a,
                                    int u_begin, int u_end, uint32_t rank) {
   ScorerSmem& S = sm.u.s;
   const uint32_t mixer = rank + 2;
   int it = 0, uu = 0, msg = 0;
   for (int ui_idx = u_begin; ui_idx < u_end; ++ui_idx, ++uu) {
-    const UnitInfo ui = unit_at(plan, sched, ui_idx);
+    const UnitInfo ui = unit_at<kShared>(plan, sched, ui_idx);
     for (int t = 0; t < ui.n_tiles; ++t, ++it) {
       for (int j = 0; j < kMsgsPerTile; ++j, ++msg) {
         const int sg = msg % kStages;
@@ -767,6 +788,7 @@ __device__ void scorer_forward_role(TcSmem& sm, const RunArgs& a, int total) {
 // MMAs, A = P (K-major, 128 rows in each mixer CTA), B = value columns of the
 // message's 64 rows of the tile stage (MN-major view of the 128-byte-swizzled
 // chunks: leading byte offset = chunk stride).
+template <bool kShared>
 __device__ void mixer_mma_role(TcSmem& sm, const PlanParams& plan, const TcSched& sched, const RunArgs& a,
                                uint32_t tbase, int u_begin, int u_end) {
   constexpr uint32_t idesc = idesc_bf16_f32(kRowsUnit, 256, 0, 1);
@@ -794,7 +816,7 @@ __device__ void mixer_mma_role(TcSmem& sm, const PlanParams& plan, const TcSched
     return r;
   };
   for (int ui_idx = u_begin; ui_idx < u_end && ok; ++ui_idx) {
-    const UnitInfo ui = unit_at(plan, sched, ui_idx);
+    const UnitInfo ui = unit_at<kShared>(plan, sched, ui_idx);
     for (int t = 0; t < ui.n_tiles && ok; ++t, ++it) {
       for (int j = 0; j < kMsgsPerTile; ++j, ++msg) {
         const int s = msg % kVStages;  // V stage of this message
@@ -885,6 +907,7 @@ __device__ void mixer_release_role(TcSmem& sm, const RunArgs& a, int total_msgs,
 constexpr int kEpiThreads = 256;
 __device__ __forceinline__ int epi_gran(int row, int k) { return k ^ ((row >> 1) & 3); }  // conflict-free both ways
 
+template <bool kShared>
 __device__ void mixer_epilogue_role(TcSmem& sm, const CUtensorMap* omap, const CUtensorMap* pmap,
                                     const PlanParams& plan, const TcSched& sched, const RunArgs& a, uint32_t tbase,
                                     int u_begin, int u_end, uint32_t rank) {
@@ -959,7 +982,7 @@ __device__ void mixer_epilogue_role(TcSmem& sm, const CUtensorMap* omap, const C
       // store; a group of 32 rows that runs past the unit's rows is stored by the
       // lanes instead (eight rows' 64 contiguous bytes per instruction), so that
       // nothing is written past them.
-      const UnitInfo ui = unit_at(plan, sched, ui_idx);
+      const UnitInfo ui = unit_at<kShared>(plan, sched, ui_idx);
       const SeqPlan& sp = plan.seq[ui.b];
       const int f = uu & 1;
       const float m = M.fin[f].m[row], lsum = M.fin[f].l[row];
@@ -995,7 +1018,7 @@ __device__ void mixer_epilogue_role(TcSmem& sm, const CUtensorMap* omap, const C
           __syncwarp();
         }
       };
-      if (ui.n_pieces == 1) {
+      if (whole_rows<kShared>(ui)) {
         const int64_t orow = (int64_t)sp.q_off * H + (valid ? r : 0);
         const int64_t orow_w = (int64_t)sp.q_off * H + r_w;
 #pragma unroll 1
@@ -1056,6 +1079,7 @@ __device__ void mixer_epilogue_role(TcSmem& sm, const CUtensorMap* omap, const C
 
 // The kernel body; `plan` and `sched` are kernel parameters (host-planned
 // calls) or live in the workspace (device-planned calls).
+template <bool kShared>
 __device__ __forceinline__ void tc_verify_body(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                                const CUtensorMap& qmap, const CUtensorMap& omap,
                                                const CUtensorMap& pmap, const PlanParams& plan,
@@ -1123,7 +1147,7 @@ __device__ __forceinline__ void tc_verify_body(const CUtensorMap& kmap, const CU
     tmem_alloc_pair(&sm.c.tmem_base, 512);
     tmem_relinquish_pair();
   }
-  const int n_tiles_all = total_tiles(plan, sched, u_begin, u_end);
+  const int n_tiles_all = total_tiles<kShared>(plan, sched, u_begin, u_end);
   const int total_msgs = kMsgsPerTile * n_tiles_all;
   // every barrier object is initialised before any thread of this CTA arms or
   // waits on one (the arming below runs in another warp than the initialisation)
@@ -1147,24 +1171,24 @@ __device__ __forceinline__ void tc_verify_body(const CUtensorMap& kmap, const CU
   }
 
   if (warp == 0) {
-    if (lane == 0) producer_role(sm, &kmap, &vmap, &qmap, plan, sched, a, u_begin, u_end, rank);
+    if (lane == 0) producer_role<kShared>(sm, &kmap, &vmap, &qmap, plan, sched, a, u_begin, u_end, rank);
   } else if (warp == 1) {
     if (lane == 0) {
-      if (rank == 0) scorer_mma_role(sm, plan, sched, a, tbase, u_begin, u_end);
-      else if (rank == 2) mixer_mma_role(sm, plan, sched, a, tbase, u_begin, u_end);
+      if (rank == 0) scorer_mma_role<kShared>(sm, plan, sched, a, tbase, u_begin, u_end);
+      else if (rank == 2) mixer_mma_role<kShared>(sm, plan, sched, a, tbase, u_begin, u_end);
       else if (rank == 3) mixer_relay_role(sm, a, total_msgs);
       else scorer_forward_role(sm, a, n_tiles_all);
     }
   } else if (rank < 2) {
     if (warp == kSenderWarp) {
-      if (lane == 0) scorer_sender_role(sm, plan, sched, a, u_begin, u_end, rank);
+      if (lane == 0) scorer_sender_role<kShared>(sm, plan, sched, a, u_begin, u_end, rank);
     } else {
-      scorer_softmax_role(sm, plan, sched, a, tbase, u_begin, u_end, rank);
+      scorer_softmax_role<kShared>(sm, plan, sched, a, tbase, u_begin, u_end, rank);
     }
   } else if (warp == 6) {
     if (lane == 0) mixer_release_role(sm, a, total_msgs, rank);
   } else {
-    mixer_epilogue_role(sm, &omap, &pmap, plan, sched, a, tbase, u_begin, u_end, rank);  // warps 2-5 and 7-10
+    mixer_epilogue_role<kShared>(sm, &omap, &pmap, plan, sched, a, tbase, u_begin, u_end, rank);  // warps 2-5 and 7-10
   }
   __syncwarp();
   tc_fence_before();
@@ -1194,12 +1218,13 @@ __device__ __forceinline__ void tc_verify_body(const CUtensorMap& kmap, const CU
   }
 }
 
+template <bool kShared>
 __global__ void __launch_bounds__(kThreadsTC, 1)
 tc_verify_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                  const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap,
                  const __grid_constant__ CUtensorMap pmap, const __grid_constant__ PlanParams plan,
                  const __grid_constant__ TcSched sched, const RunArgs a) {
-  tc_verify_body(kmap, vmap, qmap, omap, pmap, plan, sched, a);
+  tc_verify_body<kShared>(kmap, vmap, qmap, omap, pmap, plan, sched, a);
 }
 
 // Same kernel with the plan and the cluster schedule read from the workspace,
@@ -1212,7 +1237,7 @@ tc_verify_kernel_dplan(const __grid_constant__ CUtensorMap kmap, const __grid_co
   // started early behind a kernel that itself may still wait for the planner: the plan
   // and the schedule are read only once everything before this launch is complete
   grid_dependency_wait();
-  tc_verify_body(kmap, vmap, qmap, omap, pmap, *plan, *sched, a);
+  tc_verify_body<false>(kmap, vmap, qmap, omap, pmap, *plan, *sched, a);
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -1319,7 +1344,9 @@ int tc_max_clusters(int* out) {
     *out = cached[dev];
     return VMLA_OK;
   }
-  if (cudaFuncSetAttribute(tc_verify_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
+  if (cudaFuncSetAttribute(tc_verify_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
+          cudaSuccess ||
+      cudaFuncSetAttribute(tc_verify_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
           cudaSuccess ||
       cudaFuncSetAttribute(tc_verify_kernel_dplan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
           cudaSuccess)
@@ -1327,7 +1354,7 @@ int tc_max_clusters(int* out) {
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = cluster_config(1, attr);
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, tc_verify_kernel, &cfg) != cudaSuccess || n < 1) return VMLA_ERR_CUDA;
+  if (cudaOccupancyMaxActiveClusters(&n, tc_verify_kernel<false>, &cfg) != cudaSuccess || n < 1) return VMLA_ERR_CUDA;
   if (dev < 64) cached[dev] = n;
   *out = n;
   return VMLA_OK;
@@ -1346,6 +1373,7 @@ int launch_tc(const PlanParams& plan, const RunArgs& a, void* stream) {
   // and the epilogue's output maps
   CUtensorMap kmap, vmap, qmap, omap, pmap;
   if (!encode_maps(enc, a, &kmap, &vmap, &qmap, &omap, &pmap)) return VMLA_ERR_CUDA;
+  const auto kernel = plan.shared ? tc_verify_kernel<true> : tc_verify_kernel<false>;
   static thread_local TcSched sched;
   if (plan.lane_width > 0) {
     // a lane plan: one launch of lane_count lanes, each cluster working out its own streams
@@ -1355,7 +1383,7 @@ int launch_tc(const PlanParams& plan, const RunArgs& a, void* stream) {
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = cluster_config(sched.num_clusters, attr, true);
     cfg.stream = (cudaStream_t)stream;
-    if (cudaLaunchKernelEx(&cfg, tc_verify_kernel, kmap, vmap, qmap, omap, pmap, plan, sched, a) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, kernel, kmap, vmap, qmap, omap, pmap, plan, sched, a) != cudaSuccess)
       return VMLA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? VMLA_OK : VMLA_ERR_CUDA;
   }
@@ -1367,7 +1395,7 @@ int launch_tc(const PlanParams& plan, const RunArgs& a, void* stream) {
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = cluster_config(sched.num_clusters, attr, true);
     cfg.stream = (cudaStream_t)stream;
-    if (cudaLaunchKernelEx(&cfg, tc_verify_kernel, kmap, vmap, qmap, omap, pmap, plan, sched, a) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, kernel, kmap, vmap, qmap, omap, pmap, plan, sched, a) != cudaSuccess)
       return VMLA_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? VMLA_OK : VMLA_ERR_CUDA;
