@@ -54,6 +54,7 @@ extern "C" {
 #define VMLA_MAX_DRAFT 64 /* draft positions per sequence (one 64-bit visibility word each) */
 #define VMLA_MAX_BATCH 512
 #define VMLA_MAX_HEADS 128
+#define VMLA_MAX_VOCAB 262144 /* tokens of a row that verify_attn_mla_sample draws from */
 #define VMLA_WORKSPACE_ALIGN 256
 
 typedef enum vmla_status {
@@ -67,7 +68,8 @@ typedef enum vmla_status {
   VMLA_ERR_INDEX = -7,     /* a kv slot index was outside [0, pool_slots); that key still takes part,
                               with a row of zeros (score 0, value 0), in every kernel */
   VMLA_ERR_DEVICE = -8,    /* no usable sm_103 device for this library */
-  VMLA_ERR_PARENT = -9     /* a parent index was not in [-1, i) (mask left empty) */
+  VMLA_ERR_PARENT = -9,    /* a parent index was not in [-1, i) (mask left empty) */
+  VMLA_ERR_PARAM = -10     /* a row's sampling setting was out of range (that row draws no token) */
 } vmla_status;
 
 /* Description of the split plan a call would use (host only, no GPU needed). */
@@ -353,6 +355,38 @@ int verify_attn_mla_shared(const void* q, const void* kv_pool, int64_t pool_slot
                            const int32_t* parent, const int32_t* kv_indptr_host, const int32_t* qo_indptr_host,
                            int batch, int num_heads, float sm_scale, int splits, void* out, float* lse,
                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* The target's tokens that verify_attn_mla_tree_accept compares the drafts with
+ * (target_token, root_token), drawn from the verified logits instead of taken
+ * greedily; the pages do not describe sampling.  For row r with temperature T:
+ *   w_i   = exp((x_i - max x) / T) for token i with logit x_i
+ *   order = tokens by logit, descending, equal ones by index
+ *   top-k keeps the order's first top_k[r] tokens (<= 0 or >= vocab: all)
+ *   top-p keeps the shortest prefix of those with mass >= top_p[r] x their mass
+ *   min-p keeps the tokens with w_i >= min_p[r]
+ *   token[r] = the smallest index i with sum over kept j <= i of w_j
+ *              > uniform[r] x sum over all kept of w_j
+ * and for T = 0 the lowest index among the largest logits.  Weights are exact to
+ * about 2^-37 and summed without rounding, so the result does not depend on the
+ * order of summation; weights below 2^-46 of the largest count as zero.
+ *   logits   [rows, vocab], logits_fp32 0: bf16, 1: fp32; row_stride elements
+ *            from row to row (>= vocab; any alignment to the element's size).
+ *            -inf forbids a token and NaN counts as -inf; tokens at +inf share
+ *            the draw evenly.  A row without any other logit draws -1 (no error)
+ *   vocab    1 .. VMLA_MAX_VOCAB
+ *   temperature [rows] fp32: 0, or 2^-20 .. 2^20; NULL: 1
+ *   top_k    [rows] int32;  top_p [rows] fp32 in (0, 1];  min_p [rows] fp32 in
+ *            [0, 1]; NULL: off
+ *   uniform  [rows] fp32 in [0, 1]: the random numbers (1 draws the last kept
+ *            token of weight)
+ *   token    [rows] int32 out
+ *   status_word  optional, two uint32: a setting out of its range (in a greedy
+ *            row too) records VMLA_ERR_PARAM with the row, which draws -1
+ * Argument errors return before the launch.  One launch, no workspace, no host
+ * synchronisation; capture-safe. */
+int verify_attn_mla_sample(const void* logits, int logits_fp32, int64_t row_stride, int64_t rows, int vocab,
+                           const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                           const float* uniform, int32_t* token, uint32_t* status_word, void* stream);
 
 /* Append of new tokens' rows to the pool the verify calls read, with the
  * position rotation applied on the way, and the same rotation of the queries.

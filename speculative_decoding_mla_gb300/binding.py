@@ -27,11 +27,13 @@ VMLA_ERR_TIMEOUT = -6
 VMLA_ERR_INDEX = -7
 VMLA_ERR_DEVICE = -8
 VMLA_ERR_PARENT = -9
+VMLA_ERR_PARAM = -10
 VMLA_KERNEL_TC = 0
 VMLA_KERNEL_SIMT = 1
 VMLA_SPLITS_LANES = -1  # splits value: the tensor-core planner takes its lane plan where it fits
 D_QK = 576
 D_V = 512
+MAX_VOCAB = 262144
 
 EXPORTS = (
     "verify_attn_mla_plan", "verify_attn_mla_workspace_size", "verify_attn_mla", "verify_attn_mla_simt",
@@ -44,6 +46,7 @@ EXPORTS = (
     "verify_attn_mla_simt_static_check", "verify_attn_mla_defrag_append",
     "verify_attn_mla_runs_device_plan_workspace_size", "verify_attn_mla_runs_device_plan",
     "verify_attn_mla_append", "verify_attn_mla_shared", "verify_attn_mla_shared_workspace_size",
+    "verify_attn_mla_sample",
 )
 
 
@@ -95,6 +98,7 @@ def _load(path: str = LIB_PATH):
         "verify_attn_mla_shared": [vp, vp, i64, f32, vp, i64, vp, vp, vp, vp, vp, vp, vp, i32, i32, f32, i32, vp, vp, vp,
                                    sz, vp],
         "verify_attn_mla_shared_workspace_size": [i32, i32, i64, vp, vp, i32, ctypes.POINTER(sz)],
+        "verify_attn_mla_sample": [vp, i32, i64, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp],
         "verify_attn_mla_runs": run,
         "verify_attn_mla_runs_workspace_size": [i32, i32, vp, vp, i32, ctypes.POINTER(sz)],
         "verify_attn_mla_test_fault": [i32, i64],
@@ -461,6 +465,41 @@ def prepare_verify_attn_mla_shared(*a, **k) -> Prepared:
     """verify_attn_mla_shared with its arguments checked and marshalled once."""
     args, keep = _shared_args(*a, **k)
     return Prepared(_lib.verify_attn_mla_shared, "verify_attn_mla_shared", args, keep)
+
+
+def _sample_args(logits, uniform, token, temperature=None, top_k=None, top_p=None, min_p=None, status_word=None,
+                 stream=None):
+    R, V = (int(n) for n in logits.shape) if len(logits.shape) == 2 else (None, None)
+    if R is None:
+        raise ValueError(f"logits: two dimensions expected, got {tuple(logits.shape)}")
+    size = 0 if isinstance(logits, np.ndarray) else logits.element_size()
+    if size not in (2, 4) or not str(logits.dtype).endswith(("bfloat16", "float32")):
+        raise ValueError(f"logits: device memory of bfloat16 or float32 expected, got {logits.dtype}")
+    for t, name in ((uniform, "uniform"), (token, "token"), (temperature, "temperature"), (top_k, "top_k"),
+                    (top_p, "top_p"), (min_p, "min_p")):
+        if t is not None:
+            _shape(t, name, (R,))
+    if status_word is not None and status_word.numel() < 2:
+        raise ValueError("status_word: two words expected")
+    _same_device(logits=logits, uniform=uniform, token=token, temperature=temperature, top_k=top_k, top_p=top_p,
+                 min_p=min_p, status_word=status_word)
+    args = (_rows(logits, size, "logits", (R, V)), int(size == 4), _step(logits, 0, V), R, V,
+            _d(temperature, 4, "temperature"), _d(top_k, 4, "top_k"), _d(top_p, 4, "top_p"), _d(min_p, 4, "min_p"),
+            _d(uniform, 4, "uniform"), _d(token, 4, "token"), _d(status_word, 4, "status_word"), _stream(stream))
+    return args, (logits, uniform, token, temperature, top_k, top_p, min_p, status_word)
+
+
+def verify_attn_mla_sample(*a, **k):
+    """Draws one token per row of logits ([rows, vocab] bf16 or fp32, rows may be strided) into `token` [rows] int32
+    with the random numbers `uniform` [rows]; temperature, top_k, top_p and min_p are per-row arrays or None."""
+    args, _ = _sample_args(*a, **k)
+    _check(_lib.verify_attn_mla_sample(*args), "verify_attn_mla_sample")
+
+
+def prepare_verify_attn_mla_sample(*a, **k) -> Prepared:
+    """verify_attn_mla_sample with its arguments checked and marshalled once."""
+    args, keep = _sample_args(*a, **k)
+    return Prepared(_lib.verify_attn_mla_sample, "verify_attn_mla_sample", args, keep)
 
 
 def verify_attn_mla_runs_workspace_size(qo_indptr_host, kv_indptr_host, num_heads: int, splits: int = 0) -> int:

@@ -822,6 +822,34 @@ int verify_attn_mla_shared(const void* q, const void* kv_pool, int64_t pool_slot
   return launch_merge_shared(plan, a.part_o, a.part_lse, a.out, a.lse, stream);
 }
 
+int verify_attn_mla_sample(const void* logits, int logits_fp32, int64_t row_stride, int64_t rows, int vocab,
+                           const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                           const float* uniform, int32_t* token, uint32_t* status_word, void* stream) {
+  if (rows < 0 || rows > INT32_MAX / 8 || vocab < 1 || vocab > VMLA_MAX_VOCAB) return VMLA_ERR_SHAPE;
+  if (rows == 0) return VMLA_OK;
+  if (!logits || !uniform || !token) return VMLA_ERR_NULL;
+  if (row_stride < vocab || row_stride > ((int64_t)1 << 31)) return VMLA_ERR_SHAPE;
+  if (!aligned(logits, logits_fp32 ? 4 : 2) || !aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) ||
+      !aligned(min_p, 4) || !aligned(uniform, 4) || !aligned(token, 4) || !aligned(status_word, 4))
+    return VMLA_ERR_ALIGN;
+  int sms = 0;
+  int rc = current_sm_count(&sms, true);
+  if (rc != VMLA_OK) return rc;
+  SampleArgs a;
+  a.logits = logits;
+  a.stride = row_stride;
+  a.rows = rows;
+  a.vocab = vocab;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.uniform = uniform;
+  a.token = token;
+  a.status = status_word;
+  return launch_sample(a, logits_fp32 != 0, stream);
+}
+
 int verify_attn_mla_append(const void* latent, int64_t latent_stride, const void* k_rope, int64_t k_rope_stride,
                            const void* q_rope, int64_t q_rope_stride_t, int64_t q_rope_stride_h,
                            const int32_t* positions, const int32_t* slots, const float* cos_sin, int64_t table_rows,
@@ -935,6 +963,7 @@ const char* verify_attn_mla_status_string(int status) {
     case VMLA_ERR_INDEX: return "a kv slot index was outside the pool";
     case VMLA_ERR_DEVICE: return "no usable sm_103 device";
     case VMLA_ERR_PARENT: return "a draft parent index was malformed";
+    case VMLA_ERR_PARAM: return "a sampling setting was out of range";
     default: return "unknown status";
   }
 }

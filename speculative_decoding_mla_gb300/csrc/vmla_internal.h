@@ -252,6 +252,23 @@ struct AppendArgs {
 };
 int launch_append(const AppendArgs& args, void* stream);
 
+// Sampling (verify_attn_mla_sample).
+constexpr float kSampleMinTemp = 1.f / (1 << 20), kSampleMaxTemp = 1 << 20;
+struct SampleArgs {
+  const void* logits;  // [rows, vocab] bf16 or fp32, row stride in elements
+  int64_t stride;
+  int64_t rows;
+  int32_t vocab;
+  const float* temperature;  // per row; NULL: 1
+  const int32_t* top_k;      // NULL: off
+  const float* top_p;
+  const float* min_p;
+  const float* uniform;
+  int32_t* token;
+  uint32_t* status;
+};
+int launch_sample(const SampleArgs& args, bool fp32, void* stream);
+
 int launch_simt(const PlanParams& plan, const RunArgs& args, void* stream);
 int launch_tc(const PlanParams& plan, const RunArgs& args, void* stream);
 int launch_gather(const RunArgs& args, void* stream);
