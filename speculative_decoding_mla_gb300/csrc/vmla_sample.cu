@@ -17,18 +17,22 @@
 // units of 2^-45; integer sums are exact in any order.  Weights below 2^-46 of
 // the largest count as zero.
 //
-// One cluster of one to eight CTAs takes one row and keeps it in shared memory,
-// so the logits are read from memory once; a thread only ever reads back its own
-// elements until the last step.  Where a filter needs the order, the cut is
-// found without sorting:
-//   1. a histogram of counts over 44.5 buckets per factor of two in weight;
-//      counts give top-k's bucket, and bounds of each bucket's mass bracket the
-//      bucket of top-p's cut;
-//   2. for top-p, one pass that adds the exact masses of all tokens and of those
-//      above the bracket;
-//   3. inside the bracket, histograms over 1024 equal ranges of the values' bit
-//      patterns in their order (count, and exact mass for top-p), each narrowing the range to one
-//      bucket, down to one value: one or two rounds, over the few tokens left.
+// One cluster of one to eight CTAs takes one row.  With few rows a row is kept in
+// shared memory; with many, its later passes read it again, from L2, which lets
+// more rows be in work at once.  Where a filter needs the order, the cut is
+// found without sorting, from a histogram of counts over the leading 16 bits of
+// the values (bin_of): one shared-memory atomic per token.
+//   bf16: a bin holds one value (but for the bin of the values next to zero), so
+//      the masses are counts times exact weights of some thousand values, and the
+//      histogram alone gives both cuts exactly;
+//   fp32: counts give top-k's bin, bounds of each bin's mass bracket top-p's; one
+//      pass adds the exact masses of all tokens and of those above the bracket;
+//      inside a bin or bracket, histograms over 1024 equal ranges of the values'
+//      bit patterns in their order (count, and exact mass for top-p) narrow it
+//      down to one value: one to three rounds, over the few tokens left.
+// The draw first sums weights in single precision with a known error (about_of);
+// only where the random number falls so near a running sum that this could decide
+// it, the sums are taken again exactly.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -46,15 +50,17 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kChunkBytes = kThreads * 16;   // shared memory per iteration: 16 bytes per thread
-constexpr int kMaxIters = 17;                // 8 x 17 x 2048 floats hold VMLA_MAX_VOCAB and a misaligned start
-constexpr int kRoomyIters = 8;               // 64 KB: three CTAs per SM
-constexpr int kBuckets = 2048;               // of the weight histogram; the last one holds what counts as zero
+constexpr int kMaxIters = 17;                // kept rows: 8 x 17 x 2048 floats hold VMLA_MAX_VOCAB and a misaligned start
+constexpr int kMaxElems = 264;               // re-read rows: logits of one thread
+constexpr int kMaxChunks = kMaxElems / 4;    // iterations of one warp in either case
 constexpr float kOctaves = 46.f;             // weights below 2^-kOctaves count as zero
+constexpr int kNearZero = 0x3A80;            // leading 16 bits of 2^-10: smaller values share one bin
+constexpr int kBins = 18 * kThreads;         // 9216: see bin_of
 constexpr int kRanges = 1024;                // of the bit-pattern histograms
 constexpr int kUnitBits = 45;                // weights in units of 2^-45: 2^18 tokens' sum stays below 2^63
 static_assert((int64_t)VMLA_MAX_VOCAB << kUnitBits <= INT64_MAX, "sums of weights fit 63 bits");
 static_assert((int64_t)kMaxCluster * kMaxIters * (kChunkBytes / 4) >= VMLA_MAX_VOCAB + 3, "every vocabulary fits");
-static_assert((1 << 23) / 1 * 1ll * kMaxIters * 8 < (1ll << 31), "a thread's sum of high parts fits 32 bits");
+static_assert((int64_t)kMaxElems << 23 < (1ll << 32) && kMaxIters * 8 <= kMaxElems, "a thread's sum of high parts fits 32 bits");
 
 // 2^(k/64) as a pair of floats, filled by the host.
 struct ExpTable {
@@ -63,7 +69,7 @@ struct ExpTable {
 
 struct Shared {
   union {
-    uint32_t hist[kBuckets];
+    uint32_t hist[kBins];
     struct {
       uint32_t count[kRanges], mass_lo[kRanges], mass_hi[kRanges];
     } r;
@@ -72,21 +78,24 @@ struct Shared {
   uint64_t warp_u64[kWarps], warp_u64b[kWarps];
   uint32_t warp_u32[kWarps];
   float warp_f[kWarps], warp_g[kWarps];
-  // x_max, the sums, keys, count and index are read by the other CTAs of the cluster; each is written once per phase, with a cluster barrier
-  // between a phase's reads and its slot's next write
-  float x_max;
-  float exp_hi, exp_lo;    // log2(e) / temperature (written and read within the CTA)
+  float exp_hi, exp_lo;    // log2(e) / temperature
   double min_p_offset;     // temperature x ln(min_p)
-  uint64_t sum_a, sum_b;
-  uint32_t key_lo, key_hi, count;
+  // read by the other CTAs of the cluster; a cluster barrier lies between a phase's reads and the
+  // slot's next write
+  float x_max;
+  uint64_t sum_a, sum_b, tiny;
+  float sum_lo, sum_hi;
+  uint32_t key_lo, key_hi, count, bin_count;
   int32_t index;
+  // written by the one thread of the cluster that finds them, into every CTA
+  int32_t bin_k, bin_p, bracket_lo, bracket_hi, sure;
+  uint32_t bin_k_rank, bin_k_count, bin_p_count;
+  uint64_t bin_p_left;
   // results of a search, the same in every CTA
-  int32_t bucket_k, bucket_first, bucket_last;
-  uint32_t before_k;
   int32_t range;
-  uint32_t range_before, range_count;
-  uint64_t range_mass_before;
-  uint64_t chunk[kMaxIters];
+  uint32_t range_count;
+  uint64_t range_before;
+  uint64_t chunk[kMaxChunks];
 };
 
 // Whole numbers in the order of the values, without the low bits that a type's values never use.
@@ -100,6 +109,23 @@ __device__ __forceinline__ float order_value(uint32_t key) {
   const uint32_t k = key << kLowBits;
   return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~(k | ((1u << kLowBits) - 1u)));
 }
+
+// Signed number of a value's leading 16 bits, not decreasing in the value: 0 next to zero, then one
+// step per pattern.  The bin of a value is the number of the row's maximum less its own.  A weight of at
+// least 2^-46 means a value within 46 ln 2 T < 2^25 of the maximum, T being at most 2^20, and that
+// window holds at most 2 (25 + 10) 128 + 1 numbers (when zero is in its middle), so bins from
+// kBins - 1 on hold only what counts as zero.
+__device__ __forceinline__ int number_of(float x) {
+  const uint32_t b = __float_as_uint(x);
+  const int n = max((int)((b & 0x7FFFFFFFu) >> 16) - (kNearZero - 1), 0);
+  return (int)b < 0 ? -n : n;
+}
+// The value of a bf16's number other than 0, and the smallest magnitude of an fp32 with it.
+__device__ __forceinline__ float number_value(int n) {
+  const uint32_t b = (uint32_t)((n < 0 ? -n : n) + (kNearZero - 1)) << 16;
+  return __uint_as_float(n < 0 ? b | 0x80000000u : b);
+}
+static_assert(2 * (25 + 10) * 128 + 1 < kBins - 1, "every token of weight has a bin");
 
 // log2(e) / temperature in two floats, and the row's maximum.
 struct Exponent {
@@ -156,6 +182,37 @@ __device__ __forceinline__ uint64_t weight_units(float x, const Exponent& e, con
   return units(h, l);
 }
 
+// The weight in single precision, times a factor that all of a row's weights share: 2^(x c + bias),
+// bias being -max c (below 2^15) rounded to a multiple of 2^-7, which keeps bias - n exact.  The exponent is
+// split into a whole number n and f, |f| <= 1, whose error is below 2^-24; ex2 on it is good to 2^-22,
+// sums of eight in a tree to 3 x 2^-24 and their running sum in two floats to less: together below
+// 2^-20.5 of the weights summed.  A running sum C and the total W then place u W - C within
+// 2 u (1 - u) 2^-20.5 W <= 2^-21.5 W of its value.  For x c + bias > -100 only.
+struct About {
+  float hi, lo, bias, magic;
+};
+constexpr float kAboutMax = 32768.f;  // of |max c|
+constexpr int kSureBits = 21;  // a border nearer than W 2^-21 to u W is not decided by these sums
+
+__device__ __forceinline__ About about(const Exponent& e) {
+  About a;
+  a.hi = e.hi;
+  a.lo = e.lo;
+  a.bias = __fsub_rn(__fadd_rn(-e.max * e.hi, 98304.f), 98304.f);  // in [2^16, 2^17) floats are 2^-7 apart
+  a.magic = __fadd_rn(12582912.f, a.bias);  // 1.5 x 2^23 + bias: whole
+  return a;
+}
+__device__ __forceinline__ float about_of(float x, const About& a) {
+  const float t = __fmaf_rn(x, a.hi, a.magic);
+  const float n = __fsub_rn(t, 12582912.f);
+  const float f = __fmaf_rn(x, a.lo, __fmaf_rn(x, a.hi, __fsub_rn(a.bias, n)));
+  return __uint_as_float(__float_as_uint(ex2_approx(f)) + (__float_as_uint(t) << 23));
+}
+// A float's value (below 2^19) in units of 2^-45.
+__device__ __forceinline__ uint64_t about_units(float hi, float lo) {
+  return (uint64_t)(hi * 35184372088832.f) + (uint64_t)(int64_t)(lo * 35184372088832.f);
+}
+
 template <typename V>
 __device__ __forceinline__ V warp_add(V v) {
 #pragma unroll
@@ -206,6 +263,17 @@ struct Elems<float> {
   static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[4]) {
     x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
   }
+  typedef float Max;
+  static __device__ __forceinline__ Max lowest() { return -INFINITY; }
+  static __device__ __forceinline__ float largest(Max m) { return m; }
+  // The granule with NaN made -inf, and its values taken into the running maximum.
+  static __device__ __forceinline__ uint4 settle(const uint4& v, Max& m) {
+    float x[4];
+    unpack(v, x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m = fmaxf(m, x[k] = fmaxf(x[k], -INFINITY));
+    return pack(x);
+  }
   static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
     return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
   }
@@ -220,6 +288,19 @@ struct Elems<uint16_t> {  // bf16
 #pragma unroll
     for (int k = 0; k < 4; ++k) x[2 * k] = bf16_lo(w[k]), x[2 * k + 1] = bf16_hi(w[k]);
   }
+  typedef uint32_t Max;  // two bf16 maxima
+  static __device__ __forceinline__ Max lowest() { return 0xFF80FF80u; }
+  static __device__ __forceinline__ float largest(Max m) { return fmaxf(bf16_lo(m), bf16_hi(m)); }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // of a NaN and a number: the number
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ uint4 settle(const uint4& v, Max& m) {
+    const uint4 r = make_uint4(max2(v.x, lowest()), max2(v.y, lowest()), max2(v.z, lowest()), max2(v.w, lowest()));
+    m = max2(m, max2(max2(r.x, r.y), max2(r.z, r.w)));
+    return r;
+  }
   static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {  // of bf16 values: exact
     return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                       pack_bf16x2(x[6], x[7]));
@@ -228,9 +309,9 @@ struct Elems<uint16_t> {  // bf16
 
 // One row on one cluster.  Element v of the "shifted" row is token v - shift, shift being the
 // elements between the row's start and the 16-byte boundary below it, so that whole granules load
-// as vectors whatever the row's alignment; places outside the row read as -inf.  CTA r holds
+// as vectors whatever the row's alignment; places outside the row read as -inf.  CTA r takes
 // places [r S, (r + 1) S), its warp w the w-th of kWarps equal runs of them.
-template <typename T>
+template <typename T, bool kKeep>
 __global__ void __launch_bounds__(kThreads, 2)
 sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, int iters) {
   using E = Elems<T>;
@@ -248,7 +329,36 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
   const int end = a.vocab + shift;  // places [shift, end) are tokens
   const int seg = iters * kStep;    // a warp's places
   const int first = (rank * kWarps + warp) * seg;
-  uint4* mine = reinterpret_cast<uint4*>(slice_raw) + (size_t)warp * iters * 32 + lane;  // granule of iteration i: mine[32 i]
+  uint4* slice = reinterpret_cast<uint4*>(slice_raw) + lane;  // granule of warp w, iteration i: slice[32 (w iters + i)]
+  bool only_inf = false;  // the row has tokens at +inf: those count as 0, all others as -inf
+  // the granule at place p as it lies in memory
+  auto granule = [&](int p) {
+    uint4 v;
+    if (p >= shift && p + kVec <= end) {
+      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                   : "l"(base + p));
+    } else {
+      float x[kVec];
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) x[k] = p + k >= shift && p + k < end ? E::one(base + p + k) : -INFINITY;
+      v = E::pack(x);
+    }
+    return v;
+  };
+  // the logits of warp w's iteration i that fall to this lane, NaN made -inf
+  auto fetch = [&](int w, int i) {
+    if (kKeep) return slice[32 * (w * iters + i)];
+    return granule((rank * kWarps + w) * seg + i * kStep + lane * kVec);
+  };
+  auto values = [&](const uint4& v, float (&x)[kVec]) {
+    E::unpack(v, x);
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+      if (!kKeep) x[k] = fmaxf(x[k], -INFINITY);
+      if (only_inf) x[k] = x[k] == INFINITY ? 0.f : -INFINITY;
+    }
+  };
 
   // settings; a row with a bad one draws nothing
   const float temp = a.temperature ? __ldg(a.temperature + row) : 1.f;
@@ -273,41 +383,23 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     sm.exp_lo = (float)(c - (double)sm.exp_hi);
     sm.min_p_offset = min_p > 0.f && min_p < 1.f ? (double)temp * log((double)min_p) : 0.0;
   }
-  // ---- the row into shared memory, and its maximum
-  float mx = -INFINITY;
+  // ---- the row's maximum
+  typename E::Max run = E::lowest();
   constexpr int kFlight = 4;
   for (int i0 = 0; i0 < iters; i0 += kFlight) {
     uint4 v[kFlight];
 #pragma unroll
-    for (int f = 0; f < kFlight; ++f) {
-      const int p = first + (i0 + f) * kStep + lane * kVec;
-      if (i0 + f < iters) {
-        if (p >= shift && p + kVec <= end) {
-          asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(v[f].x), "=r"(v[f].y), "=r"(v[f].z), "=r"(v[f].w)
-                       : "l"(base + p));
-        } else {
-          float x[kVec];
-#pragma unroll
-          for (int k = 0; k < kVec; ++k) x[k] = p + k >= shift && p + k < end ? E::one(base + p + k) : -INFINITY;
-          v[f] = E::pack(x);
-        }
-      }
-    }
+    for (int f = 0; f < kFlight; ++f)
+      if (i0 + f < iters) v[f] = granule(first + (i0 + f) * kStep + lane * kVec);
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
       if (i0 + f < iters) {
-        float x[kVec];
-        E::unpack(v[f], x);
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) {
-          x[k] = fmaxf(x[k], -INFINITY);  // NaN counts as -inf
-          mx = fmaxf(mx, x[k]);
-        }
-        mine[32 * (i0 + f)] = E::pack(x);
+        const uint4 x = E::settle(v[f], run);  // NaN counts as -inf
+        if (kKeep) slice[32 * (warp * iters + i0 + f)] = x;
       }
     }
   }
+  float mx = E::largest(run);
   if (tid < 64) sm.table[tid] = exp_table.t[tid];
   mx = warp_max(mx);
   if (lane == 0) sm.warp_f[warp] = mx;
@@ -318,16 +410,29 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
   cluster.sync();
   for (int r = 0; r < C; ++r) mx = fmaxf(mx, *cluster.map_shared_rank(&sm.x_max, r));
 
-  // f(x, place) for every element of this thread
-  auto each = [&](auto&& f) {
+  // g(values, first place) for every granule of this thread, the next ones on their way
+  auto each_granule = [&](auto&& g) {
+    constexpr int kAhead = kKeep ? 1 : 3;
+    uint4 v[kAhead];
+#pragma unroll
+    for (int h = 0; h < kAhead; ++h)
+      if (h < iters) v[h] = fetch(warp, h);
 #pragma unroll 1
     for (int i = 0; i < iters; ++i) {
       float x[kVec];
-      E::unpack(mine[32 * i], x);
-      const int p = first + i * kStep + lane * kVec;
+      values(v[0], x);
+#pragma unroll
+      for (int h = 0; h + 1 < kAhead; ++h) v[h] = v[h + 1];
+      if (i + kAhead < iters) v[kAhead - 1] = fetch(warp, i + kAhead);
+      g(x, first + i * kStep + lane * kVec);
+    }
+  };
+  // f(x, place) for every element of this thread
+  auto each = [&](auto&& f) {
+    each_granule([&](const float (&x)[kVec], int p) {
 #pragma unroll
       for (int k = 0; k < kVec; ++k) f(x[k], p + k);
-    }
+    });
   };
 
   if (temp == 0.f || mx == -INFINITY) {
@@ -349,110 +454,76 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     cluster.sync();
     return;
   }
-  if (mx == INFINITY) {
-    // tokens at +inf share the draw evenly: they become 0, all others -inf
-#pragma unroll 1
-    for (int i = 0; i < iters; ++i) {
-      float x[kVec];
-      E::unpack(mine[32 * i], x);
-#pragma unroll
-      for (int k = 0; k < kVec; ++k) x[k] = x[k] == INFINITY ? 0.f : -INFINITY;
-      mine[32 * i] = E::pack(x);
-    }
+  if (mx == INFINITY) {  // tokens at +inf share the draw evenly
+    only_inf = true;
     mx = 0.f;
   }
   const Exponent ex = {mx, sm.exp_hi, sm.exp_lo};
-  const float per_octave = (kBuckets - 2) / kOctaves;
-  const float to_bucket = ex.hi * per_octave;
-  auto bucket_of = [&](float x) {  // non-increasing in x; kBuckets - 1: counts as zero
-    const float b = (mx - x) * to_bucket;
-    return b < (float)(kBuckets - 1) ? (int)b : kBuckets - 1;
+  auto to_all = [&](auto member, auto value) {  // into every CTA's copy of a result
+    for (int r = 0; r < C; ++r) cluster.map_shared_rank(&sm, r)->*member = value;
   };
 
   // ---- what is kept: x > cut_x, and x == cut_x up to place cut_place
   float cut_x = -INFINITY;
-  int cut_place = INT32_MAX;
   uint32_t cut_keep = 0, cut_equal = 0;  // of the tokens equal to cut_x, the first cut_keep of cut_equal
   bool with_k = top_k > 0 && top_k < a.vocab;
-  bool with_p = top_p < 1.f;
+  const bool with_p = top_p < 1.f;
   if (with_k || with_p) {
-    for (int b = tid; b < kBuckets; b += kThreads) sm.hist[b] = 0;
+    const int top_number = number_of(mx);
+    // tokens of weight lie above
+    const float x_low = fminf(mx, fmaxf(mx - kOctaves * 0.6931472f * temp * 1.0001f, -3.402823466e38f));
+    // the bins in use; every CTA sums up an equal run of them
+    const int bins = min(kBins - 1, top_number - number_of(x_low) + 1);
+    const int per = (bins + C * kThreads - 1) / (C * kThreads);  // consecutive bins of one thread
+    const int bin0 = (rank * kThreads + tid) * per;
+    const int tiny_bin = top_number;  // of number 0, where it is in use (0 <= top_number < bins)
+    for (int b = tid; b < bins; b += kThreads) sm.hist[b] = 0;
     __syncthreads();
+    uint64_t tiny = 0;  // exact mass of the values that share the bin next to zero
     each([&](float x, int) {
-      const int b = bucket_of(x);
-      if (b < kBuckets - 1) atomicAdd(&sm.hist[b], 1u);
+      const int n = number_of(x), b = top_number - n;
+      if (b < bins) {
+        atomicAdd(&sm.hist[b], 1u);
+        if (E::kLowBits && with_p && n == 0) tiny += weight_units(x, ex, sm.table);
+      }
     });
-    if (tid == 0) sm.bucket_k = -1, sm.bucket_first = sm.bucket_last = kBuckets - 1;
+    if (E::kLowBits && with_p) {
+      tiny = warp_add(tiny);
+      if (lane == 0) sm.warp_u64[warp] = tiny;
+      __syncthreads();
+      if (tid == 0) {
+        tiny = 0;
+        for (int w = 0; w < kWarps; ++w) tiny += sm.warp_u64[w];
+        sm.tiny = tiny;
+      }
+    }
     cluster.sync();
-    constexpr int kOwn = kBuckets / kThreads;
-    uint32_t n[kOwn], mine_n = 0;
-#pragma unroll
-    for (int j = 0; j < kOwn; ++j) {
-      n[j] = 0;
-      for (int r = 0; r < C; ++r) n[j] += cluster.map_shared_rank(sm.hist, r)[kOwn * tid + j];
-      mine_n += n[j];
+    // this thread's bins, summed over the CTAs (into this CTA's copy: no other CTA reads these bins
+    // of it), and the tokens ahead of them
+    uint32_t before = 0;
+    for (int j = 0; j < per && bin0 + j < bins; ++j) {
+      uint32_t n = 0;
+      for (int r = 0; r < C; ++r) n += cluster.map_shared_rank(sm.hist, r)[bin0 + j];
+      sm.hist[bin0 + j] = n;
+      before += n;
     }
     uint32_t total;
-    uint32_t before = block_scan(mine_n, sm.warp_u32, &total);
+    before = block_scan(before, sm.warp_u32, &total);
+    if (tid == 0) sm.bin_count = total;
+    cluster.sync();
+    total = 0;
+    for (int r = 0; r < C; ++r) {
+      const uint32_t n = *cluster.map_shared_rank(&sm.bin_count, r);
+      if (r < rank) before += n;
+      total += n;
+    }
     if (with_k && (uint32_t)top_k >= total) with_k = false;  // nothing of weight is past the k-th
-    if (with_k) {
-      uint32_t at = before;
-#pragma unroll
-      for (int j = 0; j < kOwn; ++j) {
-        if (at < (uint32_t)top_k && at + n[j] >= (uint32_t)top_k) sm.bucket_k = kOwn * tid + j, sm.before_k = at;
-        at += n[j];
-      }
-    }
-    if (with_p) {
-      // bounds of the mass up to each bucket, of what top-k leaves; 10^-3 covers the rounding of
-      // bounds, sums and bucket borders
-      float lo[kOwn], hi[kOwn], sum_lo = 0.f, sum_hi = 0.f;
-      uint32_t at = before;
-#pragma unroll
-      for (int j = 0; j < kOwn; ++j) {
-        const uint32_t left = with_k ? (at < (uint32_t)top_k ? (uint32_t)top_k - at : 0u) : UINT32_MAX;
-        const float m = (float)(n[j] < left ? n[j] : left);
-        const float b = (float)(kOwn * tid + j);
-        lo[j] = m * ex2_approx(-(b + 1.f) / per_octave) * 0.999f;
-        hi[j] = m * ex2_approx(-b / per_octave) * 1.001f;
-        sum_lo += lo[j];
-        sum_hi += hi[j];
-        at += n[j];
-      }
-      float all_lo, all_hi;
-      float cum_lo = block_scan(sum_lo, sm.warp_f, &all_lo), cum_hi = block_scan(sum_hi, sm.warp_g, &all_hi);
-#pragma unroll
-      for (int j = 0; j < kOwn; ++j) {
-        cum_lo += lo[j];
-        cum_hi += hi[j];
-        if (cum_hi >= top_p * all_lo * 0.999f) atomicMin(&sm.bucket_first, kOwn * tid + j);
-        if (cum_lo >= top_p * all_hi * 1.001f) atomicMin(&sm.bucket_last, kOwn * tid + j);
-      }
-    }
-    __syncthreads();
-    cluster.sync();  // the histograms have been read
 
-    // The value at which a running count (or mass) over the tokens with bucket in [b_lo, b_hi] and
-    // pattern at or above `floor_key`, in descending order, reaches `target`: its pattern, the
-    // count and mass before it, and how many tokens have it.
-    auto refine = [&](int b_lo, int b_hi, uint32_t floor_key, bool by_mass, uint64_t target, uint32_t* key,
-                      uint32_t* equal, uint64_t* left) {
-      uint32_t klo = UINT32_MAX, khi = 0;
-      each([&](float x, int) {
-        const int b = bucket_of(x);
-        const uint32_t k = order_key<E::kLowBits>(x);
-        if (b >= b_lo && b <= b_hi && b < kBuckets - 1 && k >= floor_key) klo = min(klo, k), khi = max(khi, k);
-      });
-      klo = __reduce_min_sync(0xffffffffu, klo);
-      khi = __reduce_max_sync(0xffffffffu, khi);
-      if (tid == 0) sm.key_lo = UINT32_MAX, sm.key_hi = 0;
-      __syncthreads();
-      if (lane == 0) atomicMin(&sm.key_lo, klo), atomicMax(&sm.key_hi, khi);
-      cluster.sync();
-      for (int r = 0; r < C; ++r) {
-        klo = min(klo, *cluster.map_shared_rank(&sm.key_lo, r));
-        khi = max(khi, *cluster.map_shared_rank(&sm.key_hi, r));
-      }
+    // The value at which a running count (or mass) over the tokens with a key in [klo, khi], in
+    // descending order, reaches `target`: its key, how many tokens have it, and what is left of the
+    // target for them.
+    auto refine = [&](uint32_t klo, uint32_t khi, bool by_mass, uint64_t target, uint32_t* key, uint32_t* equal,
+                      uint64_t* left) {
       // (a round leaves 10 bits fewer: 32, 22, 12, 2)
       for (int round = 0; round < 4; ++round) {
         // ranges of equal width, a power of two
@@ -499,15 +570,14 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
           if (was < target && now >= target) {  // one range of one thread
             sm.range = kRanges - 1 - (kPer * tid + j);
             sm.range_count = n2[j];
-            sm.range_mass_before = was;
+            sm.range_before = was;
           }
         }
         __syncthreads();
-        target -= sm.range_mass_before;
-        const uint32_t lo2 = klo + ((uint32_t)sm.range << width);
-        const uint32_t hi2 = lo2 + ((1u << width) - 1u);
+        target -= sm.range_before;
         *equal = sm.range_count;
-        klo = lo2;
+        klo += (uint32_t)sm.range << width;
+        const uint32_t hi2 = klo + ((1u << width) - 1u);
         khi = hi2 < khi ? hi2 : khi;
         cluster.sync();  // the histograms have been read
         if (width == 0) break;
@@ -515,53 +585,170 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
       *key = klo;
       *left = target;
     };
-
-    uint32_t floor_key = 0;
+    // Keys of the values in bins [b_first, b_last].
+    auto bin_keys = [&](int b_first, int b_last, uint32_t* klo, uint32_t* khi) {
+      constexpr int kL = E::kLowBits;
+      const uint32_t rest = (1u << (16 - kL)) - 1u;  // an fp32's patterns of one number
+      const int n_hi = top_number - b_first, n_lo = top_number - b_last;
+      // numbers above 0 start at their own value's key, those below end at it
+      const uint32_t zero = order_key<kL>(0.f), near = ((uint32_t)kNearZero << (16 - kL)) - 1u;
+      *khi = n_hi > 0 ? order_key<kL>(number_value(n_hi)) + rest
+                      : n_hi == 0 ? zero + near : order_key<kL>(number_value(n_hi));
+      *klo = n_lo > 0 ? order_key<kL>(number_value(n_lo))
+                      : n_lo == 0 ? zero - 1u - near : order_key<kL>(number_value(n_lo)) - rest;
+    };
     if (with_k) {
-      uint64_t left;
-      refine(sm.bucket_k, sm.bucket_k, 0, false, (uint64_t)top_k - sm.before_k, &floor_key, &cut_equal, &left);
-      cut_x = order_value<E::kLowBits>(floor_key);
-      cut_keep = (uint32_t)left;
-    }
-    if (with_p) {
-      // exact masses of what top-k leaves: all of it, and the part above the bracket
-      const int b_lo = sm.bucket_first, b_hi = sm.bucket_last;
-      uint32_t all_h = 0, top_h = 0;
-      int32_t all_l = 0, top_l = 0;
-      each([&](float x, int) {
-        if (x > cut_x) {
-          int32_t h, l;
-          weight_of(x, ex, sm.table, &h, &l);
-          all_h += h, all_l += l;
-          if (bucket_of(x) < b_lo) top_h += h, top_l += l;
+      uint32_t at = before;
+      for (int j = 0; j < per && bin0 + j < bins; ++j) {
+        const uint32_t n = sm.hist[bin0 + j];
+        if (at < (uint32_t)top_k && at + n >= (uint32_t)top_k) {  // one bin of the cluster
+          to_all(&Shared::bin_k, bin0 + j);
+          to_all(&Shared::bin_k_rank, (uint32_t)top_k - at);
+          to_all(&Shared::bin_k_count, n);
         }
-      });
-      uint64_t all = warp_add(units(all_h, all_l)), top = warp_add(units(top_h, top_l));
-      if (lane == 0) sm.warp_u64[warp] = all, sm.warp_u64b[warp] = top;
-      __syncthreads();
-      if (tid == 0) {
-        all = top = 0;
-        for (int w = 0; w < kWarps; ++w) all += sm.warp_u64[w], top += sm.warp_u64b[w];
-        sm.sum_a = all, sm.sum_b = top;
+        at += n;
       }
       cluster.sync();
-      all = with_k ? (uint64_t)cut_keep * weight_units(cut_x, ex, sm.table) : 0, top = 0;
-      for (int r = 0; r < C; ++r)
-        all += *cluster.map_shared_rank(&sm.sum_a, r), top += *cluster.map_shared_rank(&sm.sum_b, r);
-      // the least mass that reaches p of all: p has 24 bits, so p 2^64 is whole for p >= 2^-40
-      const uint64_t p64 = (uint64_t)(top_p * 18446744073709551616.f);
-      uint64_t target = __umul64hi(p64, all) + (p64 * all != 0 ? 1 : 0);
-      target = target > top ? target - top : 1;
-      uint32_t key, equal;
-      uint64_t left;
-      refine(b_lo, b_hi, floor_key, true, target, &key, &equal, &left);
-      const float x = order_value<E::kLowBits>(key);
-      const uint64_t w = weight_units(x, ex, sm.table);
-      uint32_t keep = w > 0 ? (uint32_t)min((left + w - 1) / w, (uint64_t)equal) : equal;
-      if (with_k && x == cut_x) {
-        cut_keep = min(cut_keep, keep);
-      } else {
-        cut_x = x, cut_keep = keep, cut_equal = equal;
+    }
+    // top-k leaves the bins up to bin_k, of that one the first k_rank tokens
+    const int bin_k = with_k ? sm.bin_k : bins - 1;
+    const uint32_t k_rank = with_k ? sm.bin_k_rank : UINT32_MAX;
+    const uint64_t p64 = (uint64_t)(top_p * 18446744073709551616.f);  // p 2^64: whole for p >= 2^-40
+    auto least_mass = [&](uint64_t all) {
+      return max((uint64_t)__umul64hi(p64, all) + (p64 * all != 0 ? 1 : 0), (uint64_t)1);
+    };
+
+    bool found = false;
+    if (E::kLowBits && !(with_k && bin_k == tiny_bin)) {
+      // bf16: bins are values
+      if (with_k) cut_x = number_value(top_number - bin_k), cut_keep = k_rank, cut_equal = sm.bin_k_count;
+      found = !with_p;
+      if (with_p) {
+        uint64_t all = 0, tiny_all = 0, own = 0, block;
+        for (int r = 0; r < C; ++r) tiny_all += *cluster.map_shared_rank(&sm.tiny, r);
+        auto bin_mass = [&](int b) -> uint64_t {
+          if (b == tiny_bin) return tiny_all;
+          const uint32_t n = b == bin_k ? min(sm.hist[b], k_rank) : sm.hist[b];
+          return n ? n * weight_units(number_value(top_number - b), ex, sm.table) : 0ull;
+        };
+        const int stop = min(bin0 + per, bin_k + 1);
+        for (int b = bin0; b < stop; ++b) own += bin_mass(b);
+        uint64_t ahead = block_scan(own, sm.warp_u64, &block);
+        if (tid == 0) sm.sum_a = block;
+        cluster.sync();
+        for (int r = 0; r < C; ++r) {
+          const uint64_t m = *cluster.map_shared_rank(&sm.sum_a, r);
+          if (r < rank) ahead += m;
+          all += m;
+        }
+        const uint64_t target = least_mass(all);
+        if (ahead < target && ahead + own >= target) {  // one thread of the cluster
+          for (int b = bin0; b < stop; ++b) {
+            const uint64_t m = bin_mass(b);
+            if (ahead + m >= target) {
+              to_all(&Shared::bin_p, b);
+              to_all(&Shared::bin_p_left, target - ahead);
+              to_all(&Shared::bin_p_count, sm.hist[b]);
+              break;
+            }
+            ahead += m;
+          }
+        }
+        cluster.sync();
+        if (sm.bin_p != tiny_bin) {
+          const float x = number_value(top_number - sm.bin_p);
+          const uint64_t w = weight_units(x, ex, sm.table);
+          const uint32_t keep = w > 0 ? (uint32_t)((sm.bin_p_left + w - 1) / w) : sm.bin_p_count;
+          if (!with_k || sm.bin_p != bin_k || keep < cut_keep) cut_x = x, cut_keep = keep, cut_equal = sm.bin_p_count;
+          found = true;
+        }
+      }
+    }
+    if (!found) {
+      int b_lo = 0, b_hi = bins - 1;
+      if (with_p) {
+        // bounds of the mass up to each bin, of what top-k leaves; 10^-3 covers the rounding of
+        // bounds and sums
+        auto bounds = [&](int b, float* lo, float* hi) {
+          uint32_t n = sm.hist[b];
+          if (b == bin_k) n = min(n, k_rank);
+          if (b > bin_k) n = 0;
+          const int v = top_number - b;
+          constexpr float kNear = 1.f / 1024;
+          const float x_hi = v > 0 ? number_value(v + 1) : v == 0 ? kNear : number_value(v);
+          const float x_lo = v > 0 ? number_value(v) : v == 0 ? -kNear : number_value(v - 1);
+          *lo = (float)n * ex2_approx((x_lo - mx) * ex.hi) * 0.999f;
+          *hi = (float)n * ex2_approx(fminf((x_hi - mx) * ex.hi, 0.f)) * 1.001f;
+        };
+        float own_lo = 0.f, own_hi = 0.f, lo, hi, all_lo, all_hi;
+        for (int b = bin0; b < bin0 + per && b < bins; ++b) bounds(b, &lo, &hi), own_lo += lo, own_hi += hi;
+        float cum_lo = block_scan(own_lo, sm.warp_f, &all_lo), cum_hi = block_scan(own_hi, sm.warp_g, &all_hi);
+        if (tid == 0) sm.sum_lo = all_lo, sm.sum_hi = all_hi, sm.bracket_lo = sm.bracket_hi = bins - 1;
+        cluster.sync();
+        all_lo = all_hi = 0.f;
+        for (int r = 0; r < C; ++r) {
+          const float l = *cluster.map_shared_rank(&sm.sum_lo, r), h = *cluster.map_shared_rank(&sm.sum_hi, r);
+          if (r < rank) cum_lo += l, cum_hi += h;
+          all_lo += l, all_hi += h;
+        }
+        for (int b = bin0; b < bin0 + per && b < bins; ++b) {
+          bounds(b, &lo, &hi);
+          cum_lo += lo, cum_hi += hi;
+          if (cum_hi >= top_p * all_lo * 0.999f) atomicMin(&sm.bracket_lo, b);
+          if (cum_lo >= top_p * all_hi * 1.001f) atomicMin(&sm.bracket_hi, b);
+        }
+        cluster.sync();
+        b_lo = b_hi = bins - 1;
+        for (int r = 0; r < C; ++r) {
+          b_lo = min(b_lo, *cluster.map_shared_rank(&sm.bracket_lo, r));
+          b_hi = min(b_hi, *cluster.map_shared_rank(&sm.bracket_hi, r));
+        }
+        b_hi = min(b_hi, bin_k);
+        b_lo = min(b_lo, b_hi);
+      }
+      cluster.sync();  // the histograms and brackets have been read
+      uint32_t floor_key = 0, klo, khi;
+      if (with_k) {
+        uint64_t left;
+        bin_keys(bin_k, bin_k, &klo, &khi);
+        refine(klo, khi, false, k_rank, &floor_key, &cut_equal, &left);
+        cut_x = order_value<E::kLowBits>(floor_key);
+        cut_keep = (uint32_t)left;
+      }
+      if (with_p) {
+        // exact masses of what top-k leaves: all of it, and the part above the bracket
+        bin_keys(b_lo, b_hi, &klo, &khi);
+        uint32_t all_h = 0, top_h = 0;
+        int32_t all_l = 0, top_l = 0;
+        each([&](float x, int) {
+          if (x > cut_x) {
+            int32_t h, l;
+            weight_of(x, ex, sm.table, &h, &l);
+            all_h += h, all_l += l;
+            if (order_key<E::kLowBits>(x) > khi) top_h += h, top_l += l;
+          }
+        });
+        uint64_t all = warp_add(units(all_h, all_l)), top = warp_add(units(top_h, top_l));
+        if (lane == 0) sm.warp_u64[warp] = all, sm.warp_u64b[warp] = top;
+        __syncthreads();
+        if (tid == 0) {
+          all = top = 0;
+          for (int w = 0; w < kWarps; ++w) all += sm.warp_u64[w], top += sm.warp_u64b[w];
+          sm.sum_a = all, sm.sum_b = top;
+        }
+        cluster.sync();
+        all = with_k ? (uint64_t)cut_keep * weight_units(cut_x, ex, sm.table) : 0, top = 0;
+        for (int r = 0; r < C; ++r)
+          all += *cluster.map_shared_rank(&sm.sum_a, r), top += *cluster.map_shared_rank(&sm.sum_b, r);
+        const uint64_t least = least_mass(all), target = least > top ? least - top : 1;
+        uint32_t key, equal;
+        uint64_t left;
+        refine(max(klo, floor_key), khi, true, target, &key, &equal, &left);
+        const float x = order_value<E::kLowBits>(key);
+        const uint64_t w = weight_units(x, ex, sm.table);
+        const uint32_t keep = w > 0 ? (uint32_t)min((left + w - 1) / w, (uint64_t)equal) : equal;
+        if (with_k && x == cut_x) cut_keep = min(cut_keep, keep);
+        else cut_x = x, cut_keep = keep, cut_equal = equal;
       }
     }
   }
@@ -570,11 +757,14 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     const float x = __double2float_ru((double)mx + sm.min_p_offset);
     if (x > cut_x) cut_x = x, cut_keep = cut_equal = 0;
   }
-  if (cut_keep < cut_equal) {
+  const bool some_equal = cut_keep < cut_equal;
+  int cut_place = INT32_MAX;
+  if (some_equal) {
     // the place of the cut_keep-th token equal to cut_x, in the order of the places
     uint32_t here = 0;
     each([&](float x, int) { here += x == cut_x ? 1u : 0u; });
     here = warp_add(here);
+    __syncthreads();
     if (lane == 0) sm.warp_u32[warp] = here;
     __syncthreads();
     uint32_t block = 0, skip = 0;
@@ -588,7 +778,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     if (skip < cut_keep && skip + here >= cut_keep) {  // one warp of the cluster
       for (int i = 0; i < iters; ++i) {
         float x[kVec];
-        E::unpack(mine[32 * i], x);
+        values(fetch(warp, i), x);
         uint32_t own = 0;
 #pragma unroll
         for (int k = 0; k < kVec; ++k) own += x[k] == cut_x ? 1u : 0u;
@@ -596,10 +786,8 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
         uint32_t at = skip + inc - own;
         if (at < cut_keep && at + own >= cut_keep) {
 #pragma unroll
-          for (int k = 0; k < kVec; ++k) {
-            if (x[k] == cut_x && ++at == cut_keep)
-              for (int r = 0; r < C; ++r) *cluster.map_shared_rank(&sm.index, r) = first + i * kStep + lane * kVec + k;
-          }
+          for (int k = 0; k < kVec; ++k)
+            if (x[k] == cut_x && ++at == cut_keep) to_all(&Shared::index, first + i * kStep + lane * kVec + k);
         }
         skip += __shfl_sync(0xffffffffu, inc, 31);
       }
@@ -608,86 +796,137 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     cut_place = sm.index;
   }
 
-  // ---- the draw, in the order of the places
-  auto kept_units = [&](float x, int p) {
-    return x > cut_x || (x == cut_x && p <= cut_place) ? weight_units(x, ex, sm.table) : 0ull;
+  // ---- the draw, in the order of the places.  With `exact` false in single precision: sm.sure tells
+  // whether that decides the token.
+  const About ab = about(ex);
+  const float x_zero = mx - kOctaves * 0.6931472f * temp;  // values below count as zero in the single-precision sums
+  auto kept = [&](float x, int p) { return x > cut_x || (x == cut_x && p <= cut_place); };
+  auto one = [&](float x, int p, bool exact) -> uint64_t {
+    if (!kept(x, p)) return 0;
+    return exact ? weight_units(x, ex, sm.table) : x >= x_zero ? about_units(about_of(x, ab), 0.f) : 0;
   };
-  uint32_t sum_h = 0;
-  int32_t sum_l = 0;
-  each([&](float x, int p) {
-    if (x > cut_x || (x == cut_x && p <= cut_place)) {
-      int32_t h, l;
-      weight_of(x, ex, sm.table, &h, &l);
-      sum_h += h, sum_l += l;
-    }
-  });
-  uint64_t sum = warp_add(units(sum_h, sum_l));
-  __syncthreads();
-  if (lane == 0) sm.warp_u64[warp] = sum;
-  __syncthreads();
-  uint64_t block = 0;
-  for (int w = 0; w < kWarps; ++w) block += sm.warp_u64[w];
-  if (tid == 0) sm.sum_a = block;
-  cluster.sync();
-  uint64_t all = 0, before = 0;
-  for (int r = 0; r < C; ++r) {
-    const uint64_t s = *cluster.map_shared_rank(&sm.sum_a, r);
-    if (r < rank) before += s;
-    all += s;
-  }
-  // the token's running sum is the first above `goal` = floor(u all)
-  const uint64_t goal = u < 1.f ? __umul64hi((uint64_t)(u * 18446744073709551616.f), all) : all - 1;
-  if (before <= goal && goal < before + block) {  // one CTA of the cluster
-    int w0 = 0;
-    while (w0 < kWarps - 1 && before + sm.warp_u64[w0] <= goal) before += sm.warp_u64[w0++];
-    // that warp's places, one iteration's per warp of this CTA
-    const uint4* theirs = reinterpret_cast<const uint4*>(slice_raw) + (size_t)w0 * iters * 32 + lane;
-    const int start = (rank * kWarps + w0) * seg + lane * kVec;
-    for (int i = warp; i < iters; i += kWarps) {
-      float x[kVec];
-      E::unpack(theirs[32 * i], x);
-      uint64_t s = 0;
-#pragma unroll 1
-      for (int k = 0; k < kVec; ++k) s += kept_units(x[k], start + i * kStep + k);
-      s = warp_add(s);
-      if (lane == 0) sm.chunk[i] = s;
-    }
-    __syncthreads();
-    if (warp == 0) {
-      int i = 0;
-      while (i < iters - 1 && before + sm.chunk[i] <= goal) before += sm.chunk[i++];
-      float x[kVec];
-      uint64_t s = 0, w[kVec];
-      E::unpack(theirs[32 * i], x);
-#pragma unroll
-      for (int k = 0; k < kVec; ++k) s += w[k] = kept_units(x[k], start + i * kStep + k);
-      uint64_t at = before + warp_scan(s, lane) - s;
-      if (at <= goal && goal < at + s) {
+  auto draw = [&](bool exact) {
+    uint64_t sum;
+    if (exact) {
+      uint32_t h = 0;
+      int32_t l = 0;
+      each([&](float x, int p) {
+        if (kept(x, p)) {
+          int32_t wh, wl;
+          weight_of(x, ex, sm.table, &wh, &wl);
+          h += wh, l += wl;
+        }
+      });
+      sum = units(h, l);
+    } else {
+      float s = 0.f, e = 0.f;  // the sum in two floats
+      const float least = fmaxf(cut_x, x_zero);
+      each_granule([&](const float (&x)[kVec], int p) {
+        float w[kVec];
 #pragma unroll
         for (int k = 0; k < kVec; ++k) {
-          if (at <= goal && goal < at + w[k]) a.token[row] = start + i * kStep + k - shift;
-          at += w[k];
+          bool in = x[k] >= least;
+          if (some_equal) in = in && (x[k] != cut_x || p + k <= cut_place);
+          w[k] = in ? about_of(x[k], ab) : 0.f;
+        }
+#pragma unroll
+        for (int o = kVec / 2; o > 0; o >>= 1)
+#pragma unroll
+          for (int k = 0; k < o; ++k) w[k] = __fadd_rn(w[k], w[k + o]);
+        const float t = __fadd_rn(s, w[0]), b = __fsub_rn(t, s);
+        e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(w[0], b)));
+        s = t;
+      });
+      sum = about_units(s, e);
+    }
+    sum = warp_add(sum);
+    __syncthreads();
+    if (lane == 0) sm.warp_u64[warp] = sum;
+    __syncthreads();
+    uint64_t block = 0;
+    for (int w = 0; w < kWarps; ++w) block += sm.warp_u64[w];
+    if (tid == 0) sm.sum_a = block;
+    cluster.sync();
+    uint64_t all = 0, before = 0;
+    for (int r = 0; r < C; ++r) {
+      const uint64_t s = *cluster.map_shared_rank(&sm.sum_a, r);
+      if (r < rank) before += s;
+      all += s;
+    }
+    // the token's running sum is the first above `goal` = floor(u all)
+    const uint64_t goal = u < 1.f ? __umul64hi((uint64_t)(u * 18446744073709551616.f), all) : all - 1;
+    if (before <= goal && goal < before + block) {  // one CTA of the cluster
+      int w0 = 0;
+      while (w0 < kWarps - 1 && before + sm.warp_u64[w0] <= goal) before += sm.warp_u64[w0++];
+      // that warp's places, one iteration's per warp of this CTA
+      const int start = (rank * kWarps + w0) * seg + lane * kVec;
+      for (int i = warp; i < iters; i += kWarps) {
+        float x[kVec];
+        values(fetch(w0, i), x);
+        uint64_t s = 0;
+#pragma unroll 1
+        for (int k = 0; k < kVec; ++k) s += one(x[k], start + i * kStep + k, exact);
+        s = warp_add(s);
+        if (lane == 0) sm.chunk[i] = s;
+      }
+      __syncthreads();
+      if (warp == 0) {
+        int i = 0;
+        while (i < iters - 1 && before + sm.chunk[i] <= goal) before += sm.chunk[i++];
+        float x[kVec];
+        uint64_t s = 0, w[kVec];
+        values(fetch(w0, i), x);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) s += w[k] = one(x[k], start + i * kStep + k, exact);
+        uint64_t at = before + warp_scan(s, lane) - s;
+        if (at <= goal && goal < at + s) {
+#pragma unroll
+          for (int k = 0; k < kVec; ++k) {
+            if (at <= goal && goal < at + w[k]) {
+              a.token[row] = start + i * kStep + k - shift;
+              const uint64_t margin = all >> kSureBits;
+              if (goal - at >= margin && at + w[k] - goal > margin) to_all(&Shared::sure, 1);
+            }
+            at += w[k];
+          }
         }
       }
     }
+    cluster.sync();  // sm.sure is settled, and no CTA leaves while another reads its shared memory
+  };
+  if (tid == 0) sm.sure = 0;
+  bool sure = false;
+  if (fabsf(mx * ex.hi) < kAboutMax) {
+    cluster.sync();  // sm.sure is cleared in every CTA
+    draw(false);
+    sure = sm.sure != 0;
   }
-  cluster.sync();  // no CTA leaves while another reads its shared memory
+  if (!sure) draw(true);
 }
 
-// CTAs per row: the smallest power of two whose slice leaves room for three CTAs on an SM (or the
-// largest cluster), then more while the rows leave SMs idle.
+// CTAs per row.  A row is kept in shared memory while that leaves no SM with more than one CTA's
+// work (measured: 1 x 32,000 bf16 TODO); rows beyond that are re-read.  Either way the cluster grows
+// while SMs would be idle, and as far as the limits on a CTA's share of a row ask.
+struct Shape {
+  int cluster, iters;
+  bool keep;
+};
 template <typename T>
-int choose_cluster(int64_t rows, int vocab, int sms, int* iters) {
-  const int64_t places = (int64_t)vocab + Elems<T>::kVec - 1;
+Shape choose_shape(const SampleArgs& a, int sms) {
+  const bool aligned = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && a.stride * sizeof(T) % 16 == 0;
+  const int64_t places = (int64_t)a.vocab + (aligned ? 0 : Elems<T>::kVec - 1);
   auto need = [&](int c) {
     const int64_t per = (int64_t)c * (kChunkBytes / sizeof(T));
     return (int)((places + per - 1) / per);
   };
-  int c = 1;
-  while (c < kMaxCluster && need(c) > kRoomyIters) c *= 2;
-  while (c < kMaxCluster && rows * c * 2 <= sms && need(c) > 1) c *= 2;
-  *iters = need(c);
-  return c;
+  Shape s;
+  s.cluster = 1;
+  while (s.cluster < kMaxCluster && a.rows * s.cluster * 2 <= 2 * sms && need(s.cluster) > 1) s.cluster *= 2;
+  s.keep = a.rows * s.cluster <= 2 * sms && need(s.cluster) <= 8;
+  const int most = s.keep ? kMaxIters : kMaxElems / Elems<T>::kVec;
+  while (s.cluster < kMaxCluster && need(s.cluster) > most) s.cluster *= 2;
+  s.iters = need(s.cluster);
+  return s;
 }
 
 template <typename T>
@@ -701,16 +940,18 @@ int launch(const SampleArgs& a, int sms, int dev, cudaStream_t stream) {
     }
     return t;
   }();
-  int iters = 0;
-  const int c = choose_cluster<T>(a.rows, a.vocab, sms, &iters);
-  if (iters > kMaxIters || a.rows * c > INT32_MAX) return VMLA_ERR_SHAPE;
-  {
+  const Shape shape = choose_shape<T>(a, sms);
+  if (shape.iters > (shape.keep ? kMaxIters : kMaxChunks) || a.rows * shape.cluster > INT32_MAX) return VMLA_ERR_SHAPE;
+  if (shape.keep) {
     static bool ready[64] = {};
     static std::mutex mu;
     std::lock_guard<std::mutex> g(mu);
     if (dev >= 64 || !ready[dev]) {
-      if (cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               kMaxIters * kChunkBytes) != cudaSuccess)
+      // (all of the SM's memory as shared memory: the default split left room for one CTA)
+      if (cudaFuncSetAttribute(sample_kernel<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kMaxIters * kChunkBytes) != cudaSuccess ||
+          cudaFuncSetAttribute(sample_kernel<T, true>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared) != cudaSuccess)
         return VMLA_ERR_CUDA;
       if (dev < 64) ready[dev] = true;
     }
@@ -718,15 +959,16 @@ int launch(const SampleArgs& a, int sms, int dev, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)c;
+  attr[0].val.clusterDim.x = (unsigned)shape.cluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)(a.rows * c), 1, 1);
+  cfg.gridDim = dim3((unsigned)(a.rows * shape.cluster), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = (size_t)iters * kChunkBytes;
+  cfg.dynamicSmemBytes = shape.keep ? (size_t)shape.iters * kChunkBytes : 0;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a, table, iters) == cudaSuccess ? VMLA_OK : VMLA_ERR_CUDA;
+  const auto kernel = shape.keep ? sample_kernel<T, true> : sample_kernel<T, false>;
+  return cudaLaunchKernelEx(&cfg, kernel, a, table, shape.iters) == cudaSuccess ? VMLA_OK : VMLA_ERR_CUDA;
 }
 
 }  // namespace
