@@ -50,17 +50,17 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kChunkBytes = kThreads * 16;   // shared memory per iteration: 16 bytes per thread
-constexpr int kMaxIters = 17;                // kept rows: 8 x 17 x 2048 floats hold VMLA_MAX_VOCAB and a misaligned start
-constexpr int kMaxElems = 264;               // re-read rows: logits of one thread
-constexpr int kMaxChunks = kMaxElems / 4;    // iterations of one warp in either case
+constexpr int kKeepIters = 8;                // a row kept in shared memory takes up to 64 KB of each CTA
+constexpr int kMaxElems = 264;               // logits of one thread
+constexpr int kMaxChunks = kMaxElems / 4;    // iterations of one warp
 constexpr float kOctaves = 46.f;             // weights below 2^-kOctaves count as zero
 constexpr int kNearZero = 0x3A80;            // leading 16 bits of 2^-10: smaller values share one bin
 constexpr int kBins = 18 * kThreads;         // 9216: see bin_of
 constexpr int kRanges = 1024;                // of the bit-pattern histograms
 constexpr int kUnitBits = 45;                // weights in units of 2^-45: 2^18 tokens' sum stays below 2^63
 static_assert((int64_t)VMLA_MAX_VOCAB << kUnitBits <= INT64_MAX, "sums of weights fit 63 bits");
-static_assert((int64_t)kMaxCluster * kMaxIters * (kChunkBytes / 4) >= VMLA_MAX_VOCAB + 3, "every vocabulary fits");
-static_assert((int64_t)kMaxElems << 23 < (1ll << 32) && kMaxIters * 8 <= kMaxElems, "a thread's sum of high parts fits 32 bits");
+static_assert((int64_t)kMaxCluster * kThreads * kMaxElems >= VMLA_MAX_VOCAB + 7, "every vocabulary fits");
+static_assert((int64_t)kMaxElems << 23 < (1ll << 32) && kKeepIters * 8 <= kMaxElems, "a thread's sum of high parts fits 32 bits");
 
 // 2^(k/64) as a pair of floats, filled by the host.
 struct ExpTable {
@@ -89,13 +89,14 @@ struct Shared {
   int32_t index;
   // written by the one thread of the cluster that finds them, into every CTA
   int32_t bin_k, bin_p, bracket_lo, bracket_hi, sure;
-  uint32_t bin_k_rank, bin_k_count, bin_p_count;
+  uint32_t bin_k_rank, bin_p_count;
   uint64_t bin_p_left;
   // results of a search, the same in every CTA
   int32_t range;
   uint32_t range_count;
   uint64_t range_before;
   uint64_t chunk[kMaxChunks];
+  uint32_t chunk_same[kMaxChunks];
 };
 
 // Whole numbers in the order of the values, without the low bits that a type's values never use.
@@ -183,35 +184,27 @@ __device__ __forceinline__ uint64_t weight_units(float x, const Exponent& e, con
 }
 
 // The weight in single precision, times a factor that all of a row's weights share: 2^(x c + bias),
-// bias being -max c (below 2^15) rounded to a multiple of 2^-7, which keeps bias - n exact.  The exponent is
-// split into a whole number n and f, |f| <= 1, whose error is below 2^-24; ex2 on it is good to 2^-22,
-// sums of eight in a tree to 3 x 2^-24 and their running sum in two floats to less: together below
-// 2^-20.5 of the weights summed.  A running sum C and the total W then place u W - C within
-// 2 u (1 - u) 2^-20.5 W <= 2^-21.5 W of its value.  For x c + bias > -100 only.
+// bias being the whole number next to -max c (below 2^20).  The exponent is split into a whole
+// number n = t - 1.5 x 2^23 and f, |f| <= 1/2: bias - n is exact, f is off by less than 2^-25, ex2 on it
+// by 2^-22 (2^-22.47 measured over 6 x 10^7 values), sums of eight in a tree by 3 x 2^-24 and their running
+// sum in two floats by less: together below 2^-20.5 of the weights summed.  A running sum C and the total
+// W then place u W - C within 2 u (1 - u) 2^-20.5 W <= 2^-21.5 W of its value.  For x c + bias > -100 only.
 struct About {
-  float hi, lo, bias, magic;
+  float hi, lo, magic;
 };
-constexpr float kAboutMax = 32768.f;  // of |max c|
-constexpr int kSureBits = 21;  // a border nearer than W 2^-21 to u W is not decided by these sums
+constexpr float kAboutMax = 1048576.f;  // of |max c|
+constexpr int kSureBits = 21;           // a border nearer than W 2^-21 to u W is not decided by these sums
 
 __device__ __forceinline__ About about(const Exponent& e) {
-  About a;
-  a.hi = e.hi;
-  a.lo = e.lo;
-  a.bias = __fsub_rn(__fadd_rn(-e.max * e.hi, 98304.f), 98304.f);  // in [2^16, 2^17) floats are 2^-7 apart
-  a.magic = __fadd_rn(12582912.f, a.bias);  // 1.5 x 2^23 + bias: whole
-  return a;
+  return {e.hi, e.lo, __fadd_rn(12582912.f, rintf(-e.max * e.hi))};  // 1.5 x 2^23 + bias
 }
 __device__ __forceinline__ float about_of(float x, const About& a) {
   const float t = __fmaf_rn(x, a.hi, a.magic);
-  const float n = __fsub_rn(t, 12582912.f);
-  const float f = __fmaf_rn(x, a.lo, __fmaf_rn(x, a.hi, __fsub_rn(a.bias, n)));
+  const float f = __fmaf_rn(x, a.lo, __fmaf_rn(x, a.hi, __fsub_rn(a.magic, t)));  // magic - t = bias - n
   return __uint_as_float(__float_as_uint(ex2_approx(f)) + (__float_as_uint(t) << 23));
 }
-// A float's value (below 2^19) in units of 2^-45.
-__device__ __forceinline__ uint64_t about_units(float hi, float lo) {
-  return (uint64_t)(hi * 35184372088832.f) + (uint64_t)(int64_t)(lo * 35184372088832.f);
-}
+// A float's value (below 2^18 1.5) in units of 2^-45.
+__device__ __forceinline__ uint64_t about_units(float v) { return (uint64_t)(v * 35184372088832.f); }
 
 template <typename V>
 __device__ __forceinline__ V warp_add(V v) {
@@ -400,6 +393,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     }
   }
   float mx = E::largest(run);
+  if (tid == 0) sm.sure = 0;  // (set from another CTA only past the barriers below)
   if (tid < 64) sm.table[tid] = exp_table.t[tid];
   mx = warp_max(mx);
   if (lane == 0) sm.warp_f[warp] = mx;
@@ -463,9 +457,10 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     for (int r = 0; r < C; ++r) cluster.map_shared_rank(&sm, r)->*member = value;
   };
 
-  // ---- what is kept: x > cut_x, and x == cut_x up to place cut_place
+  // ---- what is kept: x > cut_x, and of the tokens equal to cut_x the first cut_keep
+  constexpr uint32_t kAllEqual = UINT32_MAX;
   float cut_x = -INFINITY;
-  uint32_t cut_keep = 0, cut_equal = 0;  // of the tokens equal to cut_x, the first cut_keep of cut_equal
+  uint32_t cut_keep = kAllEqual;
   bool with_k = top_k > 0 && top_k < a.vocab;
   const bool with_p = top_p < 1.f;
   if (with_k || with_p) {
@@ -604,7 +599,6 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
         if (at < (uint32_t)top_k && at + n >= (uint32_t)top_k) {  // one bin of the cluster
           to_all(&Shared::bin_k, bin0 + j);
           to_all(&Shared::bin_k_rank, (uint32_t)top_k - at);
-          to_all(&Shared::bin_k_count, n);
         }
         at += n;
       }
@@ -621,7 +615,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     bool found = false;
     if (E::kLowBits && !(with_k && bin_k == tiny_bin)) {
       // bf16: bins are values
-      if (with_k) cut_x = number_value(top_number - bin_k), cut_keep = k_rank, cut_equal = sm.bin_k_count;
+      if (with_k) cut_x = number_value(top_number - bin_k), cut_keep = k_rank;
       found = !with_p;
       if (with_p) {
         uint64_t all = 0, tiny_all = 0, own = 0, block;
@@ -659,7 +653,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
           const float x = number_value(top_number - sm.bin_p);
           const uint64_t w = weight_units(x, ex, sm.table);
           const uint32_t keep = w > 0 ? (uint32_t)((sm.bin_p_left + w - 1) / w) : sm.bin_p_count;
-          if (!with_k || sm.bin_p != bin_k || keep < cut_keep) cut_x = x, cut_keep = keep, cut_equal = sm.bin_p_count;
+          if (!with_k || sm.bin_p != bin_k || keep < cut_keep) cut_x = x, cut_keep = keep;
           found = true;
         }
       }
@@ -711,7 +705,8 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
       if (with_k) {
         uint64_t left;
         bin_keys(bin_k, bin_k, &klo, &khi);
-        refine(klo, khi, false, k_rank, &floor_key, &cut_equal, &left);
+        uint32_t equal;
+        refine(klo, khi, false, k_rank, &floor_key, &equal, &left);
         cut_x = order_value<E::kLowBits>(floor_key);
         cut_keep = (uint32_t)left;
       }
@@ -748,87 +743,57 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
         const uint64_t w = weight_units(x, ex, sm.table);
         const uint32_t keep = w > 0 ? (uint32_t)min((left + w - 1) / w, (uint64_t)equal) : equal;
         if (with_k && x == cut_x) cut_keep = min(cut_keep, keep);
-        else cut_x = x, cut_keep = keep, cut_equal = equal;
+        else cut_x = x, cut_keep = keep;
       }
     }
   }
   if (min_p > 0.f) {
     // w >= min_p  <=>  x >= max + T ln(min_p)
     const float x = __double2float_ru((double)mx + sm.min_p_offset);
-    if (x > cut_x) cut_x = x, cut_keep = cut_equal = 0;
-  }
-  const bool some_equal = cut_keep < cut_equal;
-  int cut_place = INT32_MAX;
-  if (some_equal) {
-    // the place of the cut_keep-th token equal to cut_x, in the order of the places
-    uint32_t here = 0;
-    each([&](float x, int) { here += x == cut_x ? 1u : 0u; });
-    here = warp_add(here);
-    __syncthreads();
-    if (lane == 0) sm.warp_u32[warp] = here;
-    __syncthreads();
-    uint32_t block = 0, skip = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      block += sm.warp_u32[w];
-      if (w < warp) skip += sm.warp_u32[w];
-    }
-    if (tid == 0) sm.count = block;
-    cluster.sync();
-    for (int r = 0; r < rank; ++r) skip += *cluster.map_shared_rank(&sm.count, r);
-    if (skip < cut_keep && skip + here >= cut_keep) {  // one warp of the cluster
-      for (int i = 0; i < iters; ++i) {
-        float x[kVec];
-        values(fetch(warp, i), x);
-        uint32_t own = 0;
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) own += x[k] == cut_x ? 1u : 0u;
-        const uint32_t inc = warp_scan(own, lane);
-        uint32_t at = skip + inc - own;
-        if (at < cut_keep && at + own >= cut_keep) {
-#pragma unroll
-          for (int k = 0; k < kVec; ++k)
-            if (x[k] == cut_x && ++at == cut_keep) to_all(&Shared::index, first + i * kStep + lane * kVec + k);
-        }
-        skip += __shfl_sync(0xffffffffu, inc, 31);
-      }
-    }
-    cluster.sync();
-    cut_place = sm.index;
+    if (x > cut_x) cut_x = x, cut_keep = kAllEqual;
   }
 
-  // ---- the draw, in the order of the places.  With `exact` false in single precision: sm.sure tells
-  // whether that decides the token.
+  // ---- the draw, in the order of the places: sums of the weights above cut_x and counts of the tokens
+  // equal to it, per warp, per CTA, and in the one warp whose run holds the token, per iteration, lane
+  // and place.  With `exact` false in single precision: sm.sure tells whether that decides the token.
+  const bool partial = cut_keep != kAllEqual;
+  const float over = partial ? cut_x : nextafterf(cut_x, -INFINITY);  // kept whole: x > over
   const About ab = about(ex);
-  const float x_zero = mx - kOctaves * 0.6931472f * temp;  // values below count as zero in the single-precision sums
-  auto kept = [&](float x, int p) { return x > cut_x || (x == cut_x && p <= cut_place); };
-  auto one = [&](float x, int p, bool exact) -> uint64_t {
-    if (!kept(x, p)) return 0;
-    return exact ? weight_units(x, ex, sm.table) : x >= x_zero ? about_units(about_of(x, ab), 0.f) : 0;
-  };
+  const float x_zero = mx - kOctaves * 0.6931472f * temp;  // the single-precision sums leave out what lies below
+  const float over_about = fmaxf(over, x_zero);  // (x_zero < mx where |max c| < kAboutMax)
   auto draw = [&](bool exact) {
+    // a token's weight, if it is above the cut
+    auto weight = [&](float x) -> uint64_t {
+      if (exact) return x > over ? weight_units(x, ex, sm.table) : 0;
+      return x > over_about ? about_units(about_of(x, ab)) : 0;
+    };
+    const uint64_t w_cut =
+        !partial ? 0 : exact ? weight_units(cut_x, ex, sm.table) : cut_x >= x_zero ? about_units(about_of(cut_x, ab)) : 0;
+    // what the tokens numbered [from, to) of those equal to cut_x add
+    auto equals = [&](uint32_t from, uint32_t to) { return w_cut * (min(to, cut_keep) - min(from, cut_keep)); };
     uint64_t sum;
+    uint32_t same = 0;
     if (exact) {
       uint32_t h = 0;
       int32_t l = 0;
-      each([&](float x, int p) {
-        if (kept(x, p)) {
+      each([&](float x, int) {
+        if (x > over) {
           int32_t wh, wl;
           weight_of(x, ex, sm.table, &wh, &wl);
           h += wh, l += wl;
         }
+        if (partial && x == cut_x) ++same;
       });
       sum = units(h, l);
     } else {
       float s = 0.f, e = 0.f;  // the sum in two floats
-      const float least = fmaxf(cut_x, x_zero);
-      each_granule([&](const float (&x)[kVec], int p) {
+      each_granule([&](const float (&x)[kVec], int) {
         float w[kVec];
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) {
-          bool in = x[k] >= least;
-          if (some_equal) in = in && (x[k] != cut_x || p + k <= cut_place);
-          w[k] = in ? about_of(x[k], ab) : 0.f;
-        }
+        for (int k = 0; k < kVec; ++k) w[k] = x[k] > over_about ? about_of(x[k], ab) : 0.f;
+        if (partial)
+#pragma unroll
+          for (int k = 0; k < kVec; ++k) same += x[k] == cut_x ? 1u : 0u;
 #pragma unroll
         for (int o = kVec / 2; o > 0; o >>= 1)
 #pragma unroll
@@ -837,76 +802,102 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
         e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(w[0], b)));
         s = t;
       });
-      sum = about_units(s, e);
+      sum = about_units(s) + (uint64_t)(int64_t)(e * 35184372088832.f);
     }
     sum = warp_add(sum);
+    same = warp_add(same);
     __syncthreads();
-    if (lane == 0) sm.warp_u64[warp] = sum;
+    if (lane == 0) sm.warp_u64[warp] = sum, sm.warp_u32[warp] = same;
     __syncthreads();
-    uint64_t block = 0;
-    for (int w = 0; w < kWarps; ++w) block += sm.warp_u64[w];
-    if (tid == 0) sm.sum_a = block;
+    if (tid == 0) {
+      uint64_t s = 0;
+      uint32_t n = 0;
+      for (int w = 0; w < kWarps; ++w) s += sm.warp_u64[w], n += sm.warp_u32[w];
+      sm.sum_a = s, sm.count = n;
+    }
     cluster.sync();
-    uint64_t all = 0, before = 0;
+    uint64_t all = 0, before = 0, here = 0;  // mass of the row, of the CTAs before this one, and of this one
+    uint32_t ahead = 0, seen = 0;            // tokens equal to cut_x before this CTA; before CTA r
     for (int r = 0; r < C; ++r) {
-      const uint64_t s = *cluster.map_shared_rank(&sm.sum_a, r);
-      if (r < rank) before += s;
-      all += s;
+      const uint32_t n = *cluster.map_shared_rank(&sm.count, r);
+      const uint64_t m = *cluster.map_shared_rank(&sm.sum_a, r) + equals(seen, seen + n);
+      if (r == rank) before = all, here = m, ahead = seen;
+      all += m;
+      seen += n;
     }
     // the token's running sum is the first above `goal` = floor(u all)
     const uint64_t goal = u < 1.f ? __umul64hi((uint64_t)(u * 18446744073709551616.f), all) : all - 1;
-    if (before <= goal && goal < before + block) {  // one CTA of the cluster
+    if (before <= goal && goal < before + here) {  // one CTA of the cluster
       int w0 = 0;
-      while (w0 < kWarps - 1 && before + sm.warp_u64[w0] <= goal) before += sm.warp_u64[w0++];
+      for (; w0 < kWarps - 1; ++w0) {
+        const uint64_t m = sm.warp_u64[w0] + equals(ahead, ahead + sm.warp_u32[w0]);
+        if (goal < before + m) break;
+        before += m;
+        ahead += sm.warp_u32[w0];
+      }
       // that warp's places, one iteration's per warp of this CTA
-      const int start = (rank * kWarps + w0) * seg + lane * kVec;
       for (int i = warp; i < iters; i += kWarps) {
         float x[kVec];
         values(fetch(w0, i), x);
-        uint64_t s = 0;
-#pragma unroll 1
-        for (int k = 0; k < kVec; ++k) s += one(x[k], start + i * kStep + k, exact);
-        s = warp_add(s);
-        if (lane == 0) sm.chunk[i] = s;
+        uint64_t m = 0;
+        uint32_t n = 0;
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) m += weight(x[k]), n += partial && x[k] == cut_x ? 1u : 0u;
+        m = warp_add(m);
+        n = warp_add(n);
+        if (lane == 0) sm.chunk[i] = m, sm.chunk_same[i] = n;
       }
       __syncthreads();
       if (warp == 0) {
         int i = 0;
-        while (i < iters - 1 && before + sm.chunk[i] <= goal) before += sm.chunk[i++];
+        for (; i < iters - 1; ++i) {
+          const uint64_t m = sm.chunk[i] + equals(ahead, ahead + sm.chunk_same[i]);
+          if (goal < before + m) break;
+          before += m;
+          ahead += sm.chunk_same[i];
+        }
         float x[kVec];
-        uint64_t s = 0, w[kVec];
+        uint64_t m = 0, w[kVec];
+        uint32_t n = 0;
         values(fetch(w0, i), x);
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) s += w[k] = one(x[k], start + i * kStep + k, exact);
-        uint64_t at = before + warp_scan(s, lane) - s;
-        if (at <= goal && goal < at + s) {
+        for (int k = 0; k < kVec; ++k) m += w[k] = weight(x[k]), n += partial && x[k] == cut_x ? 1u : 0u;
+        uint32_t nth = ahead + warp_scan(n, lane) - n;
+        uint64_t at = m + equals(nth, nth + n);
+        const uint64_t mine = at;
+        at = before + warp_scan(at, lane) - at;
+        if (at <= goal && goal < at + mine) {
 #pragma unroll
           for (int k = 0; k < kVec; ++k) {
-            if (at <= goal && goal < at + w[k]) {
-              a.token[row] = start + i * kStep + k - shift;
+            const bool eq = partial && x[k] == cut_x;
+            const uint64_t own = eq ? equals(nth, nth + 1) : w[k];
+            if (eq) ++nth;
+            if (at <= goal && goal < at + own) {
+              a.token[row] = (rank * kWarps + w0) * seg + i * kStep + lane * kVec + k - shift;
               const uint64_t margin = all >> kSureBits;
-              if (goal - at >= margin && at + w[k] - goal > margin) to_all(&Shared::sure, 1);
+              if (goal - at >= margin && at + own - goal > margin) to_all(&Shared::sure, 1);
             }
-            at += w[k];
+            at += own;
           }
         }
       }
     }
     cluster.sync();  // sm.sure is settled, and no CTA leaves while another reads its shared memory
   };
-  if (tid == 0) sm.sure = 0;
   bool sure = false;
   if (fabsf(mx * ex.hi) < kAboutMax) {
-    cluster.sync();  // sm.sure is cleared in every CTA
     draw(false);
     sure = sm.sure != 0;
   }
   if (!sure) draw(true);
 }
 
-// CTAs per row.  A row is kept in shared memory while that leaves no SM with more than one CTA's
-// work (measured: 1 x 32,000 bf16 TODO); rows beyond that are re-read.  Either way the cluster grows
-// while SMs would be idle, and as far as the limits on a CTA's share of a row ask.
+// CTAs per row: more while they all find room on the SMs (two on each, and as many waiting), or while
+// one CTA's share of a row is over 20 iterations (160 KB); its row stays in shared memory where that
+// takes 64 KB.  Measured, us by cluster size 1 / 2 / 4 / 8 (kept where marked *): 512 rows of 131,072
+// bf16 154 / 126 / 128* / 188*, 150 rows 93 / 62 / 51* / 63*, 16 rows 54 / 34 / 21* / 18*; 128 rows of
+// 151,001 fp32 - / 199 / 175 / 278; 400 rows of 32,000 bf16 50* / 65* / 100* / 181*; without keeping
+// the last are 59 / 75 / 114 / 204.
 struct Shape {
   int cluster, iters;
   bool keep;
@@ -921,10 +912,10 @@ Shape choose_shape(const SampleArgs& a, int sms) {
   };
   Shape s;
   s.cluster = 1;
-  while (s.cluster < kMaxCluster && a.rows * s.cluster * 2 <= 2 * sms && need(s.cluster) > 1) s.cluster *= 2;
-  s.keep = a.rows * s.cluster <= 2 * sms && need(s.cluster) <= 8;
-  const int most = s.keep ? kMaxIters : kMaxElems / Elems<T>::kVec;
-  while (s.cluster < kMaxCluster && need(s.cluster) > most) s.cluster *= 2;
+  while (s.cluster < kMaxCluster && need(s.cluster) > 1 && (a.rows * s.cluster * 2 <= 4 * sms || need(s.cluster) > 20))
+    s.cluster *= 2;
+  s.keep = need(s.cluster) <= kKeepIters;
+  while (s.cluster < kMaxCluster && need(s.cluster) > kMaxElems / Elems<T>::kVec) s.cluster *= 2;
   s.iters = need(s.cluster);
   return s;
 }
@@ -941,7 +932,7 @@ int launch(const SampleArgs& a, int sms, int dev, cudaStream_t stream) {
     return t;
   }();
   const Shape shape = choose_shape<T>(a, sms);
-  if (shape.iters > (shape.keep ? kMaxIters : kMaxChunks) || a.rows * shape.cluster > INT32_MAX) return VMLA_ERR_SHAPE;
+  if (shape.iters > kMaxElems / Elems<T>::kVec || a.rows * shape.cluster > INT32_MAX) return VMLA_ERR_SHAPE;
   if (shape.keep) {
     static bool ready[64] = {};
     static std::mutex mu;
@@ -949,7 +940,7 @@ int launch(const SampleArgs& a, int sms, int dev, cudaStream_t stream) {
     if (dev >= 64 || !ready[dev]) {
       // (all of the SM's memory as shared memory: the default split left room for one CTA)
       if (cudaFuncSetAttribute(sample_kernel<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               kMaxIters * kChunkBytes) != cudaSuccess ||
+                               kKeepIters * kChunkBytes) != cudaSuccess ||
           cudaFuncSetAttribute(sample_kernel<T, true>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared) != cudaSuccess)
         return VMLA_ERR_CUDA;
