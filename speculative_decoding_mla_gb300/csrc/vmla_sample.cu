@@ -514,71 +514,76 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     }
     if (with_k && (uint32_t)top_k >= total) with_k = false;  // nothing of weight is past the k-th
 
+    // Histograms of counts (and masses) over the 1024 equal ranges of keys from klo on, each 2^width
+    // keys wide, of this CTA's tokens; the keys are clear when all CTAs have passed the next barrier.
+    auto range_width = [](uint32_t klo, uint32_t khi) { return max(32 - __clz((khi - klo) | 1) - 10, 0); };
+    auto clear_ranges = [&] {
+      for (int b = tid; b < kRanges; b += kThreads) sm.r.count[b] = sm.r.mass_lo[b] = sm.r.mass_hi[b] = 0;
+      __syncthreads();
+    };
+    auto add_mass = [&](uint32_t g, uint64_t w) {
+      const uint32_t wl = (uint32_t)w, old = atomicAdd(&sm.r.mass_lo[g], wl);
+      atomicAdd(&sm.r.mass_hi[g], (uint32_t)(w >> 32) + (old + wl < old ? 1u : 0u));
+    };
+    // The range in which the running count (or mass), in descending order, reaches `target`: [klo, khi]
+    // becomes it; its count; and what is left of the target.
+    auto pick = [&](bool by_mass, int width, uint32_t* klo, uint32_t* khi, uint64_t* target, uint32_t* equal) {
+      constexpr int kPer = kRanges / kThreads;
+      uint32_t n2[kPer], sum_n = 0;
+      uint64_t m2[kPer], sum_m = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int g = kRanges - 1 - (kPer * tid + j);  // descending
+        n2[j] = 0, m2[j] = 0;
+        for (int r = 0; r < C; ++r) {
+          const Shared* o = cluster.map_shared_rank(&sm, r);
+          n2[j] += o->r.count[g];
+          if (by_mass) m2[j] += ((uint64_t)o->r.mass_hi[g] << 32) + o->r.mass_lo[g];
+        }
+        sum_n += n2[j], sum_m += m2[j];
+      }
+      uint32_t all_n;
+      uint64_t all_m = 0, cum_m = 0;
+      uint32_t cum_n = block_scan(sum_n, sm.warp_u32, &all_n);
+      if (by_mass) cum_m = block_scan(sum_m, sm.warp_u64, &all_m);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const uint64_t was = by_mass ? cum_m : cum_n;
+        cum_n += n2[j], cum_m += m2[j];
+        const uint64_t now = by_mass ? cum_m : cum_n;
+        if (was < *target && now >= *target) {  // one range of one thread
+          sm.range = kRanges - 1 - (kPer * tid + j);
+          sm.range_count = n2[j];
+          sm.range_before = was;
+        }
+      }
+      __syncthreads();
+      *target -= sm.range_before;
+      *equal = sm.range_count;
+      *klo += (uint32_t)sm.range << width;
+      *khi = min(*khi, *klo + ((1u << width) - 1u));
+      cluster.sync();  // the histograms have been read
+    };
     // The value at which a running count (or mass) over the tokens with a key in [klo, khi], in
     // descending order, reaches `target`: its key, how many tokens have it, and what is left of the
-    // target for them.
-    auto refine = [&](uint32_t klo, uint32_t khi, bool by_mass, uint64_t target, uint32_t* key, uint32_t* equal,
-                      uint64_t* left) {
-      // (a round leaves 10 bits fewer: 32, 22, 12, 2)
+    // target for them.  (A round leaves 10 bits fewer: 32, 22, 12, 2.)
+    auto refine = [&](uint32_t klo, uint32_t khi, bool by_mass, uint64_t* target, uint32_t* equal) {
       for (int round = 0; round < 4; ++round) {
-        // ranges of equal width, a power of two
-        int width = 32 - __clz((khi - klo) | 1) - 10;
-        width = width < 0 ? 0 : width;
-        for (int b = tid; b < kRanges; b += kThreads) sm.r.count[b] = sm.r.mass_lo[b] = sm.r.mass_hi[b] = 0;
-        __syncthreads();
+        const int width = range_width(klo, khi);
+        clear_ranges();
         each([&](float x, int) {
           const uint32_t k = order_key<E::kLowBits>(x);
           if (k >= klo && k <= khi) {
             const uint32_t g = (k - klo) >> width;
             atomicAdd(&sm.r.count[g], 1u);
-            if (by_mass) {
-              const uint64_t w = weight_units(x, ex, sm.table);
-              const uint32_t wl = (uint32_t)w, old = atomicAdd(&sm.r.mass_lo[g], wl);
-              atomicAdd(&sm.r.mass_hi[g], (uint32_t)(w >> 32) + (old + wl < old ? 1u : 0u));
-            }
+            if (by_mass) add_mass(g, weight_units(x, ex, sm.table));
           }
         });
         cluster.sync();
-        constexpr int kPer = kRanges / kThreads;
-        uint32_t n2[kPer], sum_n = 0;
-        uint64_t m2[kPer], sum_m = 0;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const int g = kRanges - 1 - (kPer * tid + j);  // descending
-          n2[j] = 0, m2[j] = 0;
-          for (int r = 0; r < C; ++r) {
-            const Shared* o = cluster.map_shared_rank(&sm, r);
-            n2[j] += o->r.count[g];
-            if (by_mass) m2[j] += ((uint64_t)o->r.mass_hi[g] << 32) + o->r.mass_lo[g];
-          }
-          sum_n += n2[j], sum_m += m2[j];
-        }
-        uint32_t all_n;
-        uint64_t all_m = 0, cum_m = 0;
-        uint32_t cum_n = block_scan(sum_n, sm.warp_u32, &all_n);
-        if (by_mass) cum_m = block_scan(sum_m, sm.warp_u64, &all_m);
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const uint64_t was = by_mass ? cum_m : cum_n;
-          cum_n += n2[j], cum_m += m2[j];
-          const uint64_t now = by_mass ? cum_m : cum_n;
-          if (was < target && now >= target) {  // one range of one thread
-            sm.range = kRanges - 1 - (kPer * tid + j);
-            sm.range_count = n2[j];
-            sm.range_before = was;
-          }
-        }
-        __syncthreads();
-        target -= sm.range_before;
-        *equal = sm.range_count;
-        klo += (uint32_t)sm.range << width;
-        const uint32_t hi2 = klo + ((1u << width) - 1u);
-        khi = hi2 < khi ? hi2 : khi;
-        cluster.sync();  // the histograms have been read
+        pick(by_mass, width, &klo, &khi, target, equal);
         if (width == 0) break;
       }
-      *key = klo;
-      *left = target;
+      return klo;
     };
     // Keys of the values in bins [b_first, b_last].
     auto bin_keys = [&](int b_first, int b_last, uint32_t* klo, uint32_t* khi) {
@@ -701,26 +706,35 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
         b_lo = min(b_lo, b_hi);
       }
       cluster.sync();  // the histograms and brackets have been read
-      uint32_t floor_key = 0, klo, khi;
+      uint32_t floor_key = 0, klo, khi, equal;
       if (with_k) {
-        uint64_t left;
+        uint64_t left = k_rank;
         bin_keys(bin_k, bin_k, &klo, &khi);
-        uint32_t equal;
-        refine(klo, khi, false, k_rank, &floor_key, &equal, &left);
+        floor_key = refine(klo, khi, false, &left, &equal);
         cut_x = order_value<E::kLowBits>(floor_key);
         cut_keep = (uint32_t)left;
       }
       if (with_p) {
-        // exact masses of what top-k leaves: all of it, and the part above the bracket
+        // In one pass the exact masses of what top-k leaves, of its part above the bracket, and of the
+        // ranges of the bracket (of the tokens equal to top-k's cut, all: they come last)
         bin_keys(b_lo, b_hi, &klo, &khi);
+        klo = max(klo, floor_key);
+        const int width = range_width(klo, khi);
+        clear_ranges();
         uint32_t all_h = 0, top_h = 0;
         int32_t all_l = 0, top_l = 0;
         each([&](float x, int) {
-          if (x > cut_x) {
+          const uint32_t k = order_key<E::kLowBits>(x);
+          if (k >= floor_key && x != -INFINITY) {
             int32_t h, l;
             weight_of(x, ex, sm.table, &h, &l);
-            all_h += h, all_l += l;
-            if (order_key<E::kLowBits>(x) > khi) top_h += h, top_l += l;
+            if (k > floor_key) all_h += h, all_l += l;
+            if (k > khi) {
+              top_h += h, top_l += l;
+            } else if (k >= klo) {
+              atomicAdd(&sm.r.count[(k - klo) >> width], 1u);
+              add_mass((k - klo) >> width, units(h, l));
+            }
           }
         });
         uint64_t all = warp_add(units(all_h, all_l)), top = warp_add(units(top_h, top_l));
@@ -735,11 +749,11 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
         all = with_k ? (uint64_t)cut_keep * weight_units(cut_x, ex, sm.table) : 0, top = 0;
         for (int r = 0; r < C; ++r)
           all += *cluster.map_shared_rank(&sm.sum_a, r), top += *cluster.map_shared_rank(&sm.sum_b, r);
-        const uint64_t least = least_mass(all), target = least > top ? least - top : 1;
-        uint32_t key, equal;
-        uint64_t left;
-        refine(max(klo, floor_key), khi, true, target, &key, &equal, &left);
-        const float x = order_value<E::kLowBits>(key);
+        const uint64_t least = least_mass(all);
+        uint64_t left = least > top ? least - top : 1;
+        pick(true, width, &klo, &khi, &left, &equal);
+        if (width > 0) klo = refine(klo, khi, true, &left, &equal);
+        const float x = order_value<E::kLowBits>(klo);
         const uint64_t w = weight_units(x, ex, sm.table);
         const uint32_t keep = w > 0 ? (uint32_t)min((left + w - 1) / w, (uint64_t)equal) : equal;
         if (with_k && x == cut_x) cut_keep = min(cut_keep, keep);
