@@ -906,12 +906,13 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
   if (!sure) draw(true);
 }
 
-// CTAs per row: more while they all find room on the SMs (two on each, and as many waiting), or while
-// one CTA's share of a row is over 20 iterations (160 KB); its row stays in shared memory where that
-// takes 64 KB.  Measured, us by cluster size 1 / 2 / 4 / 8 (kept where marked *): 512 rows of 131,072
-// bf16 154 / 126 / 128* / 188*, 150 rows 93 / 62 / 51* / 63*, 16 rows 54 / 34 / 21* / 18*; 128 rows of
-// 151,001 fp32 - / 199 / 175 / 278; 400 rows of 32,000 bf16 50* / 65* / 100* / 181*; without keeping
-// the last are 59 / 75 / 114 / 204.
+// CTAs per row: up to four while they find room on the SMs (two on each, and as many waiting), eight
+// while that leaves SMs idle, and more while one CTA's share of a row is over 20 iterations (160 KB);
+// the row stays in shared memory where that takes 64 KB of each.  Measured, us by cluster size 1 / 2 / 4 /
+// 8 (kept where marked *): 512 rows of 131,072 bf16 154 / 126 / 128* / 188*, 150 rows 93 / 62 / 51* / 63*,
+// 16 rows 54 / 34 / 21* / 18*; with top-p, 64 rows 102 / 64 / 44* / 53*; 151,001 fp32, 128 rows - / 199 /
+// 175 / 278, 16 rows - / 120 / 80 / 73; 400 rows of 32,000 bf16 50* / 65* / 100* / 181*, without keeping
+// them 59 / 75 / 114 / 204.
 struct Shape {
   int cluster, iters;
   bool keep;
@@ -926,7 +927,8 @@ Shape choose_shape(const SampleArgs& a, int sms) {
   };
   Shape s;
   s.cluster = 1;
-  while (s.cluster < kMaxCluster && need(s.cluster) > 1 && (a.rows * s.cluster * 2 <= 4 * sms || need(s.cluster) > 20))
+  while (s.cluster < kMaxCluster && need(s.cluster) > 1 &&
+         (a.rows * s.cluster * 2 <= (s.cluster < 4 ? 4 : 1) * sms || need(s.cluster) > 20))
     s.cluster *= 2;
   s.keep = need(s.cluster) <= kKeepIters;
   while (s.cluster < kMaxCluster && need(s.cluster) > kMaxElems / Elems<T>::kVec) s.cluster *= 2;
