@@ -38,6 +38,7 @@
 
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "vmla_device.cuh"
 
@@ -143,8 +144,6 @@ __device__ __forceinline__ void weight_of(float x, const Exponent& e, const floa
   const float bb = __fsub_rn(s, e.max);
   const float err = __fsub_rn(__fsub_rn(e.max, __fsub_rn(s, bb)), __fadd_rn(x, bb));
   const float ph = __fmul_rn(s, e.hi);
-  *high = *low = 0;
-  if (!(ph < kOctaves)) return;  // also where x is -inf
   float pl = __fmaf_rn(s, e.hi, -ph);
   pl = __fmaf_rn(s, e.lo, pl);
   pl = __fmaf_rn(err, e.hi, pl);
@@ -171,8 +170,10 @@ __device__ __forceinline__ void weight_of(float x, const Exponent& e, const floa
   const float hf = __fmaf_rn(wh, scale, kWhole);
   const float res = __fmaf_rn(wl, scale, __fmaf_rn(wh, scale, -__fsub_rn(hf, kWhole)));
   const float lf = __fmaf_rn(res, 4194304.f, kHalf);
-  *high = (int)(__float_as_uint(hf) - __float_as_uint(kWhole));
-  *low = (int)(__float_as_uint(lf) - __float_as_uint(kHalf));
+  // (no branch above: the weights of a thread's tokens are worked out side by side)
+  const bool some = ph < kOctaves;  // not where x is -inf
+  *high = some ? (int)(__float_as_uint(hf) - __float_as_uint(kWhole)) : 0;
+  *low = some ? (int)(__float_as_uint(lf) - __float_as_uint(kHalf)) : 0;
 }
 
 __device__ __forceinline__ uint64_t units(int64_t high, int64_t low) { return (uint64_t)((high << 22) + low); }
@@ -185,15 +186,22 @@ __device__ __forceinline__ uint64_t weight_units(float x, const Exponent& e, con
 
 // The weight in single precision, times a factor that all of a row's weights share: 2^(x c + bias),
 // bias being the whole number next to -max c (below 2^20).  The exponent is split into a whole
-// number n = t - 1.5 x 2^23 and f, |f| <= 1/2: bias - n is exact, f is off by less than 2^-25, ex2 on it
-// by 2^-22 (2^-22.47 measured over 6 x 10^7 values), sums of eight in a tree by 3 x 2^-24 and their running
-// sum in two floats by less: together below 2^-20.5 of the weights summed.  A running sum C and the total
-// W then place u W - C within 2 u (1 - u) 2^-20.5 W <= 2^-21.5 W of its value.  For x c + bias > -100 only.
+// number n = t - 1.5 x 2^23 and f, |f| <= 1/2: bias - n is exact, f is off by at most 2^-25, which moves
+// the weight by 2.1e-8; ex2.approx on such f is off by -1.43e-7 to 1.46e-7 (every float of that range, on
+// this GPU); sums of eight in a tree add 3 x 2^-24 = 1.8e-7, their running sum in two floats nothing that
+// counts: kAboutError in all.  A running sum C and the total W then place u W - C within
+// 2 u (1 - u) kAboutError W of its value.  For x c + bias > -100 only.
 struct About {
   float hi, lo, magic;
 };
 constexpr float kAboutMax = 1048576.f;  // of |max c|
-constexpr int kSureBits = 21;           // a border nearer than W 2^-21 to u W is not decided by these sums
+constexpr float kAboutError = 3.6e-7f;
+
+// How near to u W a border may lie and still be decided by single-precision sums (2.1e-8 + 1.46e-7 +
+// 1.8e-7 = 3.5e-7; the units' own rounding, some tens, is covered by the 1024).
+__device__ __forceinline__ uint64_t about_margin(float u, uint64_t all) {
+  return (uint64_t)(2.f * u * (1.f - u) * kAboutError * (float)all) + 1024;
+}
 
 __device__ __forceinline__ About about(const Exponent& e) {
   return {e.hi, e.lo, __fadd_rn(12582912.f, rintf(-e.max * e.hi))};  // 1.5 x 2^23 + bias
@@ -205,6 +213,19 @@ __device__ __forceinline__ float about_of(float x, const About& a) {
 }
 // A float's value (below 2^18 1.5) in units of 2^-45.
 __device__ __forceinline__ uint64_t about_units(float v) { return (uint64_t)(v * 35184372088832.f); }
+__device__ __forceinline__ uint64_t about_units(float s, float e) {
+  return about_units(s) + (uint64_t)(int64_t)(e * 35184372088832.f);
+}
+// 2^d of a whole number d, zero below 2^-126 and one above 2^0.
+__device__ __forceinline__ float power_of_two(float d) {
+  return d < -126.f ? 0.f : __uint_as_float((uint32_t)(127 + (int)fminf(d, 0.f)) << 23);
+}
+// v into a sum held in two floats.
+__device__ __forceinline__ void add_in_two(float v, float* s, float* e) {
+  const float t = __fadd_rn(*s, v), b = __fsub_rn(t, *s);
+  *e = __fadd_rn(*e, __fadd_rn(__fsub_rn(*s, __fsub_rn(t, b)), __fsub_rn(v, b)));
+  *s = t;
+}
 
 template <typename V>
 __device__ __forceinline__ V warp_add(V v) {
@@ -420,6 +441,14 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
       if (i + kAhead < iters) v[kAhead - 1] = fetch(warp, i + kAhead);
       g(x, first + i * kStep + lane * kVec);
     }
+  };
+  // f(x) for every element of this thread, its code once and not once per element of a granule: for
+  // passes that few rows take, whose instructions would otherwise come from memory each time
+  auto each_small = [&](auto&& f) {
+    each_granule([&](const float (&x)[kVec], int) {
+#pragma unroll 1
+      for (int k = 0; k < kVec; ++k) f(x[k]);
+    });
   };
   // f(x, place) for every element of this thread
   auto each = [&](auto&& f) {
@@ -725,7 +754,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
         int32_t all_l = 0, top_l = 0;
         each([&](float x, int) {
           const uint32_t k = order_key<E::kLowBits>(x);
-          if (k >= floor_key && x != -INFINITY) {
+          if (k >= floor_key && x != -INFINITY) {  // (few tokens, below a top-k cut)
             int32_t h, l;
             weight_of(x, ex, sm.table, &h, &l);
             if (k > floor_key) all_h += h, all_l += l;
@@ -775,7 +804,8 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
   const About ab = about(ex);
   const float x_zero = mx - kOctaves * 0.6931472f * temp;  // the single-precision sums leave out what lies below
   const float over_about = fmaxf(over, x_zero);  // (x_zero < mx where |max c| < kAboutMax)
-  auto draw = [&](bool exact) {
+  auto draw = [&](auto exactly) {
+    constexpr bool exact = decltype(exactly)::value;
     // a token's weight, if it is above the cut
     auto weight = [&](float x) -> uint64_t {
       if (exact) return x > over ? weight_units(x, ex, sm.table) : 0;
@@ -790,13 +820,12 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     if (exact) {
       uint32_t h = 0;
       int32_t l = 0;
-      each([&](float x, int) {
-        if (x > over) {
-          int32_t wh, wl;
-          weight_of(x, ex, sm.table, &wh, &wl);
-          h += wh, l += wl;
-        }
-        if (partial && x == cut_x) ++same;
+      each_small([&](float x) {
+        int32_t wh, wl;
+        weight_of(x, ex, sm.table, &wh, &wl);
+        h += x > over ? wh : 0;
+        l += x > over ? wl : 0;
+        same += partial && x == cut_x ? 1u : 0u;
       });
       sum = units(h, l);
     } else {
@@ -812,11 +841,9 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
         for (int o = kVec / 2; o > 0; o >>= 1)
 #pragma unroll
           for (int k = 0; k < o; ++k) w[k] = __fadd_rn(w[k], w[k + o]);
-        const float t = __fadd_rn(s, w[0]), b = __fsub_rn(t, s);
-        e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(w[0], b)));
-        s = t;
+        add_in_two(w[0], &s, &e);
       });
-      sum = about_units(s) + (uint64_t)(int64_t)(e * 35184372088832.f);
+      sum = about_units(s, e);
     }
     sum = warp_add(sum);
     same = warp_add(same);
@@ -855,7 +882,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
         values(fetch(w0, i), x);
         uint64_t m = 0;
         uint32_t n = 0;
-#pragma unroll
+#pragma unroll(exact ? 1 : kVec)
         for (int k = 0; k < kVec; ++k) m += weight(x[k]), n += partial && x[k] == cut_x ? 1u : 0u;
         m = warp_add(m);
         n = warp_add(n);
@@ -874,21 +901,21 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
         uint64_t m = 0, w[kVec];
         uint32_t n = 0;
         values(fetch(w0, i), x);
-#pragma unroll
+#pragma unroll(exact ? 1 : kVec)
         for (int k = 0; k < kVec; ++k) m += w[k] = weight(x[k]), n += partial && x[k] == cut_x ? 1u : 0u;
         uint32_t nth = ahead + warp_scan(n, lane) - n;
         uint64_t at = m + equals(nth, nth + n);
         const uint64_t mine = at;
         at = before + warp_scan(at, lane) - at;
         if (at <= goal && goal < at + mine) {
-#pragma unroll
+#pragma unroll 1
           for (int k = 0; k < kVec; ++k) {
             const bool eq = partial && x[k] == cut_x;
             const uint64_t own = eq ? equals(nth, nth + 1) : w[k];
             if (eq) ++nth;
             if (at <= goal && goal < at + own) {
               a.token[row] = (rank * kWarps + w0) * seg + i * kStep + lane * kVec + k - shift;
-              const uint64_t margin = all >> kSureBits;
+              const uint64_t margin = about_margin(u, all);
               if (goal - at >= margin && at + own - goal > margin) to_all(&Shared::sure, 1);
             }
             at += own;
@@ -900,10 +927,343 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
   };
   bool sure = false;
   if (fabsf(mx * ex.hi) < kAboutMax) {
-    draw(false);
+    draw(std::false_type{});
     sure = sm.sure != 0;
   }
-  if (!sure) draw(true);
+  if (!sure) draw(std::true_type{});
+}
+
+// A row that single-precision sums did not decide, until the exact ones have.
+constexpr int32_t kUndecided = INT32_MIN;
+
+// Temperature alone (no filter given): one pass over the row.  A thread sums its weights in single
+// precision (about_of) against a bias of its own, from its first logits, which powers of two bring to
+// the row's later; the token's run is read again, from L2.  A greedy row needs its maximum and place.
+// Rows that this does not decide (and rows with +inf, or of logits beyond about_of's range) are marked
+// for the launch after it.
+struct PlainShared {
+  float2 table[64];
+  uint64_t warp_u64[kWarps], chunk[kMaxChunks];
+  float warp_f[kWarps];
+  uint32_t marked[kWarps];
+  float exp_hi, exp_lo;
+  // read by the other CTAs of the cluster
+  uint64_t sum, best;
+  float x_max;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 3)
+sample_plain_kernel(const SampleArgs a, int iters) {
+  using E = Elems<T>;
+  constexpr int kVec = E::kVec;
+  constexpr int kStep = 32 * kVec;
+  __shared__ PlainShared sm;
+  grid_dependents_launch();
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t row = (int64_t)blockIdx.x / C;
+  const T* src = static_cast<const T*>(a.logits) + row * a.stride;
+  const int shift = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));
+  const T* base = src - shift;
+  const int end = a.vocab + shift, seg = iters * kStep;
+  const int first = (rank * kWarps + warp) * seg + lane * kVec;
+  auto granule = [&](int p) {
+    uint4 v;
+    if (p >= shift && p + kVec <= end) {
+      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                   : "l"(base + p));
+    } else {
+      float x[kVec];
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) x[k] = p + k >= shift && p + k < end ? E::one(base + p + k) : -INFINITY;
+      v = E::pack(x);
+    }
+    return v;
+  };
+  constexpr int kAhead = 3;
+  uint4 ahead[kAhead];
+#pragma unroll
+  for (int h = 0; h < kAhead; ++h)
+    if (h < iters) ahead[h] = granule(first + h * kStep);
+  const float temp = a.temperature ? __ldg(a.temperature + row) : 1.f;
+  const float u = __ldg(a.uniform + row);
+  const bool good = (temp == 0.f || (temp >= kSampleMinTemp && temp <= kSampleMaxTemp)) && u >= 0.f && u <= 1.f;
+  if (!good) {  // the same in every thread of the cluster
+    if (rank == 0 && tid == 0) {
+      record_status(a.status, VMLA_ERR_PARAM, (uint32_t)row);
+      a.token[row] = -1;
+    }
+    return;
+  }
+  const bool greedy = temp == 0.f;
+  if (tid == 0 && !greedy) {
+    const double c = 1.4426950408889634 / (double)temp;
+    sm.exp_hi = (float)c;
+    sm.exp_lo = (float)(c - (double)sm.exp_hi);
+  }
+  __syncthreads();
+  About ab;
+  ab.hi = greedy ? 0.f : sm.exp_hi, ab.lo = greedy ? 0.f : sm.exp_lo, ab.magic = 12582912.f;
+  float mx = -INFINITY, s = 0.f, e = 0.f, low = 0.f, high = -INFINITY;
+  int at = 0;  // iteration of the first granule with this thread's maximum
+#pragma unroll 1
+  for (int i = 0; i < iters; ++i) {
+    float x[kVec];
+    E::unpack(ahead[0], x);
+#pragma unroll
+    for (int h = 0; h + 1 < kAhead; ++h) ahead[h] = ahead[h + 1];
+    if (i + kAhead < iters) ahead[kAhead - 1] = granule(first + (i + kAhead) * kStep);
+    float g = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) g = fmaxf(g, x[k]);
+    if (g > mx) mx = g, at = i;
+    if (!greedy) {
+      if (g > high && fabsf(g * ab.hi) < kAboutMax) {
+        // a bias for this thread's first numbers, or for weights over 2^64 times what it is for
+        const float magic = __fadd_rn(12582912.f, rintf(-g * ab.hi));
+        const float by = power_of_two(magic - ab.magic);  // (at the first, of a sum of zero)
+        s *= by, e *= by;
+        ab.magic = magic;
+        high = g + 64.f / ab.hi;
+        low = g - 100.f / ab.hi;
+      }
+      float w[kVec];
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) w[k] = about_of(fmaxf(x[k], low), ab);  // NaN and what lies 2^-100 below: next to nothing
+#pragma unroll
+      for (int o = kVec / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < o; ++k) w[k] = __fadd_rn(w[k], w[k + o]);
+      if (high > -INFINITY) add_in_two(w[0], &s, &e);
+    }
+  }
+  const float own_max = mx;
+  mx = warp_max(mx);
+  if (lane == 0) sm.warp_f[warp] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm.warp_f[w]);
+  if (greedy) {
+    // the first place of the largest value: its thread reads the granule again
+    uint64_t best = 0;
+    if (own_max == mx && mx > -INFINITY) {
+      float x[kVec];
+      E::unpack(granule(first + at * kStep), x);
+      int place = 0;
+#pragma unroll
+      for (int k = kVec - 1; k >= 0; --k) place = x[k] == mx ? first + at * kStep + k : place;
+      best = ((uint64_t)order_key<0>(mx) << 32) | (uint32_t)~place;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+    if (lane == 0) sm.warp_u64[warp] = best;
+    __syncthreads();
+    if (tid == 0) {
+      for (int w = 0; w < kWarps; ++w) best = max(best, sm.warp_u64[w]);
+      sm.best = best;
+    }
+    cluster.sync();
+    if (rank == 0 && tid == 0) {
+      for (int r = 0; r < C; ++r) best = max(best, *cluster.map_shared_rank(&sm.best, r));
+      a.token[row] = best == 0 ? -1 : (int32_t)~(uint32_t)best - shift;
+    }
+    cluster.sync();
+    return;
+  }
+  // this thread's sum at the CTA's bias, and the CTA's at its own
+  const float magic = __fadd_rn(12582912.f, rintf(-mx * ab.hi));
+  uint64_t sum = 0;
+  if (high > -INFINITY && fabsf(mx * ab.hi) < kAboutMax) {
+    const float by = power_of_two(magic - ab.magic);
+    sum = about_units(s * by, e * by);
+  }
+  sum = warp_add(sum);
+  if (lane == 0) sm.warp_u64[warp] = sum;
+  __syncthreads();
+  if (tid == 0) {
+    sum = 0;
+    for (int w = 0; w < kWarps; ++w) sum += sm.warp_u64[w];
+    sm.sum = sum;
+    sm.x_max = mx;
+  }
+  cluster.sync();
+  const float cta_max = mx;
+  for (int r = 0; r < C; ++r) mx = fmaxf(mx, *cluster.map_shared_rank(&sm.x_max, r));
+  if (!(mx > -INFINITY && fabsf(mx * ab.hi) < kAboutMax)) {
+    if (rank == 0 && tid == 0) a.token[row] = mx == -INFINITY ? -1 : kUndecided;
+    cluster.sync();
+    return;
+  }
+  // everything at the row's bias: a CTA's units by a power of two
+  const Exponent ex = {mx, ab.hi, ab.lo};
+  ab = about(ex);
+  auto shift_of = [&](float m) {
+    const float d = m > -INFINITY ? rintf(-m * ab.hi) - rintf(-mx * ab.hi) : 63.f;
+    return (int)fminf(fmaxf(d, 0.f), 63.f);
+  };
+  uint64_t all = 0, before = 0, here = 0;
+  for (int r = 0; r < C; ++r) {
+    const uint64_t m = *cluster.map_shared_rank(&sm.sum, r) >> shift_of(*cluster.map_shared_rank(&sm.x_max, r));
+    if (r == rank) before = all, here = m;
+    all += m;
+  }
+  const uint64_t goal = u < 1.f ? __umul64hi((uint64_t)(u * 18446744073709551616.f), all) : all - 1;
+  if (before <= goal && goal < before + here) {  // one CTA of the cluster
+    const int down = shift_of(cta_max);
+    const float x_zero = mx - kOctaves * 0.6931472f * temp;
+    auto weight = [&](float x) -> uint64_t { return x > x_zero ? about_units(about_of(x, ab)) : 0; };
+    int w0 = 0;
+    for (; w0 < kWarps - 1; ++w0) {
+      const uint64_t m = sm.warp_u64[w0] >> down;
+      if (goal < before + m) break;
+      before += m;
+    }
+    const int start = (rank * kWarps + w0) * seg + lane * kVec;
+    for (int i = warp; i < iters; i += kWarps) {
+      float x[kVec];
+      E::unpack(granule(start + i * kStep), x);
+      uint64_t m = 0;
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) m += weight(x[k]);
+      m = warp_add(m);
+      if (lane == 0) sm.chunk[i] = m;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      int i = 0;
+      for (; i < iters - 1 && before + sm.chunk[i] <= goal; ++i) before += sm.chunk[i];
+      float x[kVec];
+      uint64_t m = 0, w[kVec];
+      E::unpack(granule(start + i * kStep), x);
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) m += w[k] = weight(x[k]);
+      uint64_t upto = before + warp_scan(m, lane) - m;
+      // the token, or a mark where no sum, or one next to the goal, decides
+      const uint64_t margin = about_margin(u, all);
+      int token = kUndecided;
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) {
+        if (goal >= upto + margin && upto + w[k] > goal + margin) token = start + i * kStep + k - shift;
+        upto += w[k];
+      }
+      const uint32_t found = __ballot_sync(0xffffffffu, token != kUndecided);
+      if (found ? lane == __ffs(found) - 1 : lane == 0) a.token[row] = token;
+    }
+  }
+  cluster.sync();  // no CTA leaves while another reads its shared memory
+}
+
+// The rows that the launch before left undecided, by exact sums: cluster c takes rows c, c + (clusters),
+// and so on.  (Loops over a granule's elements are rolled: few rows come here, and the time of their
+// instructions' first fetch would outweigh that of running them.)
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2)
+sample_plain_exact_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, int iters) {
+  using E = Elems<T>;
+  constexpr int kVec = E::kVec;
+  constexpr int kStep = 32 * kVec;
+  __shared__ PlainShared sm;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t clusters = gridDim.x / C;
+  if (tid < 64) sm.table[tid] = exp_table.t[tid];
+  grid_dependency_wait();
+  for (int64_t first_row = blockIdx.x / C; first_row < a.rows; first_row += clusters * kThreads) {
+    // the marks of the next kThreads of this cluster's rows, read by every CTA before one is cleared
+    const int64_t my_row = first_row + tid * clusters;
+    const bool mark = my_row < a.rows && *reinterpret_cast<volatile int32_t*>(a.token + my_row) == kUndecided;
+    const uint32_t word = __ballot_sync(0xffffffffu, mark);
+    __syncthreads();
+    if (lane == 0) sm.marked[warp] = word;
+    cluster.sync();
+    for (int mw = 0; mw < kWarps; ++mw) {
+      for (uint32_t left = sm.marked[mw]; left != 0; left &= left - 1) {
+        const int64_t row = first_row + (32 * mw + __ffs(left) - 1) * clusters;
+        const T* src = static_cast<const T*>(a.logits) + row * a.stride;
+        const int shift = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));
+        const int seg = iters * kStep;
+        // the logit at a place, -inf outside the row
+        auto logit = [&](int p) {
+          return p >= shift && p < a.vocab + shift ? fmaxf(E::one(src - shift + p), -INFINITY) : -INFINITY;
+        };
+        const int first = (rank * kWarps + warp) * seg + lane * kVec;
+        float mx = -INFINITY;
+        for (int i = 0; i < iters; ++i)
+#pragma unroll
+          for (int k = 0; k < kVec; ++k) mx = fmaxf(mx, logit(first + i * kStep + k));
+        mx = warp_max(mx);
+        if (lane == 0) sm.warp_f[warp] = mx;
+        const float temp = a.temperature ? __ldg(a.temperature + row) : 1.f, u = __ldg(a.uniform + row);
+        if (tid == 0) {
+          const double c = 1.4426950408889634 / (double)temp;
+          sm.exp_hi = (float)c;
+          sm.exp_lo = (float)(c - (double)sm.exp_hi);
+        }
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm.warp_f[w]);
+        if (tid == 0) sm.x_max = mx;
+        cluster.sync();
+        for (int r = 0; r < C; ++r) mx = fmaxf(mx, *cluster.map_shared_rank(&sm.x_max, r));
+        const bool only_inf = mx == INFINITY;  // tokens at +inf share the draw evenly
+        const Exponent ex = {only_inf ? 0.f : mx, sm.exp_hi, sm.exp_lo};
+        auto weight = [&](int p) {
+          const float x = logit(p);
+          return weight_units(!only_inf ? x : x == INFINITY ? 0.f : -INFINITY, ex, sm.table);
+        };
+        uint64_t sum = 0;
+        for (int i = 0; i < iters; ++i)
+#pragma unroll 2
+          for (int k = 0; k < kVec; ++k) sum += weight(first + i * kStep + k);
+        sum = warp_add(sum);
+        if (lane == 0) sm.warp_u64[warp] = sum;
+        __syncthreads();
+        if (tid == 0) {
+          sum = 0;
+          for (int w = 0; w < kWarps; ++w) sum += sm.warp_u64[w];
+          sm.sum = sum;
+        }
+        cluster.sync();
+        uint64_t all = 0, before = 0, here = 0;
+        for (int r = 0; r < C; ++r) {
+          const uint64_t m = *cluster.map_shared_rank(&sm.sum, r);
+          if (r == rank) before = all, here = m;
+          all += m;
+        }
+        const uint64_t goal = u < 1.f ? __umul64hi((uint64_t)(u * 18446744073709551616.f), all) : all - 1;
+        if (before <= goal && goal < before + here) {
+          int w0 = 0;
+          for (; w0 < kWarps - 1 && before + sm.warp_u64[w0] <= goal; ++w0) before += sm.warp_u64[w0];
+          const int start = (rank * kWarps + w0) * seg + lane * kVec;
+          for (int i = warp; i < iters; i += kWarps) {
+            uint64_t m = 0;
+#pragma unroll 1
+            for (int k = 0; k < kVec; ++k) m += weight(start + i * kStep + k);
+            m = warp_add(m);
+            if (lane == 0) sm.chunk[i] = m;
+          }
+          __syncthreads();
+          if (warp == 0) {
+            int i = 0;
+            for (; i < iters - 1 && before + sm.chunk[i] <= goal; ++i) before += sm.chunk[i];
+            uint64_t m = 0;
+#pragma unroll 1
+            for (int k = 0; k < kVec; ++k) m += weight(start + i * kStep + k);
+            uint64_t upto = before + warp_scan(m, lane) - m;
+            if (upto <= goal && goal < upto + m) {
+              int k = 0;
+              for (uint64_t w; k < kVec - 1 && upto + (w = weight(start + i * kStep + k)) <= goal; ++k) upto += w;
+              a.token[row] = start + i * kStep + k - shift;
+            }
+          }
+        }
+        cluster.sync();  // every CTA has read the others' sums; this row's shared memory may be written again
+      }
+    }
+  }
 }
 
 // CTAs per row: up to four while they find room on the SMs (two on each, and as many waiting), eight
@@ -918,13 +1278,15 @@ struct Shape {
   bool keep;
 };
 template <typename T>
-Shape choose_shape(const SampleArgs& a, int sms) {
+int iterations(const SampleArgs& a, int cluster) {
   const bool aligned = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && a.stride * sizeof(T) % 16 == 0;
   const int64_t places = (int64_t)a.vocab + (aligned ? 0 : Elems<T>::kVec - 1);
-  auto need = [&](int c) {
-    const int64_t per = (int64_t)c * (kChunkBytes / sizeof(T));
-    return (int)((places + per - 1) / per);
-  };
+  const int64_t per = (int64_t)cluster * (kChunkBytes / sizeof(T));
+  return (int)((places + per - 1) / per);
+}
+template <typename T>
+Shape choose_shape(const SampleArgs& a, int sms) {
+  auto need = [&](int c) { return iterations<T>(a, c); };
   Shape s;
   s.cluster = 1;
   while (s.cluster < kMaxCluster && need(s.cluster) > 1 &&
@@ -934,6 +1296,31 @@ Shape choose_shape(const SampleArgs& a, int sms) {
   while (s.cluster < kMaxCluster && need(s.cluster) > kMaxElems / Elems<T>::kVec) s.cluster *= 2;
   s.iters = need(s.cluster);
   return s;
+}
+// Without filters a row costs less and needs no shared memory: TODO
+template <typename T>
+Shape choose_plain_shape(const SampleArgs& a, int sms) {
+  Shape s = choose_shape<T>(a, sms);
+  s.keep = false;
+  return s;
+}
+
+template <typename... Params, typename... Args>
+bool launch_clusters(void (*kernel)(Params...), int64_t rows, int cluster, size_t smem, bool early, cudaStream_t stream,
+                     const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1] = early_start_attribute();
+  cfg.gridDim = dim3((unsigned)(rows * cluster), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = early ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
 template <typename T>
@@ -947,14 +1334,25 @@ int launch(const SampleArgs& a, int sms, int dev, cudaStream_t stream) {
     }
     return t;
   }();
-  const Shape shape = choose_shape<T>(a, sms);
+  const bool plain = !a.top_k && !a.top_p && !a.min_p;
+  const Shape shape = plain ? choose_plain_shape<T>(a, sms) : choose_shape<T>(a, sms);
   if (shape.iters > kMaxElems / Elems<T>::kVec || a.rows * shape.cluster > INT32_MAX) return VMLA_ERR_SHAPE;
+  if (plain) {
+    // then its undecided rows, on clusters of eight that are all resident (two CTAs on an SM, and some
+    // SMs of a GPC left over)
+    const int64_t room = sms / 5 > 0 ? sms / 5 : 1, clusters = a.rows < room ? a.rows : room;
+    if (!launch_clusters(sample_plain_kernel<T>, a.rows, shape.cluster, 0, false, stream, a, shape.iters) ||
+        !launch_clusters(sample_plain_exact_kernel<T>, clusters, kMaxCluster, 0, true, stream, a, table,
+                         iterations<T>(a, kMaxCluster)))
+      return VMLA_ERR_CUDA;
+    return VMLA_OK;
+  }
   if (shape.keep) {
     static bool ready[64] = {};
     static std::mutex mu;
     std::lock_guard<std::mutex> g(mu);
+    // (all of the SM's memory as shared memory, so that two CTAs fit)
     if (dev >= 64 || !ready[dev]) {
-      // (all of the SM's memory as shared memory: the default split left room for one CTA)
       if (cudaFuncSetAttribute(sample_kernel<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                kKeepIters * kChunkBytes) != cudaSuccess ||
           cudaFuncSetAttribute(sample_kernel<T, true>, cudaFuncAttributePreferredSharedMemoryCarveout,
@@ -963,19 +1361,10 @@ int launch(const SampleArgs& a, int sms, int dev, cudaStream_t stream) {
       if (dev < 64) ready[dev] = true;
     }
   }
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)shape.cluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)(a.rows * shape.cluster), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = shape.keep ? (size_t)shape.iters * kChunkBytes : 0;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   const auto kernel = shape.keep ? sample_kernel<T, true> : sample_kernel<T, false>;
-  return cudaLaunchKernelEx(&cfg, kernel, a, table, shape.iters) == cudaSuccess ? VMLA_OK : VMLA_ERR_CUDA;
+  const size_t smem = shape.keep ? (size_t)shape.iters * kChunkBytes : 0;
+  if (!launch_clusters(kernel, a.rows, shape.cluster, smem, false, stream, a, table, shape.iters)) return VMLA_ERR_CUDA;
+  return VMLA_OK;
 }
 
 }  // namespace

@@ -202,6 +202,38 @@ def test_far_logits_and_temperatures(fp32):
         assert np.array_equal(draw(x, u, fp32, **k), reference(host(x, fp32), u, **k)), on
 
 
+@pytest.mark.parametrize("fp32", [False, True])
+def test_rising_and_falling_rows(fp32):
+    """Rows whose values rise or fall by hundreds along the way (weights of 2^1000 to the first ones), and rows
+    that start with forbidden tokens or with values far below all others."""
+    rng = np.random.default_rng(11)
+    R, V = 24, 40000
+    x = logits(rng, R, V)
+    ramp = np.linspace(0, 3000, V)
+    x[:4] += ramp
+    x[4:8] -= ramp
+    x[8:12] += 400.0 * (np.arange(V) // 5000)
+    x[12:16, :30000] = -np.inf
+    x[16:20, :30000] = -1e30 if fp32 else -3.3e38
+    x[20:22, 100:] = np.nan
+    u = rng.random(R).astype(np.float32)
+    for temp in (None, np.full(R, 0.7, np.float32), np.exp2(rng.uniform(-9, 9, R)).astype(np.float32), np.zeros(R, np.float32)):
+        k = {} if temp is None else {"temp": temp}
+        assert np.array_equal(draw(x, u, fp32, **k), reference(host(x, fp32), u, **k))
+
+
+@pytest.mark.parametrize("rows", [63, 64, 200])
+def test_undecided_rows_of_flat_logits(rows):
+    """131,072 nearly equal weights: single-precision sums leave one row of ten to exact ones."""
+    rng = np.random.default_rng(rows)
+    x = rng.normal(0, 0.01, (rows, 131072))
+    u = rng.random(rows).astype(np.float32)
+    assert np.array_equal(draw(x, u, True), reference(host(x, True), u))
+    s = settings(rng, rows, 131072)
+    k = {n: s[n] for n in ("temp", "top_p")}
+    assert np.array_equal(draw(x, u, False, **k), reference(host(x, False), u, **k))
+
+
 def test_settings_at_their_ends():
     rng = np.random.default_rng(6)
     R, V = 16, 6000
