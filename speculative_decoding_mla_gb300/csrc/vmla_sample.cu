@@ -25,6 +25,8 @@
 //   bf16: a bin holds one value (but for the bin of the values next to zero), so
 //      the masses are counts times exact weights of some thousand values, and the
 //      histogram alone gives both cuts exactly;
+//   few tokens: where top-k's bins hold at most 1024 tokens (or the vocabulary does)
+//      one CTA sorts them and does the rest: order, masses, cuts and draw;
 //   fp32: counts give top-k's bin, bounds of each bin's mass bracket top-p's; one
 //      pass adds the exact masses of all tokens and of those above the bracket;
 //      inside a bin or bracket, histograms over 1024 equal ranges of the values'
@@ -58,9 +60,11 @@ constexpr float kOctaves = 46.f;             // weights below 2^-kOctaves count 
 constexpr int kNearZero = 0x3A80;            // leading 16 bits of 2^-10: smaller values share one bin
 constexpr int kBins = 18 * kThreads;         // 9216: see bin_of
 constexpr int kRanges = 1024;                // of the bit-pattern histograms
+constexpr int kList = 2 * kThreads;          // tokens that one CTA sorts
 constexpr int kUnitBits = 45;                // weights in units of 2^-45: 2^18 tokens' sum stays below 2^63
 static_assert((int64_t)VMLA_MAX_VOCAB << kUnitBits <= INT64_MAX, "sums of weights fit 63 bits");
 static_assert((int64_t)kMaxCluster * kThreads * kMaxElems >= VMLA_MAX_VOCAB + 7, "every vocabulary fits");
+static_assert(kChunkBytes / 4 >= kList + 3, "one iteration of one CTA holds a list's worth of logits");
 static_assert((int64_t)kMaxElems << 23 < (1ll << 32) && kKeepIters * 8 <= kMaxElems, "a thread's sum of high parts fits 32 bits");
 
 // 2^(k/64) as a pair of floats, filled by the host.
@@ -74,6 +78,9 @@ struct Shared {
     struct {
       uint32_t count[kRanges], mass_lo[kRanges], mass_hi[kRanges];
     } r;
+    struct {
+      uint64_t key[kList], weight[kList], by_place[kList], spare[kList];
+    } list;
   };
   float2 table[64];
   uint64_t warp_u64[kWarps], warp_u64b[kWarps];
@@ -90,9 +97,10 @@ struct Shared {
   int32_t index;
   // written by the one thread of the cluster that finds them, into every CTA
   int32_t bin_k, bin_p, bracket_lo, bracket_hi, sure;
-  uint32_t bin_k_rank, bin_p_count;
+  uint32_t bin_k_rank, bin_k_count, bin_p_count;
   uint64_t bin_p_left;
   // results of a search, the same in every CTA
+  uint32_t listed;         // (in the first CTA) tokens in its list
   int32_t range;
   uint32_t range_count;
   uint64_t range_before;
@@ -321,6 +329,101 @@ struct Elems<uint16_t> {  // bf16
   }
 };
 
+// Descending order of these keys is that of the tokens: by value, then by place.
+__device__ __forceinline__ uint64_t sort_key(float x, int place) {
+  return ((uint64_t)order_key<0>(x) << 32) | (uint32_t)~place;
+}
+
+// keys[0, n), n a power of two from 64 to kList, in descending order (a permutation: equal keys by their
+// place).  Up to 256 keys each one's rank is counted, by 2 to 8 threads, into `spare`; more are sorted in
+// place by exchanges (45 or 55 block-wide steps).  Returns the array that holds them.
+__device__ __forceinline__ uint64_t* in_descending_order(uint64_t* keys, uint64_t* spare, int n) {
+  const int t = threadIdx.x;
+  __syncthreads();
+  if (n <= kThreads / 2) {
+    const int group = kThreads / n, e = t / group, part = t % group;
+    const uint64_t mine = keys[e];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = part; j < n; j += group) {
+      const uint64_t other = keys[j];
+      rank += other > mine || (other == mine && j < e) ? 1 : 0;
+    }
+    for (int o = group >> 1; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (part == 0) spare[rank] = mine;
+    __syncthreads();
+    return spare;
+  }
+  for (int run = 2; run <= n; run <<= 1) {
+    for (int gap = run >> 1; gap > 0; gap >>= 1) {
+      if (t < n >> 1) {
+        const int i = 2 * t - (t & (gap - 1)), j = i + gap;
+        const uint64_t x = keys[i], y = keys[j];
+        if ((x < y) == ((i & run) == 0)) keys[i] = y, keys[j] = x;
+      }
+      __syncthreads();
+    }
+  }
+  return keys;
+}
+
+// The place of the token drawn from the `listed` tokens of sm.list, which hold the row's top-k first
+// ones: in their order exact weights, whose running sums give top-p's cut; then by place, for the draw.
+__device__ __noinline__ int draw_listed(Shared& sm, const Exponent& ex, uint32_t listed, uint32_t top_k, bool with_p,
+                                        uint64_t p64, float min_p, float u) {
+  const int tid = threadIdx.x;
+  int n = 64;
+  while (n < (int)listed) n <<= 1;
+  for (int i = listed + tid; i < n; i += kThreads) sm.list.key[i] = 0;
+  const uint64_t* order = in_descending_order(sm.list.key, sm.list.spare, n);
+  const float least = min_p > 0.f ? __double2float_ru((double)ex.max + sm.min_p_offset) : -INFINITY;
+  // this thread's two tokens of the order
+  float x[2];
+  uint64_t w[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t i = 2 * tid + j;
+    const bool in = i < listed && i < top_k;
+    x[j] = in ? order_value<0>((uint32_t)(order[i] >> 32)) : -INFINITY;
+    w[j] = weight_units(x[j], ex, sm.table);
+  }
+  uint64_t all;
+  const uint64_t before = block_scan(w[0] + w[1], sm.warp_u64, &all);
+  // (the token itself is kept while the mass ahead of it does not reach p of all)
+  const uint64_t reach = with_p ? __umul64hi(p64, all) + (p64 * all != 0 ? 1 : 0) : ~0ull;
+  uint64_t at = before;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t i = 2 * tid + j;
+    const bool kept = w[j] > 0 && x[j] >= least && (at < reach || i == 0);
+    at += w[j];
+    if (!kept) w[j] = 0;
+    if (i < (uint32_t)n) {
+      // places ascend as these keys descend; a token left out comes last
+      sm.list.by_place[i] = kept ? (order[i] << 32) | i : 0;
+      sm.list.weight[i] = w[j];
+    }
+  }
+  // (with few keys `order` is the spare array, and the first one is free)
+  const uint64_t* places = in_descending_order(sm.list.by_place, sm.list.key, n);
+  uint64_t key[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int i = 2 * tid + j;
+    key[j] = i < n ? places[i] : 0;
+    w[j] = key[j] ? sm.list.weight[(uint32_t)key[j]] : 0;
+  }
+  at = block_scan(w[0] + w[1], sm.warp_u64, &all);
+  const uint64_t goal = u < 1.f ? __umul64hi((uint64_t)(u * 18446744073709551616.f), all) : all - 1;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    if (at <= goal && goal < at + w[j]) sm.index = (int)~(uint32_t)(key[j] >> 32);
+    at += w[j];
+  }
+  __syncthreads();
+  return sm.index;
+}
+
 // One row on one cluster.  Element v of the "shifted" row is token v - shift, shift being the
 // elements between the row's start and the 16-byte boundary below it, so that whole granules load
 // as vectors whatever the row's alignment; places outside the row read as -inf.  CTA r takes
@@ -414,7 +517,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     }
   }
   float mx = E::largest(run);
-  if (tid == 0) sm.sure = 0;  // (set from another CTA only past the barriers below)
+  if (tid == 0) sm.sure = 0, sm.listed = 0;  // (written from other CTAs only past the barriers below)
   if (tid < 64) sm.table[tid] = exp_table.t[tid];
   mx = warp_max(mx);
   if (lane == 0) sm.warp_f[warp] = mx;
@@ -492,6 +595,17 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
   uint32_t cut_keep = kAllEqual;
   bool with_k = top_k > 0 && top_k < a.vocab;
   const bool with_p = top_p < 1.f;
+  const uint64_t p64 = (uint64_t)(top_p * 18446744073709551616.f);  // p 2^64: whole for p >= 2^-40
+  if ((with_k || with_p) && a.vocab <= kList) {
+    // the whole row goes into a list (of one CTA: its cluster has no other)
+    each([&](float x, int p) {
+      if (x > -INFINITY) sm.list.key[atomicAdd(&sm.listed, 1u) % kList] = sort_key(x, p);
+    });
+    __syncthreads();
+    const int place = draw_listed(sm, ex, sm.listed, with_k ? (uint32_t)top_k : kList, with_p, p64, min_p, u);
+    if (tid == 0) a.token[row] = place - shift;
+    return;
+  }
   if (with_k || with_p) {
     const int top_number = number_of(mx);
     // tokens of weight lie above
@@ -633,6 +747,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
         if (at < (uint32_t)top_k && at + n >= (uint32_t)top_k) {  // one bin of the cluster
           to_all(&Shared::bin_k, bin0 + j);
           to_all(&Shared::bin_k_rank, (uint32_t)top_k - at);
+          to_all(&Shared::bin_k_count, n);
         }
         at += n;
       }
@@ -641,11 +756,28 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     // top-k leaves the bins up to bin_k, of that one the first k_rank tokens
     const int bin_k = with_k ? sm.bin_k : bins - 1;
     const uint32_t k_rank = with_k ? sm.bin_k_rank : UINT32_MAX;
-    const uint64_t p64 = (uint64_t)(top_p * 18446744073709551616.f);  // p 2^64: whole for p >= 2^-40
     auto least_mass = [&](uint64_t all) {
       return max((uint64_t)__umul64hi(p64, all) + (p64 * all != 0 ? 1 : 0), (uint64_t)1);
     };
 
+    const uint32_t top_listed = with_k ? (uint32_t)top_k - k_rank + sm.bin_k_count : UINT32_MAX;
+    if (top_listed <= kList) {
+      // Few tokens are in the bins that hold top-k's: they go into the first CTA's list (where its
+      // histogram was: all have read it), and that CTA does the rest by sorting them.
+      uint32_t klo, khi;
+      bin_keys(bin_k, bin_k, &klo, &khi);
+      const float least = order_value<E::kLowBits>(klo);
+      Shared* to = cluster.map_shared_rank(&sm, 0);
+      each([&](float x, int p) {
+        if (x >= least) to->list.key[atomicAdd(&to->listed, 1u) % kList] = sort_key(x, p);
+      });
+      cluster.sync();
+      if (rank == 0) {
+        const int place = draw_listed(sm, ex, top_listed, (uint32_t)top_k, with_p, p64, min_p, u);
+        if (tid == 0) a.token[row] = place - shift;
+      }
+      return;
+    }
     bool found = false;
     if (E::kLowBits && !(with_k && bin_k == tiny_bin)) {
       // bf16: bins are values
@@ -1266,13 +1398,14 @@ sample_plain_exact_kernel(const SampleArgs a, const __grid_constant__ ExpTable e
   }
 }
 
-// CTAs per row: up to four while they find room on the SMs (two on each, and as many waiting), eight
-// while that leaves SMs idle, and more while one CTA's share of a row is over 20 iterations (160 KB);
-// the row stays in shared memory where that takes 64 KB of each.  Measured, us by cluster size 1 / 2 / 4 /
-// 8 (kept where marked *): 512 rows of 131,072 bf16 154 / 126 / 128* / 188*, 150 rows 93 / 62 / 51* / 63*,
-// 16 rows 54 / 34 / 21* / 18*; with top-p, 64 rows 102 / 64 / 44* / 53*; 151,001 fp32, 128 rows - / 199 /
-// 175 / 278, 16 rows - / 120 / 80 / 73; 400 rows of 32,000 bf16 50* / 65* / 100* / 181*, without keeping
-// them 59 / 75 / 114 / 204.
+// CTAs per row: more while all of them are resident (two on each SM), up to four while as many wait if a
+// CTA's share of a row is over eight iterations (64 KB), eight only while that leaves SMs idle, and more
+// while a share is over 20 iterations; the row stays in shared memory where a share is at most 64 KB.
+// Measured, us by cluster size 1 / 2 / 4 / 8 (kept where marked *), without filters by the general kernel:
+// 512 rows of 131,072 bf16 154 / 126 / 128* / 188*, 150 rows 93 / 62 / 51* / 63*, 16 rows 54 / 34 / 21* /
+// 18*; with top-p, 512 rows 198 / 200 / 222* / 352*, 64 rows 102 / 64 / 44* / 53*; all filters, 151,001
+// fp32, 128 rows - / 199 / 175 / 278, 16 rows - / 120 / 80 / 73; all filters, 32,000 bf16, 400 rows 50* / 65* /
+// 100* / 181* (not kept 59 / 75 / 114 / 204), 100 rows 31* / 28* / 33* / 47*.
 struct Shape {
   int cluster, iters;
   bool keep;
@@ -1288,19 +1421,31 @@ template <typename T>
 Shape choose_shape(const SampleArgs& a, int sms) {
   auto need = [&](int c) { return iterations<T>(a, c); };
   Shape s;
-  s.cluster = 1;
+  s.cluster = 1;  // (a vocabulary of up to kList tokens stays in one CTA: one iteration holds it)
   while (s.cluster < kMaxCluster && need(s.cluster) > 1 &&
-         (a.rows * s.cluster * 2 <= (s.cluster < 4 ? 4 : 1) * sms || need(s.cluster) > 20))
+         (a.rows * s.cluster * 2 <= (s.cluster == 4 ? 1 : need(s.cluster) > kKeepIters ? 4 : 2) * sms ||
+          need(s.cluster) > 20))
     s.cluster *= 2;
   s.keep = need(s.cluster) <= kKeepIters;
   while (s.cluster < kMaxCluster && need(s.cluster) > kMaxElems / Elems<T>::kVec) s.cluster *= 2;
   s.iters = need(s.cluster);
   return s;
 }
-// Without filters a row costs less and needs no shared memory: TODO
+// Without filters a CTA does one pass and two more barriers: more CTAs per row pay off only while all are
+// resident (three on an SM).  Us by cluster size 1 / 2 / 4 / 8, both launches: 512 rows of 131,072 bf16
+// 124 / 120 / 133 / 177 (before the second launch's kernel was its own), 150 rows 58 / 52 / 57 / 68, 64 rows
+// 54 / 46 / 43 / 49, one row 26 / 19 / 15 / 13; 400 rows of 32,000 35 / 41 / 52 / 89; 128 rows of 151,001 fp32
+// - / 64 / 71 / 75.
 template <typename T>
 Shape choose_plain_shape(const SampleArgs& a, int sms) {
-  Shape s = choose_shape<T>(a, sms);
+  auto need = [&](int c) { return iterations<T>(a, c); };
+  Shape s;
+  s.cluster = 1;
+  while (s.cluster < kMaxCluster && need(s.cluster) > 1 &&
+         (a.rows * s.cluster * 2 <= 2 * sms || need(s.cluster) > 20 ||
+          need(s.cluster) > kMaxElems / Elems<T>::kVec))
+    s.cluster *= 2;
+  s.iters = need(s.cluster);
   s.keep = false;
   return s;
 }
