@@ -123,8 +123,7 @@ __device__ __forceinline__ float order_value(uint32_t key) {
 // Signed number of a value's leading 16 bits, not decreasing in the value: 0 next to zero, then one
 // step per pattern.  The bin of a value is the number of the row's maximum less its own.  A weight of at
 // least 2^-46 means a value within 46 ln 2 T < 2^25 of the maximum, T being at most 2^20, and that
-// window holds at most 2 (25 + 10) 128 + 1 numbers (when zero is in its middle), so bins from
-// kBins - 1 on hold only what counts as zero.
+// window holds at most 2 (25 + 10) 128 + 1 numbers (when zero is in its middle).
 __device__ __forceinline__ int number_of(float x) {
   const uint32_t b = __float_as_uint(x);
   const int n = max((int)((b & 0x7FFFFFFFu) >> 16) - (kNearZero - 1), 0);
@@ -135,7 +134,49 @@ __device__ __forceinline__ float number_value(int n) {
   const uint32_t b = (uint32_t)((n < 0 ? -n : n) + (kNearZero - 1)) << 16;
   return __uint_as_float(n < 0 ? b | 0x80000000u : b);
 }
-static_assert(2 * (25 + 10) * 128 + 1 < kBins - 1, "every token of weight has a bin");
+constexpr int kLastBins = 32;  // what counts as zero is thrown into these, one for each lane
+static_assert(2 * (25 + 10) * 128 + 1 <= kBins - kLastBins, "every token of weight has a bin");
+
+__device__ __forceinline__ uint32_t add2(uint32_t a, uint32_t b) {  // 16-bit halves
+  uint32_t r;
+  asm("add.s16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Bins of a granule's values, top being the number of the row's maximum and last this lane's bin for
+// what counts as zero; whether one of them is next to zero.
+__device__ __forceinline__ bool bins_of(const float (&x)[4], const uint4&, int top, int last, uint32_t (&bin)[4]) {
+  bool near = false;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int n = number_of(x[k]);
+    bin[k] = (uint32_t)min(top - n, last);
+    near |= n == 0;
+  }
+  return near;
+}
+// bf16: two at a time in 16-bit halves.  With d = max(magnitude bits - (kNearZero - 1), 0) and m = -1 where
+// the sign is set, the number is (d ^ m) - m, so the bin is top + m + 1 + ~(d ^ m) (all modulo 2^16: a
+// bin is below 2 x 17,666).
+__device__ __forceinline__ bool bins_of(const float (&)[8], const uint4& v, int top, int last, uint32_t (&bin)[8]) {
+  const uint32_t top1 = ((uint32_t)(top + 1) & 0xFFFFu) * 0x10001u, last2 = (uint32_t)last * 0x10001u;
+  constexpr uint32_t kFrom = ((uint32_t)(-(kNearZero - 1)) & 0xFFFFu) * 0x10001u;
+  const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+  uint32_t zero_halves = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t d = add2(word[k] & 0x7FFF7FFFu, kFrom), b;
+    asm("max.s16x2 %0, %1, %2;" : "=r"(d) : "r"(d), "r"(0u));
+    uint32_t m;  // each half's sign over its 16 bits
+    asm("prmt.b32 %0, %1, 0, 0xBB99;" : "=r"(m) : "r"(word[k]));
+    b = add2(add2(top1, m), ~(d ^ m));
+    asm("min.u16x2 %0, %1, %2;" : "=r"(b) : "r"(b), "r"(last2));
+    bin[2 * k] = b & 0xFFFFu;
+    bin[2 * k + 1] = b >> 16;
+    zero_halves |= (d - 0x00010001u) & ~d;  // (d is at most 0x4501 in either half: the sign bits tell)
+  }
+  return (zero_halves & 0x80008000u) != 0;
+}
 
 // log2(e) / temperature in two floats, and the row's maximum.
 struct Exponent {
@@ -288,13 +329,21 @@ struct Elems<float> {
   typedef float Max;
   static __device__ __forceinline__ Max lowest() { return -INFINITY; }
   static __device__ __forceinline__ float largest(Max m) { return m; }
-  // The granule with NaN made -inf, and its values taken into the running maximum.
-  static __device__ __forceinline__ uint4 settle(const uint4& v, Max& m) {
+  // The granule with NaN made -inf; also with its values taken into the running maximum.
+  static __device__ __forceinline__ uint4 numbers(const uint4& v) {
     float x[4];
     unpack(v, x);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) m = fmaxf(m, x[k] = fmaxf(x[k], -INFINITY));
+    for (int k = 0; k < 4; ++k) x[k] = fmaxf(x[k], -INFINITY);
     return pack(x);
+  }
+  static __device__ __forceinline__ uint4 settle(const uint4& v, Max& m) {
+    const uint4 r = numbers(v);
+    float x[4];
+    unpack(r, x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m = fmaxf(m, x[k]);
+    return r;
   }
   static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
     return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
@@ -318,8 +367,11 @@ struct Elems<uint16_t> {  // bf16
     asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
   }
+  static __device__ __forceinline__ uint4 numbers(const uint4& v) {
+    return make_uint4(max2(v.x, lowest()), max2(v.y, lowest()), max2(v.z, lowest()), max2(v.w, lowest()));
+  }
   static __device__ __forceinline__ uint4 settle(const uint4& v, Max& m) {
-    const uint4 r = make_uint4(max2(v.x, lowest()), max2(v.y, lowest()), max2(v.z, lowest()), max2(v.w, lowest()));
+    const uint4 r = numbers(v);
     m = max2(m, max2(max2(r.x, r.y), max2(r.z, r.w)));
     return r;
   }
@@ -370,7 +422,7 @@ __device__ __forceinline__ uint64_t* in_descending_order(uint64_t* keys, uint64_
 // The place of the token drawn from the `listed` tokens of sm.list, which hold the row's top-k first
 // ones: in their order exact weights, whose running sums give top-p's cut; then by place, for the draw.
 __device__ __noinline__ int draw_listed(Shared& sm, const Exponent& ex, uint32_t listed, uint32_t top_k, bool with_p,
-                                        uint64_t p64, float min_p, float u) {
+                                        uint64_t p64, float min_p, uint64_t u64) {
   const int tid = threadIdx.x;
   int n = 64;
   while (n < (int)listed) n <<= 1;
@@ -414,7 +466,7 @@ __device__ __noinline__ int draw_listed(Shared& sm, const Exponent& ex, uint32_t
     w[j] = key[j] ? sm.list.weight[(uint32_t)key[j]] : 0;
   }
   at = block_scan(w[0] + w[1], sm.warp_u64, &all);
-  const uint64_t goal = u < 1.f ? __umul64hi((uint64_t)(u * 18446744073709551616.f), all) : all - 1;
+  const uint64_t goal = __umul64hi(u64, all);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     if (at <= goal && goal < at + w[j]) sm.index = (int)~(uint32_t)(key[j] >> 32);
@@ -447,11 +499,11 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
   const int seg = iters * kStep;    // a warp's places
   const int first = (rank * kWarps + warp) * seg;
   uint4* slice = reinterpret_cast<uint4*>(slice_raw) + lane;  // granule of warp w, iteration i: slice[32 (w iters + i)]
-  bool only_inf = false;  // the row has tokens at +inf: those count as 0, all others as -inf
-  // the granule at place p as it lies in memory
-  auto granule = [&](int p) {
+  // the granule at place p as it lies in memory; `whole`: no part of this warp's run is outside the row
+  const bool whole = (rank * kWarps + warp) * seg >= shift && (rank * kWarps + warp + 1) * seg <= end;
+  auto granule = [&](int p, bool inside) {
     uint4 v;
-    if (p >= shift && p + kVec <= end) {
+    if (inside || (p >= shift && p + kVec <= end)) {
       asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                    : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                    : "l"(base + p));
@@ -466,16 +518,9 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
   // the logits of warp w's iteration i that fall to this lane, NaN made -inf
   auto fetch = [&](int w, int i) {
     if (kKeep) return slice[32 * (w * iters + i)];
-    return granule((rank * kWarps + w) * seg + i * kStep + lane * kVec);
+    return granule((rank * kWarps + w) * seg + i * kStep + lane * kVec, whole && w == warp);
   };
-  auto values = [&](const uint4& v, float (&x)[kVec]) {
-    E::unpack(v, x);
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) {
-      if (!kKeep) x[k] = fmaxf(x[k], -INFINITY);
-      if (only_inf) x[k] = x[k] == INFINITY ? 0.f : -INFINITY;
-    }
-  };
+  auto values = [&](const uint4& v, float (&x)[kVec]) { E::unpack(kKeep ? v : E::numbers(v), x); };
 
   // settings; a row with a bad one draws nothing
   const float temp = a.temperature ? __ldg(a.temperature + row) : 1.f;
@@ -507,7 +552,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     uint4 v[kFlight];
 #pragma unroll
     for (int f = 0; f < kFlight; ++f)
-      if (i0 + f < iters) v[f] = granule(first + (i0 + f) * kStep + lane * kVec);
+      if (i0 + f < iters) v[f] = granule(first + (i0 + f) * kStep + lane * kVec, whole);
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
       if (i0 + f < iters) {
@@ -528,22 +573,30 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
   cluster.sync();
   for (int r = 0; r < C; ++r) mx = fmaxf(mx, *cluster.map_shared_rank(&sm.x_max, r));
 
-  // g(values, first place) for every granule of this thread, the next ones on their way
-  auto each_granule = [&](auto&& g) {
-    constexpr int kAhead = kKeep ? 1 : 3;
+  // g(granule, values, first place) for every granule of this thread, the next ones on their way
+  auto each_raw = [&](auto&& g) {
+    constexpr int kAhead = kKeep ? 1 : 2;
     uint4 v[kAhead];
 #pragma unroll
     for (int h = 0; h < kAhead; ++h)
       if (h < iters) v[h] = fetch(warp, h);
 #pragma unroll 1
-    for (int i = 0; i < iters; ++i) {
-      float x[kVec];
-      values(v[0], x);
+    for (int i0 = 0; i0 < iters; i0 += kAhead) {
 #pragma unroll
-      for (int h = 0; h + 1 < kAhead; ++h) v[h] = v[h + 1];
-      if (i + kAhead < iters) v[kAhead - 1] = fetch(warp, i + kAhead);
-      g(x, first + i * kStep + lane * kVec);
+      for (int h = 0; h < kAhead; ++h) {
+        const int i = i0 + h;
+        if (i >= iters) break;
+        const uint4 now = kKeep ? v[h] : E::numbers(v[h]);
+        if (i + kAhead < iters) v[h] = fetch(warp, i + kAhead);
+        float x[kVec];
+        E::unpack(now, x);
+        g(now, x, first + i * kStep + lane * kVec);
+      }
     }
+  };
+  // g(values, first place)
+  auto each_granule = [&](auto&& g) {
+    each_raw([&](const uint4&, const float (&x)[kVec], int p) { g(x, p); });
   };
   // f(x) for every element of this thread, its code once and not once per element of a granule: for
   // passes that few rows take, whose instructions would otherwise come from memory each time
@@ -580,9 +633,48 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     cluster.sync();
     return;
   }
-  if (mx == INFINITY) {  // tokens at +inf share the draw evenly
-    only_inf = true;
-    mx = 0.f;
+  const uint64_t p64 = (uint64_t)(top_p * 18446744073709551616.f);  // p 2^64: whole for p >= 2^-40
+  const uint64_t u64 = u < 1.f ? (uint64_t)(u * 18446744073709551616.f) : ~0ull;
+  if (mx == INFINITY) {
+    // the tokens at +inf have equal weights, and all others none: of the first kept ones by place, the
+    // one numbered floor(u kept)
+    uint32_t here = 0;
+    each_small([&](float x) { here += x == INFINITY ? 1u : 0u; });
+    here = warp_add(here);
+    __syncthreads();
+    if (lane == 0) sm.warp_u32[warp] = here;
+    __syncthreads();
+    uint32_t block = 0, ahead = 0, all = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      block += sm.warp_u32[w];
+      if (w < warp) ahead += sm.warp_u32[w];
+    }
+    if (tid == 0) sm.count = block;
+    cluster.sync();
+    for (int r = 0; r < C; ++r) {
+      const uint32_t n = *cluster.map_shared_rank(&sm.count, r);
+      if (r < rank) ahead += n;
+      all += n;
+    }
+    if (top_k > 0) all = min(all, (uint32_t)top_k);
+    if (top_p < 1.f) all = max((uint32_t)(__umul64hi(p64, all) + (p64 * all != 0 ? 1 : 0)), 1u);
+    uint32_t nth = (uint32_t)__umul64hi(u64, all);  // (u = 1: the last)
+    if (ahead <= nth && nth < ahead + here) {       // one warp of the cluster
+      for (int i = 0; i < iters; ++i) {
+        float x[kVec];
+        values(fetch(warp, i), x);
+        uint32_t n = 0;
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) n += x[k] == INFINITY ? 1u : 0u;
+        uint32_t at = ahead + warp_scan(n, lane) - n;
+#pragma unroll
+        for (int k = 0; k < kVec; ++k)
+          if (x[k] == INFINITY && at++ == nth) a.token[row] = first + i * kStep + lane * kVec + k - shift;
+        ahead += warp_add(n);
+      }
+    }
+    cluster.sync();
+    return;
   }
   const Exponent ex = {mx, sm.exp_hi, sm.exp_lo};
   auto to_all = [&](auto member, auto value) {  // into every CTA's copy of a result
@@ -595,14 +687,13 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
   uint32_t cut_keep = kAllEqual;
   bool with_k = top_k > 0 && top_k < a.vocab;
   const bool with_p = top_p < 1.f;
-  const uint64_t p64 = (uint64_t)(top_p * 18446744073709551616.f);  // p 2^64: whole for p >= 2^-40
   if ((with_k || with_p) && a.vocab <= kList) {
     // the whole row goes into a list (of one CTA: its cluster has no other)
     each([&](float x, int p) {
       if (x > -INFINITY) sm.list.key[atomicAdd(&sm.listed, 1u) % kList] = sort_key(x, p);
     });
     __syncthreads();
-    const int place = draw_listed(sm, ex, sm.listed, with_k ? (uint32_t)top_k : kList, with_p, p64, min_p, u);
+    const int place = draw_listed(sm, ex, sm.listed, with_k ? (uint32_t)top_k : kList, with_p, p64, min_p, u64);
     if (tid == 0) a.token[row] = place - shift;
     return;
   }
@@ -611,19 +702,24 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     // tokens of weight lie above
     const float x_low = fminf(mx, fmaxf(mx - kOctaves * 0.6931472f * temp * 1.0001f, -3.402823466e38f));
     // the bins in use; every CTA sums up an equal run of them
-    const int bins = min(kBins - 1, top_number - number_of(x_low) + 1);
+    const int bins = min(kBins - kLastBins, top_number - number_of(x_low) + 1);
     const int per = (bins + C * kThreads - 1) / (C * kThreads);  // consecutive bins of one thread
     const int bin0 = (rank * kThreads + tid) * per;
     const int tiny_bin = top_number;  // of number 0, where it is in use (0 <= top_number < bins)
     for (int b = tid; b < bins; b += kThreads) sm.hist[b] = 0;
     __syncthreads();
     uint64_t tiny = 0;  // exact mass of the values that share the bin next to zero
-    each([&](float x, int) {
-      const int n = number_of(x), b = top_number - n;
-      if (b < bins) {
-        atomicAdd(&sm.hist[b], 1u);
-        if (E::kLowBits && with_p && n == 0) tiny += weight_units(x, ex, sm.table);
-      }
+    const bool need_tiny = E::kLowBits && with_p && tiny_bin >= 0 && tiny_bin < bins;
+    const int last_bin = kBins - kLastBins + lane;  // (bins from `bins` on are not looked at)
+    each_raw([&](const uint4& v, const float (&x)[kVec], int) {
+      uint32_t bin[kVec];
+      const bool near = bins_of(x, v, top_number, last_bin, bin);
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) atomicAdd(&sm.hist[bin[k]], 1u);
+      if (need_tiny && near)
+#pragma unroll 1
+        for (int k = 0; k < kVec; ++k)
+          if (number_of(x[k]) == 0) tiny += weight_units(x[k], ex, sm.table);
     });
     if (E::kLowBits && with_p) {
       tiny = warp_add(tiny);
@@ -768,12 +864,18 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
       bin_keys(bin_k, bin_k, &klo, &khi);
       const float least = order_value<E::kLowBits>(klo);
       Shared* to = cluster.map_shared_rank(&sm, 0);
-      each([&](float x, int p) {
-        if (x >= least) to->list.key[atomicAdd(&to->listed, 1u) % kList] = sort_key(x, p);
+      each_granule([&](const float (&x)[kVec], int p) {
+        bool any = false;
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) any |= x[k] >= least;
+        if (any)
+#pragma unroll
+          for (int k = 0; k < kVec; ++k)
+            if (x[k] >= least) to->list.key[atomicAdd(&to->listed, 1u) % kList] = sort_key(x[k], p + k);
       });
       cluster.sync();
       if (rank == 0) {
-        const int place = draw_listed(sm, ex, top_listed, (uint32_t)top_k, with_p, p64, min_p, u);
+        const int place = draw_listed(sm, ex, top_listed, (uint32_t)top_k, with_p, p64, min_p, u64);
         if (tid == 0) a.token[row] = place - shift;
       }
       return;
@@ -999,7 +1101,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
       seen += n;
     }
     // the token's running sum is the first above `goal` = floor(u all)
-    const uint64_t goal = u < 1.f ? __umul64hi((uint64_t)(u * 18446744073709551616.f), all) : all - 1;
+    const uint64_t goal = __umul64hi(u64, all);
     if (before <= goal && goal < before + here) {  // one CTA of the cluster
       int w0 = 0;
       for (; w0 < kWarps - 1; ++w0) {
@@ -1101,9 +1203,10 @@ sample_plain_kernel(const SampleArgs a, int iters) {
   const T* base = src - shift;
   const int end = a.vocab + shift, seg = iters * kStep;
   const int first = (rank * kWarps + warp) * seg + lane * kVec;
-  auto granule = [&](int p) {
+  const bool whole = (rank * kWarps + warp) * seg >= shift && (rank * kWarps + warp + 1) * seg <= end;
+  auto granule = [&](int p, bool inside = false) {
     uint4 v;
-    if (p >= shift && p + kVec <= end) {
+    if (inside || (p >= shift && p + kVec <= end)) {
       asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                    : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                    : "l"(base + p));
@@ -1115,11 +1218,11 @@ sample_plain_kernel(const SampleArgs a, int iters) {
     }
     return v;
   };
-  constexpr int kAhead = 3;
+  constexpr int kAhead = 2;
   uint4 ahead[kAhead];
 #pragma unroll
   for (int h = 0; h < kAhead; ++h)
-    if (h < iters) ahead[h] = granule(first + h * kStep);
+    if (h < iters) ahead[h] = granule(first + h * kStep, whole);
   const float temp = a.temperature ? __ldg(a.temperature + row) : 1.f;
   const float u = __ldg(a.uniform + row);
   const bool good = (temp == 0.f || (temp >= kSampleMinTemp && temp <= kSampleMaxTemp)) && u >= 0.f && u <= 1.f;
@@ -1142,17 +1245,19 @@ sample_plain_kernel(const SampleArgs a, int iters) {
   float mx = -INFINITY, s = 0.f, e = 0.f, low = 0.f, high = -INFINITY;
   int at = 0;  // iteration of the first granule with this thread's maximum
 #pragma unroll 1
-  for (int i = 0; i < iters; ++i) {
-    float x[kVec];
-    E::unpack(ahead[0], x);
+  for (int i0 = 0; i0 < iters; i0 += kAhead) {
 #pragma unroll
-    for (int h = 0; h + 1 < kAhead; ++h) ahead[h] = ahead[h + 1];
-    if (i + kAhead < iters) ahead[kAhead - 1] = granule(first + (i + kAhead) * kStep);
-    float g = -INFINITY;
+    for (int h = 0; h < kAhead; ++h) {
+      const int i = i0 + h;
+      if (i >= iters) break;
+      float x[kVec];
+      E::unpack(ahead[h], x);
+      if (i + kAhead < iters) ahead[h] = granule(first + (i + kAhead) * kStep, whole);
+      float g = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) g = fmaxf(g, x[k]);
-    if (g > mx) mx = g, at = i;
-    if (!greedy) {
+      for (int k = 0; k < kVec; ++k) g = fmaxf(g, x[k]);
+      if (g > mx) mx = g, at = i;
+      if (greedy) continue;
       if (g > high && fabsf(g * ab.hi) < kAboutMax) {
         // a bias for this thread's first numbers, or for weights over 2^64 times what it is for
         const float magic = __fadd_rn(12582912.f, rintf(-g * ab.hi));
