@@ -21,7 +21,7 @@
 // shared memory; with many, its later passes read it again, from L2, which lets
 // more rows be in work at once.  Where a filter needs the order, the cut is
 // found without sorting, from a histogram of counts over the leading 16 bits of
-// the values (bin_of): one shared-memory atomic per token.
+// the values (bins_of): one shared-memory atomic per token.
 //   bf16: a bin holds one value (but for the bin of the values next to zero), so
 //      the masses are counts times exact weights of some thousand values, and the
 //      histogram alone gives both cuts exactly;
@@ -34,7 +34,17 @@
 //      down to one value: one to three rounds, over the few tokens left.
 // The draw first sums weights in single precision with a known error (about_of);
 // only where the random number falls so near a running sum that this could decide
-// it, the sums are taken again exactly.
+// it, the sums are taken again exactly: by the same cluster, or, for calls without
+// any filter (which read a row once, in a kernel of their own), by a second launch.
+//
+// What bounds it: instructions, not memory.  512 rows of 131,072 bf16 (134 MB, 20 us
+// of reading) take 80 us without a filter (23 instructions a token: the weight 13,
+// the loop 5, the rest the search) and 173 us with top-p (58 a token, of them 20 the
+// histogram and 27 the draw); the histogram's atomics alone would take 30 us.  Tried
+// and not kept: top-p's masses in fp32 by single-precision sums first (a second pass
+// where they do not decide made the longest rows longer: 128 rows of 151,001, 166 ->
+// 191 us), whole rows in shared memory for 512 rows (216 us), undecided rows of the
+// filtered kernel by a second launch (203 -> 215 us).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -58,11 +68,11 @@ constexpr int kMaxElems = 264;               // logits of one thread
 constexpr int kMaxChunks = kMaxElems / 4;    // iterations of one warp
 constexpr float kOctaves = 46.f;             // weights below 2^-kOctaves count as zero
 constexpr int kNearZero = 0x3A80;            // leading 16 bits of 2^-10: smaller values share one bin
-constexpr int kBins = 18 * kThreads;         // 9216: see bin_of
+constexpr int kBins = 18 * kThreads;         // 9216: see number_of
 constexpr int kRanges = 1024;                // of the bit-pattern histograms
 constexpr int kList = 2 * kThreads;          // tokens that one CTA sorts
-constexpr int kUnitBits = 45;                // weights in units of 2^-45: 2^18 tokens' sum stays below 2^63
-static_assert((int64_t)VMLA_MAX_VOCAB << kUnitBits <= INT64_MAX, "sums of weights fit 63 bits");
+constexpr int kUnitBits = 45;                // weights in units of 2^-45
+static_assert((uint64_t)VMLA_MAX_VOCAB << kUnitBits == 1ull << 63, "a sum of weights, times the root of two, fits 64 bits");
 static_assert((int64_t)kMaxCluster * kThreads * kMaxElems >= VMLA_MAX_VOCAB + 7, "every vocabulary fits");
 static_assert(kChunkBytes / 4 >= kList + 3, "one iteration of one CTA holds a list's worth of logits");
 static_assert((int64_t)kMaxElems << 23 < (1ll << 32) && kKeepIters * 8 <= kMaxElems, "a thread's sum of high parts fits 32 bits");
@@ -1503,14 +1513,13 @@ sample_plain_exact_kernel(const SampleArgs a, const __grid_constant__ ExpTable e
   }
 }
 
-// CTAs per row: more while all of them are resident (two on each SM), up to four while as many wait if a
-// CTA's share of a row is over eight iterations (64 KB), eight only while that leaves SMs idle, and more
-// while a share is over 20 iterations; the row stays in shared memory where a share is at most 64 KB.
-// Measured, us by cluster size 1 / 2 / 4 / 8 (kept where marked *), without filters by the general kernel:
-// 512 rows of 131,072 bf16 154 / 126 / 128* / 188*, 150 rows 93 / 62 / 51* / 63*, 16 rows 54 / 34 / 21* /
-// 18*; with top-p, 512 rows 198 / 200 / 222* / 352*, 64 rows 102 / 64 / 44* / 53*; all filters, 151,001
-// fp32, 128 rows - / 199 / 175 / 278, 16 rows - / 120 / 80 / 73; all filters, 32,000 bf16, 400 rows 50* / 65* /
-// 100* / 181* (not kept 59 / 75 / 114 / 204), 100 rows 31* / 28* / 33* / 47*.
+// CTAs per row: more while all of them are resident (two on each SM), eight only while that leaves SMs
+// idle, and more while one CTA's share of a row is over 20 iterations (160 KB); the row stays in shared
+// memory where a share is at most 64 KB.  Measured, us by cluster size 1 / 2 / 4 / 8 (kept where marked *):
+// top-p of 131,072 bf16: 512 rows 169 / 176 / 216* / 366*, 150 rows 63 / 55 / 82* / 118*, 64 rows 60 / 42 / 35* /
+// 55*, 16 rows 58 / 41 / 26* / 27*; all filters of 151,001 fp32: 128 rows - / 168 / 130 / 154, 16 rows - / 91 / 63 /
+// 55; all filters of 32,000 bf16: 400 rows 48* / 62* / 92* / 161* (not kept 54 / 69 / 101 / 177), 100 rows 30* /
+// 28* / 34* / 49*.
 struct Shape {
   int cluster, iters;
   bool keep;
@@ -1528,8 +1537,7 @@ Shape choose_shape(const SampleArgs& a, int sms) {
   Shape s;
   s.cluster = 1;  // (a vocabulary of up to kList tokens stays in one CTA: one iteration holds it)
   while (s.cluster < kMaxCluster && need(s.cluster) > 1 &&
-         (a.rows * s.cluster * 2 <= (s.cluster == 4 ? 1 : need(s.cluster) > kKeepIters ? 4 : 2) * sms ||
-          need(s.cluster) > 20))
+         (a.rows * s.cluster * 2 <= (s.cluster == 4 ? 1 : 2) * sms || need(s.cluster) > 20))
     s.cluster *= 2;
   s.keep = need(s.cluster) <= kKeepIters;
   while (s.cluster < kMaxCluster && need(s.cluster) > kMaxElems / Elems<T>::kVec) s.cluster *= 2;
@@ -1537,10 +1545,8 @@ Shape choose_shape(const SampleArgs& a, int sms) {
   return s;
 }
 // Without filters a CTA does one pass and two more barriers: more CTAs per row pay off only while all are
-// resident (three on an SM).  Us by cluster size 1 / 2 / 4 / 8, both launches: 512 rows of 131,072 bf16
-// 124 / 120 / 133 / 177 (before the second launch's kernel was its own), 150 rows 58 / 52 / 57 / 68, 64 rows
-// 54 / 46 / 43 / 49, one row 26 / 19 / 15 / 13; 400 rows of 32,000 35 / 41 / 52 / 89; 128 rows of 151,001 fp32
-// - / 64 / 71 / 75.
+// resident.  Us by cluster size 1 / 2 / 4 / 8, both launches: 512 rows of 131,072 bf16 81 / 80 / 95 / 141, 150
+// rows 37 / 34 / 40 / 51, 64 rows 37 / 29 / 28 / 35, one row 23 / 17 / 14 / 13; 400 rows of 32,000 25 / 32 / 42 / 79.
 template <typename T>
 Shape choose_plain_shape(const SampleArgs& a, int sms) {
   auto need = [&](int c) { return iterations<T>(a, c); };
