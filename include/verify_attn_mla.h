@@ -382,8 +382,10 @@ int verify_attn_mla_shared(const void* q, const void* kv_pool, int64_t pool_slot
  *   token    [rows] int32 out
  *   status_word  optional, two uint32: a setting out of its range (in a greedy
  *            row too) records VMLA_ERR_PARAM with the row, which draws -1
- * Argument errors return before the launch.  One launch, no workspace, no host
- * synchronisation; capture-safe. */
+ * Argument errors return before the launch.  No workspace, no host
+ * synchronisation; capture-safe.  One launch; with top_k, top_p and min_p all
+ * NULL two, the second for the rows whose draw lies too near a border for the
+ * first one's sums: between the two token[] holds a negative mark for them. */
 int verify_attn_mla_sample(const void* logits, int logits_fp32, int64_t row_stride, int64_t rows, int vocab,
                            const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
                            const float* uniform, int32_t* token, uint32_t* status_word, void* stream);
