@@ -27,9 +27,10 @@
 //      histogram alone gives both cuts exactly;
 //   few tokens: where top-k's bins hold at most 1024 tokens (or the vocabulary does)
 //      one CTA sorts them and does the rest: order, masses, cuts and draw;
-//   fp32: counts give top-k's bin, bounds of each bin's mass bracket top-p's; one
-//      pass adds the exact masses of all tokens and of those above the bracket;
-//      inside a bin or bracket, histograms over 1024 equal ranges of the values'
+//   fp32: counts give top-k's bin, and, with each bin's middle value, the three bins
+//      that should hold top-p's cut; one pass adds the exact masses of all tokens and
+//      of those above these bins (where the cut is not in them, another over all bins);
+//      inside the bin or bins, histograms over 1024 equal ranges of the values'
 //      bit patterns in their order (count, and exact mass for top-p) narrow it
 //      down to one value: one to three rounds, over the few tokens left.
 // The draw first sums weights in single precision with a known error (about_of);
@@ -37,11 +38,12 @@
 // it, the sums are taken again exactly: by the same cluster, or, for calls without
 // any filter (which read a row once, in a kernel of their own), by a second launch.
 //
-// What bounds it: instructions, not memory.  512 rows of 131,072 bf16 (134 MB, 20 us
-// of reading) take 80 us without a filter (23 instructions a token: the weight 13,
-// the loop 5, the rest the search) and 173 us with top-p (58 a token, of them 20 the
-// histogram and 27 the draw); the histogram's atomics alone would take 30 us.  Tried
-// and not kept: top-p's masses in fp32 by single-precision sums first (a second pass
+// What bounds it: 512 rows of 131,072 bf16 (134 MB, 20 us of reading) take 81 us without a
+// filter, instructions (23 a token: the weight 13, the loop 5, the rest the search), and
+// 145 us with top-p.  There a row is one CTA's, two on an SM, for 64 us: maximum 10, the
+// histogram 22 (its shared-memory atomics, 3.8 cycles a warp for their banks' conflicts,
+// take 28 us of the whole call), cuts 10, the sums of the draw 15, its search 6, barriers.
+// Tried and not kept: top-p's masses in fp32 by single-precision sums first (a second pass
 // where they do not decide made the longest rows longer: 128 rows of 151,001, 166 ->
 // 191 us), whole rows in shared memory for 512 rows (216 us), undecided rows of the
 // filtered kernel by a second launch (203 -> 215 us).
@@ -70,6 +72,7 @@ constexpr float kOctaves = 46.f;             // weights below 2^-kOctaves count 
 constexpr int kNearZero = 0x3A80;            // leading 16 bits of 2^-10: smaller values share one bin
 constexpr int kBins = 18 * kThreads;         // 9216: see number_of
 constexpr int kRanges = 1024;                // of the bit-pattern histograms
+constexpr int kKeys = kBins - 3 * kRanges;   // of the keys that they count, listed for the next round
 constexpr int kList = 2 * kThreads;          // tokens that one CTA sorts
 constexpr int kUnitBits = 45;                // weights in units of 2^-45
 static_assert((uint64_t)VMLA_MAX_VOCAB << kUnitBits == 1ull << 63, "a sum of weights, times the root of two, fits 64 bits");
@@ -87,6 +90,7 @@ struct Shared {
     uint32_t hist[kBins];
     struct {
       uint32_t count[kRanges], mass_lo[kRanges], mass_hi[kRanges];
+      uint32_t key[kKeys];  // of this CTA's tokens that they count
     } r;
     struct {
       uint64_t key[kList], weight[kList], by_place[kList], spare[kList];
@@ -95,23 +99,25 @@ struct Shared {
   float2 table[64];
   uint64_t warp_u64[kWarps], warp_u64b[kWarps];
   uint32_t warp_u32[kWarps];
-  float warp_f[kWarps], warp_g[kWarps];
+  float warp_f[kWarps];
   float exp_hi, exp_lo;    // log2(e) / temperature
-  double min_p_offset;     // temperature x ln(min_p)
+  float ln_hi, ln_lo;      // temperature x ln(min_p)
   // read by the other CTAs of the cluster; a cluster barrier lies between a phase's reads and the
   // slot's next write
   float x_max;
   uint64_t sum_a, sum_b, tiny;
-  float sum_lo, sum_hi;
+  float sum_f;
   uint32_t key_lo, key_hi, count, bin_count;
-  int32_t index;
+  int32_t index, bin_middle;
   // written by the one thread of the cluster that finds them, into every CTA
-  int32_t bin_k, bin_p, bracket_lo, bracket_hi, sure;
-  uint32_t bin_k_rank, bin_k_count, bin_p_count;
-  uint64_t bin_p_left;
+  int32_t bin_k, bin_p, sure;
+  uint32_t bin_k_rank, bin_k_count, bin_p_keep;
   // results of a search, the same in every CTA
   uint32_t listed;         // (in the first CTA) tokens in its list
+  uint32_t keys;           // (of each CTA its own) keys in its list, more than kKeys where it is not whole
+  uint32_t few[32], few_keys;
   int32_t range;
+  uint32_t range_key;
   uint32_t range_count;
   uint64_t range_before;
   uint64_t chunk[kMaxChunks];
@@ -153,28 +159,17 @@ __device__ __forceinline__ uint32_t add2(uint32_t a, uint32_t b) {  // 16-bit ha
   return r;
 }
 
-// Bins of a granule's values, top being the number of the row's maximum and last this lane's bin for
-// what counts as zero; whether one of them is next to zero.
-__device__ __forceinline__ bool bins_of(const float (&x)[4], const uint4&, int top, int last, uint32_t (&bin)[4]) {
-  bool near = false;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int n = number_of(x[k]);
-    bin[k] = (uint32_t)min(top - n, last);
-    near |= n == 0;
-  }
-  return near;
-}
-// bf16: two at a time in 16-bit halves.  With d = max(magnitude bits - (kNearZero - 1), 0) and m = -1 where
-// the sign is set, the number is (d ^ m) - m, so the bin is top + m + 1 + ~(d ^ m) (all modulo 2^16: a
-// bin is below 2 x 17,666).
-__device__ __forceinline__ bool bins_of(const float (&)[8], const uint4& v, int top, int last, uint32_t (&bin)[8]) {
+// Bins of a granule's values by their leading 16 bits, two values at a time in 16-bit halves, top being the
+// number of the row's maximum and last this lane's bin for what counts as zero; whether a value is next to
+// zero.  With d = max(magnitude bits - (kNearZero - 1), 0) and m = -1 where the sign is set, the number is
+// (d ^ m) - m, so the bin is top + m + 1 + ~(d ^ m) (all modulo 2^16: a bin is below 2 x 17,666).
+template <int N>
+__device__ __forceinline__ bool bins_of(const uint32_t (&word)[N], int top, int last, uint32_t (&bin)[2 * N]) {
   const uint32_t top1 = ((uint32_t)(top + 1) & 0xFFFFu) * 0x10001u, last2 = (uint32_t)last * 0x10001u;
   constexpr uint32_t kFrom = ((uint32_t)(-(kNearZero - 1)) & 0xFFFFu) * 0x10001u;
-  const uint32_t word[4] = {v.x, v.y, v.z, v.w};
   uint32_t zero_halves = 0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < N; ++k) {
     uint32_t d = add2(word[k] & 0x7FFF7FFFu, kFrom), b;
     asm("max.s16x2 %0, %1, %2;" : "=r"(d) : "r"(d), "r"(0u));
     uint32_t m;  // each half's sign over its 16 bits
@@ -187,6 +182,42 @@ __device__ __forceinline__ bool bins_of(const float (&)[8], const uint4& v, int 
   }
   return (zero_halves & 0x80008000u) != 0;
 }
+__device__ __forceinline__ bool bins_of(const float (&)[8], const uint4& v, int top, int last, uint32_t (&bin)[8]) {
+  const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+  return bins_of(word, top, last, bin);
+}
+__device__ __forceinline__ bool bins_of(const float (&)[4], const uint4& v, int top, int last, uint32_t (&bin)[4]) {
+  const uint32_t word[2] = {__byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x7632)};
+  return bins_of(word, top, last, bin);
+}
+
+// Two floats in one instruction, each as by itself.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 sum2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 less2(float2 a, float2 b) { return fma2(b, both(-1.f), a); }  // a - b, rounded once
 
 // log2(e) / temperature in two floats, and the row's maximum.
 struct Exponent {
@@ -197,42 +228,55 @@ struct Exponent {
 // a = ph + pl in two floats; ph = n / 64 + r; 2^-a = 2^(-n/64) e^z with z = -(r + pl) ln 2, |z| < 2^-7.5,
 // e^z - 1 = z + z^2 (1/2 + z (1/6 + z/24)) up to 2^-44 (z in two floats, zl below 2^-18: its square is
 // left out); the table's factor times e^z in two floats.
+__device__ __forceinline__ void weights_of(float2 x, const Exponent& e, const float2* table, int32_t (&high)[2],
+                                           int32_t (&low)[2]) {
+  const float2 mx = both(e.max), hi = both(e.hi);
+  const float2 s = less2(mx, x);
+  const float2 bb = less2(s, mx);
+  const float2 err = less2(less2(mx, less2(s, bb)), sum2(x, bb));
+  const float2 ph = mul2(s, hi);
+  float2 pl = fma2(s, hi, mul2(s, both(-e.hi)));
+  pl = fma2(s, both(e.lo), pl);
+  pl = fma2(err, hi, pl);
+  constexpr float kRound = 196608.f;  // 1.5 x 2^17: a sum with it is rounded to a multiple of 1/64
+  const float2 t = sum2(ph, both(kRound));
+  const int n[2] = {(int)(__float_as_uint(kRound) - __float_as_uint(t.x)),
+                    (int)(__float_as_uint(kRound) - __float_as_uint(t.y))};
+  const float2 r = less2(sum2(t, both(-kRound)), ph);  // (of the other sign)
+  constexpr float kLn2Hi = 0.693147182464599609375f, kLn2Lo = -1.904654299957767e-9f;
+  const float2 zh = mul2(r, both(kLn2Hi)), minus_zh = mul2(r, both(-kLn2Hi));
+  float2 zl = fma2(r, both(kLn2Hi), minus_zh);
+  zl = fma2(r, both(kLn2Lo), zl);
+  zl = fma2(pl, both(-kLn2Hi), zl);
+  const float2 p2 = fma2(zh, fma2(zh, both(1.f / 24), both(1.f / 6)), both(0.5f));
+  const float2 q = fma2(mul2(zh, zh), p2, fma2(zh, zl, zl));
+  const float2 sh = sum2(zh, q), sl = less2(q, sum2(sh, minus_zh));  // e^z - 1
+  const float2 f0 = table[n[0] & 63], f1 = table[n[1] & 63];
+  const float2 fx = make_float2(f0.x, f1.x), fy = make_float2(f0.y, f1.y);
+  const float2 p = mul2(fx, sh);
+  const float2 pe = fma2(fx, sh, mul2(p, both(-1.f)));
+  const float2 rest = fma2(fy, sh, fma2(fx, sl, sum2(fy, pe)));
+  const float2 wh = sum2(fx, p);
+  const float2 wl = sum2(less2(p, less2(wh, fx)), rest);
+  const float2 scale = make_float2(__uint_as_float((uint32_t)(127 + 23 + (n[0] >> 6)) << 23),   // 2^23 x 2^floor(-a)
+                                   __uint_as_float((uint32_t)(127 + 23 + (n[1] >> 6)) << 23));
+  constexpr float kWhole = 8388608.f, kHalf = 12582912.f;  // 2^23, 1.5 x 2^23
+  const float2 hf = fma2(wh, scale, both(kWhole));
+  const float2 res = fma2(wl, scale, fma2(wh, scale, less2(both(kWhole), hf)));
+  const float2 lf = fma2(res, both(4194304.f), both(kHalf));
+  // (no branch above: the weights of a thread's tokens are worked out side by side)
+  const bool some0 = ph.x < kOctaves, some1 = ph.y < kOctaves;  // not where x is -inf
+  high[0] = some0 ? (int)(__float_as_uint(hf.x) - __float_as_uint(kWhole)) : 0;
+  high[1] = some1 ? (int)(__float_as_uint(hf.y) - __float_as_uint(kWhole)) : 0;
+  low[0] = some0 ? (int)(__float_as_uint(lf.x) - __float_as_uint(kHalf)) : 0;
+  low[1] = some1 ? (int)(__float_as_uint(lf.y) - __float_as_uint(kHalf)) : 0;
+}
+// One token's weight, by the same steps.
 __device__ __forceinline__ void weight_of(float x, const Exponent& e, const float2* table, int32_t* high,
                                           int32_t* low) {
-  const float s = __fsub_rn(e.max, x);
-  const float bb = __fsub_rn(s, e.max);
-  const float err = __fsub_rn(__fsub_rn(e.max, __fsub_rn(s, bb)), __fadd_rn(x, bb));
-  const float ph = __fmul_rn(s, e.hi);
-  float pl = __fmaf_rn(s, e.hi, -ph);
-  pl = __fmaf_rn(s, e.lo, pl);
-  pl = __fmaf_rn(err, e.hi, pl);
-  constexpr float kRound = 196608.f;  // 1.5 x 2^17: a sum with it is rounded to a multiple of 1/64
-  const float t = __fadd_rn(ph, kRound);
-  const int n = -(int)(__float_as_uint(t) - __float_as_uint(kRound));
-  const float r = __fsub_rn(ph, __fsub_rn(t, kRound));
-  constexpr float kLn2Hi = 0.693147182464599609375f, kLn2Lo = -1.904654299957767e-9f;
-  const float zh = __fmul_rn(-r, kLn2Hi);
-  float zl = __fmaf_rn(-r, kLn2Hi, -zh);
-  zl = __fmaf_rn(-r, kLn2Lo, zl);
-  zl = __fmaf_rn(-pl, kLn2Hi, zl);
-  const float p2 = __fmaf_rn(zh, __fmaf_rn(zh, 1.f / 24, 1.f / 6), 0.5f);
-  const float q = __fmaf_rn(__fmul_rn(zh, zh), p2, __fmaf_rn(zh, zl, zl));
-  const float sh = __fadd_rn(zh, q), sl = __fsub_rn(q, __fsub_rn(sh, zh));  // e^z - 1
-  const float2 f = table[n & 63];
-  const float p = __fmul_rn(f.x, sh);
-  const float pe = __fmaf_rn(f.x, sh, -p);
-  const float rest = __fmaf_rn(f.y, sh, __fmaf_rn(f.x, sl, __fadd_rn(f.y, pe)));
-  const float wh = __fadd_rn(f.x, p);
-  const float wl = __fadd_rn(__fsub_rn(p, __fsub_rn(wh, f.x)), rest);
-  const float scale = __uint_as_float((uint32_t)(127 + 23 + (n >> 6)) << 23);  // 2^23 x 2^floor(-a)
-  constexpr float kWhole = 8388608.f, kHalf = 12582912.f;                      // 2^23, 1.5 x 2^23
-  const float hf = __fmaf_rn(wh, scale, kWhole);
-  const float res = __fmaf_rn(wl, scale, __fmaf_rn(wh, scale, -__fsub_rn(hf, kWhole)));
-  const float lf = __fmaf_rn(res, 4194304.f, kHalf);
-  // (no branch above: the weights of a thread's tokens are worked out side by side)
-  const bool some = ph < kOctaves;  // not where x is -inf
-  *high = some ? (int)(__float_as_uint(hf) - __float_as_uint(kWhole)) : 0;
-  *low = some ? (int)(__float_as_uint(lf) - __float_as_uint(kHalf)) : 0;
+  int32_t h[2], l[2];
+  weights_of(make_float2(x, e.max), e, table, h, l);
+  *high = h[0], *low = l[0];
 }
 
 __device__ __forceinline__ uint64_t units(int64_t high, int64_t low) { return (uint64_t)((high << 22) + low); }
@@ -270,14 +314,52 @@ __device__ __forceinline__ float about_of(float x, const About& a) {
   const float f = __fmaf_rn(x, a.lo, __fmaf_rn(x, a.hi, __fsub_rn(a.magic, t)));  // magic - t = bias - n
   return __uint_as_float(__float_as_uint(ex2_approx(f)) + (__float_as_uint(t) << 23));
 }
-// A float's value (below 2^18 1.5) in units of 2^-45.
-__device__ __forceinline__ uint64_t about_units(float v) { return (uint64_t)(v * 35184372088832.f); }
+// about_of of a granule's values, in pairs (t - magic by an exact product with -1).
+template <int N>
+__device__ __forceinline__ void about_all(const float (&x)[N], const About& a, float (&w)[N]) {
+  const float2 hi = make_float2(a.hi, a.hi), lo = make_float2(a.lo, a.lo), magic = make_float2(a.magic, a.magic);
+#pragma unroll
+  for (int k = 0; k < N; k += 2) {
+    const float2 v = make_float2(x[k], x[k + 1]);
+    const float2 t = fma2(v, hi, magic);
+    const float2 f = fma2(v, lo, fma2(v, hi, fma2(t, make_float2(-1.f, -1.f), magic)));
+    w[k] = __uint_as_float(__float_as_uint(ex2_approx(f.x)) + (__float_as_uint(t.x) << 23));
+    w[k + 1] = __uint_as_float(__float_as_uint(ex2_approx(f.y)) + (__float_as_uint(t.y) << 23));
+  }
+}
+// Their sum, in a tree.
+__device__ __forceinline__ float tree_sum(const float (&w)[8]) {
+  const float2 a = sum2(make_float2(w[0], w[1]), make_float2(w[4], w[5]));
+  const float2 b = sum2(make_float2(w[2], w[3]), make_float2(w[6], w[7]));
+  const float2 c = sum2(a, b);
+  return __fadd_rn(c.x, c.y);
+}
+__device__ __forceinline__ float tree_sum(const float (&w)[4]) {
+  const float2 c = sum2(make_float2(w[0], w[1]), make_float2(w[2], w[3]));
+  return __fadd_rn(c.x, c.y);
+}
+// A float's value v >= 0 in units of 2^-kBits, v 2^kBits < 2^64, rounded down.  (By shifts: the conversion
+// to 64 bits runs at two lanes a cycle on an SM, which 512 threads at once would feel.)
+template <int kBits>
+__device__ __forceinline__ uint64_t fixed(float v) {
+  const uint32_t b = __float_as_uint(v), m = (b & 0x7FFFFFu) | 0x800000u;
+  const int up = (int)(b >> 23) - (150 - kBits);
+  return up >= 0 ? (uint64_t)m << min(up, 63) : m >> min(-up, 31);
+}
+__device__ __forceinline__ uint64_t about_units(float v) { return fixed<kUnitBits>(v); }
 __device__ __forceinline__ uint64_t about_units(float s, float e) {
-  return about_units(s) + (uint64_t)(int64_t)(e * 35184372088832.f);
+  const uint64_t rest = about_units(fabsf(e));
+  return about_units(s) + (e < 0.f ? 0 - rest : rest);
 }
 // 2^d of a whole number d, zero below 2^-126 and one above 2^0.
 __device__ __forceinline__ float power_of_two(float d) {
   return d < -126.f ? 0.f : __uint_as_float((uint32_t)(127 + (int)fminf(d, 0.f)) << 23);
+}
+// a + (b + c), c far below b, rounded up to a float.
+__device__ __forceinline__ float sum_rounded_up(float a, float b, float c) {
+  const float t = __fadd_rn(a, b), v = __fsub_rn(t, a);
+  const float e = __fadd_rn(__fsub_rn(a, __fsub_rn(t, v)), __fsub_rn(b, v));
+  return __fadd_ru(t, __fadd_rn(e, c));
 }
 // v into a sum held in two floats.
 __device__ __forceinline__ void add_in_two(float v, float* s, float* e) {
@@ -336,6 +418,16 @@ struct Elems<float> {
   static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[4]) {
     x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
   }
+  // f of the granule's values two at a time, its code once: for passes that few rows take, whose
+  // instructions would otherwise come from memory each time
+  template <typename F>
+  static __device__ __forceinline__ void each_pair(uint4 v, F&& f) {
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+      f(make_float2(__uint_as_float(v.x), __uint_as_float(v.y)));
+      v.x = v.z, v.y = v.w;
+    }
+  }
   typedef float Max;
   static __device__ __forceinline__ Max lowest() { return -INFINITY; }
   static __device__ __forceinline__ float largest(Max m) { return m; }
@@ -368,6 +460,14 @@ struct Elems<uint16_t> {  // bf16
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) x[2 * k] = bf16_lo(w[k]), x[2 * k + 1] = bf16_hi(w[k]);
+  }
+  template <typename F>
+  static __device__ __forceinline__ void each_pair(uint4 v, F&& f) {
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+      f(make_float2(bf16_lo(v.x), bf16_hi(v.x)));
+      v.x = v.y, v.y = v.z, v.z = v.w;
+    }
   }
   typedef uint32_t Max;  // two bf16 maxima
   static __device__ __forceinline__ Max lowest() { return 0xFF80FF80u; }
@@ -438,7 +538,7 @@ __device__ __noinline__ int draw_listed(Shared& sm, const Exponent& ex, uint32_t
   while (n < (int)listed) n <<= 1;
   for (int i = listed + tid; i < n; i += kThreads) sm.list.key[i] = 0;
   const uint64_t* order = in_descending_order(sm.list.key, sm.list.spare, n);
-  const float least = min_p > 0.f ? __double2float_ru((double)ex.max + sm.min_p_offset) : -INFINITY;
+  const float least = min_p > 0.f ? sum_rounded_up(ex.max, sm.ln_hi, sm.ln_lo) : -INFINITY;
   // this thread's two tokens of the order
   float x[2];
   uint64_t w[2];
@@ -500,6 +600,11 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
   __shared__ Shared sm;
   const cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  auto sync_all = [&] {
+    if (C > 1) cluster.sync();
+    else __syncthreads();
+  };
+  auto of = [&](int r) -> Shared& { return C > 1 ? *cluster.map_shared_rank(&sm, r) : sm; };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = (int64_t)blockIdx.x / C;
   const T* src = static_cast<const T*>(a.logits) + row * a.stride;
@@ -532,7 +637,12 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
   };
   auto values = [&](const uint4& v, float (&x)[kVec]) { E::unpack(kKeep ? v : E::numbers(v), x); };
 
-  // settings; a row with a bad one draws nothing
+  // the first granules on their way, then the settings; a row with a bad one draws nothing
+  constexpr int kFlight = 4;
+  uint4 flight[kFlight];
+#pragma unroll
+  for (int f = 0; f < kFlight; ++f)
+    if (f < iters) flight[f] = granule(first + f * kStep + lane * kVec, whole);
   const float temp = a.temperature ? __ldg(a.temperature + row) : 1.f;
   const int top_k = a.top_k ? __ldg(a.top_k + row) : 0;
   const float top_p = a.top_p ? __ldg(a.top_p + row) : 1.f;
@@ -553,16 +663,20 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     const double c = 1.4426950408889634 / (double)temp;
     sm.exp_hi = (float)c;
     sm.exp_lo = (float)(c - (double)sm.exp_hi);
-    sm.min_p_offset = min_p > 0.f && min_p < 1.f ? (double)temp * log((double)min_p) : 0.0;
+    const double l = min_p > 0.f && min_p < 1.f ? (double)temp * log((double)min_p) : 0.0;
+    sm.ln_hi = (float)l;
+    sm.ln_lo = (float)(l - (double)sm.ln_hi);
   }
   // ---- the row's maximum
   typename E::Max run = E::lowest();
-  constexpr int kFlight = 4;
+#pragma unroll 1
   for (int i0 = 0; i0 < iters; i0 += kFlight) {
     uint4 v[kFlight];
 #pragma unroll
+    for (int f = 0; f < kFlight; ++f) v[f] = flight[f];
+#pragma unroll
     for (int f = 0; f < kFlight; ++f)
-      if (i0 + f < iters) v[f] = granule(first + (i0 + f) * kStep + lane * kVec, whole);
+      if (i0 + kFlight + f < iters) flight[f] = granule(first + (i0 + kFlight + f) * kStep + lane * kVec, whole);
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
       if (i0 + f < iters) {
@@ -572,7 +686,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     }
   }
   float mx = E::largest(run);
-  if (tid == 0) sm.sure = 0, sm.listed = 0;  // (written from other CTAs only past the barriers below)
+  if (tid == 0) sm.sure = 0, sm.listed = 0, sm.tiny = 0;  // (written from other CTAs only past the barriers below)
   if (tid < 64) sm.table[tid] = exp_table.t[tid];
   mx = warp_max(mx);
   if (lane == 0) sm.warp_f[warp] = mx;
@@ -580,8 +694,8 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm.warp_f[w]);
   if (tid == 0) sm.x_max = mx;
-  cluster.sync();
-  for (int r = 0; r < C; ++r) mx = fmaxf(mx, *cluster.map_shared_rank(&sm.x_max, r));
+  sync_all();
+  for (int r = 0; r < C; ++r) mx = fmaxf(mx, of(r).x_max);
 
   // g(granule, values, first place) for every granule of this thread, the next ones on their way
   auto each_raw = [&](auto&& g) {
@@ -635,16 +749,16 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
       for (int w = 0; w < kWarps; ++w) at = min(at, (int)sm.warp_u32[w]);
       sm.index = at;
     }
-    cluster.sync();
+    sync_all();
     if (rank == 0 && tid == 0) {
-      for (int r = 0; r < C; ++r) at = min(at, *cluster.map_shared_rank(&sm.index, r));
+      for (int r = 0; r < C; ++r) at = min(at, of(r).index);
       a.token[row] = at == INT32_MAX ? -1 : at - shift;
     }
-    cluster.sync();
+    sync_all();
     return;
   }
-  const uint64_t p64 = (uint64_t)(top_p * 18446744073709551616.f);  // p 2^64: whole for p >= 2^-40
-  const uint64_t u64 = u < 1.f ? (uint64_t)(u * 18446744073709551616.f) : ~0ull;
+  const uint64_t p64 = top_p < 1.f ? fixed<64>(top_p) : ~0ull;  // p 2^64: whole for p >= 2^-40
+  const uint64_t u64 = u < 1.f ? fixed<64>(u) : ~0ull;
   if (mx == INFINITY) {
     // the tokens at +inf have equal weights, and all others none: of the first kept ones by place, the
     // one numbered floor(u kept)
@@ -660,9 +774,9 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
       if (w < warp) ahead += sm.warp_u32[w];
     }
     if (tid == 0) sm.count = block;
-    cluster.sync();
+    sync_all();
     for (int r = 0; r < C; ++r) {
-      const uint32_t n = *cluster.map_shared_rank(&sm.count, r);
+      const uint32_t n = of(r).count;
       if (r < rank) ahead += n;
       all += n;
     }
@@ -683,12 +797,12 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
         ahead += warp_add(n);
       }
     }
-    cluster.sync();
+    sync_all();
     return;
   }
   const Exponent ex = {mx, sm.exp_hi, sm.exp_lo};
   auto to_all = [&](auto member, auto value) {  // into every CTA's copy of a result
-    for (int r = 0; r < C; ++r) cluster.map_shared_rank(&sm, r)->*member = value;
+    for (int r = 0; r < C; ++r) of(r).*member = value;
   };
 
   // ---- what is kept: x > cut_x, and of the tokens equal to cut_x the first cut_keep
@@ -731,51 +845,53 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
         for (int k = 0; k < kVec; ++k)
           if (number_of(x[k]) == 0) tiny += weight_units(x[k], ex, sm.table);
     });
-    if (E::kLowBits && with_p) {
-      tiny = warp_add(tiny);
-      if (lane == 0) sm.warp_u64[warp] = tiny;
-      __syncthreads();
-      if (tid == 0) {
-        tiny = 0;
-        for (int w = 0; w < kWarps; ++w) tiny += sm.warp_u64[w];
-        sm.tiny = tiny;
-      }
-    }
-    cluster.sync();
+    if (tiny != 0) atomicAdd(reinterpret_cast<unsigned long long*>(&sm.tiny), (unsigned long long)tiny);
+    sync_all();
     // this thread's bins, summed over the CTAs (into this CTA's copy: no other CTA reads these bins
     // of it), and the tokens ahead of them
     uint32_t before = 0;
-    for (int j = 0; j < per && bin0 + j < bins; ++j) {
-      uint32_t n = 0;
-      for (int r = 0; r < C; ++r) n += cluster.map_shared_rank(sm.hist, r)[bin0 + j];
-      sm.hist[bin0 + j] = n;
-      before += n;
+    if (C > 1 || with_k)
+      for (int j = 0; j < per && bin0 + j < bins; ++j) {
+        uint32_t n = 0;
+        for (int r = 0; r < C; ++r) n += of(r).hist[bin0 + j];
+        if (C > 1) sm.hist[bin0 + j] = n;
+        before += n;
+      }
+    if (with_k) {
+      uint32_t total;
+      before = block_scan(before, sm.warp_u32, &total);
+      if (tid == 0) sm.bin_count = total;
+      sync_all();
+      total = 0;
+      for (int r = 0; r < C; ++r) {
+        const uint32_t n = of(r).bin_count;
+        if (r < rank) before += n;
+        total += n;
+      }
+      if ((uint32_t)top_k >= total) with_k = false;  // nothing of weight is past the k-th
     }
-    uint32_t total;
-    before = block_scan(before, sm.warp_u32, &total);
-    if (tid == 0) sm.bin_count = total;
-    cluster.sync();
-    total = 0;
-    for (int r = 0; r < C; ++r) {
-      const uint32_t n = *cluster.map_shared_rank(&sm.bin_count, r);
-      if (r < rank) before += n;
-      total += n;
-    }
-    if (with_k && (uint32_t)top_k >= total) with_k = false;  // nothing of weight is past the k-th
 
     // Histograms of counts (and masses) over the 1024 equal ranges of keys from klo on, each 2^width
     // keys wide, of this CTA's tokens; the keys are clear when all CTAs have passed the next barrier.
     auto range_width = [](uint32_t klo, uint32_t khi) { return max(32 - __clz((khi - klo) | 1) - 10, 0); };
-    auto clear_ranges = [&] {
+    auto clear_ranges = [&](bool list) {
       for (int b = tid; b < kRanges; b += kThreads) sm.r.count[b] = sm.r.mass_lo[b] = sm.r.mass_hi[b] = 0;
+      if (tid == 0) {
+        sm.few_keys = 0;
+        if (list) sm.keys = 0;
+      }
       __syncthreads();
+    };
+    auto list_key = [&](uint32_t k) {
+      const uint32_t at = atomicAdd(&sm.keys, 1u);
+      if (at < kKeys) sm.r.key[at] = k;
     };
     auto add_mass = [&](uint32_t g, uint64_t w) {
       const uint32_t wl = (uint32_t)w, old = atomicAdd(&sm.r.mass_lo[g], wl);
       atomicAdd(&sm.r.mass_hi[g], (uint32_t)(w >> 32) + (old + wl < old ? 1u : 0u));
     };
     // The range in which the running count (or mass), in descending order, reaches `target`: [klo, khi]
-    // becomes it; its count; and what is left of the target.
+    // becomes it; its count; and what is left of the target.  False where it is not reached.
     auto pick = [&](bool by_mass, int width, uint32_t* klo, uint32_t* khi, uint64_t* target, uint32_t* equal) {
       constexpr int kPer = kRanges / kThreads;
       uint32_t n2[kPer], sum_n = 0;
@@ -785,7 +901,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
         const int g = kRanges - 1 - (kPer * tid + j);  // descending
         n2[j] = 0, m2[j] = 0;
         for (int r = 0; r < C; ++r) {
-          const Shared* o = cluster.map_shared_rank(&sm, r);
+          const Shared* o = &of(r);
           n2[j] += o->r.count[g];
           if (by_mass) m2[j] += ((uint64_t)o->r.mass_hi[g] << 32) + o->r.mass_lo[g];
         }
@@ -795,6 +911,10 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
       uint64_t all_m = 0, cum_m = 0;
       uint32_t cum_n = block_scan(sum_n, sm.warp_u32, &all_n);
       if (by_mass) cum_m = block_scan(sum_m, sm.warp_u64, &all_m);
+      if (by_mass && *target - 1 >= all_m) {  // (0 too) the same in every thread of the cluster
+        sync_all();
+        return false;
+      }
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const uint64_t was = by_mass ? cum_m : cum_n;
@@ -811,24 +931,66 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
       *equal = sm.range_count;
       *klo += (uint32_t)sm.range << width;
       *khi = min(*khi, *klo + ((1u << width) - 1u));
-      cluster.sync();  // the histograms have been read
+      sync_all();  // the histograms have been read
+      return true;
     };
     // The value at which a running count (or mass) over the tokens with a key in [klo, khi], in
     // descending order, reaches `target`: its key, how many tokens have it, and what is left of the
-    // target for them.  (A round leaves 10 bits fewer: 32, 22, 12, 2.)
-    auto refine = [&](uint32_t klo, uint32_t khi, bool by_mass, uint64_t* target, uint32_t* equal) {
+    // target for them.  (A round leaves 10 bits fewer: 32, 22, 12, 2.)  The keys come from the list, or,
+    // where there is none yet or too many, from the row.
+    auto refine = [&](uint32_t klo, uint32_t khi, bool by_mass, bool listed, uint64_t* target, uint32_t* equal) {
+#pragma unroll 1
       for (int round = 0; round < 4; ++round) {
         const int width = range_width(klo, khi);
-        clear_ranges();
-        each([&](float x, int) {
-          const uint32_t k = order_key<E::kLowBits>(x);
-          if (k >= klo && k <= khi) {
-            const uint32_t g = (k - klo) >> width;
-            atomicAdd(&sm.r.count[g], 1u);
-            if (by_mass) add_mass(g, weight_units(x, ex, sm.table));
+        const uint32_t keys = listed ? sm.keys : kKeys + 1u;
+        const bool few = listed && *equal <= 32;
+        clear_ranges(!listed);
+        auto take = [&](uint32_t k) {
+          if (k < klo || k > khi) return;
+          if (few) {
+            sm.few[atomicAdd(&sm.few_keys, 1u) & 31u] = k;
+            return;
           }
-        });
-        cluster.sync();
+          const uint32_t g = (k - klo) >> width;
+          atomicAdd(&sm.r.count[g], 1u);
+          if (by_mass) add_mass(g, weight_units(order_value<E::kLowBits>(k), ex, sm.table));
+          if (!listed) list_key(k);
+        };
+        if (keys <= kKeys) {
+          for (uint32_t i = tid; i < keys; i += kThreads) take(sm.r.key[i]);
+        } else {
+          each([&](float x, int) { take(order_key<E::kLowBits>(x)); });
+        }
+        listed = true;
+        if (few) {
+          // one warp of each CTA takes the cluster's few keys, one to a lane
+          sync_all();
+          if (warp == 0) {
+            uint32_t k = 0, n = 0, same = 0;
+            for (int r = 0; r < C; ++r) {
+              const uint32_t here = of(r).few_keys;
+              if (lane >= n && lane < n + here) k = of(r).few[lane - n];
+              n += here;
+            }
+            const uint64_t w = by_mass ? weight_units(order_value<E::kLowBits>(k), ex, sm.table) : 1;
+            uint64_t ahead = 0;
+            for (int j = 0; j < (int)n; ++j) {
+              const uint32_t other = __shfl_sync(0xffffffffu, k, j);
+              const uint64_t its = __shfl_sync(0xffffffffu, w, j);
+              if (other > k) ahead += its;
+              if (other == k) ++same;
+            }
+            if (lane < n && ahead < *target && *target <= ahead + same * w)  // (the same in equal keys' lanes)
+              sm.range_key = k, sm.range_count = same, sm.range_before = ahead;
+          }
+          __syncthreads();
+          *target -= sm.range_before;
+          *equal = sm.range_count;
+          klo = sm.range_key;
+          sync_all();  // the keys have been read
+          break;
+        }
+        sync_all();
         pick(by_mass, width, &klo, &khi, target, equal);
         if (width == 0) break;
       }
@@ -857,7 +1019,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
         }
         at += n;
       }
-      cluster.sync();
+      sync_all();
     }
     // top-k leaves the bins up to bin_k, of that one the first k_rank tokens
     const int bin_k = with_k ? sm.bin_k : bins - 1;
@@ -873,7 +1035,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
       uint32_t klo, khi;
       bin_keys(bin_k, bin_k, &klo, &khi);
       const float least = order_value<E::kLowBits>(klo);
-      Shared* to = cluster.map_shared_rank(&sm, 0);
+      Shared* to = &of(0);
       each_granule([&](const float (&x)[kVec], int p) {
         bool any = false;
 #pragma unroll
@@ -883,7 +1045,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
           for (int k = 0; k < kVec; ++k)
             if (x[k] >= least) to->list.key[atomicAdd(&to->listed, 1u) % kList] = sort_key(x[k], p + k);
       });
-      cluster.sync();
+      sync_all();
       if (rank == 0) {
         const int place = draw_listed(sm, ex, top_listed, (uint32_t)top_k, with_p, p64, min_p, u64);
         if (tid == 0) a.token[row] = place - shift;
@@ -897,135 +1059,148 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
       found = !with_p;
       if (with_p) {
         uint64_t all = 0, tiny_all = 0, own = 0, block;
-        for (int r = 0; r < C; ++r) tiny_all += *cluster.map_shared_rank(&sm.tiny, r);
+        for (int r = 0; r < C; ++r) tiny_all += of(r).tiny;
         auto bin_mass = [&](int b) -> uint64_t {
           if (b == tiny_bin) return tiny_all;
           const uint32_t n = b == bin_k ? min(sm.hist[b], k_rank) : sm.hist[b];
           return n ? n * weight_units(number_value(top_number - b), ex, sm.table) : 0ull;
         };
         const int stop = min(bin0 + per, bin_k + 1);
-        for (int b = bin0; b < stop; ++b) own += bin_mass(b);
+        for (int b = bin0; b < stop; b += 2) {
+          // (of a row with one bin less than two, or of number 0, the value is not looked at)
+          int32_t h[2], l[2];
+          weights_of(make_float2(number_value(top_number - b), number_value(top_number - b - 1)), ex, sm.table, h, l);
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (b + j < stop)
+              own += b + j == tiny_bin ? tiny_all
+                                       : units(h[j], l[j]) * (b + j == bin_k ? min(sm.hist[b + j], k_rank) : sm.hist[b + j]);
+        }
         uint64_t ahead = block_scan(own, sm.warp_u64, &block);
         if (tid == 0) sm.sum_a = block;
-        cluster.sync();
+        sync_all();
         for (int r = 0; r < C; ++r) {
-          const uint64_t m = *cluster.map_shared_rank(&sm.sum_a, r);
+          const uint64_t m = of(r).sum_a;
           if (r < rank) ahead += m;
           all += m;
         }
         const uint64_t target = least_mass(all);
-        if (ahead < target && ahead + own >= target) {  // one thread of the cluster
-          for (int b = bin0; b < stop; ++b) {
-            const uint64_t m = bin_mass(b);
-            if (ahead + m >= target) {
-              to_all(&Shared::bin_p, b);
-              to_all(&Shared::bin_p_left, target - ahead);
-              to_all(&Shared::bin_p_count, sm.hist[b]);
-              break;
-            }
-            ahead += m;
+        // one thread of the cluster has the bin; its warp looks at that thread's bins
+        const uint32_t who = __ballot_sync(0xffffffffu, ahead < target && ahead + own >= target);
+        if (who) {
+          const int owner = __ffs(who) - 1;
+          const int b = __shfl_sync(0xffffffffu, bin0, owner) + lane;
+          const uint64_t m = lane < per && b <= bin_k ? bin_mass(b) : 0;
+          const uint64_t upto = __shfl_sync(0xffffffffu, ahead, owner) + warp_scan(m, lane);
+          if (lane == __ffs(__ballot_sync(0xffffffffu, upto >= target)) - 1) {
+            const uint64_t w = b == tiny_bin ? 0 : weight_units(number_value(top_number - b), ex, sm.table);
+            to_all(&Shared::bin_p, b);
+            to_all(&Shared::bin_p_keep, w > 0 ? (uint32_t)((target - (upto - m) + w - 1) / w) : sm.hist[b]);
           }
         }
-        cluster.sync();
+        sync_all();
         if (sm.bin_p != tiny_bin) {
-          const float x = number_value(top_number - sm.bin_p);
-          const uint64_t w = weight_units(x, ex, sm.table);
-          const uint32_t keep = w > 0 ? (uint32_t)((sm.bin_p_left + w - 1) / w) : sm.bin_p_count;
-          if (!with_k || sm.bin_p != bin_k || keep < cut_keep) cut_x = x, cut_keep = keep;
+          if (!with_k || sm.bin_p != bin_k || sm.bin_p_keep < cut_keep)
+            cut_x = number_value(top_number - sm.bin_p), cut_keep = sm.bin_p_keep;
           found = true;
         }
       }
     }
     if (!found) {
-      int b_lo = 0, b_hi = bins - 1;
+      // The bins around the one where top-p's mass is reached if every token of a bin had its middle
+      // value; where the exact masses show that it was not there, all bins are taken.
+      int b_lo = 0, b_hi = bin_k;
       if (with_p) {
-        // bounds of the mass up to each bin, of what top-k leaves; 10^-3 covers the rounding of
-        // bounds and sums
-        auto bounds = [&](int b, float* lo, float* hi) {
-          uint32_t n = sm.hist[b];
-          if (b == bin_k) n = min(n, k_rank);
-          if (b > bin_k) n = 0;
+        auto bin_mass = [&](int b) {
+          const uint32_t n = b > bin_k ? 0 : b == bin_k ? min(sm.hist[b], k_rank) : sm.hist[b];
           const int v = top_number - b;
-          constexpr float kNear = 1.f / 1024;
-          const float x_hi = v > 0 ? number_value(v + 1) : v == 0 ? kNear : number_value(v);
-          const float x_lo = v > 0 ? number_value(v) : v == 0 ? -kNear : number_value(v - 1);
-          *lo = (float)n * ex2_approx((x_lo - mx) * ex.hi) * 0.999f;
-          *hi = (float)n * ex2_approx(fminf((x_hi - mx) * ex.hi, 0.f)) * 1.001f;
+          const float middle =
+              v == 0 ? 0.f : __uint_as_float(__float_as_uint(number_value(v)) | (E::kLowBits ? 0u : 0x8000u));
+          return (float)n * ex2_approx(fminf((middle - mx) * ex.hi, 0.f));
         };
-        float own_lo = 0.f, own_hi = 0.f, lo, hi, all_lo, all_hi;
-        for (int b = bin0; b < bin0 + per && b < bins; ++b) bounds(b, &lo, &hi), own_lo += lo, own_hi += hi;
-        float cum_lo = block_scan(own_lo, sm.warp_f, &all_lo), cum_hi = block_scan(own_hi, sm.warp_g, &all_hi);
-        if (tid == 0) sm.sum_lo = all_lo, sm.sum_hi = all_hi, sm.bracket_lo = sm.bracket_hi = bins - 1;
-        cluster.sync();
-        all_lo = all_hi = 0.f;
+        float own = 0.f, all;
+        for (int b = bin0; b < bin0 + per && b < bins; ++b) own += bin_mass(b);
+        float cum = block_scan(own, sm.warp_f, &all);
+        if (tid == 0) sm.sum_f = all, sm.bin_middle = bin_k;
+        sync_all();
+        all = 0.f;
         for (int r = 0; r < C; ++r) {
-          const float l = *cluster.map_shared_rank(&sm.sum_lo, r), h = *cluster.map_shared_rank(&sm.sum_hi, r);
-          if (r < rank) cum_lo += l, cum_hi += h;
-          all_lo += l, all_hi += h;
+          const float m = of(r).sum_f;
+          if (r < rank) cum += m;
+          all += m;
         }
-        for (int b = bin0; b < bin0 + per && b < bins; ++b) {
-          bounds(b, &lo, &hi);
-          cum_lo += lo, cum_hi += hi;
-          if (cum_hi >= top_p * all_lo * 0.999f) atomicMin(&sm.bracket_lo, b);
-          if (cum_lo >= top_p * all_hi * 1.001f) atomicMin(&sm.bracket_hi, b);
-        }
-        cluster.sync();
-        b_lo = b_hi = bins - 1;
-        for (int r = 0; r < C; ++r) {
-          b_lo = min(b_lo, *cluster.map_shared_rank(&sm.bracket_lo, r));
-          b_hi = min(b_hi, *cluster.map_shared_rank(&sm.bracket_hi, r));
-        }
-        b_hi = min(b_hi, bin_k);
-        b_lo = min(b_lo, b_hi);
+        if (cum + own >= top_p * all)
+          for (int b = bin0; b < bin0 + per && b < bins; ++b) {
+            cum += bin_mass(b);
+            if (cum >= top_p * all) atomicMin(&sm.bin_middle, b);
+          }
+        sync_all();
+        for (int r = 0; r < C; ++r) b_hi = min(b_hi, of(r).bin_middle);
+        b_lo = max(b_hi - 1, 0), b_hi = min(b_hi + 1, bin_k);
       }
-      cluster.sync();  // the histograms and brackets have been read
+      sync_all();  // the histograms and middles have been read
       uint32_t floor_key = 0, klo, khi, equal;
       if (with_k) {
         uint64_t left = k_rank;
         bin_keys(bin_k, bin_k, &klo, &khi);
-        floor_key = refine(klo, khi, false, &left, &equal);
+        floor_key = refine(klo, khi, false, false, &left, &equal);
         cut_x = order_value<E::kLowBits>(floor_key);
         cut_keep = (uint32_t)left;
       }
       if (with_p) {
-        // In one pass the exact masses of what top-k leaves, of its part above the bracket, and of the
-        // ranges of the bracket (of the tokens equal to top-k's cut, all: they come last)
-        bin_keys(b_lo, b_hi, &klo, &khi);
-        klo = max(klo, floor_key);
-        const int width = range_width(klo, khi);
-        clear_ranges();
-        uint32_t all_h = 0, top_h = 0;
-        int32_t all_l = 0, top_l = 0;
-        each([&](float x, int) {
-          const uint32_t k = order_key<E::kLowBits>(x);
-          if (k >= floor_key && x != -INFINITY) {  // (few tokens, below a top-k cut)
-            int32_t h, l;
-            weight_of(x, ex, sm.table, &h, &l);
-            if (k > floor_key) all_h += h, all_l += l;
-            if (k > khi) {
-              top_h += h, top_l += l;
-            } else if (k >= klo) {
-              atomicAdd(&sm.r.count[(k - klo) >> width], 1u);
-              add_mass((k - klo) >> width, units(h, l));
+        // In one pass the exact masses of what top-k leaves, of its part above these bins, and of their
+        // ranges (of the tokens equal to top-k's cut, all: they come last)
+        uint64_t left;
+        int width;
+#pragma unroll 1
+        for (int attempt = 0; attempt < 2; ++attempt, b_lo = 0, b_hi = bin_k) {
+          bin_keys(b_lo, b_hi, &klo, &khi);
+          klo = max(klo, floor_key);
+          width = range_width(klo, khi);
+          clear_ranges(true);
+          uint32_t all_h = 0, top_h = 0;
+          int32_t all_l = 0, top_l = 0;
+          each_granule([&](const float (&x)[kVec], int) {
+            uint32_t k[kVec];
+            bool any = false;
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) k[j] = order_key<E::kLowBits>(x[j]), any |= k[j] >= floor_key;
+            if (!any) return;  // (most, where there is a top-k cut)
+#pragma unroll
+            for (int j = 0; j < kVec; j += 2) {
+              int32_t h[2], l[2];
+              weights_of(make_float2(x[j], x[j + 1]), ex, sm.table, h, l);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t key = k[j + i];
+                if (key > floor_key) all_h += h[i], all_l += l[i];
+                if (key > khi) {
+                  top_h += h[i], top_l += l[i];
+                } else if (key >= klo) {
+                  atomicAdd(&sm.r.count[(key - klo) >> width], 1u);
+                  add_mass((key - klo) >> width, units(h[i], l[i]));
+                  list_key(key);
+                }
+              }
             }
+          });
+          uint64_t all = warp_add(units(all_h, all_l)), top = warp_add(units(top_h, top_l));
+          if (lane == 0) sm.warp_u64[warp] = all, sm.warp_u64b[warp] = top;
+          __syncthreads();
+          if (tid == 0) {
+            all = top = 0;
+            for (int w = 0; w < kWarps; ++w) all += sm.warp_u64[w], top += sm.warp_u64b[w];
+            sm.sum_a = all, sm.sum_b = top;
           }
-        });
-        uint64_t all = warp_add(units(all_h, all_l)), top = warp_add(units(top_h, top_l));
-        if (lane == 0) sm.warp_u64[warp] = all, sm.warp_u64b[warp] = top;
-        __syncthreads();
-        if (tid == 0) {
-          all = top = 0;
-          for (int w = 0; w < kWarps; ++w) all += sm.warp_u64[w], top += sm.warp_u64b[w];
-          sm.sum_a = all, sm.sum_b = top;
+          sync_all();
+          all = with_k ? (uint64_t)cut_keep * weight_units(cut_x, ex, sm.table) : 0, top = 0;
+          for (int r = 0; r < C; ++r)
+            all += of(r).sum_a, top += of(r).sum_b;
+          const uint64_t least = least_mass(all);
+          left = least - top;  // (0, or over 2^63, where the cut lies above these bins)
+          if (pick(true, width, &klo, &khi, &left, &equal)) break;
         }
-        cluster.sync();
-        all = with_k ? (uint64_t)cut_keep * weight_units(cut_x, ex, sm.table) : 0, top = 0;
-        for (int r = 0; r < C; ++r)
-          all += *cluster.map_shared_rank(&sm.sum_a, r), top += *cluster.map_shared_rank(&sm.sum_b, r);
-        const uint64_t least = least_mass(all);
-        uint64_t left = least > top ? least - top : 1;
-        pick(true, width, &klo, &khi, &left, &equal);
-        if (width > 0) klo = refine(klo, khi, true, &left, &equal);
+        if (width > 0) klo = refine(klo, khi, true, true, &left, &equal);
         const float x = order_value<E::kLowBits>(klo);
         const uint64_t w = weight_units(x, ex, sm.table);
         const uint32_t keep = w > 0 ? (uint32_t)min((left + w - 1) / w, (uint64_t)equal) : equal;
@@ -1036,7 +1211,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
   }
   if (min_p > 0.f) {
     // w >= min_p  <=>  x >= max + T ln(min_p)
-    const float x = __double2float_ru((double)mx + sm.min_p_offset);
+    const float x = sum_rounded_up(mx, sm.ln_hi, sm.ln_lo);
     if (x > cut_x) cut_x = x, cut_keep = kAllEqual;
   }
 
@@ -1050,10 +1225,26 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
   const float over_about = fmaxf(over, x_zero);  // (x_zero < mx where |max c| < kAboutMax)
   auto draw = [&](auto exactly) {
     constexpr bool exact = decltype(exactly)::value;
-    // a token's weight, if it is above the cut
-    auto weight = [&](float x) -> uint64_t {
-      if (exact) return x > over ? weight_units(x, ex, sm.table) : 0;
-      return x > over_about ? about_units(about_of(x, ab)) : 0;
+    // the weights of a granule's tokens above the cut: each in units, or their sum, and how many are equal to it
+    auto about_weights = [&](const float (&x)[kVec], float (&w)[kVec]) {
+      about_all(x, ab, w);
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) w[k] = x[k] > over_about ? w[k] : 0.f;
+    };
+    auto mass = [&](const float (&x)[kVec], uint32_t* equal) -> uint64_t {
+      *equal = 0;
+      if (partial)
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) *equal += x[k] == cut_x ? 1u : 0u;
+      if (exact) {
+        uint64_t m = 0;
+#pragma unroll 1
+        for (int k = 0; k < kVec; ++k) m += x[k] > over ? weight_units(x[k], ex, sm.table) : 0;
+        return m;
+      }
+      float w[kVec];
+      about_weights(x, w);
+      return about_units(tree_sum(w));
     };
     const uint64_t w_cut =
         !partial ? 0 : exact ? weight_units(cut_x, ex, sm.table) : cut_x >= x_zero ? about_units(about_of(cut_x, ab)) : 0;
@@ -1064,28 +1255,25 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     if (exact) {
       uint32_t h = 0;
       int32_t l = 0;
-      each_small([&](float x) {
-        int32_t wh, wl;
-        weight_of(x, ex, sm.table, &wh, &wl);
-        h += x > over ? wh : 0;
-        l += x > over ? wl : 0;
-        same += partial && x == cut_x ? 1u : 0u;
+      each_raw([&](const uint4& v, const float (&)[kVec], int) {
+        E::each_pair(v, [&](float2 x) {
+          int32_t wh[2], wl[2];
+          weights_of(x, ex, sm.table, wh, wl);
+          h += (x.x > over ? wh[0] : 0) + (x.y > over ? wh[1] : 0);
+          l += (x.x > over ? wl[0] : 0) + (x.y > over ? wl[1] : 0);
+          if (partial) same += (x.x == cut_x ? 1u : 0u) + (x.y == cut_x ? 1u : 0u);
+        });
       });
       sum = units(h, l);
     } else {
       float s = 0.f, e = 0.f;  // the sum in two floats
       each_granule([&](const float (&x)[kVec], int) {
         float w[kVec];
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) w[k] = x[k] > over_about ? about_of(x[k], ab) : 0.f;
+        about_weights(x, w);
         if (partial)
 #pragma unroll
           for (int k = 0; k < kVec; ++k) same += x[k] == cut_x ? 1u : 0u;
-#pragma unroll
-        for (int o = kVec / 2; o > 0; o >>= 1)
-#pragma unroll
-          for (int k = 0; k < o; ++k) w[k] = __fadd_rn(w[k], w[k + o]);
-        add_in_two(w[0], &s, &e);
+        add_in_two(tree_sum(w), &s, &e);
       });
       sum = about_units(s, e);
     }
@@ -1100,12 +1288,12 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
       for (int w = 0; w < kWarps; ++w) s += sm.warp_u64[w], n += sm.warp_u32[w];
       sm.sum_a = s, sm.count = n;
     }
-    cluster.sync();
+    sync_all();
     uint64_t all = 0, before = 0, here = 0;  // mass of the row, of the CTAs before this one, and of this one
     uint32_t ahead = 0, seen = 0;            // tokens equal to cut_x before this CTA; before CTA r
     for (int r = 0; r < C; ++r) {
-      const uint32_t n = *cluster.map_shared_rank(&sm.count, r);
-      const uint64_t m = *cluster.map_shared_rank(&sm.sum_a, r) + equals(seen, seen + n);
+      const uint32_t n = of(r).count;
+      const uint64_t m = of(r).sum_a + equals(seen, seen + n);
       if (r == rank) before = all, here = m, ahead = seen;
       all += m;
       seen += n;
@@ -1113,61 +1301,64 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     // the token's running sum is the first above `goal` = floor(u all)
     const uint64_t goal = __umul64hi(u64, all);
     if (before <= goal && goal < before + here) {  // one CTA of the cluster
-      int w0 = 0;
-      for (; w0 < kWarps - 1; ++w0) {
-        const uint64_t m = sm.warp_u64[w0] + equals(ahead, ahead + sm.warp_u32[w0]);
-        if (goal < before + m) break;
-        before += m;
-        ahead += sm.warp_u32[w0];
-      }
+      // Of 32 runs of places, this lane's of mass m with n tokens equal to cut_x, the one that holds the
+      // goal, or -1: the last one that begins at or before it.  `before` and `ahead` move to its start.
+      auto run_of = [&](uint64_t m, uint32_t n) {
+        const uint32_t nth = ahead + warp_scan(n, lane) - n;
+        m += equals(nth, nth + n);
+        const uint64_t upto = before + warp_scan(m, lane);
+        const uint32_t past = __ballot_sync(0xffffffffu, upto > goal);
+        const int at = past ? __ffs(past) - 1 : 31;
+        before = __shfl_sync(0xffffffffu, past ? upto - m : upto, at);
+        ahead = __shfl_sync(0xffffffffu, past ? nth : nth + n, at);
+        return past ? at : -1;
+      };
+      const int w0 = max(run_of(lane < kWarps ? sm.warp_u64[lane] : 0, lane < kWarps ? sm.warp_u32[lane] : 0), 0);
       // that warp's places, one iteration's per warp of this CTA
       for (int i = warp; i < iters; i += kWarps) {
         float x[kVec];
         values(fetch(w0, i), x);
-        uint64_t m = 0;
-        uint32_t n = 0;
-#pragma unroll(exact ? 1 : kVec)
-        for (int k = 0; k < kVec; ++k) m += weight(x[k]), n += partial && x[k] == cut_x ? 1u : 0u;
+        uint32_t n;
+        uint64_t m = mass(x, &n);
         m = warp_add(m);
         n = warp_add(n);
         if (lane == 0) sm.chunk[i] = m, sm.chunk_same[i] = n;
       }
       __syncthreads();
       if (warp == 0) {
-        int i = 0;
-        for (; i < iters - 1; ++i) {
-          const uint64_t m = sm.chunk[i] + equals(ahead, ahead + sm.chunk_same[i]);
-          if (goal < before + m) break;
-          before += m;
-          ahead += sm.chunk_same[i];
+        int i = -1;
+        for (int i0 = 0; i < 0 && i0 < iters; i0 += 32) {
+          const bool in = i0 + lane < iters;
+          const int at = run_of(in ? sm.chunk[i0 + lane] : 0, in ? sm.chunk_same[i0 + lane] : 0);
+          if (at >= 0) i = i0 + at;
         }
+        i = max(i, 0);  // (in single precision the parts can miss the sum of the whole)
         float x[kVec];
-        uint64_t m = 0, w[kVec];
-        uint32_t n = 0;
         values(fetch(w0, i), x);
+        uint32_t n;
+        const uint64_t m = mass(x, &n);
+        const int lane_at = run_of(m, n);
+        if (lane == lane_at) {
+          // (before and ahead are this lane's now)
+          float w[kVec];
+          if (!exact) about_weights(x, w);
 #pragma unroll(exact ? 1 : kVec)
-        for (int k = 0; k < kVec; ++k) m += w[k] = weight(x[k]), n += partial && x[k] == cut_x ? 1u : 0u;
-        uint32_t nth = ahead + warp_scan(n, lane) - n;
-        uint64_t at = m + equals(nth, nth + n);
-        const uint64_t mine = at;
-        at = before + warp_scan(at, lane) - at;
-        if (at <= goal && goal < at + mine) {
-#pragma unroll 1
           for (int k = 0; k < kVec; ++k) {
             const bool eq = partial && x[k] == cut_x;
-            const uint64_t own = eq ? equals(nth, nth + 1) : w[k];
-            if (eq) ++nth;
-            if (at <= goal && goal < at + own) {
+            const uint64_t own = eq ? equals(ahead, ahead + 1)
+                                    : !exact ? about_units(w[k]) : x[k] > over ? weight_units(x[k], ex, sm.table) : 0;
+            if (eq) ++ahead;
+            if (before <= goal && goal < before + own) {
               a.token[row] = (rank * kWarps + w0) * seg + i * kStep + lane * kVec + k - shift;
               const uint64_t margin = about_margin(u, all);
-              if (goal - at >= margin && at + own - goal > margin) to_all(&Shared::sure, 1);
+              if (goal - before >= margin && before + own - goal > margin) to_all(&Shared::sure, 1);
             }
-            at += own;
+            before += own;
           }
         }
       }
     }
-    cluster.sync();  // sm.sure is settled, and no CTA leaves while another reads its shared memory
+    sync_all();  // sm.sure is settled, and no CTA leaves while another reads its shared memory
   };
   bool sure = false;
   if (fabsf(mx * ex.hi) < kAboutMax) {
@@ -1457,14 +1648,20 @@ sample_plain_exact_kernel(const SampleArgs a, const __grid_constant__ ExpTable e
         for (int r = 0; r < C; ++r) mx = fmaxf(mx, *cluster.map_shared_rank(&sm.x_max, r));
         const bool only_inf = mx == INFINITY;  // tokens at +inf share the draw evenly
         const Exponent ex = {only_inf ? 0.f : mx, sm.exp_hi, sm.exp_lo};
-        auto weight = [&](int p) {
+        auto scaled = [&](int p) {
           const float x = logit(p);
-          return weight_units(!only_inf ? x : x == INFINITY ? 0.f : -INFINITY, ex, sm.table);
+          return !only_inf ? x : x == INFINITY ? 0.f : -INFINITY;
+        };
+        auto weight = [&](int p) { return weight_units(scaled(p), ex, sm.table); };
+        auto weight2 = [&](int p) {  // of two places
+          int32_t h[2], l[2];
+          weights_of(make_float2(scaled(p), scaled(p + 1)), ex, sm.table, h, l);
+          return units((int64_t)h[0] + h[1], (int64_t)l[0] + l[1]);
         };
         uint64_t sum = 0;
         for (int i = 0; i < iters; ++i)
-#pragma unroll 2
-          for (int k = 0; k < kVec; ++k) sum += weight(first + i * kStep + k);
+#pragma unroll 1
+          for (int k = 0; k < kVec; k += 2) sum += weight2(first + i * kStep + k);
         sum = warp_add(sum);
         if (lane == 0) sm.warp_u64[warp] = sum;
         __syncthreads();
@@ -1488,7 +1685,7 @@ sample_plain_exact_kernel(const SampleArgs a, const __grid_constant__ ExpTable e
           for (int i = warp; i < iters; i += kWarps) {
             uint64_t m = 0;
 #pragma unroll 1
-            for (int k = 0; k < kVec; ++k) m += weight(start + i * kStep + k);
+            for (int k = 0; k < kVec; k += 2) m += weight2(start + i * kStep + k);
             m = warp_add(m);
             if (lane == 0) sm.chunk[i] = m;
           }
@@ -1498,7 +1695,7 @@ sample_plain_exact_kernel(const SampleArgs a, const __grid_constant__ ExpTable e
             for (; i < iters - 1 && before + sm.chunk[i] <= goal; ++i) before += sm.chunk[i];
             uint64_t m = 0;
 #pragma unroll 1
-            for (int k = 0; k < kVec; ++k) m += weight(start + i * kStep + k);
+            for (int k = 0; k < kVec; k += 2) m += weight2(start + i * kStep + k);
             uint64_t upto = before + warp_scan(m, lane) - m;
             if (upto <= goal && goal < upto + m) {
               int k = 0;
@@ -1513,13 +1710,15 @@ sample_plain_exact_kernel(const SampleArgs a, const __grid_constant__ ExpTable e
   }
 }
 
-// CTAs per row: more while all of them are resident (two on each SM), eight only while that leaves SMs
-// idle, and more while one CTA's share of a row is over 20 iterations (160 KB); the row stays in shared
-// memory where a share is at most 64 KB.  Measured, us by cluster size 1 / 2 / 4 / 8 (kept where marked *):
-// top-p of 131,072 bf16: 512 rows 169 / 176 / 216* / 366*, 150 rows 63 / 55 / 82* / 118*, 64 rows 60 / 42 / 35* /
-// 55*, 16 rows 58 / 41 / 26* / 27*; all filters of 151,001 fp32: 128 rows - / 168 / 130 / 154, 16 rows - / 91 / 63 /
-// 55; all filters of 32,000 bf16: 400 rows 48* / 62* / 92* / 161* (not kept 54 / 69 / 101 / 177), 100 rows 30* /
-// 28* / 34* / 49*.
+// CTAs per row: more while that leaves SMs idle, or while rows are long (over 8 iterations a CTA) and most of
+// the CTAs still find room at once (clusters do not fill every SM: 76 rows by four did not fit); eight only
+// while SMs idle.  More too while one CTA's share of a row is over 40 iterations (164,000 bf16; 320 KB), of fp32,
+// whose longest rows take more passes, over 20; the row stays in shared memory where a share is at most 64 KB.
+// Measured, us by cluster size 1 / 2 / 4 / 8, top-p of 131,072 bf16: 512 rows 146 / 164 / 210 / 363, 150 rows 55 / 52 /
+// 81 / 118, 76 rows 52 / 39 / 53 / 71, 64 rows 52 / 38 / 34 / 54, 16 rows 49 / 37 / 25 / 27; all filters of 151,001
+// fp32: 512 rows - / 344 / 318 / 422, 128 rows - / 154 / 113 / 120, 16 rows - / 67 / 47 / 40; of 64,000: 512 rows 185 /
+// 156 / 161 / 288; all filters of 32,000 bf16: 400 rows 43 / 64 / 97 / 173, 100 rows 25 / 29 / 35 / 52, 8 rows 23 / 23 /
+// 21 / 19.
 struct Shape {
   int cluster, iters;
   bool keep;
@@ -1536,9 +1735,13 @@ Shape choose_shape(const SampleArgs& a, int sms) {
   auto need = [&](int c) { return iterations<T>(a, c); };
   Shape s;
   s.cluster = 1;  // (a vocabulary of up to kList tokens stays in one CTA: one iteration holds it)
-  while (s.cluster < kMaxCluster && need(s.cluster) > 1 &&
-         (a.rows * s.cluster * 2 <= (s.cluster == 4 ? 1 : 2) * sms || need(s.cluster) > 20))
+  constexpr int kLong = Elems<T>::kLowBits ? 40 : 20;
+  while (s.cluster < kMaxCluster && need(s.cluster) > 1) {
+    const int64_t ctas = a.rows * s.cluster * 2;
+    const int room = s.cluster == 4 ? sms : sms + sms * 3 / 4;
+    if (!(need(s.cluster) > kLong || ctas <= sms / 2 || (need(s.cluster) > 8 && ctas <= room))) break;
     s.cluster *= 2;
+  }
   s.keep = need(s.cluster) <= kKeepIters;
   while (s.cluster < kMaxCluster && need(s.cluster) > kMaxElems / Elems<T>::kVec) s.cluster *= 2;
   s.iters = need(s.cluster);
