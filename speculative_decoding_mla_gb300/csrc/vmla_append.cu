@@ -9,8 +9,8 @@
 // turned by the same angles, so one launch serves both: the row goes to the
 // token's slot (bf16, or e4m3 codes of value / scale), the queries into the
 // last 64 columns of q.  Products and sums are fp32, rounded once at the store;
-// the division by the scale is a true one, since a reciprocal's rounding would
-// move values across code borders.
+// quotients by the scale are correctly rounded, since a reciprocal's rounding
+// would move values across code borders.
 //
 // A token costs 1152 bytes in, 256 of table, 1152 (or 576) out and 256 per
 // head, and nothing is read twice, so the kernel is bound by memory for many
@@ -19,10 +19,14 @@
 // 16-byte granules g and g + 4 of a 64-wide part (g = lane & 3), which contain
 // whole pairs in either pairing, and its 8 cosines and sines serve every head of
 // the warp.  The data loads do not depend on the slot or the position and are
-// issued with them.  32 heads (eight loads per lane in flight, four blocks on an
+// issued with them.  32 heads (eight loads per lane in flight, 32 warps on an
 // SM) pay off where there are many tokens of more than 16 heads: 16,384 x 64
-// heads take 55.5 us (5.6 TB/s) against 57.5 with 16; 16,001 x 16 heads, e4m3,
-// 28.9 against 26.0 us; 144 x 64 heads 4.2 against 3.8 us.
+// heads took 55.5 us against 57.5 with 16; 16,001 x 16 heads, e4m3, 28.9 against
+// 26.0 us; 144 x 64 heads 4.2 against 3.8 us.  Blocks of four warps leave an SM
+// in smaller steps than blocks of eight: 53.6 us (5.8 TB/s) against 55.4, and 5,000
+// x 16 heads, e4m3, 8.7 against 10.2; of two warps, or 48 warps on an SM, gain
+// nothing.  16,001 x 16 heads take 22.6 us in both types (4.7 and 4.3 TB/s), of which
+// 10.4 to 12.4 are the cache rows'; rows two or four to a warp took longer.
 #include <cuda_runtime.h>
 
 #include "vmla_device.cuh"
@@ -30,7 +34,7 @@
 namespace vmla {
 namespace {
 
-constexpr int kAppendWarps = 8;
+constexpr int kAppendWarps = 4;                               // of a block
 constexpr int kHeadsPerPass = 8;                              // heads a warp instruction covers (4 lanes each)
 constexpr int kRopeDim = kDqk - kDv;                          // 64
 constexpr int kLatentU4 = kDv / 8;                            // 64 granules
@@ -89,27 +93,47 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     pack_bf16x2(x[6], x[7]));
 }
 
+// x / scale of two values, correctly rounded, given r = 1 / scale correctly rounded: the estimate x r is moved
+// twice by the exact remainder times r (Markstein, IBM J. Res. Dev. 34, 1990).  For scales from 2^-60 to 2^60,
+// where no remainder that a code could show falls below the smallest float; estimates that are not below 1024
+// (infinities and NaN too) are left as they are, beyond the largest code.  (Remainders are taken as
+// q scale - x, so that a zero keeps its sign.)
+__device__ __forceinline__ float2 quotients(float2 x, float scale, float r) {
+  float2 q0, q;
+  asm("{.reg .b64 x, n, s, m, q, e;\n\tmov.b64 x, {%4, %5};\n\tmov.b64 s, {%6, %6};\n\tmov.b64 m, {%7, %7};\n\t"
+      "mov.b64 q, {%8, %8};\n\tmul.rn.f32x2 q, x, q;\n\tmov.b64 {%0, %1}, q;\n\t"
+      "mov.b64 n, {%9, %9};\n\tmul.rn.f32x2 n, x, n;\n\t"
+      "fma.rn.f32x2 e, q, s, n;\n\tfma.rn.f32x2 q, e, m, q;\n\t"
+      "fma.rn.f32x2 e, q, s, n;\n\tfma.rn.f32x2 q, e, m, q;\n\tmov.b64 {%2, %3}, q;}"
+      : "=f"(q0.x), "=f"(q0.y), "=f"(q.x), "=f"(q.y)
+      : "f"(x.x), "f"(x.y), "f"(scale), "f"(-r), "f"(r), "f"(-1.f));
+  return make_float2(fabsf(q0.x) < 1024.f ? q.x : q0.x, fabsf(q0.y) < 1024.f ? q.y : q0.y);
+}
+
 // Eight values -> eight e4m3 codes of value / scale (nearest even, beyond 448 the largest code).
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
   uint32_t w[4];
+  const float r = __frcp_rn(scale);
+  const bool usual = scale >= 0x1p-60f && scale <= 0x1p60f;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
+    const float2 v = make_float2(x[2 * k], x[2 * k + 1]);
+    const float2 q =
+        usual ? quotients(v, scale, r) : make_float2(__fdiv_rn(v.x, scale), __fdiv_rn(v.y, scale));
     uint16_t c;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-        : "=h"(c)
-        : "f"(__fdiv_rn(x[2 * k + 1], scale)), "f"(__fdiv_rn(x[2 * k], scale)));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(q.y), "f"(q.x));
     w[k] = c;
   }
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
 template <int kPasses>
-__global__ void __launch_bounds__(kAppendWarps * 32, kPasses == 4 ? 4 : 5)
+__global__ void __launch_bounds__(kAppendWarps * 32, kPasses == 4 ? 8 : 10)
 append_kernel(const AppendArgs a, int parts) {
   constexpr int kHeadsPerWarp = kHeadsPerPass * kPasses;
   const int lane = threadIdx.x & 31, g = lane & 3;
   const int64_t unit = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);  // warp-uniform
-  const int64_t t = unit / parts;
+  const int64_t t = a.tokens * parts <= UINT32_MAX ? (int64_t)((uint32_t)unit / (uint32_t)parts) : unit / parts;
   const int part = (int)(unit - t * parts);  // 0: the cache row; p > 0: heads from (p - 1) kHeadsPerWarp on
   if (t >= a.tokens) return;
   const int32_t slot = __ldg(a.slots + t), pos = __ldg(a.positions + t);

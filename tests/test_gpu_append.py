@@ -255,3 +255,20 @@ def test_binding_refuses_mismatched_arrays():
         _call(binding, c, status_word=torch.zeros(1, dtype=torch.int32, device="cuda"))
     with pytest.raises(ValueError):
         _call(binding, c, kv_scale=0.1)  # an e4m3 pool has one-byte elements
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.1, 3.0, 0.0333333, 1e-4, 7.7e3, 2.0 ** -60, 2.0 ** 60, 1e-25, 1e-38, 1e25, 3e38])
+def test_e4m3_quotients_are_rounded_as_a_division_rounds(scale):
+    """Every bf16 pattern but NaN, divided in float32 (one rounding) and converted (another): the same codes, also for
+    zeros' signs, infinities, subnormal values and scales at the ends of the range."""
+    torch, binding = _mods()
+    c = _case(128, 0, 128, seed=6)
+    every = torch.arange(65536, device="cuda", dtype=torch.int32).to(torch.int16).view(torch.bfloat16).view(128, 512)
+    c["latent"] = torch.where(every.isnan(), torch.zeros_like(every), every).contiguous()
+    c["pool"] = torch.zeros((128, 576), dtype=torch.uint8, device="cuda")
+    _call(binding, c, kv_scale=scale)
+    s32 = np.float32(scale)
+    with np.errstate(over="ignore", under="ignore"):
+        q = c["latent"].float().cpu().numpy() / s32
+    want = torch.from_numpy(np.clip(q, -448, 448)).to(torch.float8_e4m3fn).view(torch.uint8)
+    assert torch.equal(c["pool"][c["slots"].long()][:, :512].cpu(), want)
