@@ -21,7 +21,8 @@
 // shared memory; with many, its later passes read it again, from L2, which lets
 // more rows be in work at once.  Where a filter needs the order, the cut is
 // found without sorting, from a histogram of counts over the leading 16 bits of
-// the values (bins_of): one shared-memory atomic per token.
+// the values (bins_of): one shared-memory atomic per token, in the pass that finds
+// the maximum.
 //   bf16: a bin holds one value (but for the bin of the values next to zero), so
 //      the masses are counts times exact weights of some thousand values, and the
 //      histogram alone gives both cuts exactly;
@@ -38,11 +39,12 @@
 // it, the sums are taken again exactly: by the same cluster, or, for calls without
 // any filter (which read a row once, in a kernel of their own), by a second launch.
 //
-// What bounds it: 512 rows of 131,072 bf16 (134 MB, 20 us of reading) take 81 us without a
+// What bounds it: 512 rows of 131,072 bf16 (134 MB, 20 us of reading) take 80 us without a
 // filter, instructions (23 a token: the weight 13, the loop 5, the rest the search), and
-// 145 us with top-p.  There a row is one CTA's, two on an SM, for 64 us: maximum 10, the
-// histogram 22 (its shared-memory atomics, 3.8 cycles a warp for their banks' conflicts,
-// take 28 us of the whole call), cuts 10, the sums of the draw 15, its search 6, barriers.
+// 130 us with top-p.  There a row is one CTA's, two on an SM, for 57 us: maximum and
+// histogram 24 (its shared-memory atomics, 3.8 cycles a warp for their banks' conflicts,
+// take 28 us of the whole call; maximum and histogram in two passes: 145 us), cuts 10, the
+// sums of the draw 15, its search 6, barriers.
 // Tried and not kept: top-p's masses in fp32 by single-precision sums first (a second pass
 // where they do not decide made the longest rows longer: 128 rows of 151,001, 166 ->
 // 191 us), whole rows in shared memory for 512 rows (216 us), undecided rows of the
@@ -104,7 +106,7 @@ struct Shared {
   float ln_hi, ln_lo;      // temperature x ln(min_p)
   // read by the other CTAs of the cluster; a cluster barrier lies between a phase's reads and the
   // slot's next write
-  float x_max;
+  float x_max, first_max;
   uint64_t sum_a, sum_b, tiny;
   float sum_f;
   uint32_t key_lo, key_hi, count, bin_count;
@@ -150,8 +152,9 @@ __device__ __forceinline__ float number_value(int n) {
   const uint32_t b = (uint32_t)((n < 0 ? -n : n) + (kNearZero - 1)) << 16;
   return __uint_as_float(n < 0 ? b | 0x80000000u : b);
 }
+constexpr int kAbove = 128;    // numbers above the largest of the first logits
 constexpr int kLastBins = 32;  // what counts as zero is thrown into these, one for each lane
-static_assert(2 * (25 + 10) * 128 + 1 <= kBins - kLastBins, "every token of weight has a bin");
+static_assert(2 * (25 + 10) * 128 + 1 + kAbove <= kBins - kLastBins, "every token of weight has a bin");
 
 __device__ __forceinline__ uint32_t add2(uint32_t a, uint32_t b) {  // 16-bit halves
   uint32_t r;
@@ -667,8 +670,42 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     sm.ln_hi = (float)l;
     sm.ln_lo = (float)(l - (double)sm.ln_hi);
   }
-  // ---- the row's maximum
+  // ---- the row's maximum, and in the same pass the histogram, where a filter needs the order.  Its bins are
+  // counted from a number an octave above the largest logit of the first granules (an eighth of 131,072
+  // logits, spread over the row): only a row whose maximum is greater still is counted again.
+  bool with_k = top_k > 0 && top_k < a.vocab;
+  const bool with_p = top_p < 1.f, counted = temp > 0.f && (with_k || with_p) && a.vocab > kList;
   typename E::Max run = E::lowest();
+  int top_number = 0;
+  const int last_bin = kBins - kLastBins + lane;
+  auto clear_bins = [&] {
+    for (int b = tid; b < kBins - kLastBins; b += kThreads) sm.hist[b] = 0;
+  };
+  uint32_t nears = 0;  // bit min(i, 31): iteration i's granule of this lane has a value next to zero
+  auto count = [&](const uint4& v, const float (&x)[kVec], int i) {
+    uint32_t bin[kVec];
+    const bool near = bins_of(x, v, top_number, last_bin, bin);
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) atomicAdd(&sm.hist[bin[k]], 1u);
+    if (E::kLowBits && near) nears |= 1u << min(i, 31);
+  };
+  if (counted) {
+    clear_bins();
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f)
+      if (f < iters) E::settle(flight[f], run);
+    float m = warp_max(E::largest(run));
+    if (lane == 0) sm.warp_f[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.warp_f[w]);
+    if (C > 1) {
+      if (tid == 0) sm.first_max = m;
+      sync_all();
+      for (int r = 0; r < C; ++r) m = fmaxf(m, of(r).first_max);
+    }
+    top_number = number_of(m) + kAbove;
+  }
 #pragma unroll 1
   for (int i0 = 0; i0 < iters; i0 += kFlight) {
     uint4 v[kFlight];
@@ -680,11 +717,17 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
       if (i0 + f < iters) {
-        const uint4 x = E::settle(v[f], run);  // NaN counts as -inf
-        if (kKeep) slice[32 * (warp * iters + i0 + f)] = x;
+        const uint4 now = E::settle(v[f], run);  // NaN counts as -inf
+        if (kKeep) slice[32 * (warp * iters + i0 + f)] = now;
+        if (counted) {
+          float x[kVec];
+          E::unpack(now, x);
+          count(now, x, i0 + f);
+        }
       }
     }
   }
+  __syncthreads();  // (warp_f is written again)
   float mx = E::largest(run);
   if (tid == 0) sm.sure = 0, sm.listed = 0, sm.tiny = 0;  // (written from other CTAs only past the barriers below)
   if (tid < 64) sm.table[tid] = exp_table.t[tid];
@@ -809,8 +852,6 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
   constexpr uint32_t kAllEqual = UINT32_MAX;
   float cut_x = -INFINITY;
   uint32_t cut_keep = kAllEqual;
-  bool with_k = top_k > 0 && top_k < a.vocab;
-  const bool with_p = top_p < 1.f;
   if ((with_k || with_p) && a.vocab <= kList) {
     // the whole row goes into a list (of one CTA: its cluster has no other)
     each([&](float x, int p) {
@@ -822,7 +863,14 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     return;
   }
   if (with_k || with_p) {
-    const int top_number = number_of(mx);
+    if (number_of(mx) > top_number) {  // the same in every thread of the cluster
+      top_number = number_of(mx);
+      clear_bins();
+      __syncthreads();
+      nears = 0;
+      each_raw([&](const uint4& v, const float (&x)[kVec], int p) { count(v, x, (p - first) / kStep); });
+      sync_all();
+    }
     // tokens of weight lie above
     const float x_low = fminf(mx, fmaxf(mx - kOctaves * 0.6931472f * temp * 1.0001f, -3.402823466e38f));
     // the bins in use; every CTA sums up an equal run of them
@@ -830,23 +878,30 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     const int per = (bins + C * kThreads - 1) / (C * kThreads);  // consecutive bins of one thread
     const int bin0 = (rank * kThreads + tid) * per;
     const int tiny_bin = top_number;  // of number 0, where it is in use (0 <= top_number < bins)
-    for (int b = tid; b < bins; b += kThreads) sm.hist[b] = 0;
-    __syncthreads();
-    uint64_t tiny = 0;  // exact mass of the values that share the bin next to zero
-    const bool need_tiny = E::kLowBits && with_p && tiny_bin >= 0 && tiny_bin < bins;
-    const int last_bin = kBins - kLastBins + lane;  // (bins from `bins` on are not looked at)
-    each_raw([&](const uint4& v, const float (&x)[kVec], int) {
-      uint32_t bin[kVec];
-      const bool near = bins_of(x, v, top_number, last_bin, bin);
+    if (E::kLowBits && with_p && tiny_bin >= 0 && tiny_bin < bins) {
+      // exact mass of the values that share the bin next to zero (one in 2,500 for logits of deviation 2):
+      // their granules are read again, each lane its own
+      uint64_t tiny = 0;
+      for (uint32_t left = nears; left != 0; left &= left - 1) {
+        const int at = __ffs(left) - 1;
+        for (int i = at; i < (at < 31 ? at + 1 : iters); ++i) {
+          const uint4 v = kKeep ? fetch(warp, i) : E::numbers(fetch(warp, i));
+          float x[kVec];
+          E::unpack(v, x);
+          uint32_t which = 0;
 #pragma unroll
-      for (int k = 0; k < kVec; ++k) atomicAdd(&sm.hist[bin[k]], 1u);
-      if (need_tiny && near)
-#pragma unroll 1
-        for (int k = 0; k < kVec; ++k)
-          if (number_of(x[k]) == 0) tiny += weight_units(x[k], ex, sm.table);
-    });
-    if (tiny != 0) atomicAdd(reinterpret_cast<unsigned long long*>(&sm.tiny), (unsigned long long)tiny);
-    sync_all();
+          for (int k = 0; k < kVec; ++k) which |= number_of(x[k]) == 0 ? 1u << k : 0u;
+          for (; which != 0; which &= which - 1) {
+            float y = 0.f;
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) y = __ffs(which) - 1 == k ? x[k] : y;
+            tiny += weight_units(y, ex, sm.table);
+          }
+        }
+      }
+      if (tiny != 0) atomicAdd(reinterpret_cast<unsigned long long*>(&sm.tiny), (unsigned long long)tiny);
+      sync_all();
+    }
     // this thread's bins, summed over the CTAs (into this CTA's copy: no other CTA reads these bins
     // of it), and the tokens ahead of them
     uint32_t before = 0;
@@ -1453,10 +1508,10 @@ sample_plain_kernel(const SampleArgs a, int iters) {
       if (i >= iters) break;
       float x[kVec];
       E::unpack(ahead[h], x);
+      typename E::Max gm = E::lowest();
+      E::settle(ahead[h], gm);
+      const float g = E::largest(gm);
       if (i + kAhead < iters) ahead[h] = granule(first + (i + kAhead) * kStep, whole);
-      float g = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < kVec; ++k) g = fmaxf(g, x[k]);
       if (g > mx) mx = g, at = i;
       if (greedy) continue;
       if (g > high && fabsf(g * ab.hi) < kAboutMax) {
@@ -1714,7 +1769,7 @@ sample_plain_exact_kernel(const SampleArgs a, const __grid_constant__ ExpTable e
 // the CTAs still find room at once (clusters do not fill every SM: 76 rows by four did not fit); eight only
 // while SMs idle.  More too while one CTA's share of a row is over 40 iterations (164,000 bf16; 320 KB), of fp32,
 // whose longest rows take more passes, over 20; the row stays in shared memory where a share is at most 64 KB.
-// Measured, us by cluster size 1 / 2 / 4 / 8, top-p of 131,072 bf16: 512 rows 146 / 164 / 210 / 363, 150 rows 55 / 52 /
+// Measured with the maximum in a pass of its own, us by cluster size 1 / 2 / 4 / 8, top-p of 131,072 bf16: 512 rows 146 / 164 / 210 / 363, 150 rows 55 / 52 /
 // 81 / 118, 76 rows 52 / 39 / 53 / 71, 64 rows 52 / 38 / 34 / 54, 16 rows 49 / 37 / 25 / 27; all filters of 151,001
 // fp32: 512 rows - / 344 / 318 / 422, 128 rows - / 154 / 113 / 120, 16 rows - / 67 / 47 / 40; of 64,000: 512 rows 185 /
 // 156 / 161 / 288; all filters of 32,000 bf16: 400 rows 43 / 64 / 97 / 173, 100 rows 25 / 29 / 35 / 52, 8 rows 23 / 23 /

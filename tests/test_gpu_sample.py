@@ -319,3 +319,65 @@ def test_captured_two_streams_and_repeated():
     torch.cuda.synchronize()
     for t in toks:
         assert np.array_equal(t.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("R", [160, 12])
+def test_rows_whose_first_logits_mislead(R, fp32):
+    """Bins are counted from the largest of the logits that a warp loads first: rows whose maximum is far above those, rows
+    with nothing but -inf (or NaN, or large negative numbers) there, rows of values next to zero and of one value."""
+    rng = np.random.default_rng(R + fp32)
+    V = 100003
+    x = rng.normal(0, 2, (R, V)).astype(np.float32)
+    for r in range(R):
+        at = rng.integers(0, V, 30)
+        kind = r % 8
+        if kind == 0:
+            x[r, at] = rng.uniform(30, 60, 30)
+        elif kind == 1:
+            keep = x[r, at].copy()
+            x[r] = -np.inf
+            x[r, at] = keep
+        elif kind == 2:
+            x[r, :-5000] = np.where(rng.random(V - 5000) < 0.5, np.nan, -np.inf)
+        elif kind == 3:
+            x[r] = -1e30
+            x[r, at] = rng.normal(0, 2, 30)
+        elif kind == 4:
+            x[r] = rng.uniform(-2.0 ** -10, 2.0 ** -10, V)
+        elif kind == 5:
+            x[r] = rng.uniform(-2.0 ** -9, 2.0 ** -9, V)
+        elif kind == 6:
+            x[r, -300:] += 25
+        else:
+            x[r] = -7.25
+            x[r, at[0]] = rng.uniform(-7, 7)
+    for on in (("top_p",), ("top_k", "top_p", "min_p"), ("top_k",)):
+        s, u = settings(rng, R, V), rng.random(R).astype(np.float32)
+        s["top_k"] = np.where(rng.random(R) < 0.5, rng.integers(1, 200, R), rng.integers(1, V, R)).astype(np.int32)
+        k = {n: s[n] for n in on}
+        assert np.array_equal(draw(x, u, fp32, **k), reference(host(x, fp32), u, **k)), on
+
+
+@pytest.mark.parametrize("R", [150, 3])
+def test_cuts_away_from_the_bins_middles(R):
+    """Values at the ends of their bins, so that the bins' middle values place top-p's cut some bins above or below the
+    bin that it is in: widths are w = 2^-4 at 8 to 16, T = w; a token at 8 + 20 w, many just below 8 + 19 w (or above
+    8 + 18 w), more just above 8 + 15 w (or below 8 + 16 w)."""
+    rng = np.random.default_rng(R)
+    V, w = 60000, 2.0 ** -4
+    for low_then_high in (True, False):
+        n_b, n_c = (1000, 50000) if low_then_high else (2000, 20000)
+        x = np.full((R, V), -30.0, np.float32)
+        for r in range(R):
+            at, jitter = rng.permutation(V), rng.uniform(0.001, 0.02, V) * w
+            x[r, at[0]] = 8 + 20 * w
+            x[r, at[1:1 + n_b]] = (8 + 19 * w - jitter[:n_b]) if low_then_high else 8 + 18 * w + jitter[:n_b]
+            c = at[1 + n_b:1 + n_b + n_c]
+            x[r, c] = (8 + 15 * w + jitter[:n_c]) if low_then_high else 8 + 16 * w - jitter[:n_c]
+        p = rng.uniform(0.49, 0.51, R) if low_then_high else rng.uniform(0.5, 0.6, R)
+        k = dict(temp=np.full(R, w, np.float32), top_p=p.astype(np.float32))
+        u = rng.random(R).astype(np.float32)
+        assert np.array_equal(draw(x, u, True, **k), reference(x, u, **k)), low_then_high
+        k["top_k"] = rng.integers(n_b + 10000, V, R).astype(np.int32)
+        assert np.array_equal(draw(x, u, True, **k), reference(x, u, **k)), low_then_high
