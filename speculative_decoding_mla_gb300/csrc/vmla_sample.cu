@@ -28,10 +28,10 @@
 //      histogram alone gives both cuts exactly;
 //   few tokens: where top-k's bins hold at most 1024 tokens (or the vocabulary does)
 //      one CTA sorts them and does the rest: order, masses, cuts and draw;
-//   fp32: counts give top-k's bin, and, with each bin's middle value, the three bins
-//      that should hold top-p's cut; one pass adds the exact masses of all tokens and
-//      of those above these bins (where the cut is not in them, another over all bins);
-//      inside the bin or bins, histograms over 1024 equal ranges of the values'
+//   fp32: counts give top-k's bin, and, with each bin's middle value, the few bins that
+//      can hold top-p's cut; one pass adds the masses of all tokens and of those above
+//      these bins, in single precision (where its error could move the cut, again exactly),
+//      and lists the keys in them; inside the bin or bins, histograms over 1024 equal ranges of the values'
 //      bit patterns in their order (count, and exact mass for top-p) narrow it
 //      down to one value: one to three rounds, over the few tokens left.
 // The draw first sums weights in single precision with a known error (about_of);
@@ -101,16 +101,16 @@ struct Shared {
   float2 table[64];
   uint64_t warp_u64[kWarps], warp_u64b[kWarps];
   uint32_t warp_u32[kWarps];
-  float warp_f[kWarps];
+  float warp_f[kWarps], warp_g[kWarps];
   float exp_hi, exp_lo;    // log2(e) / temperature
   float ln_hi, ln_lo;      // temperature x ln(min_p)
   // read by the other CTAs of the cluster; a cluster barrier lies between a phase's reads and the
   // slot's next write
   float x_max, first_max;
   uint64_t sum_a, sum_b, tiny;
-  float sum_f;
+  float sum_f, sum_g;
   uint32_t key_lo, key_hi, count, bin_count;
-  int32_t index, bin_middle;
+  int32_t index, bin_first, bin_last;
   // written by the one thread of the cluster that finds them, into every CTA
   int32_t bin_k, bin_p, sure;
   uint32_t bin_k_rank, bin_k_count, bin_p_keep;
@@ -304,9 +304,10 @@ constexpr float kAboutMax = 1048576.f;  // of |max c|
 constexpr float kAboutError = 3.6e-7f;
 
 // How near to u W a border may lie and still be decided by single-precision sums (2.1e-8 + 1.46e-7 +
-// 1.8e-7 = 3.5e-7; the units' own rounding, some tens, is covered by the 1024).
+// 1.8e-7 = 3.5e-7; the roundings to whole units, at most one a token, by the 2^18).
+constexpr uint64_t kAboutUnits = VMLA_MAX_VOCAB;
 __device__ __forceinline__ uint64_t about_margin(float u, uint64_t all) {
-  return (uint64_t)(2.f * u * (1.f - u) * kAboutError * (float)all) + 1024;
+  return (uint64_t)(2.f * u * (1.f - u) * kAboutError * (float)all) + kAboutUnits;
 }
 
 __device__ __forceinline__ About about(const Exponent& e) {
@@ -661,11 +662,13 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     return;
   }
 
+  // one thread each: 64-bit arithmetic is some 60 times slower than 32-bit here
   if (tid == 0 && temp > 0.f) {
-    // one thread: 64-bit arithmetic is some 60 times slower than 32-bit here
     const double c = 1.4426950408889634 / (double)temp;
     sm.exp_hi = (float)c;
     sm.exp_lo = (float)(c - (double)sm.exp_hi);
+  }
+  if (tid == 32) {
     const double l = min_p > 0.f && min_p < 1.f ? (double)temp * log((double)min_p) : 0.0;
     sm.ln_hi = (float)l;
     sm.ln_lo = (float)(l - (double)sm.ln_hi);
@@ -991,9 +994,11 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     };
     // The value at which a running count (or mass) over the tokens with a key in [klo, khi], in
     // descending order, reaches `target`: its key, how many tokens have it, and what is left of the
-    // target for them.  (A round leaves 10 bits fewer: 32, 22, 12, 2.)  The keys come from the list, or,
-    // where there is none yet or too many, from the row.
-    auto refine = [&](uint32_t klo, uint32_t khi, bool by_mass, bool listed, uint64_t* target, uint32_t* equal) {
+    // target for them; false where it is not reached.  (A round leaves 10 bits fewer: 32, 22, 12, 2.)  The
+    // keys come from the list, or, where there is none yet or too many, from the row.
+    auto refine = [&](uint32_t klo, uint32_t khi, bool by_mass, bool listed, uint64_t* target, uint32_t* equal,
+                      uint32_t* key) {
+      *equal = UINT32_MAX;
 #pragma unroll 1
       for (int round = 0; round < 4; ++round) {
         const int width = range_width(klo, khi);
@@ -1046,10 +1051,11 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
           break;
         }
         sync_all();
-        pick(by_mass, width, &klo, &khi, target, equal);
+        if (!pick(by_mass, width, &klo, &khi, target, equal)) return false;
         if (width == 0) break;
       }
-      return klo;
+      *key = klo;
+      return true;
     };
     // Keys of the values in bins [b_first, b_last].
     auto bin_keys = [&](int b_first, int b_last, uint32_t* klo, uint32_t* khi) {
@@ -1058,8 +1064,9 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
       const int n_hi = top_number - b_first, n_lo = top_number - b_last;
       // numbers above 0 start at their own value's key, those below end at it
       const uint32_t zero = order_key<kL>(0.f), near = ((uint32_t)kNearZero << (16 - kL)) - 1u;
-      *khi = n_hi > 0 ? order_key<kL>(number_value(n_hi)) + rest
-                      : n_hi == 0 ? zero + near : order_key<kL>(number_value(n_hi));
+      if (n_hi >= number_of(mx)) *khi = order_key<kL>(mx);  // (the bins may begin beyond the largest number)
+      else *khi = n_hi > 0 ? order_key<kL>(number_value(n_hi)) + rest
+                           : n_hi == 0 ? zero + near : order_key<kL>(number_value(n_hi));
       *klo = n_lo > 0 ? order_key<kL>(number_value(n_lo))
                       : n_lo == 0 ? zero - 1u - near : order_key<kL>(number_value(n_lo)) - rest;
     };
@@ -1162,84 +1169,117 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
       }
     }
     if (!found) {
-      // The bins around the one where top-p's mass is reached if every token of a bin had its middle
-      // value; where the exact masses show that it was not there, all bins are taken.
+      // The bins where top-p's mass can be reached: every token of a bin is taken for the bin's middle value,
+      // which is off by at most a factor 2^h, and p all - cum, cum being the mass up to a bin, then by the error
+      // of p (all - cum) + (1 - p) cum: a few bins.
       int b_lo = 0, b_hi = bin_k;
       if (with_p) {
-        auto bin_mass = [&](int b) {
+        auto bin_mass = [&](int b, float* off) {
           const uint32_t n = b > bin_k ? 0 : b == bin_k ? min(sm.hist[b], k_rank) : sm.hist[b];
+          *off = 0.f;
+          if (n == 0) return 0.f;
           const int v = top_number - b;
-          const float middle =
-              v == 0 ? 0.f : __uint_as_float(__float_as_uint(number_value(v)) | (E::kLowBits ? 0u : 0x8000u));
-          return (float)n * ex2_approx(fminf((middle - mx) * ex.hi, 0.f));
+          const uint32_t bits = __float_as_uint(number_value(v));
+          const float middle = v == 0 ? 0.f : __uint_as_float(bits | (E::kLowBits ? 0u : 0x8000u));
+          const float reach = v == 0 ? __uint_as_float((uint32_t)kNearZero << 16)
+                                     : E::kLowBits ? 0.f : fabsf(middle - __uint_as_float(bits));
+          const float m = (float)n * ex2_approx(fminf((middle - mx) * ex.hi, 0.f));
+          *off = m * (ex2_approx(fminf(reach * ex.hi, 64.f)) - 1.f + 1e-4f);
+          return m;
         };
-        float own = 0.f, all;
-        for (int b = bin0; b < bin0 + per && b < bins; ++b) own += bin_mass(b);
-        float cum = block_scan(own, sm.warp_f, &all);
-        if (tid == 0) sm.sum_f = all, sm.bin_middle = bin_k;
+        float own = 0.f, own_off = 0.f, off, all, all_off;
+        for (int b = bin0; b < bin0 + per && b < bins; ++b) own += bin_mass(b, &off), own_off += off;
+        float cum = block_scan(own, sm.warp_f, &all), cum_off = block_scan(own_off, sm.warp_g, &all_off);
+        if (tid == 0) sm.sum_f = all, sm.sum_g = all_off, sm.bin_first = sm.bin_last = bin_k;
         sync_all();
-        all = 0.f;
+        all = all_off = 0.f;
         for (int r = 0; r < C; ++r) {
-          const float m = of(r).sum_f;
-          if (r < rank) cum += m;
-          all += m;
+          const float m = of(r).sum_f, e = of(r).sum_g;
+          if (r < rank) cum += m, cum_off += e;
+          all += m, all_off += e;
         }
-        if (cum + own >= top_p * all)
+        // (bins far before or past it need no second look)
+        if (cum + own >= top_p * all - all_off && cum <= top_p * all + all_off)
           for (int b = bin0; b < bin0 + per && b < bins; ++b) {
-            cum += bin_mass(b);
-            if (cum >= top_p * all) atomicMin(&sm.bin_middle, b);
+            const float m = bin_mass(b, &off);
+            if (m == 0.f) continue;
+            cum += m, cum_off += off;
+            const float over = cum - top_p * all, error = top_p * (all_off - cum_off) + (1.f - top_p) * cum_off;
+            if (over >= -error) atomicMin(&sm.bin_first, b);
+            if (over >= error) atomicMin(&sm.bin_last, b);
           }
         sync_all();
-        for (int r = 0; r < C; ++r) b_hi = min(b_hi, of(r).bin_middle);
-        b_lo = max(b_hi - 1, 0), b_hi = min(b_hi + 1, bin_k);
+        b_lo = b_hi;
+        for (int r = 0; r < C; ++r) b_lo = min(b_lo, of(r).bin_first), b_hi = min(b_hi, of(r).bin_last);
       }
-      sync_all();  // the histograms and middles have been read
+      sync_all();  // the histograms and what was found in them have been read
       uint32_t floor_key = 0, klo, khi, equal;
       if (with_k) {
         uint64_t left = k_rank;
         bin_keys(bin_k, bin_k, &klo, &khi);
-        floor_key = refine(klo, khi, false, false, &left, &equal);
+        refine(klo, khi, false, false, &left, &equal, &floor_key);
         cut_x = order_value<E::kLowBits>(floor_key);
         cut_keep = (uint32_t)left;
       }
       if (with_p) {
-        // In one pass the exact masses of what top-k leaves, of its part above these bins, and of their
-        // ranges (of the tokens equal to top-k's cut, all: they come last)
-        uint64_t left;
-        int width;
+        // In one pass the masses of what top-k leaves and of its part above these bins, whose own tokens (of
+        // those equal to top-k's cut, all: they come last) are listed.  First in single precision: where
+        // the cut then lies too near a border, again with exact masses; where it is not in these bins,
+        // among all.
+        const float floor_x = with_k ? cut_x : -INFINITY;
+        bool exact = !(fabsf(mx * ex.hi) < kAboutMax);
 #pragma unroll 1
-        for (int attempt = 0; attempt < 2; ++attempt, b_lo = 0, b_hi = bin_k) {
+        for (int attempt = 0; attempt < 3; ++attempt) {
           bin_keys(b_lo, b_hi, &klo, &khi);
           klo = max(klo, floor_key);
-          width = range_width(klo, khi);
-          clear_ranges(true);
-          uint32_t all_h = 0, top_h = 0;
-          int32_t all_l = 0, top_l = 0;
-          each_granule([&](const float (&x)[kVec], int) {
-            uint32_t k[kVec];
-            bool any = false;
+          const float x_lo = order_value<E::kLowBits>(klo), x_hi = order_value<E::kLowBits>(khi);
+          if (tid == 0) sm.keys = 0;
+          __syncthreads();
+          uint64_t all, top;
+          auto list = [&](const float (&x)[kVec]) {
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) k[j] = order_key<E::kLowBits>(x[j]), any |= k[j] >= floor_key;
-            if (!any) return;  // (most, where there is a top-k cut)
+            for (int j = 0; j < kVec; ++j)
+              if (x[j] >= x_lo && x[j] <= x_hi) list_key(order_key<E::kLowBits>(x[j]));
+          };
+          if (exact) {
+            uint32_t all_h = 0, top_h = 0;
+            int32_t all_l = 0, top_l = 0;
+            each_granule([&](const float (&x)[kVec], int) {
+              bool any = false;
 #pragma unroll
-            for (int j = 0; j < kVec; j += 2) {
-              int32_t h[2], l[2];
-              weights_of(make_float2(x[j], x[j + 1]), ex, sm.table, h, l);
+              for (int j = 0; j < kVec; ++j) any |= x[j] >= floor_x;
+              if (!any) return;  // (most, where there is a top-k cut)
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const uint32_t key = k[j + i];
-                if (key > floor_key) all_h += h[i], all_l += l[i];
-                if (key > khi) {
-                  top_h += h[i], top_l += l[i];
-                } else if (key >= klo) {
-                  atomicAdd(&sm.r.count[(key - klo) >> width], 1u);
-                  add_mass((key - klo) >> width, units(h[i], l[i]));
-                  list_key(key);
+              for (int j = 0; j < kVec; j += 2) {
+                int32_t h[2], l[2];
+                weights_of(make_float2(x[j], x[j + 1]), ex, sm.table, h, l);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  if (x[j + i] > floor_x) all_h += h[i], all_l += l[i];
+                  if (x[j + i] > x_hi) top_h += h[i], top_l += l[i];
                 }
               }
-            }
-          });
-          uint64_t all = warp_add(units(all_h, all_l)), top = warp_add(units(top_h, top_l));
+              list(x);
+            });
+            all = units(all_h, all_l), top = units(top_h, top_l);
+          } else {
+            const About ab = about(ex);
+            const float x_least = fmaxf(floor_x, mx - kOctaves * 0.6931472f * temp);
+            float all_s = 0.f, all_e = 0.f, top_s = 0.f, top_e = 0.f;
+            each_granule([&](const float (&x)[kVec], int) {
+              float w[kVec];
+              about_all(x, ab, w);
+#pragma unroll
+              for (int j = 0; j < kVec; ++j) w[j] = x[j] > x_least ? w[j] : 0.f;
+              add_in_two(tree_sum(w), &all_s, &all_e);
+#pragma unroll
+              for (int j = 0; j < kVec; ++j) w[j] = x[j] > x_hi ? w[j] : 0.f;
+              add_in_two(tree_sum(w), &top_s, &top_e);
+              list(x);
+            });
+            all = about_units(all_s, all_e), top = about_units(top_s, top_e);
+          }
+          all = warp_add(all), top = warp_add(top);
           if (lane == 0) sm.warp_u64[warp] = all, sm.warp_u64b[warp] = top;
           __syncthreads();
           if (tid == 0) {
@@ -1248,19 +1288,42 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
             sm.sum_a = all, sm.sum_b = top;
           }
           sync_all();
-          all = with_k ? (uint64_t)cut_keep * weight_units(cut_x, ex, sm.table) : 0, top = 0;
-          for (int r = 0; r < C; ++r)
-            all += of(r).sum_a, top += of(r).sum_b;
-          const uint64_t least = least_mass(all);
-          left = least - top;  // (0, or over 2^63, where the cut lies above these bins)
-          if (pick(true, width, &klo, &khi, &left, &equal)) break;
+          const uint64_t last = with_k ? (uint64_t)cut_keep * weight_units(cut_x, ex, sm.table) : 0;
+          all = last, top = 0;
+          if (exact) {
+            for (int r = 0; r < C; ++r) all += of(r).sum_a, top += of(r).sum_b;
+          } else {
+            // without the factor that about_of's weights share, a power of two from -1/2 to 1/2
+            const About ab = about(ex);
+            const float d = __fmaf_rn(-mx, ab.lo, __fmaf_rn(-mx, ab.hi, -__fsub_rn(ab.magic, 12582912.f)));
+            const uint64_t by = fixed<63>(ex2_approx(d));
+            for (int r = 0; r < C; ++r)
+              all += __umul64hi(of(r).sum_a, by) << 1, top += __umul64hi(of(r).sum_b, by) << 1;
+          }
+          // (0, or over 2^63, where the cut lies above these bins)
+          const uint64_t within = least_mass(all) - top;
+          uint64_t left = within;
+          if (!refine(klo, khi, true, true, &left, &equal, &klo)) {
+            if (exact) b_lo = 0, b_hi = bin_k;
+            exact = true;
+            continue;
+          }
+          const float x = order_value<E::kLowBits>(klo);
+          const uint64_t w = weight_units(x, ex, sm.table);
+          const uint32_t keep = w > 0 ? (uint32_t)min((left + w - 1) / w, (uint64_t)equal) : equal;
+          if (!exact) {
+            // p all - top is off by at most the error of p (all - top) + (1 - p) top, and by that of the
+            // factor (1.7e-7) in what is left of it, or in what the tokens at top-k's cut add to it
+            const float off = top_p * (float)(all - top) + (1.f - top_p) * (float)top;
+            const uint64_t margin =
+                (uint64_t)(off * (1.01f * kAboutError) + ((float)within + (float)last) * 1.8e-7f) + 2 * kAboutUnits;
+            exact = true;
+            if (left <= (keep - 1) * w + margin || left + margin > keep * w) continue;
+          }
+          if (with_k && x == cut_x) cut_keep = min(cut_keep, keep);
+          else cut_x = x, cut_keep = keep;
+          break;
         }
-        if (width > 0) klo = refine(klo, khi, true, true, &left, &equal);
-        const float x = order_value<E::kLowBits>(klo);
-        const uint64_t w = weight_units(x, ex, sm.table);
-        const uint32_t keep = w > 0 ? (uint32_t)min((left + w - 1) / w, (uint64_t)equal) : equal;
-        if (with_k && x == cut_x) cut_keep = min(cut_keep, keep);
-        else cut_x = x, cut_keep = keep;
       }
     }
   }
