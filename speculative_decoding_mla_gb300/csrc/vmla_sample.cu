@@ -1828,15 +1828,15 @@ sample_plain_exact_kernel(const SampleArgs a, const __grid_constant__ ExpTable e
   }
 }
 
-// CTAs per row: more while that leaves SMs idle, or while rows are long (over 8 iterations a CTA) and most of
-// the CTAs still find room at once (clusters do not fill every SM: 76 rows by four did not fit); eight only
-// while SMs idle.  More too while one CTA's share of a row is over 40 iterations (164,000 bf16; 320 KB), of fp32,
-// whose longest rows take more passes, over 20; the row stays in shared memory where a share is at most 64 KB.
-// Measured with the maximum in a pass of its own, us by cluster size 1 / 2 / 4 / 8, top-p of 131,072 bf16: 512 rows 146 / 164 / 210 / 363, 150 rows 55 / 52 /
-// 81 / 118, 76 rows 52 / 39 / 53 / 71, 64 rows 52 / 38 / 34 / 54, 16 rows 49 / 37 / 25 / 27; all filters of 151,001
-// fp32: 512 rows - / 344 / 318 / 422, 128 rows - / 154 / 113 / 120, 16 rows - / 67 / 47 / 40; of 64,000: 512 rows 185 /
-// 156 / 161 / 288; all filters of 32,000 bf16: 400 rows 43 / 64 / 97 / 173, 100 rows 25 / 29 / 35 / 52, 8 rows 23 / 23 /
-// 21 / 19.
+// CTAs per row: more while that leaves SMs idle, or while rows are long (over 8 iterations of 8 KB a CTA) and
+// most of the CTAs still find room at once (clusters do not fill every SM: 76 rows by four did not fit), or while
+// they are longer (over 20) and the CTAs take at most two rounds; eight only while SMs idle.  More too while
+// one CTA's share of a row is over 40 iterations; the row stays in shared memory where a share is at most 64 KB.
+// Measured, us by cluster size 1 / 2 / 4 / 8, top-p of 131,072 bf16: 512 rows 130 / 148 / 190 / 336, 300 rows 100 / 94 /
+// 123 / 202, 150 rows 55 / 50 / 72 / 110, 76 rows 53 / 37 / 47 / 66, 64 rows 53 / 35 / 31 / 51, 16 rows 51 / 35 / 24 / 26; all
+// filters of 151,001 fp32: 512 rows - / 205 / 245 / 390, 300 rows - / 146 / 157 / 240, 128 rows - / 89 / 83 / 116, 76 rows
+// - / 89 / 73 / 91, 16 rows - / 53 / 42 / 39; of 64,000: 512 rows 116 / 126 / 155 / 293, 128 rows 65 / 56 / 56 / 95; all filters
+// of 32,000 bf16: 400 rows 42 / 61 / 93 / 171, 100 rows 24 / 27 / 34 / 51, 8 rows 23 / 23 / 20 / 19.
 struct Shape {
   int cluster, iters;
   bool keep;
@@ -1853,11 +1853,10 @@ Shape choose_shape(const SampleArgs& a, int sms) {
   auto need = [&](int c) { return iterations<T>(a, c); };
   Shape s;
   s.cluster = 1;  // (a vocabulary of up to kList tokens stays in one CTA: one iteration holds it)
-  constexpr int kLong = Elems<T>::kLowBits ? 40 : 20;
   while (s.cluster < kMaxCluster && need(s.cluster) > 1) {
     const int64_t ctas = a.rows * s.cluster * 2;
-    const int room = s.cluster == 4 ? sms : sms + sms * 3 / 4;
-    if (!(need(s.cluster) > kLong || ctas <= sms / 2 || (need(s.cluster) > 8 && ctas <= room))) break;
+    const int n = need(s.cluster), room = s.cluster == 4 ? sms : n > 20 ? 4 * sms : sms + sms * 3 / 4;
+    if (!(n > 40 || ctas <= sms / 2 || (n > 8 && ctas <= room))) break;
     s.cluster *= 2;
   }
   s.keep = need(s.cluster) <= kKeepIters;
