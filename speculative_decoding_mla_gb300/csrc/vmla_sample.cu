@@ -30,10 +30,10 @@
 //      one CTA sorts them and does the rest: order, masses, cuts and draw;
 //   fp32: counts give top-k's bin, and, with each bin's middle value, the few bins that
 //      can hold top-p's cut; one pass adds the masses of all tokens and of those above
-//      these bins, in single precision (where its error could move the cut, again exactly),
-//      and lists the keys in them; inside the bin or bins, histograms over 1024 equal ranges of the values'
-//      bit patterns in their order (count, and exact mass for top-p) narrow it
-//      down to one value: one to three rounds, over the few tokens left.
+//      these bins, in single precision (where its error could move the cut, again
+//      exactly), and lists the keys in them; inside the bin or bins, histograms over 1024
+//      equal ranges of the values' bit patterns in their order (count, and exact mass for
+//      top-p) narrow it down to one value: one to three rounds, over the few tokens left.
 // The draw first sums weights in single precision with a known error (about_of);
 // only where the random number falls so near a running sum that this could decide
 // it, the sums are taken again exactly: by the same cluster, or, for calls without
@@ -41,14 +41,16 @@
 //
 // What bounds it: 512 rows of 131,072 bf16 (134 MB, 20 us of reading) take 80 us without a
 // filter, instructions (23 a token: the weight 13, the loop 5, the rest the search), and
-// 130 us with top-p.  There a row is one CTA's, two on an SM, for 57 us: maximum and
-// histogram 24 (its shared-memory atomics, 3.8 cycles a warp for their banks' conflicts,
-// take 28 us of the whole call; maximum and histogram in two passes: 145 us), cuts 10, the
-// sums of the draw 15, its search 6, barriers.
-// Tried and not kept: top-p's masses in fp32 by single-precision sums first (a second pass
-// where they do not decide made the longest rows longer: 128 rows of 151,001, 166 ->
-// 191 us), whole rows in shared memory for 512 rows (216 us), undecided rows of the
-// filtered kernel by a second launch (203 -> 215 us).
+// 130 us with top-p.  There a row is one CTA's, two on an SM, for 53 us: maximum and
+// histogram 18 (its shared-memory atomics, 3.8 cycles a warp for their banks' conflicts,
+// take 28 us of the whole call, and make the other CTA's shared memory slow meanwhile;
+// maximum and histogram in two passes: 145 us), values next to zero 5, cuts 7, the sums of
+// the draw 14, its search 6, barriers.  A row that the draw's first sums do not decide (one
+// in some hundred) takes 20 us more, 45 if all its tokens and not the kept ones are
+// weighed.  128 rows of 151,001 fp32 take 123 us with top-p and 84 with all filters (of
+// which most have top-k): 225 and 130 where all masses for top-p are exact.
+// Tried and not kept: whole rows in shared memory for 512 rows (216 us), undecided rows of
+// the filtered kernel by a second launch (203 -> 215 us), more loads in flight.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -97,6 +99,7 @@ struct Shared {
     struct {
       uint64_t key[kList], weight[kList], by_place[kList], spare[kList];
     } list;
+    float kept[kWarps][64 + 32 * 8];  // of each warp, tokens to weigh
   };
   float2 table[64];
   uint64_t warp_u64[kWarps], warp_u64b[kWarps];
@@ -139,7 +142,7 @@ __device__ __forceinline__ float order_value(uint32_t key) {
 }
 
 // Signed number of a value's leading 16 bits, not decreasing in the value: 0 next to zero, then one
-// step per pattern.  The bin of a value is the number of the row's maximum less its own.  A weight of at
+// step per pattern.  The bin of a value is a number not below the row's maximum's (kAbove) less its own.  A weight of at
 // least 2^-46 means a value within 46 ln 2 T < 2^25 of the maximum, T being at most 2^20, and that
 // window holds at most 2 (25 + 10) 128 + 1 numbers (when zero is in its middle).
 __device__ __forceinline__ int number_of(float x) {
@@ -422,16 +425,6 @@ struct Elems<float> {
   static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[4]) {
     x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
   }
-  // f of the granule's values two at a time, its code once: for passes that few rows take, whose
-  // instructions would otherwise come from memory each time
-  template <typename F>
-  static __device__ __forceinline__ void each_pair(uint4 v, F&& f) {
-#pragma unroll 1
-    for (int k = 0; k < 2; ++k) {
-      f(make_float2(__uint_as_float(v.x), __uint_as_float(v.y)));
-      v.x = v.z, v.y = v.w;
-    }
-  }
   typedef float Max;
   static __device__ __forceinline__ Max lowest() { return -INFINITY; }
   static __device__ __forceinline__ float largest(Max m) { return m; }
@@ -464,14 +457,6 @@ struct Elems<uint16_t> {  // bf16
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) x[2 * k] = bf16_lo(w[k]), x[2 * k + 1] = bf16_hi(w[k]);
-  }
-  template <typename F>
-  static __device__ __forceinline__ void each_pair(uint4 v, F&& f) {
-#pragma unroll 1
-    for (int k = 0; k < 4; ++k) {
-      f(make_float2(bf16_lo(v.x), bf16_hi(v.x)));
-      v.x = v.y, v.y = v.z, v.z = v.w;
-    }
   }
   typedef uint32_t Max;  // two bf16 maxima
   static __device__ __forceinline__ Max lowest() { return 0xFF80FF80u; }
@@ -1371,17 +1356,32 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
     uint64_t sum;
     uint32_t same = 0;
     if (exact) {
+      // the kept tokens, a quarter or less of many rows, are gathered first (in the histogram's place) and
+      // weighed 64 at a time by a warp
       uint32_t h = 0;
       int32_t l = 0;
-      each_raw([&](const uint4& v, const float (&)[kVec], int) {
-        E::each_pair(v, [&](float2 x) {
-          int32_t wh[2], wl[2];
-          weights_of(x, ex, sm.table, wh, wl);
-          h += (x.x > over ? wh[0] : 0) + (x.y > over ? wh[1] : 0);
-          l += (x.x > over ? wl[0] : 0) + (x.y > over ? wl[1] : 0);
-          if (partial) same += (x.x == cut_x ? 1u : 0u) + (x.y == cut_x ? 1u : 0u);
-        });
+      float* kept = sm.kept[warp];
+      int n = 0;
+      auto weigh = [&](float2 x) {
+        int32_t wh[2], wl[2];
+        weights_of(x, ex, sm.table, wh, wl);
+        h += wh[0] + wh[1];
+        l += wl[0] + wl[1];
+      };
+      each_granule([&](const float (&x)[kVec], int) {
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+          const bool keep = x[k] > over;
+          const uint32_t who = __ballot_sync(0xffffffffu, keep);
+          if (keep) kept[n + __popc(who & ((1u << lane) - 1u))] = x[k];
+          n += __popc(who);
+          if (partial) same += x[k] == cut_x ? 1u : 0u;
+        }
+        __syncwarp();
+        for (; n >= 64; n -= 64) weigh(make_float2(kept[n - 64 + lane], kept[n - 32 + lane]));
+        __syncwarp();
       });
+      weigh(make_float2(lane < n ? kept[lane] : -INFINITY, lane + 32 < n ? kept[lane + 32] : -INFINITY));
       sum = units(h, l);
     } else {
       float s = 0.f, e = 0.f;  // the sum in two floats
