@@ -1107,11 +1107,6 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
       if (with_p) {
         uint64_t all = 0, tiny_all = 0, own = 0, block;
         for (int r = 0; r < C; ++r) tiny_all += of(r).tiny;
-        auto bin_mass = [&](int b) -> uint64_t {
-          if (b == tiny_bin) return tiny_all;
-          const uint32_t n = b == bin_k ? min(sm.hist[b], k_rank) : sm.hist[b];
-          return n ? n * weight_units(number_value(top_number - b), ex, sm.table) : 0ull;
-        };
         const int stop = min(bin0 + per, bin_k + 1);
         for (int b = bin0; b < stop; b += 2) {
           // (of a row with one bin less than two, or of number 0, the value is not looked at)
@@ -1137,10 +1132,11 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
         if (who) {
           const int owner = __ffs(who) - 1;
           const int b = __shfl_sync(0xffffffffu, bin0, owner) + lane;
-          const uint64_t m = lane < per && b <= bin_k ? bin_mass(b) : 0;
+          const uint64_t w = b == tiny_bin ? 0 : weight_units(number_value(top_number - b), ex, sm.table);
+          const bool mine = lane < per && b <= bin_k;
+          const uint64_t m = !mine ? 0 : b == tiny_bin ? tiny_all : w * (b == bin_k ? min(sm.hist[b], k_rank) : sm.hist[b]);
           const uint64_t upto = __shfl_sync(0xffffffffu, ahead, owner) + warp_scan(m, lane);
           if (lane == __ffs(__ballot_sync(0xffffffffu, upto >= target)) - 1) {
-            const uint64_t w = b == tiny_bin ? 0 : weight_units(number_value(top_number - b), ex, sm.table);
             to_all(&Shared::bin_p, b);
             to_all(&Shared::bin_p_keep, w > 0 ? (uint32_t)((target - (upto - m) + w - 1) / w) : sm.hist[b]);
           }
@@ -1433,7 +1429,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
       };
       const int w0 = max(run_of(lane < kWarps ? sm.warp_u64[lane] : 0, lane < kWarps ? sm.warp_u32[lane] : 0), 0);
       // that warp's places, one iteration's per warp of this CTA
-      for (int i = warp; i < iters; i += kWarps) {
+      for (int i = warp; iters > 1 && i < iters; i += kWarps) {
         float x[kVec];
         values(fetch(w0, i), x);
         uint32_t n;
@@ -1444,7 +1440,7 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
       }
       __syncthreads();
       if (warp == 0) {
-        int i = -1;
+        int i = iters > 1 ? -1 : 0;
         for (int i0 = 0; i < 0 && i0 < iters; i0 += 32) {
           const bool in = i0 + lane < iters;
           const int at = run_of(in ? sm.chunk[i0 + lane] : 0, in ? sm.chunk_same[i0 + lane] : 0);
