@@ -295,22 +295,31 @@ __device__ __forceinline__ uint64_t weight_units(float x, const Exponent& e, con
 
 // The weight in single precision, times a factor that all of a row's weights share: 2^(x c + bias),
 // bias being the whole number next to -max c (below 2^20).  The exponent is split into a whole
-// number n = t - 1.5 x 2^23 and f, |f| <= 1/2: bias - n is exact, f is off by at most 2^-25, which moves
-// the weight by 2.1e-8; ex2.approx on such f is off by -1.43e-7 to 1.46e-7 (every float of that range, on
-// this GPU); sums of eight in a tree add 3 x 2^-24 = 1.8e-7, their running sum in two floats nothing that
-// counts: kAboutError in all.  A running sum C and the total W then place u W - C within
-// 2 u (1 - u) kAboutError W of its value.  For x c + bias > -100 only.
+// number n = t - 1.5 x 2^23 and f, |f| <= 1/2 (and what x lo adds, below 2^-4): bias - n is exact, f is off by at
+// most 2^-26 + 2^-25, which moves the weight by 3.1e-8; ex2.approx on such f is off by -1.43e-7 to 1.46e-7 (every
+// float of that range, on this GPU); sums of eight in a tree add 3 x 2^-24 = 1.79e-7, their running sum in two
+// floats nothing that counts: kAboutError in all.  For x c + bias > -100 only.
+//
+// Whether a border, the running sum C of the exact weights, lies above u W is told by C' and W', both taken from
+// sums of the same approximate weights: with e_i token i's error, W' - W = sum e_i w_i and C' - C = sum_(i <= j)
+// e_i w_i, so u W' - C' is off by u sum_(i > j) e_i w_i - (1 - u) sum_(i <= j) e_i w_i, which at a border near u W
+// is at most 2 u (1 - u) kAboutError W.  Only a sum C' made of the very numbers that make W' has these e_i.  The
+// last part of C', S up to the border, is summed anew, token by token, which gives its tokens other errors than
+// they have in W', by up to kTreeError where only the tree differs, or kAnewError where the bias does too (the
+// whole e_i, and 3.1e-8 + 1.46e-7): that much of S comes on top, whatever u is.
 struct About {
   float hi, lo, magic;
 };
 constexpr float kAboutMax = 1048576.f;  // of |max c|
-constexpr float kAboutError = 3.6e-7f;
+constexpr float kAboutError = 3.6e-7f;  // 3.1e-8 + 1.46e-7 + 1.79e-7
+constexpr float kTreeError = 1.8e-7f;
+constexpr float kAnewError = 5.4e-7f;   // kAboutError + 3.1e-8 + 1.46e-7
 
-// How near to u W a border may lie and still be decided by single-precision sums (2.1e-8 + 1.46e-7 +
-// 1.8e-7 = 3.5e-7; the roundings to whole units, at most one a token, by the 2^18).
+// How near to u W a border may lie and still be decided by single-precision sums, `anew` being what was summed
+// anew up to the border (roundings to whole units, at most one a token, by the 2^18).
 constexpr uint64_t kAboutUnits = VMLA_MAX_VOCAB;
-__device__ __forceinline__ uint64_t about_margin(float u, uint64_t all) {
-  return (uint64_t)(2.f * u * (1.f - u) * kAboutError * (float)all) + kAboutUnits;
+__device__ __forceinline__ uint64_t about_margin(float u, uint64_t all, uint64_t anew, float anew_error) {
+  return (uint64_t)(2.f * u * (1.f - u) * kAboutError * (float)all + anew_error * (float)anew) + kAboutUnits;
 }
 
 __device__ __forceinline__ About about(const Exponent& e) {
@@ -1453,7 +1462,8 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
         const uint64_t m = mass(x, &n);
         const int lane_at = run_of(m, n);
         if (lane == lane_at) {
-          // (before and ahead are this lane's now)
+          // (before and ahead are this lane's now: `before` is made of the numbers that make `all`)
+          const uint64_t start = before;
           float w[kVec];
           if (!exact) about_weights(x, w);
 #pragma unroll(exact ? 1 : kVec)
@@ -1464,8 +1474,9 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
             if (eq) ++ahead;
             if (before <= goal && goal < before + own) {
               a.token[row] = (rank * kWarps + w0) * seg + i * kStep + lane * kVec + k - shift;
-              const uint64_t margin = about_margin(u, all);
-              if (goal - before >= margin && before + own - goal > margin) to_all(&Shared::sure, 1);
+              if (!exact && goal - before >= about_margin(u, all, before - start, kTreeError) &&
+                  before + own - goal > about_margin(u, all, before + own - start, kTreeError))
+                to_all(&Shared::sure, 1);
             }
             before += own;
           }
@@ -1673,6 +1684,7 @@ sample_plain_kernel(const SampleArgs a, int iters) {
       if (goal < before + m) break;
       before += m;
     }
+    const uint64_t run = before;  // (up to here made of the numbers that make `all`)
     const int start = (rank * kWarps + w0) * seg + lane * kVec;
     for (int i = warp; i < iters; i += kWarps) {
       float x[kVec];
@@ -1694,12 +1706,15 @@ sample_plain_kernel(const SampleArgs a, int iters) {
       for (int k = 0; k < kVec; ++k) m += w[k] = weight(x[k]);
       uint64_t upto = before + warp_scan(m, lane) - m;
       // the token, or a mark where no sum, or one next to the goal, decides
-      const uint64_t margin = about_margin(u, all);
       int token = kUndecided;
+      if (upto <= goal && goal < upto + m) {  // one lane, if any
 #pragma unroll
-      for (int k = 0; k < kVec; ++k) {
-        if (goal >= upto + margin && upto + w[k] > goal + margin) token = start + i * kStep + k - shift;
-        upto += w[k];
+        for (int k = 0; k < kVec; ++k) {
+          if (upto <= goal && goal < upto + w[k] && goal - upto >= about_margin(u, all, upto - run, kAnewError) &&
+              upto + w[k] - goal > about_margin(u, all, upto + w[k] - run, kAnewError))
+            token = start + i * kStep + k - shift;
+          upto += w[k];
+        }
       }
       const uint32_t found = __ballot_sync(0xffffffffu, token != kUndecided);
       if (found ? lane == __ffs(found) - 1 : lane == 0) a.token[row] = token;
