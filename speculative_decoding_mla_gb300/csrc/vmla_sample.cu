@@ -1655,7 +1655,9 @@ sample_plain_kernel(const SampleArgs a, int iters) {
   cluster.sync();
   const float cta_max = mx;
   for (int r = 0; r < C; ++r) mx = fmaxf(mx, *cluster.map_shared_rank(&sm.x_max, r));
-  if (!(mx > -INFINITY && fabsf(mx * ab.hi) < kAboutMax)) {
+  // A thread (and a CTA) whose largest exponent is not below kAboutMax in magnitude has no bias and adds nothing:
+  // with the row's at least 64 inside, what such a thread has is infinite, or below 2^-63 of the row's largest.
+  if (!(mx > -INFINITY && fabsf(mx * ab.hi) < kAboutMax - 64.f)) {
     if (rank == 0 && tid == 0) a.token[row] = mx == -INFINITY ? -1 : kUndecided;
     cluster.sync();
     return;

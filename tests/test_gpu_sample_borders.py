@@ -97,3 +97,26 @@ def test_draws_next_to_borders_of_broad_rows(fp32):
         c = np.cumsum(np.exp(x[r].astype(np.float64)))
         u[r] = np.float32(c[rng.integers(0, V)] / c[-1])
     check(draw(x, u, fp32), x, u)
+
+
+@pytest.mark.parametrize("filters", ["none", "min_p"])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_rows_at_the_ends_of_the_single_precision_range(sign, filters):
+    """Rows whose largest exponent max x log2(e) / T lies within some hundred of +-2^20: tokens of weight on both sides of
+    the number from which on exponents are not taken in single precision."""
+    rng = np.random.default_rng(21)
+    R, V = 96, 9001
+    temp = np.resize(np.array([2.0 ** -20, 1e-3, 1.0, 300.0], np.float32), R)
+    t = temp.astype(np.float64)[:, None]
+    base = (sign * 2.0 ** 20 + np.linspace(-130, 130, R)[:, None]) * np.log(2.0) * t
+    x = (base + t * rng.normal(0, 1.5, (R, V))).astype(np.float32)
+    # one token just above 2^20 less, all others just beyond it (their weights are 0.94)
+    for r in range(0, 8):
+        x[r] = -np.float32(np.log(2.0))
+        x[r, 7 + 900 * r] = np.nextafter(x[r, 0], np.float32(0))
+        temp[r] = 2.0 ** -20
+    u = rng.random(R).astype(np.float32)
+    k = dict(temp=temp)
+    if filters != "none":
+        k["min_p"] = np.full(R, 1e-12, np.float32)
+    assert np.array_equal(draw(x, u, True, **k), reference(x, u, **k))
