@@ -1255,19 +1255,23 @@ sample_kernel(const SampleArgs a, const __grid_constant__ ExpTable exp_table, in
           } else {
             const About ab = about(ex);
             const float x_least = fmaxf(floor_x, mx - kOctaves * 0.6931472f * temp);
-            float all_s = 0.f, all_e = 0.f, top_s = 0.f, top_e = 0.f;
+            const float x_top = fmaxf(x_hi, x_least);
+            // (`all` is made of the numbers that make `top`, and those of the rest: their errors are the same in
+            // both; a tree over all of a granule would round a large token's sum with its small neighbours again)
+            float rest_s = 0.f, rest_e = 0.f, top_s = 0.f, top_e = 0.f;
             each_granule([&](const float (&x)[kVec], int) {
-              float w[kVec];
+              float w[kVec], high[kVec];
               about_all(x, ab, w);
 #pragma unroll
-              for (int j = 0; j < kVec; ++j) w[j] = x[j] > x_least ? w[j] : 0.f;
-              add_in_two(tree_sum(w), &all_s, &all_e);
-#pragma unroll
-              for (int j = 0; j < kVec; ++j) w[j] = x[j] > x_hi ? w[j] : 0.f;
-              add_in_two(tree_sum(w), &top_s, &top_e);
+              for (int j = 0; j < kVec; ++j) {
+                high[j] = x[j] > x_top ? w[j] : 0.f;
+                w[j] = x[j] > x_least && !(x[j] > x_top) ? w[j] : 0.f;
+              }
+              add_in_two(tree_sum(w), &rest_s, &rest_e);
+              add_in_two(tree_sum(high), &top_s, &top_e);
               list(x);
             });
-            all = about_units(all_s, all_e), top = about_units(top_s, top_e);
+            top = about_units(top_s, top_e), all = about_units(rest_s, rest_e) + top;
           }
           all = warp_add(all), top = warp_add(top);
           if (lane == 0) sm.warp_u64[warp] = all, sm.warp_u64b[warp] = top;

@@ -120,3 +120,28 @@ def test_rows_at_the_ends_of_the_single_precision_range(sign, filters):
     if filters != "none":
         k["min_p"] = np.full(R, 1e-12, np.float32)
     assert np.array_equal(draw(x, u, True, **k), reference(x, u, **k))
+
+
+@pytest.mark.parametrize("with_k", [False, True])
+def test_top_p_cuts_where_large_tokens_share_granules_with_small_ones(with_k):
+    """64 tokens of weight 1, each beside one of 5.9e-8 (lost when the two are added in single precision), and a tail
+    whose values fall with the index: with u = 1 the token drawn is the last of top-p's prefix."""
+    rng = np.random.default_rng(23)
+    R, V, big = 64, 100000, 64
+    x = np.full((R, V), -np.inf, np.float32)
+    x[:, 0:4 * big:4] = 0.0
+    x[:, 2:4 * big:4] = np.float32(np.log(5.9e-8))
+    n = V - 4 * big
+    x[:, 4 * big:] = np.linspace(-13.6, -14.0, n)
+    p = rng.uniform(0.9987, 0.9999, R).astype(np.float32)
+    ones = np.ones(R, np.float32)
+    k = dict(top_p=p)
+    if with_k:
+        k["top_k"] = rng.integers(V - 3000, V - 2000, R).astype(np.int32)
+    got = draw(x, ones, True, **k)
+    for r in range(R):
+        order = np.argsort(-x[r], kind="stable")[:k["top_k"][r] if with_k else V]
+        c = np.cumsum(np.exp(x[r][order].astype(np.float64)))
+        goal, off = float(p[r]) * c[-1], open_(V, float(p[r]), c[-1])
+        lo, hi = (order[np.searchsorted(c, g, side="left")] for g in (goal - off, goal + off))
+        assert lo <= got[r] <= hi <= lo + 1, (r, got[r], lo, hi)
