@@ -712,7 +712,8 @@ int verify_attn_mla_tree_accept(const int32_t* qo_indptr, const int32_t* parent,
 namespace {
 // Lengths of a shared-prefix call, beyond those of a plain one.
 int check_shared(int64_t shared_rows, const int32_t* kv_indptr_host, int batch) {
-  if (shared_rows < 0 || batch > VMLA_MAX_BATCH - 1 || shared_rows + kv_indptr_host[batch] > INT32_MAX)
+  if (shared_rows < 0 || shared_rows > INT32_MAX || batch > VMLA_MAX_BATCH - 1 ||
+      shared_rows + kv_indptr_host[batch] > INT32_MAX)
     return VMLA_ERR_SHAPE;
   return VMLA_OK;
 }
