@@ -94,7 +94,8 @@ int run_verify(int kernel, const void* q, const void* kv_pool, int64_t pool_slot
   if (!aligned(run_base, 4)) return VMLA_ERR_ALIGN;
   if (total_kv > 0 && pool_slots == 0) return VMLA_ERR_SHAPE;
   if (!aligned(q, 16) || !aligned(kv_pool, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
-      !aligned(workspace, VMLA_WORKSPACE_ALIGN) || !aligned(draft_mask, 8) || !aligned(parent, 4))
+      !aligned(workspace, VMLA_WORKSPACE_ALIGN) || !aligned(draft_mask, 8) || !aligned(parent, 4) ||
+      !aligned(kv_indices, 4) || !aligned(qo_indptr, 4) || (runs && !aligned(kv_indptr, 4)))
     return VMLA_ERR_ALIGN;
   int sms = 0;
   rc = current_sm_count(&sms, true);
@@ -305,7 +306,7 @@ int defrag_impl(const void* src_pool, int64_t src_slots, const int32_t* kv_indpt
   if (total_kv == 0 && !(max_new > 0 && batch > 0)) return VMLA_OK;
   if (!src_pool || !dst_pool || !kv_indptr || !kv_indices || !run_base) return VMLA_ERR_NULL;
   if (!aligned(src_pool, 16) || !aligned(dst_pool, 16) || !aligned(status_word, 4) || !aligned(run_base, 4) ||
-      !aligned(first_row, 4))
+      !aligned(first_row, 4) || !aligned(kv_indptr, 4) || !aligned(kv_indices, 4))
     return VMLA_ERR_ALIGN;
   int sms = 0;
   int rc = current_sm_count(&sms, true);
@@ -375,7 +376,8 @@ int verify_attn_mla_tree_mask(const int32_t* parent, const int32_t* qo_indptr, i
   if (batch < 0 || batch > VMLA_MAX_BATCH || total_q < 0) return VMLA_ERR_SHAPE;
   if (total_q == 0) return VMLA_OK;
   if (!parent || !qo_indptr || !mask_out) return VMLA_ERR_NULL;
-  if (!aligned(mask_out, 8)) return VMLA_ERR_ALIGN;
+  if (!aligned(mask_out, 8) || !aligned(parent, 4) || !aligned(qo_indptr, 4) || !aligned(status_word, 4))
+    return VMLA_ERR_ALIGN;
   int sms = 0;
   int rc = current_sm_count(&sms, true);
   if (rc != VMLA_OK) return rc;
@@ -576,7 +578,7 @@ int device_plan_impl(const void* q, const void* kv_pool, int64_t pool_slots, con
   if (max_total_kv > 0 && pool_slots == 0) return VMLA_ERR_SHAPE;
   if (!aligned(q, 16) || !aligned(kv_pool, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
       !aligned(workspace, VMLA_WORKSPACE_ALIGN) || !aligned(draft_mask, 8) || !aligned(parent, 4) ||
-      !aligned(run_base, 4))
+      !aligned(run_base, 4) || !aligned(kv_indptr, 4) || !aligned(kv_indices, 4) || !aligned(qo_indptr, 4))
     return VMLA_ERR_ALIGN;
   int sms = 0, clusters = 0;
   rc = current_sm_count(&sms, true);
@@ -767,7 +769,7 @@ int verify_attn_mla_shared(const void* q, const void* kv_pool, int64_t pool_slot
   if (pool_slots == 0) return VMLA_ERR_SHAPE;
   if (!aligned(q, 16) || !aligned(kv_pool, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
       !aligned(workspace, VMLA_WORKSPACE_ALIGN) || !aligned(draft_mask, 8) || !aligned(parent, 4) ||
-      !aligned(shared_indices, 4) || !aligned(kv_indices, 4))
+      !aligned(shared_indices, 4) || !aligned(kv_indices, 4) || !aligned(qo_indptr, 4))
     return VMLA_ERR_ALIGN;
   int sms = 0, clusters = 0;
   rc = current_sm_count(&sms, true);

@@ -23,3 +23,36 @@ def test_shared_rows_past_every_integer(B, rows):
     size = ctypes.c_size_t(0)
     f = B.lib().verify_attn_mla_shared_workspace_size
     assert f(2, 16, rows, QOH.ctypes.data, KVH.ctypes.data, 0, ctypes.byref(size)) == B.VMLA_ERR_SHAPE
+
+
+P = 1 << 20  # an aligned address that is never dereferenced
+RUN = dict(q=P, pool=P, slots=64, kvp=P, kvi=P, qop=P, mask=None, parent=P, kvh=KVH, qoh=QOH, batch=2, heads=16,
+           sm_scale=0.1, splits=0, out=P, lse=P, ws=P, wsb=1 << 30, stream=None)
+RUNS = {k if k != "kvi" else "base": v for k, v in RUN.items()}
+FP8 = dict(q=P, pool=P, slots=64, scale=0.5, **{k: v for k, v in RUN.items() if k not in ("q", "pool", "slots")})
+DPLAN = dict(q=P, pool=P, slots=64, kvp=P, kvi=P, qop=P, mask=None, parent=P, batch=2, heads=16, max_q=6, max_kv=20,
+             sm_scale=0.1, splits=0, out=P, lse=P, ws=P, wsb=1 << 30, stream=None)
+DEFRAG = dict(pool=P, slots=64, kvp=P, kvi=P, kvh=KVH, batch=2, dst=P, dst_slots=64, base=P, status=P, stream=None)
+MASK = dict(parent=P, qop=P, batch=2, total_q=6, out=P, status=P, stream=None)
+# the int32 arrays that the kernels of an entry point read
+READ = {"verify_attn_mla": (RUN, ("kvi", "qop", "parent")), "verify_attn_mla_simt": (RUN, ("kvi", "qop", "parent")),
+        "verify_attn_mla_fp8": (FP8, ("kvi", "qop", "parent")), "verify_attn_mla_runs": (RUNS, ("kvp", "base", "qop", "parent")),
+        "verify_attn_mla_device_plan": (DPLAN, ("kvp", "kvi", "qop", "parent")),
+        "verify_attn_mla_defrag": (DEFRAG, ("kvp", "kvi", "base", "status")),
+        "verify_attn_mla_tree_mask": (MASK, ("parent", "qop", "status"))}
+
+
+@pytest.mark.parametrize("entry,array", [(e, a) for e, (_, arrays) in READ.items() for a in arrays])
+def test_int32_arrays_are_aligned(B, entry, array):
+    """A kernel's load of four bytes faults on any other address."""
+    def call(**kw):
+        a = {**READ[entry][0], **kw}
+        return getattr(B.lib(), entry)(*[v.ctypes.data if isinstance(v, np.ndarray) else v for v in a.values()])
+    for off in (1, 2, 3):
+        assert call(**{array: P + off}) == B.VMLA_ERR_ALIGN
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_int32_arrays_of_the_shared_call_are_aligned(B, off):
+    for array in ("shared", "kvi", "qop", "parent"):
+        assert _shared(B, **{array: P + off}) == B.VMLA_ERR_ALIGN
