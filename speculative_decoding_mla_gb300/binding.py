@@ -194,6 +194,14 @@ def _host_i32(a) -> np.ndarray:
     return np.ascontiguousarray(a, dtype=np.int32)
 
 
+def _host_pair(batch_from, other, names):
+    """Both host offset arrays; the call takes the batch from the first and reads as many entries of the second."""
+    a, b = _host_i32(batch_from), _host_i32(other)
+    if len(a) > len(b):
+        raise ValueError(f"{names}: batch + 1 entries each expected, got {len(a)} and {len(b)}")
+    return a, b
+
+
 def _stream(stream):
     if stream is None:
         import torch
@@ -206,8 +214,7 @@ def _stream(stream):
 def verify_attn_mla_plan(kernel: int, qo_indptr_host, kv_indptr_host, num_heads: int, splits: int = 0,
                          num_sms: int = 152):
     """Host-only split plan: (PlanInfo, splits per sequence)."""
-    qo = _host_i32(qo_indptr_host)
-    kv = _host_i32(kv_indptr_host)
+    qo, kv = _host_pair(qo_indptr_host, kv_indptr_host, "qo_indptr_host, kv_indptr_host")
     B = len(qo) - 1
     info = PlanInfo()
     per = np.zeros(max(B, 1), dtype=np.int32)
@@ -217,8 +224,7 @@ def verify_attn_mla_plan(kernel: int, qo_indptr_host, kv_indptr_host, num_heads:
 
 
 def verify_attn_mla_workspace_size(qo_indptr_host, kv_indptr_host, num_heads: int, splits: int = 0) -> int:
-    qo = _host_i32(qo_indptr_host)
-    kv = _host_i32(kv_indptr_host)
+    qo, kv = _host_pair(qo_indptr_host, kv_indptr_host, "qo_indptr_host, kv_indptr_host")
     n = ctypes.c_size_t(0)
     _check(_lib.verify_attn_mla_workspace_size(len(qo) - 1, num_heads, qo.ctypes.data, kv.ctypes.data, splits,
                                                ctypes.byref(n)), "verify_attn_mla_workspace_size")
@@ -248,8 +254,7 @@ class Prepared:
 
 def _run_args(q, kv_pool, kv_indptr, kv_indices, qo_indptr, kv_indptr_host, qo_indptr_host, out, lse, workspace,
               sm_scale, draft_mask=None, parent=None, splits=0, stream=None, num_heads=None, pool_slots=None):
-    kvh = _host_i32(kv_indptr_host)
-    qoh = _host_i32(qo_indptr_host)
+    kvh, qoh = _host_pair(kv_indptr_host, qo_indptr_host, "kv_indptr_host, qo_indptr_host")
     H = int(num_heads if num_heads is not None else q.shape[1])
     S = int(pool_slots if pool_slots is not None else kv_pool.shape[0])
     args = (_d(q, 2, "q"), _d(kv_pool, 2, "kv_pool"), S, _d(kv_indptr, 4, "kv_indptr"),
@@ -418,8 +423,7 @@ def prepare_verify_attn_mla_append(*a, **k) -> Prepared:
 
 def verify_attn_mla_shared_workspace_size(shared_rows: int, qo_indptr_host, kv_indptr_host, num_heads: int,
                                           splits: int = 0) -> int:
-    qo = _host_i32(qo_indptr_host)
-    kv = _host_i32(kv_indptr_host)
+    qo, kv = _host_pair(qo_indptr_host, kv_indptr_host, "qo_indptr_host, kv_indptr_host")
     n = ctypes.c_size_t(0)
     _check(_lib.verify_attn_mla_shared_workspace_size(len(qo) - 1, num_heads, int(shared_rows), qo.ctypes.data,
                                                       kv.ctypes.data, splits, ctypes.byref(n)),
@@ -429,8 +433,7 @@ def verify_attn_mla_shared_workspace_size(shared_rows: int, qo_indptr_host, kv_i
 
 def _shared_args(q, kv_pool, shared_indices, kv_indptr, kv_indices, qo_indptr, kv_indptr_host, qo_indptr_host, out,
                  lse, workspace, sm_scale, kv_scale=0.0, draft_mask=None, parent=None, splits=0, stream=None):
-    kvh = _host_i32(kv_indptr_host)
-    qoh = _host_i32(qo_indptr_host)
+    kvh, qoh = _host_pair(kv_indptr_host, qo_indptr_host, "kv_indptr_host, qo_indptr_host")
     if len(kvh) != len(qoh) or len(kvh) < 1:
         raise ValueError("kv_indptr_host and qo_indptr_host: batch + 1 entries each expected")
     T, H, N = int(qoh[-1]), int(q.shape[1]), int(kvh[-1])
@@ -503,8 +506,7 @@ def prepare_verify_attn_mla_sample(*a, **k) -> Prepared:
 
 
 def verify_attn_mla_runs_workspace_size(qo_indptr_host, kv_indptr_host, num_heads: int, splits: int = 0) -> int:
-    qo = _host_i32(qo_indptr_host)
-    kv = _host_i32(kv_indptr_host)
+    qo, kv = _host_pair(qo_indptr_host, kv_indptr_host, "qo_indptr_host, kv_indptr_host")
     n = ctypes.c_size_t(0)
     _check(_lib.verify_attn_mla_runs_workspace_size(len(qo) - 1, num_heads, qo.ctypes.data, kv.ctypes.data, splits,
                                                     ctypes.byref(n)), "verify_attn_mla_runs_workspace_size")
@@ -529,8 +531,7 @@ def prepare_verify_attn_mla_runs(q, kv_pool, kv_indptr, run_base, qo_indptr, kv_
 
 def _fp8_args(q, kv_pool_e4m3, kv_scale, kv_indptr, kv_indices, qo_indptr, kv_indptr_host, qo_indptr_host, out, lse,
               workspace, sm_scale, draft_mask=None, parent=None, splits=0, stream=None):
-    kvh = _host_i32(kv_indptr_host)
-    qoh = _host_i32(qo_indptr_host)
+    kvh, qoh = _host_pair(kv_indptr_host, qo_indptr_host, "kv_indptr_host, qo_indptr_host")
     args = (_d(q, 2, "q"), _d(kv_pool_e4m3, 1, "kv_pool_e4m3"), int(kv_pool_e4m3.shape[0]), float(kv_scale),
             _d(kv_indptr, 4, "kv_indptr"), _d(kv_indices, 4, "kv_indices"), _d(qo_indptr, 4, "qo_indptr"),
             _d(draft_mask, 8, "draft_mask"), _d(parent, 4, "parent"), kvh.ctypes.data, qoh.ctypes.data, len(kvh) - 1,
@@ -599,8 +600,7 @@ def verify_attn_mla_check(workspace, stream=None) -> int:
 
 def verify_attn_mla_host_buffer_size(qo_indptr_host, kv_indptr_host, num_heads: int, splits: int = 0,
                                      has_mask: bool = False, has_parent: bool = False) -> int:
-    qo = _host_i32(qo_indptr_host)
-    kv = _host_i32(kv_indptr_host)
+    qo, kv = _host_pair(qo_indptr_host, kv_indptr_host, "qo_indptr_host, kv_indptr_host")
     n = ctypes.c_size_t(0)
     _check(_lib.verify_attn_mla_host_buffer_size(len(qo) - 1, num_heads, qo.ctypes.data, kv.ctypes.data, splits,
                                                  int(has_mask), int(has_parent), ctypes.byref(n)),
@@ -610,8 +610,7 @@ def verify_attn_mla_host_buffer_size(qo_indptr_host, kv_indptr_host, num_heads: 
 
 def _host_args(q_host, kv_pool, kv_indptr_host, kv_indices_host, qo_indptr_host, out_host, lse_host, device_buffer,
                sm_scale, draft_mask_host=None, parent_host=None, splits=0, stream=None, num_heads=None):
-    kvh = _host_i32(kv_indptr_host)
-    qoh = _host_i32(qo_indptr_host)
+    kvh, qoh = _host_pair(kv_indptr_host, qo_indptr_host, "kv_indptr_host, qo_indptr_host")
     H = int(num_heads if num_heads is not None else q_host.shape[1])
     args = (_h(q_host, 2, "q_host"), _d(kv_pool, 2, "kv_pool"), int(kv_pool.shape[0]), kvh.ctypes.data,
             _h(kv_indices_host, 4, "kv_indices_host"), qoh.ctypes.data, _h(draft_mask_host, 8, "draft_mask_host"),
@@ -659,8 +658,7 @@ STATIC_SCRATCH_BYTES = 32 << 20
 def verify_attn_mla_simt_static(q, kv_pool, kv_indptr, kv_indices, qo_indptr, kv_indptr_host, qo_indptr_host, out,
                                 lse, sm_scale, draft_mask=None, parent=None, splits=0, stream=None):
     """CUDA-core verify with the library's fixed scratch array instead of a workspace (no allocation)."""
-    kvh = _host_i32(kv_indptr_host)
-    qoh = _host_i32(qo_indptr_host)
+    kvh, qoh = _host_pair(kv_indptr_host, qo_indptr_host, "kv_indptr_host, qo_indptr_host")
     rc = _lib.verify_attn_mla_simt_static(_d(q, 2, "q"), _d(kv_pool, 2, "kv_pool"), int(kv_pool.shape[0]),
                                           _d(kv_indptr, 4, "kv_indptr"), _d(kv_indices, 4, "kv_indices"),
                                           _d(qo_indptr, 4, "qo_indptr"), _d(draft_mask, 8, "draft_mask"),

@@ -56,3 +56,34 @@ def test_int32_arrays_are_aligned(B, entry, array):
 def test_int32_arrays_of_the_shared_call_are_aligned(B, off):
     for array in ("shared", "kvi", "qop", "parent"):
         assert _shared(B, **{array: P + off}) == B.VMLA_ERR_ALIGN
+
+
+def test_host_offsets_of_different_lengths(B):
+    """Every call takes the batch from one of the two host arrays and reads as many entries of the other."""
+    import torch
+    qo, kv = QOH, KVH
+    sizes = [lambda q, k: B.verify_attn_mla_workspace_size(q, k, 16), lambda q, k: B.verify_attn_mla_plan(0, q, k, 16),
+             lambda q, k: B.verify_attn_mla_runs_workspace_size(q, k, 16),
+             lambda q, k: B.verify_attn_mla_host_buffer_size(q, k, 16),
+             lambda q, k: B.verify_attn_mla_shared_workspace_size(10, q, k, 16)]
+    for f in sizes:
+        for bad in (kv[:2], kv[:1], kv[:0]):
+            with pytest.raises(ValueError, match="entries"):
+                f(qo, bad)
+    q, pool = torch.zeros(6, 16, 576, dtype=torch.bfloat16), torch.zeros(64, 576, dtype=torch.bfloat16)
+    idx, ptr = torch.zeros(20, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    out, lse, ws = torch.zeros(6, 16, 512, dtype=torch.bfloat16), torch.zeros(6, 16), torch.zeros(256, dtype=torch.uint8)
+    for bad in (qo[:2], qo[:0]):
+        for f in (B.verify_attn_mla, B.verify_attn_mla_simt):
+            with pytest.raises(ValueError, match="entries"):
+                f(q, pool, ptr, idx, ptr, kv, bad, out, lse, ws, 0.1)
+        with pytest.raises(ValueError, match="entries"):
+            B.verify_attn_mla_fp8(q, pool, 0.5, ptr, idx, ptr, kv, bad, out, lse, ws, 0.1)
+        with pytest.raises(ValueError, match="entries"):
+            B.verify_attn_mla_simt_static(q, pool, ptr, idx, ptr, kv, bad, out, lse, 0.1)
+        with pytest.raises(ValueError, match="entries"):
+            B.verify_attn_mla_runs(q, pool, ptr, ptr, ptr, kv, bad, out, lse, ws, 0.1)
+        with pytest.raises(ValueError, match="entries"):
+            B.verify_attn_mla_host(q, pool, kv, idx, bad, out, lse, ws, 0.1)
+        with pytest.raises(ValueError, match="entries"):
+            B.verify_attn_mla_shared(q, pool, idx[:10], ptr, idx, ptr, kv, bad, out, lse, ws, 0.1)
