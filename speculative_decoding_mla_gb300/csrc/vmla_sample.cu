@@ -1713,15 +1713,15 @@ sample_plain_kernel(const SampleArgs a, int iters) {
       uint64_t upto = before + warp_scan(m, lane) - m;
       // the token, or a mark where no sum, or one next to the goal, decides
       int token = kUndecided;
-      if (upto <= goal && goal < upto + m) {  // one lane, if any
+      uint64_t low = 0, high = 0;  // its borders
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) {
-          if (upto <= goal && goal < upto + w[k] && goal - upto >= about_margin(u, all, upto - run, kAnewError) &&
-              upto + w[k] - goal > about_margin(u, all, upto + w[k] - run, kAnewError))
-            token = start + i * kStep + k - shift;
-          upto += w[k];
-        }
+      for (int k = 0; k < kVec; ++k) {
+        if (upto <= goal && goal < upto + w[k]) token = start + i * kStep + k - shift, low = upto, high = upto + w[k];
+        upto += w[k];
       }
+      if (token != kUndecided && (goal - low < about_margin(u, all, low - run, kAnewError) ||
+                                  high - goal <= about_margin(u, all, high - run, kAnewError)))
+        token = kUndecided;
       const uint32_t found = __ballot_sync(0xffffffffu, token != kUndecided);
       if (found ? lane == __ffs(found) - 1 : lane == 0) a.token[row] = token;
     }
