@@ -54,6 +54,7 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 #include <type_traits>
@@ -1848,7 +1849,10 @@ sample_plain_exact_kernel(const SampleArgs a, const __grid_constant__ ExpTable e
 // CTAs per row: more while that leaves SMs idle, or while rows are long (over 8 iterations of 8 KB a CTA) and
 // most of the CTAs still find room at once (clusters do not fill every SM: 76 rows by four did not fit), or while
 // they are longer (over 20) and the CTAs take at most two rounds; eight only while SMs idle.  More too while
-// one CTA's share of a row is over 40 iterations; the row stays in shared memory where a share is at most 64 KB.
+// one CTA's share of a row is over 40 iterations (bf16: 33, what kMaxElems allows: 135,168 tokens); the row stays in
+// shared memory where a share is at most 64 KB.  The rule does not look at which filters are given: 128 rows of
+// 151,001 fp32 get four CTAs, 85 us with all filters (91 by two), 139 with top-p alone (140 by two), but
+// 125 (108 by two) with top-p alone where many tokens are at -inf.
 // Measured, us by cluster size 1 / 2 / 4 / 8, top-p of 131,072 bf16: 512 rows 130 / 148 / 190 / 336, 300 rows 100 / 94 /
 // 123 / 202, 150 rows 55 / 50 / 72 / 110, 76 rows 53 / 37 / 47 / 66, 64 rows 53 / 35 / 31 / 51, 16 rows 51 / 35 / 24 / 26; all
 // filters of 151,001 fp32: 512 rows - / 205 / 245 / 390, 300 rows - / 146 / 157 / 240, 128 rows - / 89 / 83 / 116, 76 rows
@@ -1868,17 +1872,17 @@ int iterations(const SampleArgs& a, int cluster) {
 template <typename T>
 Shape choose_shape(const SampleArgs& a, int sms) {
   auto need = [&](int c) { return iterations<T>(a, c); };
+  constexpr int kMost = std::min(40, kMaxElems / Elems<T>::kVec);
   Shape s;
   s.cluster = 1;  // (a vocabulary of up to kList tokens stays in one CTA: one iteration holds it)
   while (s.cluster < kMaxCluster && need(s.cluster) > 1) {
     const int64_t ctas = a.rows * s.cluster * 2;
     const int n = need(s.cluster), room = s.cluster == 4 ? sms : n > 20 ? 4 * sms : sms + sms * 3 / 4;
-    if (!(n > 40 || ctas <= sms / 2 || (n > 8 && ctas <= room))) break;
+    if (!(n > kMost || ctas <= sms / 2 || (n > 8 && ctas <= room))) break;
     s.cluster *= 2;
   }
-  s.keep = need(s.cluster) <= kKeepIters;
-  while (s.cluster < kMaxCluster && need(s.cluster) > kMaxElems / Elems<T>::kVec) s.cluster *= 2;
   s.iters = need(s.cluster);
+  s.keep = s.iters <= kKeepIters;
   return s;
 }
 // Without filters a CTA does one pass and two more barriers: more CTAs per row pay off only while all are
