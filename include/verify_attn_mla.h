@@ -346,7 +346,8 @@ int verify_attn_mla_fp8(const void* q, const void* kv_pool_e4m3, int64_t pool_sl
  * (info of VMLA_ERR_INDEX: the row in shared order, then kv_indices' order).
  * All queries' partial results have to fit 2^31 elements
  * (total_q x num_heads x pieces x 512), else VMLA_ERR_SHAPE.  shared_rows 0 is
- * verify_attn_mla itself. */
+ * verify_attn_mla itself.  The plan is made on the host: a captured call replays
+ * the lengths it was captured with (new indices, rows and queries are read). */
 int verify_attn_mla_shared_workspace_size(int batch, int num_heads, int64_t shared_rows, const int32_t* qo_indptr_host,
                                           const int32_t* kv_indptr_host, int splits, size_t* bytes);
 int verify_attn_mla_shared(const void* q, const void* kv_pool, int64_t pool_slots, float kv_scale,
@@ -366,9 +367,13 @@ int verify_attn_mla_shared(const void* q, const void* kv_pool, int64_t pool_slot
  *   min-p keeps the tokens with w_i >= min_p[r]
  *   token[r] = the smallest index i with sum over kept j <= i of w_j
  *              > uniform[r] x sum over all kept of w_j
- * and for T = 0 the lowest index among the largest logits.  Weights are exact to
- * about 2^-37 and summed without rounding, so the result does not depend on the
- * order of summation; weights below 2^-46 of the largest count as zero.
+ * and for T = 0 the lowest index among the largest logits.  Weights are computed
+ * to about 2^-37, rounded to whole units of 2^-45 of the largest (below 2^-46 of it
+ * they count as zero) and summed without further rounding, so the result does not
+ * depend on the order of summation, and is the definition's unless u or top_p times
+ * the mass lies within vocab x 2^-46 of the largest weight, and 2^-37 of the mass,
+ * of a running sum.  Rows with top-p whose logits take few values, or differ by far
+ * less than T, take several times as long as others (their tokens share a bin).
  *   logits   [rows, vocab], logits_fp32 0: bf16, 1: fp32; row_stride elements
  *            from row to row (>= vocab; any alignment to the element's size).
  *            -inf forbids a token and NaN counts as -inf; tokens at +inf share
@@ -527,7 +532,8 @@ int verify_attn_mla_host(const void* q_host, const void* kv_pool, int64_t pool_s
 /* Measurement aid.  verify_attn_mla_timing_enable(n) creates host-side CUDA
  * events for the next n run calls (0 turns it off and frees them); while it is
  * on, every verify_attn_mla, _simt, _runs, _fp8 and _host call (not the
- * device-planned form) records events on its stream around each kernel it
+ * device-planned form, nor verify_attn_mla_shared with shared rows, the append
+ * or the sampling) records events on its stream around each kernel it
  * launches.  verify_attn_mla_timing_read() waits
  * for those events and writes, per call in launch order, the device time in ms
  * of the KV gather kernel, the verify kernel and the merge kernel (0 for a

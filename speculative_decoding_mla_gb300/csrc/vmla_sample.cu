@@ -13,9 +13,9 @@
 // The result is a whole number, so the sums that decide it must not depend on
 // the order of summation or on single precision: among 10^5 tokens a relative
 // error of 2^-20 would move the draw in one row of ten.  A weight is computed in
-// pairs of floats to about 2^-37 (weight_of) and added as a 64-bit integer in
-// units of 2^-45; integer sums are exact in any order.  Weights below 2^-46 of
-// the largest count as zero.
+// pairs of floats to about 2^-37 (weight_of), rounded to whole units of 2^-45 of
+// the largest and added as a 64-bit integer; integer sums are exact in any order.
+// Weights below 2^-46 of the largest count as zero.
 //
 // One cluster of one to eight CTAs takes one row.  With few rows a row is kept in
 // shared memory; with many, its later passes read it again, from L2, which lets
@@ -40,15 +40,22 @@
 // any filter (which read a row once, in a kernel of their own), by a second launch.
 //
 // What bounds it: 512 rows of 131,072 bf16 (134 MB, 20 us of reading) take 80 us without a
-// filter, instructions (23 a token: the weight 13, the loop 5, the rest the search), and
+// filter, instructions (22 a token: the weight 13, the loop 5, the rest the search), and
 // 130 us with top-p.  There a row is one CTA's, two on an SM, for 53 us: maximum and
 // histogram 18 (its shared-memory atomics, 3.8 cycles a warp for their banks' conflicts,
 // take 28 us of the whole call, and make the other CTA's shared memory slow meanwhile;
 // maximum and histogram in two passes: 145 us), values next to zero 5, cuts 7, the sums of
 // the draw 14, its search 6, barriers.  A row that the draw's first sums do not decide (one
 // in some hundred) takes 20 us more, 45 if all its tokens and not the kept ones are
-// weighed.  128 rows of 151,001 fp32 take 123 us with top-p and 84 with all filters (of
-// which most have top-k): 225 and 130 where all masses for top-p are exact.
+// weighed.  128 rows of 151,001 fp32 take 125 to 139 us with top-p and 85 to 93 with all filters
+// (of which most have top-k): 225 and 130 where all masses for top-p are exact.  At 64 registers a
+// thread the filtered kernel spills 588 (bf16) and 572 (fp32) bytes, 136 and 128 where the row is in
+// shared memory; the kernel without filters, at 40, 28 and 40.
+// Times depend on the values.  Rows of one or two values, or of a spread far below the temperature,
+// have many tokens in top-p's bin: their keys pass the list, each round reads the row again, and the
+// atomics go to few addresses.  128 rows of 151,001 with top-p 0.9 take 155 us (fp32) and 76 (bf16)
+// for normal logits of deviation 2, 340 and 410 of 10^-4, 670 and 500 for two values, 290 to 460 and
+// 66 to 515 for one value.
 // Tried and not kept: whole rows in shared memory for 512 rows (216 us), undecided rows of
 // the filtered kernel by a second launch (203 -> 215 us), more loads in flight.
 #include <cooperative_groups.h>
