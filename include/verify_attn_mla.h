@@ -55,6 +55,9 @@ extern "C" {
 #define VMLA_MAX_BATCH 512
 #define VMLA_MAX_HEADS 128
 #define VMLA_MAX_VOCAB 262144 /* tokens of a row that verify_attn_mla_sample draws from */
+#define VMLA_MAX_BLOCK_TOKENS 128 /* slots that share a scale (verify_attn_mla_scaled): a power of two up to this */
+#define VMLA_MAX_BEAMS 16     /* beams of a request (verify_attn_mla_beam_select) */
+#define VMLA_MAX_BEAM_KEEP 32 /* continuations it keeps */
 #define VMLA_WORKSPACE_ALIGN 256
 
 typedef enum vmla_status {
@@ -69,7 +72,8 @@ typedef enum vmla_status {
                               with a row of zeros (score 0, value 0), in every kernel */
   VMLA_ERR_DEVICE = -8,    /* no usable sm_103 device for this library */
   VMLA_ERR_PARENT = -9,    /* a parent index was not in [-1, i) (mask left empty) */
-  VMLA_ERR_PARAM = -10     /* a row's sampling setting was out of range (that row draws no token) */
+  VMLA_ERR_PARAM = -10,    /* a row's sampling setting was out of range (that row draws no token) */
+  VMLA_ERR_FULL = -11      /* a step's keys, tokens or new blocks exceed the arrays or the free list */
 } vmla_status;
 
 /* Description of the split plan a call would use (host only, no GPU needed). */
@@ -433,6 +437,147 @@ int verify_attn_mla_append(const void* latent, int64_t latent_stride, const void
                            const int32_t* positions, const int32_t* slots, const float* cos_sin, int64_t table_rows,
                            int neighbour_pairs, int64_t tokens, int num_heads, void* kv_pool, int64_t pool_slots,
                            float kv_scale, void* q, uint32_t* status_word, void* stream);
+
+/* Append of new tokens' rows to an e4m3 pool with one scale per block of
+ * block_tokens slots (1, 2, 4 .. 128): the value of a code in slot s is its
+ * e4m3 value times kv_scales[s / block_tokens].  Arguments, rotation, padding
+ * and errors as for verify_attn_mla_append; in place of one scale:
+ *   kv_scales [pool_slots / block_tokens] fp32, read and written; pool_slots is
+ *             a multiple of block_tokens
+ * The call's rows of one block set its scale:
+ *   need  = the smallest 2^k (k >= -100) with every |value| <= 448 x 2^k
+ *   scale = need if they begin at the block's first slot (what the block held
+ *           before is gone), else the larger of need and the block's scale
+ * and where that raises the scale, the block's rows in front of them are coded
+ * again: e4m3(code x old / new), nearest even (rows behind them keep their
+ * codes: nothing valid lies there when a cache grows in order).  A value of
+ * +-inf is coded as the largest code, NaN as the NaN code, which the attention
+ * does not accept.
+ * The tokens of one block stand together in the call, their slots ascending
+ * (as verify_attn_mla_step_tables lists them); tokens of a block that stand
+ * apart would set its scale twice, in either order.  A token left out by an
+ * error takes no part in its block's scale.  Appending the same rows again
+ * leaves the pool and the scales as they are. */
+int verify_attn_mla_append_scaled(const void* latent, int64_t latent_stride, const void* k_rope, int64_t k_rope_stride,
+                                  const void* q_rope, int64_t q_rope_stride_t, int64_t q_rope_stride_h,
+                                  const int32_t* positions, const int32_t* slots, const float* cos_sin,
+                                  int64_t table_rows, int neighbour_pairs, int64_t tokens, int num_heads,
+                                  void* kv_pool_e4m3, int64_t pool_slots, float* kv_scales, int block_tokens, void* q,
+                                  uint32_t* status_word, void* stream);
+
+/* The verify attention over such a pool, read in 8 bits (no staged bf16 copy),
+ * with the lengths read on the device: for single tokens (Q_b = 1), drafts and
+ * trees alike.  The definition at the top of this file with
+ *   row_j = kv_scales[s / block_tokens] x code values of slot s = kv_indices[kv_indptr[b] + j]
+ * (real products; no rounding of rows).  Scores, softmax and sums are fp32; the
+ * queries enter in two e4m3 parts (to 2^-22 of the largest of 32 rows), the
+ * weights with 9 significant bits, out is rounded once to bf16.
+ *   kv_scales  fp32, finite and >= 0 (below 2^-100: the block's values count as
+ *              zero, scored by the scale as it is)
+ *   pool_slots a multiple of block_tokens; the pool is 16-byte aligned
+ *   batch, num_heads, draft_mask, parent, q, out, lse: as for verify_attn_mla;
+ *              N_b may be any length the pool holds, Q_b up to 64
+ *   max_total_q, max_total_kv  bounds on qo_indptr[batch] and kv_indptr[batch]
+ *              at every replay, as for verify_attn_mla_device_plan: q, out and
+ *              lse hold max_total_q rows, kv_indices max_total_kv entries
+ *   workspace  >= verify_attn_mla_scaled_workspace_size() bytes, 256 B aligned,
+ *              for this call alone while it runs; its size depends on the device only
+ * A sequence without drafts writes nothing; rows of q, out and lse from
+ * qo_indptr[batch] on are left as they are.  Rows of kv_indices that no query
+ * of the sequence sees still have to hold codes other than NaN.
+ * Capture-safe; no host synchronisation.  Lengths out of order or past a bound
+ * are found on the device: nothing is computed and VMLA_ERR_SHAPE recorded.  A
+ * slot outside the pool takes part as a row of zeros and records VMLA_ERR_INDEX
+ * (index into kv_indices); malformed parents record VMLA_ERR_PARENT. */
+int verify_attn_mla_scaled_workspace_size(int batch, int num_heads, int64_t max_total_q, int64_t max_total_kv,
+                                          size_t* bytes);
+int verify_attn_mla_scaled(const void* q, const void* kv_pool_e4m3, int64_t pool_slots, const float* kv_scales,
+                           int block_tokens, const int32_t* kv_indptr, const int32_t* kv_indices,
+                           const int32_t* qo_indptr, const uint64_t* draft_mask, const int32_t* parent, int batch,
+                           int num_heads, int64_t max_total_q, int64_t max_total_kv, float sm_scale, void* out,
+                           float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The tables of a decode step from its requests' lengths, on the device: what
+ * the append and the device-planned and scaled attention calls take.  Request b
+ * holds cached[b] tokens and gets added[b] more (a prompt, a token, drafts):
+ *   n_b = cached[b] + added[b];  kv_indptr, qo_indptr = running sums of n_b, added[b]
+ *   its blocks of block_tokens slots: the first ceil(cached[b] / block_tokens)
+ *       entries of row b of block_table, then fresh ones, which the call takes
+ *       from the free list (free_blocks[count - 1] first, in the order of the
+ *       requests) and writes into the table
+ *   slot(b, p) = block(b, p / block_tokens) x block_tokens + p mod block_tokens
+ *   kv_indices[kv_indptr[b] + p] = slot(b, p) for p < n_b
+ *   positions, slots[qo_indptr[b] + i] = cached[b] + i and its slot, for i < added[b];
+ *       behind the last token positions 0 and slots -1 (padding for the appends)
+ * kv_indices behind the last key is left as it is.
+ *   cached, added  [batch] int32 >= 0
+ *   block_table    [batch, table_width] int32, table_stride entries from row to row
+ *   free_blocks    [free_size] int32;  free_count [1] int32: how many are free
+ *   free_left      [1] int32 out: how many are left (may be free_count itself,
+ *                  as a captured step needs it)
+ *   scratch        [1] uint32, zero at the first call; every call leaves it zero
+ *   kv_indices [max_total_kv], positions, slots [max_total_q], kv_indptr,
+ *   qo_indptr [batch + 1] int32 out
+ *   status_word    optional, two uint32
+ * block_tokens 1 makes block_table a table of slots.  An entry of the table that
+ * is negative, or whose slots pass 2^31, gives slots of -1.  A negative length or
+ * a request longer than the table's row records VMLA_ERR_SHAPE (request), and
+ * more keys, tokens or new blocks than there is room for VMLA_ERR_FULL: the
+ * step is then empty (indptr arrays 0, slots -1) and nothing is taken.
+ * One launch, no host synchronisation; capture-safe.  Calls on one free list are
+ * ordered on one stream, and a graph that replays the call with free_left in
+ * place of free_count's memory goes on where the last replay stopped. */
+int verify_attn_mla_step_tables(const int32_t* cached, const int32_t* added, int batch, int block_tokens,
+                                int32_t* block_table, int64_t table_stride, int64_t table_width,
+                                const int32_t* free_blocks, int64_t free_size, const int32_t* free_count,
+                                int32_t* free_left, uint32_t* scratch, int64_t max_total_q, int64_t max_total_kv,
+                                int32_t* kv_indptr, int32_t* qo_indptr, int32_t* kv_indices, int32_t* positions,
+                                int32_t* slots, uint32_t* status_word, void* stream);
+
+/* Beam search's selection: the best `keep` continuations of each request over
+ * its beams and the vocabulary.  Row r beams + w of logits x belongs to beam w
+ * of request r, whose score so far is c:
+ *   a beam that goes on offers every token v at c + x_v - ln sum_u exp(x_u)
+ *   a finished one (finished[row] != 0) offers pad_token alone, at c
+ *   a beam with c = -inf (or NaN) offers nothing
+ * parent (beam), token and new_score [requests, keep] get the best ones in
+ * descending order, equal ones by the index beam x vocab + token; places
+ * without a continuation hold -1, -1 and -inf.  -inf forbids a token, NaN
+ * counts as -inf, and tokens at +inf share their row evenly.
+ * Within a beam the order is the logits' own; scores of different beams are
+ * compared to about 2^-27, whatever the order of summation.
+ *   logits    [requests x beams, vocab], logits_fp32 0: bf16, 1: fp32; row_stride
+ *             elements from row to row (>= vocab; any alignment to the element's size)
+ *   beams     1 .. VMLA_MAX_BEAMS;  keep 1 .. VMLA_MAX_BEAM_KEEP;  requests <= 65535
+ *   vocab     1 .. VMLA_MAX_VOCAB;  pad_token in [0, vocab)
+ *   score     [requests x beams] fp32;  finished [requests x beams] int32 or NULL
+ *   workspace >= verify_attn_mla_beam_select_workspace_size() bytes (rows =
+ *             requests x beams), 256 B aligned, for this call alone while it runs
+ * parent, token and new_score overlap no input.  Two launches, no host
+ * synchronisation; capture-safe. */
+int verify_attn_mla_beam_select_workspace_size(int64_t rows, int vocab, int keep, size_t* bytes);
+int verify_attn_mla_beam_select(const void* logits, int logits_fp32, int64_t row_stride, int64_t requests, int beams,
+                                int keep, int vocab, const float* score, const int32_t* finished, int pad_token,
+                                int32_t* parent, int32_t* token, float* new_score, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* Reorders the beams' states after the selection: row r keep + k of dst gets
+ * row r beams + parent[r, k] of src.  A state is a row of 32-bit words: a
+ * beam's table of slots (its cache, at block_tokens 1: rows are shared, not
+ * copied), a hidden state of an even number of bf16.
+ *   src [requests x beams, row_words], dst [requests x keep, row_words], with
+ *       their strides in words; dst overlaps no input
+ *   length     [requests x beams] int32 or NULL: words of each row that count
+ *              (the rest of the dst row is left as it is)
+ *   new_length [requests x keep] int32 or NULL: length of the parent
+ *   status_word  optional, two uint32: a parent outside [-1, beams) or a length
+ *              outside [0, row_words] records VMLA_ERR_INDEX (row of dst; the
+ *              row is left alone, or cut to row_words)
+ * parent -1 leaves its row as it is, with new_length 0.  One launch,
+ * capture-safe. */
+int verify_attn_mla_beam_reorder(const void* src, int64_t src_stride_words, void* dst, int64_t dst_stride_words,
+                                 int64_t row_words, int64_t requests, int beams, int keep, const int32_t* parent,
+                                 const int32_t* length, int32_t* new_length, uint32_t* status_word, void* stream);
 
 /* Fixed size of the scratch array behind verify_attn_mla_simt_static (32 MiB). */
 #define VMLA_STATIC_SCRATCH_BYTES (32u << 20)

@@ -28,12 +28,16 @@ VMLA_ERR_INDEX = -7
 VMLA_ERR_DEVICE = -8
 VMLA_ERR_PARENT = -9
 VMLA_ERR_PARAM = -10
+VMLA_ERR_FULL = -11
 VMLA_KERNEL_TC = 0
 VMLA_KERNEL_SIMT = 1
 VMLA_SPLITS_LANES = -1  # splits value: the tensor-core planner takes its lane plan where it fits
 D_QK = 576
 D_V = 512
 MAX_VOCAB = 262144
+MAX_BLOCK_TOKENS = 128
+MAX_BEAMS = 16
+MAX_BEAM_KEEP = 32
 
 EXPORTS = (
     "verify_attn_mla_plan", "verify_attn_mla_workspace_size", "verify_attn_mla", "verify_attn_mla_simt",
@@ -46,7 +50,9 @@ EXPORTS = (
     "verify_attn_mla_simt_static_check", "verify_attn_mla_defrag_append",
     "verify_attn_mla_runs_device_plan_workspace_size", "verify_attn_mla_runs_device_plan",
     "verify_attn_mla_append", "verify_attn_mla_shared", "verify_attn_mla_shared_workspace_size",
-    "verify_attn_mla_sample",
+    "verify_attn_mla_sample", "verify_attn_mla_append_scaled", "verify_attn_mla_scaled",
+    "verify_attn_mla_scaled_workspace_size", "verify_attn_mla_step_tables", "verify_attn_mla_beam_select",
+    "verify_attn_mla_beam_select_workspace_size", "verify_attn_mla_beam_reorder",
 )
 
 
@@ -99,6 +105,15 @@ def _load(path: str = LIB_PATH):
                                    sz, vp],
         "verify_attn_mla_shared_workspace_size": [i32, i32, i64, vp, vp, i32, ctypes.POINTER(sz)],
         "verify_attn_mla_sample": [vp, i32, i64, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp],
+        "verify_attn_mla_append_scaled": [vp, i64, vp, i64, vp, i64, i64, vp, vp, vp, i64, i32, i64, i32, vp, i64, vp,
+                                          i32, vp, vp, vp],
+        "verify_attn_mla_scaled": [vp, vp, i64, vp, i32, vp, vp, vp, vp, vp, i32, i32, i64, i64, f32, vp, vp, vp, sz, vp],
+        "verify_attn_mla_scaled_workspace_size": [i32, i32, i64, i64, ctypes.POINTER(sz)],
+        "verify_attn_mla_step_tables": [vp, vp, i32, i32, vp, i64, i64, vp, i64, vp, vp, vp, i64, i64, vp, vp, vp, vp, vp,
+                                        vp, vp],
+        "verify_attn_mla_beam_select": [vp, i32, i64, i64, i32, i32, i32, vp, vp, i32, vp, vp, vp, vp, sz, vp],
+        "verify_attn_mla_beam_select_workspace_size": [i64, i32, i32, ctypes.POINTER(sz)],
+        "verify_attn_mla_beam_reorder": [vp, i64, vp, i64, i64, i64, i32, i32, vp, vp, vp, vp, vp],
         "verify_attn_mla_runs": run,
         "verify_attn_mla_runs_workspace_size": [i32, i32, vp, vp, i32, ctypes.POINTER(sz)],
         "verify_attn_mla_test_fault": [i32, i64],
@@ -379,10 +394,10 @@ def _step(t, dim: int, least: int) -> int:
 
 
 def _cache_append_args(latent, k_rope, positions, slots, cos_sin, kv_pool, q_rope=None, q=None, kv_scale=0.0,
-                       interleaved=True, status_word=None, stream=None):
+                       interleaved=True, status_word=None, stream=None, pool_args=None):
     T = int(latent.shape[0])
     R = D_QK - D_V
-    fp8 = float(kv_scale) != 0.0
+    fp8 = float(kv_scale) != 0.0 or pool_args is not None
     if (q_rope is None) != (q is None):
         raise ValueError("q_rope and q are given together")
     H = int(q.shape[1]) if q is not None else 0
@@ -402,8 +417,8 @@ def _cache_append_args(latent, k_rope, positions, slots, cos_sin, kv_pool, q_rop
     args = (lat, _step(latent, 0, D_V), rope, _step(k_rope, 0, R), qr, _step(q_rope, 0, R) if H else 0,
             _step(q_rope, 1, R) if H else 0, _d(positions, 4, "positions"), _d(slots, 4, "slots"),
             _d(cos_sin, 4, "cos_sin"), int(cos_sin.shape[0]), int(bool(interleaved)), T, H,
-            _d(kv_pool, 1 if fp8 else 2, "kv_pool"), int(kv_pool.shape[0]), float(kv_scale), _d(q, 2, "q"),
-            _d(status_word, 4, "status_word"), _stream(stream))
+            _d(kv_pool, 1 if fp8 else 2, "kv_pool"), int(kv_pool.shape[0]),
+            *(pool_args or (float(kv_scale),)), _d(q, 2, "q"), _d(status_word, 4, "status_word"), _stream(stream))
     return args, (latent, k_rope, positions, slots, cos_sin, kv_pool, q_rope, q, status_word)
 
 
@@ -419,6 +434,207 @@ def prepare_verify_attn_mla_append(*a, **k) -> Prepared:
     """verify_attn_mla_append with its arguments checked and marshalled once."""
     args, keep = _cache_append_args(*a, **k)
     return Prepared(_lib.verify_attn_mla_append, "verify_attn_mla_append", args, keep)
+
+
+def _append_scaled_args(latent, k_rope, positions, slots, cos_sin, kv_pool, kv_scales, block_tokens=1, q_rope=None,
+                        q=None, interleaved=True, status_word=None, stream=None):
+    _scales(kv_pool, kv_scales, block_tokens)
+    args, keep = _cache_append_args(latent, k_rope, positions, slots, cos_sin, kv_pool, q_rope, q, 0.0, interleaved,
+                                    status_word, stream, (_d(kv_scales, 4, "kv_scales"), int(block_tokens)))
+    return args, (*keep, kv_scales)
+
+
+def _scales(kv_pool, kv_scales, block_tokens):
+    """A pool of e4m3 codes and its scales, one per block of slots."""
+    _shape(kv_pool, "kv_pool", (None, D_QK))
+    if int(block_tokens) < 1 or int(kv_pool.shape[0]) % int(block_tokens):
+        raise ValueError(f"block_tokens: {block_tokens} does not divide the pool's {int(kv_pool.shape[0])} slots")
+    _shape(kv_scales, "kv_scales", (int(kv_pool.shape[0]) // int(block_tokens),))
+    if not str(kv_scales.dtype).endswith("float32"):
+        raise ValueError(f"kv_scales: float32 expected, got {kv_scales.dtype}")
+    _same_device(kv_scales=kv_scales)
+
+
+def verify_attn_mla_append_scaled(*a, **k):
+    """Writes new tokens' rows as e4m3 codes into a pool with one fp32 scale (a power of two) per block of
+    block_tokens slots, setting or raising the blocks' scales; rotation, queries and padding as in
+    verify_attn_mla_append.  Tokens of one block stand together, slots ascending."""
+    args, _ = _append_scaled_args(*a, **k)
+    _check(_lib.verify_attn_mla_append_scaled(*args), "verify_attn_mla_append_scaled")
+
+
+def prepare_verify_attn_mla_append_scaled(*a, **k) -> Prepared:
+    """verify_attn_mla_append_scaled with its arguments checked and marshalled once."""
+    args, keep = _append_scaled_args(*a, **k)
+    return Prepared(_lib.verify_attn_mla_append_scaled, "verify_attn_mla_append_scaled", args, keep)
+
+
+def verify_attn_mla_scaled_workspace_size(batch: int, num_heads: int, max_total_q: int, max_total_kv: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.verify_attn_mla_scaled_workspace_size(int(batch), int(num_heads), int(max_total_q), int(max_total_kv),
+                                                      ctypes.byref(n)), "verify_attn_mla_scaled_workspace_size")
+    return int(n.value)
+
+
+def _scaled_args(q, kv_pool, kv_scales, kv_indptr, kv_indices, qo_indptr, out, lse, workspace, sm_scale,
+                 block_tokens=1, draft_mask=None, parent=None, stream=None):
+    if len(q.shape) != 3:
+        raise ValueError(f"q: three dimensions expected, got {tuple(q.shape)}")
+    T, H, N, B = int(q.shape[0]), int(q.shape[1]), int(kv_indices.shape[0]), int(kv_indptr.shape[0]) - 1
+    _scales(kv_pool, kv_scales, block_tokens)
+    for t, name, shape in ((q, "q", (T, H, D_QK)), (out, "out", (T, H, D_V)), (lse, "lse", (T, H)),
+                           (kv_indices, "kv_indices", (N,)), (kv_indptr, "kv_indptr", (None,)),
+                           (qo_indptr, "qo_indptr", (B + 1,))):
+        _shape(t, name, shape)
+    if B < 0:
+        raise ValueError("kv_indptr: batch + 1 entries expected")
+    for t, name in ((draft_mask, "draft_mask"), (parent, "parent")):
+        if t is not None:
+            _shape(t, name, (T,))
+    _same_device(q=q, kv_pool=kv_pool, kv_indptr=kv_indptr, kv_indices=kv_indices, qo_indptr=qo_indptr, out=out, lse=lse,
+                 workspace=workspace, draft_mask=draft_mask, parent=parent)
+    args = (_d(q, 2, "q"), _d(kv_pool, 1, "kv_pool"), int(kv_pool.shape[0]), _d(kv_scales, 4, "kv_scales"),
+            int(block_tokens), _d(kv_indptr, 4, "kv_indptr"), _d(kv_indices, 4, "kv_indices"),
+            _d(qo_indptr, 4, "qo_indptr"), _d(draft_mask, 8, "draft_mask"), _d(parent, 4, "parent"), B, H, T, N,
+            float(sm_scale), _d(out, 2, "out"), _d(lse, 4, "lse"), _d(workspace, 0, "workspace"),
+            workspace.numel() * workspace.element_size(), _stream(stream))
+    return args, (q, kv_pool, kv_scales, kv_indptr, kv_indices, qo_indptr, out, lse, workspace, draft_mask, parent)
+
+
+def verify_attn_mla_scaled(*a, **k):
+    """Attention over a pool of e4m3 codes with one scale per block of block_tokens slots: single tokens, drafts or
+    trees.  The lengths are read on the device; q [T, heads, 576], out, lse and kv_indices may have room for more
+    rows than qo_indptr and kv_indptr use."""
+    args, _ = _scaled_args(*a, **k)
+    _check(_lib.verify_attn_mla_scaled(*args), "verify_attn_mla_scaled")
+
+
+def prepare_verify_attn_mla_scaled(*a, **k) -> Prepared:
+    """verify_attn_mla_scaled with its arguments checked and marshalled once."""
+    args, keep = _scaled_args(*a, **k)
+    return Prepared(_lib.verify_attn_mla_scaled, "verify_attn_mla_scaled", args, keep)
+
+
+def _tables_args(cached, added, block_table, free_blocks, free_count, free_left, scratch, kv_indptr, qo_indptr,
+                 kv_indices, positions, slots, block_tokens=1, status_word=None, stream=None):
+    B, N, T = int(cached.shape[0]), int(kv_indices.shape[0]), int(slots.shape[0])
+    for t, name, shape in ((cached, "cached", (None,)), (added, "added", (B,)), (block_table, "block_table", (B, None)),
+                           (free_blocks, "free_blocks", (None,)), (free_count, "free_count", (1,)),
+                           (free_left, "free_left", (1,)), (scratch, "scratch", (1,)), (kv_indptr, "kv_indptr", (B + 1,)),
+                           (qo_indptr, "qo_indptr", (B + 1,)), (kv_indices, "kv_indices", (None,)),
+                           (positions, "positions", (T,)), (slots, "slots", (None,))):
+        _shape(t, name, shape)
+    if status_word is not None and status_word.numel() < 2:
+        raise ValueError("status_word: two words expected")
+    _same_device(cached=cached, added=added, block_table=block_table, free_blocks=free_blocks, free_count=free_count,
+                 free_left=free_left, scratch=scratch, kv_indptr=kv_indptr, qo_indptr=qo_indptr, kv_indices=kv_indices,
+                 positions=positions, slots=slots, status_word=status_word)
+    width = int(block_table.shape[1])
+    args = (_d(cached, 4, "cached"), _d(added, 4, "added"), B, int(block_tokens),
+            _rows(block_table, 4, "block_table", (B, width)), _step(block_table, 0, width), width,
+            _d(free_blocks, 4, "free_blocks"), int(free_blocks.shape[0]), _d(free_count, 4, "free_count"),
+            _d(free_left, 4, "free_left"), _d(scratch, 4, "scratch"), T, N, _d(kv_indptr, 4, "kv_indptr"),
+            _d(qo_indptr, 4, "qo_indptr"), _d(kv_indices, 4, "kv_indices"), _d(positions, 4, "positions"),
+            _d(slots, 4, "slots"), _d(status_word, 4, "status_word"), _stream(stream))
+    return args, (cached, added, block_table, free_blocks, free_count, free_left, scratch, kv_indptr, qo_indptr,
+                  kv_indices, positions, slots, status_word)
+
+
+def verify_attn_mla_step_tables(*a, **k):
+    """kv_indptr, qo_indptr, kv_indices, positions and slots of a step from the requests' cached and added lengths
+    (int32 device arrays), growing block_table [batch, width] by blocks from the free list's end."""
+    args, _ = _tables_args(*a, **k)
+    _check(_lib.verify_attn_mla_step_tables(*args), "verify_attn_mla_step_tables")
+
+
+def prepare_verify_attn_mla_step_tables(*a, **k) -> Prepared:
+    """verify_attn_mla_step_tables with its arguments checked and marshalled once."""
+    args, keep = _tables_args(*a, **k)
+    return Prepared(_lib.verify_attn_mla_step_tables, "verify_attn_mla_step_tables", args, keep)
+
+
+def verify_attn_mla_beam_select_workspace_size(rows: int, vocab: int, keep: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.verify_attn_mla_beam_select_workspace_size(int(rows), int(vocab), int(keep), ctypes.byref(n)),
+           "verify_attn_mla_beam_select_workspace_size")
+    return int(n.value)
+
+
+def _beam_select_args(logits, score, parent, token, new_score, workspace, beams, finished=None, pad_token=0, stream=None):
+    if len(logits.shape) != 2:
+        raise ValueError(f"logits: two dimensions expected, got {tuple(logits.shape)}")
+    rows, V = (int(n) for n in logits.shape)
+    size = 0 if isinstance(logits, np.ndarray) else logits.element_size()
+    if size not in (2, 4) or not str(logits.dtype).endswith(("bfloat16", "float32")):
+        raise ValueError(f"logits: device memory of bfloat16 or float32 expected, got {logits.dtype}")
+    if int(beams) < 1 or rows % int(beams):
+        raise ValueError(f"beams: {beams} does not divide the {rows} rows of logits")
+    R = rows // int(beams)
+    _shape(parent, "parent", (R, None))
+    K = int(parent.shape[1])
+    for t, name, shape in ((score, "score", (rows,)), (token, "token", (R, K)), (new_score, "new_score", (R, K)),
+                           (finished, "finished", (rows,))):
+        if t is not None:
+            _shape(t, name, shape)
+    _same_device(logits=logits, score=score, finished=finished, parent=parent, token=token, new_score=new_score,
+                 workspace=workspace)
+    args = (_rows(logits, size, "logits", (rows, V)), int(size == 4), _step(logits, 0, V), R, int(beams), K, V,
+            _d(score, 4, "score"), _d(finished, 4, "finished"), int(pad_token), _d(parent, 4, "parent"),
+            _d(token, 4, "token"), _d(new_score, 4, "new_score"), _d(workspace, 0, "workspace"),
+            workspace.numel() * workspace.element_size(), _stream(stream))
+    return args, (logits, score, finished, parent, token, new_score, workspace)
+
+
+def verify_attn_mla_beam_select(*a, **k):
+    """The best parent.shape[1] continuations per request over `beams` beams and the vocabulary: logits [requests x
+    beams, vocab] bf16 or fp32 (rows may be strided) and scores in, parent, token and new_score [requests, keep] out."""
+    args, _ = _beam_select_args(*a, **k)
+    _check(_lib.verify_attn_mla_beam_select(*args), "verify_attn_mla_beam_select")
+
+
+def prepare_verify_attn_mla_beam_select(*a, **k) -> Prepared:
+    """verify_attn_mla_beam_select with its arguments checked and marshalled once."""
+    args, keep = _beam_select_args(*a, **k)
+    return Prepared(_lib.verify_attn_mla_beam_select, "verify_attn_mla_beam_select", args, keep)
+
+
+def _beam_reorder_args(src, dst, parent, beams, length=None, new_length=None, status_word=None, stream=None):
+    if len(src.shape) != 2 or len(parent.shape) != 2:
+        raise ValueError("src, parent: two dimensions expected")
+    R, K = (int(n) for n in parent.shape)
+    _shape(src, "src", (R * int(beams), None))
+    _shape(dst, "dst", (R * K, int(src.shape[1])))
+    for t, name, shape in ((length, "length", (R * int(beams),)), (new_length, "new_length", (R * K,))):
+        if t is not None:
+            _shape(t, name, shape)
+    if status_word is not None and status_word.numel() < 2:
+        raise ValueError("status_word: two words expected")
+    _same_device(src=src, dst=dst, parent=parent, length=length, new_length=new_length, status_word=status_word)
+    size = src.element_size() if getattr(src, "is_cuda", False) else 0
+    if size not in (2, 4, 8) or dst.element_size() != size:
+        raise ValueError("src, dst: device memory of the same type, of 2, 4 or 8 bytes, expected")
+    words = int(src.shape[1]) * size
+    steps = [_step(src, 0, int(src.shape[1])) * size, _step(dst, 0, int(dst.shape[1])) * size]
+    if words % 4 or any(s % 4 for s in steps):
+        raise ValueError("src, dst: rows and strides of whole 32-bit words expected")
+    if length is not None and size != 4:
+        raise ValueError("length: counts 32-bit words, so rows of 4-byte elements are expected with it")
+    args = (_rows(src, size, "src", tuple(src.shape)), steps[0] // 4, _rows(dst, size, "dst", tuple(dst.shape)),
+            steps[1] // 4, words // 4, R, int(beams), K, _d(parent, 4, "parent"), _d(length, 4, "length"),
+            _d(new_length, 4, "new_length"), _d(status_word, 4, "status_word"), _stream(stream))
+    return args, (src, dst, parent, length, new_length, status_word)
+
+
+def verify_attn_mla_beam_reorder(*a, **k):
+    """Row r keep + k of dst gets row r beams + parent[r, k] of src (rows of 32-bit words, `length` of each)."""
+    args, _ = _beam_reorder_args(*a, **k)
+    _check(_lib.verify_attn_mla_beam_reorder(*args), "verify_attn_mla_beam_reorder")
+
+
+def prepare_verify_attn_mla_beam_reorder(*a, **k) -> Prepared:
+    """verify_attn_mla_beam_reorder with its arguments checked and marshalled once."""
+    args, keep = _beam_reorder_args(*a, **k)
+    return Prepared(_lib.verify_attn_mla_beam_reorder, "verify_attn_mla_beam_reorder", args, keep)
 
 
 def verify_attn_mla_shared_workspace_size(shared_rows: int, qo_indptr_host, kv_indptr_host, num_heads: int,

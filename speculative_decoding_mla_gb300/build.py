@@ -21,7 +21,7 @@ LIB = os.path.join(HERE, "libvmla.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["vmla_capi.cu", "vmla_plan.cpp", "vmla_simt.cu", "vmla_merge.cu", "vmla_gather.cu", "vmla_tc.cu", "vmla_static.cu",
            "vmla_dplan.cu", "vmla_accept.cu", "vmla_defrag.cu", "vmla_append.cu",
-           "vmla_sample.cu"]
+           "vmla_sample.cu", "vmla_append_scaled.cu", "vmla_scaled.cu", "vmla_tables.cu", "vmla_beam.cu"]
 
 
 def nvcc() -> str:

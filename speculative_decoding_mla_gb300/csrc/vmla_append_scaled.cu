@@ -1,0 +1,267 @@
+// Append of new tokens' rows to a pool of 8-bit codes with one scale per block of slots.
+//
+// A row is [latent (512) | rotated part (64)] as in the append with one scale.  The rows that a call brings to one
+// block (a run: tokens that stand together, slots ascending) get the block's scale
+//   need  = the smallest power of two 2^k, k >= -100, with every |value| of the run <= 448 x 2^k
+//   scale = need where the run begins the block, else max(the block's scale, need)
+//   code  = e4m3(value / scale), nearest even,
+// and where that raises the scale the block's rows in front of the run are coded again, e4m3(code x old / new).
+// A power of two makes value / scale exact, so a code is off by its own rounding only (half of 2^-3), and lets the
+// cache's readers scale in any order; against amax / 448 it gives away less than one bit at the bottom of the range.
+//
+// A token costs 1152 bytes in, 256 of table, 576 out and 256 per head.  With blocks of one slot a warp takes a token
+// and has its row in registers while the largest value is found.  Otherwise a CTA takes a run: its warps take the
+// rows in turn, agree on the scale in shared memory, and code them, reading them a second time (from L1 or L2: a
+// run is at most 128 rows, 147 KB).  A CTA looks for runs that begin in a window of tokens: one token where there
+// are few (each run then has its own CTA; the others leave at once), else as many as a block has slots.
+#include <cuda_runtime.h>
+
+#include "vmla_device.cuh"
+#include "vmla_rope.cuh"
+
+namespace vmla {
+using namespace rope;
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxBlock = VMLA_MAX_BLOCK_TOKENS;
+constexpr int kHeadPasses = 2;  // 16 heads per warp
+static_assert(kMaxBlock <= kThreads, "one thread per token of a window");
+
+// Granules 2 lane, 2 lane + 1 of the latent and, in lanes 0 to 3, the turned granules lane and lane + 4 of the rest.
+struct Row {
+  float x0[8], x1[8], lo[8], hi[8];
+};
+
+__device__ __forceinline__ void load_row(const AppendArgs& a, int64_t t, int32_t pos, int lane, Row& r) {
+  const uint4* lat = reinterpret_cast<const uint4*>(a.latent + t * a.latent_stride);
+  const uint4* rope = reinterpret_cast<const uint4*>(a.k_rope + t * a.k_rope_stride);
+  const uint4 v0 = __ldg(lat + 2 * lane), v1 = __ldg(lat + 2 * lane + 1);
+  if (lane < 4) {
+    const uint4 r0 = __ldg(rope + lane), r1 = __ldg(rope + lane + 4);
+    const bool neighbours = a.neighbours != 0;
+    rotate(r0, r1, load_angles(a.cos_sin + (int64_t)pos * kRopeDim, lane, neighbours), neighbours, r.lo, r.hi);
+  }
+  unpack8(v0, r.x0);
+  unpack8(v1, r.x1);
+}
+
+// The row's largest magnitude (NaN left out), in every lane.
+__device__ __forceinline__ float largest(const Row& r, int lane) {
+  float m = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) m = fmaxf(m, fmaxf(fabsf(r.x0[k]), fabsf(r.x1[k])));
+  if (lane < 4)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = fmaxf(m, fmaxf(fabsf(r.lo[k]), fabsf(r.hi[k])));
+  return warp_max(m);
+}
+
+// The smallest 2^k with amax <= 448 x 2^k = 1.75 x 2^(k + 8), -100 <= k <= 120 (beyond every finite float's need).
+__device__ __forceinline__ float scale_for(float amax) {
+  const uint32_t bits = __float_as_uint(amax);
+  int k = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  k = k < -100 ? -100 : k > 120 ? 120 : k;
+  return __uint_as_float((uint32_t)(k + 127) << 23);
+}
+
+// Eight values -> codes: by a product where the scale is a power of two (then exact), else by a division.
+__device__ __forceinline__ uint2 codes_of(const float (&x)[8], float scale) {
+  if ((__float_as_uint(scale) & 0x7FFFFFu) != 0 || scale < 0x1p-120f) return codes8(x, scale);
+  const float inv = __uint_as_float((254u << 23) - __float_as_uint(scale));
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(x[2 * k + 1] * inv), "f"(x[2 * k] * inv));
+    w[k] = c;
+  }
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+__device__ __forceinline__ void store_row(const AppendArgs& a, int32_t slot, int lane, const Row& r, float scale) {
+  uint8_t* dst = reinterpret_cast<uint8_t*>(a.pool) + (int64_t)slot * kDqk;
+  const uint2 c0 = codes_of(r.x0, scale), c1 = codes_of(r.x1, scale);
+  reinterpret_cast<uint4*>(dst)[lane] = make_uint4(c0.x, c0.y, c1.x, c1.y);
+  if (lane < 4) {
+    *reinterpret_cast<uint2*>(dst + kDv + 8 * lane) = codes_of(r.lo, scale);
+    *reinterpret_cast<uint2*>(dst + kDv + 8 * (lane + 4)) = codes_of(r.hi, scale);
+  }
+}
+
+// Four codes, each times `ratio` (below 1) and coded again.
+__device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
+  uint32_t out = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t pair;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(pair) : "h"((uint16_t)(w >> (16 * h))));
+    float lo, hi;
+    asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(pair));
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(hi * ratio), "f"(lo * ratio));
+    out |= (uint32_t)c << (16 * h);
+  }
+  return out;
+}
+
+__device__ __forceinline__ bool slot_ok(const AppendArgs& a, int32_t slot) {
+  return slot >= 0 && (int64_t)slot < a.pool_slots;
+}
+
+struct RunShared {
+  int32_t start[kThreads];
+  int32_t starts;
+  int32_t warp_len[kWarps];
+  int32_t first[kWarps];
+  float amax[kWarps];
+};
+
+// All runs whose first token lies in [w0, w0 + window), by the whole CTA.
+__device__ void append_runs(const AppendArgs& a, int64_t w0, int window, RunShared& s) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int shift = a.block_shift, mask = a.block - 1;
+  if (tid == 0) s.starts = 0;
+  __syncthreads();
+  if (tid < window && w0 + tid < a.tokens) {
+    const int64_t t = w0 + tid;
+    const int32_t slot = __ldg(a.slots + t);
+    if (slot_ok(a, slot)) {
+      const int32_t prev = t > 0 ? __ldg(a.slots + t - 1) : -1;
+      if (!slot_ok(a, prev) || (prev >> shift) != (slot >> shift)) s.start[atomicAdd(&s.starts, 1)] = tid;
+      const int32_t pos = __ldg(a.positions + t);
+      if (!(pos >= 0 && (int64_t)pos < a.table_rows)) record_status(a.status, VMLA_ERR_INDEX, (uint32_t)t);
+    } else if (slot != -1) {
+      record_status(a.status, VMLA_ERR_INDEX, (uint32_t)t);
+    }
+  }
+  __syncthreads();
+  const int starts = s.starts;
+  for (int i = 0; i < starts; ++i) {
+    const int64_t t0 = w0 + s.start[i];
+    const int32_t block = __ldg(a.slots + t0) >> shift;
+    // its length: up to the first token of another block (a block's slots at most), and its first used row
+    {
+      bool in = tid < a.block && t0 + tid < a.tokens;
+      int32_t slot = -1, pos = -1;
+      if (in) {
+        slot = __ldg(a.slots + t0 + tid);
+        pos = __ldg(a.positions + t0 + tid);
+        in = slot_ok(a, slot) && (slot >> shift) == block;
+      }
+      const unsigned inside = __ballot_sync(0xffffffffu, in);
+      const int len = inside == 0xffffffffu ? 32 : __ffs(~inside) - 1;  // tokens up to the first that is not in
+      const unsigned used = __ballot_sync(0xffffffffu, lane < len && pos >= 0 && (int64_t)pos < a.table_rows);
+      const int32_t at = __shfl_sync(0xffffffffu, slot & mask, used ? __ffs(used) - 1 : 0);
+      if (lane == 0) {
+        s.warp_len[warp] = len;
+        s.first[warp] = used ? at : -1;
+      }
+    }
+    __syncthreads();
+    int n = 0, first = -1;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      if (n == 32 * w) {
+        n += s.warp_len[w];
+        if (first < 0) first = s.first[w];
+      }
+    const float old = first < 0 ? 0.f : a.kv_scales[block];
+    float m = 0.f;
+    for (int k = warp; k < n; k += kWarps) {
+      const int32_t pos = __ldg(a.positions + t0 + k);
+      if (pos >= 0 && (int64_t)pos < a.table_rows) {
+        Row r;
+        load_row(a, t0 + k, pos, lane, r);
+        m = fmaxf(m, largest(r, lane));
+      }
+    }
+    if (lane == 0) s.amax[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s.amax[w]);
+    const float need = scale_for(m), scale = first == 0 ? need : fmaxf(old, need);
+    if (first > 0 && scale > old) {
+      const float ratio = old / scale;
+      for (int row = warp; row < first; row += kWarps) {
+        uint4* codes = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.pool) +
+                                                (((int64_t)block << shift) + row) * kDqk);
+        for (int g = lane; g < kDqk / 16; g += 32) {
+          uint4 v = codes[g];
+          v.x = recode4(v.x, ratio);
+          v.y = recode4(v.y, ratio);
+          v.z = recode4(v.z, ratio);
+          v.w = recode4(v.w, ratio);
+          codes[g] = v;
+        }
+      }
+    }
+    if (tid == 0 && first >= 0) a.kv_scales[block] = scale;
+    for (int k = warp; k < n; k += kWarps) {
+      const int32_t pos = __ldg(a.positions + t0 + k);
+      if (pos >= 0 && (int64_t)pos < a.table_rows) {
+        Row r;
+        load_row(a, t0 + k, pos, lane, r);
+        store_row(a, __ldg(a.slots + t0 + k), lane, r, scale);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <bool kRuns>
+__global__ void __launch_bounds__(kThreads)
+append_scaled_kernel(const AppendArgs a, int64_t row_ctas, int window, int parts) {
+  __shared__ RunShared s;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if ((int64_t)blockIdx.x < row_ctas) {
+    if (kRuns) {
+      append_runs(a, (int64_t)blockIdx.x * window, window, s);
+      return;
+    }
+    const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
+    if (t >= a.tokens) return;
+    const int32_t slot = __ldg(a.slots + t), pos = __ldg(a.positions + t);
+    if (!slot_ok(a, slot) || !(pos >= 0 && (int64_t)pos < a.table_rows)) {
+      if (lane == 0 && slot != -1) record_status(a.status, VMLA_ERR_INDEX, (uint32_t)t);
+      return;
+    }
+    Row r;
+    load_row(a, t, pos, lane, r);
+    const float scale = scale_for(largest(r, lane));
+    store_row(a, slot, lane, r, scale);
+    if (lane == 0) a.kv_scales[slot] = scale;
+    return;
+  }
+  const int64_t unit = ((int64_t)blockIdx.x - row_ctas) * kWarps + warp;
+  const int64_t t = unit / parts;
+  if (t >= a.tokens) return;
+  const int32_t slot = __ldg(a.slots + t), pos = __ldg(a.positions + t);
+  const bool use = slot_ok(a, slot) && pos >= 0 && (int64_t)pos < a.table_rows;
+  turn_heads<kHeadPasses>(a, t, (int)(unit - t * parts), lane, use, a.cos_sin + (int64_t)(use ? pos : 0) * kRopeDim);
+}
+
+}  // namespace
+
+int launch_append_scaled(const AppendArgs& a, void* stream) {
+  if (a.tokens == 0) return VMLA_OK;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) !=
+                                                cudaSuccess)
+    return VMLA_ERR_CUDA;
+  const int heads = kHeadPasses * kHeadsPerPass;
+  const int parts = (a.num_heads + heads - 1) / heads;
+  const bool runs = a.block > 1;
+  const int window = a.tokens > 8 * (int64_t)sms ? a.block : 1;
+  const int64_t row_ctas = runs ? (a.tokens + window - 1) / window : (a.tokens + kWarps - 1) / kWarps;
+  const int64_t ctas = row_ctas + (a.tokens * parts + kWarps - 1) / kWarps;
+  if (ctas > INT32_MAX) return VMLA_ERR_SHAPE;
+  const auto kernel = runs ? append_scaled_kernel<true> : append_scaled_kernel<false>;
+  kernel<<<(unsigned)ctas, kThreads, 0, (cudaStream_t)stream>>>(a, row_ctas, window, parts);
+  return cudaGetLastError() == cudaSuccess ? VMLA_OK : VMLA_ERR_CUDA;
+}
+
+}  // namespace vmla

@@ -1,0 +1,590 @@
+// Beam search: the best continuations over a request's beams and the vocabulary, and the reordering of the beams'
+// states.
+//
+// Beam w of a request (score c_w, logits x) continues with token v at the score
+//   c_w + x_v - lse_w,   lse_w = ln sum_v exp(x_v),
+// and the K best over all (w, v) are kept, in descending order, equal ones by the index w vocab + v.
+//
+// Within a beam the order is the logits' own, so a row's first K tokens by (logit, index) are all that can be kept.
+// The first kernel reads each row once: a thread sums 2^(x log2 e - r) against a reference r of its own (raised when
+// a granule's maximum passes it by 2^30) and remembers its largest granule, (maximum, place).  The K-th largest of
+// the threads' granules bounds the row's K-th token from below, and no token above the bound lies outside the K
+// threads that have these granules: only their granules are read again (from L2), the tokens above the bound listed,
+// and the list ranked.  Rows are cut into parts, one CTA each, while that is needed to fill the GPU.
+// The second kernel, a CTA per request, joins the parts' sums and merges the sorted lists: K rounds of one warp.
+//
+// Scores of different beams are compared through lse_w, and the single-precision terms put it off by up to about
+// 4e-6 (margin_of).  Where two neighbours of the merged order, of different beams, lie closer than that, the request's
+// CTA sums the beams concerned again in whole units (weight_units, exact in any order: equal rows have equal sums
+// wherever they lie) and merges anew.  Scores closer than about 2^-27 are not told apart for certain.
+//
+// The logits bound it: 2 or 4 bytes a token in, and about four instructions.
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "vmla_device.cuh"
+#include "vmla_weights.cuh"
+
+namespace vmla {
+using namespace weights;
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxBeams = VMLA_MAX_BEAMS, kMaxKeep = VMLA_MAX_BEAM_KEEP;
+constexpr int kMaxParts = 16;
+constexpr int kList = 2048;      // tokens above the bound that are ranked at once
+constexpr int kFlush = 8;        // granules whose sum stays in single precision
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr double kLn2 = 0.69314718055994530942;
+static_assert(kMaxKeep <= 32, "one warp merges");
+
+// One part of a row: the sum of 2^(x log2 e - ref), tokens at +inf, and the first n tokens as sorted keys.
+struct alignas(16) RowPart {
+  double sum;
+  float ref;
+  uint32_t infinite;
+  uint32_t n;
+  uint32_t pad[3];
+  uint64_t key[kMaxKeep];
+};
+
+// Order of the logits as whole numbers (-0 like 0); -inf and NaN below every other, as 0.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  if (!(x > -INFINITY)) return 0;
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float ordered_value(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+// Larger keys first: by logit, then by the lower index.
+__device__ __forceinline__ uint64_t key_of(uint32_t order, uint32_t index) { return (uint64_t)order << 32 | (uint32_t)~index; }
+
+template <typename T>
+struct Row {
+  static constexpr int kVec = 16 / (int)sizeof(T);
+  const T* first;    // aligned to 16 bytes, at or before the row's first element
+  int lead;          // elements in front of the row
+  int vocab;
+  __device__ __forceinline__ Row(const void* logits, int64_t stride, int64_t row, int v) {
+    const T* p = static_cast<const T*>(logits) + row * stride;
+    lead = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+    first = p - lead;
+    vocab = v;
+  }
+  __device__ __forceinline__ int granules() const { return (vocab + lead + kVec - 1) / kVec; }
+  // whether granule g lies in the row as a whole
+  __device__ __forceinline__ bool whole(int g) const { return g * kVec >= lead && (g + 1) * kVec <= vocab + lead; }
+  __device__ __forceinline__ static float value(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+  __device__ __forceinline__ static float value(float v) { return v; }
+  // granule g's logits, -inf outside the row
+  __device__ __forceinline__ void get(int g, float (&x)[kVec]) const {
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+      const int i = g * kVec + k - lead;
+      x[k] = i >= 0 && i < vocab ? value(__ldg(first + g * kVec + k)) : -INFINITY;
+    }
+  }
+  __device__ __forceinline__ static void unpack(const uint4& v, float (&x)[kVec]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x[2 * k] = bf16_lo(w[k]);
+        x[2 * k + 1] = bf16_hi(w[k]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = __uint_as_float(w[k]);
+    }
+  }
+};
+
+// A thread's sum and largest granule.
+struct Acc {
+  float ref = -INFINITY, sum = 0.f, best = -INFINITY;
+  double total = 0.0;
+  int place = -1;
+  uint32_t infinite = 0;
+
+  template <int N>
+  __device__ __forceinline__ void add(float (&x)[N], int g) {
+    float m = x[0];
+#pragma unroll
+    for (int k = 1; k < N; ++k) m = fmaxf(m, x[k]);
+    if (m > best) {
+      best = m;
+      place = g;
+    }
+    if (!(m > -INFINITY)) return;
+    const float top = m * kLog2e;
+    if (top > ref + 30.f) {
+      if (m == INFINITY) {  // those tokens share the row evenly
+#pragma unroll
+        for (int k = 0; k < N; ++k) infinite += x[k] == INFINITY;
+        return;
+      }
+      const float f = ex2_approx(ref - top);
+      total *= (double)f;
+      sum *= f;
+      ref = top;
+    }
+    float e[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) e[k] = ex2_approx(fmaf(x[k], kLog2e, -ref));
+#pragma unroll
+    for (int s = N / 2; s > 0; s >>= 1)
+#pragma unroll
+      for (int k = 0; k < s; ++k) e[k] += e[k + s];
+    if (e[0] != e[0]) {  // NaN counts as -inf
+      float y = 0.f;
+#pragma unroll
+      for (int k = 0; k < N; ++k) y += x[k] > -INFINITY ? ex2_approx(fmaf(x[k], kLog2e, -ref)) : 0.f;
+      e[0] = y;
+    }
+    sum += e[0];
+  }
+  __device__ __forceinline__ void flush() {
+    total += (double)sum;
+    sum = 0.f;
+  }
+};
+
+struct RowShared {
+  uint64_t key[kThreads];
+  uint64_t list[kList];
+  uint64_t warp_key[kWarps];
+  int32_t thread[kMaxKeep];
+  float warp_f[kWarps];
+  double warp_d[kWarps];
+  uint32_t warp_u[kWarps];
+  uint64_t bound;
+  uint32_t chosen, listed;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+beam_rows_kernel(const BeamArgs a, RowPart* __restrict__ out, int parts) {
+  constexpr int kVec = Row<T>::kVec;
+  __shared__ RowShared s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dependents_launch();
+  const int64_t row_at = blockIdx.x / (unsigned)parts;
+  const int part = (int)(blockIdx.x % (unsigned)parts);
+  RowPart& r = out[blockIdx.x];
+  const float score = a.score[row_at];
+  if (!(score > -INFINITY) || (a.finished && a.finished[row_at])) {  // nothing of its logits counts
+    if (tid == 0) {
+      r.n = 0;
+      r.sum = 0.0;
+      r.ref = -INFINITY;
+      r.infinite = 0;
+    }
+    return;
+  }
+  const Row<T> row(a.logits, a.stride, row_at, a.vocab);
+  const int all = row.granules(), per = (all + parts - 1) / parts;
+  const int g0 = part * per, g1 = min(all, g0 + per);
+  Acc acc;
+  constexpr int kAhead = 4;
+  int since = 0;
+  for (int g = g0 + tid; g < g1; g += kAhead * kThreads) {
+    uint4 v[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int h = g + k * kThreads;
+      if (h < g1 && row.whole(h)) v[k] = __ldg(reinterpret_cast<const uint4*>(row.first) + h);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int h = g + k * kThreads;
+      if (h < g1) {
+        float x[kVec];
+        if (row.whole(h)) Row<T>::unpack(v[k], x);
+        else row.get(h, x);
+        acc.add(x, h);
+      }
+    }
+    if ((since += kAhead) >= kFlush) {
+      acc.flush();
+      since = 0;
+    }
+  }
+  acc.flush();
+  // the part's sum against its largest reference
+  float ref = warp_max(acc.ref);
+  if (lane == 0) s.warp_f[warp] = ref;
+  const uint64_t mine = acc.place >= 0 ? key_of(ordered(acc.best), (uint32_t)acc.place) : 0;
+  s.key[tid] = mine;
+  if (tid == 0) s.chosen = s.listed = 0;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) ref = fmaxf(ref, s.warp_f[w]);
+  double total = acc.ref > -INFINITY ? acc.total * (double)ex2_approx(acc.ref - ref) : 0.0;
+  uint32_t infinite = acc.infinite;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    infinite += __shfl_xor_sync(0xffffffffu, infinite, o);
+  }
+  if (lane == 0) {
+    s.warp_d[warp] = total;
+    s.warp_u[warp] = infinite;
+  }
+  // the K threads with the largest granules, and the K-th of these
+  const int keep = a.keep;
+  if (mine != 0) {
+    int above = 0;
+    for (int k = 0; k < kThreads; ++k) above += s.key[k] > mine;
+    if (above < keep) {
+      s.thread[above] = tid;
+      atomicMax(&s.chosen, (uint32_t)above + 1);
+      if (above == keep - 1) s.bound = mine;
+    }
+  }
+  __syncthreads();
+  const int chosen = (int)s.chosen;
+  const uint64_t bound = chosen == keep ? s.bound : 1;
+  const uint32_t least = (uint32_t)(bound >> 32), last_place = ~(uint32_t)bound;
+  // their tokens at or above the bound (of the bound's own value, those up to its granule)
+  const int rounds = (g1 - g0 + kThreads - 1) / kThreads;
+  for (int i = tid; i < chosen * rounds; i += kThreads) {
+    const int g = g0 + s.thread[i / rounds] + (i % rounds) * kThreads;
+    if (g >= g1) continue;
+    float x[kVec];
+    row.get(g, x);
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+      const uint32_t o = ordered(x[k]);
+      if (o != 0 && (o > least || (o == least && (uint32_t)g <= last_place))) {
+        const uint32_t at = atomicAdd(&s.listed, 1u);
+        if (at < kList) s.list[at] = key_of(o, (uint32_t)(g * kVec + k - row.lead));
+      }
+    }
+  }
+  __syncthreads();
+  const int listed = (int)s.listed;
+  if (listed <= kList) {
+    for (int i = tid; i < listed; i += kThreads) {
+      const uint64_t k = s.list[i];
+      int above = 0;
+      for (int j = 0; j < listed; ++j) above += s.list[j] > k;
+      if (above < keep) r.key[above] = k;
+    }
+  } else {
+    // more than the list holds (many large tokens in few threads' granules): the next largest, K times
+    uint64_t last = ~0ull;
+    for (int n = 0; n < keep; ++n) {
+      uint64_t best = 0;
+      for (int g = g0 + tid; g < g1; g += kThreads) {
+        float x[kVec];
+        row.get(g, x);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+          const uint32_t o = ordered(x[k]);
+          const uint64_t key = o ? key_of(o, (uint32_t)(g * kVec + k - row.lead)) : 0;
+          if (key < last && key > best) best = key;
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const uint64_t u = __shfl_xor_sync(0xffffffffu, best, o);
+        best = u > best ? u : best;
+      }
+      __syncthreads();
+      if (lane == 0) s.warp_key[warp] = best;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) best = s.warp_key[w] > best ? s.warp_key[w] : best;
+      if (tid == 0) r.key[n] = best;
+      last = best;
+    }
+  }
+  if (tid == 0) {
+    double sum = 0.0;
+    uint32_t inf = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      sum += s.warp_d[w];
+      inf += s.warp_u[w];
+    }
+    r.sum = sum;
+    r.ref = ref;
+    r.infinite = inf;
+    r.n = (uint32_t)min(listed, keep);
+  }
+}
+
+struct JoinShared {
+  double base[kMaxBeams];      // c_w - lse_w; beams with tokens at +inf: c_w - ln of their count
+  float ref[kMaxBeams];
+  bool infinite[kMaxBeams];
+  float2 table[64];
+  unsigned long long sum[kMaxBeams];
+  uint32_t unsure;             // beams whose neighbours in the order lie too close
+};
+
+// By how much a beam's lse may be off: the terms' errors (ex2.approx 2.4e-7, its argument 2e-7, a tree of eight and
+// a running sum of eight 6.6e-7, two more factors 5e-7) and log2 e as a float, 1.4e-8 of the logits' size.
+__device__ __forceinline__ double margin_of(float ref) { return 2e-6 + 1.5e-8 * (fabs((double)ref) + 30.0); }
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+beam_join_kernel(const BeamArgs a, const RowPart* __restrict__ in, int parts, const __grid_constant__ ExpTable exp_table) {
+  extern __shared__ uint64_t keys[];  // [beams x parts][keep]
+  __shared__ JoinShared s;
+  __shared__ int32_t count[kMaxBeams * kMaxParts];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int W = a.beams, K = a.keep, V = a.vocab, lists = W * parts;
+  const int64_t request = blockIdx.x;
+  if (tid < 64) s.table[tid] = exp_table.t[tid];
+  if (tid == 0) s.unsure = 0;
+  grid_dependency_wait();
+  const RowPart* rows = in + request * lists;
+  for (int l = tid; l < lists; l += kThreads) count[l] = (int)rows[l].n;
+  __syncthreads();
+  for (int i = tid; i < lists * K; i += kThreads) {
+    const int l = i / K, k = i - l * K;
+    keys[i] = k < count[l] ? rows[l].key[k] : 0;
+  }
+  if (tid < W) {
+    const float c = a.score[request * W + tid];
+    const bool done = a.finished && a.finished[request * W + tid];
+    s.sum[tid] = 0;
+    s.infinite[tid] = false;
+    s.ref[tid] = 0.f;
+    s.base[tid] = (double)c;
+    if (c > -INFINITY && !done) {
+      float ref = -INFINITY;
+      uint32_t infinite = 0;
+      for (int p = 0; p < parts; ++p) {
+        ref = fmaxf(ref, rows[tid * parts + p].ref);
+        infinite += rows[tid * parts + p].infinite;
+      }
+      double sum = 0.0;
+      for (int p = 0; p < parts; ++p) {
+        const RowPart& r = rows[tid * parts + p];
+        if (r.ref > -INFINITY) sum += r.sum * (double)ex2_approx(r.ref - ref);
+      }
+      s.ref[tid] = ref > -INFINITY ? ref : 0.f;
+      s.infinite[tid] = infinite > 0;
+      s.base[tid] = infinite ? (double)c - log((double)infinite) : (double)c - (double)s.ref[tid] * kLn2 - log(sum);
+    }
+  }
+  __syncthreads();
+  if (tid < W && a.finished && a.finished[request * W + tid] && a.score[request * W + tid] > -INFINITY) {
+    // a finished beam goes on by the padding token alone, its score as it is
+    keys[tid * parts * K] = key_of(ordered(0.f), (uint32_t)a.pad_token);
+    count[tid * parts] = 1;
+  }
+  __syncthreads();
+  // the merge, by one warp: a lane has every 32nd list
+  for (int pass = 0; pass < 2; ++pass) {
+    if (warp == 0) {
+      int at[kMaxBeams * kMaxParts / 32];
+      // a list's next token: its score (-inf: none) and index
+      auto head = [&](int l, int k, double& value, int& index) {
+        value = -INFINITY;
+        index = INT32_MAX;
+        if (k < count[l]) {
+          const uint64_t key = keys[l * K + k];
+          const int w = l / parts;
+          const float x = ordered_value((uint32_t)(key >> 32));
+          if (!s.infinite[w] || x == INFINITY) {
+            value = s.base[w] + (s.infinite[w] ? 0.0 : (double)x);
+            index = w * V + (int)~(uint32_t)key;
+          }
+        }
+      };
+      double best = -INFINITY;
+      int index = INT32_MAX, list = 0;
+      auto choose = [&]() {
+        best = -INFINITY;
+        index = INT32_MAX;
+#pragma unroll
+        for (int i = 0; i < kMaxBeams * kMaxParts / 32; ++i) {
+          const int l = lane + 32 * i;
+          if (l < lists) {
+            double v;
+            int x;
+            head(l, at[i], v, x);
+            if (v > best || (v == best && x < index)) {
+              best = v;
+              index = x;
+              list = i;
+            }
+          }
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < kMaxBeams * kMaxParts / 32; ++i) at[i] = 0;
+      choose();
+      uint32_t unsure = 0;
+      double last = INFINITY;
+      int last_beam = -1;
+      for (int k = 0; k <= K; ++k) {  // (the one after the last only for its distance)
+        double v = best;
+        int x = index;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const double v2 = __shfl_xor_sync(0xffffffffu, v, o);
+          const int x2 = __shfl_xor_sync(0xffffffffu, x, o);
+          if (v2 > v || (v2 == v && x2 < x)) {
+            v = v2;
+            x = x2;
+          }
+        }
+        const bool none = !(v > -INFINITY);
+        const int w = none ? -1 : x / V;
+        if (!none && k > 0 && w != last_beam && last - v < margin_of(s.ref[w]) + margin_of(s.ref[last_beam]))
+          unsure |= 1u << w | 1u << last_beam;
+        if (k == K) break;
+        if (lane == 0) {
+          const int64_t o = request * K + k;
+          a.parent[o] = w;
+          a.token[o] = none ? -1 : x - w * V;
+          a.new_score[o] = none ? -INFINITY : (float)v;
+        }
+        if (!none && index == x) {
+#pragma unroll
+          for (int i = 0; i < kMaxBeams * kMaxParts / 32; ++i) at[i] += i == list;
+          choose();
+        }
+        if (none) {
+          // nothing is left: the remaining places hold no token
+          if (lane == 0)
+            for (int j = k + 1; j < K; ++j) {
+              a.parent[request * K + j] = -1;
+              a.token[request * K + j] = -1;
+              a.new_score[request * K + j] = -INFINITY;
+            }
+          break;
+        }
+        last = v;
+        last_beam = w;
+      }
+      if (lane == 0) s.unsure = pass == 0 ? unsure : 0;
+    }
+    __syncthreads();
+    uint32_t unsure = s.unsure;
+    if (unsure == 0) break;
+    // the sums of the beams concerned again, exactly
+    for (; unsure != 0; unsure &= unsure - 1) {
+      const int w = __ffs(unsure) - 1;
+      if (s.infinite[w] || (a.finished && a.finished[request * W + w])) continue;  // exact already
+      uint32_t top = 0;
+      for (int p = 0; p < parts; ++p)
+        if (count[w * parts + p] > 0) top = max(top, (uint32_t)(keys[(w * parts + p) * K] >> 32));
+      const Exponent e = {ordered_value(top), 1.44269502162933349609f, 1.92596299112661746887e-8f};
+      const Row<T> row(a.logits, a.stride, request * W + w, V);
+      const int all = row.granules();
+      unsigned long long sum = 0;
+      for (int g = tid; g < all; g += kThreads) {
+        float x[Row<T>::kVec];
+        row.get(g, x);
+#pragma unroll
+        for (int k = 0; k < Row<T>::kVec; ++k) sum += x[k] > -INFINITY ? weight_units(x[k], e, s.table) : 0;
+      }
+      atomicAdd(&s.sum[w], sum);
+      __syncthreads();
+      if (tid == 0)
+        s.base[w] = (double)a.score[request * W + w] - (double)e.max - (log((double)s.sum[w]) - kUnitBits * kLn2);
+    }
+    __syncthreads();
+  }
+}
+
+// Rows of 32-bit words, `length` of each (or all), from the parents' to the children's places.
+__global__ void __launch_bounds__(kThreads)
+beam_reorder_kernel(const ReorderArgs a, int64_t rows) {
+  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+    const int64_t request = r / a.keep;
+    const int p = a.parent[r];
+    const bool real = p >= 0 && p < a.beams;
+    const int64_t source = request * a.beams + (real ? p : 0);
+    int64_t n = a.row_words;
+    if (a.length) {
+      const int32_t len = real ? a.length[source] : 0;
+      if (blockIdx.x == 0 && threadIdx.x == 0) {
+        if (len < 0 || (int64_t)len > a.row_words) record_status(a.status, VMLA_ERR_INDEX, (uint32_t)r);
+        if (a.new_length) a.new_length[r] = len;
+      }
+      n = len < 0 ? 0 : (int64_t)len < n ? (int64_t)len : n;
+    }
+    if (!real) {
+      if (blockIdx.x == 0 && threadIdx.x == 0 && p != -1) record_status(a.status, VMLA_ERR_INDEX, (uint32_t)r);
+      continue;
+    }
+    const uint32_t* src = a.src + source * a.src_stride;
+    uint32_t* dst = a.dst + r * a.dst_stride;
+    const int64_t me = (int64_t)blockIdx.x * kThreads + threadIdx.x, step = (int64_t)gridDim.x * kThreads;
+    int64_t from = 0;
+    if (((reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst)) & 15) == 0) {
+      const int64_t whole = n / 4;
+      for (int64_t i = me; i < whole; i += step)
+        reinterpret_cast<uint4*>(dst)[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+      from = whole * 4;
+    }
+    for (int64_t i = from + me; i < n; i += step) dst[i] = __ldg(src + i);
+  }
+}
+
+// CTAs per row of logits: enough to fill the GPU twice over, each with at least 4096 tokens.
+int parts_of(int64_t rows, int vocab, int sms) {
+  int parts = 1;
+  while (parts < kMaxParts && rows * parts < sms && vocab / (parts * 2) >= 4096) parts *= 2;
+  return parts;
+}
+
+template <typename T>
+int launch_select(const BeamArgs& a, int64_t requests, int parts, void* workspace, cudaStream_t stream) {
+  RowPart* part = static_cast<RowPart*>(workspace);
+  const int64_t rows = requests * a.beams;
+  beam_rows_kernel<T><<<(unsigned)(rows * parts), kThreads, 0, stream>>>(a, part, parts);
+  if (cudaGetLastError() != cudaSuccess) return VMLA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1] = {early_start_attribute()};
+  cfg.gridDim = dim3((unsigned)requests, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)a.beams * parts * a.keep * 8;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cfg.dynamicSmemBytes > 32768 &&
+      cudaFuncSetAttribute(beam_join_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kMaxBeams * kMaxParts * kMaxKeep * 8) != cudaSuccess)
+    return VMLA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, beam_join_kernel<T>, a, (const RowPart*)part, parts, exp_table()) == cudaSuccess
+             ? VMLA_OK
+             : VMLA_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t beam_workspace(int64_t rows, int vocab, int sms) {
+  return (size_t)rows * parts_of(rows, vocab, sms) * sizeof(RowPart);
+}
+
+int launch_beam_select(const BeamArgs& a, int64_t requests, bool fp32, int sms, void* workspace, void* stream) {
+  if (requests == 0) return VMLA_OK;
+  const int64_t rows = requests * a.beams;
+  const int parts = parts_of(rows, a.vocab, sms);
+  if (rows * parts > INT32_MAX) return VMLA_ERR_SHAPE;
+  return fp32 ? launch_select<float>(a, requests, parts, workspace, (cudaStream_t)stream)
+              : launch_select<uint16_t>(a, requests, parts, workspace, (cudaStream_t)stream);
+}
+
+int launch_beam_reorder(const ReorderArgs& a, int64_t requests, int sms, void* stream) {
+  const int64_t rows = requests * a.keep;
+  if (rows == 0) return VMLA_OK;
+  const int64_t wide = (a.row_words + 4 * kThreads - 1) / (4 * kThreads);
+  const unsigned y = (unsigned)(rows < 65535 ? rows : 65535);
+  const int64_t most = (8 * (int64_t)sms + y - 1) / y;
+  const unsigned x = (unsigned)(wide < 1 ? 1 : wide < most ? wide : most);
+  beam_reorder_kernel<<<dim3(x, y, 1), kThreads, 0, (cudaStream_t)stream>>>(a, rows);
+  return cudaGetLastError() == cudaSuccess ? VMLA_OK : VMLA_ERR_CUDA;
+}
+
+}  // namespace vmla

@@ -853,16 +853,19 @@ int verify_attn_mla_sample(const void* logits, int logits_fp32, int64_t row_stri
   return launch_sample(a, logits_fp32 != 0, stream);
 }
 
-int verify_attn_mla_append(const void* latent, int64_t latent_stride, const void* k_rope, int64_t k_rope_stride,
-                           const void* q_rope, int64_t q_rope_stride_t, int64_t q_rope_stride_h,
-                           const int32_t* positions, const int32_t* slots, const float* cos_sin, int64_t table_rows,
-                           int neighbour_pairs, int64_t tokens, int num_heads, void* kv_pool, int64_t pool_slots,
-                           float kv_scale, void* q, uint32_t* status_word, void* stream) {
-  if (tokens < 0 || tokens > INT32_MAX || num_heads < 0 || num_heads > VMLA_MAX_HEADS || pool_slots < 0 ||
-      pool_slots > INT32_MAX || table_rows < 0 || table_rows > INT32_MAX)
-    return VMLA_ERR_SHAPE;
-  if (kv_scale != 0.f && (!(kv_scale > 0.f) || !(kv_scale < INFINITY))) return VMLA_ERR_SHAPE;
-  if (tokens == 0) return VMLA_OK;
+namespace {
+// log2 of a block size the pools take (a power of two up to VMLA_MAX_BLOCK_TOKENS), or -1.
+int block_shift(int block_tokens) {
+  for (int s = 0; (1 << s) <= VMLA_MAX_BLOCK_TOKENS; ++s)
+    if (block_tokens == 1 << s) return s;
+  return -1;
+}
+
+// Argument checks that both appends share; what is not of the pool goes into `a`.
+int append_args(const void* latent, int64_t latent_stride, const void* k_rope, int64_t k_rope_stride,
+                const void* q_rope, int64_t q_rope_stride_t, int64_t q_rope_stride_h, const int32_t* positions,
+                const int32_t* slots, const float* cos_sin, int64_t table_rows, int neighbour_pairs, int64_t tokens,
+                int num_heads, void* kv_pool, int64_t pool_slots, void* q, uint32_t* status_word, AppendArgs* a) {
   if (!latent || !k_rope || !positions || !slots || !cos_sin || !kv_pool) return VMLA_ERR_NULL;
   if (num_heads > 0 && (!q_rope || !q)) return VMLA_ERR_NULL;
   if (latent_stride < kDv || k_rope_stride < kDqk - kDv) return VMLA_ERR_SHAPE;
@@ -882,27 +885,283 @@ int verify_attn_mla_append(const void* latent, int64_t latent_stride, const void
   int sms = 0;
   int rc = current_sm_count(&sms, true);
   if (rc != VMLA_OK) return rc;
+  a->latent = static_cast<const uint16_t*>(latent);
+  a->k_rope = static_cast<const uint16_t*>(k_rope);
+  a->q_rope = static_cast<const uint16_t*>(q_rope);
+  a->latent_stride = latent_stride;
+  a->k_rope_stride = k_rope_stride;
+  a->q_rope_stride_t = q_rope_stride_t;
+  a->q_rope_stride_h = q_rope_stride_h;
+  a->positions = positions;
+  a->slots = slots;
+  a->cos_sin = cos_sin;
+  a->table_rows = table_rows;
+  a->tokens = tokens;
+  a->num_heads = num_heads;
+  a->neighbours = neighbour_pairs != 0;
+  a->pool = kv_pool;
+  a->pool_slots = pool_slots;
+  a->kv_scale = 0.f;
+  a->kv_scales = nullptr;
+  a->block = 1;
+  a->block_shift = 0;
+  a->q = static_cast<uint16_t*>(q);
+  a->status = status_word;
+  return VMLA_OK;
+}
+
+int append_sizes(int64_t tokens, int num_heads, int64_t pool_slots, int64_t table_rows) {
+  if (tokens < 0 || tokens > INT32_MAX || num_heads < 0 || num_heads > VMLA_MAX_HEADS || pool_slots < 0 ||
+      pool_slots > INT32_MAX || table_rows < 0 || table_rows > INT32_MAX)
+    return VMLA_ERR_SHAPE;
+  return VMLA_OK;
+}
+}  // namespace
+
+int verify_attn_mla_append(const void* latent, int64_t latent_stride, const void* k_rope, int64_t k_rope_stride,
+                           const void* q_rope, int64_t q_rope_stride_t, int64_t q_rope_stride_h,
+                           const int32_t* positions, const int32_t* slots, const float* cos_sin, int64_t table_rows,
+                           int neighbour_pairs, int64_t tokens, int num_heads, void* kv_pool, int64_t pool_slots,
+                           float kv_scale, void* q, uint32_t* status_word, void* stream) {
+  int rc = append_sizes(tokens, num_heads, pool_slots, table_rows);
+  if (rc != VMLA_OK) return rc;
+  if (kv_scale != 0.f && (!(kv_scale > 0.f) || !(kv_scale < INFINITY))) return VMLA_ERR_SHAPE;
+  if (tokens == 0) return VMLA_OK;
   AppendArgs a;
-  a.latent = static_cast<const uint16_t*>(latent);
-  a.k_rope = static_cast<const uint16_t*>(k_rope);
-  a.q_rope = static_cast<const uint16_t*>(q_rope);
-  a.latent_stride = latent_stride;
-  a.k_rope_stride = k_rope_stride;
-  a.q_rope_stride_t = q_rope_stride_t;
-  a.q_rope_stride_h = q_rope_stride_h;
+  rc = append_args(latent, latent_stride, k_rope, k_rope_stride, q_rope, q_rope_stride_t, q_rope_stride_h, positions,
+                   slots, cos_sin, table_rows, neighbour_pairs, tokens, num_heads, kv_pool, pool_slots, q, status_word,
+                   &a);
+  if (rc != VMLA_OK) return rc;
+  a.kv_scale = kv_scale;
+  return launch_append(a, stream);
+}
+
+int verify_attn_mla_append_scaled(const void* latent, int64_t latent_stride, const void* k_rope, int64_t k_rope_stride,
+                                  const void* q_rope, int64_t q_rope_stride_t, int64_t q_rope_stride_h,
+                                  const int32_t* positions, const int32_t* slots, const float* cos_sin,
+                                  int64_t table_rows, int neighbour_pairs, int64_t tokens, int num_heads,
+                                  void* kv_pool_e4m3, int64_t pool_slots, float* kv_scales, int block_tokens, void* q,
+                                  uint32_t* status_word, void* stream) {
+  int rc = append_sizes(tokens, num_heads, pool_slots, table_rows);
+  if (rc != VMLA_OK) return rc;
+  const int shift = block_shift(block_tokens);
+  if (shift < 0 || pool_slots % block_tokens != 0) return VMLA_ERR_SHAPE;
+  if (tokens == 0) return VMLA_OK;
+  if (!kv_scales) return VMLA_ERR_NULL;
+  if (!aligned(kv_scales, 4)) return VMLA_ERR_ALIGN;
+  AppendArgs a;
+  rc = append_args(latent, latent_stride, k_rope, k_rope_stride, q_rope, q_rope_stride_t, q_rope_stride_h, positions,
+                   slots, cos_sin, table_rows, neighbour_pairs, tokens, num_heads, kv_pool_e4m3, pool_slots, q,
+                   status_word, &a);
+  if (rc != VMLA_OK) return rc;
+  a.kv_scales = kv_scales;
+  a.block = block_tokens;
+  a.block_shift = shift;
+  return launch_append_scaled(a, stream);
+}
+
+namespace {
+int check_scaled(int batch, int num_heads, int64_t max_total_q, int64_t max_total_kv) {
+  if (batch < 0 || batch > VMLA_MAX_BATCH || num_heads < 1 || num_heads > VMLA_MAX_HEADS) return VMLA_ERR_SHAPE;
+  if (max_total_q < 0 || max_total_kv < 0 || max_total_kv > INT32_MAX) return VMLA_ERR_SHAPE;
+  // more rows than the batch can have are never used
+  if (max_total_q > (int64_t)batch * VMLA_MAX_DRAFT) return VMLA_ERR_SHAPE;
+  return VMLA_OK;
+}
+}  // namespace
+
+int verify_attn_mla_scaled_workspace_size(int batch, int num_heads, int64_t max_total_q, int64_t max_total_kv,
+                                          size_t* bytes) {
+  if (!bytes) return VMLA_ERR_NULL;
+  int rc = check_scaled(batch, num_heads, max_total_q, max_total_kv);
+  if (rc != VMLA_OK) return rc;
+  int sms = 0;
+  rc = current_sm_count(&sms, false);
+  if (rc != VMLA_OK) return rc;
+  *bytes = scaled_workspace(sms);
+  return VMLA_OK;
+}
+
+int verify_attn_mla_scaled(const void* q, const void* kv_pool_e4m3, int64_t pool_slots, const float* kv_scales,
+                           int block_tokens, const int32_t* kv_indptr, const int32_t* kv_indices,
+                           const int32_t* qo_indptr, const uint64_t* draft_mask, const int32_t* parent, int batch,
+                           int num_heads, int64_t max_total_q, int64_t max_total_kv, float sm_scale, void* out,
+                           float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_scaled(batch, num_heads, max_total_q, max_total_kv);
+  if (rc != VMLA_OK) return rc;
+  const int shift = block_shift(block_tokens);
+  if (shift < 0 || pool_slots < 0 || pool_slots > INT32_MAX || pool_slots % block_tokens != 0) return VMLA_ERR_SHAPE;
+  if (!(sm_scale > 0.f) || !(sm_scale < INFINITY)) return VMLA_ERR_SHAPE;
+  if (!workspace) return VMLA_ERR_NULL;
+  if (batch > 0 && (!kv_indptr || !qo_indptr)) return VMLA_ERR_NULL;
+  if (max_total_q > 0 && (!q || !out || !lse)) return VMLA_ERR_NULL;
+  if (max_total_q > 0 && max_total_kv > 0 && (!kv_pool_e4m3 || !kv_scales || !kv_indices)) return VMLA_ERR_NULL;
+  if (max_total_kv > 0 && pool_slots == 0) return VMLA_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(kv_pool_e4m3, 16) || !aligned(kv_scales, 4) || !aligned(out, 16) || !aligned(lse, 4) ||
+      !aligned(workspace, VMLA_WORKSPACE_ALIGN) || !aligned(draft_mask, 8) || !aligned(parent, 4) ||
+      !aligned(kv_indptr, 4) || !aligned(kv_indices, 4) || !aligned(qo_indptr, 4))
+    return VMLA_ERR_ALIGN;
+  int sms = 0;
+  rc = current_sm_count(&sms, true);
+  if (rc != VMLA_OK) return rc;
+  if (workspace_bytes < scaled_workspace(sms)) return VMLA_ERR_WORKSPACE;
+  ScaledArgs a;
+  a.workspace = static_cast<char*>(workspace);
+  a.status = static_cast<uint32_t*>(workspace);
+  if (cudaMemsetAsync(workspace, 0, 32, (cudaStream_t)stream) != cudaSuccess) return VMLA_ERR_CUDA;
+  if (batch == 0 || max_total_q == 0) return VMLA_OK;
+  a.q = static_cast<const uint16_t*>(q);
+  a.pool = static_cast<const uint8_t*>(kv_pool_e4m3);
+  a.pool_slots = pool_slots;
+  a.kv_scales = kv_scales;
+  a.block_shift = shift;
+  a.batch = batch;
+  a.num_heads = num_heads;
+  a.kv_indptr = kv_indptr;
+  a.kv_indices = kv_indices;
+  a.qo_indptr = qo_indptr;
+  a.masks = draft_mask;
+  a.parent = draft_mask ? nullptr : parent;
+  a.max_q = max_total_q;
+  a.max_kv = max_total_kv;
+  a.sm_scale = sm_scale;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  test_fault_settings(&a.test_fault, &a.wait_cycles);
+  return launch_scaled(a, stream);
+}
+
+int verify_attn_mla_step_tables(const int32_t* cached, const int32_t* added, int batch, int block_tokens,
+                                int32_t* block_table, int64_t table_stride, int64_t table_width,
+                                const int32_t* free_blocks, int64_t free_size, const int32_t* free_count,
+                                int32_t* free_left, uint32_t* scratch, int64_t max_total_q, int64_t max_total_kv,
+                                int32_t* kv_indptr, int32_t* qo_indptr, int32_t* kv_indices, int32_t* positions,
+                                int32_t* slots, uint32_t* status_word, void* stream) {
+  const int shift = block_shift(block_tokens);
+  if (batch < 0 || batch > VMLA_MAX_BATCH || shift < 0) return VMLA_ERR_SHAPE;
+  if (table_width < 0 || table_width > INT32_MAX || table_stride < table_width || table_stride > ((int64_t)1 << 31) ||
+      free_size < 0 || free_size > INT32_MAX || max_total_q < 0 || max_total_q > INT32_MAX || max_total_kv < 0 ||
+      max_total_kv > INT32_MAX)
+    return VMLA_ERR_SHAPE;
+  if (!free_count || !free_left || !scratch || !kv_indptr || !qo_indptr) return VMLA_ERR_NULL;
+  if (batch > 0 && (!cached || !added || (table_width > 0 && !block_table))) return VMLA_ERR_NULL;
+  if ((free_size > 0 && !free_blocks) || (max_total_kv > 0 && !kv_indices) || (max_total_q > 0 && (!positions || !slots)))
+    return VMLA_ERR_NULL;
+  const void* words[] = {cached,    added,     block_table, free_blocks, free_count, free_left, scratch,
+                         kv_indptr, qo_indptr, kv_indices,  positions,   slots,      status_word};
+  for (const void* p : words)
+    if (!aligned(p, 4)) return VMLA_ERR_ALIGN;
+  int sms = 0;
+  const int rc = current_sm_count(&sms, true);
+  if (rc != VMLA_OK) return rc;
+  TablesArgs a;
+  a.cached = cached;
+  a.added = added;
+  a.batch = batch;
+  a.block = block_tokens;
+  a.block_shift = shift;
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.table_width = table_width;
+  a.free_blocks = free_blocks;
+  a.free_size = free_size;
+  a.free_count = free_count;
+  a.free_left = free_left;
+  a.scratch = scratch;
+  a.max_q = max_total_q;
+  a.max_kv = max_total_kv;
+  a.kv_indptr = kv_indptr;
+  a.qo_indptr = qo_indptr;
+  a.kv_indices = kv_indices;
   a.positions = positions;
   a.slots = slots;
-  a.cos_sin = cos_sin;
-  a.table_rows = table_rows;
-  a.tokens = tokens;
-  a.num_heads = num_heads;
-  a.neighbours = neighbour_pairs != 0;
-  a.pool = kv_pool;
-  a.pool_slots = pool_slots;
-  a.kv_scale = kv_scale;
-  a.q = static_cast<uint16_t*>(q);
   a.status = status_word;
-  return launch_append(a, stream);
+  return launch_tables(a, stream);
+}
+
+namespace {
+int check_beams(int64_t requests, int beams, int keep) {
+  if (requests < 0 || requests > 65535 || beams < 1 || beams > VMLA_MAX_BEAMS || keep < 1 || keep > VMLA_MAX_BEAM_KEEP)
+    return VMLA_ERR_SHAPE;
+  return VMLA_OK;
+}
+}  // namespace
+
+int verify_attn_mla_beam_select_workspace_size(int64_t rows, int vocab, int keep, size_t* bytes) {
+  if (!bytes) return VMLA_ERR_NULL;
+  int rc = check_beams(0, 1, keep);
+  if (rc != VMLA_OK) return rc;
+  if (rows < 0 || rows > 65535 * VMLA_MAX_BEAMS || vocab < 1 || vocab > VMLA_MAX_VOCAB) return VMLA_ERR_SHAPE;
+  int sms = 0;
+  rc = current_sm_count(&sms, false);
+  if (rc != VMLA_OK) return rc;
+  *bytes = beam_workspace(rows, vocab, sms);
+  return VMLA_OK;
+}
+
+int verify_attn_mla_beam_select(const void* logits, int logits_fp32, int64_t row_stride, int64_t requests, int beams,
+                                int keep, int vocab, const float* score, const int32_t* finished, int pad_token,
+                                int32_t* parent, int32_t* token, float* new_score, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  int rc = check_beams(requests, beams, keep);
+  if (rc != VMLA_OK) return rc;
+  if (vocab < 1 || vocab > VMLA_MAX_VOCAB || row_stride < vocab || row_stride > ((int64_t)1 << 31) || pad_token < 0 ||
+      pad_token >= vocab)
+    return VMLA_ERR_SHAPE;
+  if (requests == 0) return VMLA_OK;
+  if (!logits || !score || !parent || !token || !new_score || !workspace) return VMLA_ERR_NULL;
+  if (!aligned(logits, logits_fp32 ? 4 : 2) || !aligned(score, 4) || !aligned(finished, 4) || !aligned(parent, 4) ||
+      !aligned(token, 4) || !aligned(new_score, 4) || !aligned(workspace, VMLA_WORKSPACE_ALIGN))
+    return VMLA_ERR_ALIGN;
+  int sms = 0;
+  rc = current_sm_count(&sms, true);
+  if (rc != VMLA_OK) return rc;
+  if (workspace_bytes < beam_workspace(requests * beams, vocab, sms)) return VMLA_ERR_WORKSPACE;
+  BeamArgs a;
+  a.logits = logits;
+  a.stride = row_stride;
+  a.vocab = vocab;
+  a.beams = beams;
+  a.keep = keep;
+  a.pad_token = pad_token;
+  a.score = score;
+  a.finished = finished;
+  a.parent = parent;
+  a.token = token;
+  a.new_score = new_score;
+  return launch_beam_select(a, requests, logits_fp32 != 0, sms, workspace, stream);
+}
+
+int verify_attn_mla_beam_reorder(const void* src, int64_t src_stride_words, void* dst, int64_t dst_stride_words,
+                                 int64_t row_words, int64_t requests, int beams, int keep, const int32_t* parent,
+                                 const int32_t* length, int32_t* new_length, uint32_t* status_word, void* stream) {
+  int rc = check_beams(requests, beams, keep);
+  if (rc != VMLA_OK) return rc;
+  constexpr int64_t kMaxStride = (int64_t)1 << 31;
+  if (row_words < 0 || row_words > INT32_MAX || src_stride_words < row_words || src_stride_words > kMaxStride ||
+      dst_stride_words < row_words || dst_stride_words > kMaxStride)
+    return VMLA_ERR_SHAPE;
+  if (requests == 0) return VMLA_OK;
+  if (!parent || (row_words > 0 && (!src || !dst)) || (new_length && !length)) return VMLA_ERR_NULL;
+  if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(parent, 4) || !aligned(length, 4) || !aligned(new_length, 4) ||
+      !aligned(status_word, 4))
+    return VMLA_ERR_ALIGN;
+  int sms = 0;
+  rc = current_sm_count(&sms, true);
+  if (rc != VMLA_OK) return rc;
+  ReorderArgs a;
+  a.src = static_cast<const uint32_t*>(src);
+  a.dst = static_cast<uint32_t*>(dst);
+  a.src_stride = src_stride_words;
+  a.dst_stride = dst_stride_words;
+  a.row_words = row_words;
+  a.parent = parent;
+  a.beams = beams;
+  a.keep = keep;
+  a.length = length;
+  a.new_length = new_length;
+  a.status = status_word;
+  return launch_beam_reorder(a, requests, sms, stream);
 }
 
 int verify_attn_mla_test_fault(int fault, int64_t wait_cycles) {
@@ -967,6 +1226,7 @@ const char* verify_attn_mla_status_string(int status) {
     case VMLA_ERR_DEVICE: return "no usable sm_103 device";
     case VMLA_ERR_PARENT: return "a draft parent index was malformed";
     case VMLA_ERR_PARAM: return "a sampling setting was out of range";
+    case VMLA_ERR_FULL: return "no room for a step's keys, tokens or blocks";
     default: return "unknown status";
   }
 }

@@ -247,10 +247,88 @@ struct AppendArgs {
   void* pool;
   int64_t pool_slots;
   float kv_scale;           // 0: bf16 pool; > 0: e4m3 pool
+  float* kv_scales;         // with a scale per block: [pool_slots / block] (verify_attn_mla_append_scaled)
+  int32_t block, block_shift;
   uint16_t* q;
   uint32_t* status;
 };
 int launch_append(const AppendArgs& args, void* stream);
+int launch_append_scaled(const AppendArgs& args, void* stream);
+
+// Attention over an e4m3 pool with a scale per block of slots (verify_attn_mla_scaled); lengths are read
+// on the device.
+struct ScaledArgs {
+  const uint16_t* q;        // [max_q, num_heads, 576] bf16
+  const uint8_t* pool;      // [pool_slots, 576] e4m3
+  int64_t pool_slots;
+  const float* kv_scales;   // [pool_slots / block]
+  int32_t block_shift;
+  int32_t batch, num_heads;
+  const int32_t* kv_indptr;
+  const int32_t* kv_indices;
+  const int32_t* qo_indptr;
+  const uint64_t* masks;    // visibility words per query, or NULL
+  const int32_t* parent;    // the drafts' parents (without masks), or NULL for causal
+  int64_t max_q, max_kv;
+  float sm_scale;
+  uint16_t* out;
+  float* lse;
+  char* workspace;
+  uint32_t* status;
+  int32_t test_fault;
+  long long wait_cycles;
+};
+size_t scaled_workspace(int sms);
+int launch_scaled(const ScaledArgs& args, void* stream);
+
+// A step's tables from its requests' lengths (verify_attn_mla_step_tables).
+struct TablesArgs {
+  const int32_t* cached;
+  const int32_t* added;
+  int32_t batch;
+  int32_t block, block_shift;
+  int32_t* table;           // [batch, table_width], row stride table_stride
+  int64_t table_stride, table_width;
+  const int32_t* free_blocks;
+  int64_t free_size;
+  const int32_t* free_count;
+  int32_t* free_left;       // may be free_count
+  uint32_t* scratch;        // one word, zero between calls
+  int64_t max_q, max_kv;    // entries of positions and slots, of kv_indices
+  int32_t* kv_indptr;
+  int32_t* qo_indptr;
+  int32_t* kv_indices;
+  int32_t* positions;
+  int32_t* slots;
+  uint32_t* status;
+};
+int launch_tables(const TablesArgs& args, void* stream);
+
+// Beam search (verify_attn_mla_beam_select, verify_attn_mla_beam_reorder).
+struct BeamArgs {
+  const void* logits;       // [requests x beams, vocab] bf16 or fp32, row stride in elements
+  int64_t stride;
+  int32_t vocab, beams, keep;
+  int32_t pad_token;
+  const float* score;       // [requests x beams]
+  const int32_t* finished;  // [requests x beams] or NULL
+  int32_t* parent;          // [requests, keep]
+  int32_t* token;
+  float* new_score;
+};
+struct ReorderArgs {
+  const uint32_t* src;      // [requests x beams, row_words], row stride in words
+  uint32_t* dst;            // [requests x keep, row_words]
+  int64_t src_stride, dst_stride, row_words;
+  const int32_t* parent;    // [requests, keep]
+  int32_t beams, keep;
+  const int32_t* length;    // [requests x beams] words of each row, or NULL: all
+  int32_t* new_length;      // [requests x keep] or NULL
+  uint32_t* status;
+};
+size_t beam_workspace(int64_t rows, int vocab, int sms);
+int launch_beam_select(const BeamArgs& args, int64_t requests, bool fp32, int sms, void* workspace, void* stream);
+int launch_beam_reorder(const ReorderArgs& args, int64_t requests, int sms, void* stream);
 
 // Sampling (verify_attn_mla_sample).
 constexpr float kSampleMinTemp = 1.f / (1 << 20), kSampleMaxTemp = 1 << 20;
