@@ -1008,8 +1008,8 @@ int verify_attn_mla_scaled(const void* q, const void* kv_pool_e4m3, int64_t pool
   ScaledArgs a;
   a.workspace = static_cast<char*>(workspace);
   a.status = static_cast<uint32_t*>(workspace);
-  if (cudaMemsetAsync(workspace, 0, 32, (cudaStream_t)stream) != cudaSuccess) return VMLA_ERR_CUDA;
-  if (batch == 0 || max_total_q == 0) return VMLA_OK;
+  if (batch == 0 || max_total_q == 0)  // (otherwise the call's last launch writes the status words)
+    return cudaMemsetAsync(workspace, 0, 8, (cudaStream_t)stream) == cudaSuccess ? VMLA_OK : VMLA_ERR_CUDA;
   a.q = static_cast<const uint16_t*>(q);
   a.pool = static_cast<const uint8_t*>(kv_pool_e4m3);
   a.pool_slots = pool_slots;
@@ -1028,7 +1028,7 @@ int verify_attn_mla_scaled(const void* q, const void* kv_pool_e4m3, int64_t pool
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   test_fault_settings(&a.test_fault, &a.wait_cycles);
-  return launch_scaled(a, stream);
+  return launch_scaled(a, sms, stream);
 }
 
 int verify_attn_mla_step_tables(const int32_t* cached, const int32_t* added, int batch, int block_tokens,

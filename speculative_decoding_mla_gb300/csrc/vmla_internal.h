@@ -279,7 +279,7 @@ struct ScaledArgs {
   long long wait_cycles;
 };
 size_t scaled_workspace(int sms);
-int launch_scaled(const ScaledArgs& args, void* stream);
+int launch_scaled(const ScaledArgs& args, int sms, void* stream);
 
 // A step's tables from its requests' lengths (verify_attn_mla_step_tables).
 struct TablesArgs {
