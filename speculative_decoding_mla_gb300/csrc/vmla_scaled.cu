@@ -37,52 +37,66 @@ using namespace sm100;
 namespace {
 
 constexpr int kTile = 128;          // keys
-constexpr int kRows = 32;           // query rows of a unit
 constexpr int kChunks = kDv / 128;  // 4 column chunks of 128 bytes, and one of 64
 constexpr int kParts = 3;           // of a weight
-constexpr int kStages = 2;
-constexpr int kSoftWarps = 8;       // two per quarter of the tile's keys, 16 rows each
-constexpr int kSoftThreads = kSoftWarps * 32;
-constexpr int kHalf = kRows / 2;
+constexpr int kPerThread = 16;      // rows of a softmax thread
 constexpr int kLoadWarps = 3;
-constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kMmaWarp + 1;
-constexpr int kThreads = 32 * (kSoftWarps + 1 + kLoadWarps);
-constexpr uint32_t kOCols = kParts * kRows;      // 96 columns of tensor memory per 128 value columns
-constexpr uint32_t kSCol = kChunks * kOCols;     // 384
-constexpr uint32_t kStageBytes = kTile * kDqk;
+constexpr int kAhead = 3;           // tiles whose slots a load warp knows
+constexpr int kRopePiece = 3;       // place of the rotated columns among a tile's pieces
 constexpr int kFixed = 2;           // what a unit costs beside its tiles, in tiles
 constexpr float kNone = -3e38f;     // reference of a row that has seen no key
 constexpr float kUnit = 2048.f;     // weights are held times 2^11
 constexpr float kMost = 32768.f;    // largest weight held
 constexpr float kTiny = 0x1p-100f;  // smaller scales count as zero
-static_assert(kSCol + 2 * 2 * kRows == 512, "tensor memory");
+constexpr int kMaxRows = 64;
 
-struct Stage {
-  uint8_t latent[kChunks][kTile * 128];  // [key][128 bytes], 128-byte swizzle
-  uint8_t rope[kTile * 64];              // [key][64 bytes], 64-byte swizzle
+// A unit's size, 32 or 64 query rows, and what follows from it.
+template <int R>
+struct Shape {
+  static constexpr int kRows = R;
+  static constexpr int kSoftWarps = 4 * R / kPerThread;  // per quarter of the tile's keys, 16 rows each
+  static constexpr int kSoftThreads = kSoftWarps * 32;
+  static constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kMmaWarp + 1;
+  static constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
+  // with 32 rows the three parts of the weights stand side by side in one product (and in three sets of O's columns,
+  // added at the end); with 64 there is tensor memory for one set, and each part is a product of its own
+  static constexpr bool kWide = R == 32;
+  static constexpr uint32_t kOCols = kWide ? kParts * R : R;  // columns of tensor memory per 128 value columns
+  static constexpr uint32_t kSCol = kChunks * kOCols;
+  static constexpr int kPRow = kWide ? 128 : 64;              // bytes of a key in P: all parts, or one
+  static constexpr int kPBytes = kTile * kPRow * (kWide ? 1 : kParts);
+  static constexpr int kLatentSlots = R == 32 ? 9 : 7, kRopeSlots = R == 32 ? 2 : 1;
+  static_assert(kSCol + 2 * 2 * R == 512, "tensor memory");
 };
-static_assert(sizeof(Stage) == kStageBytes, "stage");
 
+template <int R>
 struct Shared {
-  Stage stage[kStages];
-  uint8_t q_latent[kChunks][2 * kRows * 128];  // [hi rows, lo rows][128 bytes], 128-byte swizzle
-  uint8_t q_rope[2 * kRows * 64];              // 64-byte swizzle
-  uint8_t p[2][kTile * 128];                   // [key][hi 32 | mid 32 | lo 32 | -], 128-byte swizzle
-  int64_t cost[VMLA_MAX_BATCH + 1];            // cost position of each sequence's first stream
-  int32_t kv[VMLA_MAX_BATCH + 1], qo[VMLA_MAX_BATCH + 1];
-  uint64_t mask[kRows];                        // the unit's rows: visible drafts
+  using S = Shape<R>;
+  uint8_t latent[S::kLatentSlots][kTile * 128];  // a tile's chunk: [key][128 bytes], 128-byte swizzle
+  uint8_t q_latent[kChunks][2 * R * 128];        // [hi rows, lo rows][128 bytes], 128-byte swizzle
+  uint8_t p[S::kPBytes];                         // wide: [key][hi 32 | mid 32 | lo 32 | -], 128-byte swizzle;
+                                                 // else [part][key][64], 64-byte swizzle
+  uint8_t rope[S::kRopeSlots][kTile * 64];       // [key][64 bytes], 64-byte swizzle
+  uint8_t q_rope[2 * R * 64];                    // 64-byte swizzle
+  float m[R], f[R];                              // reference of each row (log2), factor of its last change
+  float part[4][R];                              // per quarter of the keys: row maxima, or row sums
+  uint64_t mask[R];                              // the unit's rows: visible drafts
+  int64_t cost[VMLA_MAX_BATCH + 1];              // cost position of each sequence's first stream
   int32_t parent[VMLA_MAX_DRAFT];
-  float part[4][kRows];                        // per quarter of the keys: row maxima, or row sums
-  float q_max[kSoftWarps];
-  int64_t sums[4][kThreads / 32];
-  uint64_t kfull[kStages], kfree[kStages], sfull[2], sfree[2], pfull[2], pfree[2], qfull, ofree, done;
+  float q_max[S::kSoftWarps];
+  int64_t sums[4][S::kThreads / 32];
+  uint64_t lfull[S::kLatentSlots], lfree[S::kLatentSlots], rfull[S::kRopeSlots], rfree[S::kRopeSlots];
+  uint64_t sfull[2], sfree[2], pfull, pfree, qfull, ofree, done;
   uint32_t tmem;
   volatile int32_t abort_flag;
   int32_t stop;
-  uint32_t fault[2];                           // first fault of this CTA: code, info
+  uint32_t fault[2];                             // first fault of this CTA: code, info
+  int32_t cut_pieces, cut_rows;                  // the stream that starts in this CTA's lane and goes on in the next
+  int64_t cut_row;
 };
-constexpr size_t kSharedBytes = sizeof(Shared) + 1024;
-static_assert(kSharedBytes <= 232448, "shared memory");
+template <int R>
+constexpr size_t kSharedBytes = sizeof(Shared<R>) + 1024;
+static_assert(kSharedBytes<32> <= 232448 && kSharedBytes<64> <= 232448, "shared memory");
 
 // What a CTA tells the joining launch: the stream that starts in its lane and is cut by the lane's end, and its fault.
 struct alignas(32) CtaInfo {
@@ -95,11 +109,12 @@ struct alignas(32) CtaInfo {
 };
 
 struct Partials {
-  float* o;        // [2 x CTAs][kRows][512], weights times kUnit
-  float2* ml;      // [2 x CTAs][kRows]: reference (log2), sum
+  float* o;        // [2 x CTAs][R][512], weights times kUnit
+  float2* ml;      // [2 x CTAs][R]: reference (log2), sum
 };
 
-__device__ __forceinline__ void fault(Shared& sm, int code, uint32_t info) {
+template <typename Sm>
+__device__ __forceinline__ void fault(Sm& sm, int code, uint32_t info) {
   if (atomicCAS(&sm.fault[0], 0u, (uint32_t)code) == 0u) sm.fault[1] = info;
 }
 
@@ -111,46 +126,62 @@ struct Plan {
   int32_t lanes;
 };
 
-__device__ __forceinline__ int row_blocks(const Shared& sm, const ScaledArgs& a, int b) {
-  return ((sm.qo[b + 1] - sm.qo[b]) * a.num_heads + kRows - 1) / kRows;
+// A sequence's lengths.
+struct Seq {
+  int32_t q0, nq, kv0, nk;
+};
+__device__ __forceinline__ Seq seq_of(const ScaledArgs& a, int b) {
+  Seq s;
+  s.q0 = __ldg(a.qo_indptr + b);
+  s.nq = __ldg(a.qo_indptr + b + 1) - s.q0;
+  s.kv0 = __ldg(a.kv_indptr + b);
+  s.nk = __ldg(a.kv_indptr + b + 1) - s.kv0;
+  return s;
 }
-__device__ __forceinline__ int tiles_of(const Shared& sm, int b) { return (sm.kv[b + 1] - sm.kv[b] + kTile - 1) / kTile; }
+template <int R>
+__device__ __forceinline__ int row_blocks(const ScaledArgs& a, const Seq& s) { return (s.nq * a.num_heads + R - 1) / R; }
+__device__ __forceinline__ int tiles_of(const Seq& s) { return (s.nk + kTile - 1) / kTile; }
 
 // Reads the lengths and shares the work out (whole CTA); false where the lengths are out of order or past a bound.
-__device__ bool make_plan(Shared& sm, const ScaledArgs& a, Plan& plan) {
+template <int R>
+__device__ bool make_plan(Shared<R>& sm, const ScaledArgs& a, Plan& plan) {
+  constexpr int kThreads = Shape<R>::kThreads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int b = tid; b <= a.batch; b += kThreads) {
-    sm.kv[b] = a.kv_indptr[b];
-    sm.qo[b] = a.qo_indptr[b];
-  }
-  __syncthreads();
-  bool ok = sm.kv[0] == 0 && sm.qo[0] == 0 && sm.kv[a.batch] <= a.max_kv && sm.qo[a.batch] <= a.max_q;
+  bool ok = tid != 0 || (a.kv_indptr[0] == 0 && a.qo_indptr[0] == 0 && a.kv_indptr[a.batch] <= a.max_kv &&
+                         a.qo_indptr[a.batch] <= a.max_q);
   int64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll 1
   for (int b = tid; b < a.batch; b += kThreads) {
-    const int64_t nk = (int64_t)sm.kv[b + 1] - sm.kv[b], nq = (int64_t)sm.qo[b + 1] - sm.qo[b];
-    ok = ok && nq >= 0 && nq <= VMLA_MAX_DRAFT && nk >= nq;
-    if (ok) {
-      const int64_t n = row_blocks(sm, a, b), span = tiles_of(sm, b) + kFixed;
+    const int64_t k0 = __ldg(a.kv_indptr + b), k1 = __ldg(a.kv_indptr + b + 1), q0 = __ldg(a.qo_indptr + b),
+                  q1 = __ldg(a.qo_indptr + b + 1);
+    const bool good = q1 >= q0 && q1 - q0 <= VMLA_MAX_DRAFT && k1 - k0 >= q1 - q0;
+    int64_t blocks = 0, span = 0;
+    if (good) {
+      blocks = ((q1 - q0) * a.num_heads + R - 1) / R;
+      span = (k1 - k0 + kTile - 1) / kTile + kFixed;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sum[k] += ((n + (1 << k) - 1) >> k) * span;
+      for (int k = 0; k < 4; ++k) sum[k] += ((blocks + (1 << k) - 1) >> k) * span;
     }
+    ok = ok && good;
+    sm.cost[b] = blocks << 32 | span;  // (until the costs are summed up)
   }
-  if (!__syncthreads_and(ok)) return false;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
     if (lane == 0) sm.sums[k][warp] = sum[k];
   }
-  __syncthreads();
+  if (!__syncthreads_and(ok)) return false;
   // the largest G whose shares are within 1/32 of the smallest ones
   int64_t least = INT64_MAX, length[4], share[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    length[k] = 0;
-    for (int w = 0; w < kThreads / 32; ++w) length[k] += sm.sums[k][w];
+    length[k] = lane < kThreads / 32 ? sm.sums[k][lane] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) length[k] += __shfl_xor_sync(0xffffffffu, length[k], o);
     const int lanes = (int)gridDim.x >> k;
-    share[k] = lanes > 0 ? (length[k] + lanes - 1) / lanes : INT64_MAX / 2;
+    share[k] = lanes == 0 ? INT64_MAX / 2
+               : length[k] <= INT32_MAX - lanes ? (int32_t)(length[k] + lanes - 1) / lanes : (length[k] + lanes - 1) / lanes;
     least = share[k] < least ? share[k] : least;
   }
   int pick = 0;
@@ -161,29 +192,23 @@ __device__ bool make_plan(Shared& sm, const ScaledArgs& a, Plan& plan) {
   plan.lanes = (int)gridDim.x >> pick;
   plan.length = length[pick];
   plan.share = share[pick] > 0 ? share[pick] : 1;
-  if (warp == 0) {  // running sums of the sequences' costs
-    constexpr int kEach = VMLA_MAX_BATCH / 32;
-    int64_t each[kEach], all = 0;
+  if (warp == 0) {  // running sums of the sequences' costs, 32 at a time
+    int64_t before = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      const int b = b0 + lane;
+      const int64_t v = b < a.batch ? sm.cost[b] : 0;
+      const int64_t mine = (((v >> 32) + plan.group - 1) >> pick) * (v & 0xFFFFFFFF);
+      int64_t upto = mine;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int b = lane * kEach + i;
-      each[i] = b < a.batch ? ((row_blocks(sm, a, b) + plan.group - 1) >> pick) * (int64_t)(tiles_of(sm, b) + kFixed) : 0;
-      all += each[i];
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += u;
+      }
+      if (b < a.batch) sm.cost[b] = before + upto - mine;
+      before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    int64_t before = all;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += v;
-    }
-    before -= all;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int b = lane * kEach + i;
-      if (b <= a.batch) sm.cost[b] = before;
-      before += each[i];
-    }
-    if (lane == 31 && a.batch == VMLA_MAX_BATCH) sm.cost[a.batch] = before;
+    if (lane == 0) sm.cost[a.batch] = before;
   }
   __syncthreads();
   return true;
@@ -191,32 +216,31 @@ __device__ bool make_plan(Shared& sm, const ScaledArgs& a, Plan& plan) {
 
 // One row block of a sequence over some of its tiles.
 struct Unit {
-  int b, row_block, rows;   // rows of the block that are the sequence's
+  int row_block, rows;      // rows of the block that are the sequence's
   int tile0, tiles;         // its tiles
-  int64_t out_row;          // first row in q and out
+  int q0, nq;               // the sequence's drafts
   int kv0, keys, prefix;    // first entry of kv_indices; keys and prefix of the sequence
   bool whole, head;         // every tile of the stream; its first tile is among these
-  int pieces;
+  int64_t stop;             // cost position behind the stream's tiles
 };
 
 // The units of CTA j of lane l, in order.
+template <int R>
 struct Units {
   int64_t at, end, from;  // cost position of the current stream; of the lane's end and start
-  int b, g, streams, tiles, n;
-  __device__ __forceinline__ void enter(const Shared& sm, const ScaledArgs& a, const Plan& p, int sequence) {
-    b = sequence;
-    while (b < a.batch && (n = row_blocks(sm, a, b)) == 0) ++b;
-    if (b >= a.batch) {
-      at = INT64_MAX;
-      return;
+  int b, g, n;
+  Seq s;
+  __device__ __forceinline__ void enter(const Shared<R>& sm, const ScaledArgs& a, int sequence) {
+    for (b = sequence; b < a.batch; ++b) {
+      s = seq_of(a, b);
+      n = row_blocks<R>(a, s);
+      if (n > 0) break;
     }
-    streams = (n + p.group - 1) / p.group;
-    tiles = tiles_of(sm, b);
     g = 0;
-    at = sm.cost[b];
+    at = b < a.batch ? sm.cost[b] : INT64_MAX;
   }
-  __device__ __forceinline__ Units(const Shared& sm, const ScaledArgs& a, const Plan& p) {
-    const int lane = blockIdx.x / p.group;
+  __device__ __forceinline__ Units(const Shared<R>& sm, const ScaledArgs& a, const Plan& p) {
+    const int lane = (int)blockIdx.x / p.group;
     from = (int64_t)lane * p.share;
     end = from + p.share < p.length ? from + p.share : p.length;
     at = INT64_MAX;
@@ -226,42 +250,48 @@ struct Units {
       const int mid = (lo + hi) >> 1;
       if (sm.cost[mid] <= from) lo = mid; else hi = mid;
     }
-    enter(sm, a, p, lo);
+    enter(sm, a, lo);
     if (at <= from) {
-      g = (int)((from - at) / (tiles + kFixed));
-      at += (int64_t)g * (tiles + kFixed);
+      const int64_t d = from - at;
+      const int span = tiles_of(s) + kFixed;
+      g = (int)(d <= INT32_MAX ? (int32_t)d / span : d / span);
+      at += (int64_t)g * span;
     }
   }
-  __device__ __forceinline__ bool next(const Shared& sm, const ScaledArgs& a, const Plan& p, Unit& u) {
+  __device__ __noinline__ bool next(const Shared<R>& sm, const ScaledArgs& a, const Plan& p, Unit& u) {
     while (at < end) {
+      const int tiles = tiles_of(s), streams = (n + p.group - 1) / p.group;
       const int64_t lo = at > from ? at : from, stop = at + tiles, hi = stop < end ? stop : end;
       const int block = g * p.group + (int)blockIdx.x % p.group;
       const bool use = lo < hi && block < n;
       if (use) {
-        u.b = b;
         u.row_block = block;
-        const int R = (sm.qo[b + 1] - sm.qo[b]) * a.num_heads;
-        u.rows = min(kRows, R - block * kRows);
-        u.out_row = (int64_t)sm.qo[b] * a.num_heads + (int64_t)block * kRows;
+        u.rows = min(R, s.nq * a.num_heads - block * R);
         u.tile0 = (int)(lo - at);
         u.tiles = (int)(hi - lo);
-        u.kv0 = sm.kv[b];
-        u.keys = sm.kv[b + 1] - u.kv0;
-        u.prefix = u.keys - (sm.qo[b + 1] - sm.qo[b]);
+        u.q0 = s.q0;
+        u.nq = s.nq;
+        u.kv0 = s.kv0;
+        u.keys = s.nk;
+        u.prefix = s.nk - s.nq;
         u.head = lo == at;
         u.whole = u.tiles == tiles;
-        u.pieces = (int)((stop - 1) / p.share - at / p.share) + 1;
+        u.stop = stop;
       }
       if (++g < streams) at += tiles + kFixed;
-      else enter(sm, a, p, b + 1);
+      else enter(sm, a, b + 1);
       if (use) return true;
     }
     return false;
   }
 };
+__device__ __forceinline__ int64_t out_row(const ScaledArgs& a, const Unit& u, int rows) {
+  return (int64_t)u.q0 * a.num_heads + (int64_t)u.row_block * rows;
+}
 
 // ------------------------------------------------------------------ waits
-__device__ __noinline__ bool wait_slow(Shared& sm, uint64_t* bar, uint32_t parity, long long budget, uint32_t where) {
+template <typename Sm>
+__device__ __noinline__ bool wait_slow(Sm& sm, uint64_t* bar, uint32_t parity, long long budget, uint32_t where) {
   const long long t0 = clock64();
   for (;;) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -274,11 +304,13 @@ __device__ __noinline__ bool wait_slow(Shared& sm, uint64_t* bar, uint32_t parit
   }
 }
 // Bounded wait; false once it ran out, here or in another warp.
-__device__ __forceinline__ bool wait(Shared& sm, uint64_t* bar, uint32_t parity, const ScaledArgs& a, uint32_t where) {
+template <typename Sm>
+__device__ __forceinline__ bool wait(Sm& sm, uint64_t* bar, uint32_t parity, const ScaledArgs& a, uint32_t where) {
   return mbar_try_wait(bar, parity) || wait_slow(sm, bar, parity, a.wait_cycles, where);
 }
 
 // A barrier of the softmax warps that tells each whether `any` held in one of them.
+template <int kSoftThreads>
 __device__ __forceinline__ bool soft_vote(bool any) {
   uint32_t r;
   asm volatile(
@@ -288,156 +320,242 @@ __device__ __forceinline__ bool soft_vote(bool any) {
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void soft_sync() { named_bar_sync(1, kSoftThreads); }
+
+// A position in a ring of slots, and the parity of its round.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void step() {
+    if (++slot == N) {
+      slot = 0;
+      parity ^= 1;
+    }
+  }
+};
 
 // ------------------------------------------------------------------ loads (every lane of three warps)
-__device__ void load_role(Shared& sm, const CUtensorMap* latent, const CUtensorMap* rope, const ScaledArgs& a,
+// A tile's pieces in the order of their use by the score product: chunks 0, 1, 2, the rotated columns, chunk 3; the
+// warps take them in turn, a lane the four keys 4 lane .. 4 lane + 3.
+template <int R>
+__device__ void load_role(Shared<R>& sm, const CUtensorMap* latent, const CUtensorMap* rope, const ScaledArgs& a,
                           const Plan& plan) {
-  const int warp = (threadIdx.x >> 5) - kLoadWarp, lane = threadIdx.x & 31;
+  using S = Shape<R>;
+  const int warp = (threadIdx.x >> 5) - S::kLoadWarp, lane = threadIdx.x & 31;
   const int none = (int)a.pool_slots;  // outside the tensor: zeros
-  Units units(sm, a, plan);
+  Units<R> units(sm, a, plan);
   Unit u;
-  int it = 0;
+  Ring<S::kLatentSlots> lr;
+  Ring<S::kRopeSlots> rr;
+  int turn = 0;
   while (units.next(sm, a, plan, u)) {
     const int32_t* index = a.kv_indices + u.kv0;
-    int32_t next[4];
-    auto fetch = [&](int tile) {
+    const int last = min(u.keys, (u.tile0 + u.tiles) * kTile);  // behind this unit's keys
+    int32_t ahead[kAhead][4];  // slots of the tiles after the one that is loaded
+    auto fetch = [&](int32_t (&v)[4], int t) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int key = tile * kTile + 4 * lane + k;
-        next[k] = key < u.keys && tile < u.tile0 + u.tiles ? __ldg(index + key) : -1;
+        const int key = (u.tile0 + t) * kTile + 4 * lane + k;
+        v[k] = key < last ? __ldg(index + key) : -1;
       }
     };
-    fetch(u.tile0);
-    for (int t = 0; t < u.tiles; ++t, ++it) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) fetch(ahead[k], k);
+    for (int t = 0; t < u.tiles; ++t) {
       int32_t y[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        y[k] = next[k];
+        y[k] = ahead[0][k];
         if (y[k] < 0 || y[k] >= none) {
           const int key = (u.tile0 + t) * kTile + 4 * lane + k;
-          if (warp == 0 && key < u.keys) fault(sm, VMLA_ERR_INDEX, (uint32_t)(u.kv0 + key));
+          if (warp == 0 && key < last) fault(sm, VMLA_ERR_INDEX, (uint32_t)(u.kv0 + key));
           y[k] = none;
         }
-      }
-      fetch(u.tile0 + t + 1);
-      const int s = it % kStages;
-      if (!wait(sm, &sm.kfree[s], ((it / kStages) & 1) ^ 1, a, 100)) return;
-      if (warp == 0 && lane == 0) mbar_arrive_expect_tx(&sm.kfull[s], kStageBytes);
-      const uint32_t bar = smem_u32(&sm.kfull[s]);
-      Stage& st = sm.stage[s];
 #pragma unroll
-      for (int c = 0; c <= kChunks; ++c) {
-        if (c % kLoadWarps != warp) continue;
-        if (c < kChunks) tma_gather4(smem_u32(st.latent[c]) + lane * 512, latent, c * 128, y[0], y[1], y[2], y[3], bar);
-        else tma_gather4(smem_u32(st.rope) + lane * 256, rope, kDv, y[0], y[1], y[2], y[3], bar);
+        for (int j = 0; j + 1 < kAhead; ++j) ahead[j][k] = ahead[j + 1][k];
+      }
+      fetch(ahead[kAhead - 1], t + kAhead);
+      // rows on their way from memory before there is room for them: those of the last tile that is known, one CTA of
+      // the lane for each tile, a row or two for each lane of each warp
+      if (kAhead > 1 && (t + (int)blockIdx.x) % plan.group == 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if ((k < 3 ? k : 0) == warp && ahead[kAhead - 2][k] >= 0 && ahead[kAhead - 2][k] < none)
+            prefetch_l2_bulk(a.pool + (int64_t)ahead[kAhead - 2][k] * kDqk, kDqk);
+      }
+#pragma unroll 1
+      for (int piece = 0; piece <= kChunks; ++piece) {
+        const bool mine = turn == warp;
+        turn = turn == kLoadWarps - 1 ? 0 : turn + 1;
+        if (piece != kRopePiece) {
+          if (mine) {
+            if (!wait(sm, &sm.lfree[lr.slot], lr.parity ^ 1, a, 100)) return;
+            if (lane == 0) mbar_arrive_expect_tx(&sm.lfull[lr.slot], kTile * 128);
+            tma_gather4(smem_u32(sm.latent[lr.slot]) + lane * 512, latent, (piece < kRopePiece ? piece : piece - 1) * 128, y[0],
+                        y[1], y[2], y[3], smem_u32(&sm.lfull[lr.slot]));
+          }
+          lr.step();
+        } else {
+          if (mine) {
+            if (!wait(sm, &sm.rfree[rr.slot], rr.parity ^ 1, a, 101)) return;
+            if (lane == 0) mbar_arrive_expect_tx(&sm.rfull[rr.slot], kTile * 64);
+            tma_gather4(smem_u32(sm.rope[rr.slot]) + lane * 256, rope, kDv, y[0], y[1], y[2], y[3],
+                        smem_u32(&sm.rfull[rr.slot]));
+          }
+          rr.step();
+        }
       }
     }
   }
-  // the last releases of the stages have arrived before the CTA leaves
-  for (int k = 1; k <= kStages && it - k >= 0; ++k)
-    wait(sm, &sm.kfree[(it - k) % kStages], ((it - k) / kStages) & 1, a, 101);
 }
 
 // ------------------------------------------------------------------ matrix products (one thread)
-__device__ void mma_role(Shared& sm, const ScaledArgs& a, const Plan& plan, uint32_t tmem) {
-  constexpr uint32_t kScores = idesc_f8_f32(kTile, 2 * kRows, 0, 0, 0, 0);
-  constexpr uint32_t kValues = idesc_f8_f32(128, kParts * kRows, 0, 1, 1, 1);
-  Units units(sm, a, plan);
-  Unit u;
-  int units_begun = 0;
-  auto scores = [&](int it) -> bool {
-    const int s = it % kStages, sb = it & 1;
-    if (!wait(sm, &sm.kfull[s], (it / kStages) & 1, a, 200)) return false;
-    if (!wait(sm, &sm.sfree[sb], ((it >> 1) & 1) ^ 1, a, 201)) return false;
-    tc_fence_after();
-    const uint32_t d = tmem + kSCol + (uint32_t)sb * 2 * kRows;
+// Two sequences of products: scores, piece by piece, and values, chunk by chunk.  Whatever is ready goes next, scores
+// first: they keep the softmax busy, and only values make room for further loads.
+template <int R>
+__device__ void mma_role(Shared<R>& sm, const ScaledArgs& a, const Plan& plan, uint32_t tmem) {
+  using S = Shape<R>;
+  constexpr uint32_t kScores = idesc_f8_f32(kTile, 2 * R, 0, 0, 0, 0);
+  constexpr uint32_t kValues = idesc_f8_f32(128, S::kOCols, 0, 1, 1, 1);
+  Units<R> q_units(sm, a, plan), v_units(sm, a, plan);
+  Unit qu, vu;
+  bool q_more = q_units.next(sm, a, plan, qu), v_more = v_units.next(sm, a, plan, vu);
+  Ring<S::kLatentSlots> ql, vl;
+  Ring<S::kRopeSlots> qr;
+  int q_it = 0, v_it = 0, q_tile = 0, v_tile = 0, q_unit = 0, v_unit = 0, piece = 0, chunk = 0;
+  auto scores = [&]() -> bool {
+    const int sb = q_it & 1;
+    if (piece == 0 && ((q_tile == 0 && !mbar_test_wait(&sm.qfull, q_unit & 1)) ||
+                       !mbar_test_wait(&sm.sfree[sb], ((q_it >> 1) & 1) ^ 1)))
+      return false;
+    const uint32_t d = tmem + S::kSCol + (uint32_t)sb * 2 * R;
+    if (piece == kRopePiece) {
+      if (!mbar_test_wait(&sm.rfull[qr.slot], qr.parity)) return false;
+      tc_fence_after();
+      const uint32_t k = smem_u32(sm.rope[qr.slot]), q = smem_u32(sm.q_rope);
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const uint32_t k = smem_u32(sm.stage[s].latent[c]), q = smem_u32(sm.q_latent[c]);
+      for (int i = 0; i < 2; ++i)
+        mma_ss_f8(d, smem_desc(k + 32 * i, 16, 512, 4), smem_desc(q + 32 * i, 16, 512, 4), kScores, 1u);
+      mma_commit(&sm.rfree[qr.slot]);
+      qr.step();
+    } else {
+      if (!mbar_test_wait(&sm.lfull[ql.slot], ql.parity)) return false;
+      tc_fence_after();
+      const uint32_t k = smem_u32(sm.latent[ql.slot]),
+                     q = smem_u32(sm.q_latent[piece < kRopePiece ? piece : piece - 1]);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        mma_ss_f8(d, smem_desc(k + 32 * i, 16, 1024), smem_desc(q + 32 * i, 16, 1024), kScores, (c | i) != 0);
+        mma_ss_f8(d, smem_desc(k + 32 * i, 16, 1024), smem_desc(q + 32 * i, 16, 1024), kScores, piece > 0 || i > 0);
+      ql.step();
     }
-    const uint32_t k = smem_u32(sm.stage[s].rope), q = smem_u32(sm.q_rope);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      mma_ss_f8(d, smem_desc(k + 32 * i, 16, 512, 4), smem_desc(q + 32 * i, 16, 512, 4), kScores, 1u);
-    mma_commit(&sm.sfull[sb]);
+    if (++piece > kChunks) {
+      mma_commit(&sm.sfull[sb]);
+      piece = 0;
+      ++q_it;
+      if (++q_tile == qu.tiles) {
+        q_tile = 0;
+        ++q_unit;
+        q_more = q_units.next(sm, a, plan, qu);
+      }
+    }
     return true;
   };
-  auto values = [&](int it, bool first) -> bool {
-    const int s = it % kStages, pb = it & 1;
-    if (!wait(sm, &sm.pfull[pb], (it >> 1) & 1, a, 202)) return false;
+  auto values = [&]() -> bool {
+    if (chunk == 0 && (!mbar_test_wait(&sm.pfull, v_it & 1) ||
+                       (v_tile == 0 && !mbar_test_wait(&sm.ofree, (v_unit & 1) ^ 1))))  // the unit before is read out
+      return false;
     tc_fence_after();
+    const uint32_t v = smem_u32(sm.latent[vl.slot]), p = smem_u32(sm.p), d = tmem + chunk * S::kOCols;
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c)
+    for (int i = 0; i < kTile / 32; ++i) {
+      const uint64_t vd = smem_desc(v + 4096 * i, 16, 1024);
+      if constexpr (S::kWide) {
+        mma_ss_f8(d, vd, smem_desc(p + 4096 * i, 16, 1024), kValues, v_tile > 0 || i > 0);
+      } else {
 #pragma unroll
-      for (int i = 0; i < kTile / 32; ++i)
-        mma_ss_f8(tmem + c * kOCols, smem_desc(smem_u32(sm.stage[s].latent[c]) + 4096 * i, 16, 1024),
-                  smem_desc(smem_u32(sm.p[pb]) + 4096 * i, 16, 1024), kValues, !first || i > 0);
-    mma_commit(&sm.pfree[pb]);
-    mma_commit(&sm.kfree[s]);
+        for (int part = 0; part < kParts; ++part)
+          mma_ss_f8(d, vd, smem_desc(p + part * kTile * 64 + 2048 * i, 16, 512, 4), kValues,
+                    v_tile > 0 || i > 0 || part > 0);
+      }
+    }
+    mma_commit(&sm.lfree[vl.slot]);
+    vl.step();
+    if (++chunk == kChunks) {
+      mma_commit(&sm.pfree);
+      chunk = 0;
+      ++v_it;
+      if (++v_tile == vu.tiles) {
+        v_tile = 0;
+        ++v_unit;
+        v_more = v_units.next(sm, a, plan, vu);
+      }
+    }
     return true;
   };
-  // scores of a tile go ahead of the values of the one before, but for a unit's first tile, whose queries come later
-  int it = 0;
-  bool ok = true;
-  while (ok && units.next(sm, a, plan, u)) {
-    ok = wait(sm, &sm.qfull, units_begun & 1, a, 203) && scores(it);
-    for (int t = 0; ok && t < u.tiles; ++t, ++it) {
-      if (t + 1 < u.tiles) ok = scores(it + 1);
-      // (the first product into O: the unit before has been read out)
-      if (ok && t == 0) ok = wait(sm, &sm.ofree, (units_begun & 1) ^ 1, a, 204);
-      if (ok) ok = values(it, t == 0);
+  long long t0 = clock64();
+  while (q_more || v_more) {
+    if ((q_more && scores()) || (v_more && values())) {
+      t0 = clock64();
+      continue;
     }
-    ++units_begun;
+    if (sm.abort_flag) break;
+    if (clock64() - t0 > a.wait_cycles) {
+      fault(sm, VMLA_ERR_TIMEOUT, 200);
+      sm.abort_flag = 1;
+    }
   }
+  // everything issued is complete, and its signals have arrived, before the CTA leaves
   mma_commit(&sm.done);
-  const long long t0 = clock64();
+  t0 = clock64();
   while (!mbar_try_wait(&sm.done, 0) && clock64() - t0 < a.wait_cycles) {
   }
 }
 
 // ------------------------------------------------------------------ queries (softmax warps)
 // The unit's rows into shared memory in two e4m3 parts, their masks; the factor that makes a score of a product.
-__device__ float load_queries(Shared& sm, const ScaledArgs& a, const Unit& u) {
-  constexpr int kGranules = kDqk / 8;                           // of 8 bf16
-  constexpr int kEach = kRows * kGranules / kSoftThreads;      // 9 per thread
-  static_assert(kRows * kGranules % kSoftThreads == 0, "granules per thread");
+// (What runs once per unit is kept in loops: straight-line code that is run once costs more in fetching it.)
+template <int R>
+__device__ __noinline__ float load_queries(Shared<R>& sm, const ScaledArgs& a, const Unit& u) {
+  using S = Shape<R>;
+  constexpr int kGranules = kDqk / 8;                      // of 8 bf16
+  constexpr int kEach = R * kGranules / S::kSoftThreads;   // 9 per thread
+  static_assert(R * kGranules % S::kSoftThreads == 0, "granules per thread");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint4* src = reinterpret_cast<const uint4*>(a.q + u.out_row * kDqk);
+  const uint4* src = reinterpret_cast<const uint4*>(a.q + out_row(a, u, R) * kDqk);
   uint4 v[kEach];
   const int valid = u.rows * kGranules;
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
-    const int i = tid + k * kSoftThreads;
+    const int i = tid + k * S::kSoftThreads;
     v[k] = i < valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
   }
-  const int q0 = sm.qo[u.b], nq = sm.qo[u.b + 1] - q0;
-  if (a.parent && tid < nq) sm.parent[tid] = a.parent[q0 + tid];
-  uint32_t m = 0;  // largest magnitude, as bits of a bf16
+  if (a.parent && tid < u.nq) sm.parent[tid] = a.parent[u.q0 + tid];
+  uint32_t m = 0;  // largest magnitude of either half, as bits of bf16
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
     const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) m = max(m, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t x = w[j] & 0x7FFF7FFFu;
+      asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(x));
+    }
   }
-  m = __reduce_max_sync(0xffffffffu, m);
+  m = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xFFFFu));
   if (lane == 0) sm.q_max[warp] = __uint_as_float(m << 16);
-  soft_sync();
-  float top = 0.f;
-#pragma unroll
-  for (int w = 0; w < kSoftWarps; ++w) top = fmaxf(top, sm.q_max[w]);
+  named_bar_sync(1, S::kSoftThreads);
+  float top = lane < S::kSoftWarps ? sm.q_max[lane] : 0.f;
+  top = warp_max(top);
   // a: 448 = 1.75 x 2^8; queries below 2^-100 are zero to any score
   const uint32_t bits = __float_as_uint(top);
   int e = 8 - ((int)(bits >> 23) - 127) - ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   e = e > 108 ? 108 : e < -119 ? -119 : e;
   const float scale = __uint_as_float((uint32_t)(e + 127) << 23), back = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
+#pragma unroll 1
   for (int k = 0; k < kEach; ++k) {
-    const int i = tid + k * kSoftThreads, row = i / kGranules, col = (i - row * kGranules) * 8;
-    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+    const int i = tid + k * S::kSoftThreads, row = i / kGranules, col = (i - row * kGranules) * 8;
+    const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+    for (int j = 0; j + 1 < kEach; ++j) v[j] = v[j + 1];
     uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -454,28 +572,26 @@ __device__ float load_queries(Shared& sm, const ScaledArgs& a, const Unit& u) {
       hi[j >> 1] |= (uint32_t)h << (16 * (j & 1));
       lo[j >> 1] |= (uint32_t)l << (16 * (j & 1));
     }
-#pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      const int r = row + part * kRows;
-      const uint2 out = part ? make_uint2(lo[0], lo[1]) : make_uint2(hi[0], hi[1]);
-      uint8_t* dst = col < kDv ? sm.q_latent[col >> 7] + r * 128 + ((((col & 127) >> 4) ^ (r & 7)) << 4)
-                               : sm.q_rope + r * 64 + ((((col - kDv) >> 4) ^ ((r >> 1) & 3)) << 4);
-      *reinterpret_cast<uint2*>(dst + (col & 8)) = out;
-    }
+    // (rows r and R + r have the same swizzle: R is a multiple of 8)
+    uint8_t* dst = col < kDv ? sm.q_latent[col >> 7] + row * 128 + ((((col & 127) >> 4) ^ (row & 7)) << 4)
+                             : sm.q_rope + row * 64 + ((((col - kDv) >> 4) ^ ((row >> 1) & 3)) << 4);
+    dst += col & 8;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+    *reinterpret_cast<uint2*>(dst + R * (col < kDv ? 128 : 64)) = make_uint2(lo[0], lo[1]);
   }
-  if (tid < kRows) {
+  if (tid < R) {
     uint64_t word = 0;
     if (tid < u.rows) {
-      const int i = (u.row_block * kRows + tid) / a.num_heads;
+      const int i = (u.row_block * R + tid) / a.num_heads;
       if (a.masks) {
-        word = a.masks[q0 + i];
+        word = a.masks[u.q0 + i];
       } else if (a.parent) {
         int k = i;
         while (k >= 0) {
           word |= 1ull << k;
           const int p = sm.parent[k];
           if (p >= k || p < -1) {
-            fault(sm, VMLA_ERR_PARENT, (uint32_t)(q0 + i));
+            fault(sm, VMLA_ERR_PARENT, (uint32_t)(u.q0 + i));
             word = 0;
             break;
           }
@@ -486,38 +602,56 @@ __device__ float load_queries(Shared& sm, const ScaledArgs& a, const Unit& u) {
       }
     }
     sm.mask[tid] = word;
+    sm.m[tid] = kNone;
   }
   fence_proxy_async_smem();
-  soft_sync();
+  named_bar_sync(1, S::kSoftThreads);
   if (lane == 0 && a.test_fault != kFaultNoQReady) mbar_arrive(&sm.qfull);
   return a.sm_scale * 1.4426950408889634f * back;
 }
 
-// ------------------------------------------------------------------ softmax (eight warps)
-// Order of floats as whole numbers, for the maximum over a warp.
-__device__ __forceinline__ float warp_top(float v) {
-  const int i = __float_as_int(v);
-  const int m = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7FFFFFFF));
-  return __int_as_float(m ^ ((m >> 31) & 0x7FFFFFFF));
+// ------------------------------------------------------------------ softmax
+// 16 values per lane, each reduced over the warp: lane l ends up with value l >> 1.
+template <typename Op>
+__device__ __forceinline__ float reduce16(const float (&v)[16], int lane, Op op) {
+  float a[8], b[4], c[2];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float keep = lane & 16 ? v[i + 8] : v[i], send = lane & 16 ? v[i] : v[i + 8];
+    a[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, 16));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float keep = lane & 8 ? a[i + 4] : a[i], send = lane & 8 ? a[i] : a[i + 4];
+    b[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, 8));
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float keep = lane & 4 ? b[i + 2] : b[i], send = lane & 4 ? b[i] : b[i + 2];
+    c[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, 4));
+  }
+  const float keep = lane & 2 ? c[1] : c[0], send = lane & 2 ? c[0] : c[1];
+  const float d = op(keep, __shfl_xor_sync(0xffffffffu, send, 2));
+  return op(d, __shfl_xor_sync(0xffffffffu, d, 1));
 }
 
-__device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, uint32_t tmem, const Partials& part) {
+template <int R>
+__device__ void softmax_role(Shared<R>& sm, const ScaledArgs& a, const Plan& plan, uint32_t tmem, const Partials& part) {
+  using S = Shape<R>;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int quarter = warp & 3, half = warp >> 2;      // its 32 keys of a tile; its 16 rows
+  const int quarter = warp & 3, row0 = (warp >> 2) * kPerThread;  // its 32 keys of a tile; its first of 16 rows
   const int my_key = quarter * 32 + lane;
   const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-  Units units(sm, a, plan);
+  auto sync = [] { named_bar_sync(1, S::kSoftThreads); };
+  Units<R> units(sm, a, plan);
   Unit u;
-  int it = 0, units_done = 0;
+  int it = 0;
   bool more = units.next(sm, a, plan, u);
   float factor = more ? load_queries(sm, a, u) : 0.f;
   while (more) {
-    float m[kHalf], l[kHalf];
+    float l[kPerThread];
 #pragma unroll
-    for (int r = 0; r < kHalf; ++r) {
-      m[r] = kNone;
-      l[r] = 0.f;
-    }
+    for (int r = 0; r < kPerThread; ++r) l[r] = 0.f;
     // the scales of this thread's keys, fetched a tile ahead, their slots two
     const int32_t* index = a.kv_indices + u.kv0;
     auto slot_of = [&](int t) {
@@ -532,89 +666,104 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
     for (int t = 0; t < u.tiles; ++t, ++it) {
       const float next_scale = scale_of(slot);
       slot = slot_of(t + 2);
-      const int sb = it & 1;
-      wait(sm, &sm.sfull[sb], (it >> 1) & 1, a, 300);  // (should it run out, the vote below ends the work)
-      __syncwarp();
-      tc_fence_after();
-      uint32_t hi[kHalf], lo[kHalf];
-      const uint32_t col = tmem + lanes + kSCol + (uint32_t)(sb * 2 * kRows + half * kHalf);
-      tmem_ld16(col, hi);
-      tmem_ld16(col + kRows, lo);
-      tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.sfree[sb]);
-      float y[kHalf];
-#pragma unroll
-      for (int r = 0; r < kHalf; ++r) y[r] = fmaf(__uint_as_float(lo[r]), 0.0625f, __uint_as_float(hi[r]));
-      const int key = (u.tile0 + t) * kTile + my_key;
+      const int sb = it & 1, key = (u.tile0 + t) * kTile + my_key;
       uint32_t seen = key < u.keys ? 0xFFFFu : 0u;  // rows that see the key
       if (key >= u.prefix && key < u.keys) {
         seen = 0;
-#pragma unroll
-        for (int r = 0; r < kHalf; ++r) seen |= (uint32_t)((sm.mask[half * kHalf + r] >> (key - u.prefix)) & 1) << r;
+#pragma unroll 1
+        for (int r = 0; r < kPerThread; ++r) seen |= (uint32_t)((sm.mask[row0 + r] >> (key - u.prefix)) & 1) << r;
       }
       const bool all_seen = __all_sync(0xffffffffu, seen == 0xFFFFu);
       const float c = scale * factor, held = fmaxf(scale, kTiny) * kUnit;
-      const uint32_t counts = scale >= kTiny ? 0xFFFFFFFFu : 0u;
-      float p[kHalf], w[kHalf];
-      auto weigh = [&]() -> float {
+      wait(sm, &sm.sfull[sb], (it >> 1) & 1, a, 300);  // (should it run out, the vote below ends the work)
+      __syncwarp();
+      const uint32_t col = tmem + lanes + S::kSCol + (uint32_t)(sb * 2 * R + row0);
+      float w[kPerThread];
+      for (;;) {
+        tc_fence_after();
         float most = 0.f;
+        {
+          uint32_t hi[kPerThread], lo[kPerThread];
+          tmem_ld16(col, hi);
+          tmem_ld16(col + R, lo);
+          tmem_wait_ld();
 #pragma unroll
-        for (int r = 0; r < kHalf; ++r) {
-          p[r] = ex2_approx(fmaf(y[r], c, -m[r]));
-          if (!all_seen) p[r] = (seen >> r) & 1 ? p[r] : 0.f;
-          w[r] = p[r] * held;
-          most = fmaxf(most, w[r]);
+          for (int r = 0; r < kPerThread; r += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(&sm.m[row0 + r]);
+            const float mr[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float y = fmaf(__uint_as_float(lo[r + j]), 0.0625f, __uint_as_float(hi[r + j]));
+              w[r + j] = ex2_approx(fmaf(y, c, -mr[j])) * held;
+            }
+          }
         }
-        return most;
-      };
-      const float most = weigh();
-      if (soft_vote(most > kMost || sm.abort_flag != 0)) {
+        if (!all_seen) {
+#pragma unroll
+          for (int r = 0; r < kPerThread; ++r) w[r] = (seen >> r) & 1 ? w[r] : 0.f;
+        }
+#pragma unroll
+        for (int r = 0; r < kPerThread; ++r) most = fmaxf(most, w[r]);
+        if (!soft_vote<S::kSoftThreads>(most > kMost || sm.abort_flag != 0)) break;
         // some weight is too large for its row's reference: raise the references to the tile's largest
         if (tid == 0) sm.stop = sm.abort_flag;
-        const float height = __log2f(fmaxf(scale, kTiny));
+        {
+          uint32_t hi[kPerThread], lo[kPerThread];
+          tmem_ld16(col, hi);
+          tmem_ld16(col + R, lo);
+          tmem_wait_ld();
+          const float height = __log2f(fmaxf(scale, kTiny));
+          float top[kPerThread];
 #pragma unroll
-        for (int r = 0; r < kHalf; ++r) {
-          const float top = warp_top((seen >> r) & 1 ? fmaf(y[r], c, height) : -INFINITY);
-          if (lane == 0) sm.part[quarter][half * kHalf + r] = top;
+          for (int r = 0; r < kPerThread; ++r) {
+            const float y = fmaf(__uint_as_float(lo[r]), 0.0625f, __uint_as_float(hi[r]));
+            top[r] = (seen >> r) & 1 ? fmaf(y, c, height) : -INFINITY;
+          }
+          const float v = reduce16(top, lane, [](float x, float y) { return fmaxf(x, y); });
+          sm.part[quarter][row0 + (lane >> 1)] = v;
         }
-        soft_sync();
+        sync();
         if (sm.stop) return;
-        float f[kHalf];
+        if (tid < R) {
+          const float old = sm.m[tid];
+          const float top = fmaxf(fmaxf(fmaxf(sm.part[0][tid], sm.part[1][tid]), fmaxf(sm.part[2][tid], sm.part[3][tid])), old);
+          sm.f[tid] = ex2_approx(old - top);
+          sm.m[tid] = top;
+        }
+        sync();
+        float f[kPerThread];
 #pragma unroll
-        for (int r = 0; r < kHalf; ++r) {
-          float top = m[r];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) top = fmaxf(top, sm.part[k][half * kHalf + r]);
-          f[r] = ex2_approx(m[r] - top);
-          m[r] = top;
+        for (int r = 0; r < kPerThread; ++r) {
+          f[r] = sm.f[row0 + r];
           l[r] *= f[r];
         }
         if (t > 0) {
           // what has been summed so far, once the products before are complete
-          wait(sm, &sm.pfree[(it - 1) & 1], ((it - 1) >> 1) & 1, a, 301);
+          wait(sm, &sm.pfree, (it & 1) ^ 1, a, 301);
           __syncwarp();
           tc_fence_after();
 #pragma unroll 1
-          for (int k = 0; k < kChunks * kParts; ++k) {
-            const uint32_t at = tmem + lanes + (uint32_t)(k * kRows + half * kHalf);
-            uint32_t o[kHalf];
+          for (int k = 0; k < (int)S::kSCol / R; ++k) {
+            const uint32_t at = tmem + lanes + (uint32_t)(k * R + row0);
+            uint32_t o[kPerThread];
             tmem_ld16(at, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int r = 0; r < kHalf; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * f[r]);
+            for (int r = 0; r < kPerThread; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * f[r]);
             tmem_st16(at, o);
           }
           tmem_wait_st();
-          tc_fence_before();
         }
-        soft_sync();  // (part is written again only past this)
-        weigh();
+        tc_fence_before();
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.sfree[sb]);
+      const float back = __frcp_rn(held);
 #pragma unroll
-      for (int r = 0; r < kHalf; ++r) l[r] += p[r];
+      for (int r = 0; r < kPerThread; ++r) l[r] = fmaf(w[r], back, l[r]);
       // three parts of each weight, four rows to a word
+      const uint32_t counts = scale >= kTiny ? 0xFFFCFFFCu : 0u;
       uint32_t parts[kParts][4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -623,7 +772,7 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
         for (int j = 0; j < 2; ++j) {
           uint32_t x, r1, r2;
           asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(w[4 * k + 2 * j + 1]), "f"(w[4 * k + 2 * j]));
-          x = ((x + 0x00020002u) & 0xFFFCFFFCu) & counts;
+          x = (x + 0x00020002u) & counts;
           h[j][0] = x & 0xFF00FF00u;
           asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r1) : "r"(x), "r"(h[j][0]));
           h[j][1] = r1 & 0xFF00FF00u;
@@ -633,174 +782,173 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
 #pragma unroll
         for (int q = 0; q < kParts; ++q) parts[q][k] = __byte_perm(h[0][q], h[1][q], 0x7531);
       }
-      const int pb = it & 1;
-      if (wait(sm, &sm.pfree[pb], ((it >> 1) & 1) ^ 1, a, 302)) {
-        uint8_t* row = sm.p[pb] + my_key * 128;
+      if (wait(sm, &sm.pfree, (it & 1) ^ 1, a, 302)) {
 #pragma unroll
-        for (int q = 0; q < kParts; ++q)
-          *reinterpret_cast<uint4*>(row + (((2 * q + half) ^ (my_key & 7)) << 4)) =
-              make_uint4(parts[q][0], parts[q][1], parts[q][2], parts[q][3]);
+        for (int q = 0; q < kParts; ++q) {
+          uint8_t* dst = S::kWide ? sm.p + my_key * 128 + (((2 * q + (row0 >> 4)) ^ (my_key & 7)) << 4)
+                                  : sm.p + (q * kTile + my_key) * 64 + (((row0 >> 4) ^ ((my_key >> 1) & 3)) << 4);
+          *reinterpret_cast<uint4*>(dst) = make_uint4(parts[q][0], parts[q][1], parts[q][2], parts[q][3]);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.pfull[pb]);
+      if (lane == 0) mbar_arrive(&sm.pfull);
       scale = next_scale;
     }
-    // row sums over the keys
-#pragma unroll
-    for (int r = 0; r < kHalf; ++r) {
-      l[r] = warp_sum(l[r]);
-      if (lane == 0) sm.part[quarter][half * kHalf + r] = l[r];
+    // row sums over the keys; what the rows' results are scaled by
+    const float sum = reduce16(l, lane, [](float x, float y) { return x + y; });
+    sm.part[quarter][row0 + (lane >> 1)] = sum;
+    sync();
+    const int64_t piece = (int64_t)blockIdx.x * 2 + (u.head ? 1 : 0), first_row = out_row(a, u, R);
+    if (tid < R) {
+      const float total = (sm.part[0][tid] + sm.part[1][tid]) + (sm.part[2][tid] + sm.part[3][tid]), m = sm.m[tid];
+      sm.f[tid] = !u.whole ? 1.f : total > 0.f ? 1.f / (total * kUnit) : 0.f;
+      if (!u.whole) part.ml[piece * R + tid] = make_float2(m, total);
+      else if (tid < u.rows) a.lse[first_row + tid] = total > 0.f ? (m + log2f(total)) * 0.6931471805599453f : -INFINITY;
     }
-    soft_sync();
-#pragma unroll
-    for (int r = 0; r < kHalf; ++r) {
-      const int row = half * kHalf + r;
-      l[r] = (sm.part[0][row] + sm.part[1][row]) + (sm.part[2][row] + sm.part[3][row]);
+    if (tid == 0 && u.head && !u.whole) {
+      sm.cut_pieces = (int)((u.stop - 1) / plan.share) - (int)blockIdx.x / plan.group + 1;
+      sm.cut_rows = u.rows;
+      sm.cut_row = first_row;
     }
-    const Unit done = u;
+    sync();
+    float* po = part.o + piece * R * kDv;
+    uint16_t* out = u.whole ? a.out + first_row * kDv : nullptr;
+    const int rows = u.rows;
     // the next unit's queries while this one's last products run
     more = units.next(sm, a, plan, u);
     if (more) factor = load_queries(sm, a, u);
-    wait(sm, &sm.pfree[(it - 1) & 1], ((it - 1) >> 1) & 1, a, 303);
+    wait(sm, &sm.pfree, (it - 1) & 1, a, 303);
     __syncwarp();
     tc_fence_after();
-    const int64_t piece = (int64_t)blockIdx.x * 2 + (done.head ? 1 : 0);
-    float* po = part.o + piece * kRows * kDv;
 #pragma unroll 1
-    for (int c = 0; c < kChunks; ++c) {
-      const int dim = 128 * c + my_key;  // this thread's lane of O^T
-      uint32_t o[kHalf], x[kHalf];
-      const uint32_t at = tmem + lanes + (uint32_t)(c * kOCols + half * kHalf);
-      tmem_ld16(at, o);
-      tmem_ld16(at + kRows, x);
-      tmem_wait_ld();
+    for (int k = 0; k < kChunks * kPerThread / 8; ++k) {
+      const int chunk = k >> 1, r0 = row0 + 8 * (k & 1);
+      const int dim = 128 * chunk + my_key;  // this thread's lane of O^T
+      const uint32_t at = tmem + lanes + (uint32_t)(chunk * S::kOCols + r0);
+      float o[8];
+      {
+        uint32_t x[8];
+        tmem_ld8(at, x);
+        if constexpr (S::kWide) {
+          uint32_t y[8], z[8];
+          tmem_ld8(at + R, y);
+          tmem_ld8(at + 2 * R, z);
+          tmem_wait_ld();
 #pragma unroll
-      for (int r = 0; r < kHalf; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) + __uint_as_float(x[r]));
-      tmem_ld16(at + 2 * kRows, x);
-      tmem_wait_ld();
+          for (int r = 0; r < 8; ++r) o[r] = (__uint_as_float(x[r]) + __uint_as_float(y[r])) + __uint_as_float(z[r]);
+        } else {
+          tmem_wait_ld();
 #pragma unroll
-      for (int r = 0; r < kHalf; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) + __uint_as_float(x[r]));
-      if (done.whole) {
+          for (int r = 0; r < 8; ++r) o[r] = __uint_as_float(x[r]);
+        }
+      }
+      if (out) {
         // pairs of lanes exchange a value each, so that a lane stores two columns of one row
 #pragma unroll
-        for (int r = 0; r < kHalf; r += 2) {
-          const float s0 = l[r] > 0.f ? __fdividef(1.f, l[r] * kUnit) : 0.f, s1 = l[r + 1] > 0.f ? __fdividef(1.f, l[r + 1] * kUnit) : 0.f;
-          const float a0 = __uint_as_float(o[r]) * s0, a1 = __uint_as_float(o[r + 1]) * s1;
+        for (int r = 0; r < 8; r += 2) {
+          const float a0 = o[r] * sm.f[r0 + r], a1 = o[r + 1] * sm.f[r0 + r + 1];
           const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a0 : a1, 1);
           const uint32_t pair = lane & 1 ? pack_bf16x2(other, a1) : pack_bf16x2(a0, other);
-          const int row = half * kHalf + r + (lane & 1);
-          if (row < done.rows)
-            *reinterpret_cast<uint32_t*>(a.out + (done.out_row + row) * kDv + (dim & ~1)) = pair;
+          const int row = r0 + r + (lane & 1);
+          if (row < rows) *reinterpret_cast<uint32_t*>(out + row * kDv + (dim & ~1)) = pair;
         }
       } else {
 #pragma unroll
-        for (int r = 0; r < kHalf; ++r) po[(half * kHalf + r) * kDv + dim] = __uint_as_float(o[r]);
-      }
-    }
-    if (quarter == 0) {
-#pragma unroll
-      for (int r = 0; r < kHalf; ++r) {
-        const int row = half * kHalf + r;
-        if (lane == r) {
-          if (!done.whole) part.ml[piece * kRows + row] = make_float2(m[r], l[r]);
-          else if (row < done.rows)
-            a.lse[done.out_row + row] = l[r] > 0.f ? (m[r] + log2f(l[r])) * 0.6931471805599453f : -INFINITY;
-        }
+        for (int r = 0; r < 8; ++r) po[(r0 + r) * kDv + dim] = o[r];
       }
     }
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.ofree);
-    ++units_done;
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+template <int R>
+__global__ void __launch_bounds__(Shape<R>::kThreads, 1)
 scaled_kernel(const __grid_constant__ CUtensorMap latent, const __grid_constant__ CUtensorMap rope,
               const __grid_constant__ ScaledArgs a, CtaInfo* __restrict__ info, const Partials part) {
+  using S = Shape<R>;
   extern __shared__ uint8_t raw[];
-  Shared& sm = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  Shared<R>& sm = *reinterpret_cast<Shared<R>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5;
+  if (warp == S::kMmaWarp) {
+    tmem_alloc(&sm.tmem, 512);
+    tmem_relinquish();
+  }
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sm.kfull[s], 1);
-      mbar_init(&sm.kfree[s], 1);
+    for (int s = 0; s < S::kLatentSlots; ++s) {
+      mbar_init(&sm.lfull[s], 1);
+      mbar_init(&sm.lfree[s], 1);
+    }
+    for (int s = 0; s < S::kRopeSlots; ++s) {
+      mbar_init(&sm.rfull[s], 1);
+      mbar_init(&sm.rfree[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.sfull[s], 1);
-      mbar_init(&sm.sfree[s], kSoftWarps);
-      mbar_init(&sm.pfull[s], kSoftWarps);
-      mbar_init(&sm.pfree[s], 1);
+      mbar_init(&sm.sfree[s], S::kSoftWarps);
     }
-    mbar_init(&sm.qfull, kSoftWarps);
-    mbar_init(&sm.ofree, kSoftWarps);
+    mbar_init(&sm.pfull, S::kSoftWarps);
+    mbar_init(&sm.pfree, 1);
+    mbar_init(&sm.qfull, S::kSoftWarps);
+    mbar_init(&sm.ofree, S::kSoftWarps);
     mbar_init(&sm.done, 1);
     sm.abort_flag = 0;
     sm.fault[0] = sm.fault[1] = 0;
+    sm.cut_pieces = 0;
     fence_mbar_init();
     prefetch_tensormap(&latent);
     prefetch_tensormap(&rope);
   }
+  __syncwarp();
   Plan plan;
   const bool ok = make_plan(sm, a, plan);
-  CtaInfo mine = {};
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
   if (ok) {
-    if (tid == 0) {
-      Units units(sm, a, plan);
-      Unit u;
-      while (units.next(sm, a, plan, u))
-        if (u.head && !u.whole) {
-          mine.row = u.out_row;
-          mine.pieces = u.pieces;
-          mine.rows = u.rows;
-          mine.group = plan.group;
-        }
-    }
-    __syncwarp();
-    if (warp == kMmaWarp) {
-      tmem_alloc(&sm.tmem, 512);
-      tmem_relinquish();
-    }
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = sm.tmem;
-    if (warp < kSoftWarps) {
+    if (warp < S::kSoftWarps) {
       softmax_role(sm, a, plan, tmem, part);
-    } else if (warp == kMmaWarp) {
+    } else if (warp == S::kMmaWarp) {
       if ((tid & 31) == 0) mma_role(sm, a, plan, tmem);
     } else {
       load_role(sm, &latent, &rope, a, plan);
     }
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
-    grid_dependents_launch();
-    if (sm.abort_flag) {
-      // a wait ran out: loads, commits and products issued before may still be on their way into this CTA's memories,
-      // each for microseconds; half a millisecond of the global timer (at most 2^26 reads of it)
-      if (tid == 0) {
-        uint64_t t0, t;
-        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-        for (int k = 0; k < (1 << 26); ++k) {
-          asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-          if (t - t0 > 500000ull) break;
-        }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  grid_dependents_launch();
+  if (sm.abort_flag) {
+    // a wait ran out: loads, commits and products issued before may still be on their way into this CTA's memories,
+    // each for microseconds; half a millisecond of the global timer (at most 2^26 reads of it)
+    if (tid == 0) {
+      uint64_t t0, t;
+      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+      for (int k = 0; k < (1 << 26); ++k) {
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+        if (t - t0 > 500000ull) break;
       }
-      __syncthreads();
     }
-    __syncwarp();
-    if (warp == kMmaWarp) {
-      tc_fence_after();
-      tmem_dealloc(tmem, 512);
-    }
+    __syncthreads();
+  }
+  __syncwarp();
+  if (warp == S::kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
   if (tid == 0) {
+    CtaInfo mine = {};
     mine.fault = ok ? sm.fault[0] : (uint32_t)VMLA_ERR_SHAPE;
     mine.fault_info = ok ? sm.fault[1] : 0;
-    if (sm.abort_flag) mine.pieces = 0;
+    if (ok && !sm.abort_flag && sm.cut_pieces > 0) {
+      mine.pieces = sm.cut_pieces;
+      mine.rows = sm.cut_rows;
+      mine.row = sm.cut_row;
+      mine.group = plan.group;
+    }
     info[blockIdx.x] = mine;
   }
 }
@@ -808,6 +956,7 @@ scaled_kernel(const __grid_constant__ CUtensorMap latent, const __grid_constant_
 // Joins the partials of one row of a cut stream: one block per (CTA that begins the stream, row).
 constexpr int kJoinThreads = kDv / 4;
 constexpr int kMaxCtas = 512;
+template <int R>
 __global__ void __launch_bounds__(kJoinThreads)
 scaled_join_kernel(const CtaInfo* __restrict__ info, int ctas, const Partials part, uint16_t* __restrict__ out,
                    float* __restrict__ lse, uint32_t* __restrict__ status) {
@@ -829,7 +978,7 @@ scaled_join_kernel(const CtaInfo* __restrict__ info, int ctas, const Partials pa
   if (row >= i.rows || i.pieces == 0) return;
   // piece 0 lies in this CTA's second slot, piece k in the first slot of the CTA k lanes on
   auto slot = [&](int k) { return k == 0 ? (int64_t)cta * 2 + 1 : ((int64_t)cta + (int64_t)k * i.group) * 2; };
-  for (int k = tid; k < i.pieces; k += kJoinThreads) ml[k] = part.ml[slot(k) * kRows + row];
+  for (int k = tid; k < i.pieces; k += kJoinThreads) ml[k] = part.ml[slot(k) * R + row];
   __syncthreads();
   float top = kNone;
   for (int k = 0; k < i.pieces; ++k) top = fmaxf(top, ml[k].x);
@@ -838,7 +987,7 @@ scaled_join_kernel(const CtaInfo* __restrict__ info, int ctas, const Partials pa
 #pragma unroll 4
   for (int k = 0; k < i.pieces; ++k) {
     const float w = ex2_approx(ml[k].x - top);
-    const float4 v = reinterpret_cast<const float4*>(part.o + (slot(k) * kRows + row) * kDv)[tid];
+    const float4 v = reinterpret_cast<const float4*>(part.o + (slot(k) * R + row) * kDv)[tid];
     sum = fmaf(ml[k].y, w, sum);
     o.x = fmaf(v.x, w, o.x);
     o.y = fmaf(v.y, w, o.y);
@@ -854,7 +1003,7 @@ scaled_join_kernel(const CtaInfo* __restrict__ info, int ctas, const Partials pa
 // Workspace: status words, the CTAs' infos, the partials.
 constexpr size_t kInfoOff = 256;
 size_t ml_off(int sms) { return kInfoOff + (((size_t)sms * sizeof(CtaInfo) + 255) & ~(size_t)255); }
-size_t o_off(int sms) { return ml_off(sms) + (size_t)sms * 2 * kRows * sizeof(float2); }
+size_t o_off(int sms) { return ml_off(sms) + (size_t)sms * 2 * kMaxRows * sizeof(float2); }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -884,9 +1033,43 @@ bool encode_pool(EncodeTiledFn enc, CUtensorMap* map, const uint8_t* pool, int64
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int R>
+int launch(const ScaledArgs& a, int sms, const CUtensorMap& latent, const CUtensorMap& rope, cudaStream_t stream) {
+  static std::mutex mu;
+  static bool ready[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return VMLA_ERR_CUDA;
+  {
+    std::lock_guard<std::mutex> g(mu);
+    if (dev >= 64 || !ready[dev]) {
+      if (cudaFuncSetAttribute(scaled_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSharedBytes<R>) !=
+          cudaSuccess)
+        return VMLA_ERR_CUDA;
+      if (dev < 64) ready[dev] = true;
+    }
+  }
+  CtaInfo* info = reinterpret_cast<CtaInfo*>(a.workspace + kInfoOff);
+  Partials part;
+  part.ml = reinterpret_cast<float2*>(a.workspace + ml_off(sms));
+  part.o = reinterpret_cast<float*>(a.workspace + o_off(sms));
+  scaled_kernel<R><<<sms, Shape<R>::kThreads, kSharedBytes<R>, stream>>>(latent, rope, a, info, part);
+  if (cudaGetLastError() != cudaSuccess) return VMLA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1] = {early_start_attribute()};
+  cfg.gridDim = dim3((unsigned)sms, R, 1);
+  cfg.blockDim = dim3(kJoinThreads, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, scaled_join_kernel<R>, (const CtaInfo*)info, sms, part, a.out, a.lse, a.status) ==
+                 cudaSuccess
+             ? VMLA_OK
+             : VMLA_ERR_CUDA;
+}
+
 }  // namespace
 
-size_t scaled_workspace(int sms) { return o_off(sms) + (size_t)sms * 2 * kRows * kDv * sizeof(float); }
+size_t scaled_workspace(int sms) { return o_off(sms) + (size_t)sms * 2 * kMaxRows * kDv * sizeof(float); }
 
 int launch_scaled(const ScaledArgs& a, int sms, void* stream) {
   if (sms > kMaxCtas) return VMLA_ERR_DEVICE;
@@ -898,36 +1081,9 @@ int launch_scaled(const ScaledArgs& a, int sms, void* stream) {
   if (!encode_pool(enc, &latent, pool, a.pool_slots, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_pool(enc, &rope, pool, a.pool_slots, 64, CU_TENSOR_MAP_SWIZZLE_64B))
     return VMLA_ERR_CUDA;
-  static std::mutex mu;
-  static bool ready[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return VMLA_ERR_CUDA;
-  {
-    std::lock_guard<std::mutex> g(mu);
-    if (dev >= 64 || !ready[dev]) {
-      if (cudaFuncSetAttribute(scaled_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSharedBytes) !=
-          cudaSuccess)
-        return VMLA_ERR_CUDA;
-      if (dev < 64) ready[dev] = true;
-    }
-  }
-  CtaInfo* info = reinterpret_cast<CtaInfo*>(a.workspace + kInfoOff);
-  Partials part;
-  part.ml = reinterpret_cast<float2*>(a.workspace + ml_off(sms));
-  part.o = reinterpret_cast<float*>(a.workspace + o_off(sms));
-  scaled_kernel<<<sms, kThreads, kSharedBytes, (cudaStream_t)stream>>>(latent, rope, a, info, part);
-  if (cudaGetLastError() != cudaSuccess) return VMLA_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1] = {early_start_attribute()};
-  cfg.gridDim = dim3((unsigned)sms, kRows, 1);
-  cfg.blockDim = dim3(kJoinThreads, 1, 1);
-  cfg.stream = (cudaStream_t)stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, scaled_join_kernel, (const CtaInfo*)info, sms, part, a.out, a.lse, a.status) ==
-                 cudaSuccess
-             ? VMLA_OK
-             : VMLA_ERR_CUDA;
+  // by the rows that a sequence has on the average of the bounds: units of 64 once they are more than 32
+  return a.max_q * a.num_heads > 32 * (int64_t)a.batch ? launch<64>(a, sms, latent, rope, (cudaStream_t)stream)
+                                                       : launch<32>(a, sms, latent, rope, (cudaStream_t)stream);
 }
 
 }  // namespace vmla
