@@ -37,66 +37,55 @@ using namespace sm100;
 namespace {
 
 constexpr int kTile = 128;          // keys
+constexpr int kRows = 32;           // query rows of a unit
 constexpr int kChunks = kDv / 128;  // 4 column chunks of 128 bytes, and one of 64
+constexpr int kPieces = kChunks + 1;
+constexpr int kRopePiece = 3;       // place of the rotated columns among a tile's pieces
 constexpr int kParts = 3;           // of a weight
 constexpr int kPerThread = 16;      // rows of a softmax thread
-constexpr int kLoadWarps = 3;
-constexpr int kAhead = 3;           // tiles whose slots a load warp knows
-constexpr int kRopePiece = 3;       // place of the rotated columns among a tile's pieces
+constexpr int kSoftWarps = 4 * kRows / kPerThread;  // per quarter of the tile's keys, 16 rows each
+constexpr int kSoftThreads = kSoftWarps * 32;
+constexpr int kLoadWarps = 7;
+constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
+constexpr int kRun = 16;            // consecutive slots that one box fetches
+constexpr uint32_t kOCols = kParts * kRows;       // 96 columns of tensor memory per 128 value columns
+constexpr uint32_t kSCol = kChunks * kOCols;      // 384
+constexpr int kLatentSlots = 8, kRopeSlots = 2, kPSlots = 2;
 constexpr int kFixed = 2;           // what a unit costs beside its tiles, in tiles
 constexpr float kNone = -3e38f;     // reference of a row that has seen no key
 constexpr float kUnit = 2048.f;     // weights are held times 2^11
 constexpr float kMost = 32768.f;    // largest weight held
 constexpr float kTiny = 0x1p-100f;  // smaller scales count as zero
-constexpr int kMaxRows = 64;
+static_assert(kSCol + 2 * 2 * kRows == 512, "tensor memory");
+static_assert(kThreads % 128 == 0, "whole register banks");
+static_assert(kLoadWarps <= kLatentSlots && kLatentSlots <= 2 * kLoadWarps && kLatentSlots % 4 == 0 && kRopeSlots == 2,
+              "see load_role");
 
-// A unit's size, 32 or 64 query rows, and what follows from it.
-template <int R>
-struct Shape {
-  static constexpr int kRows = R;
-  static constexpr int kSoftWarps = 4 * R / kPerThread;  // per quarter of the tile's keys, 16 rows each
-  static constexpr int kSoftThreads = kSoftWarps * 32;
-  static constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kMmaWarp + 1;
-  static constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
-  // with 32 rows the three parts of the weights stand side by side in one product (and in three sets of O's columns,
-  // added at the end); with 64 there is tensor memory for one set, and each part is a product of its own
-  static constexpr bool kWide = R == 32;
-  static constexpr uint32_t kOCols = kWide ? kParts * R : R;  // columns of tensor memory per 128 value columns
-  static constexpr uint32_t kSCol = kChunks * kOCols;
-  static constexpr int kPRow = kWide ? 128 : 64;              // bytes of a key in P: all parts, or one
-  static constexpr int kPBytes = kTile * kPRow * (kWide ? 1 : kParts);
-  static constexpr int kLatentSlots = R == 32 ? 9 : 7, kRopeSlots = R == 32 ? 2 : 1;
-  static_assert(kSCol + 2 * 2 * R == 512, "tensor memory");
-};
-
-template <int R>
 struct Shared {
-  using S = Shape<R>;
-  uint8_t latent[S::kLatentSlots][kTile * 128];  // a tile's chunk: [key][128 bytes], 128-byte swizzle
-  uint8_t q_latent[kChunks][2 * R * 128];        // [hi rows, lo rows][128 bytes], 128-byte swizzle
-  uint8_t p[S::kPBytes];                         // wide: [key][hi 32 | mid 32 | lo 32 | -], 128-byte swizzle;
-                                                 // else [part][key][64], 64-byte swizzle
-  uint8_t rope[S::kRopeSlots][kTile * 64];       // [key][64 bytes], 64-byte swizzle
-  uint8_t q_rope[2 * R * 64];                    // 64-byte swizzle
-  float m[R], f[R];                              // reference of each row (log2), factor of its last change
-  float part[4][R];                              // per quarter of the keys: row maxima, or row sums
-  uint64_t mask[R];                              // the unit's rows: visible drafts
-  int64_t cost[VMLA_MAX_BATCH + 1];              // cost position of each sequence's first stream
+  uint8_t latent[kLatentSlots][kTile * 128];  // a tile's chunk: [key][128 bytes], 128-byte swizzle
+  uint8_t q_latent[kChunks][2 * kRows * 128]; // [hi rows, lo rows][128 bytes], 128-byte swizzle
+  uint8_t p[kPSlots][kTile * 128];            // [key][hi 32 | mid 32 | lo 32 | -], 128-byte swizzle
+  uint8_t rope[kRopeSlots][kTile * 64];       // [key][64 bytes], 64-byte swizzle
+  uint8_t q_rope[2 * kRows * 64];             // 64-byte swizzle
+  float m[kRows], f[kRows];                   // reference of each row (log2), factor of its last change
+  float part[4][kRows];                       // per quarter of the keys: row maxima, or row sums
+  uint64_t mask[kRows];                       // the unit's rows: visible drafts
+  uint32_t cost[VMLA_MAX_BATCH + 1];          // cost position of each sequence's first stream
   int32_t parent[VMLA_MAX_DRAFT];
-  float q_max[S::kSoftWarps];
-  int64_t sums[4][S::kThreads / 32];
-  uint64_t lfull[S::kLatentSlots], lfree[S::kLatentSlots], rfull[S::kRopeSlots], rfree[S::kRopeSlots];
-  uint64_t sfull[2], sfree[2], pfull, pfree, qfull, ofree, done;
+  float q_max[kSoftWarps];
+  uint32_t sums[2][kThreads / 32];
+  uint64_t lfull[kLatentSlots], lfree[kLatentSlots], rfull[kRopeSlots], rfree[kRopeSlots];
+  uint64_t sfull[2], sfree[2], pfull[kPSlots], pfree[kPSlots], qfull, ofree, done;
   uint32_t tmem;
   volatile int32_t abort_flag;
   int32_t stop;
-  uint32_t fault[2];                             // first fault of this CTA: code, info
-  int32_t cut_pieces, cut_rows;                  // the stream that starts in this CTA's lane and goes on in the next
+  uint32_t fault[2];                          // first fault of this CTA: code, info
+  int32_t cut_pieces, cut_rows;               // the stream that starts in this CTA's lane and goes on in the next
   int64_t cut_row;
 };
-template <int R>
-constexpr size_t kSharedBytes = sizeof(Shared<R>) + 1024;
-static_assert(kSharedBytes<32> <= 232448 && kSharedBytes<64> <= 232448, "shared memory");
+constexpr size_t kSharedBytes = sizeof(Shared) + 1024;
+static_assert(kSharedBytes <= 232448, "shared memory");
 
 // What a CTA tells the joining launch: the stream that starts in its lane and is cut by the lane's end, and its fault.
 struct alignas(32) CtaInfo {
@@ -109,20 +98,56 @@ struct alignas(32) CtaInfo {
 };
 
 struct Partials {
-  float* o;        // [2 x CTAs][R][512], weights times kUnit
-  float2* ml;      // [2 x CTAs][R]: reference (log2), sum
+  float* o;        // [2 x CTAs][kRows][512], weights times kUnit
+  float2* ml;      // [2 x CTAs][kRows]: reference (log2), sum
 };
 
-template <typename Sm>
-__device__ __forceinline__ void fault(Sm& sm, int code, uint32_t info) {
+__device__ __forceinline__ void fault(Shared& sm, int code, uint32_t info) {
   if (atomicCAS(&sm.fault[0], 0u, (uint32_t)code) == 0u) sm.fault[1] = info;
 }
 
+struct Maps {
+  CUtensorMap latent, rope;          // gathers of four rows
+  CUtensorMap latent_run, rope_run;  // boxes of kRun rows
+};
+
+// Ends the work of every CTA of the lane: their waits give up.
+template <int C>
+__device__ __noinline__ void give_up(Shared& sm) {
+  sm.abort_flag = 1;
+  if (C > 1) {
+    const uint32_t flag = smem_u32(const_cast<const int32_t*>(&sm.abort_flag));
+    for (uint32_t r = 0; r < C; ++r) st_cluster_u32(mapa(flag, r), 1u);
+  }
+}
+
+// One arrival at the barrier, in every CTA of the lane, once this thread's products so far are complete.
+template <int C>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if (C == 1) mma_commit(bar);
+  else mma_commit_multicast(bar, (uint16_t)((1 << C) - 1));
+}
+
+// Copies into the same place of every CTA of the lane.
+template <int C>
+__device__ __forceinline__ void load_gather(uint32_t dst, const CUtensorMap* map, int x, int y0, int y1, int y2, int y3,
+                                            uint32_t bar) {
+  if (C == 1) tma_gather4(dst, map, x, y0, y1, y2, y3, bar);
+  else tma_gather4_multicast(dst, map, x, y0, y1, y2, y3, bar, (uint16_t)((1 << C) - 1));
+}
+template <int C>
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  if (C == 1) tma_load_2d(dst, map, x, y, bar);
+  else tma_load_2d_multicast(dst, map, x, y, bar, (uint16_t)((1 << C) - 1));
+}
+
 // ------------------------------------------------------------------ plan
+// Costs are counted in tiles of whole lanes: at most 2^24 tiles (2^31 keys) x 256 row blocks / C, and kFixed a stream,
+// which fit 32 bits but for C = 1, where a sequence has few row blocks on the average of the call's bounds; a plan whose
+// cost does not fit is refused.
 struct Plan {
-  int64_t length;  // of all streams
-  int64_t share;   // of a lane
-  int32_t group;   // CTAs of a lane
+  uint32_t length;  // of all streams
+  uint32_t share;   // of a lane
   int32_t lanes;
 };
 
@@ -138,113 +163,88 @@ __device__ __forceinline__ Seq seq_of(const ScaledArgs& a, int b) {
   s.nk = __ldg(a.kv_indptr + b + 1) - s.kv0;
   return s;
 }
-template <int R>
-__device__ __forceinline__ int row_blocks(const ScaledArgs& a, const Seq& s) { return (s.nq * a.num_heads + R - 1) / R; }
-__device__ __forceinline__ int tiles_of(const Seq& s) { return (s.nk + kTile - 1) / kTile; }
+// Streams of C row blocks.
+template <int C>
+__device__ __forceinline__ int streams_of(const ScaledArgs& a, int nq) {
+  return (nq * a.num_heads + C * kRows - 1) / (C * kRows);
+}
+__device__ __forceinline__ int tiles_of(int nk) { return nk / kTile + (nk % kTile != 0); }
 
 // Reads the lengths and shares the work out (whole CTA); false where the lengths are out of order or past a bound.
-template <int R>
-__device__ bool make_plan(Shared<R>& sm, const ScaledArgs& a, Plan& plan) {
-  constexpr int kThreads = Shape<R>::kThreads;
+template <int C>
+__device__ bool make_plan(Shared& sm, const ScaledArgs& a, Plan& plan) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  bool ok = tid != 0 || (a.kv_indptr[0] == 0 && a.qo_indptr[0] == 0 && a.kv_indptr[a.batch] <= a.max_kv &&
-                         a.qo_indptr[a.batch] <= a.max_q);
-  int64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll 1
-  for (int b = tid; b < a.batch; b += kThreads) {
-    const int64_t k0 = __ldg(a.kv_indptr + b), k1 = __ldg(a.kv_indptr + b + 1), q0 = __ldg(a.qo_indptr + b),
-                  q1 = __ldg(a.qo_indptr + b + 1);
-    const bool good = q1 >= q0 && q1 - q0 <= VMLA_MAX_DRAFT && k1 - k0 >= q1 - q0;
-    int64_t blocks = 0, span = 0;
-    if (good) {
-      blocks = ((q1 - q0) * a.num_heads + R - 1) / R;
-      span = (k1 - k0 + kTile - 1) / kTile + kFixed;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) sum[k] += ((blocks + (1 << k) - 1) >> k) * span;
-    }
-    ok = ok && good;
-    sm.cost[b] = blocks << 32 | span;  // (until the costs are summed up)
+  static_assert(kThreads >= VMLA_MAX_BATCH, "a thread per sequence");
+  bool ok = true;
+  uint64_t cost = 0;
+  if (tid < a.batch) {
+    const int64_t k0 = __ldg(a.kv_indptr + tid), k1 = __ldg(a.kv_indptr + tid + 1), q0 = __ldg(a.qo_indptr + tid),
+                  q1 = __ldg(a.qo_indptr + tid + 1);
+    ok = q1 >= q0 && q1 - q0 <= VMLA_MAX_DRAFT && k1 - k0 >= q1 - q0;
+    if (tid == 0) ok = ok && k0 == 0 && q0 == 0;
+    if (tid == a.batch - 1) ok = ok && k1 <= a.max_kv && q1 <= a.max_q;
+    if (ok) cost = (uint64_t)streams_of<C>(a, (int)(q1 - q0)) * (uint64_t)(tiles_of((int)(k1 - k0)) + kFixed);
   }
+  uint64_t upto = cost;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
-    if (lane == 0) sm.sums[k][warp] = sum[k];
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t u = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += u;
   }
+  if (upto > 0x08000000u) ok = false;  // (so that sixteen warps' sums fit 32 bits)
+  if (lane == 31) sm.sums[0][warp] = (uint32_t)upto;
   if (!__syncthreads_and(ok)) return false;
-  // the largest G whose shares are within 1/32 of the smallest ones
-  int64_t least = INT64_MAX, length[4], share[4];
+  uint32_t all = lane < kThreads / 32 ? sm.sums[0][lane] : 0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    length[k] = lane < kThreads / 32 ? sm.sums[k][lane] : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) length[k] += __shfl_xor_sync(0xffffffffu, length[k], o);
-    const int lanes = (int)gridDim.x >> k;
-    share[k] = lanes == 0 ? INT64_MAX / 2
-               : length[k] <= INT32_MAX - lanes ? (int32_t)(length[k] + lanes - 1) / lanes : (length[k] + lanes - 1) / lanes;
-    least = share[k] < least ? share[k] : least;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, all, o);
+    if (lane >= o) all += u;
   }
-  int pick = 0;
-#pragma unroll
-  for (int k = 1; k < 4; ++k)
-    if (share[k] <= least + least / 32) pick = k;
-  plan.group = 1 << pick;
-  plan.lanes = (int)gridDim.x >> pick;
-  plan.length = length[pick];
-  plan.share = share[pick] > 0 ? share[pick] : 1;
-  if (warp == 0) {  // running sums of the sequences' costs, 32 at a time
-    int64_t before = 0;
-#pragma unroll 1
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-      const int b = b0 + lane;
-      const int64_t v = b < a.batch ? sm.cost[b] : 0;
-      const int64_t mine = (((v >> 32) + plan.group - 1) >> pick) * (v & 0xFFFFFFFF);
-      int64_t upto = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += u;
-      }
-      if (b < a.batch) sm.cost[b] = before + upto - mine;
-      before += __shfl_sync(0xffffffffu, upto, 31);
-    }
-    if (lane == 0) sm.cost[a.batch] = before;
-  }
+  plan.length = __shfl_sync(0xffffffffu, all, 31);
+  const uint32_t before = warp > 0 ? __shfl_sync(0xffffffffu, all, warp - 1) : 0;
+  if (tid <= a.batch) sm.cost[tid] = before + (uint32_t)(upto - cost);
+  if (tid == 0 && a.batch == kThreads) sm.cost[a.batch] = plan.length;
+  plan.lanes = (int)gridDim.x / C;
+  plan.share = (plan.length + plan.lanes - 1) / plan.lanes;
+  if (plan.share == 0) plan.share = 1;
   __syncthreads();
   return true;
 }
 
 // One row block of a sequence over some of its tiles.
 struct Unit {
-  int row_block, rows;      // rows of the block that are the sequence's
+  int row_block, rows;      // rows of the block that are the sequence's (0: none; the CTA goes along for its lane's loads)
   int tile0, tiles;         // its tiles
   int q0, nq;               // the sequence's drafts
   int kv0, keys, prefix;    // first entry of kv_indices; keys and prefix of the sequence
   bool whole, head;         // every tile of the stream; its first tile is among these
-  int64_t stop;             // cost position behind the stream's tiles
+  uint32_t stop;            // cost position behind the stream's tiles
 };
 
-// The units of CTA j of lane l, in order.
-template <int R>
+// The units of a CTA in its lane, in order; the CTAs of a lane have the same tiles.
+template <int C>
 struct Units {
-  int64_t at, end, from;  // cost position of the current stream; of the lane's end and start
+  uint32_t at, end, from;  // cost position of the current stream; of the lane's end and start
   int b, g, n;
   Seq s;
-  __device__ __forceinline__ void enter(const Shared<R>& sm, const ScaledArgs& a, int sequence) {
+  __device__ __forceinline__ void enter(const Shared& sm, const ScaledArgs& a, int sequence) {
     for (b = sequence; b < a.batch; ++b) {
       s = seq_of(a, b);
-      n = row_blocks<R>(a, s);
+      n = streams_of<C>(a, s.nq);
       if (n > 0) break;
     }
     g = 0;
-    at = b < a.batch ? sm.cost[b] : INT64_MAX;
+    at = b < a.batch ? sm.cost[b] : 0xFFFFFFFFu;
   }
-  __device__ __forceinline__ Units(const Shared<R>& sm, const ScaledArgs& a, const Plan& p) {
-    const int lane = (int)blockIdx.x / p.group;
-    from = (int64_t)lane * p.share;
+  __device__ __forceinline__ Units(const Shared& sm, const ScaledArgs& a, const Plan& p) {
+    const uint32_t lane = blockIdx.x / C;
+    from = lane * p.share;  // (below the length plus one share: fits)
     end = from + p.share < p.length ? from + p.share : p.length;
-    at = INT64_MAX;
-    if (lane >= p.lanes || from >= end) return;
+    at = 0xFFFFFFFFu;
+    if ((int)lane >= p.lanes || from >= end) {
+      end = 0;
+      return;
+    }
     int lo = 0, hi = a.batch;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -252,21 +252,19 @@ struct Units {
     }
     enter(sm, a, lo);
     if (at <= from) {
-      const int64_t d = from - at;
-      const int span = tiles_of(s) + kFixed;
-      g = (int)(d <= INT32_MAX ? (int32_t)d / span : d / span);
-      at += (int64_t)g * span;
+      const uint32_t span = tiles_of(s.nk) + kFixed;
+      g = (int)((from - at) / span);
+      at += (uint32_t)g * span;
     }
   }
-  __device__ __noinline__ bool next(const Shared<R>& sm, const ScaledArgs& a, const Plan& p, Unit& u) {
+  __device__ __noinline__ bool next(const Shared& sm, const ScaledArgs& a, Unit& u) {
     while (at < end) {
-      const int tiles = tiles_of(s), streams = (n + p.group - 1) / p.group;
-      const int64_t lo = at > from ? at : from, stop = at + tiles, hi = stop < end ? stop : end;
-      const int block = g * p.group + (int)blockIdx.x % p.group;
-      const bool use = lo < hi && block < n;
+      const int tiles = tiles_of(s.nk);
+      const uint32_t lo = at > from ? at : from, stop = at + tiles, hi = stop < end ? stop : end;
+      const bool use = lo < hi;
       if (use) {
-        u.row_block = block;
-        u.rows = min(R, s.nq * a.num_heads - block * R);
+        u.row_block = g * C + (int)(blockIdx.x % C);
+        u.rows = max(0, min(kRows, s.nq * a.num_heads - u.row_block * kRows));
         u.tile0 = (int)(lo - at);
         u.tiles = (int)(hi - lo);
         u.q0 = s.q0;
@@ -278,39 +276,38 @@ struct Units {
         u.whole = u.tiles == tiles;
         u.stop = stop;
       }
-      if (++g < streams) at += tiles + kFixed;
+      if (++g < n) at += tiles + kFixed;
       else enter(sm, a, b + 1);
       if (use) return true;
     }
     return false;
   }
 };
-__device__ __forceinline__ int64_t out_row(const ScaledArgs& a, const Unit& u, int rows) {
-  return (int64_t)u.q0 * a.num_heads + (int64_t)u.row_block * rows;
+__device__ __forceinline__ int64_t out_row(const ScaledArgs& a, const Unit& u) {
+  return (int64_t)u.q0 * a.num_heads + (int64_t)u.row_block * kRows;
 }
 
 // ------------------------------------------------------------------ waits
-template <typename Sm>
-__device__ __noinline__ bool wait_slow(Sm& sm, uint64_t* bar, uint32_t parity, long long budget, uint32_t where) {
+template <int C>
+__device__ __noinline__ bool wait_slow(Shared& sm, uint64_t* bar, uint32_t parity, long long budget, uint32_t where) {
   const long long t0 = clock64();
   for (;;) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait_cluster(bar, parity)) return true;
     if (sm.abort_flag) return false;
     if (clock64() - t0 > budget) {
       fault(sm, VMLA_ERR_TIMEOUT, where);
-      sm.abort_flag = 1;
+      give_up<C>(sm);
       return false;
     }
   }
 }
 // Bounded wait; false once it ran out, here or in another warp.
-template <typename Sm>
-__device__ __forceinline__ bool wait(Sm& sm, uint64_t* bar, uint32_t parity, const ScaledArgs& a, uint32_t where) {
-  return mbar_try_wait(bar, parity) || wait_slow(sm, bar, parity, a.wait_cycles, where);
+template <int C>
+__device__ __forceinline__ bool wait(Shared& sm, uint64_t* bar, uint32_t parity, const ScaledArgs& a, uint32_t where) {
+  return mbar_try_wait_cluster(bar, parity) || wait_slow<C>(sm, bar, parity, a.wait_cycles, where);
 }
 
 // A barrier of the softmax warps that tells each whether `any` held in one of them.
-template <int kSoftThreads>
 __device__ __forceinline__ bool soft_vote(bool any) {
   uint32_t r;
   asm volatile(
@@ -334,178 +331,215 @@ struct Ring {
   }
 };
 
-// ------------------------------------------------------------------ loads (every lane of three warps)
-// A tile's pieces in the order of their use by the score product: chunks 0, 1, 2, the rotated columns, chunk 3; the
-// warps take them in turn, a lane the four keys 4 lane .. 4 lane + 3.
-template <int R>
-__device__ void load_role(Shared<R>& sm, const CUtensorMap* latent, const CUtensorMap* rope, const ScaledArgs& a,
-                          const Plan& plan) {
-  using S = Shape<R>;
-  const int warp = (threadIdx.x >> 5) - S::kLoadWarp, lane = threadIdx.x & 31;
+// ------------------------------------------------------------------ loads (every lane of seven warps)
+// A tile's pieces in the order of their use by the score product: chunks 0, 1, 2, the rotated columns, chunk 3.  The CTAs
+// of a lane fetch them in turn, each for all; in a CTA its warps, a lane the four keys 4 lane .. 4 lane + 3.  (An
+// instruction that starts a copy takes its thread some 50 clocks, and the lanes' go one by one: seven warps keep the copy
+// engine busy, three do not.)  Where all of a tile's slots are consecutive in groups of kRun, a box fetches each group.
+template <int C>
+__device__ void load_role(Shared& sm, const Maps& maps, const ScaledArgs& a, Units<C>& units, Unit& u, bool more) {
+  const int warp = (threadIdx.x >> 5) - kLoadWarp, lane = threadIdx.x & 31;
+  const uint32_t me = C > 1 ? cluster_ctarank() : 0;
   const int none = (int)a.pool_slots;  // outside the tensor: zeros
-  Units<R> units(sm, a, plan);
-  Unit u;
-  Ring<S::kLatentSlots> lr;
-  Ring<S::kRopeSlots> rr;
+  Ring<kLatentSlots> lr;
+  Ring<kRopeSlots> rr;
+  // the warp that sees to the next chunk, in every CTA.  A barrier's parity tells apart two rounds of its slot, no more, so
+  // a warp's chunks lie no further apart than there are slots (when it comes to one, the slot's round before the last is
+  // over, since that of its own chunk before was), and nothing waits for a slot but who fills it next (the round that it
+  // waits for cannot pass unseen); the rotated columns' slots have a warp each for the same reason
   int turn = 0;
-  while (units.next(sm, a, plan, u)) {
+  for (; more; more = units.next(sm, a, u)) {
     const int32_t* index = a.kv_indices + u.kv0;
     const int last = min(u.keys, (u.tile0 + u.tiles) * kTile);  // behind this unit's keys
-    int32_t ahead[kAhead][4];  // slots of the tiles after the one that is loaded
-    auto fetch = [&](int32_t (&v)[4], int t) {
+    int32_t ahead[4];
+    auto fetch = [&](int t) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int key = (u.tile0 + t) * kTile + 4 * lane + k;
-        v[k] = key < last ? __ldg(index + key) : -1;
+        ahead[k] = key < last ? __ldg(index + key) : -1;
       }
     };
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) fetch(ahead[k], k);
+    fetch(0);
     for (int t = 0; t < u.tiles; ++t) {
       int32_t y[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        y[k] = ahead[0][k];
+        y[k] = ahead[k];
         if (y[k] < 0 || y[k] >= none) {
           const int key = (u.tile0 + t) * kTile + 4 * lane + k;
           if (warp == 0 && key < last) fault(sm, VMLA_ERR_INDEX, (uint32_t)(u.kv0 + key));
           y[k] = none;
         }
-#pragma unroll
-        for (int j = 0; j + 1 < kAhead; ++j) ahead[j][k] = ahead[j + 1][k];
       }
-      fetch(ahead[kAhead - 1], t + kAhead);
-      // rows on their way from memory before there is room for them: those of the last tile that is known, one CTA of
-      // the lane for each tile, a row or two for each lane of each warp
-      if (kAhead > 1 && (t + (int)blockIdx.x) % plan.group == 0) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if ((k < 3 ? k : 0) == warp && ahead[kAhead - 2][k] >= 0 && ahead[kAhead - 2][k] < none)
-            prefetch_l2_bulk(a.pool + (int64_t)ahead[kAhead - 2][k] * kDqk, kDqk);
-      }
+      fetch(t + 1);
+      const int first = __shfl_sync(0xffffffffu, y[0], lane & ~3);
+      const bool runs = __all_sync(0xffffffffu, y[0] == first + 4 * (lane & 3) && y[1] == y[0] + 1 && y[2] == y[0] + 2 &&
+                                                    y[3] == y[0] + 3 && y[3] < none);
 #pragma unroll 1
-      for (int piece = 0; piece <= kChunks; ++piece) {
-        const bool mine = turn == warp;
-        turn = turn == kLoadWarps - 1 ? 0 : turn + 1;
-        if (piece != kRopePiece) {
-          if (mine) {
-            if (!wait(sm, &sm.lfree[lr.slot], lr.parity ^ 1, a, 100)) return;
-            if (lane == 0) mbar_arrive_expect_tx(&sm.lfull[lr.slot], kTile * 128);
-            tma_gather4(smem_u32(sm.latent[lr.slot]) + lane * 512, latent, (piece < kRopePiece ? piece : piece - 1) * 128, y[0],
-                        y[1], y[2], y[3], smem_u32(&sm.lfull[lr.slot]));
+      for (int piece = 0; piece < kPieces; ++piece) {
+        const bool is_rope = piece == kRopePiece;
+        const bool mine = is_rope ? warp == kLoadWarps - 1 - rr.slot : turn == warp;
+        // (pieces by turns, also where a tile has fewer of a kind than there are CTAs)
+        const bool here = C == 1 || (is_rope ? (uint32_t)rr.slot + 2 * rr.parity : (uint32_t)lr.slot) % C == me;
+        if (mine) {
+          uint64_t* full = is_rope ? &sm.rfull[rr.slot] : &sm.lfull[lr.slot];
+          uint64_t* free = is_rope ? &sm.rfree[rr.slot] : &sm.lfree[lr.slot];
+          if (!__all_sync(0xffffffffu, wait<C>(sm, free, (is_rope ? rr.parity : lr.parity) ^ 1, a, 100))) return;
+          if (lane == 0) mbar_arrive_expect_tx(full, is_rope ? kTile * 64 : kTile * 128);
+          __syncwarp();
+          if (here) {
+            const uint32_t bar = smem_u32(full), dst = is_rope ? smem_u32(sm.rope[rr.slot]) : smem_u32(sm.latent[lr.slot]);
+            const int x = is_rope ? kDv : (piece < kRopePiece ? piece : piece - 1) * 128, row = is_rope ? 64 : 128;
+            if (runs) {
+              if ((lane & 3) == 0)
+                load_box<C>(dst + lane * 4 * row, is_rope ? &maps.rope_run : &maps.latent_run, x, y[0], bar);
+            } else {
+              load_gather<C>(dst + lane * 4 * row, is_rope ? &maps.rope : &maps.latent, x, y[0], y[1], y[2], y[3], bar);
+            }
           }
-          lr.step();
-        } else {
-          if (mine) {
-            if (!wait(sm, &sm.rfree[rr.slot], rr.parity ^ 1, a, 101)) return;
-            if (lane == 0) mbar_arrive_expect_tx(&sm.rfull[rr.slot], kTile * 64);
-            tma_gather4(smem_u32(sm.rope[rr.slot]) + lane * 256, rope, kDv, y[0], y[1], y[2], y[3],
-                        smem_u32(&sm.rfull[rr.slot]));
-          }
+        }
+        if (is_rope) {
           rr.step();
+        } else {
+          lr.step();
+          turn = turn == kLoadWarps - 1 ? 0 : turn + 1;
         }
       }
     }
   }
+  // the slots' last releases, which come from every CTA of the lane, have arrived before this CTA may leave: each is
+  // waited for by who filled the slot last
+  for (int k = 0; k < kLatentSlots; ++k) {
+    if ((turn + k + kLoadWarps * 2 - kLatentSlots) % kLoadWarps == warp) wait<C>(sm, &sm.lfree[lr.slot], lr.parity ^ 1, a, 101);
+    lr.step();
+  }
+  for (int k = 0; k < kRopeSlots; ++k) {
+    if (warp == kLoadWarps - 1 - rr.slot) wait<C>(sm, &sm.rfree[rr.slot], rr.parity ^ 1, a, 102);
+    rr.step();
+  }
+  __syncwarp();
 }
 
-// ------------------------------------------------------------------ matrix products (one thread)
-// Two sequences of products: scores, piece by piece, and values, chunk by chunk.  Whatever is ready goes next, scores
-// first: they keep the softmax busy, and only values make room for further loads.
-template <int R>
-__device__ void mma_role(Shared<R>& sm, const ScaledArgs& a, const Plan& plan, uint32_t tmem) {
-  using S = Shape<R>;
-  constexpr uint32_t kScores = idesc_f8_f32(kTile, 2 * R, 0, 0, 0, 0);
-  constexpr uint32_t kValues = idesc_f8_f32(128, S::kOCols, 0, 1, 1, 1);
-  Units<R> q_units(sm, a, plan), v_units(sm, a, plan);
-  Unit qu, vu;
-  bool q_more = q_units.next(sm, a, plan, qu), v_more = v_units.next(sm, a, plan, vu);
-  Ring<S::kLatentSlots> ql, vl;
-  Ring<S::kRopeSlots> qr;
-  int q_it = 0, v_it = 0, q_tile = 0, v_tile = 0, q_unit = 0, v_unit = 0, piece = 0, chunk = 0;
+// ------------------------------------------------------------------ matrix products (one warp)
+// Two sequences of products: scores, piece by piece as a tile's columns arrive, and values, a tile at a time.  Whatever
+// is ready goes next, scores first: they keep the softmax busy, and only values make room for further loads.  What lies
+// between two products is short: a look at a barrier and the bookkeeping take as long as ten of them.
+template <int C>
+__device__ void mma_role(Shared& sm, const ScaledArgs& a, uint32_t tmem, const Units<C>& units, const Unit& first,
+                         bool more) {
+  constexpr uint32_t kScores = idesc_f8_f32(kTile, 2 * kRows, 0, 0, 0, 0);
+  constexpr uint32_t kValues = idesc_f8_f32(128, kOCols, 0, 1, 1, 1);
+  Units<C> q_units = units, v_units = units;
+  Unit u = first;
+  bool q_more = more, v_more = more;
+  int q_tiles = u.tiles, v_tiles = u.tiles;  // left of the unit
+  bool q_first = true, v_first = true;       // no tile of the unit yet
+  Ring<kLatentSlots> ql, vl;
+  Ring<kRopeSlots> qr;
+  // lower words of the descriptors at the first slot, and the upper words, which depend on the layout alone
+  constexpr uint32_t kHi128 = (uint32_t)(smem_desc_fixed(16, 1024, 2) >> 32), kHi64 = (uint32_t)(smem_desc_fixed(16, 512, 4) >> 32);
+  constexpr uint32_t kLo = (uint32_t)smem_desc_fixed(16, 0, 0);
+  auto low = [&](const void* at) { return smem_u32(at) >> 4 | kLo; };
+  const uint32_t latent_lo = low(sm.latent[0]), rope_lo = low(sm.rope[0]), q_latent_lo = low(sm.q_latent[0]),
+                 q_rope_lo = low(sm.q_rope), p_lo = low(sm.p[0]);
+  uint32_t q_it = 0, v_it = 0, q_unit = 0, v_unit = 0;
+  int piece = 0;
+  auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait_cluster(bar, parity)) != 0; };
   auto scores = [&]() -> bool {
-    const int sb = q_it & 1;
-    if (piece == 0 && ((q_tile == 0 && !mbar_test_wait(&sm.qfull, q_unit & 1)) ||
-                       !mbar_test_wait(&sm.sfree[sb], ((q_it >> 1) & 1) ^ 1)))
+    const uint32_t sb = q_it & 1;
+    if (piece == 0 && ((q_first && !ready(&sm.qfull, q_unit & 1)) || !ready(&sm.sfree[sb], ((q_it >> 1) & 1) ^ 1)))
       return false;
-    const uint32_t d = tmem + S::kSCol + (uint32_t)sb * 2 * R;
-    if (piece == kRopePiece) {
-      if (!mbar_test_wait(&sm.rfull[qr.slot], qr.parity)) return false;
-      tc_fence_after();
-      const uint32_t k = smem_u32(sm.rope[qr.slot]), q = smem_u32(sm.q_rope);
+    const uint32_t d = tmem + kSCol + sb * 2 * kRows;
+    const int begun = piece;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        mma_ss_f8(d, smem_desc(k + 32 * i, 16, 512, 4), smem_desc(q + 32 * i, 16, 512, 4), kScores, 1u);
-      mma_commit(&sm.rfree[qr.slot]);
-      qr.step();
-    } else {
-      if (!mbar_test_wait(&sm.lfull[ql.slot], ql.parity)) return false;
-      tc_fence_after();
-      const uint32_t k = smem_u32(sm.latent[ql.slot]),
-                     q = smem_u32(sm.q_latent[piece < kRopePiece ? piece : piece - 1]);
+    for (int k = 0; k <= kChunks; ++k) {
+      if (k != piece) continue;
+      if (k == kRopePiece) {
+        if (!ready(&sm.rfull[qr.slot], qr.parity)) break;
+        tc_fence_after();
+        const uint32_t key = rope_lo + qr.slot * (kTile * 64 / 16);
+        if (elect_one()) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        mma_ss_f8(d, smem_desc(k + 32 * i, 16, 1024), smem_desc(q + 32 * i, 16, 1024), kScores, piece > 0 || i > 0);
-      ql.step();
+          for (int i = 0; i < 2; ++i) mma_ss_f8(d, key + 2 * i, kHi64, q_rope_lo + 2 * i, kHi64, kScores, 1u);
+          commit<C>(&sm.rfree[qr.slot]);
+        }
+        qr.step();
+      } else {
+        if (!ready(&sm.lfull[ql.slot], ql.parity)) break;
+        tc_fence_after();
+        const uint32_t key = latent_lo + ql.slot * (kTile * 128 / 16),
+                       q = q_latent_lo + (k < kRopePiece ? k : k - 1) * (2 * kRows * 128 / 16);
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mma_ss_f8(d, key + 2 * i, kHi128, q + 2 * i, kHi128, kScores, k > 0 || i > 0);
+          if (k == kChunks) mma_commit(&sm.sfull[sb]);
+        }
+        ql.step();
+      }
+      __syncwarp();
+      piece = k + 1;
     }
-    if (++piece > kChunks) {
-      mma_commit(&sm.sfull[sb]);
+    if (piece == begun) return false;
+    if (piece > kChunks) {
       piece = 0;
       ++q_it;
-      if (++q_tile == qu.tiles) {
-        q_tile = 0;
+      q_first = false;
+      if (--q_tiles == 0) {
         ++q_unit;
-        q_more = q_units.next(sm, a, plan, qu);
+        q_first = true;
+        q_more = q_units.next(sm, a, u);
+        q_tiles = u.tiles;
       }
     }
     return true;
   };
   auto values = [&]() -> bool {
-    if (chunk == 0 && (!mbar_test_wait(&sm.pfull, v_it & 1) ||
-                       (v_tile == 0 && !mbar_test_wait(&sm.ofree, (v_unit & 1) ^ 1))))  // the unit before is read out
-      return false;
+    // (the first product into O: the unit before has been read out)
+    const uint32_t pb = v_it % kPSlots;
+    if (!ready(&sm.pfull[pb], (v_it / kPSlots) & 1) || (v_first && !ready(&sm.ofree, (v_unit & 1) ^ 1))) return false;
     tc_fence_after();
-    const uint32_t v = smem_u32(sm.latent[vl.slot]), p = smem_u32(sm.p), d = tmem + chunk * S::kOCols;
+    const uint32_t go_on = v_first ? 0u : 1u, p = p_lo + pb * (kTile * 128 / 16);
 #pragma unroll
-    for (int i = 0; i < kTile / 32; ++i) {
-      const uint64_t vd = smem_desc(v + 4096 * i, 16, 1024);
-      if constexpr (S::kWide) {
-        mma_ss_f8(d, vd, smem_desc(p + 4096 * i, 16, 1024), kValues, v_tile > 0 || i > 0);
-      } else {
+    for (int c = 0; c < kChunks; ++c) {
+      const uint32_t v = latent_lo + vl.slot * (kTile * 128 / 16), d = tmem + c * kOCols;
+      if (elect_one()) {
 #pragma unroll
-        for (int part = 0; part < kParts; ++part)
-          mma_ss_f8(d, vd, smem_desc(p + part * kTile * 64 + 2048 * i, 16, 512, 4), kValues,
-                    v_tile > 0 || i > 0 || part > 0);
+        for (int i = 0; i < kTile / 32; ++i)
+          mma_ss_f8(d, v + 256 * i, kHi128, p + 256 * i, kHi128, kValues, i > 0 ? 1u : go_on);
+        commit<C>(&sm.lfree[vl.slot]);
+        if (c == kChunks - 1) mma_commit(&sm.pfree[pb]);
       }
+      __syncwarp();
+      vl.step();
     }
-    mma_commit(&sm.lfree[vl.slot]);
-    vl.step();
-    if (++chunk == kChunks) {
-      mma_commit(&sm.pfree);
-      chunk = 0;
-      ++v_it;
-      if (++v_tile == vu.tiles) {
-        v_tile = 0;
-        ++v_unit;
-        v_more = v_units.next(sm, a, plan, vu);
-      }
+    ++v_it;
+    v_first = false;
+    if (--v_tiles == 0) {
+      ++v_unit;
+      v_first = true;
+      v_more = v_units.next(sm, a, u);
+      v_tiles = u.tiles;
     }
     return true;
   };
-  long long t0 = clock64();
+  int idle = 0;
+  long long t0 = 0;
   while (q_more || v_more) {
-    if ((q_more && scores()) || (v_more && values())) {
-      t0 = clock64();
-      continue;
-    }
-    if (sm.abort_flag) break;
-    if (clock64() - t0 > a.wait_cycles) {
-      fault(sm, VMLA_ERR_TIMEOUT, 200);
-      sm.abort_flag = 1;
+    if (q_more && scores()) idle = 0;
+    if (v_more && values()) idle = 0;
+    if (++idle < 256) continue;
+    if (idle == 256) t0 = clock64();
+    if (__any_sync(0xffffffffu, sm.abort_flag != 0)) break;
+    if (__any_sync(0xffffffffu, clock64() - t0 > a.wait_cycles)) {
+      if (elect_one()) fault(sm, VMLA_ERR_TIMEOUT, 200);
+      give_up<C>(sm);
+      __syncwarp();
     }
   }
   // everything issued is complete, and its signals have arrived, before the CTA leaves
-  mma_commit(&sm.done);
+  if (elect_one()) mma_commit(&sm.done);
+  __syncwarp();
   t0 = clock64();
   while (!mbar_try_wait(&sm.done, 0) && clock64() - t0 < a.wait_cycles) {
   }
@@ -514,19 +548,17 @@ __device__ void mma_role(Shared<R>& sm, const ScaledArgs& a, const Plan& plan, u
 // ------------------------------------------------------------------ queries (softmax warps)
 // The unit's rows into shared memory in two e4m3 parts, their masks; the factor that makes a score of a product.
 // (What runs once per unit is kept in loops: straight-line code that is run once costs more in fetching it.)
-template <int R>
-__device__ __noinline__ float load_queries(Shared<R>& sm, const ScaledArgs& a, const Unit& u) {
-  using S = Shape<R>;
+__device__ __noinline__ float load_queries(Shared& sm, const ScaledArgs& a, const Unit& u) {
   constexpr int kGranules = kDqk / 8;                      // of 8 bf16
-  constexpr int kEach = R * kGranules / S::kSoftThreads;   // 9 per thread
-  static_assert(R * kGranules % S::kSoftThreads == 0, "granules per thread");
+  constexpr int kEach = kRows * kGranules / kSoftThreads;   // 9 per thread
+  static_assert(kRows * kGranules % kSoftThreads == 0, "granules per thread");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint4* src = reinterpret_cast<const uint4*>(a.q + out_row(a, u, R) * kDqk);
+  const uint4* src = reinterpret_cast<const uint4*>(a.q + out_row(a, u) * kDqk);
   uint4 v[kEach];
   const int valid = u.rows * kGranules;
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
-    const int i = tid + k * S::kSoftThreads;
+    const int i = tid + k * kSoftThreads;
     v[k] = i < valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
   }
   if (a.parent && tid < u.nq) sm.parent[tid] = a.parent[u.q0 + tid];
@@ -542,8 +574,8 @@ __device__ __noinline__ float load_queries(Shared<R>& sm, const ScaledArgs& a, c
   }
   m = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xFFFFu));
   if (lane == 0) sm.q_max[warp] = __uint_as_float(m << 16);
-  named_bar_sync(1, S::kSoftThreads);
-  float top = lane < S::kSoftWarps ? sm.q_max[lane] : 0.f;
+  named_bar_sync(1, kSoftThreads);
+  float top = lane < kSoftWarps ? sm.q_max[lane] : 0.f;
   top = warp_max(top);
   // a: 448 = 1.75 x 2^8; queries below 2^-100 are zero to any score
   const uint32_t bits = __float_as_uint(top);
@@ -552,7 +584,7 @@ __device__ __noinline__ float load_queries(Shared<R>& sm, const ScaledArgs& a, c
   const float scale = __uint_as_float((uint32_t)(e + 127) << 23), back = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll 1
   for (int k = 0; k < kEach; ++k) {
-    const int i = tid + k * S::kSoftThreads, row = i / kGranules, col = (i - row * kGranules) * 8;
+    const int i = tid + k * kSoftThreads, row = i / kGranules, col = (i - row * kGranules) * 8;
     const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
     for (int j = 0; j + 1 < kEach; ++j) v[j] = v[j + 1];
@@ -572,17 +604,17 @@ __device__ __noinline__ float load_queries(Shared<R>& sm, const ScaledArgs& a, c
       hi[j >> 1] |= (uint32_t)h << (16 * (j & 1));
       lo[j >> 1] |= (uint32_t)l << (16 * (j & 1));
     }
-    // (rows r and R + r have the same swizzle: R is a multiple of 8)
+    // (rows r and kRows + r have the same swizzle)
     uint8_t* dst = col < kDv ? sm.q_latent[col >> 7] + row * 128 + ((((col & 127) >> 4) ^ (row & 7)) << 4)
                              : sm.q_rope + row * 64 + ((((col - kDv) >> 4) ^ ((row >> 1) & 3)) << 4);
     dst += col & 8;
     *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-    *reinterpret_cast<uint2*>(dst + R * (col < kDv ? 128 : 64)) = make_uint2(lo[0], lo[1]);
+    *reinterpret_cast<uint2*>(dst + kRows * (col < kDv ? 128 : 64)) = make_uint2(lo[0], lo[1]);
   }
-  if (tid < R) {
+  if (tid < kRows) {
     uint64_t word = 0;
     if (tid < u.rows) {
-      const int i = (u.row_block * R + tid) / a.num_heads;
+      const int i = (u.row_block * kRows + tid) / a.num_heads;
       if (a.masks) {
         word = a.masks[u.q0 + i];
       } else if (a.parent) {
@@ -605,7 +637,7 @@ __device__ __noinline__ float load_queries(Shared<R>& sm, const ScaledArgs& a, c
     sm.m[tid] = kNone;
   }
   fence_proxy_async_smem();
-  named_bar_sync(1, S::kSoftThreads);
+  named_bar_sync(1, kSoftThreads);
   if (lane == 0 && a.test_fault != kFaultNoQReady) mbar_arrive(&sm.qfull);
   return a.sm_scale * 1.4426950408889634f * back;
 }
@@ -635,18 +667,15 @@ __device__ __forceinline__ float reduce16(const float (&v)[16], int lane, Op op)
   return op(d, __shfl_xor_sync(0xffffffffu, d, 1));
 }
 
-template <int R>
-__device__ void softmax_role(Shared<R>& sm, const ScaledArgs& a, const Plan& plan, uint32_t tmem, const Partials& part) {
-  using S = Shape<R>;
+template <int C>
+__device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, uint32_t tmem, const Partials& part,
+                             Units<C>& units, Unit& u, bool more) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int quarter = warp & 3, row0 = (warp >> 2) * kPerThread;  // its 32 keys of a tile; its first of 16 rows
   const int my_key = quarter * 32 + lane;
   const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-  auto sync = [] { named_bar_sync(1, S::kSoftThreads); };
-  Units<R> units(sm, a, plan);
-  Unit u;
+  auto sync = [] { named_bar_sync(1, kSoftThreads); };
   int it = 0;
-  bool more = units.next(sm, a, plan, u);
   float factor = more ? load_queries(sm, a, u) : 0.f;
   while (more) {
     float l[kPerThread];
@@ -675,9 +704,9 @@ __device__ void softmax_role(Shared<R>& sm, const ScaledArgs& a, const Plan& pla
       }
       const bool all_seen = __all_sync(0xffffffffu, seen == 0xFFFFu);
       const float c = scale * factor, held = fmaxf(scale, kTiny) * kUnit;
-      wait(sm, &sm.sfull[sb], (it >> 1) & 1, a, 300);  // (should it run out, the vote below ends the work)
+      wait<C>(sm, &sm.sfull[sb], (it >> 1) & 1, a, 300);  // (should it run out, the vote below ends the work)
       __syncwarp();
-      const uint32_t col = tmem + lanes + S::kSCol + (uint32_t)(sb * 2 * R + row0);
+      const uint32_t col = tmem + lanes + kSCol + (uint32_t)(sb * 2 * kRows + row0);
       float w[kPerThread];
       for (;;) {
         tc_fence_after();
@@ -685,7 +714,7 @@ __device__ void softmax_role(Shared<R>& sm, const ScaledArgs& a, const Plan& pla
         {
           uint32_t hi[kPerThread], lo[kPerThread];
           tmem_ld16(col, hi);
-          tmem_ld16(col + R, lo);
+          tmem_ld16(col + kRows, lo);
           tmem_wait_ld();
 #pragma unroll
           for (int r = 0; r < kPerThread; r += 4) {
@@ -704,13 +733,13 @@ __device__ void softmax_role(Shared<R>& sm, const ScaledArgs& a, const Plan& pla
         }
 #pragma unroll
         for (int r = 0; r < kPerThread; ++r) most = fmaxf(most, w[r]);
-        if (!soft_vote<S::kSoftThreads>(most > kMost || sm.abort_flag != 0)) break;
+        if (!soft_vote(most > kMost || sm.abort_flag != 0)) break;
         // some weight is too large for its row's reference: raise the references to the tile's largest
         if (tid == 0) sm.stop = sm.abort_flag;
         {
           uint32_t hi[kPerThread], lo[kPerThread];
           tmem_ld16(col, hi);
-          tmem_ld16(col + R, lo);
+          tmem_ld16(col + kRows, lo);
           tmem_wait_ld();
           const float height = __log2f(fmaxf(scale, kTiny));
           float top[kPerThread];
@@ -724,7 +753,7 @@ __device__ void softmax_role(Shared<R>& sm, const ScaledArgs& a, const Plan& pla
         }
         sync();
         if (sm.stop) return;
-        if (tid < R) {
+        if (tid < kRows) {
           const float old = sm.m[tid];
           const float top = fmaxf(fmaxf(fmaxf(sm.part[0][tid], sm.part[1][tid]), fmaxf(sm.part[2][tid], sm.part[3][tid])), old);
           sm.f[tid] = ex2_approx(old - top);
@@ -739,12 +768,12 @@ __device__ void softmax_role(Shared<R>& sm, const ScaledArgs& a, const Plan& pla
         }
         if (t > 0) {
           // what has been summed so far, once the products before are complete
-          wait(sm, &sm.pfree, (it & 1) ^ 1, a, 301);
+          wait<C>(sm, &sm.pfree[(it - 1) % kPSlots], ((it - 1) / kPSlots) & 1, a, 301);
           __syncwarp();
           tc_fence_after();
 #pragma unroll 1
-          for (int k = 0; k < (int)S::kSCol / R; ++k) {
-            const uint32_t at = tmem + lanes + (uint32_t)(k * R + row0);
+          for (int k = 0; k < (int)kSCol / kRows; ++k) {
+            const uint32_t at = tmem + lanes + (uint32_t)(k * kRows + row0);
             uint32_t o[kPerThread];
             tmem_ld16(at, o);
             tmem_wait_ld();
@@ -782,66 +811,60 @@ __device__ void softmax_role(Shared<R>& sm, const ScaledArgs& a, const Plan& pla
 #pragma unroll
         for (int q = 0; q < kParts; ++q) parts[q][k] = __byte_perm(h[0][q], h[1][q], 0x7531);
       }
-      if (wait(sm, &sm.pfree, (it & 1) ^ 1, a, 302)) {
+      const int pb = it % kPSlots;
+      if (wait<C>(sm, &sm.pfree[pb], ((it / kPSlots) & 1) ^ 1, a, 302)) {
 #pragma unroll
         for (int q = 0; q < kParts; ++q) {
-          uint8_t* dst = S::kWide ? sm.p + my_key * 128 + (((2 * q + (row0 >> 4)) ^ (my_key & 7)) << 4)
-                                  : sm.p + (q * kTile + my_key) * 64 + (((row0 >> 4) ^ ((my_key >> 1) & 3)) << 4);
+          uint8_t* dst = sm.p[pb] + my_key * 128 + (((2 * q + (row0 >> 4)) ^ (my_key & 7)) << 4);
           *reinterpret_cast<uint4*>(dst) = make_uint4(parts[q][0], parts[q][1], parts[q][2], parts[q][3]);
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.pfull);
+      if (lane == 0) mbar_arrive(&sm.pfull[pb]);
       scale = next_scale;
     }
     // row sums over the keys; what the rows' results are scaled by
     const float sum = reduce16(l, lane, [](float x, float y) { return x + y; });
     sm.part[quarter][row0 + (lane >> 1)] = sum;
     sync();
-    const int64_t piece = (int64_t)blockIdx.x * 2 + (u.head ? 1 : 0), first_row = out_row(a, u, R);
-    if (tid < R) {
+    const int64_t piece = (int64_t)blockIdx.x * 2 + (u.head ? 1 : 0), first_row = out_row(a, u);
+    if (tid < kRows) {
       const float total = (sm.part[0][tid] + sm.part[1][tid]) + (sm.part[2][tid] + sm.part[3][tid]), m = sm.m[tid];
       sm.f[tid] = !u.whole ? 1.f : total > 0.f ? 1.f / (total * kUnit) : 0.f;
-      if (!u.whole) part.ml[piece * R + tid] = make_float2(m, total);
+      if (!u.whole) part.ml[piece * kRows + tid] = make_float2(m, total);
       else if (tid < u.rows) a.lse[first_row + tid] = total > 0.f ? (m + log2f(total)) * 0.6931471805599453f : -INFINITY;
     }
     if (tid == 0 && u.head && !u.whole) {
-      sm.cut_pieces = (int)((u.stop - 1) / plan.share) - (int)blockIdx.x / plan.group + 1;
+      sm.cut_pieces = (int)((u.stop - 1) / plan.share) - (int)(blockIdx.x / C) + 1;
       sm.cut_rows = u.rows;
       sm.cut_row = first_row;
     }
     sync();
-    float* po = part.o + piece * R * kDv;
+    float* po = part.o + piece * kRows * kDv;
     uint16_t* out = u.whole ? a.out + first_row * kDv : nullptr;
     const int rows = u.rows;
     // the next unit's queries while this one's last products run
-    more = units.next(sm, a, plan, u);
+    more = units.next(sm, a, u);
     if (more) factor = load_queries(sm, a, u);
-    wait(sm, &sm.pfree, (it - 1) & 1, a, 303);
+    wait<C>(sm, &sm.pfree[(it - 1) % kPSlots], ((it - 1) / kPSlots) & 1, a, 303);
     __syncwarp();
     tc_fence_after();
 #pragma unroll 1
     for (int k = 0; k < kChunks * kPerThread / 8; ++k) {
       const int chunk = k >> 1, r0 = row0 + 8 * (k & 1);
       const int dim = 128 * chunk + my_key;  // this thread's lane of O^T
-      const uint32_t at = tmem + lanes + (uint32_t)(chunk * S::kOCols + r0);
+      const uint32_t at = tmem + lanes + (uint32_t)(chunk * kOCols + r0);
       float o[8];
       {
         uint32_t x[8];
         tmem_ld8(at, x);
-        if constexpr (S::kWide) {
-          uint32_t y[8], z[8];
-          tmem_ld8(at + R, y);
-          tmem_ld8(at + 2 * R, z);
-          tmem_wait_ld();
+        uint32_t y[8], z[8];
+        tmem_ld8(at + kRows, y);
+        tmem_ld8(at + 2 * kRows, z);
+        tmem_wait_ld();
 #pragma unroll
-          for (int r = 0; r < 8; ++r) o[r] = (__uint_as_float(x[r]) + __uint_as_float(y[r])) + __uint_as_float(z[r]);
-        } else {
-          tmem_wait_ld();
-#pragma unroll
-          for (int r = 0; r < 8; ++r) o[r] = __uint_as_float(x[r]);
-        }
+        for (int r = 0; r < 8; ++r) o[r] = (__uint_as_float(x[r]) + __uint_as_float(y[r])) + __uint_as_float(z[r]);
       }
       if (out) {
         // pairs of lanes exchange a value each, so that a lane stores two columns of one row
@@ -864,63 +887,79 @@ __device__ void softmax_role(Shared<R>& sm, const ScaledArgs& a, const Plan& pla
   }
 }
 
-template <int R>
-__global__ void __launch_bounds__(Shape<R>::kThreads, 1)
-scaled_kernel(const __grid_constant__ CUtensorMap latent, const __grid_constant__ CUtensorMap rope,
-              const __grid_constant__ ScaledArgs a, CtaInfo* __restrict__ info, const Partials part) {
-  using S = Shape<R>;
+template <int C>
+__global__ void __launch_bounds__(kThreads, 1)
+scaled_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ScaledArgs a, CtaInfo* __restrict__ info,
+              const Partials part) {
   extern __shared__ uint8_t raw[];
-  Shared<R>& sm = *reinterpret_cast<Shared<R>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  Shared& sm = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5;
-  if (warp == S::kMmaWarp) {
+  if (warp == kMmaWarp) {
     tmem_alloc(&sm.tmem, 512);
     tmem_relinquish();
   }
   if (tid == 0) {
-    for (int s = 0; s < S::kLatentSlots; ++s) {
+    for (int s = 0; s < kLatentSlots; ++s) {
       mbar_init(&sm.lfull[s], 1);
-      mbar_init(&sm.lfree[s], 1);
+      mbar_init(&sm.lfree[s], C);  // every CTA of the lane has used it
     }
-    for (int s = 0; s < S::kRopeSlots; ++s) {
+    for (int s = 0; s < kRopeSlots; ++s) {
       mbar_init(&sm.rfull[s], 1);
-      mbar_init(&sm.rfree[s], 1);
+      mbar_init(&sm.rfree[s], C);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.sfull[s], 1);
-      mbar_init(&sm.sfree[s], S::kSoftWarps);
+      mbar_init(&sm.sfree[s], kSoftWarps);
     }
-    mbar_init(&sm.pfull, S::kSoftWarps);
-    mbar_init(&sm.pfree, 1);
-    mbar_init(&sm.qfull, S::kSoftWarps);
-    mbar_init(&sm.ofree, S::kSoftWarps);
+    for (int s = 0; s < kPSlots; ++s) {
+      mbar_init(&sm.pfull[s], kSoftWarps);
+      mbar_init(&sm.pfree[s], 1);
+    }
+    mbar_init(&sm.qfull, kSoftWarps);
+    mbar_init(&sm.ofree, kSoftWarps);
     mbar_init(&sm.done, 1);
     sm.abort_flag = 0;
     sm.fault[0] = sm.fault[1] = 0;
     sm.cut_pieces = 0;
     fence_mbar_init();
-    prefetch_tensormap(&latent);
-    prefetch_tensormap(&rope);
+    prefetch_tensormap(&maps.latent);
+    prefetch_tensormap(&maps.rope);
+    prefetch_tensormap(&maps.latent_run);
+    prefetch_tensormap(&maps.rope_run);
   }
   __syncwarp();
   Plan plan;
-  const bool ok = make_plan(sm, a, plan);
+  const bool ok = make_plan<C>(sm, a, plan);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (C > 1) {  // no copy or signal goes to a CTA whose barriers are not ready
+    cluster_arrive();
+    cluster_wait();
+  }
   const uint32_t tmem = sm.tmem;
   if (ok) {
-    if (warp < S::kSoftWarps) {
-      softmax_role(sm, a, plan, tmem, part);
-    } else if (warp == S::kMmaWarp) {
-      if ((tid & 31) == 0) mma_role(sm, a, plan, tmem);
+    // the CTA's first unit, which every role begins with
+    Units<C> units(sm, a, plan);
+    Unit u;
+    const bool more = units.next(sm, a, u);
+    if (warp < kSoftWarps) {
+      softmax_role<C>(sm, a, plan, tmem, part, units, u, more);
+    } else if (warp == kMmaWarp) {
+      mma_role<C>(sm, a, tmem, units, u, more);
     } else {
-      load_role(sm, &latent, &rope, a, plan);
+      load_role<C>(sm, maps, a, units, u, more);
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   grid_dependents_launch();
+  if (C > 1) {  // nor leaves a CTA while another may still signal to it
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+  }
   if (sm.abort_flag) {
     // a wait ran out: loads, commits and products issued before may still be on their way into this CTA's memories,
     // each for microseconds; half a millisecond of the global timer (at most 2^26 reads of it)
@@ -935,7 +974,7 @@ scaled_kernel(const __grid_constant__ CUtensorMap latent, const __grid_constant_
     __syncthreads();
   }
   __syncwarp();
-  if (warp == S::kMmaWarp) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -947,7 +986,7 @@ scaled_kernel(const __grid_constant__ CUtensorMap latent, const __grid_constant_
       mine.pieces = sm.cut_pieces;
       mine.rows = sm.cut_rows;
       mine.row = sm.cut_row;
-      mine.group = plan.group;
+      mine.group = C;
     }
     info[blockIdx.x] = mine;
   }
@@ -956,7 +995,6 @@ scaled_kernel(const __grid_constant__ CUtensorMap latent, const __grid_constant_
 // Joins the partials of one row of a cut stream: one block per (CTA that begins the stream, row).
 constexpr int kJoinThreads = kDv / 4;
 constexpr int kMaxCtas = 512;
-template <int R>
 __global__ void __launch_bounds__(kJoinThreads)
 scaled_join_kernel(const CtaInfo* __restrict__ info, int ctas, const Partials part, uint16_t* __restrict__ out,
                    float* __restrict__ lse, uint32_t* __restrict__ status) {
@@ -978,7 +1016,7 @@ scaled_join_kernel(const CtaInfo* __restrict__ info, int ctas, const Partials pa
   if (row >= i.rows || i.pieces == 0) return;
   // piece 0 lies in this CTA's second slot, piece k in the first slot of the CTA k lanes on
   auto slot = [&](int k) { return k == 0 ? (int64_t)cta * 2 + 1 : ((int64_t)cta + (int64_t)k * i.group) * 2; };
-  for (int k = tid; k < i.pieces; k += kJoinThreads) ml[k] = part.ml[slot(k) * R + row];
+  for (int k = tid; k < i.pieces; k += kJoinThreads) ml[k] = part.ml[slot(k) * kRows + row];
   __syncthreads();
   float top = kNone;
   for (int k = 0; k < i.pieces; ++k) top = fmaxf(top, ml[k].x);
@@ -987,7 +1025,7 @@ scaled_join_kernel(const CtaInfo* __restrict__ info, int ctas, const Partials pa
 #pragma unroll 4
   for (int k = 0; k < i.pieces; ++k) {
     const float w = ex2_approx(ml[k].x - top);
-    const float4 v = reinterpret_cast<const float4*>(part.o + (slot(k) * R + row) * kDv)[tid];
+    const float4 v = reinterpret_cast<const float4*>(part.o + (slot(k) * kRows + row) * kDv)[tid];
     sum = fmaf(ml[k].y, w, sum);
     o.x = fmaf(v.x, w, o.x);
     o.y = fmaf(v.y, w, o.y);
@@ -1003,7 +1041,7 @@ scaled_join_kernel(const CtaInfo* __restrict__ info, int ctas, const Partials pa
 // Workspace: status words, the CTAs' infos, the partials.
 constexpr size_t kInfoOff = 256;
 size_t ml_off(int sms) { return kInfoOff + (((size_t)sms * sizeof(CtaInfo) + 255) & ~(size_t)255); }
-size_t o_off(int sms) { return ml_off(sms) + (size_t)sms * 2 * kMaxRows * sizeof(float2); }
+size_t o_off(int sms) { return ml_off(sms) + (size_t)sms * 2 * kRows * sizeof(float2); }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -1021,47 +1059,78 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// The pool as rows of bytes, boxes one row high and `width` bytes wide for gathers of four rows.
-bool encode_pool(EncodeTiledFn enc, CUtensorMap* map, const uint8_t* pool, int64_t slots, uint32_t width,
+// The pool as rows of bytes: boxes `width` bytes wide, one row high for gathers of four rows, or kRun.
+bool encode_pool(EncodeTiledFn enc, CUtensorMap* map, const uint8_t* pool, int64_t slots, uint32_t width, uint32_t rows,
                  CUtensorMapSwizzle swizzle) {
   cuuint64_t gdim[2] = {(cuuint64_t)kDqk, (cuuint64_t)(slots > 0 ? slots : 1)};
   cuuint64_t gstride[1] = {(cuuint64_t)kDqk};
-  cuuint32_t box[2] = {width, 1};
+  cuuint32_t box[2] = {width, rows};
   cuuint32_t estride[2] = {1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(pool), gdim, gstride, box, estride,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int R>
-int launch(const ScaledArgs& a, int sms, const CUtensorMap& latent, const CUtensorMap& rope, cudaStream_t stream) {
+template <int C>
+cudaLaunchConfig_t kernel_config(int ctas, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSharedBytes;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Lanes that are resident together on the current device (a GPC's last SMs may not fill one).
+template <int C>
+int max_lanes(int sms, int* lanes) {
   static std::mutex mu;
-  static bool ready[64] = {};
+  static int known[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return VMLA_ERR_CUDA;
-  {
-    std::lock_guard<std::mutex> g(mu);
-    if (dev >= 64 || !ready[dev]) {
-      if (cudaFuncSetAttribute(scaled_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSharedBytes<R>) !=
-          cudaSuccess)
-        return VMLA_ERR_CUDA;
-      if (dev < 64) ready[dev] = true;
+  std::lock_guard<std::mutex> g(mu);
+  if (dev >= 64 || known[dev] == 0) {
+    if (cudaFuncSetAttribute(scaled_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSharedBytes) !=
+        cudaSuccess)
+      return VMLA_ERR_CUDA;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = kernel_config<C>(C, attr);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, scaled_kernel<C>, &cfg) != cudaSuccess || n < 1) return VMLA_ERR_CUDA;
+    n = n < sms / C ? n : sms / C;
+    if (dev >= 64) {
+      *lanes = n;
+      return VMLA_OK;
     }
+    known[dev] = n;
   }
+  *lanes = known[dev];
+  return VMLA_OK;
+}
+
+template <int C>
+int launch(const ScaledArgs& a, int sms, const Maps& maps, cudaStream_t stream) {
+  int lanes = 0;
+  const int rc = max_lanes<C>(sms, &lanes);
+  if (rc != VMLA_OK) return rc;
   CtaInfo* info = reinterpret_cast<CtaInfo*>(a.workspace + kInfoOff);
   Partials part;
   part.ml = reinterpret_cast<float2*>(a.workspace + ml_off(sms));
   part.o = reinterpret_cast<float*>(a.workspace + o_off(sms));
-  scaled_kernel<R><<<sms, Shape<R>::kThreads, kSharedBytes<R>, stream>>>(latent, rope, a, info, part);
-  if (cudaGetLastError() != cudaSuccess) return VMLA_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1] = {early_start_attribute()};
-  cfg.gridDim = dim3((unsigned)sms, R, 1);
-  cfg.blockDim = dim3(kJoinThreads, 1, 1);
+  const int ctas = lanes * C;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = kernel_config<C>(ctas, attr);
   cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, scaled_join_kernel<R>, (const CtaInfo*)info, sms, part, a.out, a.lse, a.status) ==
+  if (cudaLaunchKernelEx(&cfg, scaled_kernel<C>, maps, a, info, part) != cudaSuccess) return VMLA_ERR_CUDA;
+  attr[0] = early_start_attribute();
+  cfg.gridDim = dim3((unsigned)ctas, kRows, 1);
+  cfg.blockDim = dim3(kJoinThreads, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, scaled_join_kernel, (const CtaInfo*)info, ctas, part, a.out, a.lse, a.status) ==
                  cudaSuccess
              ? VMLA_OK
              : VMLA_ERR_CUDA;
@@ -1069,21 +1138,24 @@ int launch(const ScaledArgs& a, int sms, const CUtensorMap& latent, const CUtens
 
 }  // namespace
 
-size_t scaled_workspace(int sms) { return o_off(sms) + (size_t)sms * 2 * kMaxRows * kDv * sizeof(float); }
+size_t scaled_workspace(int sms) { return o_off(sms) + (size_t)sms * 2 * kRows * kDv * sizeof(float); }
 
 int launch_scaled(const ScaledArgs& a, int sms, void* stream) {
-  if (sms > kMaxCtas) return VMLA_ERR_DEVICE;
+  if (sms > kMaxCtas || sms < 4) return VMLA_ERR_DEVICE;
   EncodeTiledFn enc = encode_fn();
   if (!enc) return VMLA_ERR_DEVICE;
-  CUtensorMap latent, rope;
+  Maps maps;
   // (without keys nothing is fetched: any address does)
   const uint8_t* pool = a.pool ? a.pool : reinterpret_cast<const uint8_t*>(a.workspace);
-  if (!encode_pool(enc, &latent, pool, a.pool_slots, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_pool(enc, &rope, pool, a.pool_slots, 64, CU_TENSOR_MAP_SWIZZLE_64B))
+  if (!encode_pool(enc, &maps.latent, pool, a.pool_slots, 128, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_pool(enc, &maps.rope, pool, a.pool_slots, 64, 1, CU_TENSOR_MAP_SWIZZLE_64B) ||
+      !encode_pool(enc, &maps.latent_run, pool, a.pool_slots, 128, kRun, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_pool(enc, &maps.rope_run, pool, a.pool_slots, 64, kRun, CU_TENSOR_MAP_SWIZZLE_64B))
     return VMLA_ERR_CUDA;
-  // by the rows that a sequence has on the average of the bounds: units of 64 once they are more than 32
-  return a.max_q * a.num_heads > 32 * (int64_t)a.batch ? launch<64>(a, sms, latent, rope, (cudaStream_t)stream)
-                                                       : launch<32>(a, sms, latent, rope, (cudaStream_t)stream);
+  // lanes of as many CTAs as a sequence has row blocks on the average of the bounds, up to four
+  const int64_t rows = a.max_q * a.num_heads, blocks = (int64_t)a.batch * kRows;
+  cudaStream_t st = (cudaStream_t)stream;
+  return rows > 2 * blocks ? launch<4>(a, sms, maps, st) : rows > blocks ? launch<2>(a, sms, maps, st) : launch<1>(a, sms, maps, st);
 }
 
 }  // namespace vmla
