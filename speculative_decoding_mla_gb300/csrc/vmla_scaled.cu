@@ -45,28 +45,27 @@ constexpr int kParts = 3;           // of a weight
 constexpr int kPerThread = 16;      // rows of a softmax thread
 constexpr int kSoftWarps = 4 * kRows / kPerThread;  // per quarter of the tile's keys, 16 rows each
 constexpr int kSoftThreads = kSoftWarps * 32;
-constexpr int kLoadWarps = 7;
-constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kMmaWarp + 1;
+constexpr int kScoreWarp = kSoftWarps, kValueWarp = kScoreWarp + 1, kLoadWarp = kValueWarp + 1;
+constexpr int kLoadWarps = 6;
 constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
 constexpr int kRun = 16;            // consecutive slots that one box fetches
 constexpr uint32_t kOCols = kParts * kRows;       // 96 columns of tensor memory per 128 value columns
 constexpr uint32_t kSCol = kChunks * kOCols;      // 384
-constexpr int kLatentSlots = 8, kRopeSlots = 2, kPSlots = 2;
-constexpr int kFixed = 2;           // what a unit costs beside its tiles, in tiles
+constexpr int kStages = 2;          // tiles in shared memory, each chunk with barriers of its own
+constexpr int kFixed = 8;           // what a unit costs beside its tiles, in tiles
 constexpr float kNone = -3e38f;     // reference of a row that has seen no key
-constexpr float kUnit = 2048.f;     // weights are held times 2^11
+constexpr float kUnit = 512.f;      // weights are held times 2^9
 constexpr float kMost = 32768.f;    // largest weight held
 constexpr float kTiny = 0x1p-100f;  // smaller scales count as zero
 static_assert(kSCol + 2 * 2 * kRows == 512, "tensor memory");
 static_assert(kThreads % 128 == 0, "whole register banks");
-static_assert(kLoadWarps <= kLatentSlots && kLatentSlots <= 2 * kLoadWarps && kLatentSlots % 4 == 0 && kRopeSlots == 2,
-              "see load_role");
+static_assert(kStages == 2 && kLoadWarps == kChunks + 2 && kTile / kRun == 8, "see load_role");
 
 struct Shared {
-  uint8_t latent[kLatentSlots][kTile * 128];  // a tile's chunk: [key][128 bytes], 128-byte swizzle
+  uint8_t latent[kStages][kChunks][kTile * 128];  // a tile's chunk: [key][128 bytes], 128-byte swizzle
   uint8_t q_latent[kChunks][2 * kRows * 128]; // [hi rows, lo rows][128 bytes], 128-byte swizzle
-  uint8_t p[kPSlots][kTile * 128];            // [key][hi 32 | mid 32 | lo 32 | -], 128-byte swizzle
-  uint8_t rope[kRopeSlots][kTile * 64];       // [key][64 bytes], 64-byte swizzle
+  uint8_t p[kStages][kTile * 128];            // [key][hi 32 | mid 32 | lo 32 | -], 128-byte swizzle
+  uint8_t rope[kStages][kTile * 64];          // [key][64 bytes], 64-byte swizzle
   uint8_t q_rope[2 * kRows * 64];             // 64-byte swizzle
   float m[kRows], f[kRows];                   // reference of each row (log2), factor of its last change
   float part[4][kRows];                       // per quarter of the keys: row maxima, or row sums
@@ -75,8 +74,8 @@ struct Shared {
   int32_t parent[VMLA_MAX_DRAFT];
   float q_max[kSoftWarps];
   uint32_t sums[2][kThreads / 32];
-  uint64_t lfull[kLatentSlots], lfree[kLatentSlots], rfull[kRopeSlots], rfree[kRopeSlots];
-  uint64_t sfull[2], sfree[2], pfull[kPSlots], pfree[kPSlots], qfull, ofree, done;
+  uint64_t full[kStages][kPieces], free[kStages][kPieces];  // of a tile's pieces
+  uint64_t sfull[kStages], sfree[kStages], pfull[kStages], pfree[kStages], qfull, ofree;
   uint32_t tmem;
   volatile int32_t abort_flag;
   int32_t stop;
@@ -92,9 +91,8 @@ struct alignas(32) CtaInfo {
   int64_t row;      // first row of out
   int32_t pieces;   // 0: no such stream
   int32_t rows;
-  int32_t group;    // G
   uint32_t fault, fault_info;
-  int32_t pad;
+  int32_t pad[2];
 };
 
 struct Partials {
@@ -111,43 +109,11 @@ struct Maps {
   CUtensorMap latent_run, rope_run;  // boxes of kRun rows
 };
 
-// Ends the work of every CTA of the lane: their waits give up.
-template <int C>
-__device__ __noinline__ void give_up(Shared& sm) {
-  sm.abort_flag = 1;
-  if (C > 1) {
-    const uint32_t flag = smem_u32(const_cast<const int32_t*>(&sm.abort_flag));
-    for (uint32_t r = 0; r < C; ++r) st_cluster_u32(mapa(flag, r), 1u);
-  }
-}
-
-// One arrival at the barrier, in every CTA of the lane, once this thread's products so far are complete.
-template <int C>
-__device__ __forceinline__ void commit(uint64_t* bar) {
-  if (C == 1) mma_commit(bar);
-  else mma_commit_multicast(bar, (uint16_t)((1 << C) - 1));
-}
-
-// Copies into the same place of every CTA of the lane.
-template <int C>
-__device__ __forceinline__ void load_gather(uint32_t dst, const CUtensorMap* map, int x, int y0, int y1, int y2, int y3,
-                                            uint32_t bar) {
-  if (C == 1) tma_gather4(dst, map, x, y0, y1, y2, y3, bar);
-  else tma_gather4_multicast(dst, map, x, y0, y1, y2, y3, bar, (uint16_t)((1 << C) - 1));
-}
-template <int C>
-__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  if (C == 1) tma_load_2d(dst, map, x, y, bar);
-  else tma_load_2d_multicast(dst, map, x, y, bar, (uint16_t)((1 << C) - 1));
-}
-
 // ------------------------------------------------------------------ plan
-// Costs are counted in tiles of whole lanes: at most 2^24 tiles (2^31 keys) x 256 row blocks / C, and kFixed a stream,
-// which fit 32 bits but for C = 1, where a sequence has few row blocks on the average of the call's bounds; a plan whose
-// cost does not fit is refused.
+// Costs are counted in tiles; a call whose cost does not fit 31 bits (2^27 for any 32 sequences) is refused.
 struct Plan {
   uint32_t length;  // of all streams
-  uint32_t share;   // of a lane
+  uint32_t share;   // of a CTA
   int32_t lanes;
 };
 
@@ -163,15 +129,12 @@ __device__ __forceinline__ Seq seq_of(const ScaledArgs& a, int b) {
   s.nk = __ldg(a.kv_indptr + b + 1) - s.kv0;
   return s;
 }
-// Streams of C row blocks.
-template <int C>
-__device__ __forceinline__ int streams_of(const ScaledArgs& a, int nq) {
-  return (nq * a.num_heads + C * kRows - 1) / (C * kRows);
+__device__ __forceinline__ int row_blocks(const ScaledArgs& a, int nq) {
+  return (nq * a.num_heads + kRows - 1) / kRows;
 }
 __device__ __forceinline__ int tiles_of(int nk) { return nk / kTile + (nk % kTile != 0); }
 
 // Reads the lengths and shares the work out (whole CTA); false where the lengths are out of order or past a bound.
-template <int C>
 __device__ bool make_plan(Shared& sm, const ScaledArgs& a, Plan& plan) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   static_assert(kThreads >= VMLA_MAX_BATCH, "a thread per sequence");
@@ -183,7 +146,7 @@ __device__ bool make_plan(Shared& sm, const ScaledArgs& a, Plan& plan) {
     ok = q1 >= q0 && q1 - q0 <= VMLA_MAX_DRAFT && k1 - k0 >= q1 - q0;
     if (tid == 0) ok = ok && k0 == 0 && q0 == 0;
     if (tid == a.batch - 1) ok = ok && k1 <= a.max_kv && q1 <= a.max_q;
-    if (ok) cost = (uint64_t)streams_of<C>(a, (int)(q1 - q0)) * (uint64_t)(tiles_of((int)(k1 - k0)) + kFixed);
+    if (ok) cost = (uint64_t)row_blocks(a, (int)(q1 - q0)) * (uint64_t)(tiles_of((int)(k1 - k0)) + kFixed);
   }
   uint64_t upto = cost;
 #pragma unroll
@@ -204,7 +167,7 @@ __device__ bool make_plan(Shared& sm, const ScaledArgs& a, Plan& plan) {
   const uint32_t before = warp > 0 ? __shfl_sync(0xffffffffu, all, warp - 1) : 0;
   if (tid <= a.batch) sm.cost[tid] = before + (uint32_t)(upto - cost);
   if (tid == 0 && a.batch == kThreads) sm.cost[a.batch] = plan.length;
-  plan.lanes = (int)gridDim.x / C;
+  plan.lanes = (int)gridDim.x;
   plan.share = (plan.length + plan.lanes - 1) / plan.lanes;
   if (plan.share == 0) plan.share = 1;
   __syncthreads();
@@ -213,7 +176,7 @@ __device__ bool make_plan(Shared& sm, const ScaledArgs& a, Plan& plan) {
 
 // One row block of a sequence over some of its tiles.
 struct Unit {
-  int row_block, rows;      // rows of the block that are the sequence's (0: none; the CTA goes along for its lane's loads)
+  int row_block, rows;      // rows of the block that are the sequence's 
   int tile0, tiles;         // its tiles
   int q0, nq;               // the sequence's drafts
   int kv0, keys, prefix;    // first entry of kv_indices; keys and prefix of the sequence
@@ -222,7 +185,6 @@ struct Unit {
 };
 
 // The units of a CTA in its lane, in order; the CTAs of a lane have the same tiles.
-template <int C>
 struct Units {
   uint32_t at, end, from;  // cost position of the current stream; of the lane's end and start
   int b, g, n;
@@ -230,14 +192,14 @@ struct Units {
   __device__ __forceinline__ void enter(const Shared& sm, const ScaledArgs& a, int sequence) {
     for (b = sequence; b < a.batch; ++b) {
       s = seq_of(a, b);
-      n = streams_of<C>(a, s.nq);
+      n = row_blocks(a, s.nq);
       if (n > 0) break;
     }
     g = 0;
     at = b < a.batch ? sm.cost[b] : 0xFFFFFFFFu;
   }
   __device__ __forceinline__ Units(const Shared& sm, const ScaledArgs& a, const Plan& p) {
-    const uint32_t lane = blockIdx.x / C;
+    const uint32_t lane = blockIdx.x;
     from = lane * p.share;  // (below the length plus one share: fits)
     end = from + p.share < p.length ? from + p.share : p.length;
     at = 0xFFFFFFFFu;
@@ -263,8 +225,8 @@ struct Units {
       const uint32_t lo = at > from ? at : from, stop = at + tiles, hi = stop < end ? stop : end;
       const bool use = lo < hi;
       if (use) {
-        u.row_block = g * C + (int)(blockIdx.x % C);
-        u.rows = max(0, min(kRows, s.nq * a.num_heads - u.row_block * kRows));
+        u.row_block = g;
+        u.rows = min(kRows, s.nq * a.num_heads - g * kRows);
         u.tile0 = (int)(lo - at);
         u.tiles = (int)(hi - lo);
         u.q0 = s.q0;
@@ -288,23 +250,21 @@ __device__ __forceinline__ int64_t out_row(const ScaledArgs& a, const Unit& u) {
 }
 
 // ------------------------------------------------------------------ waits
-template <int C>
 __device__ __noinline__ bool wait_slow(Shared& sm, uint64_t* bar, uint32_t parity, long long budget, uint32_t where) {
   const long long t0 = clock64();
   for (;;) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if (sm.abort_flag) return false;
     if (clock64() - t0 > budget) {
       fault(sm, VMLA_ERR_TIMEOUT, where);
-      give_up<C>(sm);
+      sm.abort_flag = 1;
       return false;
     }
   }
 }
 // Bounded wait; false once it ran out, here or in another warp.
-template <int C>
 __device__ __forceinline__ bool wait(Shared& sm, uint64_t* bar, uint32_t parity, const ScaledArgs& a, uint32_t where) {
-  return mbar_try_wait_cluster(bar, parity) || wait_slow<C>(sm, bar, parity, a.wait_cycles, where);
+  return mbar_try_wait(bar, parity) || wait_slow(sm, bar, parity, a.wait_cycles, where);
 }
 
 // A barrier of the softmax warps that tells each whether `any` held in one of them.
@@ -318,230 +278,183 @@ __device__ __forceinline__ bool soft_vote(bool any) {
   return r != 0;
 }
 
-// A position in a ring of slots, and the parity of its round.
-template <int N>
-struct Ring {
-  int slot = 0;
-  uint32_t parity = 0;
-  __device__ __forceinline__ void step() {
-    if (++slot == N) {
-      slot = 0;
-      parity ^= 1;
-    }
-  }
-};
-
-// ------------------------------------------------------------------ loads (every lane of seven warps)
-// A tile's pieces in the order of their use by the score product: chunks 0, 1, 2, the rotated columns, chunk 3.  The CTAs
-// of a lane fetch them in turn, each for all; in a CTA its warps, a lane the four keys 4 lane .. 4 lane + 3.  (An
-// instruction that starts a copy takes its thread some 50 clocks, and the lanes' go one by one: seven warps keep the copy
-// engine busy, three do not.)  Where all of a tile's slots are consecutive in groups of kRun, a box fetches each group.
-template <int C>
-__device__ void load_role(Shared& sm, const Maps& maps, const ScaledArgs& a, Units<C>& units, Unit& u, bool more) {
+// ------------------------------------------------------------------ loads (six warps)
+// A tile's pieces are its four chunks and the rotated columns, each with a barrier of its own per stage.  Where all of the
+// tile's slots are consecutive in groups of kRun, a piece is eight boxes and one or two warps'; otherwise it is 32 gathers
+// of four rows, dealt out to all six: starting a copy takes its thread some 80 clocks.  The
+// slots are brought to all lanes of a warp, and one lane starts the copies, with operands that the whole warp has (see
+// elect_one).
+// A barrier's parity tells apart two rounds of its stage, no more.  Every warp has a part in a chunk of every tile and waits
+// for it, so it is never two rounds ahead of any piece (its chunk's release three tiles ago follows all of the tile before
+// that), and no round that it waits for can pass unseen, since the piece lacks its part.
+__device__ void load_role(Shared& sm, const Maps& maps, const ScaledArgs& a, Units& units, Unit& u, bool more) {
   const int warp = (threadIdx.x >> 5) - kLoadWarp, lane = threadIdx.x & 31;
-  const uint32_t me = C > 1 ? cluster_ctarank() : 0;
-  const int none = (int)a.pool_slots;  // outside the tensor: zeros
-  Ring<kLatentSlots> lr;
-  Ring<kRopeSlots> rr;
-  // the warp that sees to the next chunk, in every CTA.  A barrier's parity tells apart two rounds of its slot, no more, so
-  // a warp's chunks lie no further apart than there are slots (when it comes to one, the slot's round before the last is
-  // over, since that of its own chunk before was), and nothing waits for a slot but who fills it next (the round that it
-  // waits for cannot pass unseen); the rotated columns' slots have a warp each for the same reason
-  int turn = 0;
+  const int none = (int)a.pool_slots;       // outside the tensor: zeros
+  constexpr int kGroups = (kTile / 4 + kLoadWarps - 1) / kLoadWarps;  // of four keys, the warp's: warp, warp + 6 ..
+  constexpr int kBoxes = kTile / kRun;
+  const bool last_group = warp + kLoadWarps * (kGroups - 1) < kTile / 4;
+  const uint32_t full0 = smem_u32(&sm.full[0][0]), latent0 = smem_u32(sm.latent[0][0]), rope0 = smem_u32(sm.rope[0]);
+  uint32_t it = 0;
   for (; more; more = units.next(sm, a, u)) {
     const int32_t* index = a.kv_indices + u.kv0;
     const int last = min(u.keys, (u.tile0 + u.tiles) * kTile);  // behind this unit's keys
+    const int tiles = u.tiles;
+    int key = u.tile0 * kTile + 4 * lane;
     int32_t ahead[4];
-    auto fetch = [&](int t) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int key = (u.tile0 + t) * kTile + 4 * lane + k;
-        ahead[k] = key < last ? __ldg(index + key) : -1;
-      }
-    };
-    fetch(0);
-    for (int t = 0; t < u.tiles; ++t) {
+    for (int k = 0; k < 4; ++k) ahead[k] = key + k < last ? __ldg(index + key + k) : -1;
+#pragma unroll 1
+    for (int t = 0; t < tiles; ++t, ++it) {
       int32_t y[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         y[k] = ahead[k];
-        if (y[k] < 0 || y[k] >= none) {
-          const int key = (u.tile0 + t) * kTile + 4 * lane + k;
-          if (warp == 0 && key < last) fault(sm, VMLA_ERR_INDEX, (uint32_t)(u.kv0 + key));
+        if ((uint32_t)y[k] >= (uint32_t)none) {
+          if (warp == 0 && key + k < last) fault(sm, VMLA_ERR_INDEX, (uint32_t)(u.kv0 + key + k));
           y[k] = none;
         }
       }
-      fetch(t + 1);
+      key += kTile;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) ahead[k] = key + k < last ? __ldg(index + key + k) : -1;
       const int first = __shfl_sync(0xffffffffu, y[0], lane & ~3);
       const bool runs = __all_sync(0xffffffffu, y[0] == first + 4 * (lane & 3) && y[1] == y[0] + 1 && y[2] == y[0] + 2 &&
                                                     y[3] == y[0] + 3 && y[3] < none);
-#pragma unroll 1
-      for (int piece = 0; piece < kPieces; ++piece) {
-        const bool is_rope = piece == kRopePiece;
-        const bool mine = is_rope ? warp == kLoadWarps - 1 - rr.slot : turn == warp;
-        // (pieces by turns, also where a tile has fewer of a kind than there are CTAs)
-        const bool here = C == 1 || (is_rope ? (uint32_t)rr.slot + 2 * rr.parity : (uint32_t)lr.slot) % C == me;
-        if (mine) {
-          uint64_t* full = is_rope ? &sm.rfull[rr.slot] : &sm.lfull[lr.slot];
-          uint64_t* free = is_rope ? &sm.rfree[rr.slot] : &sm.lfree[lr.slot];
-          if (!__all_sync(0xffffffffu, wait<C>(sm, free, (is_rope ? rr.parity : lr.parity) ^ 1, a, 100))) return;
-          if (lane == 0) mbar_arrive_expect_tx(full, is_rope ? kTile * 64 : kTile * 128);
-          __syncwarp();
-          if (here) {
-            const uint32_t bar = smem_u32(full), dst = is_rope ? smem_u32(sm.rope[rr.slot]) : smem_u32(sm.latent[lr.slot]);
-            const int x = is_rope ? kDv : (piece < kRopePiece ? piece : piece - 1) * 128, row = is_rope ? 64 : 128;
-            if (runs) {
-              if ((lane & 3) == 0)
-                load_box<C>(dst + lane * 4 * row, is_rope ? &maps.rope_run : &maps.latent_run, x, y[0], bar);
-            } else {
-              load_gather<C>(dst + lane * 4 * row, is_rope ? &maps.rope : &maps.latent, x, y[0], y[1], y[2], y[3], bar);
+      const uint32_t stage = it & 1, parity = (it >> 1) & 1;
+      if (runs) {
+        // warps 0 to 3 have a chunk each, 4 and 5 half of chunks 0 and 1, and the rotated columns
+        const int chunk = warp & 3, piece = chunk < kRopePiece ? chunk : chunk + 1;
+        const bool upper = warp >= kChunks, whole = chunk >= kLoadWarps - kChunks;
+        int32_t r[kBoxes];
+#pragma unroll
+        for (int k = 0; k < kBoxes; ++k) r[k] = __shfl_sync(0xffffffffu, y[0], (upper ? k ^ (kBoxes / 2) : k) * (kRun / 4));
+        const uint32_t at0 = upper ? kBoxes / 2 : 0;  // r[k]: box k ^ at0
+        if (!__all_sync(0xffffffffu, wait(sm, &sm.free[stage][piece], parity ^ 1, a, 100))) return;
+        if (elect_one()) {
+          const uint32_t bar = full0 + (stage * kPieces + piece) * 8, dst = latent0 + (stage * kChunks + chunk) * (kTile * 128);
+          if (!upper) mbar_arrive_expect_tx(bar, kTile * 128);
+#pragma unroll
+          for (int k = 0; k < kBoxes; ++k)
+            if (k < kBoxes / 2 || whole) tma_load_2d(dst + (k ^ at0) * kRun * 128, &maps.latent_run, chunk * 128, r[k], bar);
+        }
+        __syncwarp();
+        if (upper) {
+          if (!__all_sync(0xffffffffu, wait(sm, &sm.free[stage][kRopePiece], parity ^ 1, a, 101))) return;
+          if (elect_one()) {
+            const uint32_t bar = full0 + (stage * kPieces + kRopePiece) * 8, dst = rope0 + stage * (kTile * 64);
+            if (warp == kChunks) mbar_arrive_expect_tx(bar, kTile * 64);
+            // (boxes 4 to 7 by warp 4, which has them first, 0 to 3 by warp 5)
+#pragma unroll
+            for (int k = 0; k < kBoxes / 2; ++k) {
+              const int q = warp == kChunks ? k : k + kBoxes / 2;
+              tma_load_2d(dst + (q ^ at0) * kRun * 64, &maps.rope_run, kDv, warp == kChunks ? r[k] : r[k + kBoxes / 2], bar);
             }
           }
+          __syncwarp();
         }
-        if (is_rope) {
-          rr.step();
-        } else {
-          lr.step();
-          turn = turn == kLoadWarps - 1 ? 0 : turn + 1;
+        continue;
+      }
+      int32_t g[kGroups][4];
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) g[k][q] = __shfl_sync(0xffffffffu, y[q], (warp + kLoadWarps * k) & 31);
+#pragma unroll
+      for (int piece = 0; piece < kPieces; ++piece) {
+        const int chunk = piece < kRopePiece ? piece : piece - 1, row = piece == kRopePiece ? 64 : 128;
+        if (!__all_sync(0xffffffffu, wait(sm, &sm.free[stage][piece], parity ^ 1, a, 102))) return;
+        if (elect_one()) {
+          const uint32_t bar = full0 + (stage * kPieces + piece) * 8,
+                         dst = piece == kRopePiece ? rope0 + stage * (kTile * 64) : latent0 + (stage * kChunks + chunk) * (kTile * 128);
+          if (warp == 0) mbar_arrive_expect_tx(bar, kTile * row);
+#pragma unroll
+          for (int k = 0; k < kGroups; ++k)
+            if (k < kGroups - 1 || last_group)
+              tma_gather4(dst + (warp + kLoadWarps * k) * 4 * row, piece == kRopePiece ? &maps.rope : &maps.latent,
+                          piece == kRopePiece ? kDv : chunk * 128, g[k][0], g[k][1], g[k][2], g[k][3], bar);
         }
+        __syncwarp();
       }
     }
   }
-  // the slots' last releases, which come from every CTA of the lane, have arrived before this CTA may leave: each is
-  // waited for by who filled the slot last
-  for (int k = 0; k < kLatentSlots; ++k) {
-    if ((turn + k + kLoadWarps * 2 - kLatentSlots) % kLoadWarps == warp) wait<C>(sm, &sm.lfree[lr.slot], lr.parity ^ 1, a, 101);
-    lr.step();
-  }
-  for (int k = 0; k < kRopeSlots; ++k) {
-    if (warp == kLoadWarps - 1 - rr.slot) wait<C>(sm, &sm.rfree[rr.slot], rr.parity ^ 1, a, 102);
-    rr.step();
-  }
+  // the pieces' last releases have arrived before the CTA may leave
+  if (warp == 0)
+    for (int k = 0; k < kStages; ++k, ++it)
+      for (int piece = 0; piece < kPieces; ++piece) wait(sm, &sm.free[it & 1][piece], ((it >> 1) & 1) ^ 1, a, 103);
   __syncwarp();
 }
 
-// ------------------------------------------------------------------ matrix products (one warp)
-// Two sequences of products: scores, piece by piece as a tile's columns arrive, and values, a tile at a time.  Whatever
-// is ready goes next, scores first: they keep the softmax busy, and only values make room for further loads.  What lies
-// between two products is short: a look at a barrier and the bookkeeping take as long as ten of them.
-template <int C>
-__device__ void mma_role(Shared& sm, const ScaledArgs& a, uint32_t tmem, const Units<C>& units, const Unit& first,
-                         bool more) {
-  constexpr uint32_t kScores = idesc_f8_f32(kTile, 2 * kRows, 0, 0, 0, 0);
-  constexpr uint32_t kValues = idesc_f8_f32(128, kOCols, 0, 1, 1, 1);
-  Units<C> q_units = units, v_units = units;
-  Unit u = first;
-  bool q_more = more, v_more = more;
-  int q_tiles = u.tiles, v_tiles = u.tiles;  // left of the unit
-  bool q_first = true, v_first = true;       // no tile of the unit yet
-  Ring<kLatentSlots> ql, vl;
-  Ring<kRopeSlots> qr;
-  // lower words of the descriptors at the first slot, and the upper words, which depend on the layout alone
-  constexpr uint32_t kHi128 = (uint32_t)(smem_desc_fixed(16, 1024, 2) >> 32), kHi64 = (uint32_t)(smem_desc_fixed(16, 512, 4) >> 32);
-  constexpr uint32_t kLo = (uint32_t)smem_desc_fixed(16, 0, 0);
-  auto low = [&](const void* at) { return smem_u32(at) >> 4 | kLo; };
-  const uint32_t latent_lo = low(sm.latent[0]), rope_lo = low(sm.rope[0]), q_latent_lo = low(sm.q_latent[0]),
-                 q_rope_lo = low(sm.q_rope), p_lo = low(sm.p[0]);
-  uint32_t q_it = 0, v_it = 0, q_unit = 0, v_unit = 0;
-  int piece = 0;
-  auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait_cluster(bar, parity)) != 0; };
-  auto scores = [&]() -> bool {
-    const uint32_t sb = q_it & 1;
-    if (piece == 0 && ((q_first && !ready(&sm.qfull, q_unit & 1)) || !ready(&sm.sfree[sb], ((q_it >> 1) & 1) ^ 1)))
-      return false;
-    const uint32_t d = tmem + kSCol + sb * 2 * kRows;
-    const int begun = piece;
+// ------------------------------------------------------------------ matrix products (a warp each for scores and values)
+// Lower words of the operands' descriptors; the upper words depend on the layout alone.
+constexpr uint32_t kHi128 = (uint32_t)(smem_desc_fixed(16, 1024, 2) >> 32), kHi64 = (uint32_t)(smem_desc_fixed(16, 512, 4) >> 32);
+__device__ __forceinline__ uint32_t desc_low(const void* at) { return smem_u32(at) >> 4 | (uint32_t)smem_desc_fixed(16, 0, 0); }
+
+// Piece by piece as a tile's columns arrive.
+__device__ void score_role(Shared& sm, const ScaledArgs& a, uint32_t tmem, Units& units, Unit& u, bool more) {
+  constexpr uint32_t kDesc = idesc_f8_f32(kTile, 2 * kRows, 0, 0, 0, 0);
+  const uint32_t latent_lo = desc_low(sm.latent[0][0]), rope_lo = desc_low(sm.rope[0]), q_latent_lo = desc_low(sm.q_latent[0]),
+                 q_rope_lo = desc_low(sm.q_rope);
+  uint32_t it = 0, unit = 0;
+  for (; more; more = units.next(sm, a, u), ++unit) {
+    const int tiles = u.tiles;
+    if (!__all_sync(0xffffffffu, wait(sm, &sm.qfull, unit & 1, a, 200))) return;
+#pragma unroll 1
+    for (int t = 0; t < tiles; ++t, ++it) {
+      const uint32_t stage = it & 1, parity = (it >> 1) & 1, d = tmem + kSCol + stage * 2 * kRows;
+      if (!__all_sync(0xffffffffu, wait(sm, &sm.sfree[stage], parity ^ 1, a, 201))) return;
 #pragma unroll
-    for (int k = 0; k <= kChunks; ++k) {
-      if (k != piece) continue;
-      if (k == kRopePiece) {
-        if (!ready(&sm.rfull[qr.slot], qr.parity)) break;
+      for (int piece = 0; piece < kPieces; ++piece) {
+        if (!__all_sync(0xffffffffu, wait(sm, &sm.full[stage][piece], parity, a, 202))) return;
         tc_fence_after();
-        const uint32_t key = rope_lo + qr.slot * (kTile * 64 / 16);
         if (elect_one()) {
+          if (piece == kRopePiece) {
+            const uint32_t key = rope_lo + stage * (kTile * 64 / 16);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) mma_ss_f8(d, key + 2 * i, kHi64, q_rope_lo + 2 * i, kHi64, kScores, 1u);
-          commit<C>(&sm.rfree[qr.slot]);
+            for (int i = 0; i < 2; ++i) mma_ss_f8(d, key + 2 * i, kHi64, q_rope_lo + 2 * i, kHi64, kDesc, 1u);
+            mma_commit(&sm.free[stage][piece]);
+          } else {
+            const int chunk = piece < kRopePiece ? piece : piece - 1;
+            const uint32_t key = latent_lo + (stage * kChunks + chunk) * (kTile * 128 / 16),
+                           q = q_latent_lo + chunk * (2 * kRows * 128 / 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma_ss_f8(d, key + 2 * i, kHi128, q + 2 * i, kHi128, kDesc, piece > 0 || i > 0);
+          }
+          if (piece == kPieces - 1) mma_commit(&sm.sfull[stage]);
         }
-        qr.step();
-      } else {
-        if (!ready(&sm.lfull[ql.slot], ql.parity)) break;
-        tc_fence_after();
-        const uint32_t key = latent_lo + ql.slot * (kTile * 128 / 16),
-                       q = q_latent_lo + (k < kRopePiece ? k : k - 1) * (2 * kRows * 128 / 16);
-        if (elect_one()) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma_ss_f8(d, key + 2 * i, kHi128, q + 2 * i, kHi128, kScores, k > 0 || i > 0);
-          if (k == kChunks) mma_commit(&sm.sfull[sb]);
-        }
-        ql.step();
+        __syncwarp();
       }
-      __syncwarp();
-      piece = k + 1;
-    }
-    if (piece == begun) return false;
-    if (piece > kChunks) {
-      piece = 0;
-      ++q_it;
-      q_first = false;
-      if (--q_tiles == 0) {
-        ++q_unit;
-        q_first = true;
-        q_more = q_units.next(sm, a, u);
-        q_tiles = u.tiles;
-      }
-    }
-    return true;
-  };
-  auto values = [&]() -> bool {
-    // (the first product into O: the unit before has been read out)
-    const uint32_t pb = v_it % kPSlots;
-    if (!ready(&sm.pfull[pb], (v_it / kPSlots) & 1) || (v_first && !ready(&sm.ofree, (v_unit & 1) ^ 1))) return false;
-    tc_fence_after();
-    const uint32_t go_on = v_first ? 0u : 1u, p = p_lo + pb * (kTile * 128 / 16);
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const uint32_t v = latent_lo + vl.slot * (kTile * 128 / 16), d = tmem + c * kOCols;
-      if (elect_one()) {
-#pragma unroll
-        for (int i = 0; i < kTile / 32; ++i)
-          mma_ss_f8(d, v + 256 * i, kHi128, p + 256 * i, kHi128, kValues, i > 0 ? 1u : go_on);
-        commit<C>(&sm.lfree[vl.slot]);
-        if (c == kChunks - 1) mma_commit(&sm.pfree[pb]);
-      }
-      __syncwarp();
-      vl.step();
-    }
-    ++v_it;
-    v_first = false;
-    if (--v_tiles == 0) {
-      ++v_unit;
-      v_first = true;
-      v_more = v_units.next(sm, a, u);
-      v_tiles = u.tiles;
-    }
-    return true;
-  };
-  int idle = 0;
-  long long t0 = 0;
-  while (q_more || v_more) {
-    if (q_more && scores()) idle = 0;
-    if (v_more && values()) idle = 0;
-    if (++idle < 256) continue;
-    if (idle == 256) t0 = clock64();
-    if (__any_sync(0xffffffffu, sm.abort_flag != 0)) break;
-    if (__any_sync(0xffffffffu, clock64() - t0 > a.wait_cycles)) {
-      if (elect_one()) fault(sm, VMLA_ERR_TIMEOUT, 200);
-      give_up<C>(sm);
-      __syncwarp();
     }
   }
-  // everything issued is complete, and its signals have arrived, before the CTA leaves
-  if (elect_one()) mma_commit(&sm.done);
-  __syncwarp();
-  t0 = clock64();
-  while (!mbar_try_wait(&sm.done, 0) && clock64() - t0 < a.wait_cycles) {
+}
+
+// A tile at a time; each chunk makes room for a later tile's.
+__device__ void value_role(Shared& sm, const ScaledArgs& a, uint32_t tmem, Units& units, Unit& u, bool more) {
+  constexpr uint32_t kDesc = idesc_f8_f32(128, kOCols, 0, 1, 1, 1);
+  const uint32_t latent_lo = desc_low(sm.latent[0][0]), p_lo = desc_low(sm.p[0]);
+  uint32_t it = 0, unit = 0;
+  for (; more; more = units.next(sm, a, u), ++unit) {
+    const int tiles = u.tiles;
+    // (the first product into O: the unit before has been read out)
+    if (!__all_sync(0xffffffffu, wait(sm, &sm.ofree, (unit & 1) ^ 1, a, 210))) return;
+#pragma unroll 1
+    for (int t = 0; t < tiles; ++t, ++it) {
+      const uint32_t stage = it & 1, parity = (it >> 1) & 1;
+      if (!__all_sync(0xffffffffu, wait(sm, &sm.pfull[stage], parity, a, 211))) return;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t go_on = t > 0, p = p_lo + stage * (kTile * 128 / 16), v = latent_lo + stage * (kChunks * kTile * 128 / 16);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+#pragma unroll
+          for (int i = 0; i < kTile / 32; ++i)
+            mma_ss_f8(tmem + c * kOCols, v + c * (kTile * 128 / 16) + 256 * i, kHi128, p + 256 * i, kHi128, kDesc,
+                      i > 0 ? 1u : go_on);
+          mma_commit(&sm.free[stage][c < kRopePiece ? c : c + 1]);
+        }
+        mma_commit(&sm.pfree[stage]);
+      }
+      __syncwarp();
+    }
   }
 }
 
@@ -667,9 +580,8 @@ __device__ __forceinline__ float reduce16(const float (&v)[16], int lane, Op op)
   return op(d, __shfl_xor_sync(0xffffffffu, d, 1));
 }
 
-template <int C>
 __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, uint32_t tmem, const Partials& part,
-                             Units<C>& units, Unit& u, bool more) {
+                             Units& units, Unit& u, bool more) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int quarter = warp & 3, row0 = (warp >> 2) * kPerThread;  // its 32 keys of a tile; its first of 16 rows
   const int my_key = quarter * 32 + lane;
@@ -704,7 +616,7 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
       }
       const bool all_seen = __all_sync(0xffffffffu, seen == 0xFFFFu);
       const float c = scale * factor, held = fmaxf(scale, kTiny) * kUnit;
-      wait<C>(sm, &sm.sfull[sb], (it >> 1) & 1, a, 300);  // (should it run out, the vote below ends the work)
+      wait(sm, &sm.sfull[sb], (it >> 1) & 1, a, 300);  // (should it run out, the vote below ends the work)
       __syncwarp();
       const uint32_t col = tmem + lanes + kSCol + (uint32_t)(sb * 2 * kRows + row0);
       float w[kPerThread];
@@ -768,18 +680,23 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
         }
         if (t > 0) {
           // what has been summed so far, once the products before are complete
-          wait<C>(sm, &sm.pfree[(it - 1) % kPSlots], ((it - 1) / kPSlots) & 1, a, 301);
+          wait(sm, &sm.pfree[(it - 1) % kStages], ((it - 1) / kStages) & 1, a, 301);
           __syncwarp();
           tc_fence_after();
 #pragma unroll 1
-          for (int k = 0; k < (int)kSCol / kRows; ++k) {
+          for (int k = 0; k < (int)kSCol / kRows; k += 2) {
             const uint32_t at = tmem + lanes + (uint32_t)(k * kRows + row0);
-            uint32_t o[kPerThread];
+            uint32_t o[kPerThread], o2[kPerThread];
             tmem_ld16(at, o);
+            tmem_ld16(at + kRows, o2);
             tmem_wait_ld();
 #pragma unroll
-            for (int r = 0; r < kPerThread; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * f[r]);
+            for (int r = 0; r < kPerThread; ++r) {
+              o[r] = __float_as_uint(__uint_as_float(o[r]) * f[r]);
+              o2[r] = __float_as_uint(__uint_as_float(o2[r]) * f[r]);
+            }
             tmem_st16(at, o);
+            tmem_st16(at + kRows, o2);
           }
           tmem_wait_st();
         }
@@ -811,8 +728,8 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
 #pragma unroll
         for (int q = 0; q < kParts; ++q) parts[q][k] = __byte_perm(h[0][q], h[1][q], 0x7531);
       }
-      const int pb = it % kPSlots;
-      if (wait<C>(sm, &sm.pfree[pb], ((it / kPSlots) & 1) ^ 1, a, 302)) {
+      const int pb = it % kStages;
+      if (wait(sm, &sm.pfree[pb], ((it / kStages) & 1) ^ 1, a, 302)) {
 #pragma unroll
         for (int q = 0; q < kParts; ++q) {
           uint8_t* dst = sm.p[pb] + my_key * 128 + (((2 * q + (row0 >> 4)) ^ (my_key & 7)) << 4);
@@ -836,7 +753,7 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
       else if (tid < u.rows) a.lse[first_row + tid] = total > 0.f ? (m + log2f(total)) * 0.6931471805599453f : -INFINITY;
     }
     if (tid == 0 && u.head && !u.whole) {
-      sm.cut_pieces = (int)((u.stop - 1) / plan.share) - (int)(blockIdx.x / C) + 1;
+      sm.cut_pieces = (int)((u.stop - 1) / plan.share) - (int)blockIdx.x + 1;
       sm.cut_rows = u.rows;
       sm.cut_row = first_row;
     }
@@ -847,7 +764,7 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
     // the next unit's queries while this one's last products run
     more = units.next(sm, a, u);
     if (more) factor = load_queries(sm, a, u);
-    wait<C>(sm, &sm.pfree[(it - 1) % kPSlots], ((it - 1) / kPSlots) & 1, a, 303);
+    wait(sm, &sm.pfree[(it - 1) % kStages], ((it - 1) / kStages) & 1, a, 303);
     __syncwarp();
     tc_fence_after();
 #pragma unroll 1
@@ -887,37 +804,29 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
   }
 }
 
-template <int C>
 __global__ void __launch_bounds__(kThreads, 1)
 scaled_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ScaledArgs a, CtaInfo* __restrict__ info,
               const Partials part) {
   extern __shared__ uint8_t raw[];
   Shared& sm = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5;
-  if (warp == kMmaWarp) {
+  if (warp == kValueWarp) {
     tmem_alloc(&sm.tmem, 512);
     tmem_relinquish();
   }
   if (tid == 0) {
-    for (int s = 0; s < kLatentSlots; ++s) {
-      mbar_init(&sm.lfull[s], 1);
-      mbar_init(&sm.lfree[s], C);  // every CTA of the lane has used it
-    }
-    for (int s = 0; s < kRopeSlots; ++s) {
-      mbar_init(&sm.rfull[s], 1);
-      mbar_init(&sm.rfree[s], C);
-    }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kStages; ++s) {
+      for (int k = 0; k < kPieces; ++k) {
+        mbar_init(&sm.full[s][k], 1);
+        mbar_init(&sm.free[s][k], 1);
+      }
       mbar_init(&sm.sfull[s], 1);
       mbar_init(&sm.sfree[s], kSoftWarps);
-    }
-    for (int s = 0; s < kPSlots; ++s) {
       mbar_init(&sm.pfull[s], kSoftWarps);
       mbar_init(&sm.pfree[s], 1);
     }
     mbar_init(&sm.qfull, kSoftWarps);
     mbar_init(&sm.ofree, kSoftWarps);
-    mbar_init(&sm.done, 1);
     sm.abort_flag = 0;
     sm.fault[0] = sm.fault[1] = 0;
     sm.cut_pieces = 0;
@@ -929,37 +838,30 @@ scaled_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ScaledA
   }
   __syncwarp();
   Plan plan;
-  const bool ok = make_plan<C>(sm, a, plan);
+  const bool ok = make_plan(sm, a, plan);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (C > 1) {  // no copy or signal goes to a CTA whose barriers are not ready
-    cluster_arrive();
-    cluster_wait();
-  }
   const uint32_t tmem = sm.tmem;
   if (ok) {
     // the CTA's first unit, which every role begins with
-    Units<C> units(sm, a, plan);
+    Units units(sm, a, plan);
     Unit u;
     const bool more = units.next(sm, a, u);
     if (warp < kSoftWarps) {
-      softmax_role<C>(sm, a, plan, tmem, part, units, u, more);
-    } else if (warp == kMmaWarp) {
-      mma_role<C>(sm, a, tmem, units, u, more);
+      softmax_role(sm, a, plan, tmem, part, units, u, more);
+    } else if (warp == kScoreWarp) {
+      score_role(sm, a, tmem, units, u, more);
+    } else if (warp == kValueWarp) {
+      value_role(sm, a, tmem, units, u, more);
     } else {
-      load_role<C>(sm, maps, a, units, u, more);
+      load_role(sm, maps, a, units, u, more);
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   grid_dependents_launch();
-  if (C > 1) {  // nor leaves a CTA while another may still signal to it
-    __syncwarp();
-    cluster_arrive();
-    cluster_wait();
-  }
   if (sm.abort_flag) {
     // a wait ran out: loads, commits and products issued before may still be on their way into this CTA's memories,
     // each for microseconds; half a millisecond of the global timer (at most 2^26 reads of it)
@@ -974,7 +876,7 @@ scaled_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ScaledA
     __syncthreads();
   }
   __syncwarp();
-  if (warp == kMmaWarp) {
+  if (warp == kValueWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -986,7 +888,6 @@ scaled_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ScaledA
       mine.pieces = sm.cut_pieces;
       mine.rows = sm.cut_rows;
       mine.row = sm.cut_row;
-      mine.group = C;
     }
     info[blockIdx.x] = mine;
   }
@@ -1014,8 +915,8 @@ scaled_join_kernel(const CtaInfo* __restrict__ info, int ctas, const Partials pa
   }
   const CtaInfo i = info[cta];
   if (row >= i.rows || i.pieces == 0) return;
-  // piece 0 lies in this CTA's second slot, piece k in the first slot of the CTA k lanes on
-  auto slot = [&](int k) { return k == 0 ? (int64_t)cta * 2 + 1 : ((int64_t)cta + (int64_t)k * i.group) * 2; };
+  // piece 0 lies in this CTA's second slot, piece k in the first slot of the k-th CTA after it
+  auto slot = [&](int k) { return k == 0 ? (int64_t)cta * 2 + 1 : ((int64_t)cta + k) * 2; };
   for (int k = tid; k < i.pieces; k += kJoinThreads) ml[k] = part.ml[slot(k) * kRows + row];
   __syncthreads();
   float top = kNone;
@@ -1071,66 +972,33 @@ bool encode_pool(EncodeTiledFn enc, CUtensorMap* map, const uint8_t* pool, int64
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int C>
-cudaLaunchConfig_t kernel_config(int ctas, cudaLaunchAttribute* attr) {
-  cudaLaunchConfig_t cfg = {};
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)ctas, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSharedBytes;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cfg;
-}
-
-// Lanes that are resident together on the current device (a GPC's last SMs may not fill one).
-template <int C>
-int max_lanes(int sms, int* lanes) {
+int launch(const ScaledArgs& a, int sms, const Maps& maps, cudaStream_t stream) {
   static std::mutex mu;
-  static int known[64] = {};
+  static bool ready[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return VMLA_ERR_CUDA;
-  std::lock_guard<std::mutex> g(mu);
-  if (dev >= 64 || known[dev] == 0) {
-    if (cudaFuncSetAttribute(scaled_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSharedBytes) !=
-        cudaSuccess)
-      return VMLA_ERR_CUDA;
-    cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = kernel_config<C>(C, attr);
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, scaled_kernel<C>, &cfg) != cudaSuccess || n < 1) return VMLA_ERR_CUDA;
-    n = n < sms / C ? n : sms / C;
-    if (dev >= 64) {
-      *lanes = n;
-      return VMLA_OK;
+  {
+    std::lock_guard<std::mutex> g(mu);
+    if (dev >= 64 || !ready[dev]) {
+      if (cudaFuncSetAttribute(scaled_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSharedBytes) != cudaSuccess)
+        return VMLA_ERR_CUDA;
+      if (dev < 64) ready[dev] = true;
     }
-    known[dev] = n;
   }
-  *lanes = known[dev];
-  return VMLA_OK;
-}
-
-template <int C>
-int launch(const ScaledArgs& a, int sms, const Maps& maps, cudaStream_t stream) {
-  int lanes = 0;
-  const int rc = max_lanes<C>(sms, &lanes);
-  if (rc != VMLA_OK) return rc;
   CtaInfo* info = reinterpret_cast<CtaInfo*>(a.workspace + kInfoOff);
   Partials part;
   part.ml = reinterpret_cast<float2*>(a.workspace + ml_off(sms));
   part.o = reinterpret_cast<float*>(a.workspace + o_off(sms));
-  const int ctas = lanes * C;
-  cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = kernel_config<C>(ctas, attr);
-  cfg.stream = stream;
-  if (cudaLaunchKernelEx(&cfg, scaled_kernel<C>, maps, a, info, part) != cudaSuccess) return VMLA_ERR_CUDA;
-  attr[0] = early_start_attribute();
-  cfg.gridDim = dim3((unsigned)ctas, kRows, 1);
+  scaled_kernel<<<sms, kThreads, kSharedBytes, stream>>>(maps, a, info, part);
+  if (cudaGetLastError() != cudaSuccess) return VMLA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1] = {early_start_attribute()};
+  cfg.gridDim = dim3((unsigned)sms, kRows, 1);
   cfg.blockDim = dim3(kJoinThreads, 1, 1);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, scaled_join_kernel, (const CtaInfo*)info, ctas, part, a.out, a.lse, a.status) ==
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, scaled_join_kernel, (const CtaInfo*)info, sms, part, a.out, a.lse, a.status) ==
                  cudaSuccess
              ? VMLA_OK
              : VMLA_ERR_CUDA;
@@ -1141,7 +1009,7 @@ int launch(const ScaledArgs& a, int sms, const Maps& maps, cudaStream_t stream) 
 size_t scaled_workspace(int sms) { return o_off(sms) + (size_t)sms * 2 * kRows * kDv * sizeof(float); }
 
 int launch_scaled(const ScaledArgs& a, int sms, void* stream) {
-  if (sms > kMaxCtas || sms < 4) return VMLA_ERR_DEVICE;
+  if (sms > kMaxCtas) return VMLA_ERR_DEVICE;
   EncodeTiledFn enc = encode_fn();
   if (!enc) return VMLA_ERR_DEVICE;
   Maps maps;
@@ -1152,10 +1020,7 @@ int launch_scaled(const ScaledArgs& a, int sms, void* stream) {
       !encode_pool(enc, &maps.latent_run, pool, a.pool_slots, 128, kRun, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_pool(enc, &maps.rope_run, pool, a.pool_slots, 64, kRun, CU_TENSOR_MAP_SWIZZLE_64B))
     return VMLA_ERR_CUDA;
-  // lanes of as many CTAs as a sequence has row blocks on the average of the bounds, up to four
-  const int64_t rows = a.max_q * a.num_heads, blocks = (int64_t)a.batch * kRows;
-  cudaStream_t st = (cudaStream_t)stream;
-  return rows > 2 * blocks ? launch<4>(a, sms, maps, st) : rows > blocks ? launch<2>(a, sms, maps, st) : launch<1>(a, sms, maps, st);
+  return launch(a, sms, maps, (cudaStream_t)stream);
 }
 
 }  // namespace vmla
