@@ -51,7 +51,7 @@ constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
 constexpr int kRun = 16;            // consecutive slots that one box fetches
 constexpr uint32_t kOCols = kParts * kRows;       // 96 columns of tensor memory per 128 value columns
 constexpr uint32_t kSCol = kChunks * kOCols;      // 384
-constexpr int kStages = 2;          // tiles in shared memory, each chunk with barriers of its own
+constexpr int kSlots = 10;          // chunks in shared memory: two and a half tiles
 constexpr int kFixed = 8;           // what a unit costs beside its tiles, in tiles
 constexpr float kNone = -3e38f;     // reference of a row that has seen no key
 constexpr float kUnit = 512.f;      // weights are held times 2^9
@@ -59,23 +59,31 @@ constexpr float kMost = 32768.f;    // largest weight held
 constexpr float kTiny = 0x1p-100f;  // smaller scales count as zero
 static_assert(kSCol + 2 * 2 * kRows == 512, "tensor memory");
 static_assert(kThreads % 128 == 0, "whole register banks");
-static_assert(kStages == 2 && kLoadWarps == kChunks + 2 && kTile / kRun == 8, "see load_role");
+static_assert(kLoadWarps == kChunks + 2 && kTile / kRun == 8, "see load_role");
+
+// A sequence's lengths.
+struct Seq {
+  int32_t q0, nq, kv0, nk;
+};
 
 struct Shared {
-  uint8_t latent[kStages][kChunks][kTile * 128];  // a tile's chunk: [key][128 bytes], 128-byte swizzle
+  uint8_t latent[kSlots][kTile * 128];        // a tile's chunk: [key][128 bytes], 128-byte swizzle
   uint8_t q_latent[kChunks][2 * kRows * 128]; // [hi rows, lo rows][128 bytes], 128-byte swizzle
-  uint8_t p[kStages][kTile * 128];            // [key][hi 32 | mid 32 | lo 32 | -], 128-byte swizzle
-  uint8_t rope[kStages][kTile * 64];          // [key][64 bytes], 64-byte swizzle
+  uint8_t p[kTile * 128];                     // [key][hi 32 | mid 32 | lo 32 | -], 128-byte swizzle
+  uint8_t rope[kTile * 64];                   // [key][64 bytes], 64-byte swizzle
   uint8_t q_rope[2 * kRows * 64];             // 64-byte swizzle
   float m[kRows], f[kRows];                   // reference of each row (log2), factor of its last change
   float part[4][kRows];                       // per quarter of the keys: row maxima, or row sums
   uint64_t mask[kRows];                       // the unit's rows: visible drafts
   uint32_t cost[VMLA_MAX_BATCH + 1];          // cost position of each sequence's first stream
+  Seq first_seq;                              // where this CTA's share begins: sequence, row block, cost position
+  int32_t first_b, first_g;
+  uint32_t first_at;
   int32_t parent[VMLA_MAX_DRAFT];
   float q_max[kSoftWarps];
   uint32_t sums[2][kThreads / 32];
-  uint64_t full[kStages][kPieces], free[kStages][kPieces];  // of a tile's pieces
-  uint64_t sfull[kStages], sfree[kStages], pfull[kStages], pfree[kStages], qfull, ofree;
+  uint64_t full[kSlots], free[kSlots], rope_full, rope_free;
+  uint64_t sfull[2], sfree[2], pfull, pfree, qfull, ofree;
   uint32_t tmem;
   volatile int32_t abort_flag;
   int32_t stop;
@@ -114,13 +122,8 @@ struct Maps {
 struct Plan {
   uint32_t length;  // of all streams
   uint32_t share;   // of a CTA
-  int32_t lanes;
 };
 
-// A sequence's lengths.
-struct Seq {
-  int32_t q0, nq, kv0, nk;
-};
 __device__ __forceinline__ Seq seq_of(const ScaledArgs& a, int b) {
   Seq s;
   s.q0 = __ldg(a.qo_indptr + b);
@@ -167,9 +170,18 @@ __device__ bool make_plan(Shared& sm, const ScaledArgs& a, Plan& plan) {
   const uint32_t before = warp > 0 ? __shfl_sync(0xffffffffu, all, warp - 1) : 0;
   if (tid <= a.batch) sm.cost[tid] = before + (uint32_t)(upto - cost);
   if (tid == 0 && a.batch == kThreads) sm.cost[a.batch] = plan.length;
-  plan.lanes = (int)gridDim.x;
-  plan.share = (plan.length + plan.lanes - 1) / plan.lanes;
+  plan.share = (plan.length + gridDim.x - 1) / gridDim.x;
   if (plan.share == 0) plan.share = 1;
+  // the sequence that this CTA's share begins in
+  const uint32_t from = blockIdx.x * plan.share, at = before + (uint32_t)(upto - cost);  // (from: below length + share)
+  if (from >= at && from - at < (uint32_t)cost) {
+    const Seq s = seq_of(a, tid);
+    const uint32_t span = tiles_of(s.nk) + kFixed, g = (from - at) / span;
+    sm.first_seq = s;
+    sm.first_b = tid;
+    sm.first_g = (int)g;
+    sm.first_at = at + g * span;
+  }
   __syncthreads();
   return true;
 }
@@ -199,25 +211,18 @@ struct Units {
     at = b < a.batch ? sm.cost[b] : 0xFFFFFFFFu;
   }
   __device__ __forceinline__ Units(const Shared& sm, const ScaledArgs& a, const Plan& p) {
-    const uint32_t lane = blockIdx.x;
-    from = lane * p.share;  // (below the length plus one share: fits)
+    from = blockIdx.x * p.share;
     end = from + p.share < p.length ? from + p.share : p.length;
-    at = 0xFFFFFFFFu;
-    if ((int)lane >= p.lanes || from >= end) {
+    if (from >= end) {
       end = 0;
+      at = 0xFFFFFFFFu;
       return;
     }
-    int lo = 0, hi = a.batch;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (sm.cost[mid] <= from) lo = mid; else hi = mid;
-    }
-    enter(sm, a, lo);
-    if (at <= from) {
-      const uint32_t span = tiles_of(s.nk) + kFixed;
-      g = (int)((from - at) / span);
-      at += (uint32_t)g * span;
-    }
+    b = sm.first_b;
+    g = sm.first_g;
+    at = sm.first_at;
+    s = sm.first_seq;
+    n = row_blocks(a, s.nq);
   }
   __device__ __noinline__ bool next(const Shared& sm, const ScaledArgs& a, Unit& u) {
     while (at < end) {
@@ -267,6 +272,18 @@ __device__ __forceinline__ bool wait(Shared& sm, uint64_t* bar, uint32_t parity,
   return mbar_try_wait(bar, parity) || wait_slow(sm, bar, parity, a.wait_cycles, where);
 }
 
+// A position in the ring of chunks, and the parity of its round.
+struct Ring {
+  uint32_t slot = 0, parity = 0;
+  __device__ __forceinline__ Ring plus(uint32_t n) const {  // n < kSlots
+    Ring r;
+    const bool wrap = slot + n >= kSlots;
+    r.slot = wrap ? slot + n - kSlots : slot + n;
+    r.parity = parity ^ wrap;
+    return r;
+  }
+};
+
 // A barrier of the softmax warps that tells each whether `any` held in one of them.
 __device__ __forceinline__ bool soft_vote(bool any) {
   uint32_t r;
@@ -293,7 +310,9 @@ __device__ void load_role(Shared& sm, const Maps& maps, const ScaledArgs& a, Uni
   constexpr int kGroups = (kTile / 4 + kLoadWarps - 1) / kLoadWarps;  // of four keys, the warp's: warp, warp + 6 ..
   constexpr int kBoxes = kTile / kRun;
   const bool last_group = warp + kLoadWarps * (kGroups - 1) < kTile / 4;
-  const uint32_t full0 = smem_u32(&sm.full[0][0]), latent0 = smem_u32(sm.latent[0][0]), rope0 = smem_u32(sm.rope[0]);
+  const uint32_t full0 = smem_u32(&sm.full[0]), latent0 = smem_u32(sm.latent[0]), rope0 = smem_u32(sm.rope),
+                 rope_bar = smem_u32(&sm.rope_full);
+  Ring ring;  // of the tile's first chunk
   uint32_t it = 0;
   for (; more; more = units.next(sm, a, u)) {
     const int32_t* index = a.kv_indices + u.kv0;
@@ -304,7 +323,7 @@ __device__ void load_role(Shared& sm, const Maps& maps, const ScaledArgs& a, Uni
 #pragma unroll
     for (int k = 0; k < 4; ++k) ahead[k] = key + k < last ? __ldg(index + key + k) : -1;
 #pragma unroll 1
-    for (int t = 0; t < tiles; ++t, ++it) {
+    for (int t = 0; t < tiles; ++t, ++it, ring = ring.plus(kChunks)) {
       int32_t y[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -320,18 +339,18 @@ __device__ void load_role(Shared& sm, const Maps& maps, const ScaledArgs& a, Uni
       const int first = __shfl_sync(0xffffffffu, y[0], lane & ~3);
       const bool runs = __all_sync(0xffffffffu, y[0] == first + 4 * (lane & 3) && y[1] == y[0] + 1 && y[2] == y[0] + 2 &&
                                                     y[3] == y[0] + 3 && y[3] < none);
-      const uint32_t stage = it & 1, parity = (it >> 1) & 1;
       if (runs) {
         // warps 0 to 3 have a chunk each, 4 and 5 half of chunks 0 and 1, and the rotated columns
-        const int chunk = warp & 3, piece = chunk < kRopePiece ? chunk : chunk + 1;
+        const int chunk = warp & 3;
+        const Ring at = ring.plus(chunk);
         const bool upper = warp >= kChunks, whole = chunk >= kLoadWarps - kChunks;
         int32_t r[kBoxes];
 #pragma unroll
         for (int k = 0; k < kBoxes; ++k) r[k] = __shfl_sync(0xffffffffu, y[0], (upper ? k ^ (kBoxes / 2) : k) * (kRun / 4));
         const uint32_t at0 = upper ? kBoxes / 2 : 0;  // r[k]: box k ^ at0
-        if (!__all_sync(0xffffffffu, wait(sm, &sm.free[stage][piece], parity ^ 1, a, 100))) return;
+        if (!__all_sync(0xffffffffu, wait(sm, &sm.free[at.slot], at.parity ^ 1, a, 100))) return;
         if (elect_one()) {
-          const uint32_t bar = full0 + (stage * kPieces + piece) * 8, dst = latent0 + (stage * kChunks + chunk) * (kTile * 128);
+          const uint32_t bar = full0 + at.slot * 8, dst = latent0 + at.slot * (kTile * 128);
           if (!upper) mbar_arrive_expect_tx(bar, kTile * 128);
 #pragma unroll
           for (int k = 0; k < kBoxes; ++k)
@@ -339,15 +358,15 @@ __device__ void load_role(Shared& sm, const Maps& maps, const ScaledArgs& a, Uni
         }
         __syncwarp();
         if (upper) {
-          if (!__all_sync(0xffffffffu, wait(sm, &sm.free[stage][kRopePiece], parity ^ 1, a, 101))) return;
+          if (!__all_sync(0xffffffffu, wait(sm, &sm.rope_free, (it & 1) ^ 1, a, 101))) return;
           if (elect_one()) {
-            const uint32_t bar = full0 + (stage * kPieces + kRopePiece) * 8, dst = rope0 + stage * (kTile * 64);
-            if (warp == kChunks) mbar_arrive_expect_tx(bar, kTile * 64);
+            if (warp == kChunks) mbar_arrive_expect_tx(rope_bar, kTile * 64);
             // (boxes 4 to 7 by warp 4, which has them first, 0 to 3 by warp 5)
 #pragma unroll
             for (int k = 0; k < kBoxes / 2; ++k) {
               const int q = warp == kChunks ? k : k + kBoxes / 2;
-              tma_load_2d(dst + (q ^ at0) * kRun * 64, &maps.rope_run, kDv, warp == kChunks ? r[k] : r[k + kBoxes / 2], bar);
+              tma_load_2d(rope0 + (q ^ at0) * kRun * 64, &maps.rope_run, kDv, warp == kChunks ? r[k] : r[k + kBoxes / 2],
+                          rope_bar);
             }
           }
           __syncwarp();
@@ -362,10 +381,13 @@ __device__ void load_role(Shared& sm, const Maps& maps, const ScaledArgs& a, Uni
 #pragma unroll
       for (int piece = 0; piece < kPieces; ++piece) {
         const int chunk = piece < kRopePiece ? piece : piece - 1, row = piece == kRopePiece ? 64 : 128;
-        if (!__all_sync(0xffffffffu, wait(sm, &sm.free[stage][piece], parity ^ 1, a, 102))) return;
+        const Ring at = ring.plus(chunk);
+        if (!__all_sync(0xffffffffu, piece == kRopePiece ? wait(sm, &sm.rope_free, (it & 1) ^ 1, a, 102)
+                                                         : wait(sm, &sm.free[at.slot], at.parity ^ 1, a, 102)))
+          return;
         if (elect_one()) {
-          const uint32_t bar = full0 + (stage * kPieces + piece) * 8,
-                         dst = piece == kRopePiece ? rope0 + stage * (kTile * 64) : latent0 + (stage * kChunks + chunk) * (kTile * 128);
+          const uint32_t bar = piece == kRopePiece ? rope_bar : full0 + at.slot * 8,
+                         dst = piece == kRopePiece ? rope0 : latent0 + at.slot * (kTile * 128);
           if (warp == 0) mbar_arrive_expect_tx(bar, kTile * row);
 #pragma unroll
           for (int k = 0; k < kGroups; ++k)
@@ -378,9 +400,15 @@ __device__ void load_role(Shared& sm, const Maps& maps, const ScaledArgs& a, Uni
     }
   }
   // the pieces' last releases have arrived before the CTA may leave
-  if (warp == 0)
-    for (int k = 0; k < kStages; ++k, ++it)
-      for (int piece = 0; piece < kPieces; ++piece) wait(sm, &sm.free[it & 1][piece], ((it >> 1) & 1) ^ 1, a, 103);
+  // (each is waited for by a warp that filled its slot last: the first warp fills part of every tile's first chunk, and
+  // the later ones follow it)
+  if (warp == 0) {
+    for (uint32_t k = 0; k < kSlots; ++k) {
+      const Ring at = ring.plus(k);
+      wait(sm, &sm.free[at.slot], at.parity ^ 1, a, 103);
+    }
+    wait(sm, &sm.rope_free, (it & 1) ^ 1, a, 104);
+  }
   __syncwarp();
 }
 
@@ -392,34 +420,36 @@ __device__ __forceinline__ uint32_t desc_low(const void* at) { return smem_u32(a
 // Piece by piece as a tile's columns arrive.
 __device__ void score_role(Shared& sm, const ScaledArgs& a, uint32_t tmem, Units& units, Unit& u, bool more) {
   constexpr uint32_t kDesc = idesc_f8_f32(kTile, 2 * kRows, 0, 0, 0, 0);
-  const uint32_t latent_lo = desc_low(sm.latent[0][0]), rope_lo = desc_low(sm.rope[0]), q_latent_lo = desc_low(sm.q_latent[0]),
+  const uint32_t latent_lo = desc_low(sm.latent[0]), rope_lo = desc_low(sm.rope), q_latent_lo = desc_low(sm.q_latent[0]),
                  q_rope_lo = desc_low(sm.q_rope);
+  Ring ring;
   uint32_t it = 0, unit = 0;
   for (; more; more = units.next(sm, a, u), ++unit) {
     const int tiles = u.tiles;
     if (!__all_sync(0xffffffffu, wait(sm, &sm.qfull, unit & 1, a, 200))) return;
 #pragma unroll 1
-    for (int t = 0; t < tiles; ++t, ++it) {
-      const uint32_t stage = it & 1, parity = (it >> 1) & 1, d = tmem + kSCol + stage * 2 * kRows;
-      if (!__all_sync(0xffffffffu, wait(sm, &sm.sfree[stage], parity ^ 1, a, 201))) return;
+    for (int t = 0; t < tiles; ++t, ++it, ring = ring.plus(kChunks)) {
+      const uint32_t sb = it & 1, d = tmem + kSCol + sb * 2 * kRows;
+      if (!__all_sync(0xffffffffu, wait(sm, &sm.sfree[sb], ((it >> 1) & 1) ^ 1, a, 201))) return;
 #pragma unroll
       for (int piece = 0; piece < kPieces; ++piece) {
-        if (!__all_sync(0xffffffffu, wait(sm, &sm.full[stage][piece], parity, a, 202))) return;
+        const int chunk = piece < kRopePiece ? piece : piece - 1;
+        const Ring at = ring.plus(chunk);
+        if (!__all_sync(0xffffffffu, piece == kRopePiece ? wait(sm, &sm.rope_full, it & 1, a, 202)
+                                                         : wait(sm, &sm.full[at.slot], at.parity, a, 202)))
+          return;
         tc_fence_after();
         if (elect_one()) {
           if (piece == kRopePiece) {
-            const uint32_t key = rope_lo + stage * (kTile * 64 / 16);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) mma_ss_f8(d, key + 2 * i, kHi64, q_rope_lo + 2 * i, kHi64, kDesc, 1u);
-            mma_commit(&sm.free[stage][piece]);
+            for (int i = 0; i < 2; ++i) mma_ss_f8(d, rope_lo + 2 * i, kHi64, q_rope_lo + 2 * i, kHi64, kDesc, 1u);
+            mma_commit(&sm.rope_free);
           } else {
-            const int chunk = piece < kRopePiece ? piece : piece - 1;
-            const uint32_t key = latent_lo + (stage * kChunks + chunk) * (kTile * 128 / 16),
-                           q = q_latent_lo + chunk * (2 * kRows * 128 / 16);
+            const uint32_t key = latent_lo + at.slot * (kTile * 128 / 16), q = q_latent_lo + chunk * (2 * kRows * 128 / 16);
 #pragma unroll
             for (int i = 0; i < 4; ++i) mma_ss_f8(d, key + 2 * i, kHi128, q + 2 * i, kHi128, kDesc, piece > 0 || i > 0);
           }
-          if (piece == kPieces - 1) mma_commit(&sm.sfull[stage]);
+          if (piece == kPieces - 1) mma_commit(&sm.sfull[sb]);
         }
         __syncwarp();
       }
@@ -430,28 +460,29 @@ __device__ void score_role(Shared& sm, const ScaledArgs& a, uint32_t tmem, Units
 // A tile at a time; each chunk makes room for a later tile's.
 __device__ void value_role(Shared& sm, const ScaledArgs& a, uint32_t tmem, Units& units, Unit& u, bool more) {
   constexpr uint32_t kDesc = idesc_f8_f32(128, kOCols, 0, 1, 1, 1);
-  const uint32_t latent_lo = desc_low(sm.latent[0][0]), p_lo = desc_low(sm.p[0]);
+  const uint32_t latent_lo = desc_low(sm.latent[0]), p_lo = desc_low(sm.p);
+  Ring ring;
   uint32_t it = 0, unit = 0;
   for (; more; more = units.next(sm, a, u), ++unit) {
     const int tiles = u.tiles;
     // (the first product into O: the unit before has been read out)
     if (!__all_sync(0xffffffffu, wait(sm, &sm.ofree, (unit & 1) ^ 1, a, 210))) return;
 #pragma unroll 1
-    for (int t = 0; t < tiles; ++t, ++it) {
-      const uint32_t stage = it & 1, parity = (it >> 1) & 1;
-      if (!__all_sync(0xffffffffu, wait(sm, &sm.pfull[stage], parity, a, 211))) return;
+    for (int t = 0; t < tiles; ++t, ++it, ring = ring.plus(kChunks)) {
+      if (!__all_sync(0xffffffffu, wait(sm, &sm.pfull, it & 1, a, 211))) return;
       tc_fence_after();
       if (elect_one()) {
-        const uint32_t go_on = t > 0, p = p_lo + stage * (kTile * 128 / 16), v = latent_lo + stage * (kChunks * kTile * 128 / 16);
+        const uint32_t go_on = t > 0;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
+          const Ring at = ring.plus(c);
+          const uint32_t v = latent_lo + at.slot * (kTile * 128 / 16);
 #pragma unroll
           for (int i = 0; i < kTile / 32; ++i)
-            mma_ss_f8(tmem + c * kOCols, v + c * (kTile * 128 / 16) + 256 * i, kHi128, p + 256 * i, kHi128, kDesc,
-                      i > 0 ? 1u : go_on);
-          mma_commit(&sm.free[stage][c < kRopePiece ? c : c + 1]);
+            mma_ss_f8(tmem + c * kOCols, v + 256 * i, kHi128, p_lo + 256 * i, kHi128, kDesc, i > 0 ? 1u : go_on);
+          mma_commit(&sm.free[at.slot]);
         }
-        mma_commit(&sm.pfree[stage]);
+        mma_commit(&sm.pfree);
       }
       __syncwarp();
     }
@@ -495,34 +526,39 @@ __device__ __noinline__ float load_queries(Shared& sm, const ScaledArgs& a, cons
   int e = 8 - ((int)(bits >> 23) - 127) - ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   e = e > 108 ? 108 : e < -119 ? -119 : e;
   const float scale = __uint_as_float((uint32_t)(e + 127) << 23), back = __uint_as_float((uint32_t)(127 - e) << 23);
+  constexpr int kSide = 3;  // granules worked on side by side
+  static_assert(kEach % kSide == 0, "granules per thread");
 #pragma unroll 1
-  for (int k = 0; k < kEach; ++k) {
-    const int i = tid + k * kSoftThreads, row = i / kGranules, col = (i - row * kGranules) * 8;
-    const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+  for (int k = 0; k < kEach; k += kSide) {
 #pragma unroll
-    for (int j = 0; j + 1 < kEach; ++j) v[j] = v[j + 1];
-    uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float x0 = bf16_lo(w[j]) * scale, x1 = bf16_hi(w[j]) * scale;
-      uint16_t h, l;
-      uint32_t back2;
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(x1), "f"(x0));
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back2) : "h"(h));
-      float y0, y1;
-      asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;}"
-          : "=f"(y0), "=f"(y1)
-          : "r"(back2));
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(l) : "f"((x1 - y1) * 16.f), "f"((x0 - y0) * 16.f));
-      hi[j >> 1] |= (uint32_t)h << (16 * (j & 1));
-      lo[j >> 1] |= (uint32_t)l << (16 * (j & 1));
+    for (int side = 0; side < kSide; ++side) {
+      const int i = tid + (k + side) * kSoftThreads, row = i / kGranules, col = (i - row * kGranules) * 8;
+      const uint32_t w[4] = {v[side].x, v[side].y, v[side].z, v[side].w};
+      uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+  #pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float x0 = bf16_lo(w[j]) * scale, x1 = bf16_hi(w[j]) * scale;
+        uint16_t h, l;
+        uint32_t back2;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(x1), "f"(x0));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back2) : "h"(h));
+        float y0, y1;
+        asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;}"
+            : "=f"(y0), "=f"(y1)
+            : "r"(back2));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(l) : "f"((x1 - y1) * 16.f), "f"((x0 - y0) * 16.f));
+        hi[j >> 1] |= (uint32_t)h << (16 * (j & 1));
+        lo[j >> 1] |= (uint32_t)l << (16 * (j & 1));
+      }
+      // (rows r and kRows + r have the same swizzle)
+      uint8_t* dst = col < kDv ? sm.q_latent[col >> 7] + row * 128 + ((((col & 127) >> 4) ^ (row & 7)) << 4)
+                               : sm.q_rope + row * 64 + ((((col - kDv) >> 4) ^ ((row >> 1) & 3)) << 4);
+      dst += col & 8;
+      *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(dst + kRows * (col < kDv ? 128 : 64)) = make_uint2(lo[0], lo[1]);
     }
-    // (rows r and kRows + r have the same swizzle)
-    uint8_t* dst = col < kDv ? sm.q_latent[col >> 7] + row * 128 + ((((col & 127) >> 4) ^ (row & 7)) << 4)
-                             : sm.q_rope + row * 64 + ((((col - kDv) >> 4) ^ ((row >> 1) & 3)) << 4);
-    dst += col & 8;
-    *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-    *reinterpret_cast<uint2*>(dst + kRows * (col < kDv ? 128 : 64)) = make_uint2(lo[0], lo[1]);
+#pragma unroll
+    for (int j = 0; j + kSide < kEach; ++j) v[j] = v[j + kSide];
   }
   if (tid < kRows) {
     uint64_t word = 0;
@@ -680,7 +716,7 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
         }
         if (t > 0) {
           // what has been summed so far, once the products before are complete
-          wait(sm, &sm.pfree[(it - 1) % kStages], ((it - 1) / kStages) & 1, a, 301);
+          wait(sm, &sm.pfree, (it - 1) & 1, a, 301);
           __syncwarp();
           tc_fence_after();
 #pragma unroll 1
@@ -728,17 +764,16 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
 #pragma unroll
         for (int q = 0; q < kParts; ++q) parts[q][k] = __byte_perm(h[0][q], h[1][q], 0x7531);
       }
-      const int pb = it % kStages;
-      if (wait(sm, &sm.pfree[pb], ((it / kStages) & 1) ^ 1, a, 302)) {
+      if (wait(sm, &sm.pfree, (it & 1) ^ 1, a, 302)) {
 #pragma unroll
         for (int q = 0; q < kParts; ++q) {
-          uint8_t* dst = sm.p[pb] + my_key * 128 + (((2 * q + (row0 >> 4)) ^ (my_key & 7)) << 4);
+          uint8_t* dst = sm.p + my_key * 128 + (((2 * q + (row0 >> 4)) ^ (my_key & 7)) << 4);
           *reinterpret_cast<uint4*>(dst) = make_uint4(parts[q][0], parts[q][1], parts[q][2], parts[q][3]);
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.pfull[pb]);
+      if (lane == 0) mbar_arrive(&sm.pfull);
       scale = next_scale;
     }
     // row sums over the keys; what the rows' results are scaled by
@@ -764,7 +799,7 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
     // the next unit's queries while this one's last products run
     more = units.next(sm, a, u);
     if (more) factor = load_queries(sm, a, u);
-    wait(sm, &sm.pfree[(it - 1) % kStages], ((it - 1) / kStages) & 1, a, 303);
+    wait(sm, &sm.pfree, (it - 1) & 1, a, 303);
     __syncwarp();
     tc_fence_after();
 #pragma unroll 1
@@ -815,16 +850,18 @@ scaled_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ScaledA
     tmem_relinquish();
   }
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      for (int k = 0; k < kPieces; ++k) {
-        mbar_init(&sm.full[s][k], 1);
-        mbar_init(&sm.free[s][k], 1);
-      }
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.free[s], 1);
+    }
+    mbar_init(&sm.rope_full, 1);
+    mbar_init(&sm.rope_free, 1);
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.sfull[s], 1);
       mbar_init(&sm.sfree[s], kSoftWarps);
-      mbar_init(&sm.pfull[s], kSoftWarps);
-      mbar_init(&sm.pfree[s], 1);
     }
+    mbar_init(&sm.pfull, kSoftWarps);
+    mbar_init(&sm.pfree, 1);
     mbar_init(&sm.qfull, kSoftWarps);
     mbar_init(&sm.ofree, kSoftWarps);
     sm.abort_flag = 0;
