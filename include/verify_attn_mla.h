@@ -454,8 +454,8 @@ int verify_attn_mla_append(const void* latent, int64_t latent_stride, const void
  * +-inf is coded as the largest code, NaN as the NaN code, which the attention
  * does not accept.
  * The tokens of one block stand together in the call, their slots ascending
- * (as verify_attn_mla_step_tables lists them); tokens of a block that stand
- * apart would set its scale twice, in either order.  A token left out by an
+ * (as verify_attn_mla_step_tables lists them; padding may stand between them);
+ * tokens of a block that stand apart would set its scale twice, in either order.  A token left out by an
  * error takes no part in its block's scale.  Appending the same rows again
  * leaves the pool and the scales as they are. */
 int verify_attn_mla_append_scaled(const void* latent, int64_t latent_stride, const void* k_rope, int64_t k_rope_stride,

@@ -130,8 +130,10 @@ __device__ void append_runs(const AppendArgs& a, int64_t w0, int window, RunShar
     const int64_t t = w0 + tid;
     const int32_t slot = __ldg(a.slots + t);
     if (slot_ok(a, slot)) {
-      const int32_t prev = t > 0 ? __ldg(a.slots + t - 1) : -1;
-      if (!slot_ok(a, prev) || (prev >> shift) != (slot >> shift)) s.start[atomicAdd(&s.starts, 1)] = tid;
+      // (tokens without a slot may stand between those of a block)
+      int64_t before = t - 1;
+      while (before >= 0 && !slot_ok(a, __ldg(a.slots + before))) --before;
+      if (before < 0 || (__ldg(a.slots + before) >> shift) != (slot >> shift)) s.start[atomicAdd(&s.starts, 1)] = tid;
       const int32_t pos = __ldg(a.positions + t);
       if (!(pos >= 0 && (int64_t)pos < a.table_rows)) record_status(a.status, VMLA_ERR_INDEX, (uint32_t)t);
     } else if (slot != -1) {
@@ -143,37 +145,36 @@ __device__ void append_runs(const AppendArgs& a, int64_t w0, int window, RunShar
   for (int i = 0; i < starts; ++i) {
     const int64_t t0 = w0 + s.start[i];
     const int32_t block = __ldg(a.slots + t0) >> shift;
-    // its length: up to the first token of another block (a block's slots at most), and its first used row
-    {
-      bool in = tid < a.block && t0 + tid < a.tokens;
-      int32_t slot = -1, pos = -1;
-      if (in) {
-        slot = __ldg(a.slots + t0 + tid);
-        pos = __ldg(a.positions + t0 + tid);
-        in = slot_ok(a, slot) && (slot >> shift) == block;
-      }
-      const unsigned inside = __ballot_sync(0xffffffffu, in);
-      const int len = inside == 0xffffffffu ? 32 : __ffs(~inside) - 1;  // tokens up to the first that is not in
-      const unsigned used = __ballot_sync(0xffffffffu, lane < len && pos >= 0 && (int64_t)pos < a.table_rows);
+    // its length: up to the first token of another block, and the first row that it brings
+    int n = 0, first = -1;
+    for (bool more = true; more;) {
+      const int64_t t = t0 + n + tid;
+      const int32_t slot = t < a.tokens ? __ldg(a.slots + t) : -1, pos = t < a.tokens ? __ldg(a.positions + t) : -1;
+      const bool in = slot_ok(a, slot) && (slot >> shift) == block, ends = t >= a.tokens || (slot_ok(a, slot) && !in);
+      const unsigned end = __ballot_sync(0xffffffffu, ends);
+      const int len = end ? __ffs(end) - 1 : 32;
+      const unsigned used = __ballot_sync(0xffffffffu, in && lane < len && pos >= 0 && (int64_t)pos < a.table_rows);
       const int32_t at = __shfl_sync(0xffffffffu, slot & mask, used ? __ffs(used) - 1 : 0);
       if (lane == 0) {
         s.warp_len[warp] = len;
         s.first[warp] = used ? at : -1;
       }
-    }
-    __syncthreads();
-    int n = 0, first = -1;
+      __syncthreads();
+      const int n0 = n;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      if (n == 32 * w) {
-        n += s.warp_len[w];
-        if (first < 0) first = s.first[w];
-      }
+      for (int w = 0; w < kWarps; ++w)
+        if (n == n0 + 32 * w) {
+          n += s.warp_len[w];
+          if (first < 0) first = s.first[w];
+        }
+      more = n == n0 + kThreads;
+      __syncthreads();
+    }
     const float old = first < 0 ? 0.f : a.kv_scales[block];
     float m = 0.f;
     for (int k = warp; k < n; k += kWarps) {
       const int32_t pos = __ldg(a.positions + t0 + k);
-      if (pos >= 0 && (int64_t)pos < a.table_rows) {
+      if (slot_ok(a, __ldg(a.slots + t0 + k)) && pos >= 0 && (int64_t)pos < a.table_rows) {
         Row r;
         load_row(a, t0 + k, pos, lane, r);
         m = fmaxf(m, largest(r, lane));
@@ -201,11 +202,11 @@ __device__ void append_runs(const AppendArgs& a, int64_t w0, int window, RunShar
     }
     if (tid == 0 && first >= 0) a.kv_scales[block] = scale;
     for (int k = warp; k < n; k += kWarps) {
-      const int32_t pos = __ldg(a.positions + t0 + k);
-      if (pos >= 0 && (int64_t)pos < a.table_rows) {
+      const int32_t pos = __ldg(a.positions + t0 + k), slot = __ldg(a.slots + t0 + k);
+      if (slot_ok(a, slot) && pos >= 0 && (int64_t)pos < a.table_rows) {
         Row r;
         load_row(a, t0 + k, pos, lane, r);
-        store_row(a, __ldg(a.slots + t0 + k), lane, r, scale);
+        store_row(a, slot, lane, r, scale);
       }
     }
     __syncthreads();

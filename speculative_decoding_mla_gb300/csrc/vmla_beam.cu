@@ -6,17 +6,18 @@
 // and the K best over all (w, v) are kept, in descending order, equal ones by the index w vocab + v.
 //
 // Within a beam the order is the logits' own, so a row's first K tokens by (logit, index) are all that can be kept.
-// The first kernel reads each row once: a thread sums 2^(x log2 e - r) against a reference r of its own (raised when
-// a granule's maximum passes it by 2^30) and remembers its largest granule, (maximum, place).  The K-th largest of
+// The first kernel reads each row once: a thread sums exp(x - r) against a reference r of its own, a logit (raised when
+// a granule's maximum passes it by 20) and remembers its largest granule, (maximum, place).  The K-th largest of
 // the threads' granules bounds the row's K-th token from below, and no token above the bound lies outside the K
 // threads that have these granules: only their granules are read again (from L2), the tokens above the bound listed,
 // and the list ranked.  Rows are cut into parts, one CTA each, while that is needed to fill the GPU.
 // The second kernel, a CTA per request, joins the parts' sums and merges the sorted lists: K rounds of one warp.
 //
 // Scores of different beams are compared through lse_w, and the single-precision terms put it off by up to about
-// 4e-6 (margin_of).  Where two neighbours of the merged order, of different beams, lie closer than that, the request's
-// CTA sums the beams concerned again in whole units (weight_units, exact in any order: equal rows have equal sums
-// wherever they lie) and merges anew.  Scores closer than about 2^-27 are not told apart for certain.
+// 4e-6 (kMargin).  Where two neighbours of the merged order, or the last of it and one that is left out, are of
+// different beams and lie closer than that, the request's CTA sums the beams concerned again in whole units
+// (weight_units, exact in any order: equal rows have equal sums wherever they lie) and merges anew, until no beam is
+// left in doubt.  Scores closer than about 2^-27 are not told apart for certain.
 //
 // The logits bound it: 2 or 4 bytes a token in, and about four instructions.
 #include <cuda_runtime.h>
@@ -38,9 +39,9 @@ constexpr int kList = 2048;      // tokens above the bound that are ranked at on
 constexpr int kFlush = 8;        // granules whose sum stays in single precision
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr double kLn2 = 0.69314718055994530942;
-static_assert(kMaxKeep <= 32, "one warp merges");
+static_assert(kMaxKeep <= kThreads, "a thread per place");
 
-// One part of a row: the sum of 2^(x log2 e - ref), tokens at +inf, and the first n tokens as sorted keys.
+// One part of a row: the sum of exp(x - ref), tokens at +inf, and the first n tokens as sorted keys.
 struct alignas(16) RowPart {
   double sum;
   float ref;
@@ -81,6 +82,10 @@ struct Row {
   __device__ __forceinline__ static float value(float v) { return v; }
   // granule g's logits, -inf outside the row
   __device__ __forceinline__ void get(int g, float (&x)[kVec]) const {
+    if (whole(g)) {
+      unpack(__ldg(reinterpret_cast<const uint4*>(first) + g), x);
+      return;
+    }
 #pragma unroll
     for (int k = 0; k < kVec; ++k) {
       const int i = g * kVec + k - lead;
@@ -119,21 +124,20 @@ struct Acc {
       place = g;
     }
     if (!(m > -INFINITY)) return;
-    const float top = m * kLog2e;
-    if (top > ref + 30.f) {
+    if (m > ref + 20.f) {
       if (m == INFINITY) {  // those tokens share the row evenly
 #pragma unroll
         for (int k = 0; k < N; ++k) infinite += x[k] == INFINITY;
         return;
       }
-      const float f = ex2_approx(ref - top);
+      const float f = ex2_approx((ref - m) * kLog2e);
       total *= (double)f;
       sum *= f;
-      ref = top;
+      ref = m;
     }
     float e[N];
 #pragma unroll
-    for (int k = 0; k < N; ++k) e[k] = ex2_approx(fmaf(x[k], kLog2e, -ref));
+    for (int k = 0; k < N; ++k) e[k] = ex2_approx((x[k] - ref) * kLog2e);
 #pragma unroll
     for (int s = N / 2; s > 0; s >>= 1)
 #pragma unroll
@@ -141,7 +145,7 @@ struct Acc {
     if (e[0] != e[0]) {  // NaN counts as -inf
       float y = 0.f;
 #pragma unroll
-      for (int k = 0; k < N; ++k) y += x[k] > -INFINITY ? ex2_approx(fmaf(x[k], kLog2e, -ref)) : 0.f;
+      for (int k = 0; k < N; ++k) y += x[k] > -INFINITY ? ex2_approx((x[k] - ref) * kLog2e) : 0.f;
       e[0] = y;
     }
     sum += e[0];
@@ -153,7 +157,7 @@ struct Acc {
 };
 
 struct RowShared {
-  uint64_t key[kThreads];
+  alignas(16) uint64_t key[kThreads];
   uint64_t list[kList];
   uint64_t warp_key[kWarps];
   int32_t thread[kMaxKeep];
@@ -188,15 +192,24 @@ beam_rows_kernel(const BeamArgs a, RowPart* __restrict__ out, int parts) {
   const int all = row.granules(), per = (all + parts - 1) / parts;
   const int g0 = part * per, g1 = min(all, g0 + per);
   Acc acc;
+  // four granules at a time, the next four on their way meanwhile
   constexpr int kAhead = 4;
-  int since = 0;
-  for (int g = g0 + tid; g < g1; g += kAhead * kThreads) {
-    uint4 v[kAhead];
+  uint4 next[kAhead];
+  auto fetch = [&](int g) {
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int h = g + k * kThreads;
-      if (h < g1 && row.whole(h)) v[k] = __ldg(reinterpret_cast<const uint4*>(row.first) + h);
+      if (h < g1 && row.whole(h)) next[k] = __ldg(reinterpret_cast<const uint4*>(row.first) + h);
     }
+  };
+  fetch(g0 + tid);
+  int since = 0;
+#pragma unroll 1
+  for (int g = g0 + tid; g < g1; g += kAhead * kThreads) {
+    uint4 v[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) v[k] = next[k];
+    fetch(g + kAhead * kThreads);
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int h = g + k * kThreads;
@@ -222,7 +235,7 @@ beam_rows_kernel(const BeamArgs a, RowPart* __restrict__ out, int parts) {
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) ref = fmaxf(ref, s.warp_f[w]);
-  double total = acc.ref > -INFINITY ? acc.total * (double)ex2_approx(acc.ref - ref) : 0.0;
+  double total = acc.ref > -INFINITY ? acc.total * (double)ex2_approx((acc.ref - ref) * kLog2e) : 0.0;
   uint32_t infinite = acc.infinite;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -237,7 +250,11 @@ beam_rows_kernel(const BeamArgs a, RowPart* __restrict__ out, int parts) {
   const int keep = a.keep;
   if (mine != 0) {
     int above = 0;
-    for (int k = 0; k < kThreads; ++k) above += s.key[k] > mine;
+#pragma unroll 8
+    for (int k = 0; k < kThreads; k += 2) {
+      const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(&s.key[k]);
+      above += (two.x > mine) + (two.y > mine);
+    }
     if (above < keep) {
       s.thread[above] = tid;
       atomicMax(&s.chosen, (uint32_t)above + 1);
@@ -318,17 +335,47 @@ beam_rows_kernel(const BeamArgs a, RowPart* __restrict__ out, int parts) {
 }
 
 struct JoinShared {
-  double base[kMaxBeams];      // c_w - lse_w; beams with tokens at +inf: c_w - ln of their count
+  double base[kMaxBeams];      // c_w - ln of the sum of exp(x - ref); beams with tokens at +inf: c_w - ln of their count
   float ref[kMaxBeams];
   bool infinite[kMaxBeams];
   float2 table[64];
   unsigned long long sum[kMaxBeams];
-  uint32_t unsure;             // beams whose neighbours in the order lie too close
+  uint32_t unsure;             // beams whose neighbours in the order lie too close, and whose sum is not exact yet
+  uint32_t exact;              // beams whose sum is
+  alignas(16) uint64_t top[kThreads];  // each thread's best score
+  uint32_t top_index[kThreads];
+  uint64_t order[kMaxKeep];            // the best scores in order, and their indexes
+  uint32_t index[kMaxKeep];
+  uint64_t bound;
+  uint32_t bound_index, chosen, listed;
 };
 
-// By how much a beam's lse may be off: the terms' errors (ex2.approx 2.4e-7, its argument 2e-7, a tree of eight and
-// a running sum of eight 6.6e-7, two more factors 5e-7) and log2 e as a float, 1.4e-8 of the logits' size.
-__device__ __forceinline__ double margin_of(float ref) { return 2e-6 + 1.5e-8 * (fabs((double)ref) + 30.0); }
+// Order of scores as whole numbers: 0 for none.
+__device__ __forceinline__ uint64_t ordered64(double v) {
+  if (!(v > -INFINITY)) return 0;
+  const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
+  return u >> 63 ? ~u : u | 1ull << 63;
+}
+__device__ __forceinline__ double ordered64_value(uint64_t k) {
+  return __longlong_as_double((long long)(k >> 63 ? k & ~(1ull << 63) : ~k));
+}
+// Whether (score, index) a comes before b.
+__device__ __forceinline__ bool before(uint64_t a, uint32_t ia, uint64_t b, uint32_t ib) {
+  return a > b || (a == b && ia < ib);
+}
+
+// By how much a beam's score may be off: the terms' errors (ex2.approx 2.4e-7; its argument, log2 e as a float among
+// it, d 1.4e-7 for a term e^-d; a tree of eight and a running sum of eight 6.6e-7; two more factors 5e-7).
+constexpr double kMargin = 2e-6;
+
+// Notes beams w and v whose scores a >= b lie closer than their sums are known to.
+__device__ __forceinline__ void doubt(JoinShared& s, uint64_t a, int w, uint64_t b, int v) {
+  if (w == v) return;
+  const uint32_t open = (1u << w | 1u << v) & ~s.exact;
+  if (open == 0) return;
+  const double margin = kMargin * __popc(open);
+  if (ordered64_value(a) - ordered64_value(b) <= margin) atomicOr(&s.unsure, open);
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
@@ -336,11 +383,12 @@ beam_join_kernel(const BeamArgs a, const RowPart* __restrict__ in, int parts, co
   extern __shared__ uint64_t keys[];  // [beams x parts][keep]
   __shared__ JoinShared s;
   __shared__ int32_t count[kMaxBeams * kMaxParts];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x;
   const int W = a.beams, K = a.keep, V = a.vocab, lists = W * parts;
   const int64_t request = blockIdx.x;
   if (tid < 64) s.table[tid] = exp_table.t[tid];
-  if (tid == 0) s.unsure = 0;
+  if (tid == 0) s.exact = 0;
+  grid_dependents_launch();
   grid_dependency_wait();
   const RowPart* rows = in + request * lists;
   for (int l = tid; l < lists; l += kThreads) count[l] = (int)rows[l].n;
@@ -366,11 +414,11 @@ beam_join_kernel(const BeamArgs a, const RowPart* __restrict__ in, int parts, co
       double sum = 0.0;
       for (int p = 0; p < parts; ++p) {
         const RowPart& r = rows[tid * parts + p];
-        if (r.ref > -INFINITY) sum += r.sum * (double)ex2_approx(r.ref - ref);
+        if (r.ref > -INFINITY) sum += r.sum * (double)ex2_approx((r.ref - ref) * kLog2e);
       }
       s.ref[tid] = ref > -INFINITY ? ref : 0.f;
       s.infinite[tid] = infinite > 0;
-      s.base[tid] = infinite ? (double)c - log((double)infinite) : (double)c - (double)s.ref[tid] * kLn2 - log(sum);
+      s.base[tid] = (double)c - log(infinite ? (double)infinite : sum);
     }
   }
   __syncthreads();
@@ -380,96 +428,100 @@ beam_join_kernel(const BeamArgs a, const RowPart* __restrict__ in, int parts, co
     count[tid * parts] = 1;
   }
   __syncthreads();
-  // the merge, by one warp: a lane has every 32nd list
-  for (int pass = 0; pass < 2; ++pass) {
-    if (warp == 0) {
-      int at[kMaxBeams * kMaxParts / 32];
-      // a list's next token: its score (-inf: none) and index
-      auto head = [&](int l, int k, double& value, int& index) {
-        value = -INFINITY;
-        index = INT32_MAX;
-        if (k < count[l]) {
-          const uint64_t key = keys[l * K + k];
-          const int w = l / parts;
-          const float x = ordered_value((uint32_t)(key >> 32));
-          if (!s.infinite[w] || x == INFINITY) {
-            value = s.base[w] + (s.infinite[w] ? 0.0 : (double)x);
-            index = w * V + (int)~(uint32_t)key;
-          }
-        }
-      };
-      double best = -INFINITY;
-      int index = INT32_MAX, list = 0;
-      auto choose = [&]() {
-        best = -INFINITY;
-        index = INT32_MAX;
-#pragma unroll
-        for (int i = 0; i < kMaxBeams * kMaxParts / 32; ++i) {
-          const int l = lane + 32 * i;
-          if (l < lists) {
-            double v;
-            int x;
-            head(l, at[i], v, x);
-            if (v > best || (v == best && x < index)) {
-              best = v;
-              index = x;
-              list = i;
-            }
-          }
-        }
-      };
-#pragma unroll
-      for (int i = 0; i < kMaxBeams * kMaxParts / 32; ++i) at[i] = 0;
-      choose();
-      uint32_t unsure = 0;
-      double last = INFINITY;
-      int last_beam = -1;
-      for (int k = 0; k <= K; ++k) {  // (the one after the last only for its distance)
-        double v = best;
-        int x = index;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          const double v2 = __shfl_xor_sync(0xffffffffu, v, o);
-          const int x2 = __shfl_xor_sync(0xffffffffu, x, o);
-          if (v2 > v || (v2 == v && x2 < x)) {
-            v = v2;
-            x = x2;
-          }
-        }
-        const bool none = !(v > -INFINITY);
-        const int w = none ? -1 : x / V;
-        if (!none && k > 0 && w != last_beam && last - v < margin_of(s.ref[w]) + margin_of(s.ref[last_beam]))
-          unsure |= 1u << w | 1u << last_beam;
-        if (k == K) break;
-        if (lane == 0) {
-          const int64_t o = request * K + k;
-          a.parent[o] = w;
-          a.token[o] = none ? -1 : x - w * V;
-          a.new_score[o] = none ? -INFINITY : (float)v;
-        }
-        if (!none && index == x) {
-#pragma unroll
-          for (int i = 0; i < kMaxBeams * kMaxParts / 32; ++i) at[i] += i == list;
-          choose();
-        }
-        if (none) {
-          // nothing is left: the remaining places hold no token
-          if (lane == 0)
-            for (int j = k + 1; j < K; ++j) {
-              a.parent[request * K + j] = -1;
-              a.token[request * K + j] = -1;
-              a.new_score[request * K + j] = -INFINITY;
-            }
-          break;
-        }
-        last = v;
-        last_beam = w;
+  // the K best: as for a row, the threads' best ones bound them, the entries at or above the bound are listed (at most K
+  // threads', of up to 32 entries each) and ranked
+  const int entries = lists * K;
+  auto score_of = [&](int i, uint32_t& index) -> uint64_t {
+    const int l = i / K, w = l / parts;
+    if (i - l * K >= count[l]) return 0;
+    const uint64_t key = keys[i];
+    const float x = ordered_value((uint32_t)(key >> 32));
+    if (s.infinite[w] && x != INFINITY) return 0;
+    index = (uint32_t)(w * V) + ~(uint32_t)key;
+    return ordered64(s.base[w] + (s.infinite[w] ? 0.0 : (double)x - (double)s.ref[w]));
+  };
+  uint64_t* const list = keys + entries;                                 // [K x rounds] scores, then their indexes
+  const int rounds = (entries + kThreads - 1) / kThreads;
+  uint32_t* const list_index = reinterpret_cast<uint32_t*>(list + (size_t)K * rounds);
+  for (int pass = 0; pass <= W; ++pass) {
+    uint64_t best = 0;
+    uint32_t best_index = 0xffffffffu;
+    for (int i = tid; i < entries; i += kThreads) {
+      uint32_t x = 0;
+      const uint64_t v = score_of(i, x);
+      if (v != 0 && before(v, x, best, best_index)) {
+        best = v;
+        best_index = x;
       }
-      if (lane == 0) s.unsure = pass == 0 ? unsure : 0;
+    }
+    s.top[tid] = best;
+    s.top_index[tid] = best_index;
+    if (tid < K) s.order[tid] = 0;
+    if (tid == 0) s.chosen = s.listed = s.unsure = 0;
+    __syncthreads();
+    if (best != 0) {
+      const int threads = entries < kThreads ? entries : kThreads;
+      int above = 0;
+#pragma unroll 4
+      for (int k = 0; k < threads; ++k) above += before(s.top[k], s.top_index[k], best, best_index);
+      if (above < K) {
+        atomicMax(&s.chosen, (uint32_t)above + 1);
+        if (above == K - 1) {
+          s.bound = best;
+          s.bound_index = best_index;
+        }
+      }
+    }
+    __syncthreads();
+    const bool bounded = (int)s.chosen == K;
+    const uint64_t bound = bounded ? s.bound : 0;
+    const uint32_t bound_index = bounded ? s.bound_index : 0xffffffffu;
+    for (int i = tid; i < entries; i += kThreads) {
+      uint32_t x = 0;
+      const uint64_t v = score_of(i, x);
+      if (v != 0 && !before(bound, bound_index, v, x)) {
+        const uint32_t at = atomicAdd(&s.listed, 1u);
+        list[at] = v;
+        list_index[at] = x;
+      }
+    }
+    __syncthreads();
+    const int listed = (int)s.listed;
+    for (int i = tid; i < listed; i += kThreads) {
+      const uint64_t v = list[i];
+      const uint32_t x = list_index[i];
+      int above = 0;
+#pragma unroll 4
+      for (int k = 0; k < listed; ++k) above += before(list[k], list_index[k], v, x);
+      if (above < K) {
+        s.order[above] = v;
+        s.index[above] = x;
+      }
+    }
+    __syncthreads();
+    if (tid < K) {
+      const uint64_t v = s.order[tid];
+      const int x = (int)s.index[tid], w = v ? x / V : -1;
+      const int64_t o = request * K + tid;
+      a.parent[o] = w;
+      a.token[o] = v ? x - w * V : -1;
+      a.new_score[o] = v ? (float)ordered64_value(v) : -INFINITY;
+      if (tid > 0 && v != 0) doubt(s, s.order[tid - 1], (int)s.index[tid - 1] / V, v, w);
+    }
+    const uint64_t last = s.order[K - 1];
+    if (last != 0) {
+      const uint32_t last_index = s.index[K - 1];
+      for (int i = tid; i < entries; i += kThreads) {
+        uint32_t x = 0;
+        const uint64_t v = score_of(i, x);
+        if (v != 0 && before(last, last_index, v, x)) doubt(s, last, (int)last_index / V, v, (int)x / V);
+      }
     }
     __syncthreads();
     uint32_t unsure = s.unsure;
     if (unsure == 0) break;
+    __syncthreads();
+    if (tid == 0) s.exact |= unsure;
     // the sums of the beams concerned again, exactly
     for (; unsure != 0; unsure &= unsure - 1) {
       const int w = __ffs(unsure) - 1;
@@ -489,8 +541,10 @@ beam_join_kernel(const BeamArgs a, const RowPart* __restrict__ in, int parts, co
       }
       atomicAdd(&s.sum[w], sum);
       __syncthreads();
-      if (tid == 0)
-        s.base[w] = (double)a.score[request * W + w] - (double)e.max - (log((double)s.sum[w]) - kUnitBits * kLn2);
+      if (tid == 0) {
+        s.ref[w] = e.max;
+        s.base[w] = (double)a.score[request * W + w] - (log((double)s.sum[w]) - kUnitBits * kLn2);
+      }
     }
     __syncthreads();
   }
@@ -499,6 +553,7 @@ beam_join_kernel(const BeamArgs a, const RowPart* __restrict__ in, int parts, co
 // Rows of 32-bit words, `length` of each (or all), from the parents' to the children's places.
 __global__ void __launch_bounds__(kThreads)
 beam_reorder_kernel(const ReorderArgs a, int64_t rows) {
+  grid_dependency_wait();
   for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
     const int64_t request = r / a.keep;
     const int p = a.parent[r];
@@ -523,6 +578,7 @@ beam_reorder_kernel(const ReorderArgs a, int64_t rows) {
     int64_t from = 0;
     if (((reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst)) & 15) == 0) {
       const int64_t whole = n / 4;
+#pragma unroll 2
       for (int64_t i = me; i < whole; i += step)
         reinterpret_cast<uint4*>(dst)[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
       from = whole * 4;
@@ -531,10 +587,10 @@ beam_reorder_kernel(const ReorderArgs a, int64_t rows) {
   }
 }
 
-// CTAs per row of logits: enough to fill the GPU twice over, each with at least 4096 tokens.
+// CTAs per row of logits: three for each SM, as far as each has 4096 tokens.
 int parts_of(int64_t rows, int vocab, int sms) {
   int parts = 1;
-  while (parts < kMaxParts && rows * parts < sms && vocab / (parts * 2) >= 4096) parts *= 2;
+  while (parts < kMaxParts && rows * parts < 3 * (int64_t)sms && vocab / (parts * 2) >= 4096) parts *= 2;
   return parts;
 }
 
@@ -548,13 +604,15 @@ int launch_select(const BeamArgs& a, int64_t requests, int parts, void* workspac
   cudaLaunchAttribute attr[1] = {early_start_attribute()};
   cfg.gridDim = dim3((unsigned)requests, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = (size_t)a.beams * parts * a.keep * 8;
+  const size_t entries = (size_t)a.beams * parts * a.keep;
+  const auto bytes = [](size_t n, size_t keep) { return n * 8 + keep * ((n + kThreads - 1) / kThreads) * 12; };
+  cfg.dynamicSmemBytes = bytes(entries, a.keep);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cfg.dynamicSmemBytes > 32768 &&
       cudaFuncSetAttribute(beam_join_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kMaxBeams * kMaxParts * kMaxKeep * 8) != cudaSuccess)
+                           (int)bytes(kMaxBeams * kMaxParts * kMaxKeep, kMaxKeep)) != cudaSuccess)
     return VMLA_ERR_CUDA;
   return cudaLaunchKernelEx(&cfg, beam_join_kernel<T>, a, (const RowPart*)part, parts, exp_table()) == cudaSuccess
              ? VMLA_OK
@@ -581,10 +639,16 @@ int launch_beam_reorder(const ReorderArgs& a, int64_t requests, int sms, void* s
   if (rows == 0) return VMLA_OK;
   const int64_t wide = (a.row_words + 4 * kThreads - 1) / (4 * kThreads);
   const unsigned y = (unsigned)(rows < 65535 ? rows : 65535);
-  const int64_t most = (8 * (int64_t)sms + y - 1) / y;
+  const int64_t most = (16 * (int64_t)sms + y - 1) / y;
   const unsigned x = (unsigned)(wide < 1 ? 1 : wide < most ? wide : most);
-  beam_reorder_kernel<<<dim3(x, y, 1), kThreads, 0, (cudaStream_t)stream>>>(a, rows);
-  return cudaGetLastError() == cudaSuccess ? VMLA_OK : VMLA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1] = {early_start_attribute()};
+  cfg.gridDim = dim3(x, y, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = (cudaStream_t)stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, beam_reorder_kernel, a, rows) == cudaSuccess ? VMLA_OK : VMLA_ERR_CUDA;
 }
 
 }  // namespace vmla
