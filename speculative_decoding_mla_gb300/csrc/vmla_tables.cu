@@ -23,7 +23,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPerThread = VMLA_MAX_BATCH / kThreads;
-constexpr int kVec = 4;  // keys of a thread, one 16-byte store where the array is aligned
+constexpr int kVec = 4;                    // keys of a lane together, one 16-byte store where the array is aligned
+constexpr int kSide = 2;                   // such quads that a lane looks up side by side
+constexpr int kRound = 32 * kVec * kSide;  // keys of a warp at a time
 static_assert(VMLA_MAX_BATCH % kThreads == 0, "requests per thread");
 
 struct Sums {
@@ -122,44 +124,61 @@ tables_kernel(const TablesArgs a) {
   }
   __syncthreads();
   const int32_t n_kv = fits ? s.kv[a.batch] : 0, n_q = fits ? s.qo[a.batch] : 0, n_new = fits ? s.grown[a.batch] : 0;
-  // block k of request b (-1: the table's entry is no block, or its slots pass 2^31)
+  // block k of request b, and the slot of position p in it (-1: no block, or its slots pass 2^31)
+  const int32_t mask = a.block - 1;
+  const uint32_t last_block = (uint32_t)INT32_MAX >> a.block_shift;
   auto block_of = [&](int b, int k) -> int32_t {
     const int h = s.have[b];
     return k < h ? a.table[(int64_t)b * a.table_stride + k] : a.free_blocks[count - 1 - (s.grown[b] + (k - h))];
   };
   auto slot_in = [&](int32_t block, int p) -> int32_t {
-    const int64_t v = ((int64_t)block << a.block_shift) + (p & (a.block - 1));
-    return block < 0 || v > INT32_MAX ? -1 : (int32_t)v;
+    return (uint32_t)block > last_block ? -1 : (block << a.block_shift) + (p & mask);
   };
   const int64_t threads = (int64_t)gridDim.x * kThreads, me = (int64_t)blockIdx.x * kThreads + tid;
   const bool wide = (reinterpret_cast<uintptr_t>(a.kv_indices) & 15) == 0;
-  for (int64_t v = me * kVec; v < n_kv; v += threads * kVec) {
-    const int32_t j0 = (int32_t)v;
-    int b = owner(s.kv, a.batch, j0);
-    int32_t out[kVec];
-    int have_b = -1, have_k = -1;
-    int32_t block = -1;
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      const int32_t j = j0 + i;
-      out[i] = -1;
-      if (j < n_kv) {
-        while (s.kv[b + 1] <= j) ++b;
-        const int p = j - s.kv[b], k = p >> a.block_shift;
-        if (b != have_b || k != have_k) {
-          block = block_of(b, k);
-          have_b = b;
-          have_k = k;
-        }
-        out[i] = slot_in(block, p);
-      }
-    }
-    if (wide && v + kVec <= n_kv) {
-      *reinterpret_cast<int4*>(a.kv_indices + v) = make_int4(out[0], out[1], out[2], out[3]);
+  auto put = [&](int64_t j, const int32_t (&out)[kVec]) {
+    if (wide && j + kVec <= n_kv) {
+      *reinterpret_cast<int4*>(a.kv_indices + j) = make_int4(out[0], out[1], out[2], out[3]);
     } else {
 #pragma unroll
       for (int i = 0; i < kVec; ++i)
-        if (v + i < n_kv) a.kv_indices[v + i] = out[i];
+        if (j + i < n_kv) a.kv_indices[j + i] = out[i];
+    }
+  };
+  for (int64_t base = (me >> 5) * kRound; base < n_kv; base += (threads >> 5) * kRound) {
+    // the whole warp's keys: one bisection, and mostly all in blocks that one request had before
+    int b = owner(s.kv, a.batch, (int32_t)base);
+    while (s.kv[b + 1] <= (int32_t)base) ++b;
+    const int p0 = (int32_t)base - s.kv[b];
+    if (s.kv[b + 1] - (int32_t)base >= kRound && (p0 + kRound - 1) >> a.block_shift < s.have[b]) {
+      const int32_t* __restrict__ row = a.table + (int64_t)b * a.table_stride;
+      int32_t out[kSide][kVec];
+#pragma unroll
+      for (int u = 0; u < kSide; ++u)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) out[u][i] = row[(p0 + (u * 32 + lane) * kVec + i) >> a.block_shift];
+#pragma unroll
+      for (int u = 0; u < kSide; ++u) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) out[u][i] = slot_in(out[u][i], p0 + (u * 32 + lane) * kVec + i);
+        put(base + (u * 32 + lane) * kVec, out[u]);
+      }
+      continue;
+    }
+    for (int u = 0; u < kSide; ++u) {
+      const int64_t j0 = base + (u * 32 + lane) * kVec;
+      int32_t out[kVec];
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const int64_t j = j0 + i;
+        out[i] = -1;
+        if (j < n_kv) {
+          while (s.kv[b + 1] <= (int32_t)j) ++b;
+          const int p = (int32_t)j - s.kv[b];
+          out[i] = slot_in(block_of(b, p >> a.block_shift), p);
+        }
+      }
+      put(j0, out);
     }
   }
   for (int64_t t = me; t < a.max_q; t += threads) {
@@ -201,7 +220,7 @@ int launch_tables(const TablesArgs& a, void* stream) {
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) !=
                                                 cudaSuccess)
     return VMLA_ERR_CUDA;
-  const int64_t items = (a.max_kv + kVec - 1) / kVec > a.max_q ? (a.max_kv + kVec - 1) / kVec : a.max_q;
+  const int64_t lanes = (a.max_kv + kVec * kSide - 1) / (kVec * kSide), items = lanes > a.max_q ? lanes : a.max_q;
   const int64_t want = (items + kThreads - 1) / kThreads, most = (int64_t)sms * 4;
   const int64_t blocks = want < 1 ? 1 : want < most ? want : most;
   tables_kernel<<<(unsigned)blocks, kThreads, 0, (cudaStream_t)stream>>>(a);
