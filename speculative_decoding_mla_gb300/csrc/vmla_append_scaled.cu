@@ -23,10 +23,11 @@ namespace vmla {
 using namespace rope;
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxBlock = VMLA_MAX_BLOCK_TOKENS;
 constexpr int kHeadPasses = 2;  // 16 heads per warp
+constexpr int kSide = 4;        // rows of a run that a warp has at a time
 static_assert(kMaxBlock <= kThreads, "one thread per token of a window");
 
 // Granules 2 lane, 2 lane + 1 of the latent and, in lanes 0 to 3, the turned granules lane and lane + 4 of the rest.
@@ -112,6 +113,98 @@ __device__ __forceinline__ bool slot_ok(const AppendArgs& a, int32_t slot) {
   return slot >= 0 && (int64_t)slot < a.pool_slots;
 }
 
+// Four rows of a run by one warp.  Of each lane's: granules 2 lane, 2 lane + 1 of every latent as they came, and of
+// row lane / 8 the eight turned elements 4 h .. 4 h + 3 and 32 + 4 h .. 32 + 4 h + 3, h = lane mod 8, and the slot
+// (-1: nothing to write).
+struct Four {
+  uint4 v0[kSide], v1[kSide];
+  float x[8];
+  int32_t slot;
+};
+
+// Tokens t0 + k .. t0 + k + 3 below t0 + n.
+__device__ __forceinline__ void fetch_four(const AppendArgs& a, int64_t t0, int k, int n, int lane, Four& f) {
+  const int mine = k + (lane >> 3), h = lane & 7;
+  const int64_t t = t0 + mine;
+  int32_t slot = -1, pos = -1;
+  uint2 lo = make_uint2(0, 0), hi = lo;
+  if (mine < n) {
+    const uint2* rope = reinterpret_cast<const uint2*>(a.k_rope + t * a.k_rope_stride);
+    slot = __ldg(a.slots + t);
+    pos = __ldg(a.positions + t);
+    lo = __ldg(rope + h);
+    hi = __ldg(rope + h + 8);
+  }
+#pragma unroll
+  for (int i = 0; i < kSide; ++i) {
+    f.v0[i] = f.v1[i] = make_uint4(0, 0, 0, 0);
+    if (k + i < n) {
+      const uint4* lat = reinterpret_cast<const uint4*>(a.latent + (t0 + k + i) * a.latent_stride);
+      f.v0[i] = __ldg(lat + 2 * lane);
+      f.v1[i] = __ldg(lat + 2 * lane + 1);
+    }
+  }
+  f.slot = slot_ok(a, slot) && pos >= 0 && (int64_t)pos < a.table_rows ? slot : -1;
+  if (f.slot >= 0) {
+    const float* row = a.cos_sin + (int64_t)pos * kRopeDim;
+    float c[4], sn[4];
+    auto load4 = [&](const float* from, float (&to)[4]) {
+      if (a.neighbours != 0) {
+        const float2 u = __ldg(reinterpret_cast<const float2*>(from) + h), v = __ldg(reinterpret_cast<const float2*>(from) + 8 + h);
+        to[0] = u.x; to[1] = u.y; to[2] = v.x; to[3] = v.y;
+      } else {
+        const float4 u = __ldg(reinterpret_cast<const float4*>(from) + h);
+        to[0] = u.x; to[1] = u.y; to[2] = u.z; to[3] = u.w;
+      }
+    };
+    load4(row, c);
+    load4(row + kRopeDim / 2, sn);
+    unpack8(make_uint4(lo.x, lo.y, hi.x, hi.y), f.x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (a.neighbours != 0) turn(f.x[2 * i], f.x[2 * i + 1], c[i], sn[i]);
+      else turn(f.x[i], f.x[4 + i], c[i], sn[i]);
+    }
+  }
+}
+
+// Their largest magnitude (NaN left out), in every lane.
+__device__ __forceinline__ float largest(const Four& f) {
+  uint32_t m2 = 0;  // of two columns (max gives the other operand where one is NaN)
+  auto take = [&](uint32_t w) { asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(w & 0x7FFF7FFFu)); };
+#pragma unroll
+  for (int i = 0; i < kSide; ++i)
+    if (__shfl_sync(0xffffffffu, f.slot, 8 * i) >= 0) {
+      take(f.v0[i].x); take(f.v0[i].y); take(f.v0[i].z); take(f.v0[i].w);
+      take(f.v1[i].x); take(f.v1[i].y); take(f.v1[i].z); take(f.v1[i].w);
+    }
+  float m = fmaxf(bf16_lo(m2), bf16_hi(m2));
+  if (f.slot >= 0)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(f.x[k]));
+  return warp_max(m);
+}
+
+__device__ __forceinline__ void store_four(const AppendArgs& a, int lane, const Four& f, float scale) {
+  uint8_t* pool = reinterpret_cast<uint8_t*>(a.pool);
+#pragma unroll
+  for (int i = 0; i < kSide; ++i) {
+    const int32_t slot = __shfl_sync(0xffffffffu, f.slot, 8 * i);
+    if (slot < 0) continue;
+    float x0[8], x1[8];
+    unpack8(f.v0[i], x0);
+    unpack8(f.v1[i], x1);
+    const uint2 c0 = codes_of(x0, scale), c1 = codes_of(x1, scale);
+    reinterpret_cast<uint4*>(pool + (int64_t)slot * kDqk)[lane] = make_uint4(c0.x, c0.y, c1.x, c1.y);
+  }
+  if (f.slot >= 0) {
+    uint32_t* dst = reinterpret_cast<uint32_t*>(pool + (int64_t)f.slot * kDqk + kDv) + (lane & 7);
+    const uint2 c = codes_of(f.x, scale);
+    dst[0] = c.x;
+    dst[8] = c.y;
+  }
+}
+
 struct RunShared {
   int32_t start[kThreads];
   int32_t starts;
@@ -172,13 +265,10 @@ __device__ void append_runs(const AppendArgs& a, int64_t w0, int window, RunShar
     }
     const float old = first < 0 ? 0.f : a.kv_scales[block];
     float m = 0.f;
-    for (int k = warp; k < n; k += kWarps) {
-      const int32_t pos = __ldg(a.positions + t0 + k);
-      if (slot_ok(a, __ldg(a.slots + t0 + k)) && pos >= 0 && (int64_t)pos < a.table_rows) {
-        Row r;
-        load_row(a, t0 + k, pos, lane, r);
-        m = fmaxf(m, largest(r, lane));
-      }
+    Four f;
+    for (int k = kSide * warp; k < n; k += kSide * kWarps) {
+      fetch_four(a, t0, k, n, lane, f);
+      m = fmaxf(m, largest(f));
     }
     if (lane == 0) s.amax[warp] = m;
     __syncthreads();
@@ -201,20 +291,16 @@ __device__ void append_runs(const AppendArgs& a, int64_t w0, int window, RunShar
       }
     }
     if (tid == 0 && first >= 0) a.kv_scales[block] = scale;
-    for (int k = warp; k < n; k += kWarps) {
-      const int32_t pos = __ldg(a.positions + t0 + k), slot = __ldg(a.slots + t0 + k);
-      if (slot_ok(a, slot) && pos >= 0 && (int64_t)pos < a.table_rows) {
-        Row r;
-        load_row(a, t0 + k, pos, lane, r);
-        store_row(a, slot, lane, r, scale);
-      }
+    for (int k = kSide * warp; k < n; k += kSide * kWarps) {
+      if (n > kSide * kWarps) fetch_four(a, t0, k, n, lane, f);  // (else it has them still)
+      store_four(a, lane, f, scale);
     }
     __syncthreads();
   }
 }
 
 template <bool kRuns>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 append_scaled_kernel(const AppendArgs a, int64_t row_ctas, int window, int parts) {
   __shared__ RunShared s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

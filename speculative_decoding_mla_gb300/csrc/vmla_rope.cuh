@@ -40,16 +40,17 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
   }
 }
 
+__device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
+  const float xr = fmaf(x, c, -(y * s)), yr = fmaf(x, s, y * c);
+  x = xr;
+  y = yr;
+}
+
 // The granules g (lo) and g + 4 (hi) of a 64-wide part, turned.
 __device__ __forceinline__ void rotate(const uint4& vlo, const uint4& vhi, const Angles& a, bool neighbours,
                                        float (&lo)[8], float (&hi)[8]) {
   unpack8(vlo, lo);
   unpack8(vhi, hi);
-  auto turn = [](float& x, float& y, float c, float s) {
-    const float xr = fmaf(x, c, -(y * s)), yr = fmaf(x, s, y * c);
-    x = xr;
-    y = yr;
-  };
   if (neighbours) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) turn(lo[2 * k], lo[2 * k + 1], a.c[k], a.s[k]);
