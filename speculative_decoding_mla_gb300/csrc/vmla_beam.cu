@@ -36,10 +36,10 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxBeams = VMLA_MAX_BEAMS, kMaxKeep = VMLA_MAX_BEAM_KEEP;
 constexpr int kMaxParts = 16;
 constexpr int kList = 2048;      // tokens above the bound that are ranked at once
-constexpr int kFlush = 8;        // granules whose sum stays in single precision
+constexpr float kLowest = -3.402823466e38f;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr double kLn2 = 0.69314718055994530942;
-static_assert(kMaxKeep <= kThreads, "a thread per place");
+static_assert(kMaxKeep <= kThreads && kMaxBeams * kMaxParts <= kThreads, "a thread per place and per list");
 
 // One part of a row: the sum of exp(x - ref), tokens at +inf, and the first n tokens as sorted keys.
 struct alignas(16) RowPart {
@@ -107,69 +107,96 @@ struct Row {
   }
 };
 
-// A thread's sum and largest granule.
+// A granule's logits in pairs, and the largest of them (NaN left out, unless there is nothing else).
+__device__ __forceinline__ float pairs_of(const uint4& v, float2 (&x)[4], uint16_t) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t m = w[0];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    x[k] = make_float2(bf16_lo(w[k]), bf16_hi(w[k]));
+    if (k > 0) asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[k]));
+  }
+  return fmaxf(bf16_lo(m), bf16_hi(m));
+}
+__device__ __forceinline__ float pairs_of(const uint4& v, float2 (&x)[2], float) {
+  x[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+  x[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+  return fmaxf(fmaxf(x[0].x, x[0].y), fmaxf(x[1].x, x[1].y));
+}
+
+// A thread's sum, as high + low + sum, and its largest granule.
 struct Acc {
-  float ref = -INFINITY, sum = 0.f, best = -INFINITY;
-  double total = 0.0;
+  float ref = kLowest, limit = -INFINITY, sum = 0.f, high = 0.f, low = 0.f, best = -INFINITY;
   int place = -1;
   uint32_t infinite = 0;
 
   template <int N>
-  __device__ __forceinline__ void add(float (&x)[N], int g) {
-    float m = x[0];
-#pragma unroll
-    for (int k = 1; k < N; ++k) m = fmaxf(m, x[k]);
+  __device__ __forceinline__ void add(const float2 (&x)[N], float m, int g) {
     if (m > best) {
       best = m;
       place = g;
     }
-    if (!(m > -INFINITY)) return;
-    if (m > ref + 20.f) {
+    if (m > limit) {
       if (m == INFINITY) {  // those tokens share the row evenly
 #pragma unroll
-        for (int k = 0; k < N; ++k) infinite += x[k] == INFINITY;
+        for (int k = 0; k < N; ++k) infinite += (x[k].x == INFINITY) + (x[k].y == INFINITY);
         return;
       }
       const float f = ex2_approx((ref - m) * kLog2e);
-      total *= (double)f;
+      high *= f;
+      low *= f;
       sum *= f;
       ref = m;
+      limit = m + 20.f;
     }
-    float e[N];
+    const float2 r = make_float2(-ref, -ref), scale = make_float2(kLog2e, kLog2e);
+    float2 e[N];
 #pragma unroll
-    for (int k = 0; k < N; ++k) e[k] = ex2_approx((x[k] - ref) * kLog2e);
+    for (int k = 0; k < N; ++k) {
+      const float2 d = mul2(sum2(x[k], r), scale);
+      e[k] = make_float2(ex2_approx(d.x), ex2_approx(d.y));
+    }
 #pragma unroll
     for (int s = N / 2; s > 0; s >>= 1)
 #pragma unroll
-      for (int k = 0; k < s; ++k) e[k] += e[k + s];
-    if (e[0] != e[0]) {  // NaN counts as -inf
-      float y = 0.f;
+      for (int k = 0; k < s; ++k) e[k] = sum2(e[k], e[k + s]);
+    float t = e[0].x + e[0].y;
+    if (t != t) {  // NaN counts as -inf
+      t = 0.f;
 #pragma unroll
-      for (int k = 0; k < N; ++k) y += x[k] > -INFINITY ? ex2_approx((x[k] - ref) * kLog2e) : 0.f;
-      e[0] = y;
+      for (int k = 0; k < N; ++k) {
+        t += x[k].x > -INFINITY ? ex2_approx((x[k].x - ref) * kLog2e) : 0.f;
+        t += x[k].y > -INFINITY ? ex2_approx((x[k].y - ref) * kLog2e) : 0.f;
+      }
     }
-    sum += e[0];
+    sum += t;
   }
+  // (two-sum: high + low holds what single precision would drop)
   __device__ __forceinline__ void flush() {
-    total += (double)sum;
+    const float to = high + sum, part = to - high;
+    low += (high - (to - part)) + (sum - part);
+    high = to;
     sum = 0.f;
   }
+  __device__ __forceinline__ double total() const { return (double)high + (double)low; }
 };
 
 struct RowShared {
-  alignas(16) uint64_t key[kThreads];
   uint64_t list[kList];
   uint64_t warp_key[kWarps];
+  uint8_t thread_of[kThreads];
+  uint32_t warp_low[kWarps];
   int32_t thread[kMaxKeep];
   float warp_f[kWarps];
   double warp_d[kWarps];
   uint32_t warp_u[kWarps];
   uint64_t bound;
-  uint32_t chosen, listed;
+  uint32_t listed;
 };
+static_assert(kThreads <= 256 && kThreads <= kList, "the threads' list");
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 beam_rows_kernel(const BeamArgs a, RowPart* __restrict__ out, int parts) {
   constexpr int kVec = Row<T>::kVec;
   __shared__ RowShared s;
@@ -178,6 +205,21 @@ beam_rows_kernel(const BeamArgs a, RowPart* __restrict__ out, int parts) {
   const int64_t row_at = blockIdx.x / (unsigned)parts;
   const int part = (int)(blockIdx.x % (unsigned)parts);
   RowPart& r = out[blockIdx.x];
+  const Row<T> row(a.logits, a.stride, row_at, a.vocab);
+  const int all = row.granules(), per = (all + parts - 1) / parts;
+  const int g0 = part * per, g1 = min(all, g0 + per);
+  // four granules at a time, the next four on their way meanwhile
+  constexpr int kAhead = 4, kRound = kAhead * kThreads;
+  const int w0 = row.lead ? 1 : 0, w1 = min(g1, (a.vocab + row.lead) / kVec);  // granules in the row as a whole
+  uint4 next[kAhead];
+  auto fetch = [&](int g) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int h = g + k * kThreads;
+      if (h >= w0 && h < w1) next[k] = __ldg(reinterpret_cast<const uint4*>(row.first) + h);
+    }
+  };
+  fetch(g0 + tid);
   const float score = a.score[row_at];
   if (!(score > -INFINITY) || (a.finished && a.finished[row_at])) {  // nothing of its logits counts
     if (tid == 0) {
@@ -188,54 +230,54 @@ beam_rows_kernel(const BeamArgs a, RowPart* __restrict__ out, int parts) {
     }
     return;
   }
-  const Row<T> row(a.logits, a.stride, row_at, a.vocab);
-  const int all = row.granules(), per = (all + parts - 1) / parts;
-  const int g0 = part * per, g1 = min(all, g0 + per);
   Acc acc;
-  // four granules at a time, the next four on their way meanwhile
-  constexpr int kAhead = 4;
-  uint4 next[kAhead];
-  auto fetch = [&](int g) {
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int h = g + k * kThreads;
-      if (h < g1 && row.whole(h)) next[k] = __ldg(reinterpret_cast<const uint4*>(row.first) + h);
-    }
-  };
-  fetch(g0 + tid);
-  int since = 0;
 #pragma unroll 1
-  for (int g = g0 + tid; g < g1; g += kAhead * kThreads) {
+  for (int base = g0; base < g1; base += kRound) {
+    const int g = base + tid;
     uint4 v[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) v[k] = next[k];
-    fetch(g + kAhead * kThreads);
+    fetch(g + kRound);
+    if (base >= w0 && base + kRound <= w1) {
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int h = g + k * kThreads;
-      if (h < g1) {
-        float x[kVec];
-        if (row.whole(h)) Row<T>::unpack(v[k], x);
-        else row.get(h, x);
-        acc.add(x, h);
+      for (int k = 0; k < kAhead; ++k) {
+        float2 x[kVec / 2];
+        const float m = pairs_of(v[k], x, T());
+        acc.add(x, m, g + k * kThreads);
+      }
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < kAhead; ++k) {
+        const int h = g + k * kThreads;
+        const uint4 q = k == 0 ? v[0] : k == 1 ? v[1] : k == 2 ? v[2] : v[3];
+        if (h >= g1) break;
+        float2 x[kVec / 2];
+        float m;
+        if (h >= w0 && h < w1) {
+          m = pairs_of(q, x, T());
+        } else {
+          float y[kVec];
+          row.get(h, y);
+          m = y[0];
+#pragma unroll
+          for (int i = 1; i < kVec; ++i) m = fmaxf(m, y[i]);
+#pragma unroll
+          for (int i = 0; i < kVec / 2; ++i) x[i] = make_float2(y[2 * i], y[2 * i + 1]);
+        }
+        acc.add(x, m, h);
       }
     }
-    if ((since += kAhead) >= kFlush) {
-      acc.flush();
-      since = 0;
-    }
+    acc.flush();
   }
-  acc.flush();
   // the part's sum against its largest reference
-  float ref = warp_max(acc.ref);
+  float ref = warp_max(acc.place >= 0 ? acc.ref : -INFINITY);
   if (lane == 0) s.warp_f[warp] = ref;
   const uint64_t mine = acc.place >= 0 ? key_of(ordered(acc.best), (uint32_t)acc.place) : 0;
-  s.key[tid] = mine;
-  if (tid == 0) s.chosen = s.listed = 0;
+  if (tid == 0) s.listed = 0;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) ref = fmaxf(ref, s.warp_f[w]);
-  double total = acc.ref > -INFINITY ? acc.total * (double)ex2_approx((acc.ref - ref) * kLog2e) : 0.0;
+  double total = acc.place >= 0 ? acc.total() * (double)ex2_approx((acc.ref - ref) * kLog2e) : 0.0;
   uint32_t infinite = acc.infinite;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -246,25 +288,42 @@ beam_rows_kernel(const BeamArgs a, RowPart* __restrict__ out, int parts) {
     s.warp_d[warp] = total;
     s.warp_u[warp] = infinite;
   }
-  // the K threads with the largest granules, and the K-th of these
+  // The K threads with the largest granules, and the K-th of these: each warp's ceil(K / warps)-th value bounds them
+  // together, the threads at or above the least of these bounds are listed, and the list ranked.
   const int keep = a.keep;
-  if (mine != 0) {
+  const uint32_t order = (uint32_t)(mine >> 32);
+  uint32_t rest = order, low = 0;
+  for (int n = (keep + kWarps - 1) / kWarps; n > 0; --n) {
+    low = __reduce_max_sync(0xffffffffu, rest);
+    if (rest == low) rest = 0;
+  }
+  if (lane == 0) s.warp_low[warp] = low;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) low = min(low, s.warp_low[w]);
+  if (mine != 0 && order >= low) {
+    const uint32_t at = atomicAdd(&s.listed, 1u);
+    s.list[at] = mine;
+    s.thread_of[at] = (uint8_t)tid;
+  }
+  __syncthreads();
+  const int top = (int)s.listed;
+  if (tid < top) {
+    const uint64_t k = s.list[tid];
     int above = 0;
-#pragma unroll 8
-    for (int k = 0; k < kThreads; k += 2) {
-      const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(&s.key[k]);
-      above += (two.x > mine) + (two.y > mine);
-    }
+#pragma unroll 4
+    for (int i = 0; i < top; ++i) above += s.list[i] > k;
     if (above < keep) {
-      s.thread[above] = tid;
-      atomicMax(&s.chosen, (uint32_t)above + 1);
-      if (above == keep - 1) s.bound = mine;
+      s.thread[above] = s.thread_of[tid];
+      if (above == keep - 1) s.bound = k;
     }
   }
   __syncthreads();
-  const int chosen = (int)s.chosen;
+  if (tid == 0) s.listed = 0;
+  const int chosen = min(top, keep);
   const uint64_t bound = chosen == keep ? s.bound : 1;
   const uint32_t least = (uint32_t)(bound >> 32), last_place = ~(uint32_t)bound;
+  __syncthreads();
   // their tokens at or above the bound (of the bound's own value, those up to its granule)
   const int rounds = (g1 - g0 + kThreads - 1) / kThreads;
   for (int i = tid; i < chosen * rounds; i += kThreads) {
@@ -342,13 +401,16 @@ struct JoinShared {
   unsigned long long sum[kMaxBeams];
   uint32_t unsure;             // beams whose neighbours in the order lie too close, and whose sum is not exact yet
   uint32_t exact;              // beams whose sum is
-  alignas(16) uint64_t top[kThreads];  // each thread's best score
-  uint32_t top_index[kThreads];
-  uint64_t order[kMaxKeep];            // the best scores in order, and their indexes
+  uint64_t head[kMaxBeams * kMaxParts];       // each list's best score, and its index
+  uint32_t head_index[kMaxBeams * kMaxParts];
+  int32_t count[kMaxBeams * kMaxParts];       // and its entries
+  int32_t list[kMaxKeep];                     // the lists with the K best heads, in order
+  uint64_t score[kMaxKeep][kMaxKeep];         // of the r-th of them the first K - r scores and indexes
+  uint32_t place[kMaxKeep][kMaxKeep];
+  uint64_t order[kMaxKeep];                   // the best scores in order, and their indexes
   uint32_t index[kMaxKeep];
-  uint64_t bound;
-  uint32_t bound_index, chosen, listed;
 };
+static_assert(kMaxKeep <= 32, "a lane per list");
 
 // Order of scores as whole numbers: 0 for none.
 __device__ __forceinline__ uint64_t ordered64(double v) {
@@ -380,10 +442,8 @@ __device__ __forceinline__ void doubt(JoinShared& s, uint64_t a, int w, uint64_t
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 beam_join_kernel(const BeamArgs a, const RowPart* __restrict__ in, int parts, const __grid_constant__ ExpTable exp_table) {
-  extern __shared__ uint64_t keys[];  // [beams x parts][keep]
   __shared__ JoinShared s;
-  __shared__ int32_t count[kMaxBeams * kMaxParts];
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp_id = tid >> 5;
   const int W = a.beams, K = a.keep, V = a.vocab, lists = W * parts;
   const int64_t request = blockIdx.x;
   if (tid < 64) s.table[tid] = exp_table.t[tid];
@@ -391,112 +451,123 @@ beam_join_kernel(const BeamArgs a, const RowPart* __restrict__ in, int parts, co
   grid_dependents_launch();
   grid_dependency_wait();
   const RowPart* rows = in + request * lists;
-  for (int l = tid; l < lists; l += kThreads) count[l] = (int)rows[l].n;
-  __syncthreads();
-  for (int i = tid; i < lists * K; i += kThreads) {
-    const int l = i / K, k = i - l * K;
-    keys[i] = k < count[l] ? rows[l].key[k] : 0;
-  }
-  if (tid < W) {
-    const float c = a.score[request * W + tid];
-    const bool done = a.finished && a.finished[request * W + tid];
-    s.sum[tid] = 0;
-    s.infinite[tid] = false;
-    s.ref[tid] = 0.f;
-    s.base[tid] = (double)c;
-    if (c > -INFINITY && !done) {
-      float ref = -INFINITY;
-      uint32_t infinite = 0;
-      for (int p = 0; p < parts; ++p) {
-        ref = fmaxf(ref, rows[tid * parts + p].ref);
-        infinite += rows[tid * parts + p].infinite;
+  // a thread per list (the parts of a beam, a power of two, stand side by side in a warp)
+  const bool real = tid < lists;
+  const int my_beam = real ? tid / parts : 0;
+  int count = 0;       // entries
+  uint64_t first = 0;  // the first one's key
+  if (tid < (lists + 31) / 32 * 32) {
+    const RowPart& r = rows[real ? tid : 0];
+    const float c = a.score[request * W + my_beam];
+    const bool done = a.finished && a.finished[request * W + my_beam];
+    const float own = real ? r.ref : -INFINITY;
+    double sum = real ? r.sum : 0.0;
+    uint32_t infinite = real ? r.infinite : 0;
+    if (real) {
+      count = (int)r.n;
+      first = r.key[0];
+      if (done && c > -INFINITY) {
+        // a finished beam goes on by the padding token alone, its score as it is
+        count = tid % parts == 0;
+        first = key_of(ordered(0.f), (uint32_t)a.pad_token);
       }
-      double sum = 0.0;
-      for (int p = 0; p < parts; ++p) {
-        const RowPart& r = rows[tid * parts + p];
-        if (r.ref > -INFINITY) sum += r.sum * (double)ex2_approx((r.ref - ref) * kLog2e);
-      }
-      s.ref[tid] = ref > -INFINITY ? ref : 0.f;
-      s.infinite[tid] = infinite > 0;
-      s.base[tid] = (double)c - log(infinite ? (double)infinite : sum);
+    }
+    if (real) s.count[tid] = count;
+    float ref = own;
+    for (int o = parts >> 1; o > 0; o >>= 1) {
+      ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
+      infinite += __shfl_xor_sync(0xffffffffu, infinite, o);
+    }
+    sum = own > -INFINITY ? sum * (double)ex2_approx((own - ref) * kLog2e) : 0.0;
+    for (int o = parts >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (real && tid % parts == 0) {
+      const bool counts = c > -INFINITY && !done;
+      s.sum[my_beam] = 0;
+      s.ref[my_beam] = counts && ref > -INFINITY ? ref : 0.f;
+      s.infinite[my_beam] = counts && infinite > 0;
+      s.base[my_beam] = counts ? (double)c - log(infinite ? (double)infinite : sum) : (double)c;
     }
   }
   __syncthreads();
-  if (tid < W && a.finished && a.finished[request * W + tid] && a.score[request * W + tid] > -INFINITY) {
-    // a finished beam goes on by the padding token alone, its score as it is
-    keys[tid * parts * K] = key_of(ordered(0.f), (uint32_t)a.pad_token);
-    count[tid * parts] = 1;
-  }
-  __syncthreads();
-  // the K best: as for a row, the threads' best ones bound them, the entries at or above the bound are listed (at most K
-  // threads', of up to 32 entries each) and ranked
-  const int entries = lists * K;
-  auto score_of = [&](int i, uint32_t& index) -> uint64_t {
-    const int l = i / K, w = l / parts;
-    if (i - l * K >= count[l]) return 0;
-    const uint64_t key = keys[i];
+  auto score_of = [&](int w, uint64_t key) -> uint64_t {
     const float x = ordered_value((uint32_t)(key >> 32));
-    if (s.infinite[w] && x != INFINITY) return 0;
-    index = (uint32_t)(w * V) + ~(uint32_t)key;
-    return ordered64(s.base[w] + (s.infinite[w] ? 0.0 : (double)x - (double)s.ref[w]));
+    if (s.infinite[w]) return x == INFINITY ? ordered64(s.base[w]) : 0;
+    return ordered64(s.base[w] + ((double)x - (double)s.ref[w]));
   };
-  uint64_t* const list = keys + entries;                                 // [K x rounds] scores, then their indexes
-  const int rounds = (entries + kThreads - 1) / kThreads;
-  uint32_t* const list_index = reinterpret_cast<uint32_t*>(list + (size_t)K * rounds);
   for (int pass = 0; pass <= W; ++pass) {
-    uint64_t best = 0;
-    uint32_t best_index = 0xffffffffu;
-    for (int i = tid; i < entries; i += kThreads) {
-      uint32_t x = 0;
-      const uint64_t v = score_of(i, x);
-      if (v != 0 && before(v, x, best, best_index)) {
-        best = v;
-        best_index = x;
+    // The lists are sorted, so an entry has those before it in its list and the better lists' heads in front of it:
+    // entry k of the list with the r-th best head is among the K best only if r + k < K.
+    uint64_t head = 0;
+    uint32_t head_index = 0;
+    if (real) {
+      if (count > 0) {
+        head = score_of(my_beam, first);
+        head_index = (uint32_t)(my_beam * V) + ~(uint32_t)first;
+      }
+      s.head[tid] = head;
+      s.head_index[tid] = head_index;
+    }
+    if (tid < K) s.list[tid] = -1;
+    if (tid == 0) s.unsure = 0;
+    __syncthreads();
+    int rank = K;
+    if (head != 0) {
+      rank = 0;
+#pragma unroll 4
+      for (int l = 0; l < lists; ++l) rank += before(s.head[l], s.head_index[l], head, head_index);
+      if (rank < K) {
+        s.list[rank] = tid;
+        s.score[rank][0] = head;
+        s.place[rank][0] = head_index;
       }
     }
-    s.top[tid] = best;
-    s.top_index[tid] = best_index;
-    if (tid < K) s.order[tid] = 0;
-    if (tid == 0) s.chosen = s.listed = s.unsure = 0;
     __syncthreads();
-    if (best != 0) {
-      const int threads = entries < kThreads ? entries : kThreads;
-      int above = 0;
-#pragma unroll 4
-      for (int k = 0; k < threads; ++k) above += before(s.top[k], s.top_index[k], best, best_index);
-      if (above < K) {
-        atomicMax(&s.chosen, (uint32_t)above + 1);
-        if (above == K - 1) {
-          s.bound = best;
-          s.bound_index = best_index;
+    constexpr int kEach = (kMaxKeep * kMaxKeep + kThreads - 1) / kThreads;
+    uint64_t key[kEach];
+    int from[kEach];
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      const int i = tid + u * kThreads, r = i / K, k = i - r * K;
+      from[u] = r < K && k > 0 && r + k < K ? s.list[r] : -1;
+      if (from[u] >= 0 && k < s.count[from[u]]) key[u] = rows[from[u]].key[k];
+    }
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      const int i = tid + u * kThreads, r = i / K, k = i - r * K, l = from[u];
+      if (l < 0) continue;
+      const bool is = k < s.count[l];
+      s.score[r][k] = is ? score_of(l / parts, key[u]) : 0;
+      s.place[r][k] = is ? (uint32_t)(l / parts * V) + ~(uint32_t)key[u] : 0;
+    }
+    __syncthreads();
+    if (warp_id == 0) {
+      // a lane per list, its next entry in registers: K times the best of them
+      const bool has = lane < K && s.list[lane < K ? lane : 0] >= 0;
+      int at = 0;
+      uint64_t v = has ? s.score[lane][0] : 0;
+      uint32_t x = has ? s.place[lane][0] : 0;
+      for (int n = 0; n < K; ++n) {
+        const uint32_t hi = (uint32_t)(v >> 32), most = __reduce_max_sync(0xffffffffu, hi);
+        unsigned who = __ballot_sync(0xffffffffu, hi == most);
+        if (who & (who - 1)) {
+          const uint32_t lo = hi == most ? (uint32_t)v : 0, more = __reduce_max_sync(0xffffffffu, lo);
+          const bool tie = hi == most && lo == more;
+          const uint32_t ix = tie ? x : 0xffffffffu, least = __reduce_min_sync(0xffffffffu, ix);
+          who = __ballot_sync(0xffffffffu, tie && ix == least);
+        }
+        if (lane == __ffs(who) - 1) {
+          s.order[n] = v;
+          s.index[n] = x;
+          ++at;
+          const bool more = v != 0 && lane + at < K;
+          v = more ? s.score[lane][at] : 0;
+          x = more ? s.place[lane][at] : 0;
         }
       }
-    }
-    __syncthreads();
-    const bool bounded = (int)s.chosen == K;
-    const uint64_t bound = bounded ? s.bound : 0;
-    const uint32_t bound_index = bounded ? s.bound_index : 0xffffffffu;
-    for (int i = tid; i < entries; i += kThreads) {
-      uint32_t x = 0;
-      const uint64_t v = score_of(i, x);
-      if (v != 0 && !before(bound, bound_index, v, x)) {
-        const uint32_t at = atomicAdd(&s.listed, 1u);
-        list[at] = v;
-        list_index[at] = x;
-      }
-    }
-    __syncthreads();
-    const int listed = (int)s.listed;
-    for (int i = tid; i < listed; i += kThreads) {
-      const uint64_t v = list[i];
-      const uint32_t x = list_index[i];
-      int above = 0;
-#pragma unroll 4
-      for (int k = 0; k < listed; ++k) above += before(list[k], list_index[k], v, x);
-      if (above < K) {
-        s.order[above] = v;
-        s.index[above] = x;
-      }
+      __syncwarp();
+      // what lies closest behind the last one kept: of each list the entry at which it stands
+      const uint64_t last = s.order[K - 1];
+      if (last != 0 && v != 0) doubt(s, last, (int)s.index[K - 1] / V, v, (int)x / V);
     }
     __syncthreads();
     if (tid < K) {
@@ -508,15 +579,7 @@ beam_join_kernel(const BeamArgs a, const RowPart* __restrict__ in, int parts, co
       a.new_score[o] = v ? (float)ordered64_value(v) : -INFINITY;
       if (tid > 0 && v != 0) doubt(s, s.order[tid - 1], (int)s.index[tid - 1] / V, v, w);
     }
-    const uint64_t last = s.order[K - 1];
-    if (last != 0) {
-      const uint32_t last_index = s.index[K - 1];
-      for (int i = tid; i < entries; i += kThreads) {
-        uint32_t x = 0;
-        const uint64_t v = score_of(i, x);
-        if (v != 0 && before(last, last_index, v, x)) doubt(s, last, (int)last_index / V, v, (int)x / V);
-      }
-    }
+    if (s.order[K - 1] != 0 && head != 0 && rank >= K) doubt(s, s.order[K - 1], (int)s.index[K - 1] / V, head, my_beam);
     __syncthreads();
     uint32_t unsure = s.unsure;
     if (unsure == 0) break;
@@ -528,7 +591,7 @@ beam_join_kernel(const BeamArgs a, const RowPart* __restrict__ in, int parts, co
       if (s.infinite[w] || (a.finished && a.finished[request * W + w])) continue;  // exact already
       uint32_t top = 0;
       for (int p = 0; p < parts; ++p)
-        if (count[w * parts + p] > 0) top = max(top, (uint32_t)(keys[(w * parts + p) * K] >> 32));
+        if (rows[w * parts + p].n > 0) top = max(top, (uint32_t)(rows[w * parts + p].key[0] >> 32));
       const Exponent e = {ordered_value(top), 1.44269502162933349609f, 1.92596299112661746887e-8f};
       const Row<T> row(a.logits, a.stride, request * W + w, V);
       const int all = row.granules();
@@ -604,16 +667,9 @@ int launch_select(const BeamArgs& a, int64_t requests, int parts, void* workspac
   cudaLaunchAttribute attr[1] = {early_start_attribute()};
   cfg.gridDim = dim3((unsigned)requests, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  const size_t entries = (size_t)a.beams * parts * a.keep;
-  const auto bytes = [](size_t n, size_t keep) { return n * 8 + keep * ((n + kThreads - 1) / kThreads) * 12; };
-  cfg.dynamicSmemBytes = bytes(entries, a.keep);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cfg.dynamicSmemBytes > 32768 &&
-      cudaFuncSetAttribute(beam_join_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)bytes(kMaxBeams * kMaxParts * kMaxKeep, kMaxKeep)) != cudaSuccess)
-    return VMLA_ERR_CUDA;
   return cudaLaunchKernelEx(&cfg, beam_join_kernel<T>, a, (const RowPart*)part, parts, exp_table()) == cudaSuccess
              ? VMLA_OK
              : VMLA_ERR_CUDA;
