@@ -209,7 +209,7 @@ struct RunShared {
   int32_t start[kThreads];
   int32_t starts;
   int32_t warp_len[kWarps];
-  int32_t first[kWarps];
+  int32_t first[kWarps], last[kWarps];
   float amax[kWarps];
 };
 
@@ -239,7 +239,7 @@ __device__ void append_runs(const AppendArgs& a, int64_t w0, int window, RunShar
     const int64_t t0 = w0 + s.start[i];
     const int32_t block = __ldg(a.slots + t0) >> shift;
     // its length: up to the first token of another block, and the first row that it brings
-    int n = 0, first = -1;
+    int n = 0, used_n = 0, first = -1;
     for (bool more = true; more;) {
       const int64_t t = t0 + n + tid;
       const int32_t slot = t < a.tokens ? __ldg(a.slots + t) : -1, pos = t < a.tokens ? __ldg(a.positions + t) : -1;
@@ -251,6 +251,7 @@ __device__ void append_runs(const AppendArgs& a, int64_t w0, int window, RunShar
       if (lane == 0) {
         s.warp_len[warp] = len;
         s.first[warp] = used ? at : -1;
+        s.last[warp] = used ? 32 - __clz(used) : 0;
       }
       __syncthreads();
       const int n0 = n;
@@ -259,10 +260,12 @@ __device__ void append_runs(const AppendArgs& a, int64_t w0, int window, RunShar
         if (n == n0 + 32 * w) {
           n += s.warp_len[w];
           if (first < 0) first = s.first[w];
+          if (s.last[w] > 0) used_n = n0 + 32 * w + s.last[w];
         }
       more = n == n0 + kThreads;
       __syncthreads();
     }
+    n = used_n;  // (padding behind the last row of the block costs nothing more)
     const float old = first < 0 ? 0.f : a.kv_scales[block];
     float m = 0.f;
     Four f;

@@ -72,6 +72,7 @@ struct Shared {
   uint8_t p[kTile * 128];                     // [key][hi 32 | mid 32 | lo 32 | -], 128-byte swizzle
   uint8_t rope[kTile * 64];                   // [key][64 bytes], 64-byte swizzle
   uint8_t q_rope[2 * kRows * 64];             // 64-byte swizzle
+  float back[kRows];                          // of each row: what its products are times as a score (log2)
   float m[kRows], f[kRows];                   // reference of each row (log2), factor of its last change
   float part[4][kRows];                       // per quarter of the keys: row maxima, or row sums
   uint64_t mask[kRows];                       // the unit's rows: visible drafts
@@ -80,7 +81,6 @@ struct Shared {
   int32_t first_b, first_g;
   uint32_t first_at;
   int32_t parent[VMLA_MAX_DRAFT];
-  float q_max[kSoftWarps];
   uint32_t sums[2][kThreads / 32];
   uint64_t full[kSlots], free[kSlots], rope_full, rope_free;
   uint64_t sfull[2], sfree[2], pfull, pfree, qfull, ofree;
@@ -490,52 +490,68 @@ __device__ void value_role(Shared& sm, const ScaledArgs& a, uint32_t tmem, Units
 }
 
 // ------------------------------------------------------------------ queries (softmax warps)
-// The unit's rows into shared memory in two e4m3 parts, their masks; the factor that makes a score of a product.
+// The unit's rows into shared memory in two e4m3 parts, what makes a score of each row's products, their masks.
 // (What runs once per unit is kept in loops: straight-line code that is run once costs more in fetching it.)
-__device__ __noinline__ float load_queries(Shared& sm, const ScaledArgs& a, const Unit& u) {
-  constexpr int kGranules = kDqk / 8;                      // of 8 bf16
-  constexpr int kEach = kRows * kGranules / kSoftThreads;   // 9 per thread
-  static_assert(kRows * kGranules % kSoftThreads == 0, "granules per thread");
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint4* src = reinterpret_cast<const uint4*>(a.q + out_row(a, u) * kDqk);
+__device__ __noinline__ void load_queries(Shared& sm, const ScaledArgs& a, const Unit& u) {
+  constexpr int kGranules = kDqk / 8;              // of 8 bf16
+  constexpr int kWarpRows = kRows / kSoftWarps;    // a warp has four whole rows
+  constexpr int kEach = kWarpRows * kGranules / 32;  // 9 granules per thread
+  static_assert(kWarpRows * kGranules % 32 == 0, "granules per thread");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, first = warp * kWarpRows;
+  const uint4* src = reinterpret_cast<const uint4*>(a.q + (out_row(a, u) + first) * kDqk);
   uint4 v[kEach];
-  const int valid = u.rows * kGranules;
+  const int valid = (u.rows - first) * kGranules;
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
-    const int i = tid + k * kSoftThreads;
+    const int i = lane + k * 32;
     v[k] = i < valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
   }
   if (a.parent && tid < u.nq) sm.parent[tid] = a.parent[u.q0 + tid];
-  uint32_t m = 0;  // largest magnitude of either half, as bits of bf16
+  // each row's largest magnitude, as bits of bf16
+  uint32_t most[kWarpRows];
+#pragma unroll
+  for (int r = 0; r < kWarpRows; ++r) most[r] = 0;
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
     const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+    uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t x = w[j] & 0x7FFF7FFFu;
       asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(x));
     }
+    m = max(m >> 16, m & 0xFFFFu);
+#pragma unroll
+    for (int r = 0; r < kWarpRows; ++r)
+      if (k * 32 < (r + 1) * kGranules && (k + 1) * 32 > r * kGranules) {  // (known when compiling)
+        const int i = lane + k * 32;
+        if (i >= r * kGranules && i < (r + 1) * kGranules) most[r] = max(most[r], m);
+      }
   }
-  m = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xFFFFu));
-  if (lane == 0) sm.q_max[warp] = __uint_as_float(m << 16);
-  named_bar_sync(1, kSoftThreads);
-  float top = lane < kSoftWarps ? sm.q_max[lane] : 0.f;
-  top = warp_max(top);
-  // a: 448 = 1.75 x 2^8; queries below 2^-100 are zero to any score
-  const uint32_t bits = __float_as_uint(top);
-  int e = 8 - ((int)(bits >> 23) - 127) - ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  e = e > 108 ? 108 : e < -119 ? -119 : e;
-  const float scale = __uint_as_float((uint32_t)(e + 127) << 23), back = __uint_as_float((uint32_t)(127 - e) << 23);
+  float mine = 0.f;  // lane r < 4: the power of two that brings row r's largest to (224, 448], 448 = 1.75 x 2^8
+#pragma unroll
+  for (int r = 0; r < kWarpRows; ++r) {
+    const uint32_t bits = __reduce_max_sync(0xffffffffu, most[r]) << 16;
+    int e = 8 - ((int)(bits >> 23) - 127) - ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    e = e > 108 ? 108 : e < -119 ? -119 : e;  // (queries below 2^-100 are zero to any score)
+    const float scale = __uint_as_float((uint32_t)(e + 127) << 23), back = __uint_as_float((uint32_t)(127 - e) << 23);
+    if (lane == r) {
+      mine = scale;
+      // a row with an infinity or NaN has scores of NaN
+      sm.back[first + r] = bits >= 0x7F800000u ? __uint_as_float(0x7FFFFFFFu) : a.sm_scale * 1.4426950408889634f * back;
+    }
+  }
   constexpr int kSide = 3;  // granules worked on side by side
   static_assert(kEach % kSide == 0, "granules per thread");
 #pragma unroll 1
   for (int k = 0; k < kEach; k += kSide) {
 #pragma unroll
     for (int side = 0; side < kSide; ++side) {
-      const int i = tid + (k + side) * kSoftThreads, row = i / kGranules, col = (i - row * kGranules) * 8;
+      const int i = lane + (k + side) * 32, at = i / kGranules, row = first + at, col = (i - at * kGranules) * 8;
+      const float scale = __shfl_sync(0xffffffffu, mine, at);
       const uint32_t w[4] = {v[side].x, v[side].y, v[side].z, v[side].w};
       uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-  #pragma unroll
+#pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float x0 = bf16_lo(w[j]) * scale, x1 = bf16_hi(w[j]) * scale;
         uint16_t h, l;
@@ -560,6 +576,7 @@ __device__ __noinline__ float load_queries(Shared& sm, const ScaledArgs& a, cons
 #pragma unroll
     for (int j = 0; j + kSide < kEach; ++j) v[j] = v[j + kSide];
   }
+  named_bar_sync(1, kSoftThreads);  // (the parents)
   if (tid < kRows) {
     uint64_t word = 0;
     if (tid < u.rows) {
@@ -588,7 +605,6 @@ __device__ __noinline__ float load_queries(Shared& sm, const ScaledArgs& a, cons
   fence_proxy_async_smem();
   named_bar_sync(1, kSoftThreads);
   if (lane == 0 && a.test_fault != kFaultNoQReady) mbar_arrive(&sm.qfull);
-  return a.sm_scale * 1.4426950408889634f * back;
 }
 
 // ------------------------------------------------------------------ softmax
@@ -616,6 +632,24 @@ __device__ __forceinline__ float reduce16(const float (&v)[16], int lane, Op op)
   return op(d, __shfl_xor_sync(0xffffffffu, d, 1));
 }
 
+// Puts zeros in place of a key's NaN codes, once its scores are there (rows that see it have sums of NaN, so their
+// results are NaN all the same; the others' weights of zero would make NaN of them).
+__device__ __noinline__ void clear_nan(Shared& sm, const ScaledArgs& a, uint32_t tile, int key, bool mine) {
+  for (uint32_t c = 0; c < kChunks; ++c) {
+    const uint32_t at = (tile * kChunks + c) % kSlots;
+    wait(sm, &sm.full[at], ((tile * kChunks + c) / kSlots) & 1, a, 304);  // (long ago: the scores came of it)
+    if (!mine) continue;
+    uint4* row = reinterpret_cast<uint4*>(sm.latent[at] + key * 128);
+    for (int g = 0; g < 8; ++g) {
+      uint32_t w[4] = {row[g].x, row[g].y, row[g].z, row[g].w};
+      for (int j = 0; j < 4; ++j)
+        for (int k = 0; k < 4; ++k)
+          if ((w[j] >> (8 * k) & 0x7F) == 0x7F) w[j] &= ~(0xFFu << (8 * k));
+      row[g] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
 __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, uint32_t tmem, const Partials& part,
                              Units& units, Unit& u, bool more) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -624,7 +658,7 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
   const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
   auto sync = [] { named_bar_sync(1, kSoftThreads); };
   int it = 0;
-  float factor = more ? load_queries(sm, a, u) : 0.f;
+  if (more) load_queries(sm, a, u);
   while (more) {
     float l[kPerThread];
 #pragma unroll
@@ -651,7 +685,7 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
         for (int r = 0; r < kPerThread; ++r) seen |= (uint32_t)((sm.mask[row0 + r] >> (key - u.prefix)) & 1) << r;
       }
       const bool all_seen = __all_sync(0xffffffffu, seen == 0xFFFFu);
-      const float c = scale * factor, held = fmaxf(scale, kTiny) * kUnit;
+      const float held = fmaxf(scale, kTiny) * kUnit;
       wait(sm, &sm.sfull[sb], (it >> 1) & 1, a, 300);  // (should it run out, the vote below ends the work)
       __syncwarp();
       const uint32_t col = tmem + lanes + kSCol + (uint32_t)(sb * 2 * kRows + row0);
@@ -667,17 +701,24 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
 #pragma unroll
           for (int r = 0; r < kPerThread; r += 4) {
             const float4 m = *reinterpret_cast<const float4*>(&sm.m[row0 + r]);
-            const float mr[4] = {m.x, m.y, m.z, m.w};
+            const float4 b = *reinterpret_cast<const float4*>(&sm.back[row0 + r]);
+            const float mr[4] = {m.x, m.y, m.z, m.w}, c[4] = {b.x * scale, b.y * scale, b.z * scale, b.w * scale};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const float y = fmaf(__uint_as_float(lo[r + j]), 0.0625f, __uint_as_float(hi[r + j]));
-              w[r + j] = ex2_approx(fmaf(y, c, -mr[j])) * held;
+              w[r + j] = ex2_approx(fmaf(y, c[j], -mr[j])) * held;
             }
           }
         }
         if (!all_seen) {
+          bool broken = false;  // NaN in a place that is not seen: the key's codes may be NaN, and must not reach the sums
 #pragma unroll
-          for (int r = 0; r < kPerThread; ++r) w[r] = (seen >> r) & 1 ? w[r] : 0.f;
+          for (int r = 0; r < kPerThread; ++r) {
+            const bool is = (seen >> r) & 1;
+            broken |= !is && w[r] != w[r];
+            w[r] = is ? w[r] : 0.f;
+          }
+          if (__any_sync(0xffffffffu, broken)) clear_nan(sm, a, (uint32_t)it, my_key, broken);
         }
 #pragma unroll
         for (int r = 0; r < kPerThread; ++r) most = fmaxf(most, w[r]);
@@ -694,7 +735,7 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
 #pragma unroll
           for (int r = 0; r < kPerThread; ++r) {
             const float y = fmaf(__uint_as_float(lo[r]), 0.0625f, __uint_as_float(hi[r]));
-            top[r] = (seen >> r) & 1 ? fmaf(y, c, height) : -INFINITY;
+            top[r] = (seen >> r) & 1 ? fmaf(y, sm.back[row0 + r] * scale, height) : -INFINITY;
           }
           const float v = reduce16(top, lane, [](float x, float y) { return fmaxf(x, y); });
           sm.part[quarter][row0 + (lane >> 1)] = v;
@@ -783,9 +824,9 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
     const int64_t piece = (int64_t)blockIdx.x * 2 + (u.head ? 1 : 0), first_row = out_row(a, u);
     if (tid < kRows) {
       const float total = (sm.part[0][tid] + sm.part[1][tid]) + (sm.part[2][tid] + sm.part[3][tid]), m = sm.m[tid];
-      sm.f[tid] = !u.whole ? 1.f : total > 0.f ? 1.f / (total * kUnit) : 0.f;
+      sm.f[tid] = !u.whole ? 1.f : total != 0.f ? 1.f / (total * kUnit) : 0.f;
       if (!u.whole) part.ml[piece * kRows + tid] = make_float2(m, total);
-      else if (tid < u.rows) a.lse[first_row + tid] = total > 0.f ? (m + log2f(total)) * 0.6931471805599453f : -INFINITY;
+      else if (tid < u.rows) a.lse[first_row + tid] = total != 0.f ? (m + log2f(total)) * 0.6931471805599453f : -INFINITY;
     }
     if (tid == 0 && u.head && !u.whole) {
       sm.cut_pieces = (int)((u.stop - 1) / plan.share) - (int)blockIdx.x + 1;
@@ -798,7 +839,7 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
     const int rows = u.rows;
     // the next unit's queries while this one's last products run
     more = units.next(sm, a, u);
-    if (more) factor = load_queries(sm, a, u);
+    if (more) load_queries(sm, a, u);
     wait(sm, &sm.pfree, (it - 1) & 1, a, 303);
     __syncwarp();
     tc_fence_after();
@@ -970,10 +1011,10 @@ scaled_join_kernel(const CtaInfo* __restrict__ info, int ctas, const Partials pa
     o.z = fmaf(v.z, w, o.z);
     o.w = fmaf(v.w, w, o.w);
   }
-  const float f = sum > 0.f ? 1.f / (sum * kUnit) : 0.f;
+  const float f = sum != 0.f ? 1.f / (sum * kUnit) : 0.f;
   reinterpret_cast<uint2*>(out + (i.row + row) * kDv)[tid] =
       make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
-  if (tid == 0) lse[i.row + row] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  if (tid == 0) lse[i.row + row] = sum != 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
 // Workspace: status words, the CTAs' infos, the partials.

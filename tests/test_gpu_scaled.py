@@ -104,9 +104,9 @@ def reference(c, parent=None, draft_mask=None, sm=SM):
             outs.append(w @ rows[:, :DV])
             lses.append(l)
             mags.append(w @ rows[:, :DV].abs())
-            # queries in two parts: 2^-22.8 of the largest of the block's rows, for every element of the key; the dot
-            # product's own sums in single precision
-            split = q.abs().max() * 2.0 ** -22 * (rows.abs().sum(1).max() * sm)
+            # queries in two parts: 2^-22.8 of the row's largest, for every element of the key; the dot product's own
+            # sums in single precision
+            split = q.abs().amax(-1) * 2.0 ** -22 * (rows.abs().sum(1).max() * sm)
             errs.append(mag.amax(-1) * (D + 8) * 2.0 ** -24 + split)
         t0 += m
         k0 += n
@@ -259,6 +259,58 @@ def test_slots_outside_the_pool_read_zeros(B):
     assert B.verify_attn_mla_check(ws) == B.VMLA_ERR_INDEX
     assert int(ws[:8].view(torch.int32)[1]) in (5, 300, 800)
     check(c, out, lse)
+
+
+def test_rows_of_very_different_sizes(B):
+    """A row's precision does not depend on the rows beside it, and an infinite or broken one spoils no other."""
+    c = case([700, 300], [3, 2], 16, seed=21)
+    c["q"][1, 4] *= 2.0 ** 24
+    c["q"][2, 5] *= 2.0 ** -60
+    c["q"][3, 0] *= 2.0 ** 16
+    out, lse, _ = run(B, c)
+    check(c, out, lse)
+    c["q"][0, 7, 100] = math.inf
+    c["q"][4, 9, 570] = math.nan
+    broken = torch.zeros((5, 16), dtype=torch.bool, device="cuda")
+    broken[0, 7] = broken[4, 9] = True
+    got, got_l, _ = run(B, c)
+    assert bool(got[broken].isnan().all()) and bool(got_l[broken].isnan().all())
+    want, want_l, _ = run(B, {**c, "q": torch.where(broken[:, :, None], 0, c["q"])})
+    # (the others as without them, but for when their references rise)
+    assert torch.allclose(got[~broken].float(), want[~broken].float(), rtol=2.0 ** -6, atol=1e-2)
+    assert torch.allclose(got_l[~broken], want_l[~broken], rtol=2.0 ** -18, atol=1e-5)
+
+
+@pytest.mark.parametrize("nk,heads", [(1, 16), (130, 16), (700, 1), (5000, 40)])
+def test_nan_in_masked_places(B, nk, heads):
+    """A draft whose codes are NaN makes NaN of the rows that see it and of no other."""
+    nq = min(nk, 9)
+    c = case([nk, 40], [nq, 1], heads, seed=nk)
+    bad = nq // 2
+    slot = int(c["kv"][nk - nq + bad])
+    keep = c["pool"].clone()
+    c["pool"][slot, 5] = 0x7F
+    c["pool"][slot, 300:500] = 0xFF
+    c["pool"][slot, 575] = 0x7F
+    sees = torch.zeros((nq, nq), dtype=torch.bool)
+    for i in range(nq):
+        sees[i, :i + 1] = True
+        sees[i, bad] = i in (bad, nq - 1)
+    words = [int(sum(1 << k for k in range(nq) if sees[i, k])) for i in range(nq)] + [1]
+    mask = torch.tensor(words, dtype=torch.int64, device="cuda")
+    out, lse, _ = run(B, c, draft_mask=mask)
+    for i in range(nq):
+        if sees[i, bad]:
+            assert bool(out[i].isnan().all()) and bool(lse[i].isnan().all())
+    # the others: as if the place were not there
+    zero = {**c, "pool": keep}
+    zero["pool"][slot] = 0
+    o, l, mag, es = reference(zero, draft_mask=mask)
+    rows = [i for i in range(nq) if not sees[i, bad]] + [nq]
+    want_o, want_l, _ = run(B, zero, draft_mask=mask)
+    check(zero, want_o, want_l, draft_mask=mask)
+    for i in rows:
+        assert torch.equal(out[i], want_o[i]) and torch.equal(lse[i], want_l[i])
 
 
 def test_malformed_parents(B):
