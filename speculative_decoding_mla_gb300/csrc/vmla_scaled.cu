@@ -31,9 +31,13 @@
 
 #include "vmla_device.cuh"
 #include "vmla_sm100.cuh"
+#include "vmla_weights.cuh"
 
 namespace vmla {
 using namespace sm100;
+using weights::both;
+using weights::fma2;
+using weights::mul2;
 namespace {
 
 constexpr int kTile = 128;          // keys
@@ -73,7 +77,7 @@ struct Shared {
   uint8_t rope[kTile * 64];                   // [key][64 bytes], 64-byte swizzle
   uint8_t q_rope[2 * kRows * 64];             // 64-byte swizzle
   float back[kRows];                          // of each row: what its products are times as a score (log2)
-  float m[kRows], f[kRows];                   // reference of each row (log2), factor of its last change
+  float minus[kRows], f[kRows];               // minus each row's reference (log2), factor of its last change
   float part[4][kRows];                       // per quarter of the keys: row maxima, or row sums
   uint64_t mask[kRows];                       // the unit's rows: visible drafts
   uint32_t cost[VMLA_MAX_BATCH + 1];          // cost position of each sequence's first stream
@@ -600,7 +604,7 @@ __device__ __noinline__ void load_queries(Shared& sm, const ScaledArgs& a, const
       }
     }
     sm.mask[tid] = word;
-    sm.m[tid] = kNone;
+    sm.minus[tid] = -kNone;
   }
   fence_proxy_async_smem();
   named_bar_sync(1, kSoftThreads);
@@ -699,15 +703,14 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
           tmem_ld16(col + kRows, lo);
           tmem_wait_ld();
 #pragma unroll
-          for (int r = 0; r < kPerThread; r += 4) {
-            const float4 m = *reinterpret_cast<const float4*>(&sm.m[row0 + r]);
-            const float4 b = *reinterpret_cast<const float4*>(&sm.back[row0 + r]);
-            const float mr[4] = {m.x, m.y, m.z, m.w}, c[4] = {b.x * scale, b.y * scale, b.z * scale, b.w * scale};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float y = fmaf(__uint_as_float(lo[r + j]), 0.0625f, __uint_as_float(hi[r + j]));
-              w[r + j] = ex2_approx(fmaf(y, c[j], -mr[j])) * held;
-            }
+          for (int r = 0; r < kPerThread; r += 2) {
+            const float2 c = mul2(*reinterpret_cast<const float2*>(&sm.back[row0 + r]), both(scale));
+            const float2 y = fma2(make_float2(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1])), both(0.0625f),
+                                  make_float2(__uint_as_float(hi[r]), __uint_as_float(hi[r + 1])));
+            const float2 z = fma2(y, c, *reinterpret_cast<const float2*>(&sm.minus[row0 + r]));
+            const float2 e = mul2(make_float2(ex2_approx(z.x), ex2_approx(z.y)), both(held));
+            w[r] = e.x;
+            w[r + 1] = e.y;
           }
         }
         if (!all_seen) {
@@ -743,10 +746,10 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
         sync();
         if (sm.stop) return;
         if (tid < kRows) {
-          const float old = sm.m[tid];
+          const float old = -sm.minus[tid];
           const float top = fmaxf(fmaxf(fmaxf(sm.part[0][tid], sm.part[1][tid]), fmaxf(sm.part[2][tid], sm.part[3][tid])), old);
           sm.f[tid] = ex2_approx(old - top);
-          sm.m[tid] = top;
+          sm.minus[tid] = -top;
         }
         sync();
         float f[kPerThread];
@@ -784,7 +787,11 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
       if (lane == 0) mbar_arrive(&sm.sfree[sb]);
       const float back = __frcp_rn(held);
 #pragma unroll
-      for (int r = 0; r < kPerThread; ++r) l[r] = fmaf(w[r], back, l[r]);
+      for (int r = 0; r < kPerThread; r += 2) {
+        const float2 sum = fma2(make_float2(w[r], w[r + 1]), both(back), make_float2(l[r], l[r + 1]));
+        l[r] = sum.x;
+        l[r + 1] = sum.y;
+      }
       // three parts of each weight, four rows to a word
       const uint32_t counts = scale >= kTiny ? 0xFFFCFFFCu : 0u;
       uint32_t parts[kParts][4];
@@ -823,7 +830,7 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
     sync();
     const int64_t piece = (int64_t)blockIdx.x * 2 + (u.head ? 1 : 0), first_row = out_row(a, u);
     if (tid < kRows) {
-      const float total = (sm.part[0][tid] + sm.part[1][tid]) + (sm.part[2][tid] + sm.part[3][tid]), m = sm.m[tid];
+      const float total = (sm.part[0][tid] + sm.part[1][tid]) + (sm.part[2][tid] + sm.part[3][tid]), m = -sm.minus[tid];
       sm.f[tid] = !u.whole ? 1.f : total != 0.f ? 1.f / (total * kUnit) : 0.f;
       if (!u.whole) part.ml[piece * kRows + tid] = make_float2(m, total);
       else if (tid < u.rows) a.lse[first_row + tid] = total != 0.f ? (m + log2f(total)) * 0.6931471805599453f : -INFINITY;
