@@ -610,8 +610,8 @@ def _beam_reorder_args(src, dst, parent, beams, length=None, new_length=None, st
     if status_word is not None and status_word.numel() < 2:
         raise ValueError("status_word: two words expected")
     _same_device(src=src, dst=dst, parent=parent, length=length, new_length=new_length, status_word=status_word)
-    size = src.element_size() if getattr(src, "is_cuda", False) else 0
-    if size not in (2, 4, 8) or dst.element_size() != size:
+    size, to = (t.element_size() if getattr(t, "is_cuda", False) else 0 for t in (src, dst))
+    if size not in (2, 4, 8) or to != size:
         raise ValueError("src, dst: device memory of the same type, of 2, 4 or 8 bytes, expected")
     words = int(src.shape[1]) * size
     steps = [_step(src, 0, int(src.shape[1])) * size, _step(dst, 0, int(dst.shape[1])) * size]
