@@ -451,8 +451,7 @@ int verify_attn_mla_append(const void* latent, int64_t latent_stride, const void
  * and where that raises the scale, the block's rows in front of them are coded
  * again: e4m3(code x old / new), nearest even (rows behind them keep their
  * codes: nothing valid lies there when a cache grows in order).  A value of
- * +-inf is coded as the largest code, NaN as the NaN code, which the attention
- * does not accept.
+ * +-inf is coded as the largest code, NaN as the NaN code.
  * The tokens of one block stand together in the call, their slots ascending
  * (as verify_attn_mla_step_tables lists them; padding may stand between them);
  * tokens of a block that stand apart would set its scale twice, in either order.  A token left out by an
@@ -470,8 +469,10 @@ int verify_attn_mla_append_scaled(const void* latent, int64_t latent_stride, con
  * trees alike.  The definition at the top of this file with
  *   row_j = kv_scales[s / block_tokens] x code values of slot s = kv_indices[kv_indptr[b] + j]
  * (real products; no rounding of rows).  Scores, softmax and sums are fp32; the
- * queries enter in two e4m3 parts (to 2^-22 of the largest of 32 rows), the
- * weights with 9 significant bits, out is rounded once to bf16.
+ * queries enter in two e4m3 parts (to 2^-22 of the row's largest), the weights
+ * with 9 significant bits, out is rounded once to bf16.  A query row that holds
+ * an infinity or NaN, or sees a key with a NaN code, gets out and lse of NaN; no
+ * other row does.
  *   kv_scales  fp32, finite and >= 0 (below 2^-100: the block's values count as
  *              zero, scored by the scale as it is)
  *   pool_slots a multiple of block_tokens; the pool is 16-byte aligned
@@ -483,8 +484,7 @@ int verify_attn_mla_append_scaled(const void* latent, int64_t latent_stride, con
  *   workspace  >= verify_attn_mla_scaled_workspace_size() bytes, 256 B aligned,
  *              for this call alone while it runs; its size depends on the device only
  * A sequence without drafts writes nothing; rows of q, out and lse from
- * qo_indptr[batch] on are left as they are.  Rows of kv_indices that no query
- * of the sequence sees still have to hold codes other than NaN.
+ * qo_indptr[batch] on are left as they are.
  * Capture-safe; no host synchronisation.  Lengths out of order or past a bound
  * are found on the device: nothing is computed and VMLA_ERR_SHAPE recorded.  A
  * slot outside the pool takes part as a row of zeros and records VMLA_ERR_INDEX
@@ -519,7 +519,10 @@ int verify_attn_mla_scaled(const void* q, const void* kv_pool_e4m3, int64_t pool
  *   kv_indices [max_total_kv], positions, slots [max_total_q], kv_indptr,
  *   qo_indptr [batch + 1] int32 out
  *   status_word    optional, two uint32
- * block_tokens 1 makes block_table a table of slots.  An entry of the table that
+ * block_tokens 1 makes block_table a table of slots.  Blocks that cached[b] no
+ * longer reaches (a step whose drafts were rejected began them) are replaced by
+ * fresh ones when the request grows again: give them back to the free list, or
+ * keep room for them.  An entry of the table that
  * is negative, or whose slots pass 2^31, gives slots of -1.  A negative length or
  * a request longer than the table's row records VMLA_ERR_SHAPE (request), and
  * more keys, tokens or new blocks than there is room for VMLA_ERR_FULL: the

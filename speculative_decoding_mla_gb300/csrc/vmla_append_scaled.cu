@@ -10,10 +10,13 @@
 // cache's readers scale in any order; against amax / 448 it gives away less than one bit at the bottom of the range.
 //
 // A token costs 1152 bytes in, 256 of table, 576 out and 256 per head.  With blocks of one slot a warp takes a token
-// and has its row in registers while the largest value is found.  Otherwise a CTA takes a run: its warps take the
-// rows in turn, agree on the scale in shared memory, and code them, reading them a second time (from L1 or L2: a
-// run is at most 128 rows, 147 KB).  A CTA looks for runs that begin in a window of tokens: one token where there
-// are few (each run then has its own CTA; the others leave at once), else as many as a block has slots.
+// and has its row in registers while the largest value is found.  Otherwise a CTA takes a run: each of its 16 warps has
+// four rows at a time, all their loads on their way together; the CTA agrees on the scale in shared memory, and the rows
+// are coded from the registers (a run of more than 64 rows is read a second time, from L1 or L2).  A CTA looks for runs
+// that begin in a window of tokens: one token where there are few (each run then has its own CTA; the others leave at
+// once), else as many as a block has slots.
+// Measured: 17 000 tokens of 16 heads in blocks of 64 24.9 us, 4.1 TB/s (a row at a time by eight warps, read twice: 32.1);
+// a step of 144 tokens of 64 heads 6 to 8 us, which are launch and latencies.
 #include <cuda_runtime.h>
 
 #include "vmla_device.cuh"

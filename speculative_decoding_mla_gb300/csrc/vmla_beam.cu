@@ -11,7 +11,8 @@
 // the threads' granules bounds the row's K-th token from below, and no token above the bound lies outside the K
 // threads that have these granules: only their granules are read again (from L2), the tokens above the bound listed,
 // and the list ranked.  Rows are cut into parts, one CTA each, while that is needed to fill the GPU.
-// The second kernel, a CTA per request, joins the parts' sums and merges the sorted lists: K rounds of one warp.
+// The second kernel, a CTA per request, joins the parts' sums and merges the sorted lists: the lists' heads are ranked,
+// which leaves at most K (K + 1) / 2 entries, and one warp takes the best of them K times, a lane per list.
 //
 // Scores of different beams are compared through lse_w, and the single-precision terms put it off by up to about
 // 4e-6 (kMargin).  Where two neighbours of the merged order, or the last of it and one that is left out, are of
@@ -19,7 +20,13 @@
 // (weight_units, exact in any order: equal rows have equal sums wherever they lie) and merges anew, until no beam is
 // left in doubt.  Scores closer than about 2^-27 are not told apart for certain.
 //
-// The logits bound it: 2 or 4 bytes a token in, and about four instructions.
+// Sums are kept as two floats (an exact sum of two): doubles cost more than all the rest, at their rate on this GPU.
+//
+// What bounds it: for many rows the logits, 2 or 4 bytes a token in, and the exponentials, 16 a clock and SM.  Measured:
+// 64 x 8 beams of 131 072 tokens in bf16 (134 MB) 45 us, the rows' kernel 31 of them (4.3 TB/s; 60 % of the issue slots),
+// the join 9, the reordering of tables of 4000 slots 7; 9 x 15 beams, 30 kept, of 151 001 tokens in fp32 (82 MB) 48 us:
+// 24, 14 and 11; one request of four beams 16 us: 7, 8 and 4, all latency.  (Doubles in the loop, every thread ranked
+// against all and the entries ranked against each other: 60, 77 and 18.4 us.)
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -650,7 +657,8 @@ beam_reorder_kernel(const ReorderArgs a, int64_t rows) {
   }
 }
 
-// CTAs per row of logits: three for each SM, as far as each has 4096 tokens.
+// CTAs per row of logits: three for each SM, as far as each has 4096 tokens.  (64 x 8 rows of 131 072: one part each
+// 45 us, two 47; 135 rows of 151 001: four parts 48 us, two 48, eight 56, as lists to merge grow with the parts.)
 int parts_of(int64_t rows, int vocab, int sms) {
   int parts = 1;
   while (parts < kMaxParts && rows * parts < 3 * (int64_t)sms && vocab / (parts * 2) >= 4096) parts *= 2;

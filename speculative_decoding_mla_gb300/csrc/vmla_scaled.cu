@@ -4,9 +4,9 @@
 //   s_rj = sm_scale a_j <q_r, k_j>,  p_rj = 2^(s_rj log2 e - m_r),  out_r = sum_j p_rj a_j k_j[:512] / sum_j p_rj.
 // The codes are operands as they are: nothing is converted to bf16, staged, or written back.  What is not 8 bits wide
 // is split into parts that are, exactly or nearly so:
-//   queries  q a = hi + lo / 16, both e4m3, a the power of two that brings the largest of the 32 rows to (224, 448]:
+//   queries  q a_r = hi + lo / 16, both e4m3, a_r the power of two that brings the row's largest to (224, 448]:
 //            off by at most 2^-14 of what is 448 at the largest (2^-22.8), less than an fp32 dot product's rounding
-//   weights  p a_j 2^11, in fp16 rounded to 9 bits, cut into three parts of three bits, e5m2: the upper byte of an fp16
+//   weights  p a_j 2^9, in fp16 rounded to 9 bits, cut into three parts of three bits, e5m2: the upper byte of an fp16
 //            number is an e5m2 number, so a part is an AND and the rest an exact difference.  Its range (2^-16 to 2^15
 //            here) is why it is not two e4m3 parts: beside a key of much weight, 10^5 keys of weight 10^-5 each still count.
 //
@@ -17,13 +17,26 @@
 // A softmax thread has one key and 16 rows: a_j is its own number, the reference m_r is raised only when a weight passes
 // 2^15 (told by one barrier with a vote per tile), and row sums stay in registers until the unit ends.
 //
-// Rows are fetched by tile::gather4 (four slots x 128 bytes, swizzled as the products read them) straight from the pool;
-// a slot that is none, or a place behind the last key, is a coordinate outside the tensor and reads zeros.
+// Rows are fetched straight from the pool, 128 columns at a time into a ring of ten such chunks (two and a half tiles): by
+// boxes of 16 slots where the slots of a tile are consecutive in 16s, else by gathers of four slots; a slot that is none,
+// or a place behind the last key, is a coordinate outside the tensor and reads zeros.
 //
-// Work: CTAs (one per SM) form lanes of G; row blocks of a sequence form streams of G over its key tiles, laid end to end
-// (a stream costs its tiles and kFixed more); lane l takes the l-th share of the whole length.  The G CTAs of a lane read
-// the same rows at about the same time, from L2 but for the first.  Streams cut by a lane's end leave fp32 partials
-// (at most two per CTA), and a second launch joins them.  Every CTA works the plan out from the device's lengths.
+// Work: the row blocks (32 rows) of a sequence form streams over its key tiles, laid end to end (a stream costs its tiles
+// and kFixed more); the l-th of the CTAs, one per SM, takes the l-th share of the whole length.  Streams cut by the end of a
+// share leave fp32 partials (at most two per CTA), and a second launch joins them.  Every CTA works the plan out from the
+// device's lengths.
+//
+// What bounds it: shared memory.  Of its 128 bytes a clock a tile takes 1755 wavefronts as operands of the products, 540
+// as it arrives, and some 900 for weights, references, indices and shuffles; with eight trees of 40 to 64 drafts over
+// 9 000 to 16 000 keys the pipe is busy 83 % of the whole launch, the tensor pipe 37 %, DRAM 4 %.  A tile takes 1.5 us
+// there, of which its products are 0.9; 1.65 us where the rows come from DRAM (32 requests of 64 heads).  About 18 us of
+// a call are launches, plan, queries, the first tile's loads, results and the join (one request of 1024 keys: 20 us).
+// Measured (us): 32 requests of 64 heads, up to 60 000 keys 117; 64 requests of 8 heads and 4 drafts, up to 32 768 keys 82;
+// eight trees 276; 185 000 keys, 64 heads, 4 drafts 138.  Tried, without gain: clusters of two and four CTAs that share
+// each tile's loads by multicast (faster than one issuing thread that also loaded, slower than this form: 142 us against
+// 121); units of 64 rows (as fast; the accumulators of three parts would not fit, so the parts took turns); 16 softmax
+// warps of 8 rows; a vote by word and barrier or cast early and counted late; longer sleeps of the waiting warps;
+// references in registers; rows fetched into L2 ahead (all within 2 %).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -92,13 +105,13 @@ struct Shared {
   volatile int32_t abort_flag;
   int32_t stop;
   uint32_t fault[2];                          // first fault of this CTA: code, info
-  int32_t cut_pieces, cut_rows;               // the stream that starts in this CTA's lane and goes on in the next
+  int32_t cut_pieces, cut_rows;               // the stream that starts in this CTA's share and goes on in the next
   int64_t cut_row;
 };
 constexpr size_t kSharedBytes = sizeof(Shared) + 1024;
 static_assert(kSharedBytes <= 232448, "shared memory");
 
-// What a CTA tells the joining launch: the stream that starts in its lane and is cut by the lane's end, and its fault.
+// What a CTA tells the joining launch: the stream that starts in its share and is cut by the share's end, and its fault.
 struct alignas(32) CtaInfo {
   int64_t row;      // first row of out
   int32_t pieces;   // 0: no such stream
@@ -192,7 +205,7 @@ __device__ bool make_plan(Shared& sm, const ScaledArgs& a, Plan& plan) {
 
 // One row block of a sequence over some of its tiles.
 struct Unit {
-  int row_block, rows;      // rows of the block that are the sequence's 
+  int row_block, rows;      // rows of the block that are the sequence's
   int tile0, tiles;         // its tiles
   int q0, nq;               // the sequence's drafts
   int kv0, keys, prefix;    // first entry of kv_indices; keys and prefix of the sequence
@@ -200,9 +213,9 @@ struct Unit {
   uint32_t stop;            // cost position behind the stream's tiles
 };
 
-// The units of a CTA in its lane, in order; the CTAs of a lane have the same tiles.
+// The units of a CTA, in order.
 struct Units {
-  uint32_t at, end, from;  // cost position of the current stream; of the lane's end and start
+  uint32_t at, end, from;  // cost position of the current stream; of the share's end and start
   int b, g, n;
   Seq s;
   __device__ __forceinline__ void enter(const Shared& sm, const ScaledArgs& a, int sequence) {
@@ -300,11 +313,10 @@ __device__ __forceinline__ bool soft_vote(bool any) {
 }
 
 // ------------------------------------------------------------------ loads (six warps)
-// A tile's pieces are its four chunks and the rotated columns, each with a barrier of its own per stage.  Where all of the
+// A tile's pieces are its four chunks and the rotated columns, each with a barrier of its own per place.  Where all of the
 // tile's slots are consecutive in groups of kRun, a piece is eight boxes and one or two warps'; otherwise it is 32 gathers
-// of four rows, dealt out to all six: starting a copy takes its thread some 80 clocks.  The
-// slots are brought to all lanes of a warp, and one lane starts the copies, with operands that the whole warp has (see
-// elect_one).
+// of four rows, dealt out to all six: starting a copy takes its thread some 80 clocks.  The slots are brought to all lanes
+// of a warp, and one lane starts the copies, with operands that the whole warp has (see elect_one).
 // A barrier's parity tells apart two rounds of its stage, no more.  Every warp has a part in a chunk of every tile and waits
 // for it, so it is never two rounds ahead of any piece (its chunk's release three tiles ago follows all of the tile before
 // that), and no round that it waits for can pass unseen, since the piece lacks its part.

@@ -10,7 +10,11 @@
 // A call writes 4 bytes a key and reads 4 a block, so large ones are bound by the writes and small ones by a chain of
 // loads.  One launch: every CTA takes the running sums of all requests itself (at most 512, two a thread: one chain
 // of loads and three barriers, instead of a second launch behind a first), checks them, and then writes its part of
-// each array; the entry of a thread's first key is found by bisection in shared memory, the others by going on.
+// each array.  A warp takes 256 keys at a time: one bisection in shared memory, and where they lie in one request's
+// old blocks, which is mostly so, eight keys a lane looked up side by side; else key by key.
+// Measured: 256 requests of up to 65 536 tokens in blocks of 64 (5.7 M keys, 23 MB) 14.3 us, 1.6 TB/s, of which some 5 us
+// are the launch and the sums (a bisection and a block's test per four keys: 22.5 us, bound by instructions); 32
+// requests slot by slot (0.3 M keys) 6.6 us.
 // Entries that the call adds to the block table are never read back from it (they follow from the free list), so
 // CTAs need no order among them; the count of free blocks, which may be updated in place, is written by the CTA that
 // finishes last.
