@@ -71,7 +71,7 @@ constexpr uint32_t kSCol = kChunks * kOCols;      // 384
 constexpr int kSlots = 10;          // chunks in shared memory: two and a half tiles
 constexpr int kFixed = 8;           // what a unit costs beside its tiles, in tiles
 constexpr float kNone = -3e38f;     // reference of a row that has seen no key
-constexpr float kUnit = 512.f;      // weights are held times 2^9
+constexpr float kUnitBits = 9.f;    // weights are held times 2^9
 constexpr float kMost = 32768.f;    // largest weight held
 constexpr float kTiny = 0x1p-100f;  // smaller scales count as zero
 static_assert(kSCol + 2 * 2 * kRows == 512, "tensor memory");
@@ -90,7 +90,7 @@ struct Shared {
   uint8_t rope[kTile * 64];                   // [key][64 bytes], 64-byte swizzle
   uint8_t q_rope[2 * kRows * 64];             // 64-byte swizzle
   float back[kRows];                          // of each row: what its products are times as a score (log2)
-  float minus[kRows], f[kRows];               // minus each row's reference (log2), factor of its last change
+  float minus[kRows], f[kRows];               // kUnitBits less each row's reference (log2), factor of its last change
   float part[4][kRows];                       // per quarter of the keys: row maxima, or row sums
   uint64_t mask[kRows];                       // the unit's rows: visible drafts
   uint32_t cost[VMLA_MAX_BATCH + 1];          // cost position of each sequence's first stream
@@ -121,8 +121,8 @@ struct alignas(32) CtaInfo {
 };
 
 struct Partials {
-  float* o;        // [2 x CTAs][kRows][512], weights times kUnit
-  float2* ml;      // [2 x CTAs][kRows]: reference (log2), sum
+  float* o;        // [2 x CTAs][kRows][512]
+  float2* ml;      // [2 x CTAs][kRows]: reference less kUnitBits (log2), sum
 };
 
 __device__ __forceinline__ void fault(Shared& sm, int code, uint32_t info) {
@@ -701,12 +701,12 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
         for (int r = 0; r < kPerThread; ++r) seen |= (uint32_t)((sm.mask[row0 + r] >> (key - u.prefix)) & 1) << r;
       }
       const bool all_seen = __all_sync(0xffffffffu, seen == 0xFFFFu);
-      const float held = fmaxf(scale, kTiny) * kUnit;
+      const float held = fmaxf(scale, kTiny);
       wait(sm, &sm.sfull[sb], (it >> 1) & 1, a, 300);  // (should it run out, the vote below ends the work)
       __syncwarp();
       const uint32_t col = tmem + lanes + kSCol + (uint32_t)(sb * 2 * kRows + row0);
       float w[kPerThread];
-      for (;;) {
+      for (bool raised = false;; raised = true) {
         tc_fence_after();
         float most = 0.f;
         {
@@ -737,6 +737,15 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
         }
 #pragma unroll
         for (int r = 0; r < kPerThread; ++r) most = fmaxf(most, w[r]);
+        if (raised) {
+          // 2^9 at the most now, but for scores so large that a unit in their last place is several powers of two: there the
+          // reference is rounded down, so that the largest weight is not lost, and what passes 2^15 is cut
+          if (most > kMost) {
+#pragma unroll
+            for (int r = 0; r < kPerThread; ++r) w[r] = w[r] > kMost ? kMost : w[r];  // (NaN stays)
+          }
+          break;
+        }
         if (!soft_vote(most > kMost || sm.abort_flag != 0)) break;
         // some weight is too large for its row's reference: raise the references to the tile's largest
         if (tid == 0) sm.stop = sm.abort_flag;
@@ -750,7 +759,7 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
 #pragma unroll
           for (int r = 0; r < kPerThread; ++r) {
             const float y = fmaf(__uint_as_float(lo[r]), 0.0625f, __uint_as_float(hi[r]));
-            top[r] = (seen >> r) & 1 ? fmaf(y, sm.back[row0 + r] * scale, height) : -INFINITY;
+            top[r] = (seen >> r) & 1 ? __fmaf_rd(y, sm.back[row0 + r] * scale, height) : -INFINITY;
           }
           const float v = reduce16(top, lane, [](float x, float y) { return fmaxf(x, y); });
           sm.part[quarter][row0 + (lane >> 1)] = v;
@@ -758,10 +767,11 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
         sync();
         if (sm.stop) return;
         if (tid < kRows) {
-          const float old = -sm.minus[tid];
-          const float top = fmaxf(fmaxf(fmaxf(sm.part[0][tid], sm.part[1][tid]), fmaxf(sm.part[2][tid], sm.part[3][tid])), old);
-          sm.f[tid] = ex2_approx(old - top);
-          sm.minus[tid] = -top;
+          const float old = sm.minus[tid];
+          const float top = fmaxf(fmaxf(sm.part[0][tid], sm.part[1][tid]), fmaxf(sm.part[2][tid], sm.part[3][tid]));
+          const float now = fminf(__fsub_ru(kUnitBits, top), old);
+          sm.f[tid] = ex2_approx(now - old);
+          sm.minus[tid] = now;
         }
         sync();
         float f[kPerThread];
@@ -843,7 +853,7 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
     const int64_t piece = (int64_t)blockIdx.x * 2 + (u.head ? 1 : 0), first_row = out_row(a, u);
     if (tid < kRows) {
       const float total = (sm.part[0][tid] + sm.part[1][tid]) + (sm.part[2][tid] + sm.part[3][tid]), m = -sm.minus[tid];
-      sm.f[tid] = !u.whole ? 1.f : total != 0.f ? 1.f / (total * kUnit) : 0.f;
+      sm.f[tid] = !u.whole ? 1.f : total != 0.f ? 1.f / total : 0.f;
       if (!u.whole) part.ml[piece * kRows + tid] = make_float2(m, total);
       else if (tid < u.rows) a.lse[first_row + tid] = total != 0.f ? (m + log2f(total)) * 0.6931471805599453f : -INFINITY;
     }
@@ -1030,7 +1040,7 @@ scaled_join_kernel(const CtaInfo* __restrict__ info, int ctas, const Partials pa
     o.z = fmaf(v.z, w, o.z);
     o.w = fmaf(v.w, w, o.w);
   }
-  const float f = sum != 0.f ? 1.f / (sum * kUnit) : 0.f;
+  const float f = sum != 0.f ? 1.f / sum : 0.f;
   reinterpret_cast<uint2*>(out + (i.row + row) * kDv)[tid] =
       make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
   if (tid == 0) lse[i.row + row] = sum != 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;

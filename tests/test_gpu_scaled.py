@@ -281,6 +281,79 @@ def test_rows_of_very_different_sizes(B):
     assert torch.allclose(got_l[~broken], want_l[~broken], rtol=2.0 ** -18, atol=1e-5)
 
 
+@pytest.mark.parametrize("power", [-90, -40, 40, 100, 110])
+def test_scales_far_from_one(B, power):
+    """Scales anywhere in their range, queries that bring the scores back to where softmax has work."""
+    c = case([600, 77], [2, 1], 24, block=16, seed=power + 200)
+    c["scales"] *= 2.0 ** power
+    c["q"] = (c["q"].float() * 2.0 ** -power).to(torch.bfloat16)
+    out, lse, _ = run(B, c)
+    assert bool(torch.isfinite(lse).all())
+    check(c, out, lse)
+
+
+@pytest.mark.parametrize("power,queries", [(40, 2.0 ** -12), (40, 1.0), (20, 2.0 ** 9), (0, 2.0 ** 30), (0, 2.0 ** 60)])
+def test_scores_beyond_their_precision(B, power, queries):
+    """Scores whose last place is whole powers of e: each row gets its largest key's values, or, where two are as large
+    within that place, something between keys."""
+    c = case([900, 300], [1, 3], 16, block=4, seed=3)
+    c["scales"] *= 2.0 ** power
+    c["q"] = (c["q"].float() * queries).to(torch.bfloat16)
+    out, lse, ws = run(B, c)
+    assert B.verify_attn_mla_check(ws) == 0
+    o, l, mag, es = reference(c)
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    assert bool(((lse - l).abs() <= es + l.abs() * 2.0 ** -21 + 1).all())
+    t0 = k0 = clear = 0
+    for n, m in zip(c["nk"], c["nq"]):
+        slot = c["kv"][k0:k0 + n].long()
+        rows = c["pool"][slot].view(torch.float8_e4m3fn).double() * c["scales"].double()[slot // c["block"]][:, None]
+        z = torch.einsum("thd,nd->thn", c["q"][t0:t0 + m].double(), rows) * SM
+        z[:, :, n - m:].masked_fill_(torch.ones((m, m), device="cuda").triu(1).bool()[:, None, :], -math.inf)
+        two = z.topk(2, -1).values
+        sure = two[..., 0] - two[..., 1] > 2 * es[t0:t0 + m] + two[..., 0].abs() * 2.0 ** -21 + 64
+        got, want = out[t0:t0 + m].double(), rows[z.argmax(-1)][..., :DV]
+        assert bool(((got - want).abs() <= want.abs() * 2.0 ** -6)[sure].all())
+        clear += int(sure.sum())
+        t0, k0 = t0 + m, k0 + n
+    assert clear > 30
+
+
+def test_two_streams_at_once(B):
+    """Calls that run side by side, each with its own workspace."""
+    a, b = case([9000, 4000], [4, 2], 16, seed=5), case([700] * 40, [3] * 40, 16, block=16, seed=6)
+    want_a, want_b = run(B, a), run(B, b)
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for s, c in ((one, a), (two, b)):
+            with torch.cuda.stream(s):
+                got.append((c is a, run(B, c)))
+    torch.cuda.synchronize()
+    for is_a, (o, l, _) in got:
+        w = want_a if is_a else want_b
+        assert torch.equal(o, w[0]) and torch.equal(l, w[1])
+
+
+def test_pool_past_32_bits(B):
+    """Slots whose bytes lie beyond 2^32 and 2^33: written by the append, read by the attention."""
+    S, n = 16_000_000, 300
+    pool = torch.zeros((S, D), dtype=torch.uint8, device="cuda")
+    c = case([n], [2], 16, block=8, seed=9)
+    slots = torch.cat([torch.arange(40), 7_456_540 + torch.arange(100), 14_913_080 + torch.arange(100), S - 60 + torch.arange(60)]).to(torch.int32).cuda()
+    scales = torch.zeros(S // 8, device="cuda")
+    kv = torch.randn((n, D), device="cuda").to(torch.bfloat16)
+    one = torch.cat([torch.ones(1, 32), torch.zeros(1, 32)], 1).cuda()
+    B.verify_attn_mla_append_scaled(kv[:, :DV], kv[:, DV:], torch.zeros(n, dtype=torch.int32, device="cuda"), slots, one, pool, scales, block_tokens=8)
+    rows = pool[slots.long()].view(torch.float8_e4m3fn).double() * scales.double()[slots.long() // 8][:, None]
+    assert bool(((rows - kv.double()).abs() <= kv.double().abs() * 2.0 ** -4 * 2.1 + scales.double()[slots.long() // 8][:, None] * 2.0 ** -9).all())
+    assert int((pool.view(-1, 8 * D)[::9973] != 0).any(1).sum()) < 50 and int((scales != 0).sum()) <= 45
+    c.update(pool=pool, scales=scales, kv=slots)
+    out, lse, _ = run(B, c)
+    check(c, out, lse)
+
+
 @pytest.mark.parametrize("nk,heads", [(1, 16), (130, 16), (700, 1), (5000, 40)])
 def test_nan_in_masked_places(B, nk, heads):
     """A draft whose codes are NaN makes NaN of the rows that see it and of no other."""
