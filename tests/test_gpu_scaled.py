@@ -17,6 +17,10 @@ def B():
     return binding
 
 
+def ints(a):
+    return torch.tensor(a, dtype=torch.int32, device="cuda")
+
+
 def pool_of(g, blocks, block, powers=True, spread=0.4):
     x = torch.randn((blocks, block * D), generator=g, device="cuda") * (
         0.5 * torch.exp(spread * torch.randn((blocks, 1), generator=g, device="cuda")))
@@ -237,6 +241,30 @@ def test_a_key_of_much_weight_beside_many_of_little(B):
     sm = math.log(40000.0) / (448.0 * sc)
     out, lse, ws = run(B, c, sm=sm)
     check(c, out, lse, sm=sm)
+
+
+def test_weights_at_their_floor(B):
+    """A column in which the key of most weight has a zero shows what becomes of the small ones: 9 bits down to 2^-17 of the
+    largest, steps of 2^-25 below that."""
+    n, H = 512, 16
+    drop = torch.linspace(0.0, 30.0, n, dtype=torch.float64)  # key j's weight is 2^-drop[j]
+    pool = torch.zeros((n, D), dtype=torch.float8_e4m3fn, device="cuda")
+    pool[:, DV] = -1.0                                        # scores fall with the keys' scales
+    pool[torch.arange(n), torch.arange(n)] = 16.0             # column j: key j alone
+    scales = (1.0 + drop / 64.0).float().cuda()
+    q = torch.zeros((1, H, D), dtype=torch.bfloat16, device="cuda")
+    q[:, :, DV] = 64.0
+    c = dict(q=q, pool=pool.view(torch.uint8), scales=scales, kv=torch.arange(n, dtype=torch.int32, device="cuda"), block=1, nk=[n], nq=[1],
+             kv_indptr=ints([0, n]), qo_indptr=ints([0, 1]))
+    sm = math.log(2.0)                                        # in powers of two: 2^-(64 scale) = 2^-64 2^-drop
+    out, lse, _ = run(B, c, sm=sm)
+    score = -64.0 * scales.double() * sm
+    p = (score - torch.logsumexp(score, 0)).exp()
+    want = p * 16.0 * scales.double()
+    err = (out[0, 0].double() - want).abs()
+    floor = float(p.max()) * 2.0 ** -26 * 16.0 * 1.5          # half a step of the weight times scale (at most 1.5 of the first key's)
+    rel = 2.0 ** -8 + 2.0 ** -9 + 1e-4                        # bf16, the weight's bits, the scores (fp32 about 64 ln 2)
+    assert bool((err <= want * rel + floor).all()), float(((err - want * rel) / floor).max())
 
 
 def test_zero_scales_and_zero_rows(B):
