@@ -224,3 +224,16 @@ def test_captured_and_replayed(B):
         g.replay()
         torch.cuda.synchronize()
         c.check(pool0, scales0)
+
+
+@pytest.mark.parametrize("tokens", [600, 9000])
+def test_padding_in_front_between_and_behind(B, tokens):
+    """A padded batch: long stretches without slots, few tokens to write."""
+    runs = [(3, 0, 64), (1, 60, 4), (7, 5, 20)]
+    c = Case(runs, 64, heads=2, seed=tokens, pad=[0] * (tokens // 3) + [tokens // 3 + 40] * 100 + [tokens // 3 + 100 + 88] * (tokens // 2))
+    pool0, scales0, q0 = c.pool.clone(), c.scales.clone(), c.q.clone()
+    c.call(B)
+    c.check(pool0, scales0)
+    assert c.status.tolist() == [0, 0]
+    pad = c.slots < 0
+    assert torch.equal(c.q[pad], q0[pad]) and not torch.equal(c.q[~pad], q0[~pad])

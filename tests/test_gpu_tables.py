@@ -158,3 +158,33 @@ def test_captured_steps_go_on_where_the_last_stopped(B):
         assert np.array_equal(s.base.cpu().numpy(), base)
         assert s.count.tolist() == [left] and s.kv.tolist()[:len(kv)] == kv
         lengths = [c + a for c, a in zip(lengths, added)]
+
+
+@pytest.mark.parametrize("block", [1, 4, 32, 128])
+def test_long_requests_with_broken_entries_and_outputs_of_any_alignment(B, block):
+    """Whole stretches of keys in old blocks: negative blocks, blocks whose slots pass 2^31, arrays off 16 bytes."""
+    r = np.random.default_rng(block)
+    for off in range(4):
+        s = Step([5000, 300, 2049, 256, 255], [3, 0, 64, 1, 257], block, seed=off)
+        broken = {}
+        for b, n in enumerate([5000, 300, 2049, 256, 255]):
+            for k in r.integers(0, -(-n // block), 3):
+                broken[b, int(k)] = int(r.choice([-1, -2 ** 31, 2 ** 31 - 1, 2 ** 31 // block - 1]))
+        for (b, k), v in broken.items():
+            s.base[b, k] = v
+            s.want["base"][b, k] = v
+        whole = torch.full((s.kv.numel() + off,), -3, dtype=torch.int32, device="cuda")
+        s.kv = whole[off:]
+        s.call(B)
+        kv, first = np.array(s.want["kv"]), s.want["kv_indptr"]
+        for (b, k), v in broken.items():
+            for p in range(k * block, min((k + 1) * block, int(first[b + 1] - first[b]))):
+                slot = v * block + p % block
+                kv[first[b] + p] = slot if 0 <= slot < 2 ** 31 else -1
+        s.want["kv"] = kv
+        slots = []
+        for b, n in enumerate([3, 0, 64, 1, 257]):
+            slots += list(kv[first[b + 1] - n:first[b + 1]])
+        s.want["slots"] = slots + [-1] * 3
+        s.check()
+        assert bool((whole[:off] == -3).all())
