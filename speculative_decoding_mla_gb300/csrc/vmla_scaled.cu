@@ -706,47 +706,50 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
       __syncwarp();
       const uint32_t col = tmem + lanes + kSCol + (uint32_t)(sb * 2 * kRows + row0);
       float w[kPerThread];
-      for (bool raised = false;; raised = true) {
+      // (a unit's first tile sets the references before anything else)
+      for (bool raised = false, look = t > 0;; raised = look = true) {
         tc_fence_after();
-        float most = 0.f;
-        {
-          uint32_t hi[kPerThread], lo[kPerThread];
-          tmem_ld16(col, hi);
-          tmem_ld16(col + kRows, lo);
-          tmem_wait_ld();
+        if (look) {
+          float most = 0.f;
+          {
+            uint32_t hi[kPerThread], lo[kPerThread];
+            tmem_ld16(col, hi);
+            tmem_ld16(col + kRows, lo);
+            tmem_wait_ld();
 #pragma unroll
-          for (int r = 0; r < kPerThread; r += 2) {
-            const float2 c = mul2(*reinterpret_cast<const float2*>(&sm.back[row0 + r]), both(scale));
-            const float2 y = fma2(make_float2(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1])), both(0.0625f),
-                                  make_float2(__uint_as_float(hi[r]), __uint_as_float(hi[r + 1])));
-            const float2 z = fma2(y, c, *reinterpret_cast<const float2*>(&sm.minus[row0 + r]));
-            const float2 e = mul2(make_float2(ex2_approx(z.x), ex2_approx(z.y)), both(held));
-            w[r] = e.x;
-            w[r + 1] = e.y;
+            for (int r = 0; r < kPerThread; r += 2) {
+              const float2 c = mul2(*reinterpret_cast<const float2*>(&sm.back[row0 + r]), both(scale));
+              const float2 y = fma2(make_float2(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1])), both(0.0625f),
+                                    make_float2(__uint_as_float(hi[r]), __uint_as_float(hi[r + 1])));
+              const float2 z = fma2(y, c, *reinterpret_cast<const float2*>(&sm.minus[row0 + r]));
+              const float2 e = mul2(make_float2(ex2_approx(z.x), ex2_approx(z.y)), both(held));
+              w[r] = e.x;
+              w[r + 1] = e.y;
+            }
           }
-        }
-        if (!all_seen) {
-          bool broken = false;  // NaN in a place that is not seen: the key's codes may be NaN, and must not reach the sums
+          if (!all_seen) {
+            bool broken = false;  // NaN in a place that is not seen: the key's codes may be NaN, and must not reach the sums
 #pragma unroll
-          for (int r = 0; r < kPerThread; ++r) {
-            const bool is = (seen >> r) & 1;
-            broken |= !is && w[r] != w[r];
-            w[r] = is ? w[r] : 0.f;
+            for (int r = 0; r < kPerThread; ++r) {
+              const bool is = (seen >> r) & 1;
+              broken |= !is && w[r] != w[r];
+              w[r] = is ? w[r] : 0.f;
+            }
+            if (__any_sync(0xffffffffu, broken)) clear_nan(sm, a, (uint32_t)it, my_key, broken);
           }
-          if (__any_sync(0xffffffffu, broken)) clear_nan(sm, a, (uint32_t)it, my_key, broken);
-        }
 #pragma unroll
-        for (int r = 0; r < kPerThread; ++r) most = fmaxf(most, w[r]);
-        if (raised) {
-          // 2^9 at the most now, but for scores so large that a unit in their last place is several powers of two: there the
-          // reference is rounded down, so that the largest weight is not lost, and what passes 2^15 is cut
-          if (most > kMost) {
+          for (int r = 0; r < kPerThread; ++r) most = fmaxf(most, w[r]);
+          if (raised) {
+            // 2^9 at the most now, but for scores so large that a unit in their last place is several powers of two: there the
+            // reference is rounded down, so that the largest weight is not lost, and what passes 2^15 is cut
+            if (most > kMost) {
 #pragma unroll
-            for (int r = 0; r < kPerThread; ++r) w[r] = w[r] > kMost ? kMost : w[r];  // (NaN stays)
+              for (int r = 0; r < kPerThread; ++r) w[r] = w[r] > kMost ? kMost : w[r];  // (NaN stays)
+            }
+            break;
           }
-          break;
+          if (!soft_vote(most > kMost || sm.abort_flag != 0)) break;
         }
-        if (!soft_vote(most > kMost || sm.abort_flag != 0)) break;
         // some weight is too large for its row's reference: raise the references to the tile's largest
         if (tid == 0) sm.stop = sm.abort_flag;
         {
