@@ -1003,51 +1003,63 @@ scaled_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ScaledA
   }
 }
 
-// Joins the partials of one row of a cut stream: one block per (CTA that begins the stream, row).
-constexpr int kJoinThreads = kDv / 4;
+// Joins the partials of a cut stream: a warp per 128 columns of a row, in CTAs of kJoinRows rows of the stream that begins
+// in a CTA's share.  (A CTA per row: 4864 of them, most with nothing to do, cost 1 us more; a warp for a whole row has too
+// few loads on their way: 185 000 keys in 19 pieces 5 us more.)
+constexpr int kJoinRows = 2, kJoinWarps = 4 * kJoinRows;
 constexpr int kMaxCtas = 512;
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinWarps * 32)
 scaled_join_kernel(const CtaInfo* __restrict__ info, int ctas, const Partials part, uint16_t* __restrict__ out,
                    float* __restrict__ lse, uint32_t* __restrict__ status) {
-  __shared__ float2 ml[kMaxCtas];
-  const int tid = threadIdx.x, cta = blockIdx.x, row = blockIdx.y;
+  __shared__ float weight[kJoinWarps][kMaxCtas + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x, row = blockIdx.y * kJoinRows + (warp >> 2), at = (warp & 3) * 32 + lane;
   grid_dependency_wait();
-  if (cta == 0 && row == 0 && tid < 32) {
+  const CtaInfo i = info[cta];
+  if (cta == 0 && blockIdx.y == 0 && warp == 0) {
     // the call's status: the first CTA's fault
     uint32_t first = 0xffffffffu;
-    for (int k = tid; k < ctas; k += 32)
+    for (int k = lane; k < ctas; k += 32)
       if (info[k].fault != 0) first = min(first, (uint32_t)k);
     first = __reduce_min_sync(0xffffffffu, first);
-    if (tid == 0) {
+    if (lane == 0) {
       status[0] = first == 0xffffffffu ? 0u : info[first].fault;
       status[1] = first == 0xffffffffu ? 0u : info[first].fault_info;
     }
   }
-  const CtaInfo i = info[cta];
   if (row >= i.rows || i.pieces == 0) return;
   // piece 0 lies in this CTA's second slot, piece k in the first slot of the k-th CTA after it
   auto slot = [&](int k) { return k == 0 ? (int64_t)cta * 2 + 1 : ((int64_t)cta + k) * 2; };
-  for (int k = tid; k < i.pieces; k += kJoinThreads) ml[k] = part.ml[slot(k) * kRows + row];
-  __syncthreads();
   float top = kNone;
-  for (int k = 0; k < i.pieces; ++k) top = fmaxf(top, ml[k].x);
+  for (int k = lane; k < i.pieces; k += 32) {
+    const float m = part.ml[slot(k) * kRows + row].x;
+    weight[warp][k] = m;
+    top = fmaxf(top, m);
+  }
+  top = warp_max(top);
   float sum = 0.f;
+  for (int k = lane; k < i.pieces; k += 32) {
+    const float w = ex2_approx(weight[warp][k] - top);
+    weight[warp][k] = w;
+    sum = fmaf(part.ml[slot(k) * kRows + row].y, w, sum);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  __syncwarp();
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
   for (int k = 0; k < i.pieces; ++k) {
-    const float w = ex2_approx(ml[k].x - top);
-    const float4 v = reinterpret_cast<const float4*>(part.o + (slot(k) * kRows + row) * kDv)[tid];
-    sum = fmaf(ml[k].y, w, sum);
-    o.x = fmaf(v.x, w, o.x);
-    o.y = fmaf(v.y, w, o.y);
-    o.z = fmaf(v.z, w, o.z);
-    o.w = fmaf(v.w, w, o.w);
+    const float w = weight[warp][k];
+    const float4 x = reinterpret_cast<const float4*>(part.o + (slot(k) * kRows + row) * kDv)[at];
+    o.x = fmaf(x.x, w, o.x);
+    o.y = fmaf(x.y, w, o.y);
+    o.z = fmaf(x.z, w, o.z);
+    o.w = fmaf(x.w, w, o.w);
   }
   const float f = sum != 0.f ? 1.f / sum : 0.f;
-  reinterpret_cast<uint2*>(out + (i.row + row) * kDv)[tid] =
-      make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
-  if (tid == 0) lse[i.row + row] = sum != 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  reinterpret_cast<uint2*>(out + (i.row + row) * kDv)[at] = make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
+  if (at == 0) lse[i.row + row] = sum != 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
+static_assert(kRows % kJoinRows == 0 && kDv == 4 * 32 * 4, "four warps per row, four columns a lane");
 
 // Workspace: status words, the CTAs' infos, the partials.
 constexpr size_t kInfoOff = 256;
@@ -1103,8 +1115,8 @@ int launch(const ScaledArgs& a, int sms, const Maps& maps, cudaStream_t stream) 
   if (cudaGetLastError() != cudaSuccess) return VMLA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1] = {early_start_attribute()};
-  cfg.gridDim = dim3((unsigned)sms, kRows, 1);
-  cfg.blockDim = dim3(kJoinThreads, 1, 1);
+  cfg.gridDim = dim3((unsigned)sms, kRows / kJoinRows, 1);
+  cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
