@@ -40,6 +40,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cstddef>
 #include <mutex>
 
 #include "vmla_device.cuh"
@@ -83,6 +84,12 @@ struct Seq {
   int32_t q0, nq, kv0, nk;
 };
 
+// Barriers.
+struct Bars {
+  uint64_t full[kSlots], free[kSlots], rope_full, rope_free;
+  uint64_t sfull[2], sfree[2], pfull, pfree, qfull, ofree;
+};
+
 struct Shared {
   uint8_t latent[kSlots][kTile * 128];        // a tile's chunk: [key][128 bytes], 128-byte swizzle
   uint8_t q_latent[kChunks][2 * kRows * 128]; // [hi rows, lo rows][128 bytes], 128-byte swizzle
@@ -99,8 +106,7 @@ struct Shared {
   uint32_t first_at;
   int32_t parent[VMLA_MAX_DRAFT];
   uint32_t sums[2][kThreads / 32];
-  uint64_t full[kSlots], free[kSlots], rope_full, rope_free;
-  uint64_t sfull[2], sfree[2], pfull, pfree, qfull, ofree;
+  Bars bars;
   uint32_t tmem;
   volatile int32_t abort_flag;
   int32_t stop;
@@ -154,15 +160,28 @@ __device__ __forceinline__ int row_blocks(const ScaledArgs& a, int nq) {
 }
 __device__ __forceinline__ int tiles_of(int nk) { return nk / kTile + (nk % kTile != 0); }
 
-// Reads the lengths and shares the work out (whole CTA); false where the lengths are out of order or past a bound.
-__device__ bool make_plan(Shared& sm, const ScaledArgs& a, Plan& plan) {
+// Ends of a thread's sequence in the lengths' arrays.
+struct Ends {
+  int32_t k0 = 0, k1 = 0, q0 = 0, q1 = 0;
+  __device__ __forceinline__ explicit Ends(const ScaledArgs& a) {
+    const int b = threadIdx.x;
+    if (b < a.batch) {
+      k0 = __ldg(a.kv_indptr + b);
+      k1 = __ldg(a.kv_indptr + b + 1);
+      q0 = __ldg(a.qo_indptr + b);
+      q1 = __ldg(a.qo_indptr + b + 1);
+    }
+  }
+};
+
+// Shares the work out (whole CTA); false where the lengths are out of order or past a bound.
+__device__ bool make_plan(Shared& sm, const ScaledArgs& a, const Ends& mine, Plan& plan) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   static_assert(kThreads >= VMLA_MAX_BATCH, "a thread per sequence");
   bool ok = true;
   uint64_t cost = 0;
   if (tid < a.batch) {
-    const int64_t k0 = __ldg(a.kv_indptr + tid), k1 = __ldg(a.kv_indptr + tid + 1), q0 = __ldg(a.qo_indptr + tid),
-                  q1 = __ldg(a.qo_indptr + tid + 1);
+    const int64_t k0 = mine.k0, k1 = mine.k1, q0 = mine.q0, q1 = mine.q1;
     ok = q1 >= q0 && q1 - q0 <= VMLA_MAX_DRAFT && k1 - k0 >= q1 - q0;
     if (tid == 0) ok = ok && k0 == 0 && q0 == 0;
     if (tid == a.batch - 1) ok = ok && k1 <= a.max_kv && q1 <= a.max_q;
@@ -192,7 +211,7 @@ __device__ bool make_plan(Shared& sm, const ScaledArgs& a, Plan& plan) {
   // the sequence that this CTA's share begins in
   const uint32_t from = blockIdx.x * plan.share, at = before + (uint32_t)(upto - cost);  // (from: below length + share)
   if (from >= at && from - at < (uint32_t)cost) {
-    const Seq s = seq_of(a, tid);
+    const Seq s = {mine.q0, mine.q1 - mine.q0, mine.k0, mine.k1 - mine.k0};
     const uint32_t span = tiles_of(s.nk) + kFixed, g = (from - at) / span;
     sm.first_seq = s;
     sm.first_b = tid;
@@ -241,30 +260,35 @@ struct Units {
     s = sm.first_seq;
     n = row_blocks(a, s.nq);
   }
+  // The current stream's tiles that lie in the share; whether there are any.
+  __device__ __forceinline__ bool current(const ScaledArgs& a, Unit& u) const {
+    const int tiles = tiles_of(s.nk);
+    const uint32_t lo = at > from ? at : from, stop = at + tiles, hi = stop < end ? stop : end;
+    if (lo >= hi) return false;
+    u.row_block = g;
+    u.rows = min(kRows, s.nq * a.num_heads - g * kRows);
+    u.tile0 = (int)(lo - at);
+    u.tiles = (int)(hi - lo);
+    u.q0 = s.q0;
+    u.nq = s.nq;
+    u.kv0 = s.kv0;
+    u.keys = s.nk;
+    u.prefix = s.nk - s.nq;
+    u.head = lo == at;
+    u.whole = u.tiles == tiles;
+    u.stop = stop;
+    return true;
+  }
   __device__ __noinline__ bool next(const Shared& sm, const ScaledArgs& a, Unit& u) {
-    while (at < end) {
-      const int tiles = tiles_of(s.nk);
-      const uint32_t lo = at > from ? at : from, stop = at + tiles, hi = stop < end ? stop : end;
-      const bool use = lo < hi;
-      if (use) {
-        u.row_block = g;
-        u.rows = min(kRows, s.nq * a.num_heads - g * kRows);
-        u.tile0 = (int)(lo - at);
-        u.tiles = (int)(hi - lo);
-        u.q0 = s.q0;
-        u.nq = s.nq;
-        u.kv0 = s.kv0;
-        u.keys = s.nk;
-        u.prefix = s.nk - s.nq;
-        u.head = lo == at;
-        u.whole = u.tiles == tiles;
-        u.stop = stop;
-      }
-      if (++g < n) at += tiles + kFixed;
+    do {
+      if (++g < n) at += tiles_of(s.nk) + kFixed;
       else enter(sm, a, b + 1);
-      if (use) return true;
-    }
-    return false;
+      if (at >= end) return false;
+    } while (!current(a, u));
+    return true;
+  }
+  __device__ __forceinline__ bool first(const Shared& sm, const ScaledArgs& a, Unit& u) {
+    return at < end && (current(a, u) || next(sm, a, u));
   }
 };
 __device__ __forceinline__ int64_t out_row(const ScaledArgs& a, const Unit& u) {
@@ -326,8 +350,8 @@ __device__ void load_role(Shared& sm, const Maps& maps, const ScaledArgs& a, Uni
   constexpr int kGroups = (kTile / 4 + kLoadWarps - 1) / kLoadWarps;  // of four keys, the warp's: warp, warp + 6 ..
   constexpr int kBoxes = kTile / kRun;
   const bool last_group = warp + kLoadWarps * (kGroups - 1) < kTile / 4;
-  const uint32_t full0 = smem_u32(&sm.full[0]), latent0 = smem_u32(sm.latent[0]), rope0 = smem_u32(sm.rope),
-                 rope_bar = smem_u32(&sm.rope_full);
+  const uint32_t full0 = smem_u32(&sm.bars.full[0]), latent0 = smem_u32(sm.latent[0]), rope0 = smem_u32(sm.rope),
+                 rope_bar = smem_u32(&sm.bars.rope_full);
   Ring ring;  // of the tile's first chunk
   uint32_t it = 0;
   for (; more; more = units.next(sm, a, u)) {
@@ -364,7 +388,7 @@ __device__ void load_role(Shared& sm, const Maps& maps, const ScaledArgs& a, Uni
 #pragma unroll
         for (int k = 0; k < kBoxes; ++k) r[k] = __shfl_sync(0xffffffffu, y[0], (upper ? k ^ (kBoxes / 2) : k) * (kRun / 4));
         const uint32_t at0 = upper ? kBoxes / 2 : 0;  // r[k]: box k ^ at0
-        if (!__all_sync(0xffffffffu, wait(sm, &sm.free[at.slot], at.parity ^ 1, a, 100))) return;
+        if (!__all_sync(0xffffffffu, wait(sm, &sm.bars.free[at.slot], at.parity ^ 1, a, 100))) return;
         if (elect_one()) {
           const uint32_t bar = full0 + at.slot * 8, dst = latent0 + at.slot * (kTile * 128);
           if (!upper) mbar_arrive_expect_tx(bar, kTile * 128);
@@ -374,7 +398,7 @@ __device__ void load_role(Shared& sm, const Maps& maps, const ScaledArgs& a, Uni
         }
         __syncwarp();
         if (upper) {
-          if (!__all_sync(0xffffffffu, wait(sm, &sm.rope_free, (it & 1) ^ 1, a, 101))) return;
+          if (!__all_sync(0xffffffffu, wait(sm, &sm.bars.rope_free, (it & 1) ^ 1, a, 101))) return;
           if (elect_one()) {
             if (warp == kChunks) mbar_arrive_expect_tx(rope_bar, kTile * 64);
             // (boxes 4 to 7 by warp 4, which has them first, 0 to 3 by warp 5)
@@ -398,8 +422,8 @@ __device__ void load_role(Shared& sm, const Maps& maps, const ScaledArgs& a, Uni
       for (int piece = 0; piece < kPieces; ++piece) {
         const int chunk = piece < kRopePiece ? piece : piece - 1, row = piece == kRopePiece ? 64 : 128;
         const Ring at = ring.plus(chunk);
-        if (!__all_sync(0xffffffffu, piece == kRopePiece ? wait(sm, &sm.rope_free, (it & 1) ^ 1, a, 102)
-                                                         : wait(sm, &sm.free[at.slot], at.parity ^ 1, a, 102)))
+        if (!__all_sync(0xffffffffu, piece == kRopePiece ? wait(sm, &sm.bars.rope_free, (it & 1) ^ 1, a, 102)
+                                                         : wait(sm, &sm.bars.free[at.slot], at.parity ^ 1, a, 102)))
           return;
         if (elect_one()) {
           const uint32_t bar = piece == kRopePiece ? rope_bar : full0 + at.slot * 8,
@@ -421,9 +445,9 @@ __device__ void load_role(Shared& sm, const Maps& maps, const ScaledArgs& a, Uni
   if (warp == 0) {
     for (uint32_t k = 0; k < kSlots; ++k) {
       const Ring at = ring.plus(k);
-      wait(sm, &sm.free[at.slot], at.parity ^ 1, a, 103);
+      wait(sm, &sm.bars.free[at.slot], at.parity ^ 1, a, 103);
     }
-    wait(sm, &sm.rope_free, (it & 1) ^ 1, a, 104);
+    wait(sm, &sm.bars.rope_free, (it & 1) ^ 1, a, 104);
   }
   __syncwarp();
 }
@@ -442,30 +466,30 @@ __device__ void score_role(Shared& sm, const ScaledArgs& a, uint32_t tmem, Units
   uint32_t it = 0, unit = 0;
   for (; more; more = units.next(sm, a, u), ++unit) {
     const int tiles = u.tiles;
-    if (!__all_sync(0xffffffffu, wait(sm, &sm.qfull, unit & 1, a, 200))) return;
+    if (!__all_sync(0xffffffffu, wait(sm, &sm.bars.qfull, unit & 1, a, 200))) return;
 #pragma unroll 1
     for (int t = 0; t < tiles; ++t, ++it, ring = ring.plus(kChunks)) {
       const uint32_t sb = it & 1, d = tmem + kSCol + sb * 2 * kRows;
-      if (!__all_sync(0xffffffffu, wait(sm, &sm.sfree[sb], ((it >> 1) & 1) ^ 1, a, 201))) return;
+      if (!__all_sync(0xffffffffu, wait(sm, &sm.bars.sfree[sb], ((it >> 1) & 1) ^ 1, a, 201))) return;
 #pragma unroll
       for (int piece = 0; piece < kPieces; ++piece) {
         const int chunk = piece < kRopePiece ? piece : piece - 1;
         const Ring at = ring.plus(chunk);
-        if (!__all_sync(0xffffffffu, piece == kRopePiece ? wait(sm, &sm.rope_full, it & 1, a, 202)
-                                                         : wait(sm, &sm.full[at.slot], at.parity, a, 202)))
+        if (!__all_sync(0xffffffffu, piece == kRopePiece ? wait(sm, &sm.bars.rope_full, it & 1, a, 202)
+                                                         : wait(sm, &sm.bars.full[at.slot], at.parity, a, 202)))
           return;
         tc_fence_after();
         if (elect_one()) {
           if (piece == kRopePiece) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) mma_ss_f8(d, rope_lo + 2 * i, kHi64, q_rope_lo + 2 * i, kHi64, kDesc, 1u);
-            mma_commit(&sm.rope_free);
+            mma_commit(&sm.bars.rope_free);
           } else {
             const uint32_t key = latent_lo + at.slot * (kTile * 128 / 16), q = q_latent_lo + chunk * (2 * kRows * 128 / 16);
 #pragma unroll
             for (int i = 0; i < 4; ++i) mma_ss_f8(d, key + 2 * i, kHi128, q + 2 * i, kHi128, kDesc, piece > 0 || i > 0);
           }
-          if (piece == kPieces - 1) mma_commit(&sm.sfull[sb]);
+          if (piece == kPieces - 1) mma_commit(&sm.bars.sfull[sb]);
         }
         __syncwarp();
       }
@@ -482,10 +506,10 @@ __device__ void value_role(Shared& sm, const ScaledArgs& a, uint32_t tmem, Units
   for (; more; more = units.next(sm, a, u), ++unit) {
     const int tiles = u.tiles;
     // (the first product into O: the unit before has been read out)
-    if (!__all_sync(0xffffffffu, wait(sm, &sm.ofree, (unit & 1) ^ 1, a, 210))) return;
+    if (!__all_sync(0xffffffffu, wait(sm, &sm.bars.ofree, (unit & 1) ^ 1, a, 210))) return;
 #pragma unroll 1
     for (int t = 0; t < tiles; ++t, ++it, ring = ring.plus(kChunks)) {
-      if (!__all_sync(0xffffffffu, wait(sm, &sm.pfull, it & 1, a, 211))) return;
+      if (!__all_sync(0xffffffffu, wait(sm, &sm.bars.pfull, it & 1, a, 211))) return;
       tc_fence_after();
       if (elect_one()) {
         const uint32_t go_on = t > 0;
@@ -496,9 +520,9 @@ __device__ void value_role(Shared& sm, const ScaledArgs& a, uint32_t tmem, Units
 #pragma unroll
           for (int i = 0; i < kTile / 32; ++i)
             mma_ss_f8(tmem + c * kOCols, v + 256 * i, kHi128, p_lo + 256 * i, kHi128, kDesc, i > 0 ? 1u : go_on);
-          mma_commit(&sm.free[at.slot]);
+          mma_commit(&sm.bars.free[at.slot]);
         }
-        mma_commit(&sm.pfree);
+        mma_commit(&sm.bars.pfree);
       }
       __syncwarp();
     }
@@ -569,16 +593,16 @@ __device__ __noinline__ void load_queries(Shared& sm, const ScaledArgs& a, const
       uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
+        // (as fp16 exact wherever a part shows it: a bf16 number from 2^-14 to 448)
         const float x0 = bf16_lo(w[j]) * scale, x1 = bf16_hi(w[j]) * scale;
         uint16_t h, l;
-        uint32_t back2;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(x1), "f"(x0));
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back2) : "h"(h));
-        float y0, y1;
-        asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;}"
-            : "=f"(y0), "=f"(y1)
-            : "r"(back2));
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(l) : "f"((x1 - y1) * 16.f), "f"((x0 - y0) * 16.f));
+        uint32_t x, y;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(x1), "f"(x0));
+        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(x));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(h));
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(y));
+        asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(0x4C004C00u));  // 16
+        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(x));
         hi[j >> 1] |= (uint32_t)h << (16 * (j & 1));
         lo[j >> 1] |= (uint32_t)l << (16 * (j & 1));
       }
@@ -620,7 +644,7 @@ __device__ __noinline__ void load_queries(Shared& sm, const ScaledArgs& a, const
   }
   fence_proxy_async_smem();
   named_bar_sync(1, kSoftThreads);
-  if (lane == 0 && a.test_fault != kFaultNoQReady) mbar_arrive(&sm.qfull);
+  if (lane == 0 && a.test_fault != kFaultNoQReady) mbar_arrive(&sm.bars.qfull);
 }
 
 // ------------------------------------------------------------------ softmax
@@ -653,7 +677,7 @@ __device__ __forceinline__ float reduce16(const float (&v)[16], int lane, Op op)
 __device__ __noinline__ void clear_nan(Shared& sm, const ScaledArgs& a, uint32_t tile, int key, bool mine) {
   for (uint32_t c = 0; c < kChunks; ++c) {
     const uint32_t at = (tile * kChunks + c) % kSlots;
-    wait(sm, &sm.full[at], ((tile * kChunks + c) / kSlots) & 1, a, 304);  // (long ago: the scores came of it)
+    wait(sm, &sm.bars.full[at], ((tile * kChunks + c) / kSlots) & 1, a, 304);  // (long ago: the scores came of it)
     if (!mine) continue;
     uint4* row = reinterpret_cast<uint4*>(sm.latent[at] + key * 128);
     for (int g = 0; g < 8; ++g) {
@@ -702,7 +726,7 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
       }
       const bool all_seen = __all_sync(0xffffffffu, seen == 0xFFFFu);
       const float held = fmaxf(scale, kTiny);
-      wait(sm, &sm.sfull[sb], (it >> 1) & 1, a, 300);  // (should it run out, the vote below ends the work)
+      wait(sm, &sm.bars.sfull[sb], (it >> 1) & 1, a, 300);  // (should it run out, the vote below ends the work)
       __syncwarp();
       const uint32_t col = tmem + lanes + kSCol + (uint32_t)(sb * 2 * kRows + row0);
       float w[kPerThread];
@@ -785,7 +809,7 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
         }
         if (t > 0) {
           // what has been summed so far, once the products before are complete
-          wait(sm, &sm.pfree, (it - 1) & 1, a, 301);
+          wait(sm, &sm.bars.pfree, (it - 1) & 1, a, 301);
           __syncwarp();
           tc_fence_after();
 #pragma unroll 1
@@ -809,7 +833,7 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.sfree[sb]);
+      if (lane == 0) mbar_arrive(&sm.bars.sfree[sb]);
       const float back = __frcp_rn(held);
 #pragma unroll
       for (int r = 0; r < kPerThread; r += 2) {
@@ -837,7 +861,7 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
 #pragma unroll
         for (int q = 0; q < kParts; ++q) parts[q][k] = __byte_perm(h[0][q], h[1][q], 0x7531);
       }
-      if (wait(sm, &sm.pfree, (it & 1) ^ 1, a, 302)) {
+      if (wait(sm, &sm.bars.pfree, (it & 1) ^ 1, a, 302)) {
 #pragma unroll
         for (int q = 0; q < kParts; ++q) {
           uint8_t* dst = sm.p + my_key * 128 + (((2 * q + (row0 >> 4)) ^ (my_key & 7)) << 4);
@@ -846,7 +870,7 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.pfull);
+      if (lane == 0) mbar_arrive(&sm.bars.pfull);
       scale = next_scale;
     }
     // row sums over the keys; what the rows' results are scaled by
@@ -872,7 +896,7 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
     // the next unit's queries while this one's last products run
     more = units.next(sm, a, u);
     if (more) load_queries(sm, a, u);
-    wait(sm, &sm.pfree, (it - 1) & 1, a, 303);
+    wait(sm, &sm.bars.pfree, (it - 1) & 1, a, 303);
     __syncwarp();
     tc_fence_after();
 #pragma unroll 1
@@ -908,7 +932,7 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
     }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.ofree);
+    if (lane == 0) mbar_arrive(&sm.bars.ofree);
   }
 }
 
@@ -918,29 +942,23 @@ scaled_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ScaledA
   extern __shared__ uint8_t raw[];
   Shared& sm = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5;
+  const Ends ends(a);  // (on their way while the barriers are made)
   if (warp == kValueWarp) {
     tmem_alloc(&sm.tmem, 512);
     tmem_relinquish();
   }
-  if (tid == 0) {
-    for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.free[s], 1);
-    }
-    mbar_init(&sm.rope_full, 1);
-    mbar_init(&sm.rope_free, 1);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&sm.sfull[s], 1);
-      mbar_init(&sm.sfree[s], kSoftWarps);
-    }
-    mbar_init(&sm.pfull, kSoftWarps);
-    mbar_init(&sm.pfree, 1);
-    mbar_init(&sm.qfull, kSoftWarps);
-    mbar_init(&sm.ofree, kSoftWarps);
+  static_assert(sizeof(Bars) == 8 * 30, "every barrier is counted here");
+  if (tid < (int)(sizeof(Bars) / 8)) {
+    constexpr int first = offsetof(Bars, sfree) / 8;
+    const bool soft = tid == first || tid == first + 1 || tid == (int)offsetof(Bars, pfull) / 8 ||
+                      tid == (int)offsetof(Bars, qfull) / 8 || tid == (int)offsetof(Bars, ofree) / 8;
+    mbar_init(reinterpret_cast<uint64_t*>(&sm.bars) + tid, soft ? kSoftWarps : 1);
+    fence_mbar_init();
+  } else if (tid == 32) {
     sm.abort_flag = 0;
     sm.fault[0] = sm.fault[1] = 0;
     sm.cut_pieces = 0;
-    fence_mbar_init();
+  } else if (tid == kLoadWarp * 32) {
     prefetch_tensormap(&maps.latent);
     prefetch_tensormap(&maps.rope);
     prefetch_tensormap(&maps.latent_run);
@@ -948,7 +966,7 @@ scaled_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ScaledA
   }
   __syncwarp();
   Plan plan;
-  const bool ok = make_plan(sm, a, plan);
+  const bool ok = make_plan(sm, a, ends, plan);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -957,7 +975,7 @@ scaled_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ScaledA
     // the CTA's first unit, which every role begins with
     Units units(sm, a, plan);
     Unit u;
-    const bool more = units.next(sm, a, u);
+    const bool more = units.first(sm, a, u);
     if (warp < kSoftWarps) {
       softmax_role(sm, a, plan, tmem, part, units, u, more);
     } else if (warp == kScoreWarp) {
