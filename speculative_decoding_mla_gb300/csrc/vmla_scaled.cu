@@ -29,10 +29,11 @@
 // What bounds it: shared memory.  Of its 128 bytes a clock a tile takes 1755 wavefronts as operands of the products, 540
 // as it arrives, and some 900 for weights, references, indices and shuffles; with eight trees of 40 to 64 drafts over
 // 9 000 to 16 000 keys the pipe is busy 83 % of the whole launch, the tensor pipe 37 %, DRAM 4 %.  A tile takes 1.5 us
-// there, of which its products are 0.9; 1.65 us where the rows come from DRAM (32 requests of 64 heads).  About 18 us of
-// a call are launches, plan, queries, the first tile's loads, results and the join (one request of 1024 keys: 20 us).
-// Measured (us): 32 requests of 64 heads, up to 60 000 keys 117; 64 requests of 8 heads and 4 drafts, up to 32 768 keys 82;
-// eight trees 276; 185 000 keys, 64 heads, 4 drafts 138.  Tried, without gain: clusters of two and four CTAs that share
+// there, of which its products are 0.9; 1.65 us where the rows come from DRAM (32 requests of 64 heads).  About 16 us of
+// a call are launches, plan, queries, the first tile's loads, results and the join (one request of 1024 keys: 18.4 us, of
+// which 1.2 the barriers, 0.8 the plan, 3.9 the queries and 3.1 the first tile's scores and weights).
+// Measured (us): 32 requests of 64 heads, up to 60 000 keys 114; 64 requests of 8 heads and 4 drafts, up to 32 768 keys 80;
+// eight trees 264 to 272; 185 000 keys, 64 heads, 4 drafts 136.  Tried, without gain: clusters of two and four CTAs that share
 // each tile's loads by multicast (faster than one issuing thread that also loaded, slower than this form: 142 us against
 // 121); units of 64 rows (as fast; the accumulators of three parts would not fit, so the parts took turns); 16 softmax
 // warps of 8 rows; a vote by word and barrier or cast early and counted late; longer sleeps of the waiting warps;
