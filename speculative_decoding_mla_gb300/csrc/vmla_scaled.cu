@@ -851,7 +851,8 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           uint32_t x, r1, r2;
-          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(w[4 * k + 2 * j + 1]), "f"(w[4 * k + 2 * j]));
+          // (cut to 11 bits, then rounded to 9: one rounding, not two)
+          asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(w[4 * k + 2 * j + 1]), "f"(w[4 * k + 2 * j]));
           x = (x + 0x00020002u) & counts;
           h[j][0] = x & 0xFF00FF00u;
           asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r1) : "r"(x), "r"(h[j][0]));
