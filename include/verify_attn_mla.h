@@ -681,8 +681,8 @@ int verify_attn_mla_host(const void* q_host, const void* kv_pool, int64_t pool_s
 /* Measurement aid.  verify_attn_mla_timing_enable(n) creates host-side CUDA
  * events for the next n run calls (0 turns it off and frees them); while it is
  * on, every verify_attn_mla, _simt, _runs, _fp8 and _host call (not the
- * device-planned form, nor verify_attn_mla_shared with shared rows, the append
- * or the sampling) records events on its stream around each kernel it
+ * device-planned form, nor verify_attn_mla_shared with shared rows, the appends,
+ * verify_attn_mla_scaled, the tables, the beams or the sampling) records events on its stream around each kernel it
  * launches.  verify_attn_mla_timing_read() waits
  * for those events and writes, per call in launch order, the device time in ms
  * of the KV gather kernel, the verify kernel and the merge kernel (0 for a
