@@ -7,7 +7,7 @@
 //
 // Within a beam the order is the logits' own, so a row's first K tokens by (logit, index) are all that can be kept.
 // The first kernel reads each row once: a thread sums exp(x - r) against a reference r of its own, a logit (raised when
-// a granule's maximum passes it by 20) and remembers its largest granule, (maximum, place).  The K-th largest of
+// a granule's maximum passes it by 8) and remembers its largest granule, (maximum, place).  The K-th largest of
 // the threads' granules bounds the row's K-th token from below, and no token above the bound lies outside the K
 // threads that have these granules: only their granules are read again (from L2), the tokens above the bound listed,
 // and the list ranked.  Rows are cut into parts, one CTA each, while that is needed to fill the GPU.
@@ -44,6 +44,7 @@ constexpr int kMaxBeams = VMLA_MAX_BEAMS, kMaxKeep = VMLA_MAX_BEAM_KEEP;
 constexpr int kMaxParts = 16;
 constexpr int kList = 2048;      // tokens above the bound that are ranked at once
 constexpr float kLowest = -3.402823466e38f;
+constexpr float kAbove = 8.f;    // how far a thread's terms may lie above its reference (see kMargin)
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr double kLn2 = 0.69314718055994530942;
 static_assert(kMaxKeep <= kThreads && kMaxBeams * kMaxParts <= kThreads, "a thread per place and per list");
@@ -154,7 +155,7 @@ struct Acc {
       low *= f;
       sum *= f;
       ref = m;
-      limit = m + 20.f;
+      limit = m + kAbove;
     }
     const float2 r = make_float2(-ref, -ref), scale = make_float2(kLog2e, kLog2e);
     float2 e[N];
@@ -433,9 +434,14 @@ __device__ __forceinline__ bool before(uint64_t a, uint32_t ia, uint64_t b, uint
   return a > b || (a == b && ia < ib);
 }
 
-// By how much a beam's score may be off: the terms' errors (ex2.approx 2.4e-7; its argument, log2 e as a float among
-// it, d 1.4e-7 for a term e^-d; a tree of eight and a running sum of eight 6.6e-7; two more factors 5e-7).
-constexpr double kMargin = 2e-6;
+// By how much a beam's score may be off, with u = 2^-24.  An exponent d puts its power of e off by 2.23 u |d| (the
+// difference, log2 e as a float, their product).  A term x lies d <= kAbove above its thread's reference; from there the
+// raises and the factors that join threads and parts lead up to the row's largest reference, by D + d together where
+// the row's largest logit lies D above x, and the term has at most e^-D of the sum: (2 kAbove + D) e^-D 2.23 u is
+// 2.12e-6 at the most, for D = 0.  Four powers (term, raise, thread, part) by ex2.approx, 2^-22 each, 9.6e-7; sums of
+// 8 (one after the other where one is NaN) and of 4, and a raise's product, 12 u = 7.2e-7.
+constexpr double kMargin = 4e-6;
+static_assert(2 * kAbove * 2.23 / (1 << 24) + 4.0 / (1 << 22) + 12.0 / (1 << 24) < kMargin, "see above");
 
 // Notes beams w and v whose scores a >= b lie closer than their sums are known to.
 __device__ __forceinline__ void doubt(JoinShared& s, uint64_t a, int w, uint64_t b, int v) {
