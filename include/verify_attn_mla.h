@@ -470,8 +470,10 @@ int verify_attn_mla_append_scaled(const void* latent, int64_t latent_stride, con
  *   row_j = kv_scales[s / block_tokens] x code values of slot s = kv_indices[kv_indptr[b] + j]
  * (real products; no rounding of rows).  Scores, softmax and sums are fp32; the
  * queries enter in two e4m3 parts (to 2^-22 of the row's largest), the weights
- * p_j kv_scale_j with 9 significant bits down to 2^-17 of the row's largest and
- * in steps of 2^-25 below, out is rounded once to bf16.  A query row that holds
+ * p_j kv_scale_j with 9 significant bits down to 2^-19 of the largest that the
+ * row has met so far and to within 2^-28 of it below that (rounded to either
+ * side; below 2^-32 of it a weight is zero in out, but not in lse), out is
+ * rounded once to bf16.  A query row that holds
  * an infinity or NaN, or sees a key with a NaN code, gets out and lse of NaN; no
  * other row does.
  *   kv_scales  fp32, finite and >= 0 (below 2^-100: the block's values count as

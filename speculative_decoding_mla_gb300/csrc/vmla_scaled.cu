@@ -7,8 +7,10 @@
 //   queries  q a_r = hi + lo / 16, both e4m3, a_r the power of two that brings the row's largest to (224, 448]:
 //            off by at most 2^-14 of what is 448 at the largest (2^-22.8), less than an fp32 dot product's rounding
 //   weights  p a_j 2^9, in fp16 rounded to 9 bits, cut into three parts of three bits, e5m2: the upper byte of an fp16
-//            number is an e5m2 number, so a part is an AND and the rest an exact difference.  Its range (2^-16 to 2^15
-//            here) is why it is not two e4m3 parts: beside a key of much weight, 10^5 keys of weight 10^-5 each still count.
+//            number is an e5m2 number, so a part is an AND and the rest an exact difference.  The last part is held times
+//            2^6 (it has sums of its own) and rounded: its range ends at 2^-22 instead of 2^-16, where small weights would
+//            all be cut, a loss that grows with their number.  The range (2^-22 to 2^15) is why it is not two e4m3 parts:
+//            beside a key of much weight, 10^5 keys of weight 10^-8 each still count.
 //
 // Keys are the matrix products' M (tiles of 128), query rows their N (units of 32), so that few rows waste nothing:
 //   S^T [128 keys x 64]  = K [128 x 576] (Q hi | Q lo)^T               18 products, M128 N64 K32
@@ -75,6 +77,7 @@ constexpr int kFixed = 8;           // what a unit costs beside its tiles, in ti
 constexpr float kNone = -3e38f;     // reference of a row that has seen no key
 constexpr float kUnitBits = 9.f;    // weights are held times 2^9
 constexpr float kMost = 32768.f;    // largest weight held
+constexpr float kLow = 64.f;        // what the last part of a weight is held times: it is below 2^9
 constexpr float kTiny = 0x1p-100f;  // smaller scales count as zero
 static_assert(kSCol + 2 * 2 * kRows == 512, "tensor memory");
 static_assert(kThreads % 128 == 0, "whole register banks");
@@ -858,7 +861,9 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
           asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r1) : "r"(x), "r"(h[j][0]));
           h[j][1] = r1 & 0xFF00FF00u;
           asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r2) : "r"(r1), "r"(h[j][1]));
-          h[j][2] = r2;
+          // (three bits at the most for weights from 2^-10 on, whose rounding changes nothing; up to six below that)
+          asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(r2) : "r"(0x54005400u));  // kLow
+          h[j][2] = r2 + 0x00800080u;
         }
 #pragma unroll
         for (int q = 0; q < kParts; ++q) parts[q][k] = __byte_perm(h[0][q], h[1][q], 0x7531);
@@ -915,7 +920,7 @@ __device__ void softmax_role(Shared& sm, const ScaledArgs& a, const Plan& plan, 
         tmem_ld8(at + 2 * kRows, z);
         tmem_wait_ld();
 #pragma unroll
-        for (int r = 0; r < 8; ++r) o[r] = (__uint_as_float(x[r]) + __uint_as_float(y[r])) + __uint_as_float(z[r]);
+        for (int r = 0; r < 8; ++r) o[r] = fmaf(__uint_as_float(z[r]), 1.f / kLow, __uint_as_float(x[r]) + __uint_as_float(y[r]));
       }
       if (out) {
         // pairs of lanes exchange a value each, so that a lane stores two columns of one row
