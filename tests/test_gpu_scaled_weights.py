@@ -1,4 +1,4 @@
-"""Weights far below a row's largest.
+"""Weights far below a row's largest, and references raised behind a unit's first tile.
 
 A unit is what one CTA has of a stream (32 rows of one sequence over its tiles), and its weights are held against a
 reference of its own.  So that units are whole streams of many tiles here, a call has as many sequences as there are SMs, all
@@ -9,7 +9,7 @@ import math
 import pytest
 import torch
 
-from tests.test_gpu_scaled import D, DV, ints
+from tests.test_gpu_scaled import D, DV, SM, check, ints, pool_of
 
 pytestmark = pytest.mark.gpu
 H, TILE, ROWS = 128, 128, 32
@@ -93,3 +93,30 @@ def test_many_small_weights_beside_a_large_one(B, drop, place):
     assert bool(((out[:, 256:].double() - large).abs() <= large * (2.0 ** -9 + 2.0 ** -8)).all())
     # sums of at most n / 128 numbers by a thread
     assert bool(((lse.double() - math.log(total)).abs() <= 2.0 ** -20 + n / 128 * 2.0 ** -24).all())
+
+
+@pytest.mark.parametrize("spread", [0.0, 1.5])
+def test_references_raised_in_many_tiles(B, spread):
+    """Keys in rising order of their scores for half of the heads, falling for the others: what has been summed is scaled down
+    again and again."""
+    n = 47 * TILE - 31
+    g = torch.Generator(device="cuda").manual_seed(int(spread * 10))
+    pool, scales = pool_of(g, n, 1, True, spread)
+    rows = pool.view(torch.float8_e4m3fn).double() * scales.double()[:, None]
+    base = torch.randn((1, D), generator=g, device="cuda")
+    gain = torch.linspace(-9.0, 9.0, H, device="cuda")[:, None]
+    q = (base * gain + 0.05 * torch.randn((H, D), generator=g, device="cuda")).to(torch.bfloat16)
+    kv = (rows @ base[0].double()).argsort().to(torch.int32)
+    z = (q.double() @ rows[kv.long()].t()) * SM / math.log(2.0) + scales.double()[kv.long()].log2()
+    tops = torch.stack([t.amax(1) for t in z.split(TILE, 1)], 1)  # each row's largest weight per tile, as a power of two
+    reach = tops.cummax(1).values
+    rises = torch.zeros(H, dtype=torch.int64, device="cuda")
+    ref = reach[:, 0].clone()
+    for t in range(1, reach.shape[1]):  # (2^6 above the reference: raised)
+        up = reach[:, t] > ref + 6.01
+        rises += up
+        ref = torch.where(up, reach[:, t], ref)
+    assert int((rises >= 3).sum()) >= H // 4 and int((rises == 0).sum()) >= H // 4
+    out, lse = whole_streams(B, q, pool, scales, kv, SM)
+    c = dict(q=q[None], pool=pool, scales=scales, kv=kv, block=1, nk=[n], nq=[1])
+    check(c, out[None], lse[None])
