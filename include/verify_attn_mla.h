@@ -558,7 +558,8 @@ int verify_attn_mla_step_tables(const int32_t* cached, const int32_t* added, int
  *   vocab     1 .. VMLA_MAX_VOCAB;  pad_token in [0, vocab)
  *   score     [requests x beams] fp32;  finished [requests x beams] int32 or NULL
  *   workspace >= verify_attn_mla_beam_select_workspace_size() bytes (rows =
- *             requests x beams), 256 B aligned, for this call alone while it runs
+ *             requests x beams), 256 B aligned, for this call alone while it runs;
+ *             the size for the largest batch and vocabulary serves every smaller one
  * parent, token and new_score overlap no input.  Two launches, no host
  * synchronisation; capture-safe. */
 int verify_attn_mla_beam_select_workspace_size(int64_t rows, int vocab, int keep, size_t* bytes);

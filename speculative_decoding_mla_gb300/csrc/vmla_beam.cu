@@ -29,6 +29,7 @@
 // against all and the entries ranked against each other: 60, 77 and 18.4 us.)
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "vmla_device.cuh"
@@ -691,8 +692,18 @@ int launch_select(const BeamArgs& a, int64_t requests, int parts, void* workspac
 
 }  // namespace
 
-size_t beam_workspace(int64_t rows, int vocab, int sms) {
+size_t beam_workspace_used(int64_t rows, int vocab, int sms) {
   return (size_t)rows * parts_of(rows, vocab, sms) * sizeof(RowPart);
+}
+
+// What every call of up to `rows` rows and `vocab` tokens uses at most (fewer rows may have more parts).
+size_t beam_workspace(int64_t rows, int vocab, int sms) {
+  int64_t most = rows;
+  for (int parts = 2; parts <= kMaxParts && vocab / parts >= 4096; parts *= 2) {
+    const int64_t last = (6 * (int64_t)sms - 1) / parts;  // the most rows that get so many (see parts_of)
+    most = std::max(most, std::min(rows, last) * parts);
+  }
+  return (size_t)most * sizeof(RowPart);
 }
 
 int launch_beam_select(const BeamArgs& a, int64_t requests, bool fp32, int sms, void* workspace, void* stream) {

@@ -1116,7 +1116,7 @@ int verify_attn_mla_beam_select(const void* logits, int logits_fp32, int64_t row
   int sms = 0;
   rc = current_sm_count(&sms, true);
   if (rc != VMLA_OK) return rc;
-  if (workspace_bytes < beam_workspace(requests * beams, vocab, sms)) return VMLA_ERR_WORKSPACE;
+  if (workspace_bytes < beam_workspace_used(requests * beams, vocab, sms)) return VMLA_ERR_WORKSPACE;
   BeamArgs a;
   a.logits = logits;
   a.stride = row_stride;

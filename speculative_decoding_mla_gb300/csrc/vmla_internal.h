@@ -326,7 +326,8 @@ struct ReorderArgs {
   int32_t* new_length;      // [requests x keep] or NULL
   uint32_t* status;
 };
-size_t beam_workspace(int64_t rows, int vocab, int sms);
+size_t beam_workspace(int64_t rows, int vocab, int sms);       // for every call of up to so many rows and tokens
+size_t beam_workspace_used(int64_t rows, int vocab, int sms);  // for this one
 int launch_beam_select(const BeamArgs& args, int64_t requests, bool fp32, int sms, void* workspace, void* stream);
 int launch_beam_reorder(const ReorderArgs& args, int64_t requests, int sms, void* stream);
 
