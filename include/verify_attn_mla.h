@@ -445,13 +445,15 @@ int verify_attn_mla_append(const void* latent, int64_t latent_stride, const void
  *   kv_scales [pool_slots / block_tokens] fp32, read and written; pool_slots is
  *             a multiple of block_tokens
  * The call's rows of one block set its scale:
- *   need  = the smallest 2^k (k >= -100) with every |value| <= 448 x 2^k
+ *   need  = the smallest 2^k (k >= -100) with every finite |value| <= 448 x 2^k
  *   scale = need if they begin at the block's first slot (what the block held
  *           before is gone), else the larger of need and the block's scale
  * and where that raises the scale, the block's rows in front of them are coded
  * again: e4m3(code x old / new), nearest even (rows behind them keep their
  * codes: nothing valid lies there when a cache grows in order).  A value of
- * +-inf is coded as the largest code, NaN as the NaN code.
+ * +-inf is coded as the largest code, NaN as the NaN code, and neither takes
+ * part in the scale (but with block_tokens 1, where the row is alone, an
+ * infinity gives 2^120, by which the largest code is an infinity again).
  * The tokens of one block stand together in the call, their slots ascending
  * (as verify_attn_mla_step_tables lists them; padding may stand between them);
  * tokens of a block that stand apart would set its scale twice, in either order.  A token left out by an

@@ -2,7 +2,7 @@
 //
 // A row is [latent (512) | rotated part (64)] as in the append with one scale.  The rows that a call brings to one
 // block (a run: tokens that stand together, slots ascending) get the block's scale
-//   need  = the smallest power of two 2^k, k >= -100, with every |value| of the run <= 448 x 2^k
+//   need  = the smallest power of two 2^k, k >= -100, with every finite |value| of the run <= 448 x 2^k
 //   scale = need where the run begins the block, else max(the block's scale, need)
 //   code  = e4m3(value / scale), nearest even,
 // and where that raises the scale the block's rows in front of the run are coded again, e4m3(code x old / new).
@@ -171,21 +171,23 @@ __device__ __forceinline__ void fetch_four(const AppendArgs& a, int64_t t0, int 
   }
 }
 
-// Their largest magnitude (NaN left out), in every lane.
+// Their largest finite magnitude, in every lane: a scale that an infinity set would leave nothing of the block's other rows.
+// (Magnitudes' bits order as whole numbers do, and with one more in the exponent infinities and NaN are negative.)
 __device__ __forceinline__ float largest(const Four& f) {
-  uint32_t m2 = 0;  // of two columns (max gives the other operand where one is NaN)
-  auto take = [&](uint32_t w) { asm("max.bf16x2 %0, %0, %1;" : "+r"(m2) : "r"(w & 0x7FFF7FFFu)); };
+  constexpr uint32_t kOne = 0x00800080u;
+  uint32_t m2 = kOne;  // of two columns
+  auto take = [&](uint32_t w) { m2 = __viaddmax_s16x2(w & 0x7FFF7FFFu, kOne, m2); };
 #pragma unroll
   for (int i = 0; i < kSide; ++i)
     if (__shfl_sync(0xffffffffu, f.slot, 8 * i) >= 0) {
       take(f.v0[i].x); take(f.v0[i].y); take(f.v0[i].z); take(f.v0[i].w);
       take(f.v1[i].x); take(f.v1[i].y); take(f.v1[i].z); take(f.v1[i].w);
     }
-  float m = fmaxf(bf16_lo(m2), bf16_hi(m2));
+  int m = (int)max(m2 << 16, m2 & 0xFFFF0000u);
   if (f.slot >= 0)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(f.x[k]));
-  return warp_max(m);
+    for (int k = 0; k < 8; ++k) m = __viaddmax_s32((int)(__float_as_uint(f.x[k]) & 0x7FFFFFFFu), (int)(kOne & 0xFFFF0000u), m);
+  return __uint_as_float((uint32_t)__reduce_max_sync(0xffffffffu, m) - (kOne & 0xFFFF0000u));
 }
 
 __device__ __forceinline__ void store_four(const AppendArgs& a, int lane, const Four& f, float scale) {
