@@ -56,6 +56,7 @@ extern "C" {
 #define VMLA_MAX_HEADS 128
 #define VMLA_MAX_VOCAB 262144 /* tokens of a row that verify_attn_mla_sample draws from */
 #define VMLA_MAX_BLOCK_TOKENS 128 /* slots that share a scale (verify_attn_mla_scaled): a power of two up to this */
+#define VMLA_MAX_SCALED_KV 2147483136 /* 2^31 - 512: keys of a verify_attn_mla_scaled call */
 #define VMLA_MAX_BEAMS 16     /* beams of a request (verify_attn_mla_beam_select) */
 #define VMLA_MAX_BEAM_KEEP 32 /* continuations it keeps */
 #define VMLA_WORKSPACE_ALIGN 256
@@ -482,16 +483,20 @@ int verify_attn_mla_append_scaled(const void* latent, int64_t latent_stride, con
  *              zero, scored by the scale as it is)
  *   pool_slots a multiple of block_tokens; the pool is 16-byte aligned
  *   batch, num_heads, draft_mask, parent, q, out, lse: as for verify_attn_mla;
- *              N_b may be any length the pool holds, Q_b up to 64
+ *              N_b may be any length up to VMLA_MAX_SCALED_KV (a slot may come
+ *              more than once), Q_b up to 64; the sum of ceil(Q_b num_heads / 32) x
+ *              (ceil(N_b / 128) + 8) over sequences 32 k .. 32 k + 31 is at most
+ *              2^27 for each k (one sequence of 64 drafts and 128 heads: 67 M keys)
  *   max_total_q, max_total_kv  bounds on qo_indptr[batch] and kv_indptr[batch]
  *              at every replay, as for verify_attn_mla_device_plan: q, out and
- *              lse hold max_total_q rows, kv_indices max_total_kv entries
+ *              lse hold max_total_q rows, kv_indices max_total_kv entries (at most
+ *              VMLA_MAX_SCALED_KV)
  *   workspace  >= verify_attn_mla_scaled_workspace_size() bytes, 256 B aligned,
  *              for this call alone while it runs; its size depends on the device only
  * A sequence without drafts writes nothing; rows of q, out and lse from
  * qo_indptr[batch] on are left as they are.
- * Capture-safe; no host synchronisation.  Lengths out of order or past a bound
- * are found on the device: nothing is computed and VMLA_ERR_SHAPE recorded.  A
+ * Capture-safe; no host synchronisation.  Lengths out of order or past a bound,
+ * and sums above 2^27, are found on the device: nothing is computed and VMLA_ERR_SHAPE recorded.  A
  * slot outside the pool takes part as a row of zeros and records VMLA_ERR_INDEX
  * (index into kv_indices); malformed parents record VMLA_ERR_PARENT. */
 int verify_attn_mla_scaled_workspace_size(int batch, int num_heads, int64_t max_total_q, int64_t max_total_kv,

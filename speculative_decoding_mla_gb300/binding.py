@@ -36,6 +36,7 @@ D_QK = 576
 D_V = 512
 MAX_VOCAB = 262144
 MAX_BLOCK_TOKENS = 128
+MAX_SCALED_KV = 2 ** 31 - 512
 MAX_BEAMS = 16
 MAX_BEAM_KEEP = 32
 

@@ -963,7 +963,7 @@ int verify_attn_mla_append_scaled(const void* latent, int64_t latent_stride, con
 namespace {
 int check_scaled(int batch, int num_heads, int64_t max_total_q, int64_t max_total_kv) {
   if (batch < 0 || batch > VMLA_MAX_BATCH || num_heads < 1 || num_heads > VMLA_MAX_HEADS) return VMLA_ERR_SHAPE;
-  if (max_total_q < 0 || max_total_kv < 0 || max_total_kv > INT32_MAX) return VMLA_ERR_SHAPE;
+  if (max_total_q < 0 || max_total_kv < 0 || max_total_kv > VMLA_MAX_SCALED_KV) return VMLA_ERR_SHAPE;
   // more rows than the batch can have are never used
   if (max_total_q > (int64_t)batch * VMLA_MAX_DRAFT) return VMLA_ERR_SHAPE;
   return VMLA_OK;

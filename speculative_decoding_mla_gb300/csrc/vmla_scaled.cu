@@ -145,7 +145,9 @@ struct Maps {
 };
 
 // ------------------------------------------------------------------ plan
-// Costs are counted in tiles; a call whose cost does not fit 31 bits (2^27 for any 32 sequences) is refused.
+// Costs are counted in tiles; a call whose cost does not fit 31 bits (2^27 for a warp's 32 sequences) is refused.
+// Keys are looked up to two tiles ahead of the last one, in 32 bits.
+static_assert(VMLA_MAX_SCALED_KV <= INT32_MAX - 3 * kTile, "positions of keys fit 32 bits");
 struct Plan {
   uint32_t length;  // of all streams
   uint32_t share;   // of a CTA
