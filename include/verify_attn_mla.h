@@ -526,13 +526,18 @@ int verify_attn_mla_scaled(const void* q, const void* kv_pool_e4m3, int64_t pool
  *   free_left      [1] int32 out: how many are left (may be free_count itself,
  *                  as a captured step needs it)
  *   scratch        [1] uint32, zero at the first call; every call leaves it zero
+ *                  (for this call alone while it runs)
  *   kv_indices [max_total_kv], positions, slots [max_total_q], kv_indptr,
  *   qo_indptr [batch + 1] int32 out
  *   status_word    optional, two uint32
  * block_tokens 1 makes block_table a table of slots.  Blocks that cached[b] no
  * longer reaches (a step whose drafts were rejected began them) are replaced by
- * fresh ones when the request grows again: give them back to the free list, or
- * keep room for them.  An entry of the table that
+ * fresh ones when the request grows again, and so are those of beams that a
+ * selection dropped.  No call gives them back: keep room for them, or, every so
+ * often between steps, mark the blocks that the tables still reach, write the
+ * others to the front of free_blocks (free_size: all blocks) and set free_count
+ * to their number, which elementary device operations do and a captured step
+ * can hold.  A list that runs out records VMLA_ERR_FULL.  An entry of the table that
  * is negative, or whose slots pass 2^31, gives slots of -1.  A negative length or
  * a request longer than the table's row records VMLA_ERR_SHAPE (request), and
  * more keys, tokens or new blocks than there is room for VMLA_ERR_FULL: the
