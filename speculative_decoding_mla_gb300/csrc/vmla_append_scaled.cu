@@ -70,9 +70,10 @@ __device__ __forceinline__ float scale_for(float amax) {
   return __uint_as_float((uint32_t)(k + 127) << 23);
 }
 
-// Eight values -> codes: by a product where the scale is a power of two (then exact), else by a division.
+// Eight values -> codes: by a product where the scale is a power of two (then exact) whose reciprocal is a normal number,
+// else by a division.
 __device__ __forceinline__ uint2 codes_of(const float (&x)[8], float scale) {
-  if ((__float_as_uint(scale) & 0x7FFFFFu) != 0 || scale < 0x1p-120f) return codes8(x, scale);
+  if ((__float_as_uint(scale) & 0x7FFFFFu) != 0 || !(scale >= 0x1p-120f && scale <= 0x1p126f)) return codes8(x, scale);
   const float inv = __uint_as_float((254u << 23) - __float_as_uint(scale));
   uint32_t w[4];
 #pragma unroll
