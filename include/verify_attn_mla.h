@@ -563,7 +563,8 @@ int verify_attn_mla_step_tables(const int32_t* cached, const int32_t* added, int
  * without a continuation hold -1, -1 and -inf.  -inf forbids a token, NaN
  * counts as -inf, and tokens at +inf share their row evenly.
  * Within a beam the order is the logits' own; scores of different beams are
- * compared to about 2^-27, whatever the order of summation.
+ * compared to about 2^-27, whatever the order of summation; new_score is within
+ * 4e-6 and its rounding to fp32.
  *   logits    [requests x beams, vocab], logits_fp32 0: bf16, 1: fp32; row_stride
  *             elements from row to row (>= vocab; any alignment to the element's size)
  *   beams     1 .. VMLA_MAX_BEAMS;  keep 1 .. VMLA_MAX_BEAM_KEEP;  requests <= 65535

@@ -18,13 +18,15 @@
 // 4e-6 (kMargin).  Where two neighbours of the merged order, or the last of it and one that is left out, are of
 // different beams and lie closer than that, the request's CTA sums the beams concerned again in whole units
 // (weight_units, exact in any order: equal rows have equal sums wherever they lie) and merges anew, until no beam is
-// left in doubt.  Scores closer than about 2^-27 are not told apart for certain.
+// left in doubt.  Scores closer than about 2^-27 are not told apart for certain.  A CTA takes 0.6 to 0.9 ns a token for
+// this, the requests side by side: with two equal beams a call takes 75 us instead of 15 (4 beams of 32 000 tokens) or 234
+// instead of 39 (64 x 8 of 131 072), with all equal 130 and 822, and 16 equal ones of 262 144 tokens 2.6 ms.
 //
 // Sums are kept as two floats (an exact sum of two): doubles cost more than all the rest, at their rate on this GPU.
 //
 // What bounds it: for many rows the logits, 2 or 4 bytes a token in, and the exponentials, 16 a clock and SM.  Measured:
 // 64 x 8 beams of 131 072 tokens in bf16 (134 MB) 45 us, the rows' kernel 31 of them (4.3 TB/s; 60 % of the issue slots),
-// the join 9, the reordering of tables of 4000 slots 7; 9 x 15 beams, 30 kept, of 151 001 tokens in fp32 (82 MB) 48 us:
+// the join 9, the reordering of tables of 4000 slots 7; 9 x 15 beams, 30 kept, of 151 001 tokens in fp32 (82 MB) 49 us:
 // 24, 14 and 11; one request of four beams 16 us: 7, 8 and 4, all latency.  (Doubles in the loop, every thread ranked
 // against all and the entries ranked against each other: 60, 77 and 18.4 us.)
 #include <cuda_runtime.h>
